@@ -4,7 +4,10 @@ The operator returns logp[t] = h_t . W_{y_t} - logsumexp_{v < V_true}(h_t . W_v)
 (fp32) without materialising the [T, V] logits, plus dH / dW of
 sum_t g_t logp_t. It is a C ABI shared library (include/rlk.h, built into
 ``_build/librlk.so`` from ``csrc/``) with hand-written sm_103a kernels
-(tcgen05 / TMEM / TMA); this package is its thin ctypes binding.
+(tcgen05 / TMEM / TMA); this package is its thin ctypes binding. Next to it stand the
+operators over logits that already exist (module ``logits``): token log probabilities with
+rank, entropy and top alternatives, and distillation from a teacher's top logits, each with
+its gradient.
 """
 from ._binding import (  # noqa: F401
     LEAF_WIDTH, MAX_SHARDS, RLK_BWD_DH, RLK_BWD_DW, RLK_BWD_DZ, RLK_ERR_CUDA, RLK_ERR_INVALID_ARG,
@@ -16,3 +19,7 @@ from ._binding import (  # noqa: F401
     saved_logits_bytes, saved_probs_bytes, selftest_bounds_check, selftest_wait_timeout,
     shard_bounds, shard_sum_bf16, version)
 from .autograd import LinearLogp, linear_logp  # noqa: F401
+from .logits import (  # noqa: F401
+    MAX_LOGITS_VOCAB, MAX_TOP_K, RLK_DTYPE_BF16, RLK_DTYPE_F16, RLK_DTYPE_F32, TokenLogprobs,
+    bwd_dz_view, distill_topk, distill_topk_bwd, distill_topk_fwd, distill_topk_fwd_bwd,
+    token_logprobs, token_logprobs_autograd, token_logprobs_bwd)

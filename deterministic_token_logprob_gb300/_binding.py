@@ -108,6 +108,19 @@ def _declare(lib):
     lib.rlk_linear_logp_bwd_fp8.argtypes = [P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64,
                                             P, I32, P, P, P, SZ, P]
     lib.rlk_linear_logp_bwd_fp8.restype = ctypes.c_int
+    F64 = ctypes.c_double
+    rows = [P, I32, I64, I64, I64, F64]      # logits, dtype, T, ld, V_true, temperature
+    grad = [P, I32, I64, I64]                # dlogits, out_dtype, V, out_ld
+    lib.rlk_token_logprobs.argtypes = rows + [P, I32, P, P, P, P, P, P, P, P]
+    lib.rlk_token_logprobs.restype = ctypes.c_int
+    lib.rlk_token_logprobs_bwd.argtypes = rows + [P, P, P, P, P] + grad + [P, P]
+    lib.rlk_token_logprobs_bwd.restype = ctypes.c_int
+    lib.rlk_distill_topk_fwd.argtypes = rows + [P, P, I32, P, P, P, P]
+    lib.rlk_distill_topk_fwd.restype = ctypes.c_int
+    lib.rlk_distill_topk_bwd.argtypes = rows + [P, P, I32, P, P] + grad + [P, P]
+    lib.rlk_distill_topk_bwd.restype = ctypes.c_int
+    lib.rlk_distill_topk_fwd_bwd.argtypes = rows + [P, P, I32, P, P, P] + grad + [P, P]
+    lib.rlk_distill_topk_fwd_bwd.restype = ctypes.c_int
     lib.rlk_status_string.argtypes = [ctypes.c_int]
     lib.rlk_status_string.restype = ctypes.c_char_p
     lib.rlk_version.argtypes = []

@@ -1,0 +1,326 @@
+"""Operators over logits that already exist: token log probabilities with entropy and top
+alternatives (:func:`token_logprobs`), their gradient (:func:`token_logprobs_bwd`), and
+distillation from a teacher's top logits (:func:`distill_topk_fwd`, :func:`distill_topk_bwd`,
+:func:`distill_topk_fwd_bwd`).
+
+Argument marshalling around the C entry points of the same names (include/rlk.h states their
+mathematics, special rows and errors); all arithmetic runs in the library's CUDA kernels.
+``logits`` is a [T, V] CUDA tensor of bfloat16, float16 or float32 whose rows are contiguous
+(stride(1) == 1; stride(0) is free, so a slice of a wider buffer serves), and ``V_true``
+defaults to V. Work is enqueued on ``stream`` (default: the current stream of the logits'
+device); with a ``stream`` given, outputs are allocated on it and the inputs are recorded as
+used there.
+
+:func:`token_logprobs_autograd` and :func:`distill_topk` are the autograd forms.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from typing import NamedTuple, Optional, Sequence, Tuple
+
+import torch
+
+from . import _binding
+from ._binding import _check, _load
+
+RLK_DTYPE_BF16 = 0
+RLK_DTYPE_F16 = 1
+RLK_DTYPE_F32 = 2
+MAX_TOP_K = 128
+MAX_LOGITS_VOCAB = 1 << 20
+
+_DTYPES = {torch.bfloat16: RLK_DTYPE_BF16, torch.float16: RLK_DTYPE_F16, torch.float32: RLK_DTYPE_F32}
+
+
+class TokenLogprobs(NamedTuple):
+    """Per row: the token's log probability (fp32) and rank (int32, 1 = most likely), lse and
+    entropy (fp32), and the top_k best tokens (int64 [T, top_k], -1 where there is none) with
+    their log probabilities (fp32 [T, top_k]). Without targets logp and rank are None; with
+    top_k = 0 the last two are."""
+    logp: Optional[torch.Tensor]
+    rank: Optional[torch.Tensor]
+    lse: torch.Tensor
+    entropy: torch.Tensor
+    top_ids: Optional[torch.Tensor]
+    top_logp: Optional[torch.Tensor]
+
+
+def _rows(t: torch.Tensor, name: str, dtypes=_DTYPES) -> Tuple[int, int, int]:
+    """Checks a [T, V] tensor with contiguous rows; (T, V, row distance)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
+    T, V = t.shape
+    ld, inner = t.stride()
+    if V > 1 and inner != 1:
+        raise ValueError(f"{name} must have contiguous rows (stride(1) == 1)")
+    if T <= 1:  # the stride of a single row says nothing
+        ld = max(ld, V)
+    if ld < V:
+        raise ValueError(f"{name} must not have overlapping rows")
+    return T, V, ld
+
+
+def _per_row(t, name: str, dtype, shape, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _flag(err_flag, device):
+    if err_flag is None:
+        return None
+    return _per_row(err_flag, "err_flag", torch.int32, (1,), device)
+
+
+@contextlib.contextmanager
+def _launch_on(stream, device, tensors):
+    """The stream handle to launch on, with `device` current; outputs made inside belong to that
+    stream, and `tensors` are recorded as used there when it is not their current stream."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+            return
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def _true_vocab(V_true: Optional[int], V: int) -> int:
+    V_true = V if V_true is None else int(V_true)
+    if not 0 < V_true <= V:
+        raise ValueError(f"V_true must be in 1 .. {V}, got {V_true}")
+    return V_true
+
+
+def token_logprobs(logits: torch.Tensor, y: Optional[torch.Tensor] = None, *, top_k: int = 0,
+                   V_true: Optional[int] = None, temperature: float = 1.0,
+                   out: Optional[Sequence[Optional[torch.Tensor]]] = None,
+                   err_flag: Optional[torch.Tensor] = None, stream=None) -> TokenLogprobs:
+    """rlk_token_logprobs: the log probability and rank of each row's token y (int64 [T]), lse,
+    entropy and the top_k alternatives of softmax(logits / temperature).
+
+    `out` supplies the six output tensors in the order of :class:`TokenLogprobs` (a serving loop
+    keeps them between steps); None in a place leaves that output out."""
+    T, V, ld = _rows(logits, "logits")
+    dev = logits.device
+    V_true = _true_vocab(V_true, V)
+    if not 0 <= top_k <= MAX_TOP_K:
+        raise ValueError(f"top_k must be in 0 .. {MAX_TOP_K}, got {top_k}")
+    if y is not None:
+        _per_row(y, "y", torch.int64, (T,), dev)
+    flag = _flag(err_flag, dev)
+    with _launch_on(stream, dev, (logits, y, err_flag, *(out or ()))) as handle:
+        if out is None:
+            f32 = dict(dtype=torch.float32, device=dev)
+            out = (None if y is None else torch.empty(T, **f32),
+                   None if y is None else torch.empty(T, dtype=torch.int32, device=dev),
+                   torch.empty(T, **f32), torch.empty(T, **f32),
+                   torch.empty((T, top_k), dtype=torch.int64, device=dev) if top_k else None,
+                   torch.empty((T, top_k), **f32) if top_k else None)
+        elif len(out) != 6:
+            raise ValueError("out must hold six tensors (or None): logp, rank, lse, entropy, top_ids, top_logp")
+        r = TokenLogprobs(*out)
+        shapes = dict(logp=(torch.float32, (T,)), rank=(torch.int32, (T,)), lse=(torch.float32, (T,)),
+                      entropy=(torch.float32, (T,)), top_ids=(torch.int64, (T, top_k)),
+                      top_logp=(torch.float32, (T, top_k)))
+        p = [None if t is None else _per_row(t, n, *shapes[n], dev) for n, t in zip(r._fields, r)]
+        st = _load().rlk_token_logprobs(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
+                                        float(temperature), None if y is None else y.data_ptr(),
+                                        int(top_k), *p, flag, handle)
+    _check("rlk_token_logprobs", st)
+    return r
+
+
+def _gradient(logits, T, V, out, out_dtype):
+    """The dlogits tensor to fill: `out` ([T, at least V], rows contiguous), or a new [T, V] one."""
+    if out is None:
+        dtype = out_dtype or logits.dtype
+        if dtype not in _DTYPES:
+            raise TypeError(f"out_dtype must be one of {[str(d) for d in _DTYPES]}, got {dtype}")
+        return torch.empty((T, V), dtype=dtype, device=logits.device), V, max(V, 1)
+    oT, oV, old = _rows(out, "out")
+    if oT != T or oV < V:
+        raise ValueError(f"out must have {T} rows of at least {V} columns, got {tuple(out.shape)}")
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
+    if out.device != logits.device:
+        raise ValueError(f"out must be on {logits.device}, got {out.device}")
+    return out, oV, old
+
+
+def token_logprobs_bwd(logits: torch.Tensor, y: torch.Tensor, lse: torch.Tensor,
+                       entropy: Optional[torch.Tensor], g_logp: torch.Tensor,
+                       g_entropy: Optional[torch.Tensor] = None, *, V_true: Optional[int] = None,
+                       temperature: float = 1.0, out: Optional[torch.Tensor] = None,
+                       out_dtype: Optional[torch.dtype] = None,
+                       err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """rlk_token_logprobs_bwd -> dlogits of sum_t (g_logp logp + g_entropy entropy), from the
+    forward's lse and entropy. The result has the logits' shape and type (or out_dtype: bfloat16
+    for float32 logits); `out` supplies it, the logits themselves included."""
+    T, V, ld = _rows(logits, "logits")
+    dev = logits.device
+    V_true = _true_vocab(V_true, V)
+    p = [_per_row(y, "y", torch.int64, (T,), dev), _per_row(lse, "lse", torch.float32, (T,), dev),
+         None if entropy is None else _per_row(entropy, "entropy", torch.float32, (T,), dev),
+         _per_row(g_logp, "g_logp", torch.float32, (T,), dev),
+         None if g_entropy is None else _per_row(g_entropy, "g_entropy", torch.float32, (T,), dev)]
+    if g_entropy is not None and entropy is None:
+        raise ValueError("g_entropy needs the forward's entropy")
+    flag = _flag(err_flag, dev)
+    with _launch_on(stream, dev, (logits, y, lse, entropy, g_logp, g_entropy, out, err_flag)) as handle:
+        dlogits, oV, old = _gradient(logits, T, V, out, out_dtype)
+        st = _load().rlk_token_logprobs_bwd(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
+                                            float(temperature), *p, dlogits.data_ptr(),
+                                            _DTYPES[dlogits.dtype], oV, old, flag, handle)
+    _check("rlk_token_logprobs_bwd", st)
+    return dlogits
+
+
+def _teacher(ids, teacher, T, dev):
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be an int64 [T, K] tensor")
+    K = ids.shape[1]
+    if not 1 <= K <= MAX_TOP_K:
+        raise ValueError(f"K must be in 1 .. {MAX_TOP_K}, got {K}")
+    return K, [_per_row(ids, "ids", torch.int64, (T, K), dev),
+               _per_row(teacher, "teacher", torch.float32, (T, K), dev), K]
+
+
+def distill_topk_fwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *,
+                     V_true: Optional[int] = None, temperature: float = 1.0,
+                     err_flag: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """rlk_distill_topk_fwd -> (loss, lse), fp32 [T] each: the KL divergence from the softmax of
+    the teacher's top logits (fp32 [T, K], at columns ids int64 [T, K], -1: none) to
+    softmax(logits / temperature), and the student's lse for the backward."""
+    T, V, ld = _rows(logits, "logits")
+    dev = logits.device
+    V_true = _true_vocab(V_true, V)
+    _, p = _teacher(ids, teacher, T, dev)
+    flag = _flag(err_flag, dev)
+    with _launch_on(stream, dev, (logits, ids, teacher, err_flag)) as handle:
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        st = _load().rlk_distill_topk_fwd(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
+                                          float(temperature), *p, loss.data_ptr(), lse.data_ptr(), flag,
+                                          handle)
+    _check("rlk_distill_topk_fwd", st)
+    return loss, lse
+
+
+def distill_topk_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
+                     lse: torch.Tensor, g: torch.Tensor, *, V_true: Optional[int] = None,
+                     temperature: float = 1.0, out: Optional[torch.Tensor] = None,
+                     out_dtype: Optional[torch.dtype] = None,
+                     err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """rlk_distill_topk_bwd -> dlogits of sum_t g[t] loss[t], from the forward's lse. Shape, type
+    and `out` as in :func:`token_logprobs_bwd`."""
+    T, V, ld = _rows(logits, "logits")
+    dev = logits.device
+    V_true = _true_vocab(V_true, V)
+    _, p = _teacher(ids, teacher, T, dev)
+    p += [_per_row(lse, "lse", torch.float32, (T,), dev), _per_row(g, "g", torch.float32, (T,), dev)]
+    flag = _flag(err_flag, dev)
+    with _launch_on(stream, dev, (logits, ids, teacher, lse, g, out, err_flag)) as handle:
+        dlogits, oV, old = _gradient(logits, T, V, out, out_dtype)
+        st = _load().rlk_distill_topk_bwd(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
+                                          float(temperature), *p, dlogits.data_ptr(),
+                                          _DTYPES[dlogits.dtype], oV, old, flag, handle)
+    _check("rlk_distill_topk_bwd", st)
+    return dlogits
+
+
+def distill_topk_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor,
+                         g: torch.Tensor, *, V_true: Optional[int] = None, temperature: float = 1.0,
+                         out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                         err_flag: Optional[torch.Tensor] = None,
+                         stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """rlk_distill_topk_fwd_bwd -> (loss, lse, dlogits): :func:`distill_topk_fwd` and
+    :func:`distill_topk_bwd` in one call, for weights g known before the loss (a token mask over
+    a count). The same bits; the logits are read from memory once."""
+    T, V, ld = _rows(logits, "logits")
+    dev = logits.device
+    V_true = _true_vocab(V_true, V)
+    _, p = _teacher(ids, teacher, T, dev)
+    p.append(_per_row(g, "g", torch.float32, (T,), dev))
+    flag = _flag(err_flag, dev)
+    with _launch_on(stream, dev, (logits, ids, teacher, g, out, err_flag)) as handle:
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        dlogits, oV, old = _gradient(logits, T, V, out, out_dtype)
+        st = _load().rlk_distill_topk_fwd_bwd(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
+                                              float(temperature), *p, loss.data_ptr(), lse.data_ptr(),
+                                              dlogits.data_ptr(), _DTYPES[dlogits.dtype], oV, old, flag,
+                                              handle)
+    _check("rlk_distill_topk_fwd_bwd", st)
+    return loss, lse, dlogits
+
+
+def bwd_dz_view(workspace: torch.Tensor, T: int, V_local: int) -> torch.Tensor:
+    """The dz array at the start of a :func:`linear_logp_bwd` workspace as a bf16
+    [T, round_up(V_local, 256)] tensor: a gradient written there (``out=``) is what the stages
+    RLK_BWD_DH and RLK_BWD_DW turn into dH and dW."""
+    Vd = -(-V_local // 256) * 256
+    n = T * Vd * 2
+    if workspace.dtype != torch.uint8 or workspace.dim() != 1 or workspace.numel() < n:
+        raise ValueError(f"workspace must be a uint8 tensor of at least {n} bytes")
+    return workspace[:n].view(torch.bfloat16).view(T, Vd)
+
+
+class _TokenLogprobsFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, y, V_true, temperature):
+        r = token_logprobs(logits, y, V_true=V_true, temperature=temperature)
+        ctx.save_for_backward(logits, y, r.lse, r.entropy)
+        ctx.args = dict(V_true=V_true, temperature=temperature)
+        return r.logp, r.entropy
+
+    @staticmethod
+    def backward(ctx, g_logp, g_entropy):
+        logits, y, lse, entropy = ctx.saved_tensors
+        d = token_logprobs_bwd(logits, y, lse, entropy, g_logp.contiguous(), g_entropy.contiguous(), **ctx.args)
+        return d, None, None, None
+
+
+def token_logprobs_autograd(logits: torch.Tensor, y: torch.Tensor, *, V_true: Optional[int] = None,
+                            temperature: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
+    """(logp, entropy) of each row, fp32 [T], differentiable in the logits (both gradients)."""
+    return _TokenLogprobsFn.apply(logits, y, V_true, temperature)
+
+
+class _DistillTopkFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, ids, teacher, V_true, temperature):
+        loss, lse = distill_topk_fwd(logits, ids, teacher, V_true=V_true, temperature=temperature)
+        ctx.save_for_backward(logits, ids, teacher, lse)
+        ctx.args = dict(V_true=V_true, temperature=temperature)
+        return loss
+
+    @staticmethod
+    def backward(ctx, g):
+        logits, ids, teacher, lse = ctx.saved_tensors
+        return distill_topk_bwd(logits, ids, teacher, lse, g.contiguous(), **ctx.args), None, None, None, None
+
+
+def distill_topk(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *,
+                 V_true: Optional[int] = None, temperature: float = 1.0) -> torch.Tensor:
+    """The distillation loss of each row, fp32 [T], differentiable in the logits (the teacher is
+    a constant)."""
+    return _DistillTopkFn.apply(logits, ids, teacher, V_true, temperature)

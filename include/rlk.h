@@ -92,7 +92,8 @@ typedef enum {
 /* bits ORed into *err_flag by the kernels */
 #define RLK_FLAG_BAD_TARGET 1
 #define RLK_FLAG_TIMEOUT 2
-#define RLK_FLAG_NONFINITE 4 /* rlk_quantize_rows_e4m3: a row held a NaN or an infinity */
+#define RLK_FLAG_NONFINITE 4 /* rlk_quantize_rows_e4m3: a row held a NaN or an infinity; operators over
+                                logits: a row held a NaN or +inf */
 #define RLK_FLAG_BOUNDS 8    /* debug-checks builds only: an index or tensor-copy coordinate
                                 check failed; the access was skipped (see rlk_debug_checks) */
 
@@ -363,6 +364,118 @@ RLK_API rlk_status rlk_linear_logp_bwd_fp8(const void* h, const void* W, const v
                                            void* dH, int32_t dH_fp32_partial, float* dW,
                                            int32_t* err_flag, void* workspace,
                                            size_t workspace_bytes, void* stream);
+
+/*
+ * Operators over logits that already exist, next to the fused head: a serving engine has
+ * them after sampling, rlk_linear_logp_fwd_save leaves them as saved logits. All of them
+ * take the rows' scaled logits x = s z, s = 1 / temperature (rounded once to fp32), over the
+ * columns below V_true; what the columns at and beyond V_true hold is never read. Common
+ * arguments:
+ *   logits   device [T][ld] of type dtype (RLK_DTYPE_*), rows `ld` elements apart, aligned to
+ *            its element size only (rows of an odd length may start anywhere)
+ *   ld       row distance in elements, at least V_true
+ *   V_true   1 .. RLK_MAX_LOGITS_VOCAB
+ *   temperature  RLK_MIN_TEMPERATURE .. RLK_MAX_TEMPERATURE
+ *   err_flag device int32 or NULL, as everywhere
+ * Numerical contract: fp32 statistics in one fixed order over column indices (leaves of 1024
+ * columns about their own maximum, then all leaves about the row's), so every output of a row
+ * depends on that row's inputs alone: not on T, on the other rows, on alignment or strides, on
+ * the launch shape or on the GPU's SM count. e^x = ex2.approx.ftz(x log2 e), log is logf.
+ * Nothing needs a workspace. T == 0 returns RLK_OK and launches nothing.
+ *
+ * Special rows. -inf logits are masked columns: probability 0. A row of nothing but -inf has
+ * lse -inf, logp -inf, entropy 0, no alternatives, and a zero gradient. A row with a NaN or
+ * +inf below V_true has NaN in lse, logp, entropy and loss, rank 0, no alternatives (id -1, log
+ * probability NaN), a zero gradient, and RLK_FLAG_NONFINITE is ORed into *err_flag. A target
+ * outside [0, V_true) has logp NaN, rank 0 and a zero gradient row, and RLK_FLAG_BAD_TARGET is
+ * ORed in.
+ */
+typedef enum { RLK_DTYPE_BF16 = 0, RLK_DTYPE_F16 = 1, RLK_DTYPE_F32 = 2 } rlk_dtype;
+
+#define RLK_MAX_TOP_K 128
+#define RLK_MAX_LOGITS_VOCAB (1 << 20)
+#define RLK_MAX_LOGITS_ROWS (1 << 28)
+#define RLK_MIN_TEMPERATURE 1e-6
+#define RLK_MAX_TEMPERATURE 1e6
+
+/*
+ * Log probabilities of given tokens, with entropy and top alternatives. Per row t:
+ *   lse      = log sum_v e^{x_v}
+ *   logp     = x_y - lse
+ *   rank     = 1 + #{v : z_v > z_y, or z_v = z_y and v < y}     (1: the most likely token)
+ *   entropy  = -sum_v p_v log p_v,  p_v = e^{x_v - lse}
+ *   top_ids, top_logp: the top_k best columns in the order of rank and their x_v - lse
+ *            (so a token of rank r <= top_k stands in place r - 1); places beyond the columns
+ *            that are not -inf hold id -1 and -inf
+ *   y        device int64 [T], or NULL (then logp and rank must be NULL)
+ *   logp, lse, entropy  device fp32 [T], rank device int32 [T], each may be NULL
+ *   top_k    0 .. RLK_MAX_TOP_K; top_ids device int64 [T][top_k] and top_logp device fp32
+ *            [T][top_k], both given when top_k > 0
+ */
+RLK_API rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t ld,
+                                      int64_t V_true, double temperature, const int64_t* y,
+                                      int32_t top_k, float* logp, int32_t* rank, float* lse,
+                                      float* entropy, int64_t* top_ids, float* top_logp,
+                                      int32_t* err_flag, void* stream);
+
+/*
+ * Gradient of sum_t (g_logp[t] logp[t] + g_entropy[t] entropy[t]) with respect to the logits:
+ *   dlogits[t][v] = s (g_logp (1[v = y] - p_v) - g_entropy p_v (log p_v + entropy))
+ * in fp32 and rounded once to out_dtype; columns V_true .. V - 1 get 0. A row whose two
+ * gradients are 0 gets zeros whatever its logits hold (padding tokens).
+ *   lse, entropy  device fp32 [T], as rlk_token_logprobs gave them (entropy may be NULL when
+ *            g_entropy is); g_logp device fp32 [T]; g_entropy device fp32 [T] or NULL
+ *   dlogits  device [T][out_ld] of type out_dtype, out_ld >= V >= V_true: the logits' type, or
+ *            RLK_DTYPE_BF16 for fp32 logits. The first round_up(V_local, 256) * T elements of
+ *            rlk_linear_logp_bwd's workspace are such an array (bf16, V = out_ld =
+ *            round_up(V_local, 256)): with dlogits there, RLK_BWD_DH and RLK_BWD_DW of
+ *            rlk_linear_logp_bwd_stages give this loss's dH and dW. dlogits may be the logits
+ *            themselves (same type, base and row distance); else the two must not overlap.
+ */
+RLK_API rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld,
+                                          int64_t V_true, double temperature, const int64_t* y,
+                                          const float* lse, const float* entropy,
+                                          const float* g_logp, const float* g_entropy,
+                                          void* dlogits, int32_t out_dtype, int64_t V,
+                                          int64_t out_ld, int32_t* err_flag, void* stream);
+
+/*
+ * Distillation from a teacher's top logits. q = softmax(s t_k) over the row's entries, and
+ *   loss[t] = sum_k q_k (log q_k - (x_{id_k} - lse))       (the KL divergence from q to p)
+ *   dlogits[t][v] = s g[t] (p_v - sum_{k : id_k = v} q_k)  of sum_t g[t] loss[t]
+ * (teacher log probabilities serve as well as logits: q does not change under a shift).
+ *   ids      device int64 [T][K], K in 1 .. RLK_MAX_TOP_K; id -1: no entry (as rlk_token_logprobs
+ *            marks missing alternatives); an id may come twice, then both count
+ *   teacher  device fp32 [T][K]; -inf: probability 0
+ *   g        device fp32 [T]
+ *   loss, lse  device fp32 [T]; lse (of the student's logits) feeds the backward, may be NULL
+ * A row without entries (or with all teacher values -inf) has loss 0 and a zero gradient. A row
+ * with an id outside [-1, V_true) (RLK_FLAG_BAD_TARGET) or a teacher value of NaN or +inf
+ * (RLK_FLAG_NONFINITE) has loss NaN and a zero gradient. Where the student's logit of an entry
+ * with q > 0 is -inf the loss is +inf. dlogits, out_dtype, V, out_ld as in
+ * rlk_token_logprobs_bwd, with rows of g = 0 zero.
+ *
+ * rlk_distill_topk_fwd_bwd gives both at once, for weights g that are known before the loss (a
+ * token mask over a count): the same bits as the two calls, and the logits are read from memory
+ * once (their second reading is meant to hit in L2).
+ */
+RLK_API rlk_status rlk_distill_topk_fwd(const void* logits, int32_t dtype, int64_t T, int64_t ld,
+                                        int64_t V_true, double temperature, const int64_t* ids,
+                                        const float* teacher, int32_t K, float* loss, float* lse,
+                                        int32_t* err_flag, void* stream);
+
+RLK_API rlk_status rlk_distill_topk_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld,
+                                        int64_t V_true, double temperature, const int64_t* ids,
+                                        const float* teacher, int32_t K, const float* lse,
+                                        const float* g, void* dlogits, int32_t out_dtype, int64_t V,
+                                        int64_t out_ld, int32_t* err_flag, void* stream);
+
+RLK_API rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld,
+                                            int64_t V_true, double temperature, const int64_t* ids,
+                                            const float* teacher, int32_t K, const float* g,
+                                            float* loss, float* lse, void* dlogits,
+                                            int32_t out_dtype, int64_t V, int64_t out_ld,
+                                            int32_t* err_flag, void* stream);
 
 /*
  * Forward without a workspace argument, for callers that cannot allocate device
