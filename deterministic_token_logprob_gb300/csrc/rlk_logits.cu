@@ -17,12 +17,15 @@ constexpr int ROW_WARPS = ROW_THREADS / 32;
 // statistics of one row by one CTA: every warp takes every ROW_WARPS-th leaf
 // ---------------------------------------------------------------------------
 template <class E>
-__device__ __forceinline__ Stats row_stats(const typename E::bits* row, int n, float c, Stats* leaves) {
+__device__ __forceinline__ Stats row_stats(const Row<E>& row, float c, Stats* leaves) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_leaves = (n + ROW_LEAF - 1) / ROW_LEAF;
+  const int n_leaves = (row.n + ROW_LEAF - 1) / ROW_LEAF;
   for (int l = warp; l < n_leaves; l += ROW_WARPS) {
+    Pack<E> k[LEAF_GROUPS];
+    load_leaf(row, l, lane, k);
     float v[32];
-    load_leaf<E>(row, n, l, lane, v);
+#pragma unroll
+    for (int j = 0; j < LEAF_GROUPS; ++j) unpack(k[j], v + 8 * j);
     const Stats x = leaf_stats(v, c);
     if (lane == 0) leaves[l] = x;
   }
@@ -53,7 +56,7 @@ __global__ void __launch_bounds__(ROW_THREADS) token_logprobs_kernel(const Score
   const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const LogitRows& in = a.in;
   const auto* row = static_cast<const typename E::bits*>(in.base) + static_cast<int64_t>(t) * in.ld;
-  const Stats r = row_stats<E>(row, in.n, in.c, leaves);
+  const Stats r = row_stats(Row<E>(row, in.n), in.c, leaves);
   const float lse = row_lse(r, in.s);
   const bool bad = isnan(lse);
   const int64_t y = a.y ? a.y[t] : 0;
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(ROW_THREADS) distill_kernel(const DistillArgs 
                in.c, lane);
   float lse;
   if constexpr (FWD) {
-    lse = row_lse(row_stats<E>(row, in.n, in.c, leaves), in.s);
+    lse = row_lse(row_stats(Row<E>(row, in.n), in.c, leaves), in.s);
     if (warp == 0) {
       const float l = row_loss<E>(q, row, lse, in.s);
       if (lane == 0) {

@@ -32,16 +32,19 @@ constexpr uint32_t kFullWarp = 0xffffffffu;
 // ---------------------------------------------------------------------------
 struct Bf16 {
   using bits = uint16_t;
+  static constexpr bits kNegInf = 0xFF80u;
   static __device__ __forceinline__ float to_f32(bits b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
   static __device__ __forceinline__ bits from_f32(float v) { return static_cast<bits>(pack_bf16x2(v, 0.f) & 0xFFFFu); }
 };
 struct F16 {
   using bits = uint16_t;
+  static constexpr bits kNegInf = 0xFC00u;
   static __device__ __forceinline__ float to_f32(bits b) { return __half2float(__ushort_as_half(b)); }
   static __device__ __forceinline__ bits from_f32(float v) { return __half_as_ushort(__float2half_rn(v)); }
 };
 struct F32 {
   using bits = uint32_t;
+  static constexpr bits kNegInf = 0xFF800000u;
   static __device__ __forceinline__ float to_f32(bits b) { return __uint_as_float(b); }
   static __device__ __forceinline__ bits from_f32(float v) { return __float_as_uint(v); }
 };
@@ -55,6 +58,108 @@ struct LogitRows {
   float c;       // rn(s log2 e): e^{s d} = ex2(d c)
   int32_t* err_flag;
 };
+
+// ---------------------------------------------------------------------------
+// packs: 8 consecutive elements of a row, loaded as aligned 16-byte vectors
+// ---------------------------------------------------------------------------
+// Rows may start at any multiple of the element size (an odd row length in 16-bit types).
+// A pack that is not 16-byte aligned is cut from two (three for fp32) neighbouring aligned
+// vectors with funnel shifts: the second vector is the neighbouring lane's first and comes
+// from L1, and no lane ever owns other columns than in the aligned case, so alignment cannot
+// change the order of a sum. Only vectors that lie wholly inside the row are loaded; packs at
+// its ends fall back to single elements.
+template <class E>
+struct Pack {
+  static constexpr int EB = sizeof(typename E::bits);
+  static constexpr int WORDS = 2 * EB;  // 4 (16-bit types) or 8
+  uint32_t w[WORDS];
+};
+
+// A row (or the rest of one): its first n elements are valid.
+template <class E>
+struct Row {
+  const typename E::bits* p;
+  int32_t n;
+  uint32_t shift;  // bytes that p lies past a 16-byte boundary; the same for every thread
+  __device__ __forceinline__ Row(const typename E::bits* p_, int n_)
+      : p(p_), n(n_), shift(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p_) & 15u)) {}
+  __device__ __forceinline__ float at(int64_t c) const { return E::to_f32(p[c]); }
+};
+
+// True when pack columns [c0, c1) (multiples of 8) load as vectors inside the row.
+template <class E>
+__device__ __forceinline__ bool packs_inside(const Row<E>& r, int c0, int c1) {
+  if (r.shift == 0) return c1 <= r.n;
+  return c0 > 0 && c1 + static_cast<int>((16u - r.shift) / Pack<E>::EB) <= r.n;
+}
+
+__device__ __forceinline__ void ld_vec(uint32_t* w, const void* p) {
+  const uint4 v = *static_cast<const uint4*>(p);
+  w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+}
+
+// Pack at column c0 (a multiple of 8); packs_inside must hold for it.
+template <class E>
+__device__ __forceinline__ Pack<E> load_pack(const Row<E>& r, int c0) {
+  constexpr int W = Pack<E>::WORDS;
+  Pack<E> k;
+  const char* q = reinterpret_cast<const char*>(r.p) - r.shift + static_cast<int64_t>(c0) * Pack<E>::EB;
+  if (r.shift == 0) {
+#pragma unroll
+    for (int i = 0; i < W; i += 4) ld_vec(k.w + i, q + 4 * i);
+    return k;
+  }
+  uint32_t y[W + 4];
+#pragma unroll
+  for (int i = 0; i < W + 4; i += 4) ld_vec(y + i, q + 4 * i);
+  // words shift / 4 .. of y, then the bytes within a word
+  const bool two = r.shift & 8u, one = r.shift & 4u;
+  uint32_t x[W + 2];
+#pragma unroll
+  for (int i = 0; i < W + 2; ++i) x[i] = two ? y[i + 2] : y[i];
+  if constexpr (Pack<E>::EB == 4) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) k.w[i] = one ? x[i + 1] : x[i];
+  } else {
+    uint32_t t[W + 1];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) t[i] = one ? x[i + 1] : x[i];
+    const uint32_t bits = (r.shift & 3u) * 8u;
+#pragma unroll
+    for (int i = 0; i < W; ++i) k.w[i] = __funnelshift_r(t[i], t[i + 1], bits);
+  }
+  return k;
+}
+
+// Pack at column c0 near the row's ends, element by element; -inf beyond the row.
+template <class E>
+__device__ __forceinline__ Pack<E> load_pack_edge(const Row<E>& r, int c0) {
+  Pack<E> k;
+#pragma unroll
+  for (int i = 0; i < Pack<E>::WORDS; ++i) {
+    if constexpr (Pack<E>::EB == 4) {
+      k.w[i] = c0 + i < r.n ? r.p[c0 + i] : E::kNegInf;
+    } else {
+      const uint32_t lo = c0 + 2 * i < r.n ? r.p[c0 + 2 * i] : E::kNegInf;
+      const uint32_t hi = c0 + 2 * i + 1 < r.n ? r.p[c0 + 2 * i + 1] : E::kNegInf;
+      k.w[i] = lo | hi << 16;
+    }
+  }
+  return k;
+}
+
+template <class E>
+__device__ __forceinline__ void unpack(const Pack<E>& k, float* v) {
+#pragma unroll
+  for (int i = 0; i < Pack<E>::WORDS; ++i) {
+    if constexpr (Pack<E>::EB == 4) {
+      v[i] = E::to_f32(k.w[i]);
+    } else {
+      v[2 * i] = E::to_f32(static_cast<uint16_t>(k.w[i]));
+      v[2 * i + 1] = E::to_f32(static_cast<uint16_t>(k.w[i] >> 16));
+    }
+  }
+}
 
 // ---------------------------------------------------------------------------
 // row statistics
@@ -75,14 +180,19 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// Columns of a lane: v[8 j + e] is column 256 j + 8 lane + e of the leaf; -inf beyond the row.
+// Packs of a lane: k[j] holds columns 256 j + 8 lane .. + 7 of the leaf; -inf beyond the row.
 template <class E>
-__device__ __forceinline__ void load_leaf(const typename E::bits* row, int n, int leaf, int lane, float (&v)[32]) {
+__device__ __forceinline__ void load_leaf(const Row<E>& r, int leaf, int lane, Pack<E> (&k)[LEAF_GROUPS]) {
+  const int c0 = leaf * ROW_LEAF + lane * 8;
+  if (packs_inside(r, leaf * ROW_LEAF, (leaf + 1) * ROW_LEAF)) {  // the same for the whole warp
 #pragma unroll
-  for (int j = 0; j < LEAF_GROUPS; ++j) {
-    const int c0 = leaf * ROW_LEAF + j * LEAF_GROUP + lane * 8;
+    for (int j = 0; j < LEAF_GROUPS; ++j) k[j] = load_pack(r, c0 + j * LEAF_GROUP);
+  } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[8 * j + e] = c0 + e < n ? E::to_f32(row[c0 + e]) : neg_inf();
+    for (int j = 0; j < LEAF_GROUPS; ++j) {
+      const int c = c0 + j * LEAF_GROUP;
+      k[j] = packs_inside(r, c, c + 8) ? load_pack(r, c) : load_pack_edge(r, c);
+    }
   }
 }
 
