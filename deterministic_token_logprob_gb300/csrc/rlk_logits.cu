@@ -11,30 +11,173 @@ namespace rlk {
 namespace {
 
 constexpr int ROW_THREADS = 256;
-constexpr int ROW_WARPS = ROW_THREADS / 32;
+constexpr int MAX_CLUSTER = 8;                               // CTAs of one row (the portable cluster size)
+constexpr int MAX_ROW_WARPS = MAX_CLUSTER * 32;
+constexpr int GROUPS_PER_LEAF = LEAF_GROUPS;                 // 256-column groups, the units of the alternatives' search
+constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates that the search keeps
 
 // ---------------------------------------------------------------------------
-// statistics of one row by one CTA: every warp takes every ROW_WARPS-th leaf
+// one pass over a row by a cluster of CTAs (one CTA when there are rows enough)
 // ---------------------------------------------------------------------------
+// Warp g of the row's C x (blockDim / 32) warps takes leaves g, g + (number of warps), ... and
+// leaves what it found in the shared memory of the cluster's CTA 0 (distributed shared memory):
+// (m, s, u) of each leaf, the order keys of its four groups' maxima (TOP), and how many of its
+// columns stand ahead of the target (RANK).
+struct RowSmem {
+  Stats* leaf;      // [n_leaves]
+  uint32_t* key;    // [round_up(4 n_leaves, 128)]
+  int* count;       // [MAX_ROW_WARPS]
+};
+
+__host__ __device__ constexpr int leaves_of(int n) { return (n + ROW_LEAF - 1) / ROW_LEAF; }
+__host__ __device__ constexpr int keys_of(int n) { return (leaves_of(n) * GROUPS_PER_LEAF + 127) / 128 * 128; }
+
+struct RankOf {     // the target of the row, when its rank is wanted
+  bool on;
+  int y;
+  float z;
+  uint32_t ge, gt;  // its logit and the next value above it, in both halves of a word for 16-bit types
+};
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
+// a before b in the order of the alternatives
+__device__ __forceinline__ bool ahead(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+
+// Columns of this lane's packs that stand ahead of the target.
 template <class E>
-__device__ __forceinline__ Stats row_stats(const Row<E>& row, float c, Stats* leaves) {
+__device__ __forceinline__ int count_ahead(const Pack<E> (&k)[LEAF_GROUPS], const RankOf& q, int leaf, int lane) {
+  int n = 0;
+  if (leaf == q.y / ROW_LEAF) {
+#pragma unroll
+    for (int j = 0; j < LEAF_GROUPS; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 z = pair(k[j], i / 2);
+        n += ahead(i & 1 ? z.y : z.x, leaf * ROW_LEAF + j * LEAF_GROUP + lane * 8 + i, q.z, q.y);
+      }
+    return n;
+  }
+  const uint32_t bar = leaf < q.y / ROW_LEAF ? q.ge : q.gt;  // ties count before the target, not after
+  if constexpr (Pack<E>::EB == 4) {
+#pragma unroll
+    for (int j = 0; j < LEAF_GROUPS; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) n += __uint_as_float(k[j].w[i]) >= __uint_as_float(bar);
+  } else {
+    uint32_t acc = 0;
+#pragma unroll
+    for (int j = 0; j < LEAF_GROUPS; ++j)
+#pragma unroll
+      for (int i = 0; i < Pack<E>::WORDS; ++i) acc = E::count_ge2(k[j].w[i], bar, acc);
+    const float2 c = E::to_f32x2(acc);
+    n = static_cast<int>(c.x) + static_cast<int>(c.y);
+  }
+  return n;
+}
+
+template <class E, bool TOP>
+__device__ __forceinline__ void row_pass(const Row<E>& row, float c, const RankOf& rank, const RowSmem& sm, int C, int r) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n_leaves = (row.n + ROW_LEAF - 1) / ROW_LEAF;
-  for (int l = warp; l < n_leaves; l += ROW_WARPS) {
+  const int warps = blockDim.x >> 5, g = r * warps + warp, n_leaves = leaves_of(row.n);
+  if (C > 1) cluster_arrive();  // CTA 0 must have started before anyone writes to it
+  bool waited = C == 1;
+  const uint32_t leaf0 = map_to_cta(smem_u32(sm.leaf), 0), key0 = TOP ? map_to_cta(smem_u32(sm.key), 0) : 0;
+  int count = 0;
+  for (int l = g; l < n_leaves; l += C * warps) {
     Pack<E> k[LEAF_GROUPS];
     load_leaf(row, l, lane, k);
-    float v[32];
+    float gm[LEAF_GROUPS], m;
 #pragma unroll
-    for (int j = 0; j < LEAF_GROUPS; ++j) unpack(k[j], v + 8 * j);
-    const Stats x = leaf_stats(v, c);
-    if (lane == 0) leaves[l] = x;
+    for (int j = 0; j < LEAF_GROUPS; ++j) {
+      gm[j] = pack_max(k[j]);
+      if constexpr (TOP) gm[j] = warp_max(gm[j]);
+    }
+    m = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
+    if constexpr (!TOP) m = warp_max(m);
+    float part;  // lanes 0-15: s, lanes 16-31: u
+    if (m == neg_inf()) part = any_nan(k) && lane < 16 ? quiet_nan() : 0.f;
+    else part = leaf_sums(k, m, c, lane);
+    if (rank.on) count += count_ahead(k, rank, l, lane);
+    if (!waited) {
+      cluster_wait();
+      waited = true;
+    }
+    const uint32_t at = leaf0 + static_cast<uint32_t>(l * sizeof(Stats));
+    if (lane == 0) {
+      st_cluster_u32(at, __float_as_uint(m));
+      st_cluster_u32(at + 4, __float_as_uint(part));
+    }
+    if (lane == 16) st_cluster_u32(at + 8, __float_as_uint(part));
+    if (TOP && lane < GROUPS_PER_LEAF) {
+      const float v = lane < 2 ? (lane == 0 ? gm[0] : gm[1]) : (lane == 2 ? gm[2] : gm[3]);
+      const int i = l * GROUPS_PER_LEAF + lane;  // groups past the row take key 0: never chosen
+      st_cluster_u32(key0 + static_cast<uint32_t>(i * 4), i * LEAF_GROUP < row.n ? order_key(v) : 0u);
+    }
   }
-  __syncthreads();
-  return fold_leaves(leaves, n_leaves, c, lane);  // every warp: the same bits
+  if (!waited) cluster_wait();
+  if (rank.on) {
+    count = __reduce_add_sync(kFullWarp, count);
+    if (lane == 0) st_cluster_u32(map_to_cta(smem_u32(sm.count + g), 0), static_cast<uint32_t>(count));
+  }
+  if (TOP && r == 0)
+    for (int i = n_leaves * GROUPS_PER_LEAF + threadIdx.x; i < keys_of(row.n); i += blockDim.x) sm.key[i] = 0u;
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+}
+
+// ---------------------------------------------------------------------------
+// the best k of N keys, by one warp
+// ---------------------------------------------------------------------------
+// Chooses min(k, N) places of key[0 .. N) -- the largest keys, the lower place first among equals --
+// writes them to `place` in ascending order and returns the smallest chosen key >> shift. N is
+// padded with zero keys to a multiple of 128. The keys hold nothing in their low `shift` bits, so
+// the search (bisection on the key, counting the keys at or above the middle) ends after at most
+// 32 - shift rounds; usually it hits a key that exactly k reach earlier.
+__device__ __forceinline__ uint32_t choose_best(const uint32_t* key, int N, int k, int shift, int* place, int lane) {
+  const int padded = (N + 127) / 128 * 128;
+  const auto count_from = [&](uint32_t bar) {
+    int n = 0;
+    for (int i = lane * 4; i < padded; i += 128) {
+      const uint4 v = *reinterpret_cast<const uint4*>(key + i);
+      n += (v.x >> shift >= bar) + (v.y >> shift >= bar) + (v.z >> shift >= bar) + (v.w >> shift >= bar);
+    }
+    return __reduce_add_sync(kFullWarp, n);
+  };
+  // 32 lanes' maxima: 32 places reach the smallest of them
+  uint32_t top = 0;
+  for (int i = lane; i < N; i += 32) top = max(top, key[i]);
+  uint32_t hi = (__reduce_max_sync(kFullWarp, top) >> shift) + 1;       // fewer than k reach it
+  uint32_t lo = k <= 32 && N >= 32 ? __reduce_min_sync(kFullWarp, top) >> shift : 0u;  // at least min(k, N) do
+  if (k >= N) hi = lo = 0;
+  while (hi - lo > 1) {
+    const uint32_t mid = lo + (hi - lo) / 2;
+    const int n = count_from(mid);
+    if (n >= k) lo = mid;
+    else hi = mid;
+    if (n == k) break;
+  }
+  int ties = k;  // places at lo that are taken
+  if (k < N) ties -= count_from(lo + 1);
+  int out = 0;
+  for (int i0 = 0; i0 < N; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t v = i < N ? key[i] >> shift : 0u;
+    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t eq = __ballot_sync(kFullWarp, i < N && v == lo);
+    const bool take = i < N && (v > lo || (v == lo && __popc(eq & below) < ties));
+    const uint32_t taken = __ballot_sync(kFullWarp, take);
+    if (take) place[out + __popc(taken & below)] = i;
+    out += __popc(taken);
+    ties -= min(ties, __popc(eq));
+  }
+  return lo;
 }
 
 struct ScoreArgs {
   LogitRows in;
+  int32_t cluster;
   const int64_t* y;
   int32_t top_k;
   float* logp;
@@ -45,68 +188,171 @@ struct ScoreArgs {
   float* top_logp;
 };
 
-// a before b in the order of the alternatives
-__device__ __forceinline__ bool ahead(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+// Shared memory of the alternatives' search.
+struct TopSmem {
+  unsigned long long cand[CAND];   // order key in the high word, ~column in the low one
+  int place[RLK_MAX_TOP_K];        // chosen groups, then chosen octets
+  int n_cand;
+  uint32_t bar;                    // smallest chosen key >> kKeyShift
+  float lse;
+};
 
+// Dynamic shared memory of a row: the octets' keys take the place of the leaves' statistics and the
+// groups' keys, which have been used by then.
+__host__ __device__ constexpr size_t row_smem_bytes(int n, bool top) {
+  size_t b = static_cast<size_t>((leaves_of(n) * sizeof(Stats) + 15) / 16 * 16);
+  if (!top) return b;
+  b += static_cast<size_t>(keys_of(n)) * 4;
+  const size_t octets = RLK_MAX_TOP_K * 32 * 4;
+  return b > octets ? b : octets;
+}
+
+// The top_k alternatives of a row, by one CTA, from its groups' keys.
+//  1. The k groups of 256 columns with the largest maxima (lower group first among equals) hold
+//     the k best columns: a column outside them has k group maxima ahead of it.
+//  2. Their columns that reach the smallest chosen maximum are the candidates: k or a few more,
+//     unless good columns crowd into few groups or are tied.
+//  3. If they are too many, the same choice among the chosen groups' octets (8 columns) leaves
+//     at most 8 k.
+//  4. Each candidate's place is the number of candidates ahead of it.
 template <class E>
-__global__ void __launch_bounds__(ROW_THREADS) token_logprobs_kernel(const ScoreArgs a) {
-  extern __shared__ Stats leaves[];
-  __shared__ float best_v[ROW_WARPS];
-  __shared__ int best_i[ROW_WARPS];
-  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const LogitRows& in = a.in;
-  const auto* row = static_cast<const typename E::bits*>(in.base) + static_cast<int64_t>(t) * in.ld;
-  const Stats r = row_stats(Row<E>(row, in.n), in.c, leaves);
-  const float lse = row_lse(r, in.s);
-  const bool bad = isnan(lse);
-  const int64_t y = a.y ? a.y[t] : 0;
-  const bool y_ok = y >= 0 && y < in.n;
-  const float zy = y_ok ? E::to_f32(row[y]) : 0.f;
-  int ahead_of_y = 0;
-  if (a.rank && y_ok && !bad)
-    for (int v = threadIdx.x; v < in.n; v += ROW_THREADS) ahead_of_y += ahead(E::to_f32(row[v]), v, zy, static_cast<int>(y));
-  ahead_of_y = __reduce_add_sync(kFullWarp, ahead_of_y);
-  if (lane == 0) best_i[warp] = ahead_of_y;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int rank = 1;
-    for (int w = 0; w < ROW_WARPS; ++w) rank += best_i[w];
-    if (a.lse) a.lse[t] = lse;
-    if (a.entropy) a.entropy[t] = row_entropy(r, in.s);
-    if (a.logp) a.logp[t] = y_ok && !bad ? token_logp(zy, in.s, lse) : quiet_nan();
-    if (a.rank) a.rank[t] = y_ok && !bad ? rank : 0;
-    if (in.err_flag && bad) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
-    if (in.err_flag && a.y && !y_ok) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
-  }
-  // k rounds: the best column after the one chosen last
-  float pv = __int_as_float(0x7f800000);
-  int pi = -1;
-  for (int k = 0; k < a.top_k; ++k) {
-    float bv = neg_inf();
-    int bi = INT32_MAX;
-    if (!bad)
-      for (int v = threadIdx.x; v < in.n; v += ROW_THREADS) {
-        const float z = E::to_f32(row[v]);
-        if (ahead(pv, pi, z, v) && ahead(z, v, bv, bi)) bv = z, bi = v;
-      }
+__device__ void find_top(const Row<E>& row, const ScoreArgs& a, int64_t t, const RowSmem& sm, TopSmem& ts,
+                         bool bad, float lse) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int groups = (row.n + LEAF_GROUP - 1) / LEAF_GROUP, K = a.top_k, chosen = min(K, groups);
+  constexpr int FEW = 256;
+  const auto pack_of = [&](int c) {
+    return packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c);
+  };
+  const auto offer = [&](float z, int col, uint32_t bar, int most) {
+    const uint32_t o = order_key(z);
+    if (o >> E::kKeyShift < bar || z == neg_inf()) return;
+    const int at = atomicAdd(&ts.n_cand, 1);
+    if (at < most) ts.cand[at] = static_cast<unsigned long long>(o) << 32 | static_cast<uint32_t>(~col);
+  };
+  const uint32_t bar = ts.bar;
+  if (!bad) {
+    for (int i0 = warp; i0 < chosen; i0 += 4 * warps) {
+      Pack<E> k[4];
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) {
-      const float ov = __shfl_xor_sync(kFullWarp, bv, d);
-      const int oi = __shfl_xor_sync(kFullWarp, bi, d);
-      if (ahead(ov, oi, bv, bi)) bv = ov, bi = oi;
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * warps < chosen) k[u] = pack_of(ts.place[i0 + u * warps] * LEAF_GROUP + lane * 8);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (i0 + u * warps >= chosen) break;
+        const float m = pack_max(k[u]);
+        if (order_key(m) >> E::kKeyShift < bar || m == neg_inf()) continue;
+        const int c = ts.place[i0 + u * warps] * LEAF_GROUP + lane * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 z = pair(k[u], i / 2);
+          offer(i & 1 ? z.y : z.x, c + i, bar, FEW);
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (ts.n_cand > FEW) {  // the same for the whole CTA
+    uint32_t* okey = reinterpret_cast<uint32_t*>(sm.leaf);
+    const int N = chosen * 32;
+    for (int i = warp; i < chosen; i += warps)
+      okey[i * 32 + lane] = order_key(pack_max(pack_of(ts.place[i] * LEAF_GROUP + lane * 8)));
+    for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) okey[i] = 0u;
+    __syncthreads();
+    int* octet = reinterpret_cast<int*>(ts.cand) + 2 * CAND - RLK_MAX_TOP_K;  // not yet in use
+    if (warp == 0) {
+      const uint32_t b = choose_best(okey, N, min(K, N), E::kKeyShift, octet, lane);
+      if (lane == 0) ts.bar = b, ts.n_cand = 0;
     }
     __syncthreads();
-    if (lane == 0) best_v[warp] = bv, best_i[warp] = bi;
-    __syncthreads();
-    bv = best_v[0], bi = best_i[0];
-    for (int w = 1; w < ROW_WARPS; ++w)
-      if (ahead(best_v[w], best_i[w], bv, bi)) bv = best_v[w], bi = best_i[w];
-    const bool none = bv == neg_inf();
-    if (threadIdx.x == 0) {
-      a.top_ids[static_cast<int64_t>(t) * a.top_k + k] = none ? -1 : bi;
-      a.top_logp[static_cast<int64_t>(t) * a.top_k + k] = bad ? quiet_nan() : none ? neg_inf() : token_logp(bv, in.s, lse);
+    int mine = -1;  // first column of this thread's octet
+    if (threadIdx.x < min(K, N)) {
+      const int o = octet[threadIdx.x];
+      mine = ts.place[o / 32] * LEAF_GROUP + o % 32 * 8;
     }
-    pv = bv, pi = bi;
+    const uint32_t b2 = ts.bar;
+    __syncthreads();
+    if (mine >= 0) {
+      const Pack<E> k = pack_of(mine);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 z = pair(k, i / 2);
+        offer(i & 1 ? z.y : z.x, mine + i, b2, CAND);
+      }
+    }
+    __syncthreads();
+  }
+  const int n = ts.n_cand;
+  int64_t* ids = a.top_ids + t * K;
+  float* lps = a.top_logp + t * K;
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    const unsigned long long me = ts.cand[i];
+    int place = 0;
+    for (int j = 0; j < n; ++j) place += ts.cand[j] > me;
+    if (place < K) {
+      ids[place] = static_cast<int64_t>(~static_cast<uint32_t>(me));
+      lps[place] = token_logp(key_value(static_cast<uint32_t>(me >> 32)), a.in.s, lse);
+    }
+  }
+  for (int i = n + threadIdx.x; i < K; i += blockDim.x) {
+    ids[i] = -1;
+    lps[i] = bad ? quiet_nan() : neg_inf();
+  }
+}
+
+template <class E, bool TOP>
+__global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const ScoreArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ int counts[MAX_ROW_WARPS];
+  __shared__ __align__(16) unsigned char top_raw[TOP ? sizeof(TopSmem) : 16];
+  TopSmem& ts = *reinterpret_cast<TopSmem*>(top_raw);
+  const LogitRows& in = a.in;
+  const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x / C;
+  const Row<E> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
+  RowSmem sm;
+  sm.leaf = reinterpret_cast<Stats*>(dyn);
+  sm.key = reinterpret_cast<uint32_t*>(dyn + (leaves_of(in.n) * sizeof(Stats) + 15) / 16 * 16);
+  sm.count = counts;
+  const int64_t y = a.y ? a.y[t] : -1;
+  const bool y_ok = y >= 0 && y < in.n;
+  RankOf rank{a.rank != nullptr && y_ok, static_cast<int>(y), 0.f, 0u, 0u};
+  if (y_ok) {
+    const typename E::bits b = row.p[y];
+    rank.z = E::to_f32(b);
+    rank.ge = b;
+    rank.gt = next_above<E>(b);
+    if constexpr (Pack<E>::EB == 2) rank.ge *= 0x10001u, rank.gt *= 0x10001u;
+  }
+  if (TOP && threadIdx.x == 0) ts.n_cand = 0;
+  row_pass<E, TOP>(row, in.c, rank, sm, C, r);
+  if (r != 0) return;
+  if (warp == 1) {
+    const Stats x = fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane);
+    const float lse = row_lse(x, in.s);
+    const bool bad = isnan(lse);
+    int before = 0;
+    if (rank.on)
+      for (int i = lane; i < C * (ROW_THREADS / 32); i += 32) before += counts[i];
+    before = __reduce_add_sync(kFullWarp, before);
+    if (lane == 0) {
+      if (TOP) ts.lse = lse;
+      if (a.lse) a.lse[t] = lse;
+      if (a.entropy) a.entropy[t] = row_entropy(x, in.s);
+      if (a.logp) a.logp[t] = y_ok && !bad ? token_logp(rank.z, in.s, lse) : quiet_nan();
+      if (a.rank) a.rank[t] = y_ok && !bad ? 1 + before : 0;
+      if (in.err_flag && bad) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
+      if (in.err_flag && a.y && !y_ok) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
+    }
+  }
+  if constexpr (TOP) {
+    if (warp == 0) {
+      const int groups = (in.n + LEAF_GROUP - 1) / LEAF_GROUP;
+      const uint32_t b = choose_best(sm.key, groups, min(a.top_k, groups), E::kKeyShift, ts.place, lane);
+      if (lane == 0) ts.bar = b;
+    }
+    __syncthreads();
+    find_top(row, a, t, sm, ts, isnan(ts.lse), ts.lse);
   }
 }
 
@@ -156,6 +402,7 @@ __global__ void __launch_bounds__(ROW_THREADS) token_grad_kernel(const TokenGrad
 struct DistillArgs {
   LogitRows in;
   GradOut out;
+  int32_t cluster;
   const int64_t* ids;
   const float* teacher;
   int32_t K;
@@ -167,81 +414,109 @@ struct DistillArgs {
 
 // Loss of one row by one warp (every lane gets it).
 template <class E>
-__device__ __forceinline__ float row_loss(const Teacher& q, const typename E::bits* row, float lse, float s) {
+__device__ __forceinline__ float row_loss(const TeacherRow& q, const Row<E>& row, float lse, float s, int lane) {
   float sum = 0.f;
 #pragma unroll
-  for (int i = 0; i < RLK_MAX_TOP_K / 32; ++i)
-    if (q.q[i] > 0.f)
-      sum = __fmaf_rn(q.q[i], __fsub_rn(q.logq[i], token_logp(E::to_f32(row[q.id[i]]), s, lse)), sum);
+  for (int i = 0; i < RLK_MAX_TOP_K / 32; ++i) {
+    const int k = lane + 32 * i;
+    if (q.t[k] > 0.f) sum = __fmaf_rn(q.t[k], __fsub_rn(q.logq[k], token_logp(row.at(q.id[k]), s, lse)), sum);
+  }
   return warp_sum(sum);
 }
 
 template <class E, class O, bool FWD, bool BWD>
-__global__ void __launch_bounds__(ROW_THREADS) distill_kernel(const DistillArgs a) {
-  extern __shared__ Stats leaves[];
-  __shared__ int ids[RLK_MAX_TOP_K];
-  __shared__ float qs[RLK_MAX_TOP_K], zs[RLK_MAX_TOP_K];
-  const int t = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ TeacherRow q;
+  __shared__ float zs[RLK_MAX_TOP_K];
+  __shared__ float row_lse_s;
   const LogitRows& in = a.in;
-  const auto* row = static_cast<const typename E::bits*>(in.base) + static_cast<int64_t>(t) * in.ld;
-  Teacher q;
-  load_teacher(q, a.ids + static_cast<int64_t>(t) * a.K, a.teacher + static_cast<int64_t>(t) * a.K, a.K, in.n, in.s,
-               in.c, lane);
-  float lse;
+  const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x / C;
+  const Row<E> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
+  if (warp == 1 && (BWD || r == 0))
+    teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, lane);
   if constexpr (FWD) {
-    lse = row_lse(row_stats(Row<E>(row, in.n), in.c, leaves), in.s);
-    if (warp == 0) {
-      const float l = row_loss<E>(q, row, lse, in.s);
+    RowSmem sm{reinterpret_cast<Stats*>(dyn), nullptr, nullptr};
+    row_pass<E, false>(row, in.c, RankOf{false, 0, 0.f, 0u, 0u}, sm, C, r);
+    if (r == 0 && warp == 0) {
+      const float lse = row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s);
+      if (BWD && lane < C) st_cluster_u32(map_to_cta(smem_u32(&row_lse_s), lane), __float_as_uint(lse));
+      const float l = row_loss<E>(q, row, lse, in.s, lane);
       if (lane == 0) {
-        a.loss[t] = isnan(lse) || q.bad_id || q.nonfinite ? quiet_nan() : l;
+        a.loss[t] = isnan(lse) || q.bad ? quiet_nan() : l;
         if (a.lse) a.lse[t] = lse;
-        if (in.err_flag && (isnan(lse) || q.nonfinite)) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
+        if (isnan(lse) && in.err_flag) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
       }
+    }
+    if constexpr (!BWD) {
+      if (r != 0) return;
     }
   } else {
-    lse = a.lse_in[t];
-    if (threadIdx.x == 0 && in.err_flag && q.nonfinite) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
+    if (threadIdx.x == 0) row_lse_s = a.lse_in[t];
   }
-  if (threadIdx.x == 0 && in.err_flag && q.bad_id) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
   if constexpr (BWD) {
-    auto* out = static_cast<typename O::bits*>(a.out.base) + static_cast<int64_t>(t) * a.out.ld;
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+    const float lse = row_lse_s;
+    auto* out = static_cast<typename O::bits*>(a.out.base) + t * a.out.ld;
     const float g = a.g[t];
-    const bool live = !isnan(lse) && lse != neg_inf() && q.any && !q.bad_id && !q.nonfinite && g != 0.f;
+    const bool live = !isnan(lse) && lse != neg_inf() && q.any && !q.bad && g != 0.f;
     const float A = __fmul_rn(in.s, g);
-    if (warp == 0) {
-#pragma unroll
-      for (int i = 0; i < RLK_MAX_TOP_K / 32; ++i) {
-        const int k = lane + 32 * i;
-        const bool some = live && q.q[i] > 0.f;
-        ids[k] = some ? static_cast<int>(q.id[i]) : -1;
-        qs[k] = some ? q.q[i] : 0.f;
-        zs[k] = some ? E::to_f32(row[q.id[i]]) : 0.f;
-      }
-    }
+    const int span = (a.out.V + C - 1) / C, lo = r * span, hi = min(a.out.V, lo + span);
+    for (int k = threadIdx.x; k < a.K; k += ROW_THREADS)
+      zs[k] = live && q.id[k] >= lo && q.id[k] < hi ? row.at(q.id[k]) : 0.f;
     __syncthreads();
-    for (int v = threadIdx.x; v < a.out.V; v += ROW_THREADS) {
+    for (int v = lo + threadIdx.x; v < hi; v += ROW_THREADS) {
       float dz = 0.f;
-      if (live && v < in.n) dz = __fmul_rn(A, prob_of(__fmaf_rn(E::to_f32(row[v]), in.s, -lse)));
+      if (live && v < in.n) dz = __fmaf_rn(A, prob_of(__fmaf_rn(row.at(v), in.s, -lse)), 0.f);
       out[v] = O::from_f32(dz);
     }
     __syncthreads();
     // the teacher's columns: the first entry of an id writes the sum over its entries
     for (int k = threadIdx.x; k < a.K; k += ROW_THREADS) {
-      const int id = ids[k];
-      bool first = id >= 0;
+      const int id = q.id[k];
+      if (!live || id < lo || id >= hi) continue;
+      bool first = true;
       float qk = 0.f;
       for (int j = 0; j < a.K; ++j) {
-        if (ids[j] != id) continue;
+        if (q.id[j] != id) continue;
         if (j < k) first = false;
-        qk = __fadd_rn(qk, qs[j]);
+        qk = __fadd_rn(qk, q.t[j]);
       }
       if (first) out[id] = O::from_f32(__fmul_rn(A, __fsub_rn(prob_of(__fmaf_rn(zs[k], in.s, -lse)), qk)));
     }
+  } else {
+    __syncthreads();
   }
+  if (r == 0 && threadIdx.x == 0 && q.bad && in.err_flag) atomicOr(in.err_flag, q.bad);
 }
 
-size_t leaves_bytes(const LogitRows& in) {
-  return static_cast<size_t>((in.n + ROW_LEAF - 1) / ROW_LEAF) * sizeof(Stats);
+// CTAs of ROW_THREADS per row: one where the rows fill the GPU, else up to MAX_CLUSTER so that few
+// rows still spread over it; never more than the row has leaves for.
+int row_cluster(const LogitRows& in) {
+  constexpr int64_t kResident = 4 * 152;  // CTAs of ROW_THREADS that run at once
+  int c = 1;
+  while (c < MAX_CLUSTER && 2 * c * in.T <= kResident && 2 * c * (ROW_THREADS / 32) <= 2 * leaves_of(in.n)) c *= 2;
+  return c;
+}
+
+// Launches a row kernel: `cluster` CTAs for each of T rows.
+template <class K, class A>
+rlk_status launch_rows(K kernel, const A& args, int64_t T, int cluster, size_t smem, void* stream) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(T * cluster));
+  cfg.blockDim = dim3(ROW_THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 1 : 0;
+  if (cudaLaunchKernelEx(&cfg, kernel, args) != cudaSuccess) return RLK_ERR_CUDA;
+  return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
 }
 
 rlk_status launched() { return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA; }
@@ -302,11 +577,15 @@ rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
   a.entropy = entropy;
   a.top_ids = top_ids;
   a.top_logp = top_logp;
-  with_types(dtype, dtype, [&](auto e, auto) {
-    token_logprobs_kernel<decltype(e)><<<static_cast<unsigned>(T), ROW_THREADS, leaves_bytes(a.in),
-                                         static_cast<cudaStream_t>(stream)>>>(a);
-  });
-  return launched();
+  a.cluster = row_cluster(a.in);
+  const auto run = [&](auto kernel, bool top) {
+    return launch_rows(kernel, a, T, a.cluster, row_smem_bytes(a.in.n, top), stream);
+  };
+  switch (dtype) {
+    case RLK_DTYPE_BF16: return top_k ? run(token_logprobs_kernel<Bf16, true>, true) : run(token_logprobs_kernel<Bf16, false>, false);
+    case RLK_DTYPE_F16: return top_k ? run(token_logprobs_kernel<F16, true>, true) : run(token_logprobs_kernel<F16, false>, false);
+    default: return top_k ? run(token_logprobs_kernel<F32, true>, true) : run(token_logprobs_kernel<F32, false>, false);
+  }
 }
 
 rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
@@ -349,12 +628,14 @@ rlk_status check_distill(const void* logits, int32_t dtype, int64_t T, int64_t l
 }
 
 template <bool FWD, bool BWD>
-rlk_status launch_distill(const DistillArgs& a, int32_t dtype, int32_t out_dtype, void* stream) {
+rlk_status launch_distill(DistillArgs& a, int32_t dtype, int32_t out_dtype, void* stream) {
+  a.cluster = row_cluster(a.in);
+  rlk_status st = RLK_OK;
   with_types(dtype, out_dtype, [&](auto e, auto o) {
-    distill_kernel<decltype(e), decltype(o), FWD, BWD>
-        <<<static_cast<unsigned>(a.in.T), ROW_THREADS, leaves_bytes(a.in), static_cast<cudaStream_t>(stream)>>>(a);
+    st = launch_rows(distill_kernel<decltype(e), decltype(o), FWD, BWD>, a, a.in.T, a.cluster,
+                     row_smem_bytes(a.in.n, false), stream);
   });
-  return launched();
+  return st;
 }
 
 }  // namespace

@@ -14,6 +14,7 @@
 // launch shape or on which CTA took which leaf.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include "rlk.h"
@@ -33,21 +34,96 @@ constexpr uint32_t kFullWarp = 0xffffffffu;
 struct Bf16 {
   using bits = uint16_t;
   static constexpr bits kNegInf = 0xFF80u;
+  static constexpr int kKeyShift = 16;  // low bits of the fp32 image that carry nothing
   static __device__ __forceinline__ float to_f32(bits b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
   static __device__ __forceinline__ bits from_f32(float v) { return static_cast<bits>(pack_bf16x2(v, 0.f) & 0xFFFFu); }
+  static __device__ __forceinline__ float2 to_f32x2(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmax2(reinterpret_cast<__nv_bfloat162&>(a), reinterpret_cast<__nv_bfloat162&>(b));
+    return reinterpret_cast<const uint32_t&>(r);
+  }
+  // acc + (a >= b), per half; counts up to 256 are exact
+  static __device__ __forceinline__ uint32_t count_ge2(uint32_t a, uint32_t b, uint32_t acc) {
+    const __nv_bfloat162 r = __hadd2(reinterpret_cast<__nv_bfloat162&>(acc),
+                                     __hge2(reinterpret_cast<__nv_bfloat162&>(a), reinterpret_cast<__nv_bfloat162&>(b)));
+    return reinterpret_cast<const uint32_t&>(r);
+  }
 };
 struct F16 {
   using bits = uint16_t;
   static constexpr bits kNegInf = 0xFC00u;
+  static constexpr int kKeyShift = 13;
   static __device__ __forceinline__ float to_f32(bits b) { return __half2float(__ushort_as_half(b)); }
   static __device__ __forceinline__ bits from_f32(float v) { return __half_as_ushort(__float2half_rn(v)); }
+  static __device__ __forceinline__ float2 to_f32x2(uint32_t w) {
+    return __half22float2(reinterpret_cast<const __half2&>(w));
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmax2(reinterpret_cast<__half2&>(a), reinterpret_cast<__half2&>(b));
+    return reinterpret_cast<const uint32_t&>(r);
+  }
+  static __device__ __forceinline__ uint32_t count_ge2(uint32_t a, uint32_t b, uint32_t acc) {
+    const __half2 r = __hadd2(reinterpret_cast<__half2&>(acc),
+                              __hge2(reinterpret_cast<__half2&>(a), reinterpret_cast<__half2&>(b)));
+    return reinterpret_cast<const uint32_t&>(r);
+  }
 };
 struct F32 {
   using bits = uint32_t;
   static constexpr bits kNegInf = 0xFF800000u;
+  static constexpr int kKeyShift = 0;
   static __device__ __forceinline__ float to_f32(bits b) { return __uint_as_float(b); }
   static __device__ __forceinline__ bits from_f32(float v) { return __float_as_uint(v); }
 };
+
+// The next value above b in its type (b not NaN or +inf): z > b exactly when z >= next_above(b).
+template <class E>
+__device__ __forceinline__ typename E::bits next_above(typename E::bits b) {
+  using B = typename E::bits;
+  constexpr B sign = static_cast<B>(B(1) << (8 * sizeof(B) - 1));
+  if ((b & static_cast<B>(~sign)) == 0) return 1;  // either zero
+  return static_cast<B>((b & sign) ? b - 1 : b + 1);
+}
+
+// Order-preserving unsigned image of a float (both zeros alike) and back.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = __float_as_uint(__fadd_rn(v, 0.f));
+  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
+}
+
+// Two fp32 values in one 64-bit register: one instruction rounds both (the same rounding as the
+// scalar operations).
+using F32x2 = unsigned long long;
+__device__ __forceinline__ F32x2 pack_f32x2(float lo, float hi) {
+  F32x2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(F32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ F32x2 add2(F32x2 a, F32x2 b) {
+  F32x2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F32x2 mul2(F32x2 a, F32x2 b) {
+  F32x2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ F32x2 fma2(F32x2 a, F32x2 b, F32x2 c) {
+  F32x2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 // One launch's logits: T rows of `ld` elements, the first n (= V_true) of each valid.
 struct LogitRows {
@@ -81,9 +157,10 @@ struct Row {
   const typename E::bits* p;
   int32_t n;
   uint32_t shift;  // bytes that p lies past a 16-byte boundary; the same for every thread
-  __device__ __forceinline__ Row(const typename E::bits* p_, int n_)
-      : p(p_), n(n_), shift(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p_) & 15u)) {}
-  __device__ __forceinline__ float at(int64_t c) const { return E::to_f32(p[c]); }
+  int32_t* err;    // for the index checks of debug-checks builds
+  __device__ __forceinline__ Row(const typename E::bits* p_, int n_, int32_t* err_)
+      : p(p_), n(n_), shift(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p_) & 15u)), err(err_) {}
+  __device__ __forceinline__ float at(int64_t c) const { return dbg_ok(c >= 0 && c < n, err) ? E::to_f32(p[c]) : 0.f; }
 };
 
 // True when pack columns [c0, c1) (multiples of 8) load as vectors inside the row.
@@ -102,7 +179,13 @@ __device__ __forceinline__ void ld_vec(uint32_t* w, const void* p) {
 template <class E>
 __device__ __forceinline__ Pack<E> load_pack(const Row<E>& r, int c0) {
   constexpr int W = Pack<E>::WORDS;
-  Pack<E> k;
+  Pack<E> k{};
+  // the first byte of the first vector and the last of the last one lie in the row
+  if (!dbg_ok(c0 >= 0 && static_cast<int64_t>(c0) * Pack<E>::EB >= r.shift &&
+                  static_cast<int64_t>(c0 + 8) * Pack<E>::EB + (r.shift ? 16 - r.shift : 0) <=
+                      static_cast<int64_t>(r.n) * Pack<E>::EB,
+              r.err))
+    return k;
   const char* q = reinterpret_cast<const char*>(r.p) - r.shift + static_cast<int64_t>(c0) * Pack<E>::EB;
   if (r.shift == 0) {
 #pragma unroll
@@ -148,16 +231,24 @@ __device__ __forceinline__ Pack<E> load_pack_edge(const Row<E>& r, int c0) {
   return k;
 }
 
+// Elements 2 i and 2 i + 1 of a pack.
 template <class E>
-__device__ __forceinline__ void unpack(const Pack<E>& k, float* v) {
+__device__ __forceinline__ float2 pair(const Pack<E>& k, int i) {
+  if constexpr (Pack<E>::EB == 4) return make_float2(__uint_as_float(k.w[2 * i]), __uint_as_float(k.w[2 * i + 1]));
+  else return E::to_f32x2(k.w[i]);
+}
+
+// Largest element of a pack (NaN is passed over).
+template <class E>
+__device__ __forceinline__ float pack_max(const Pack<E>& k) {
+  if constexpr (Pack<E>::EB == 4) {
+    float m = __uint_as_float(k.w[0]);
 #pragma unroll
-  for (int i = 0; i < Pack<E>::WORDS; ++i) {
-    if constexpr (Pack<E>::EB == 4) {
-      v[i] = E::to_f32(k.w[i]);
-    } else {
-      v[2 * i] = E::to_f32(static_cast<uint16_t>(k.w[i]));
-      v[2 * i + 1] = E::to_f32(static_cast<uint16_t>(k.w[i] >> 16));
-    }
+    for (int i = 1; i < 8; ++i) m = fmaxf(m, __uint_as_float(k.w[i]));
+    return m;
+  } else {
+    const float2 m = E::to_f32x2(E::max2(E::max2(k.w[0], k.w[1]), E::max2(k.w[2], k.w[3])));
+    return fmaxf(m.x, m.y);
   }
 }
 
@@ -169,9 +260,9 @@ struct Stats {
 };
 
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) v = fmaxf(v, __shfl_xor_sync(kFullWarp, v, d));
-  return v;
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -196,29 +287,64 @@ __device__ __forceinline__ void load_leaf(const Row<E>& r, int leaf, int lane, P
   }
 }
 
-// Statistics of one leaf, the same in every lane. NaN or +inf among the columns makes s NaN;
-// a leaf that is -inf throughout gives {-inf, 0, 0}.
-__device__ __forceinline__ Stats leaf_stats(const float (&v)[32], float c) {
-  float m = v[0];
+// Butterfly sums of two values with one exchange a level: lanes 0-15 end with the sum of a,
+// lanes 16-31 with the sum of b (the bits of warp_sum).
+__device__ __forceinline__ float warp_sum_pair(float a, float b, int lane) {
+  const bool low = lane < 16;
+  float v = __fadd_rn(low ? a : b, __shfl_xor_sync(kFullWarp, low ? b : a, 16));
 #pragma unroll
-  for (int i = 1; i < 32; ++i) m = fmaxf(m, v[i]);
-  bool nan = false;  // fmaxf drops NaN: only a leaf of nothing but -inf and NaN needs the test
+  for (int d = 8; d >= 1; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFullWarp, v, d));
+  return v;
+}
+
+// s and u of a leaf about its maximum m (not -inf): lanes 0-15 return s, lanes 16-31 u. NaN or
+// +inf among the columns makes s NaN.
+template <class E>
+__device__ __forceinline__ float leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], float m, float c, int lane) {
+  const F32x2 nm = pack_f32x2(-m, -m), cc = pack_f32x2(c, c);
+  F32x2 s2 = 0, u2 = 0;  // even and odd columns
 #pragma unroll
-  for (int i = 0; i < 32; ++i) nan |= isnan(v[i]);
-  m = warp_max(m);
-  nan = __any_sync(kFullWarp, nan);
-  if (m == neg_inf()) return Stats{m, nan ? __int_as_float(0x7fc00000) : 0.f, 0.f};
-  float s2[2] = {0.f, 0.f}, u2[2] = {0.f, 0.f};
+  for (int j = 0; j < LEAF_GROUPS; ++j)
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    // -inf columns have weight 0: a finite d keeps 0 * d out of NaN (fmaxf(NaN, x) = x, but
-    // the NaN reaches s through the weight)
-    const float d = __fsub_rn(v[i], m);
-    const float w = ex2_approx(__fmul_rn(d, c));
-    s2[i & 1] = __fadd_rn(s2[i & 1], w);
-    u2[i & 1] = __fmaf_rn(w, fmaxf(d, -3.4028235e38f), u2[i & 1]);
+    for (int i = 0; i < 4; ++i) {
+      const float2 z = pair(k[j], i);
+      const F32x2 d = add2(pack_f32x2(z.x, z.y), nm);
+      const float2 x = unpack_f32x2(mul2(d, cc));
+      const F32x2 w = pack_f32x2(ex2_approx(x.x), ex2_approx(x.y));
+      s2 = add2(s2, w);
+      u2 = fma2(w, d, u2);
+    }
+  const float2 s = unpack_f32x2(s2), u = unpack_f32x2(u2);
+  const float sl = __fadd_rn(s.x, s.y);
+  float ul = __fadd_rn(u.x, u.y);
+  if (__any_sync(kFullWarp, isnan(ul))) {
+    // masked columns: weight 0 times d = -inf. Once more with d kept finite (a NaN logit reaches
+    // s through its weight); every other term is what it was.
+    float v[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < LEAF_GROUPS; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 z = pair(k[j], i / 2);
+        const float d = __fsub_rn(i & 1 ? z.y : z.x, m);
+        v[i & 1] = __fmaf_rn(ex2_approx(__fmul_rn(d, c)), fmaxf(d, -3.4028235e38f), v[i & 1]);
+      }
+    ul = __fadd_rn(v[0], v[1]);
   }
-  return Stats{m, warp_sum(__fadd_rn(s2[0], s2[1])), warp_sum(__fadd_rn(u2[0], u2[1]))};
+  return warp_sum_pair(sl, ul, lane);
+}
+
+template <class E>
+__device__ __forceinline__ bool any_nan(const Pack<E> (&k)[LEAF_GROUPS]) {
+  bool nan = false;
+#pragma unroll
+  for (int j = 0; j < LEAF_GROUPS; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 z = pair(k[j], i);
+      nan |= isnan(z.x) || isnan(z.y);
+    }
+  return __any_sync(kFullWarp, nan);
 }
 
 // One warp folds the leaves' statistics (shared memory); every lane gets the row's.
@@ -264,55 +390,58 @@ __device__ __forceinline__ float token_logp(float z, float s, float lse) {
 __device__ __forceinline__ float prob_of(float d) { return ex2_approx(__fmul_rn(d, kLog2e)); }
 
 // ---------------------------------------------------------------------------
-// the teacher's distribution of one row, by one warp
+// the teacher's distribution of one row
 // ---------------------------------------------------------------------------
-// q = softmax(s t_k) over the entries with an id (id -1: none); lane i holds entries i + 32 r.
-struct Teacher {
-  int64_t id[RLK_MAX_TOP_K / 32];   // -1: no entry
-  float q[RLK_MAX_TOP_K / 32];
-  float logq[RLK_MAX_TOP_K / 32];   // 0 where q is 0
-  bool any;                         // some entry has q > 0
-  bool bad_id, nonfinite;           // an id outside [-1, n) / a teacher value that is NaN or +inf
+struct TeacherRow {                // in shared memory, one entry per k < RLK_MAX_TOP_K
+  int32_t id[RLK_MAX_TOP_K];       // -1: no entry
+  float t[RLK_MAX_TOP_K];          // teacher value; after teacher_softmax: q (0 without an entry)
+  float logq[RLK_MAX_TOP_K];       // 0 where q is 0
+  int32_t any;                     // some entry has q > 0
+  int32_t bad;                     // RLK_FLAG_BAD_TARGET / RLK_FLAG_NONFINITE of the row
 };
 
-__device__ __forceinline__ void load_teacher(Teacher& r, const int64_t* ids, const float* t, int K, int n,
-                                             float s, float c, int lane) {
+// q = softmax(s t_k) over the row's entries, by one warp: lane i takes entries i, i + 32, ...
+__device__ __forceinline__ void teacher_softmax(TeacherRow& r, const int64_t* ids, const float* t, int K, int n,
+                                                float s, float c, int lane) {
   constexpr int R = RLK_MAX_TOP_K / 32;
+  int32_t id[R];
   float v[R];
   float m = neg_inf();
   bool bad = false, inf = false;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     const int k = lane + 32 * i;
-    r.id[i] = k < K ? ids[k] : -1;
+    const int64_t x = k < K ? ids[k] : -1;
     v[i] = k < K ? t[k] : neg_inf();
-    if (r.id[i] < -1 || r.id[i] >= n) {
-      bad = true;
-      r.id[i] = -1;
-    }
-    if (r.id[i] < 0) v[i] = neg_inf();
+    bad |= x < -1 || x >= n;
+    id[i] = x < 0 || x >= n ? -1 : static_cast<int32_t>(x);
+    if (id[i] < 0) v[i] = neg_inf();
     inf |= !(v[i] < __int_as_float(0x7f800000));  // NaN or +inf
     m = fmaxf(m, v[i]);
   }
-  r.bad_id = __any_sync(kFullWarp, bad);
-  r.nonfinite = __any_sync(kFullWarp, inf);
+  bad = __any_sync(kFullWarp, bad);
+  inf = __any_sync(kFullWarp, inf);
   m = warp_max(m);
-  r.any = m > neg_inf();
-  float sum = 0.f;
+  float w[R], sum = 0.f;
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const float d = v[i] > neg_inf() ? __fsub_rn(v[i], m) : neg_inf();
-    r.q[i] = ex2_approx(__fmul_rn(d, c));
-    r.logq[i] = __fmul_rn(d, s);
-    sum = __fadd_rn(sum, r.q[i]);
+    v[i] = v[i] > neg_inf() ? __fsub_rn(v[i], m) : neg_inf();
+    w[i] = ex2_approx(__fmul_rn(v[i], c));
+    sum = __fadd_rn(sum, w[i]);
   }
   sum = warp_sum(sum);
-  const float ls = r.any ? logf(sum) : 0.f;
+  const float ls = logf(sum);
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const bool some = r.q[i] > 0.f;
-    r.q[i] = some ? __fdiv_rn(r.q[i], sum) : 0.f;
-    r.logq[i] = some ? __fsub_rn(r.logq[i], ls) : 0.f;
+    const int k = lane + 32 * i;
+    const bool some = w[i] > 0.f;
+    r.id[k] = id[i];
+    r.t[k] = some ? __fdiv_rn(w[i], sum) : 0.f;
+    r.logq[k] = some ? __fmaf_rn(v[i], s, -ls) : 0.f;
+  }
+  if (lane == 0) {
+    r.any = m > neg_inf();
+    r.bad = (bad ? RLK_FLAG_BAD_TARGET : 0) | (inf ? RLK_FLAG_NONFINITE : 0);
   }
 }
 
