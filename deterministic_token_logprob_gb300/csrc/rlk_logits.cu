@@ -14,6 +14,7 @@ constexpr int ROW_THREADS = 256;
 constexpr int MAX_CLUSTER = 8;                               // CTAs of one row (the portable cluster size)
 constexpr int MAX_ROW_WARPS = MAX_CLUSTER * 32;
 constexpr int GROUPS_PER_LEAF = LEAF_GROUPS;                 // 256-column groups, the units of the alternatives' search
+constexpr int GRAD_PACKS = 4;                                // packs a thread has in flight in the gradients
 constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates that the search keeps
 
 // ---------------------------------------------------------------------------
@@ -368,6 +369,7 @@ struct GradOut {
 struct TokenGradArgs {
   LogitRows in;
   GradOut out;
+  int32_t parts;     // CTAs of a row
   const int64_t* y;
   const float* lse;
   const float* entropy;
@@ -375,34 +377,134 @@ struct TokenGradArgs {
   const float* g_entropy;
 };
 
+// The columns of one row of dlogits that one CTA writes, in packs of 8 that are 16-byte aligned in
+// the output: `head` columns lie before the first of them, fewer than 8 after the last. The row is
+// divided into `parts` runs of packs; the first part takes the head, the last the tail. The input
+// packs of the same columns may lie at any alignment (Row); where dlogits are the logits
+// themselves they are aligned as well, so no thread reads a column that another one writes.
 template <class E, class O>
+struct GradPart {
+  Row<E> in;                  // from column `head` on
+  typename O::bits* out;      // the row's first column
+  int n, V, head, packs, q0, q1, lo, hi;
+  __device__ __forceinline__ GradPart(const typename E::bits* z, int n_, typename O::bits* o, int V_, int part, int parts,
+                                      int32_t* err)
+      : in(z, n_, err), out(o), n(n_), V(V_) {
+    constexpr int OB = sizeof(typename O::bits);
+    head = min(V, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(o) & 15u)) & 15u) / OB);
+    packs = (V - head) / 8;
+    const int per = (packs + parts - 1) / parts;
+    q0 = min(packs, part * per);
+    q1 = min(packs, q0 + per);
+    lo = part == 0 ? 0 : head + 8 * q0;
+    hi = part == parts - 1 ? V : head + 8 * q1;
+    in = Row<E>(z + head, max(0, n - head), err);
+  }
+  __device__ __forceinline__ bool owns(int64_t c) const { return c >= lo && c < hi; }
+  __device__ __forceinline__ void put(int c, float v) const {
+    if (dbg_ok(c >= 0 && c < V, in.err)) out[c] = O::from_f32(v);
+  }
+};
+
+template <class O>
+__device__ __forceinline__ void store_pack(typename O::bits* p, const float (&v)[8]) {
+  uint4* q = reinterpret_cast<uint4*>(p);
+  if constexpr (sizeof(typename O::bits) == 4) {
+    q[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    q[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+  } else {
+    q[0] = make_uint4(O::pack2(v[0], v[1]), O::pack2(v[2], v[3]), O::pack2(v[4], v[5]), O::pack2(v[6], v[7]));
+  }
+}
+
+// Writes f(z) for the part's columns (0 past the row's n columns, and everywhere when !live, without
+// reading). Each thread has U packs in flight; `first` runs in every thread between the first
+// loads and the first store.
+template <int U, class E, class O, class F, class B>
+__device__ __forceinline__ void write_part(const GradPart<E, O>& g, bool live, F f, B first) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  bool begun = false;
+  for (int q = g.q0 + tid; !begun || q - tid < g.q1; q += U * threads) {
+    Pack<E> k[U];
+    if (live) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int c = (q + u * threads) * 8;
+        if (q + u * threads < g.q1) k[u] = packs_inside(g.in, c, c + 8) ? load_pack(g.in, c) : load_pack_edge(g.in, c);
+      }
+    }
+    if (!begun) {
+      begun = true;
+      first();
+      // the columns outside the packs: before the head and after the last pack
+      const int tail0 = g.head + 8 * g.packs;
+      if (tid < 16) {
+        const int c = tid < 8 ? tid : tail0 + tid - 8;
+        if (g.owns(c) && (tid >= 8 || c < g.head)) {
+          g.put(c, live && c < g.n ? f(make_float2(E::to_f32(g.in.p[c - g.head]), 0.f)).x : 0.f);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int c = (q + u * threads) * 8;
+      if (q + u * threads >= g.q1) break;
+      float v[8] = {};
+      if (live) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = f(pair(k[u], i));
+          v[2 * i] = x.x;
+          v[2 * i + 1] = x.y;
+        }
+      }
+      if (dbg_ok(g.head + c + 8 <= g.V, g.in.err)) store_pack<O>(g.out + g.head + c, v);
+    }
+  }
+}
+
+constexpr float kLowestLogp = -1e4f;  // p = 0 far above it, and B d stays a number
+
+// dz = p (A + B d) for a pair of logits, d = s z - lse = log p. A masked column (d = -inf) has p = 0
+// and a finite d.
+__device__ __forceinline__ float2 token_dz(float2 z, float s, float lse, float A, float B) {
+  const float2 d = unpack_f32x2(fma2(pack_f32x2(z.x, z.y), pack_f32x2(s, s), pack_f32x2(-lse, -lse)));
+  const F32x2 dd = pack_f32x2(fmaxf(d.x, kLowestLogp), fmaxf(d.y, kLowestLogp));
+  const float2 x = unpack_f32x2(mul2(dd, pack_f32x2(kLog2e, kLog2e)));
+  const F32x2 p = pack_f32x2(ex2_approx(x.x), ex2_approx(x.y));
+  return unpack_f32x2(fma2(p, fma2(pack_f32x2(B, B), dd, pack_f32x2(A, A)), 0ull));
+}
+
+template <class E, class O, int U>
 __global__ void __launch_bounds__(ROW_THREADS) token_grad_kernel(const TokenGradArgs a) {
-  const int t = blockIdx.x;
   const LogitRows& in = a.in;
-  const auto* row = static_cast<const typename E::bits*>(in.base) + static_cast<int64_t>(t) * in.ld;
-  auto* out = static_cast<typename O::bits*>(a.out.base) + static_cast<int64_t>(t) * a.out.ld;
+  const int64_t t = blockIdx.x / a.parts;
+  const GradPart<E, O> part(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n,
+                            static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
+                            static_cast<int>(blockIdx.x % a.parts), a.parts, in.err_flag);
   const float lse = a.lse[t], g = a.g_logp[t], ge = a.g_entropy ? a.g_entropy[t] : 0.f;
   const int64_t y = a.y[t];
   const bool y_ok = y >= 0 && y < in.n;
-  if (!y_ok && threadIdx.x == 0 && in.err_flag) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
+  if (!y_ok && threadIdx.x == 0 && part.q0 == 0 && in.err_flag) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
   const bool live = y_ok && !isnan(lse) && lse != neg_inf() && !(g == 0.f && ge == 0.f);
-  // dz = p (A + B d) (+ C at y), d = log p
   const float ent = a.g_entropy ? a.entropy[t] : 0.f;
-  const float A = __fmul_rn(-in.s, __fmaf_rn(ge, ent, g)), B = __fmul_rn(-in.s, ge), C = __fmul_rn(in.s, g);
-  for (int v = threadIdx.x; v < a.out.V; v += ROW_THREADS) {
-    float dz = 0.f;
-    if (live && v < in.n) {
-      const float d = __fmaf_rn(E::to_f32(row[v]), in.s, -lse);
-      dz = __fmaf_rn(prob_of(d), __fmaf_rn(B, fmaxf(d, -1e30f), A), v == y ? C : 0.f);
-    }
-    out[v] = O::from_f32(dz);
+  const float A = __fmul_rn(-in.s, __fmaf_rn(ge, ent, g)), B = __fmul_rn(-in.s, ge);
+  // the target's column, from its logit as read before anything is written
+  const bool mine = live && part.owns(y) && threadIdx.x == 0;
+  float dz_y = 0.f;
+  if (mine) {
+    const float d = __fmaf_rn(E::to_f32(static_cast<const typename E::bits*>(in.base)[t * in.ld + y]), in.s, -lse);
+    dz_y = __fmaf_rn(prob_of(d), __fmaf_rn(B, fmaxf(d, kLowestLogp), A), __fmul_rn(in.s, g));
   }
+  write_part<U>(part, live, [&](float2 z) { return token_dz(z, in.s, lse, A, B); }, [] { __syncthreads(); });
+  __syncthreads();
+  if (mine) part.put(static_cast<int>(y), dz_y);
 }
 
 struct DistillArgs {
   LogitRows in;
   GradOut out;
-  int32_t cluster;
+  int32_t cluster;       // CTAs of a row (a cluster in the forward)
   const int64_t* ids;
   const float* teacher;
   int32_t K;
@@ -424,72 +526,91 @@ __device__ __forceinline__ float row_loss(const TeacherRow& q, const Row<E>& row
   return warp_sum(sum);
 }
 
-template <class E, class O, bool FWD, bool BWD>
+// The gradient of one part of a row, by one CTA. q holds the row's teacher distribution.
+template <int U, class E, class O>
+__device__ __forceinline__ void distill_part(const GradPart<E, O>& part, const typename E::bits* z, const TeacherRow& q,
+                                             float* zs, int K, float s, float lse, float g) {
+  const bool live = !isnan(lse) && lse != neg_inf() && q.any && !q.bad && g != 0.f;
+  const float A = __fmul_rn(s, g);
+  // the logits of the teacher's columns, read before anything is written
+  for (int k = threadIdx.x; k < K; k += blockDim.x)
+    zs[k] = live && part.owns(q.id[k]) ? E::to_f32(z[q.id[k]]) : 0.f;
+  const F32x2 ss = pack_f32x2(s, s), nl = pack_f32x2(-lse, -lse), le = pack_f32x2(kLog2e, kLog2e), AA = pack_f32x2(A, A);
+  const auto dz = [&](float2 v) {
+    const float2 x = unpack_f32x2(mul2(fma2(pack_f32x2(v.x, v.y), ss, nl), le));
+    return unpack_f32x2(fma2(AA, pack_f32x2(ex2_approx(x.x), ex2_approx(x.y)), 0ull));
+  };
+  write_part<U>(part, live, dz, [] { __syncthreads(); });
+  __syncthreads();
+  if (!live) return;
+  // the teacher's columns: the first entry of an id writes the sum over its entries
+  for (int k = threadIdx.x; k < K; k += blockDim.x) {
+    const int id = q.id[k];
+    if (id < 0 || !part.owns(id)) continue;
+    bool first = true;
+    float qk = 0.f;
+    for (int j = 0; j < K; ++j) {
+      if (q.id[j] != id) continue;
+      if (j < k) first = false;
+      qk = __fadd_rn(qk, q.t[j]);
+    }
+    if (first) part.put(id, __fmul_rn(A, __fsub_rn(prob_of(__fmaf_rn(zs[k], s, -lse)), qk)));
+  }
+}
+
+// Backward alone: a.parts CTAs of a row, each its own part.
+template <class E, class O, int U>
+__global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const DistillArgs a) {
+  __shared__ TeacherRow q;
+  __shared__ float zs[RLK_MAX_TOP_K];
+  const LogitRows& in = a.in;
+  const int64_t t = blockIdx.x / a.cluster;
+  const auto* z = static_cast<const typename E::bits*>(in.base) + t * in.ld;
+  const GradPart<E, O> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
+                            static_cast<int>(blockIdx.x % a.cluster), a.cluster, in.err_flag);
+  const float lse = a.lse_in[t], g = a.g[t];
+  if (threadIdx.x < 32)
+    teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, threadIdx.x);
+  __syncthreads();
+  if (q.bad && part.q0 == 0 && threadIdx.x == 0 && in.err_flag) atomicOr(in.err_flag, q.bad);
+  distill_part<U>(part, z, q, zs, a.K, in.s, lse, g);
+}
+
+// Forward (a cluster of CTAs a row), and with BWD the gradient in the same launch: every CTA of the
+// row writes its part, whose logits the cluster has just read.
+template <class E, class O, bool BWD>
 __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ TeacherRow q;
   __shared__ float zs[RLK_MAX_TOP_K];
-  __shared__ float row_lse_s;
+  __shared__ float lse_s;
   const LogitRows& in = a.in;
   const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x / C;
-  const Row<E> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
-  if (warp == 1 && (BWD || r == 0))
+  const auto* z = static_cast<const typename E::bits*>(in.base) + t * in.ld;
+  const Row<E> row(z, in.n, in.err_flag);
+  if (warp == ROW_THREADS / 32 - 1 && (BWD || r == 0))
     teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, lane);
-  if constexpr (FWD) {
-    RowSmem sm{reinterpret_cast<Stats*>(dyn), nullptr, nullptr};
-    row_pass<E, false>(row, in.c, RankOf{false, 0, 0.f, 0u, 0u}, sm, C, r);
-    if (r == 0 && warp == 0) {
-      const float lse = row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s);
-      if (BWD && lane < C) st_cluster_u32(map_to_cta(smem_u32(&row_lse_s), lane), __float_as_uint(lse));
-      const float l = row_loss<E>(q, row, lse, in.s, lane);
-      if (lane == 0) {
-        a.loss[t] = isnan(lse) || q.bad ? quiet_nan() : l;
-        if (a.lse) a.lse[t] = lse;
-        if (isnan(lse) && in.err_flag) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
-      }
+  RowSmem sm{reinterpret_cast<Stats*>(dyn), nullptr, nullptr};
+  row_pass<E, false>(row, in.c, RankOf{false, 0, 0.f, 0u, 0u}, sm, C, r);
+  if (r == 0 && warp == 0) {
+    const float lse = row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s);
+    if (BWD && lane < C) st_cluster_u32(map_to_cta(smem_u32(&lse_s), lane), __float_as_uint(lse));
+    const float l = row_loss<E>(q, row, lse, in.s, lane);
+    if (lane == 0) {
+      a.loss[t] = isnan(lse) || q.bad ? quiet_nan() : l;
+      if (a.lse) a.lse[t] = lse;
+      const int flags = q.bad | (isnan(lse) ? RLK_FLAG_NONFINITE : 0);
+      if (flags && in.err_flag) atomicOr(in.err_flag, flags);
     }
-    if constexpr (!BWD) {
-      if (r != 0) return;
-    }
-  } else {
-    if (threadIdx.x == 0) row_lse_s = a.lse_in[t];
   }
   if constexpr (BWD) {
-    if (C > 1) cluster_sync();
+    if (C > 1) cluster_sync();  // the loss has read its logits, and every CTA has the lse
     else __syncthreads();
-    const float lse = row_lse_s;
-    auto* out = static_cast<typename O::bits*>(a.out.base) + t * a.out.ld;
-    const float g = a.g[t];
-    const bool live = !isnan(lse) && lse != neg_inf() && q.any && !q.bad && g != 0.f;
-    const float A = __fmul_rn(in.s, g);
-    const int span = (a.out.V + C - 1) / C, lo = r * span, hi = min(a.out.V, lo + span);
-    for (int k = threadIdx.x; k < a.K; k += ROW_THREADS)
-      zs[k] = live && q.id[k] >= lo && q.id[k] < hi ? row.at(q.id[k]) : 0.f;
-    __syncthreads();
-    for (int v = lo + threadIdx.x; v < hi; v += ROW_THREADS) {
-      float dz = 0.f;
-      if (live && v < in.n) dz = __fmaf_rn(A, prob_of(__fmaf_rn(row.at(v), in.s, -lse)), 0.f);
-      out[v] = O::from_f32(dz);
-    }
-    __syncthreads();
-    // the teacher's columns: the first entry of an id writes the sum over its entries
-    for (int k = threadIdx.x; k < a.K; k += ROW_THREADS) {
-      const int id = q.id[k];
-      if (!live || id < lo || id >= hi) continue;
-      bool first = true;
-      float qk = 0.f;
-      for (int j = 0; j < a.K; ++j) {
-        if (q.id[j] != id) continue;
-        if (j < k) first = false;
-        qk = __fadd_rn(qk, q.t[j]);
-      }
-      if (first) out[id] = O::from_f32(__fmul_rn(A, __fsub_rn(prob_of(__fmaf_rn(zs[k], in.s, -lse)), qk)));
-    }
-  } else {
-    __syncthreads();
+    const GradPart<E, O> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V, r, C,
+                              in.err_flag);
+    distill_part<2>(part, z, q, zs, a.K, in.s, lse_s, a.g[t]);
   }
-  if (r == 0 && threadIdx.x == 0 && q.bad && in.err_flag) atomicOr(in.err_flag, q.bad);
 }
 
 // CTAs of ROW_THREADS per row: one where the rows fill the GPU, else up to MAX_CLUSTER so that few
@@ -501,15 +622,15 @@ int row_cluster(const LogitRows& in) {
   return c;
 }
 
-// Launches a row kernel: `cluster` CTAs for each of T rows.
+// Launches `ctas` CTAs of ROW_THREADS in clusters of `cluster`.
 template <class K, class A>
-rlk_status launch_rows(K kernel, const A& args, int64_t T, int cluster, size_t smem, void* stream) {
+rlk_status launch_rows(K kernel, const A& args, int64_t ctas, int cluster, size_t smem, void* stream) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(T * cluster));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(ROW_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
@@ -519,7 +640,12 @@ rlk_status launch_rows(K kernel, const A& args, int64_t T, int cluster, size_t s
   return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
 }
 
-rlk_status launched() { return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA; }
+// CTAs of a row in a kernel that writes gradients alone: U packs of every thread.
+template <int U>
+int grad_parts(const GradOut& o) {
+  constexpr int kCols = 8 * U * ROW_THREADS;
+  return (o.V + kCols - 1) / kCols;
+}
 
 // dlogits: the logits' type, or bf16 for fp32 logits
 rlk_status check_out(const LogitRows& in, int32_t dtype, void* dlogits, int32_t out_dtype, int64_t V, int64_t out_ld,
@@ -579,7 +705,7 @@ rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
   a.top_logp = top_logp;
   a.cluster = row_cluster(a.in);
   const auto run = [&](auto kernel, bool top) {
-    return launch_rows(kernel, a, T, a.cluster, row_smem_bytes(a.in.n, top), stream);
+    return launch_rows(kernel, a, T * a.cluster, a.cluster, row_smem_bytes(a.in.n, top), stream);
   };
   switch (dtype) {
     case RLK_DTYPE_BF16: return top_k ? run(token_logprobs_kernel<Bf16, true>, true) : run(token_logprobs_kernel<Bf16, false>, false);
@@ -603,11 +729,12 @@ rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t T, 
   a.entropy = entropy;
   a.g_logp = g_logp;
   a.g_entropy = g_entropy;
+  a.parts = grad_parts<GRAD_PACKS>(a.out);
+  if (T * a.parts > INT32_MAX) return RLK_ERR_UNSUPPORTED;
   with_types(dtype, out_dtype, [&](auto e, auto o) {
-    token_grad_kernel<decltype(e), decltype(o)>
-        <<<static_cast<unsigned>(T), ROW_THREADS, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    st = launch_rows(token_grad_kernel<decltype(e), decltype(o), GRAD_PACKS>, a, T * a.parts, 1, 0, stream);
   });
-  return launched();
+  return st;
 }
 
 }  // extern "C"
@@ -627,13 +754,13 @@ rlk_status check_distill(const void* logits, int32_t dtype, int64_t T, int64_t l
   return RLK_OK;
 }
 
-template <bool FWD, bool BWD>
+template <bool BWD>
 rlk_status launch_distill(DistillArgs& a, int32_t dtype, int32_t out_dtype, void* stream) {
   a.cluster = row_cluster(a.in);
   rlk_status st = RLK_OK;
   with_types(dtype, out_dtype, [&](auto e, auto o) {
-    st = launch_rows(distill_kernel<decltype(e), decltype(o), FWD, BWD>, a, a.in.T, a.cluster,
-                     row_smem_bytes(a.in.n, false), stream);
+    st = launch_rows(distill_kernel<decltype(e), decltype(o), BWD>, a, static_cast<int64_t>(a.in.T) * a.cluster,
+                     a.cluster, row_smem_bytes(a.in.n, false), stream);
   });
   return st;
 }
@@ -653,7 +780,7 @@ rlk_status rlk_distill_topk_fwd(const void* logits, int32_t dtype, int64_t T, in
   if (T == 0) return RLK_OK;
   a.loss = loss;
   a.lse = lse;
-  return launch_distill<true, false>(a, dtype, dtype, stream);
+  return launch_distill<false>(a, dtype, dtype, stream);
 }
 
 rlk_status rlk_distill_topk_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
@@ -668,7 +795,12 @@ rlk_status rlk_distill_topk_bwd(const void* logits, int32_t dtype, int64_t T, in
   if (T == 0) return RLK_OK;
   a.lse_in = lse;
   a.g = g;
-  return launch_distill<false, true>(a, dtype, out_dtype, stream);
+  a.cluster = grad_parts<GRAD_PACKS>(a.out);
+  if (T * a.cluster > INT32_MAX) return RLK_ERR_UNSUPPORTED;
+  with_types(dtype, out_dtype, [&](auto e, auto o) {
+    st = launch_rows(distill_grad_kernel<decltype(e), decltype(o), GRAD_PACKS>, a, T * a.cluster, 1, 0, stream);
+  });
+  return st;
 }
 
 rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
@@ -684,7 +816,7 @@ rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, int64_t T
   a.g = g;
   a.loss = loss;
   a.lse = lse;
-  return launch_distill<true, true>(a, dtype, out_dtype, stream);
+  return launch_distill<true>(a, dtype, out_dtype, stream);
 }
 
 }  // extern "C"

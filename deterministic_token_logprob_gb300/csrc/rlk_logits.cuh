@@ -37,6 +37,7 @@ struct Bf16 {
   static constexpr int kKeyShift = 16;  // low bits of the fp32 image that carry nothing
   static __device__ __forceinline__ float to_f32(bits b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
   static __device__ __forceinline__ bits from_f32(float v) { return static_cast<bits>(pack_bf16x2(v, 0.f) & 0xFFFFu); }
+  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) { return pack_bf16x2(lo, hi); }
   static __device__ __forceinline__ float2 to_f32x2(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }
@@ -57,6 +58,10 @@ struct F16 {
   static constexpr int kKeyShift = 13;
   static __device__ __forceinline__ float to_f32(bits b) { return __half2float(__ushort_as_half(b)); }
   static __device__ __forceinline__ bits from_f32(float v) { return __half_as_ushort(__float2half_rn(v)); }
+  static __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __half2 r = __floats2half2_rn(lo, hi);
+    return reinterpret_cast<const uint32_t&>(r);
+  }
   static __device__ __forceinline__ float2 to_f32x2(uint32_t w) {
     return __half22float2(reinterpret_cast<const __half2&>(w));
   }
