@@ -78,8 +78,8 @@ __device__ __forceinline__ int count_ahead(const Pack<E> (&k)[LEAF_GROUPS], cons
   return n;
 }
 
-template <class E, bool TOP>
-__device__ __forceinline__ void row_pass(const Row<E>& row, float c, const RankOf& rank, const RowSmem& sm, int C, int r) {
+template <bool TOP, class R, class E = typename R::E>
+__device__ __forceinline__ void row_pass(const R& row, float c, const RankOf& rank, const RowSmem& sm, int C, int r) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5, g = r * warps + warp, n_leaves = leaves_of(row.n);
   if (C > 1) cluster_arrive();  // CTA 0 must have started before anyone writes to it
@@ -216,8 +216,8 @@ __host__ __device__ constexpr size_t row_smem_bytes(int n, bool top) {
 //  3. If they are too many, the same choice among the chosen groups' octets (8 columns) leaves
 //     at most 8 k.
 //  4. Each candidate's place is the number of candidates ahead of it.
-template <class E>
-__device__ void find_top(const Row<E>& row, const ScoreArgs& a, int64_t t, const RowSmem& sm, TopSmem& ts,
+template <class R, class E = typename R::E>
+__device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowSmem& sm, TopSmem& ts,
                          bool bad, float lse) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int groups = (row.n + LEAF_GROUP - 1) / LEAF_GROUP, K = a.top_k, chosen = min(K, groups);
@@ -301,7 +301,7 @@ __device__ void find_top(const Row<E>& row, const ScoreArgs& a, int64_t t, const
   }
 }
 
-template <class E, bool TOP>
+template <class E, bool TOP, bool AL>
 __global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const ScoreArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ int counts[MAX_ROW_WARPS];
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const Sc
   const LogitRows& in = a.in;
   const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x / C;
-  const Row<E> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
+  const Row<E, AL> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
   RowSmem sm;
   sm.leaf = reinterpret_cast<Stats*>(dyn);
   sm.key = reinterpret_cast<uint32_t*>(dyn + (leaves_of(in.n) * sizeof(Stats) + 15) / 16 * 16);
@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const Sc
     if constexpr (Pack<E>::EB == 2) rank.ge *= 0x10001u, rank.gt *= 0x10001u;
   }
   if (TOP && threadIdx.x == 0) ts.n_cand = 0;
-  row_pass<E, TOP>(row, in.c, rank, sm, C, r);
+  row_pass<TOP>(row, in.c, rank, sm, C, r);
   if (r != 0) return;
   if (warp == 1) {
     const Stats x = fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane);
@@ -382,9 +382,11 @@ struct TokenGradArgs {
 // divided into `parts` runs of packs; the first part takes the head, the last the tail. The input
 // packs of the same columns may lie at any alignment (Row); where dlogits are the logits
 // themselves they are aligned as well, so no thread reads a column that another one writes.
-template <class E, class O>
+template <class E_, class O_, bool AL>
 struct GradPart {
-  Row<E> in;                  // from column `head` on
+  using E = E_;
+  using O = O_;
+  Row<E, AL> in;              // from column `head` on
   typename O::bits* out;      // the row's first column
   int n, V, head, packs, q0, q1, lo, hi;
   __device__ __forceinline__ GradPart(const typename E::bits* z, int n_, typename O::bits* o, int V_, int part, int parts,
@@ -398,7 +400,7 @@ struct GradPart {
     q1 = min(packs, q0 + per);
     lo = part == 0 ? 0 : head + 8 * q0;
     hi = part == parts - 1 ? V : head + 8 * q1;
-    in = Row<E>(z + head, max(0, n - head), err);
+    in = Row<E, AL>(z + head, max(0, n - head), err);
   }
   __device__ __forceinline__ bool owns(int64_t c) const { return c >= lo && c < hi; }
   __device__ __forceinline__ void put(int c, float v) const {
@@ -417,20 +419,36 @@ __device__ __forceinline__ void store_pack(typename O::bits* p, const float (&v)
   }
 }
 
-// Writes f(z) for the part's columns (0 past the row's n columns, and everywhere when !live, without
-// reading). Each thread has U packs in flight; `first` runs in every thread between the first
-// loads and the first store.
-template <int U, class E, class O, class F, class B>
-__device__ __forceinline__ void write_part(const GradPart<E, O>& g, bool live, F f, B first) {
+// Writes f(z, column) for the part's columns (0 past the row's n columns, and everywhere when !live,
+// without reading). Each thread has U packs in flight; `first` runs in every thread between the
+// first loads and the first store.
+template <int U, class G, class F, class B>
+__device__ __forceinline__ void write_part(const G& g, bool live, F f, B first) {
+  using E = typename G::E;
+  using O = typename G::O;
   const int tid = threadIdx.x, threads = blockDim.x;
   bool begun = false;
-  for (int q = g.q0 + tid; !begun || q - tid < g.q1; q += U * threads) {
+  const auto put_pack = [&](const Pack<E>& k, int c) {
+    float v[8];
+    f.pack(k, g.head + c, v);
+    if (c + 8 > g.in.n) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i >= g.in.n) v[i] = 0.f;
+    }
+    if (dbg_ok(g.head + c + 8 <= g.V, g.in.err)) store_pack<O>(g.out + g.head + c, v);
+  };
+  for (int q = g.q0; !begun || q < g.q1; q += U * threads) {
     Pack<E> k[U];
-    if (live) {
+    const bool full = live && q + U * threads <= g.q1 && packs_inside(g.in, q * 8, (q + U * threads) * 8);
+    if (full) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) k[u] = load_pack(g.in, (q + tid + u * threads) * 8);
+    } else if (live) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int c = (q + u * threads) * 8;
-        if (q + u * threads < g.q1) k[u] = packs_inside(g.in, c, c + 8) ? load_pack(g.in, c) : load_pack_edge(g.in, c);
+        const int p = q + tid + u * threads;
+        if (p < g.q1) k[u] = packs_inside(g.in, p * 8, p * 8 + 8) ? load_pack(g.in, p * 8) : load_pack_edge(g.in, p * 8);
       }
     }
     if (!begun) {
@@ -440,65 +458,82 @@ __device__ __forceinline__ void write_part(const GradPart<E, O>& g, bool live, F
       const int tail0 = g.head + 8 * g.packs;
       if (tid < 16) {
         const int c = tid < 8 ? tid : tail0 + tid - 8;
-        if (g.owns(c) && (tid >= 8 || c < g.head)) {
-          g.put(c, live && c < g.n ? f(make_float2(E::to_f32(g.in.p[c - g.head]), 0.f)).x : 0.f);
-        }
+        if (g.owns(c) && (tid >= 8 || c < g.head))
+          g.put(c, live && c < g.n ? f.one(E::to_f32(g.in.p[c - g.head]), c) : 0.f);
       }
     }
+    if (full) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = (q + u * threads) * 8;
-      if (q + u * threads >= g.q1) break;
-      float v[8] = {};
-      if (live) {
+      for (int u = 0; u < U; ++u) put_pack(k[u], (q + tid + u * threads) * 8);
+    } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 x = f(pair(k[u], i));
-          v[2 * i] = x.x;
-          v[2 * i + 1] = x.y;
+      for (int u = 0; u < U; ++u) {
+        const int p = q + tid + u * threads;
+        if (p >= g.q1) break;
+        if (live) {
+          put_pack(k[u], p * 8);
+        } else {
+          const float v[8] = {};
+          store_pack<O>(g.out + g.head + p * 8, v);
         }
       }
-      if (dbg_ok(g.head + c + 8 <= g.V, g.in.err)) store_pack<O>(g.out + g.head + c, v);
     }
   }
 }
 
 constexpr float kLowestLogp = -1e4f;  // p = 0 far above it, and B d stays a number
 
-// dz = p (A + B d) for a pair of logits, d = s z - lse = log p. A masked column (d = -inf) has p = 0
-// and a finite d.
-__device__ __forceinline__ float2 token_dz(float2 z, float s, float lse, float A, float B) {
-  const float2 d = unpack_f32x2(fma2(pack_f32x2(z.x, z.y), pack_f32x2(s, s), pack_f32x2(-lse, -lse)));
-  const F32x2 dd = pack_f32x2(fmaxf(d.x, kLowestLogp), fmaxf(d.y, kLowestLogp));
-  const float2 x = unpack_f32x2(mul2(dd, pack_f32x2(kLog2e, kLog2e)));
-  const F32x2 p = pack_f32x2(ex2_approx(x.x), ex2_approx(x.y));
-  return unpack_f32x2(fma2(p, fma2(pack_f32x2(B, B), dd, pack_f32x2(A, A)), 0ull));
-}
+// dz = p (A + B d), and p (A + B d) + C at the target, with d = s z - lse = log p. A masked column
+// (d = -inf) has p = 0 and a finite d.
+struct TokenDz {
+  float s, lse, A, B, C;
+  int y;
+  __device__ __forceinline__ float one(float z, int c) const {
+    const float d = fmaxf(__fmaf_rn(z, s, -lse), kLowestLogp);
+    const float p = prob_of(d), t = __fmaf_rn(B, d, A);
+    return c == y ? __fmaf_rn(p, t, C) : __fmul_rn(p, t);
+  }
+  template <class E>
+  __device__ __forceinline__ void pack(const Pack<E>& k, int c, float (&v)[8]) const {
+    const F32x2 ss = pack_f32x2(s, s), nl = pack_f32x2(-lse, -lse), le = pack_f32x2(kLog2e, kLog2e);
+    const F32x2 AA = pack_f32x2(A, A), BB = pack_f32x2(B, B);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 z = pair(k, i);
+      const float2 d = unpack_f32x2(fma2(pack_f32x2(z.x, z.y), ss, nl));
+      const F32x2 dd = pack_f32x2(fmaxf(d.x, kLowestLogp), fmaxf(d.y, kLowestLogp));
+      const float2 x = unpack_f32x2(mul2(dd, le));
+      const float2 r = unpack_f32x2(mul2(pack_f32x2(ex2_approx(x.x), ex2_approx(x.y)), fma2(BB, dd, AA)));
+      v[2 * i] = r.x;
+      v[2 * i + 1] = r.y;
+    }
+    if (static_cast<unsigned>(y - c) < 8u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 z = pair(k, i);
+        if (y == c + 2 * i) v[2 * i] = one(z.x, y);
+        if (y == c + 2 * i + 1) v[2 * i + 1] = one(z.y, y);
+      }
+    }
+  }
+};
 
-template <class E, class O, int U>
+template <class E, class O, bool AL>
 __global__ void __launch_bounds__(ROW_THREADS) token_grad_kernel(const TokenGradArgs a) {
   const LogitRows& in = a.in;
   const int64_t t = blockIdx.x / a.parts;
-  const GradPart<E, O> part(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n,
-                            static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
-                            static_cast<int>(blockIdx.x % a.parts), a.parts, in.err_flag);
+  const GradPart<E, O, AL> part(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n,
+                                static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
+                                static_cast<int>(blockIdx.x % a.parts), a.parts, in.err_flag);
   const float lse = a.lse[t], g = a.g_logp[t], ge = a.g_entropy ? a.g_entropy[t] : 0.f;
+  const float ent = a.g_entropy ? a.entropy[t] : 0.f;
   const int64_t y = a.y[t];
   const bool y_ok = y >= 0 && y < in.n;
-  if (!y_ok && threadIdx.x == 0 && part.q0 == 0 && in.err_flag) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
+  if (!y_ok && threadIdx.x == 0 && part.lo == 0 && in.err_flag) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
   const bool live = y_ok && !isnan(lse) && lse != neg_inf() && !(g == 0.f && ge == 0.f);
-  const float ent = a.g_entropy ? a.entropy[t] : 0.f;
-  const float A = __fmul_rn(-in.s, __fmaf_rn(ge, ent, g)), B = __fmul_rn(-in.s, ge);
-  // the target's column, from its logit as read before anything is written
-  const bool mine = live && part.owns(y) && threadIdx.x == 0;
-  float dz_y = 0.f;
-  if (mine) {
-    const float d = __fmaf_rn(E::to_f32(static_cast<const typename E::bits*>(in.base)[t * in.ld + y]), in.s, -lse);
-    dz_y = __fmaf_rn(prob_of(d), __fmaf_rn(B, fmaxf(d, kLowestLogp), A), __fmul_rn(in.s, g));
-  }
-  write_part<U>(part, live, [&](float2 z) { return token_dz(z, in.s, lse, A, B); }, [] { __syncthreads(); });
-  __syncthreads();
-  if (mine) part.put(static_cast<int>(y), dz_y);
+  const TokenDz dz{in.s, lse, __fmul_rn(-in.s, __fmaf_rn(ge, ent, g)), __fmul_rn(-in.s, ge), __fmul_rn(in.s, g),
+                   static_cast<int>(y)};
+  write_part<GRAD_PACKS>(part, live, dz, [] {});  // every thread reads and writes columns of its own
 }
 
 struct DistillArgs {
@@ -515,8 +550,8 @@ struct DistillArgs {
 };
 
 // Loss of one row by one warp (every lane gets it).
-template <class E>
-__device__ __forceinline__ float row_loss(const TeacherRow& q, const Row<E>& row, float lse, float s, int lane) {
+template <class R>
+__device__ __forceinline__ float row_loss(const TeacherRow& q, const R& row, float lse, float s, int lane) {
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < RLK_MAX_TOP_K / 32; ++i) {
@@ -526,21 +561,34 @@ __device__ __forceinline__ float row_loss(const TeacherRow& q, const Row<E>& row
   return warp_sum(sum);
 }
 
+// dz = A p, p = e^{s z - lse}.
+struct DistillDz {
+  float s, lse, A;
+  __device__ __forceinline__ float one(float z, int) const { return __fmul_rn(A, prob_of(__fmaf_rn(z, s, -lse))); }
+  template <class E>
+  __device__ __forceinline__ void pack(const Pack<E>& k, int, float (&v)[8]) const {
+    const F32x2 ss = pack_f32x2(s, s), nl = pack_f32x2(-lse, -lse), le = pack_f32x2(kLog2e, kLog2e), AA = pack_f32x2(A, A);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 z = pair(k, i);
+      const float2 x = unpack_f32x2(mul2(fma2(pack_f32x2(z.x, z.y), ss, nl), le));
+      const float2 r = unpack_f32x2(mul2(AA, pack_f32x2(ex2_approx(x.x), ex2_approx(x.y))));
+      v[2 * i] = r.x;
+      v[2 * i + 1] = r.y;
+    }
+  }
+};
+
 // The gradient of one part of a row, by one CTA. q holds the row's teacher distribution.
-template <int U, class E, class O>
-__device__ __forceinline__ void distill_part(const GradPart<E, O>& part, const typename E::bits* z, const TeacherRow& q,
-                                             float* zs, int K, float s, float lse, float g) {
+template <int U, class G>
+__device__ __forceinline__ void distill_part(const G& part, const typename G::E::bits* z, const TeacherRow& q, float* zs,
+                                             int K, float s, float lse, float g) {
   const bool live = !isnan(lse) && lse != neg_inf() && q.any && !q.bad && g != 0.f;
   const float A = __fmul_rn(s, g);
   // the logits of the teacher's columns, read before anything is written
   for (int k = threadIdx.x; k < K; k += blockDim.x)
-    zs[k] = live && part.owns(q.id[k]) ? E::to_f32(z[q.id[k]]) : 0.f;
-  const F32x2 ss = pack_f32x2(s, s), nl = pack_f32x2(-lse, -lse), le = pack_f32x2(kLog2e, kLog2e), AA = pack_f32x2(A, A);
-  const auto dz = [&](float2 v) {
-    const float2 x = unpack_f32x2(mul2(fma2(pack_f32x2(v.x, v.y), ss, nl), le));
-    return unpack_f32x2(fma2(AA, pack_f32x2(ex2_approx(x.x), ex2_approx(x.y)), 0ull));
-  };
-  write_part<U>(part, live, dz, [] { __syncthreads(); });
+    zs[k] = live && part.owns(q.id[k]) ? G::E::to_f32(z[q.id[k]]) : 0.f;
+  write_part<U>(part, live, DistillDz{s, lse, A}, [] { __syncthreads(); });
   __syncthreads();
   if (!live) return;
   // the teacher's columns: the first entry of an id writes the sum over its entries
@@ -559,26 +607,27 @@ __device__ __forceinline__ void distill_part(const GradPart<E, O>& part, const t
 }
 
 // Backward alone: a.parts CTAs of a row, each its own part.
-template <class E, class O, int U>
+template <class E, class O, bool AL>
 __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const DistillArgs a) {
   __shared__ TeacherRow q;
   __shared__ float zs[RLK_MAX_TOP_K];
   const LogitRows& in = a.in;
   const int64_t t = blockIdx.x / a.cluster;
   const auto* z = static_cast<const typename E::bits*>(in.base) + t * in.ld;
-  const GradPart<E, O> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
+  const GradPart<E, O, AL> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
                             static_cast<int>(blockIdx.x % a.cluster), a.cluster, in.err_flag);
   const float lse = a.lse_in[t], g = a.g[t];
   if (threadIdx.x < 32)
     teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, threadIdx.x);
   __syncthreads();
-  if (q.bad && part.q0 == 0 && threadIdx.x == 0 && in.err_flag) atomicOr(in.err_flag, q.bad);
-  distill_part<U>(part, z, q, zs, a.K, in.s, lse, g);
+  if (q.bad && part.lo == 0 && threadIdx.x == 0 && in.err_flag) atomicOr(in.err_flag, q.bad);
+  distill_part<GRAD_PACKS>(part, z, q, zs, a.K, in.s, lse, g);
 }
 
 // Forward (a cluster of CTAs a row), and with BWD the gradient in the same launch: every CTA of the
 // row writes its part, whose logits the cluster has just read.
-template <class E, class O, bool BWD>
+// AL: the rows are aligned; GAL: the gradient's packs are (always where dlogits are the logits).
+template <class E, class O, bool BWD, bool AL, bool GAL>
 __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ TeacherRow q;
@@ -588,15 +637,15 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
   const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x / C;
   const auto* z = static_cast<const typename E::bits*>(in.base) + t * in.ld;
-  const Row<E> row(z, in.n, in.err_flag);
+  const Row<E, AL> row(z, in.n, in.err_flag);
   if (warp == ROW_THREADS / 32 - 1 && (BWD || r == 0))
     teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, lane);
   RowSmem sm{reinterpret_cast<Stats*>(dyn), nullptr, nullptr};
-  row_pass<E, false>(row, in.c, RankOf{false, 0, 0.f, 0u, 0u}, sm, C, r);
+  row_pass<false>(row, in.c, RankOf{false, 0, 0.f, 0u, 0u}, sm, C, r);
   if (r == 0 && warp == 0) {
     const float lse = row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s);
     if (BWD && lane < C) st_cluster_u32(map_to_cta(smem_u32(&lse_s), lane), __float_as_uint(lse));
-    const float l = row_loss<E>(q, row, lse, in.s, lane);
+    const float l = row_loss(q, row, lse, in.s, lane);
     if (lane == 0) {
       a.loss[t] = isnan(lse) || q.bad ? quiet_nan() : l;
       if (a.lse) a.lse[t] = lse;
@@ -607,7 +656,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
   if constexpr (BWD) {
     if (C > 1) cluster_sync();  // the loss has read its logits, and every CTA has the lse
     else __syncthreads();
-    const GradPart<E, O> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V, r, C,
+    const GradPart<E, O, GAL> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V, r, C,
                               in.err_flag);
     distill_part<2>(part, z, q, zs, a.K, in.s, lse_s, a.g[t]);
   }
@@ -640,10 +689,9 @@ rlk_status launch_rows(K kernel, const A& args, int64_t ctas, int cluster, size_
   return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
 }
 
-// CTAs of a row in a kernel that writes gradients alone: U packs of every thread.
-template <int U>
+// CTAs of a row in a kernel that writes gradients alone.
 int grad_parts(const GradOut& o) {
-  constexpr int kCols = 8 * U * ROW_THREADS;
+  constexpr int kCols = 8 * GRAD_PACKS * ROW_THREADS;
   return (o.V + kCols - 1) / kCols;
 }
 
@@ -668,13 +716,38 @@ rlk_status check_out(const LogitRows& in, int32_t dtype, void* dlogits, int32_t 
   return RLK_OK;
 }
 
-// Calls f with the element types of (dtype, out_dtype).
+// Whether every row starts on a 16-byte boundary.
+bool aligned_rows(const void* base, int64_t ld, int bytes) {
+  return reinterpret_cast<uintptr_t>(base) % 16 == 0 && ld * bytes % 16 == 0;
+}
+
+// Whether the packs of every row's gradient are aligned in the logits as well: both sets of rows
+// are, or they lie alike (the same type, and the same distance from a boundary in every row).
+bool aligned_pair(const LogitRows& in, int32_t dtype, const GradOut& o, int32_t out_dtype) {
+  const int eb = dtype_bytes(dtype), ob = dtype_bytes(out_dtype);
+  if (aligned_rows(in.base, in.ld, eb) && aligned_rows(o.base, o.ld, ob)) return true;
+  return eb == ob && (reinterpret_cast<uintptr_t>(in.base) - reinterpret_cast<uintptr_t>(o.base)) % 16 == 0 &&
+         (in.ld - o.ld) * eb % 16 == 0;
+}
+
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
+};
+
+// Calls f with the element type(s) and the alignment as types.
 template <class F>
-void with_types(int32_t dtype, int32_t out_dtype, F f) {
-  if (dtype == RLK_DTYPE_BF16) f(Bf16{}, Bf16{});
-  else if (dtype == RLK_DTYPE_F16) f(F16{}, F16{});
-  else if (out_dtype == RLK_DTYPE_BF16) f(F32{}, Bf16{});
-  else f(F32{}, F32{});
+rlk_status with_types(int32_t dtype, bool aligned, F f) {
+  const auto al = [&](auto e) { return aligned ? f(e, Flag<true>{}) : f(e, Flag<false>{}); };
+  return dtype == RLK_DTYPE_BF16 ? al(Bf16{}) : dtype == RLK_DTYPE_F16 ? al(F16{}) : al(F32{});
+}
+
+template <class F>
+rlk_status with_types(int32_t dtype, int32_t out_dtype, bool aligned, F f) {
+  const auto al = [&](auto e, auto o) { return aligned ? f(e, o, Flag<true>{}) : f(e, o, Flag<false>{}); };
+  if (dtype == RLK_DTYPE_BF16) return al(Bf16{}, Bf16{});
+  if (dtype == RLK_DTYPE_F16) return al(F16{}, F16{});
+  return out_dtype == RLK_DTYPE_BF16 ? al(F32{}, Bf16{}) : al(F32{}, F32{});
 }
 
 }  // namespace
@@ -704,14 +777,12 @@ rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
   a.top_ids = top_ids;
   a.top_logp = top_logp;
   a.cluster = row_cluster(a.in);
-  const auto run = [&](auto kernel, bool top) {
-    return launch_rows(kernel, a, T * a.cluster, a.cluster, row_smem_bytes(a.in.n, top), stream);
-  };
-  switch (dtype) {
-    case RLK_DTYPE_BF16: return top_k ? run(token_logprobs_kernel<Bf16, true>, true) : run(token_logprobs_kernel<Bf16, false>, false);
-    case RLK_DTYPE_F16: return top_k ? run(token_logprobs_kernel<F16, true>, true) : run(token_logprobs_kernel<F16, false>, false);
-    default: return top_k ? run(token_logprobs_kernel<F32, true>, true) : run(token_logprobs_kernel<F32, false>, false);
-  }
+  return with_types(dtype, aligned_rows(logits, ld, dtype_bytes(dtype)), [&](auto e, auto al) {
+    using E = decltype(e);
+    constexpr bool AL = decltype(al)::value;
+    return launch_rows(top_k ? token_logprobs_kernel<E, true, AL> : token_logprobs_kernel<E, false, AL>, a,
+                       T * a.cluster, a.cluster, row_smem_bytes(a.in.n, top_k > 0), stream);
+  });
 }
 
 rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
@@ -729,12 +800,11 @@ rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t T, 
   a.entropy = entropy;
   a.g_logp = g_logp;
   a.g_entropy = g_entropy;
-  a.parts = grad_parts<GRAD_PACKS>(a.out);
+  a.parts = grad_parts(a.out);
   if (T * a.parts > INT32_MAX) return RLK_ERR_UNSUPPORTED;
-  with_types(dtype, out_dtype, [&](auto e, auto o) {
-    st = launch_rows(token_grad_kernel<decltype(e), decltype(o), GRAD_PACKS>, a, T * a.parts, 1, 0, stream);
+  return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto al) {
+    return launch_rows(token_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, T * a.parts, 1, 0, stream);
   });
-  return st;
 }
 
 }  // extern "C"
@@ -754,15 +824,9 @@ rlk_status check_distill(const void* logits, int32_t dtype, int64_t T, int64_t l
   return RLK_OK;
 }
 
-template <bool BWD>
-rlk_status launch_distill(DistillArgs& a, int32_t dtype, int32_t out_dtype, void* stream) {
-  a.cluster = row_cluster(a.in);
-  rlk_status st = RLK_OK;
-  with_types(dtype, out_dtype, [&](auto e, auto o) {
-    st = launch_rows(distill_kernel<decltype(e), decltype(o), BWD>, a, static_cast<int64_t>(a.in.T) * a.cluster,
-                     a.cluster, row_smem_bytes(a.in.n, false), stream);
-  });
-  return st;
+template <class K>
+rlk_status launch_distill(K kernel, const DistillArgs& a, void* stream) {
+  return launch_rows(kernel, a, static_cast<int64_t>(a.in.T) * a.cluster, a.cluster, row_smem_bytes(a.in.n, false), stream);
 }
 
 }  // namespace
@@ -780,7 +844,11 @@ rlk_status rlk_distill_topk_fwd(const void* logits, int32_t dtype, int64_t T, in
   if (T == 0) return RLK_OK;
   a.loss = loss;
   a.lse = lse;
-  return launch_distill<false>(a, dtype, dtype, stream);
+  a.cluster = row_cluster(a.in);
+  return with_types(dtype, aligned_rows(logits, ld, dtype_bytes(dtype)), [&](auto e, auto al) {
+    using E = decltype(e);
+    return launch_distill(distill_kernel<E, E, false, decltype(al)::value, false>, a, stream);
+  });
 }
 
 rlk_status rlk_distill_topk_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
@@ -795,12 +863,11 @@ rlk_status rlk_distill_topk_bwd(const void* logits, int32_t dtype, int64_t T, in
   if (T == 0) return RLK_OK;
   a.lse_in = lse;
   a.g = g;
-  a.cluster = grad_parts<GRAD_PACKS>(a.out);
+  a.cluster = grad_parts(a.out);
   if (T * a.cluster > INT32_MAX) return RLK_ERR_UNSUPPORTED;
-  with_types(dtype, out_dtype, [&](auto e, auto o) {
-    st = launch_rows(distill_grad_kernel<decltype(e), decltype(o), GRAD_PACKS>, a, T * a.cluster, 1, 0, stream);
+  return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto al) {
+    return launch_rows(distill_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, T * a.cluster, 1, 0, stream);
   });
-  return st;
 }
 
 rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
@@ -816,7 +883,15 @@ rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, int64_t T
   a.g = g;
   a.loss = loss;
   a.lse = lse;
-  return launch_distill<true>(a, dtype, out_dtype, stream);
+  a.cluster = row_cluster(a.in);
+  const bool aligned = aligned_rows(logits, ld, dtype_bytes(dtype));
+  return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto gal) {
+    using E = decltype(e);
+    using O = decltype(o);
+    constexpr bool GAL = decltype(gal)::value;
+    return launch_distill(aligned && GAL ? distill_kernel<E, O, true, GAL, GAL> : distill_kernel<E, O, true, false, GAL>,
+                          a, stream);
+  });
 }
 
 }  // extern "C"

@@ -156,23 +156,27 @@ struct Pack {
   uint32_t w[WORDS];
 };
 
-// A row (or the rest of one): its first n elements are valid.
-template <class E>
+// A row (or the rest of one): its first n elements are valid. AL: it starts on a 16-byte boundary
+// (decided once for a launch; the general form costs 15 more instructions a pack, 1.9 an element,
+// which at 16-bit types is a quarter of what the row statistics take).
+template <class E_, bool AL_>
 struct Row {
+  using E = E_;
+  static constexpr bool AL = AL_;
   const typename E::bits* p;
   int32_t n;
   uint32_t shift;  // bytes that p lies past a 16-byte boundary; the same for every thread
   int32_t* err;    // for the index checks of debug-checks builds
   __device__ __forceinline__ Row(const typename E::bits* p_, int n_, int32_t* err_)
-      : p(p_), n(n_), shift(static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p_) & 15u)), err(err_) {}
+      : p(p_), n(n_), shift(AL ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p_) & 15u)), err(err_) {}
   __device__ __forceinline__ float at(int64_t c) const { return dbg_ok(c >= 0 && c < n, err) ? E::to_f32(p[c]) : 0.f; }
 };
 
 // True when pack columns [c0, c1) (multiples of 8) load as vectors inside the row.
-template <class E>
-__device__ __forceinline__ bool packs_inside(const Row<E>& r, int c0, int c1) {
-  if (r.shift == 0) return c1 <= r.n;
-  return c0 > 0 && c1 + static_cast<int>((16u - r.shift) / Pack<E>::EB) <= r.n;
+template <class R>
+__device__ __forceinline__ bool packs_inside(const R& r, int c0, int c1) {
+  if constexpr (R::AL) return c1 <= r.n;
+  return (c0 > 0 || r.shift == 0) && c1 + static_cast<int>((16u - r.shift) / sizeof(*r.p)) <= r.n;
 }
 
 __device__ __forceinline__ void ld_vec(uint32_t* w, const void* p) {
@@ -181,47 +185,48 @@ __device__ __forceinline__ void ld_vec(uint32_t* w, const void* p) {
 }
 
 // Pack at column c0 (a multiple of 8); packs_inside must hold for it.
-template <class E>
-__device__ __forceinline__ Pack<E> load_pack(const Row<E>& r, int c0) {
-  constexpr int W = Pack<E>::WORDS;
+template <class R, class E = typename R::E>
+__device__ __forceinline__ Pack<E> load_pack(const R& r, int c0) {
+  constexpr int W = Pack<E>::WORDS, EB = Pack<E>::EB;
   Pack<E> k{};
   // the first byte of the first vector and the last of the last one lie in the row
-  if (!dbg_ok(c0 >= 0 && static_cast<int64_t>(c0) * Pack<E>::EB >= r.shift &&
-                  static_cast<int64_t>(c0 + 8) * Pack<E>::EB + (r.shift ? 16 - r.shift : 0) <=
-                      static_cast<int64_t>(r.n) * Pack<E>::EB,
+  if (!dbg_ok(c0 >= 0 && static_cast<int64_t>(c0) * EB >= r.shift &&
+                  static_cast<int64_t>(c0 + 8) * EB + (R::AL ? 0 : 16 - static_cast<int>(r.shift)) <=
+                      static_cast<int64_t>(r.n) * EB,
               r.err))
     return k;
-  const char* q = reinterpret_cast<const char*>(r.p) - r.shift + static_cast<int64_t>(c0) * Pack<E>::EB;
-  if (r.shift == 0) {
+  const char* q = reinterpret_cast<const char*>(r.p) + static_cast<int64_t>(c0) * EB;
+  if constexpr (R::AL) {
 #pragma unroll
     for (int i = 0; i < W; i += 4) ld_vec(k.w + i, q + 4 * i);
-    return k;
-  }
-  uint32_t y[W + 4];
-#pragma unroll
-  for (int i = 0; i < W + 4; i += 4) ld_vec(y + i, q + 4 * i);
-  // words shift / 4 .. of y, then the bytes within a word
-  const bool two = r.shift & 8u, one = r.shift & 4u;
-  uint32_t x[W + 2];
-#pragma unroll
-  for (int i = 0; i < W + 2; ++i) x[i] = two ? y[i + 2] : y[i];
-  if constexpr (Pack<E>::EB == 4) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) k.w[i] = one ? x[i + 1] : x[i];
   } else {
-    uint32_t t[W + 1];
+    q -= r.shift;
+    uint32_t y[W + 4];
 #pragma unroll
-    for (int i = 0; i < W + 1; ++i) t[i] = one ? x[i + 1] : x[i];
-    const uint32_t bits = (r.shift & 3u) * 8u;
+    for (int i = 0; i < W + 4; i += 4) ld_vec(y + i, q + 4 * i);
+    // words shift / 4 .. of y, then the bytes within a word
+    const bool two = r.shift & 8u, one = r.shift & 4u;
+    uint32_t x[W + 2];
 #pragma unroll
-    for (int i = 0; i < W; ++i) k.w[i] = __funnelshift_r(t[i], t[i + 1], bits);
+    for (int i = 0; i < W + 2; ++i) x[i] = two ? y[i + 2] : y[i];
+    if constexpr (EB == 4) {
+#pragma unroll
+      for (int i = 0; i < W; ++i) k.w[i] = one ? x[i + 1] : x[i];
+    } else {
+      uint32_t t[W + 1];
+#pragma unroll
+      for (int i = 0; i < W + 1; ++i) t[i] = one ? x[i + 1] : x[i];
+      const uint32_t bits = (r.shift & 3u) * 8u;
+#pragma unroll
+      for (int i = 0; i < W; ++i) k.w[i] = __funnelshift_r(t[i], t[i + 1], bits);
+    }
   }
   return k;
 }
 
 // Pack at column c0 near the row's ends, element by element; -inf beyond the row.
-template <class E>
-__device__ __forceinline__ Pack<E> load_pack_edge(const Row<E>& r, int c0) {
+template <class R, class E = typename R::E>
+__device__ __noinline__ Pack<E> load_pack_edge(const R r, int c0) {
   Pack<E> k;
 #pragma unroll
   for (int i = 0; i < Pack<E>::WORDS; ++i) {
@@ -277,8 +282,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // Packs of a lane: k[j] holds columns 256 j + 8 lane .. + 7 of the leaf; -inf beyond the row.
-template <class E>
-__device__ __forceinline__ void load_leaf(const Row<E>& r, int leaf, int lane, Pack<E> (&k)[LEAF_GROUPS]) {
+template <class R>
+__device__ __forceinline__ void load_leaf(const R& r, int leaf, int lane, Pack<typename R::E> (&k)[LEAF_GROUPS]) {
   const int c0 = leaf * ROW_LEAF + lane * 8;
   if (packs_inside(r, leaf * ROW_LEAF, (leaf + 1) * ROW_LEAF)) {  // the same for the whole warp
 #pragma unroll
