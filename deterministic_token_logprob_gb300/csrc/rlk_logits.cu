@@ -15,18 +15,18 @@ constexpr int MAX_CLUSTER = 8;                               // CTAs of one row 
 constexpr int MAX_ROW_WARPS = MAX_CLUSTER * 32;
 constexpr int GROUPS_PER_LEAF = LEAF_GROUPS;                 // 256-column groups, the units of the alternatives' search
 constexpr int GRAD_PACKS = 4;                                // packs a thread has in flight in the gradients
-constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates that the search keeps
+constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates: 8 columns of each chosen octet
 
 // ---------------------------------------------------------------------------
 // one pass over a row by a cluster of CTAs (one CTA when there are rows enough)
 // ---------------------------------------------------------------------------
 // Warp g of the row's C x (blockDim / 32) warps takes leaves g, g + (number of warps), ... and
 // leaves what it found in the shared memory of the cluster's CTA 0 (distributed shared memory):
-// (m, s, u) of each leaf, the order keys of its four groups' maxima (TOP), and how many of its
-// columns stand ahead of the target (RANK).
+// (m, s, u) of each leaf, the maxima of its four groups (TOP), and how many columns stand ahead of
+// the target.
 struct RowSmem {
   Stats* leaf;      // [n_leaves]
-  uint32_t* key;    // [round_up(4 n_leaves, 128)]
+  float* group;     // [round_up(4 n_leaves, 128)]; then their order keys
   int* count;       // [MAX_ROW_WARPS]
 };
 
@@ -40,6 +40,10 @@ struct RankOf {     // the target of the row, when its rank is wanted
   uint32_t ge, gt;  // its logit and the next value above it, in both halves of a word for 16-bit types
 };
 
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.relaxed.cluster.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d)
+               : "memory");
+}
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 
@@ -78,89 +82,111 @@ __device__ __forceinline__ int count_ahead(const Pack<E> (&k)[LEAF_GROUPS], cons
   return n;
 }
 
-template <bool TOP, class R, class E = typename R::E>
+// What one leaf leaves behind (see RowSmem); returns how many of the lane's columns stand ahead of
+// the target.
+template <bool ENT, bool TOP, class E>
+__device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l, float c, const RankOf& rank,
+                                         uint32_t leaf0, uint32_t group0, int lane) {
+  float gm[LEAF_GROUPS], m;
+#pragma unroll
+  for (int j = 0; j < LEAF_GROUPS; ++j) {
+    gm[j] = pack_max(k[j]);
+    if constexpr (TOP) gm[j] = warp_max(gm[j]);
+  }
+  m = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
+  if constexpr (!TOP) m = warp_max(m);
+  float2 x;
+  if (m == neg_inf()) x = make_float2(any_nan(k) ? quiet_nan() : 0.f, 0.f);
+  else x = leaf_sums<ENT>(k, m, c, lane);
+  if (lane == 0) {
+    st_cluster_f32x4(leaf0 + static_cast<uint32_t>(l * 16), m, x.x, x.y, 0.f);
+    if (TOP) st_cluster_f32x4(group0 + static_cast<uint32_t>(l * 16), gm[0], gm[1], gm[2], gm[3]);
+  }
+  // a leaf whose best column is below the target has none ahead of it: for a likely token, most
+  return rank.on && m >= rank.z ? count_ahead(k, rank, l, lane) : 0;
+}
+
+// Leaves that a warp loads at once: 64 bytes a lane and leaf in 16-bit types leave too little in
+// flight (96 -> 83 us at 1820 rows of 151936), 128 in fp32 do.
+template <class E>
+constexpr int kLeavesAtOnce = sizeof(typename E::bits) == 2 ? 1 : 1;
+
+template <bool ENT, bool TOP, class R, class E = typename R::E>
 __device__ __forceinline__ void row_pass(const R& row, float c, const RankOf& rank, const RowSmem& sm, int C, int r) {
+  constexpr int U = kLeavesAtOnce<E>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int warps = blockDim.x >> 5, g = r * warps + warp, n_leaves = leaves_of(row.n);
+  const int warps = blockDim.x >> 5, g = r * warps + warp, n_leaves = leaves_of(row.n), step = C * warps;
   if (C > 1) cluster_arrive();  // CTA 0 must have started before anyone writes to it
   bool waited = C == 1;
-  const uint32_t leaf0 = map_to_cta(smem_u32(sm.leaf), 0), key0 = TOP ? map_to_cta(smem_u32(sm.key), 0) : 0;
+  const uint32_t leaf0 = map_to_cta(smem_u32(sm.leaf), 0), group0 = TOP ? map_to_cta(smem_u32(sm.group), 0) : 0;
   int count = 0;
-  for (int l = g; l < n_leaves; l += C * warps) {
-    Pack<E> k[LEAF_GROUPS];
-    load_leaf(row, l, lane, k);
-    float gm[LEAF_GROUPS], m;
+  for (int l = g; l < n_leaves; l += U * step) {
+    Pack<E> k[U][LEAF_GROUPS];
 #pragma unroll
-    for (int j = 0; j < LEAF_GROUPS; ++j) {
-      gm[j] = pack_max(k[j]);
-      if constexpr (TOP) gm[j] = warp_max(gm[j]);
-    }
-    m = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
-    if constexpr (!TOP) m = warp_max(m);
-    float part;  // lanes 0-15: s, lanes 16-31: u
-    if (m == neg_inf()) part = any_nan(k) && lane < 16 ? quiet_nan() : 0.f;
-    else part = leaf_sums(k, m, c, lane);
-    if (rank.on) count += count_ahead(k, rank, l, lane);
+    for (int u = 0; u < U; ++u)
+      if (u == 0 || l + u * step < n_leaves) load_leaf(row, l + u * step, lane, k[u]);
     if (!waited) {
       cluster_wait();
       waited = true;
     }
-    const uint32_t at = leaf0 + static_cast<uint32_t>(l * sizeof(Stats));
-    if (lane == 0) {
-      st_cluster_u32(at, __float_as_uint(m));
-      st_cluster_u32(at + 4, __float_as_uint(part));
-    }
-    if (lane == 16) st_cluster_u32(at + 8, __float_as_uint(part));
-    if (TOP && lane < GROUPS_PER_LEAF) {
-      const float v = lane < 2 ? (lane == 0 ? gm[0] : gm[1]) : (lane == 2 ? gm[2] : gm[3]);
-      const int i = l * GROUPS_PER_LEAF + lane;  // groups past the row take key 0: never chosen
-      st_cluster_u32(key0 + static_cast<uint32_t>(i * 4), i * LEAF_GROUP < row.n ? order_key(v) : 0u);
-    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (u == 0 || l + u * step < n_leaves)
+        count += leaf_pass<ENT, TOP>(k[u], l + u * step, c, rank, leaf0, group0, lane);
   }
   if (!waited) cluster_wait();
   if (rank.on) {
     count = __reduce_add_sync(kFullWarp, count);
     if (lane == 0) st_cluster_u32(map_to_cta(smem_u32(sm.count + g), 0), static_cast<uint32_t>(count));
   }
-  if (TOP && r == 0)
-    for (int i = n_leaves * GROUPS_PER_LEAF + threadIdx.x; i < keys_of(row.n); i += blockDim.x) sm.key[i] = 0u;
   if (C > 1) cluster_sync();
   else __syncthreads();
 }
 
 // ---------------------------------------------------------------------------
-// the best k of N keys, by one warp
+// the best of N keys, by one warp
 // ---------------------------------------------------------------------------
-// Chooses min(k, N) places of key[0 .. N) -- the largest keys, the lower place first among equals --
-// writes them to `place` in ascending order and returns the smallest chosen key >> shift. N is
-// padded with zero keys to a multiple of 128. The keys hold nothing in their low `shift` bits, so
-// the search (bisection on the key, counting the keys at or above the middle) ends after at most
-// 32 - shift rounds; usually it hits a key that exactly k reach earlier.
-__device__ __forceinline__ uint32_t choose_best(const uint32_t* key, int N, int k, int shift, int* place, int lane) {
+// Chooses between k and `most` places of key[0 .. N) (all of them when N <= k) that hold its k best --
+// the largest keys, the lower place first among equals -- writes them to `place` in ascending order,
+// and the key >> shift that all of them reach to *bar. N is padded with zero keys to a multiple of
+// 128; the keys hold nothing in their low `shift` bits. A first bar that k places reach is the k-th
+// of the 32 lanes' maxima (k <= 32); where more than `most` reach it, bisection on the key raises
+// it, counting the keys at or above the middle, and ties that no bar can part are cut by place.
+__device__ __forceinline__ int choose_best(const uint32_t* key, int N, int k, int most, int shift, int* place,
+                                           uint32_t* bar, int lane) {
   const int padded = (N + 127) / 128 * 128;
-  const auto count_from = [&](uint32_t bar) {
+  const auto count_from = [&](uint32_t b) {
     int n = 0;
     for (int i = lane * 4; i < padded; i += 128) {
       const uint4 v = *reinterpret_cast<const uint4*>(key + i);
-      n += (v.x >> shift >= bar) + (v.y >> shift >= bar) + (v.z >> shift >= bar) + (v.w >> shift >= bar);
+      n += (v.x >> shift >= b) + (v.y >> shift >= b) + (v.z >> shift >= b) + (v.w >> shift >= b);
     }
     return __reduce_add_sync(kFullWarp, n);
   };
-  // 32 lanes' maxima: 32 places reach the smallest of them
-  uint32_t top = 0;
-  for (int i = lane; i < N; i += 32) top = max(top, key[i]);
-  uint32_t hi = (__reduce_max_sync(kFullWarp, top) >> shift) + 1;       // fewer than k reach it
-  uint32_t lo = k <= 32 && N >= 32 ? __reduce_min_sync(kFullWarp, top) >> shift : 0u;  // at least min(k, N) do
-  if (k >= N) hi = lo = 0;
-  while (hi - lo > 1) {
-    const uint32_t mid = lo + (hi - lo) / 2;
-    const int n = count_from(mid);
-    if (n >= k) lo = mid;
-    else hi = mid;
-    if (n == k) break;
+  uint32_t lo = 0;
+  int n = N, ties = N;  // places that reach lo; places at lo that are taken
+  if (N > k) {
+    uint32_t top = 0;
+    for (int i = lane; i < N; i += 32) top = max(top, key[i] >> shift);
+    uint32_t hi = __reduce_max_sync(kFullWarp, top) + 1;  // fewer than k reach it
+    if (k <= 32 && N >= 32) {
+      int before = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const uint32_t other = __shfl_sync(kFullWarp, top, j);
+        before += other > top || (other == top && j < lane);
+      }
+      lo = __shfl_sync(kFullWarp, top, __ffs(__ballot_sync(kFullWarp, before == k - 1)) - 1);
+      n = count_from(lo);
+    }
+    while (n > most && hi - lo > 1) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      const int m = count_from(mid);
+      if (m >= k) lo = mid, n = m;
+      else hi = mid;
+    }
+    if (n > most) ties = k - count_from(lo + 1);
   }
-  int ties = k;  // places at lo that are taken
-  if (k < N) ties -= count_from(lo + 1);
   int out = 0;
   for (int i0 = 0; i0 < N; i0 += 32) {
     const int i = i0 + lane;
@@ -173,7 +199,8 @@ __device__ __forceinline__ uint32_t choose_best(const uint32_t* key, int N, int 
     out += __popc(taken);
     ties -= min(ties, __popc(eq));
   }
-  return lo;
+  *bar = lo;
+  return out;
 }
 
 struct ScoreArgs {
@@ -190,96 +217,102 @@ struct ScoreArgs {
 };
 
 // Shared memory of the alternatives' search.
+constexpr int FEW = 256;           // candidates that go straight to the last step
 struct TopSmem {
   unsigned long long cand[CAND];   // order key in the high word, ~column in the low one
-  int place[RLK_MAX_TOP_K];        // chosen groups, then chosen octets
-  int n_cand;
-  uint32_t bar;                    // smallest chosen key >> kKeyShift
+  int place[RLK_MAX_TOP_K];        // chosen groups
+  int octet[RLK_MAX_TOP_K];        // chosen octets
+  int n_place, n_octet, n_cand;
+  uint32_t bar;                    // key >> kKeyShift that the chosen reach
   float lse;
 };
 
 // Dynamic shared memory of a row: the octets' keys take the place of the leaves' statistics and the
 // groups' keys, which have been used by then.
 __host__ __device__ constexpr size_t row_smem_bytes(int n, bool top) {
-  size_t b = static_cast<size_t>((leaves_of(n) * sizeof(Stats) + 15) / 16 * 16);
+  size_t b = leaves_of(n) * sizeof(Stats);
   if (!top) return b;
   b += static_cast<size_t>(keys_of(n)) * 4;
   const size_t octets = RLK_MAX_TOP_K * 32 * 4;
   return b > octets ? b : octets;
 }
 
+__device__ __forceinline__ int chosen_most(int k) { return min(RLK_MAX_TOP_K, 2 * k + 16); }
+
+// The smallest finite value whose order key >> shift reaches `bar`.
+__device__ __forceinline__ float bar_value(uint32_t bar, int shift) {
+  const uint32_t key = bar << shift;
+  return key <= order_key(neg_inf()) ? -3.4028235e38f : key_value(key);
+}
+
+// Adds the columns of a pack (its first column c) that reach the value `bar` to the candidates,
+// `most` of them at the most; n_cand counts them all. Few lanes have any.
+template <class E>
+__device__ __forceinline__ void offer(const Pack<E>& k, int c, float bar, int most, TopSmem& ts) {
+  if (!(pack_max(k) >= bar)) return;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 z2 = pair(k, i / 2);
+    const float z = i & 1 ? z2.y : z2.x;
+    if (z >= bar) {
+      const int at = atomicAdd(&ts.n_cand, 1);
+      if (at < most) ts.cand[at] = static_cast<unsigned long long>(order_key(z)) << 32 | static_cast<uint32_t>(~(c + i));
+    }
+  }
+}
+
 // The top_k alternatives of a row, by one CTA, from its groups' keys.
 //  1. The k groups of 256 columns with the largest maxima (lower group first among equals) hold
-//     the k best columns: a column outside them has k group maxima ahead of it.
-//  2. Their columns that reach the smallest chosen maximum are the candidates: k or a few more,
-//     unless good columns crowd into few groups or are tied.
+//     the k best columns: a column outside them has k group maxima ahead of it. choose_best gives
+//     them and a few more, and a bar that k columns reach.
+//  2. Their columns that reach the bar are the candidates: little more than k, unless good columns
+//     crowd into few groups or are tied.
 //  3. If they are too many, the same choice among the chosen groups' octets (8 columns) leaves
-//     at most 8 k.
+//     at most CAND.
 //  4. Each candidate's place is the number of candidates ahead of it.
 template <class R, class E = typename R::E>
 __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowSmem& sm, TopSmem& ts,
                          bool bad, float lse) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int groups = (row.n + LEAF_GROUP - 1) / LEAF_GROUP, K = a.top_k, chosen = min(K, groups);
-  constexpr int FEW = 256;
+  const int K = a.top_k, chosen = bad ? 0 : ts.n_place;
   const auto pack_of = [&](int c) {
     return packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c);
   };
-  const auto offer = [&](float z, int col, uint32_t bar, int most) {
-    const uint32_t o = order_key(z);
-    if (o >> E::kKeyShift < bar || z == neg_inf()) return;
-    const int at = atomicAdd(&ts.n_cand, 1);
-    if (at < most) ts.cand[at] = static_cast<unsigned long long>(o) << 32 | static_cast<uint32_t>(~col);
-  };
-  const uint32_t bar = ts.bar;
-  if (!bad) {
+  const float bar = bar_value(ts.bar, E::kKeyShift);
+  bool many = !bad && ts.bar == 0 && row.n > FEW;  // every column reaches the bar
+  if (!many) {
     for (int i0 = warp; i0 < chosen; i0 += 4 * warps) {
       Pack<E> k[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (i0 + u * warps < chosen) k[u] = pack_of(ts.place[i0 + u * warps] * LEAF_GROUP + lane * 8);
+      int c[4];
+      const int n = min(4, (chosen - i0 + warps - 1) / warps);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        if (i0 + u * warps >= chosen) break;
-        const float m = pack_max(k[u]);
-        if (order_key(m) >> E::kKeyShift < bar || m == neg_inf()) continue;
-        const int c = ts.place[i0 + u * warps] * LEAF_GROUP + lane * 8;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 z = pair(k[u], i / 2);
-          offer(i & 1 ? z.y : z.x, c + i, bar, FEW);
-        }
+        c[u] = u < n ? ts.place[i0 + u * warps] * LEAF_GROUP + lane * 8 : 0;
+        if (u < n) k[u] = pack_of(c[u]);
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (u < n) offer(k[u], c[u], bar, FEW, ts);
     }
+    __syncthreads();
+    many = ts.n_cand > FEW;
   }
-  __syncthreads();
-  if (ts.n_cand > FEW) {  // the same for the whole CTA
+  if (many) {  // the same for the whole CTA
     uint32_t* okey = reinterpret_cast<uint32_t*>(sm.leaf);
     const int N = chosen * 32;
     for (int i = warp; i < chosen; i += warps)
       okey[i * 32 + lane] = order_key(pack_max(pack_of(ts.place[i] * LEAF_GROUP + lane * 8)));
     for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) okey[i] = 0u;
     __syncthreads();
-    int* octet = reinterpret_cast<int*>(ts.cand) + 2 * CAND - RLK_MAX_TOP_K;  // not yet in use
     if (warp == 0) {
-      const uint32_t b = choose_best(okey, N, min(K, N), E::kKeyShift, octet, lane);
-      if (lane == 0) ts.bar = b, ts.n_cand = 0;
+      uint32_t b;
+      const int m = choose_best(okey, N, K, chosen_most(K), E::kKeyShift, ts.octet, &b, lane);
+      if (lane == 0) ts.bar = b, ts.n_octet = m, ts.n_cand = 0;
     }
     __syncthreads();
-    int mine = -1;  // first column of this thread's octet
-    if (threadIdx.x < min(K, N)) {
-      const int o = octet[threadIdx.x];
-      mine = ts.place[o / 32] * LEAF_GROUP + o % 32 * 8;
-    }
-    const uint32_t b2 = ts.bar;
-    __syncthreads();
-    if (mine >= 0) {
-      const Pack<E> k = pack_of(mine);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 z = pair(k, i / 2);
-        offer(i & 1 ? z.y : z.x, mine + i, b2, CAND);
-      }
+    for (int i = threadIdx.x; i < ts.n_octet; i += blockDim.x) {
+      const int c = ts.place[ts.octet[i] / 32] * LEAF_GROUP + ts.octet[i] % 32 * 8;
+      offer(pack_of(c), c, bar_value(ts.bar, E::kKeyShift), CAND, ts);
     }
     __syncthreads();
   }
@@ -289,6 +322,7 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowS
   for (int i = threadIdx.x; i < n; i += blockDim.x) {
     const unsigned long long me = ts.cand[i];
     int place = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) place += ts.cand[j] > me;
     if (place < K) {
       ids[place] = static_cast<int64_t>(~static_cast<uint32_t>(me));
@@ -313,7 +347,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const Sc
   const Row<E, AL> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
   RowSmem sm;
   sm.leaf = reinterpret_cast<Stats*>(dyn);
-  sm.key = reinterpret_cast<uint32_t*>(dyn + (leaves_of(in.n) * sizeof(Stats) + 15) / 16 * 16);
+  sm.group = reinterpret_cast<float*>(sm.leaf + leaves_of(in.n));
   sm.count = counts;
   const int64_t y = a.y ? a.y[t] : -1;
   const bool y_ok = y >= 0 && y < in.n;
@@ -326,15 +360,21 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const Sc
     if constexpr (Pack<E>::EB == 2) rank.ge *= 0x10001u, rank.gt *= 0x10001u;
   }
   if (TOP && threadIdx.x == 0) ts.n_cand = 0;
-  row_pass<TOP>(row, in.c, rank, sm, C, r);
+  row_pass<true, TOP>(row, in.c, rank, sm, C, r);
   if (r != 0) return;
-  if (warp == 1) {
+  const int groups = (in.n + LEAF_GROUP - 1) / LEAF_GROUP;
+  uint32_t* key = reinterpret_cast<uint32_t*>(sm.group);
+  if constexpr (TOP) {  // maxima to keys; places past the last group get key 0: never chosen
+    for (int i = threadIdx.x; i < keys_of(in.n); i += blockDim.x) key[i] = i < groups ? order_key(sm.group[i]) : 0u;
+    __syncthreads();
+  }
+  if (warp == (blockDim.x > 32)) {
     const Stats x = fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane);
     const float lse = row_lse(x, in.s);
     const bool bad = isnan(lse);
     int before = 0;
     if (rank.on)
-      for (int i = lane; i < C * (ROW_THREADS / 32); i += 32) before += counts[i];
+      for (int i = lane; i < C * static_cast<int>(blockDim.x >> 5); i += 32) before += counts[i];
     before = __reduce_add_sync(kFullWarp, before);
     if (lane == 0) {
       if (TOP) ts.lse = lse;
@@ -348,9 +388,9 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const Sc
   }
   if constexpr (TOP) {
     if (warp == 0) {
-      const int groups = (in.n + LEAF_GROUP - 1) / LEAF_GROUP;
-      const uint32_t b = choose_best(sm.key, groups, min(a.top_k, groups), E::kKeyShift, ts.place, lane);
-      if (lane == 0) ts.bar = b;
+      uint32_t b;
+      const int m = choose_best(key, groups, a.top_k, chosen_most(a.top_k), E::kKeyShift, ts.place, &b, lane);
+      if (lane == 0) ts.bar = b, ts.n_place = m;
     }
     __syncthreads();
     find_top(row, a, t, sm, ts, isnan(ts.lse), ts.lse);
@@ -641,7 +681,7 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
   if (warp == ROW_THREADS / 32 - 1 && (BWD || r == 0))
     teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, lane);
   RowSmem sm{reinterpret_cast<Stats*>(dyn), nullptr, nullptr};
-  row_pass<false>(row, in.c, RankOf{false, 0, 0.f, 0u, 0u}, sm, C, r);
+  row_pass<false, false>(row, in.c, RankOf{false, 0, 0.f, 0u, 0u}, sm, C, r);
   if (r == 0 && warp == 0) {
     const float lse = row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s);
     if (BWD && lane < C) st_cluster_u32(map_to_cta(smem_u32(&lse_s), lane), __float_as_uint(lse));

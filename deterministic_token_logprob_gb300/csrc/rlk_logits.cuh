@@ -265,8 +265,8 @@ __device__ __forceinline__ float pack_max(const Pack<E>& k) {
 // ---------------------------------------------------------------------------
 // row statistics
 // ---------------------------------------------------------------------------
-struct Stats {
-  float m, s, u;
+struct alignas(16) Stats {
+  float m, s, u, pad;
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -297,20 +297,19 @@ __device__ __forceinline__ void load_leaf(const R& r, int leaf, int lane, Pack<t
   }
 }
 
-// Butterfly sums of two values with one exchange a level: lanes 0-15 end with the sum of a,
-// lanes 16-31 with the sum of b (the bits of warp_sum).
-__device__ __forceinline__ float warp_sum_pair(float a, float b, int lane) {
+// Butterfly sums of two values with one exchange a level (the bits of warp_sum): lanes 0-15 work
+// on the first, lanes 16-31 on the second; lane 0 gets both.
+__device__ __forceinline__ float2 warp_sum_pair(float a, float b, int lane) {
   const bool low = lane < 16;
   float v = __fadd_rn(low ? a : b, __shfl_xor_sync(kFullWarp, low ? b : a, 16));
 #pragma unroll
   for (int d = 8; d >= 1; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFullWarp, v, d));
-  return v;
+  return make_float2(v, __shfl_down_sync(kFullWarp, v, 16));
 }
 
-// s and u of a leaf about its maximum m (not -inf): lanes 0-15 return s, lanes 16-31 u. NaN or
-// +inf among the columns makes s NaN.
-template <class E>
-__device__ __forceinline__ float leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], float m, float c, int lane) {
+// s and, with ENT, u of a leaf about its maximum m (not -inf). NaN or +inf among the columns makes s NaN.
+template <bool ENT, class E>
+__device__ __forceinline__ float2 leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], float m, float c, int lane) {
   const F32x2 nm = pack_f32x2(-m, -m), cc = pack_f32x2(c, c);
   F32x2 s2 = 0, u2 = 0;  // even and odd columns
 #pragma unroll
@@ -322,10 +321,11 @@ __device__ __forceinline__ float leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], floa
       const float2 x = unpack_f32x2(mul2(d, cc));
       const F32x2 w = pack_f32x2(ex2_approx(x.x), ex2_approx(x.y));
       s2 = add2(s2, w);
-      u2 = fma2(w, d, u2);
+      if constexpr (ENT) u2 = fma2(w, d, u2);
     }
   const float2 s = unpack_f32x2(s2), u = unpack_f32x2(u2);
   const float sl = __fadd_rn(s.x, s.y);
+  if constexpr (!ENT) return make_float2(warp_sum(sl), 0.f);
   float ul = __fadd_rn(u.x, u.y);
   if (__any_sync(kFullWarp, isnan(ul))) {
     // masked columns: weight 0 times d = -inf. Once more with d kept finite (a NaN logit reaches
@@ -372,7 +372,7 @@ __device__ __forceinline__ Stats fold_leaves(const Stats* leaf, int n_leaves, fl
     // u relative to M: sum w (z - M) = u + s (m - M); a leaf too far down to count adds nothing
     if (f != 0.f) U = __fmaf_rn(f, __fmaf_rn(x.s, d, x.u), U);
   }
-  return Stats{M, warp_sum(S), warp_sum(U)};
+  return Stats{M, warp_sum(S), warp_sum(U), 0.f};
 }
 
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
