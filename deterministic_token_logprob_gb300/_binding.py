@@ -52,6 +52,9 @@ def library_path() -> str:
 
 def _load():
     global _lib
+    loaded = _lib
+    if loaded is not None:
+        return loaded
     with _lock:
         if _lib is not None:
             return _lib

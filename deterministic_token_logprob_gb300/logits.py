@@ -16,12 +16,10 @@ used there.
 from __future__ import annotations
 
 import contextlib
-import ctypes
 from typing import NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
-from . import _binding
 from ._binding import _check, _load
 
 RLK_DTYPE_BF16 = 0
@@ -46,31 +44,33 @@ class TokenLogprobs(NamedTuple):
     top_logp: Optional[torch.Tensor]
 
 
-def _rows(t: torch.Tensor, name: str, dtypes=_DTYPES) -> Tuple[int, int, int]:
-    """Checks a [T, V] tensor with contiguous rows; (T, V, row distance)."""
+def _rows(t: torch.Tensor, name: str) -> Tuple[int, int, int, int]:
+    """Checks a [T, V] tensor with contiguous rows; (T, V, row distance, dtype code)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be one of {[str(d) for d in dtypes]}, got {t.dtype}")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be one of {[str(d) for d in _DTYPES]}, got {t.dtype}")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
     T, V = t.shape
     ld, inner = t.stride()
-    if V > 1 and inner != 1:
+    if inner != 1 and V > 1:
         raise ValueError(f"{name} must have contiguous rows (stride(1) == 1)")
-    if T <= 1:  # the stride of a single row says nothing
-        ld = max(ld, V)
     if ld < V:
-        raise ValueError(f"{name} must not have overlapping rows")
-    return T, V, ld
+        if T > 1:
+            raise ValueError(f"{name} must not have overlapping rows")
+        ld = V  # the stride of a single row says nothing
+    return T, V, ld, code
 
 
-def _per_row(t, name: str, dtype, shape, device):
+def _per_row(t, name: str, dtype, shape, device) -> int:
+    """The address of a contiguous tensor of this dtype, shape and device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
@@ -82,21 +82,30 @@ def _per_row(t, name: str, dtype, shape, device):
 
 
 def _flag(err_flag, device):
-    if err_flag is None:
-        return None
-    return _per_row(err_flag, "err_flag", torch.int32, (1,), device)
+    return None if err_flag is None else _per_row(err_flag, "err_flag", torch.int32, (1,), device)
+
+
+# The current stream's handle without building a torch.cuda.Stream: a small call (one token, or a
+# small model's step) is bounded by its work on the host.
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _away(stream, device) -> bool:
+    """Whether a call has to change the current stream or device first (see _elsewhere)."""
+    return stream is not None or device.index != torch.cuda.current_device()
 
 
 @contextlib.contextmanager
-def _launch_on(stream, device, tensors):
-    """The stream handle to launch on, with `device` current; outputs made inside belong to that
-    stream, and `tensors` are recorded as used there when it is not their current stream."""
+def _elsewhere(stream, device, tensors):
+    """Makes `device` and `stream` current, so that outputs belong to that stream, and records
+    `tensors` as used there."""
     with torch.cuda.device(device):
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
+            yield
             return
         with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+            yield
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
@@ -118,51 +127,60 @@ def token_logprobs(logits: torch.Tensor, y: Optional[torch.Tensor] = None, *, to
 
     `out` supplies the six output tensors in the order of :class:`TokenLogprobs` (a serving loop
     keeps them between steps); None in a place leaves that output out."""
-    T, V, ld = _rows(logits, "logits")
+    T, V, ld, code = _rows(logits, "logits")
     dev = logits.device
+    if _away(stream, dev):
+        with _elsewhere(stream, dev, (logits, y, err_flag, *(out or ()))):
+            return token_logprobs(logits, y, top_k=top_k, V_true=V_true, temperature=temperature, out=out,
+                                  err_flag=err_flag)
     V_true = _true_vocab(V_true, V)
     if not 0 <= top_k <= MAX_TOP_K:
         raise ValueError(f"top_k must be in 0 .. {MAX_TOP_K}, got {top_k}")
-    if y is not None:
-        _per_row(y, "y", torch.int64, (T,), dev)
-    flag = _flag(err_flag, dev)
-    with _launch_on(stream, dev, (logits, y, err_flag, *(out or ()))) as handle:
-        if out is None:
-            f32 = dict(dtype=torch.float32, device=dev)
-            out = (None if y is None else torch.empty(T, **f32),
-                   None if y is None else torch.empty(T, dtype=torch.int32, device=dev),
-                   torch.empty(T, **f32), torch.empty(T, **f32),
-                   torch.empty((T, top_k), dtype=torch.int64, device=dev) if top_k else None,
-                   torch.empty((T, top_k), **f32) if top_k else None)
-        elif len(out) != 6:
-            raise ValueError("out must hold six tensors (or None): logp, rank, lse, entropy, top_ids, top_logp")
+    rows, i32, i64, f32 = (T,), torch.int32, torch.int64, torch.float32
+    py = None if y is None else _per_row(y, "y", i64, rows, dev)
+    if out is None:
+        r = TokenLogprobs(None if y is None else torch.empty(rows, dtype=f32, device=dev),
+                          None if y is None else torch.empty(rows, dtype=i32, device=dev),
+                          torch.empty(rows, dtype=f32, device=dev), torch.empty(rows, dtype=f32, device=dev),
+                          torch.empty((T, top_k), dtype=i64, device=dev) if top_k else None,
+                          torch.empty((T, top_k), dtype=f32, device=dev) if top_k else None)
+    elif len(out) != 6:
+        raise ValueError("out must hold six tensors (or None): logp, rank, lse, entropy, top_ids, top_logp")
+    else:
         r = TokenLogprobs(*out)
-        shapes = dict(logp=(torch.float32, (T,)), rank=(torch.int32, (T,)), lse=(torch.float32, (T,)),
-                      entropy=(torch.float32, (T,)), top_ids=(torch.int64, (T, top_k)),
-                      top_logp=(torch.float32, (T, top_k)))
-        p = [None if t is None else _per_row(t, n, *shapes[n], dev) for n, t in zip(r._fields, r)]
-        st = _load().rlk_token_logprobs(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
-                                        float(temperature), None if y is None else y.data_ptr(),
-                                        int(top_k), *p, flag, handle)
-    _check("rlk_token_logprobs", st)
+    logp, rank, lse, entropy, ids, top = r
+    st = _load().rlk_token_logprobs(
+        logits.data_ptr(), code, T, ld, V_true, temperature, py, top_k,
+        None if logp is None else _per_row(logp, "logp", f32, rows, dev),
+        None if rank is None else _per_row(rank, "rank", i32, rows, dev),
+        None if lse is None else _per_row(lse, "lse", f32, rows, dev),
+        None if entropy is None else _per_row(entropy, "entropy", f32, rows, dev),
+        None if ids is None else _per_row(ids, "top_ids", i64, (T, top_k), dev),
+        None if top is None else _per_row(top, "top_logp", f32, (T, top_k), dev),
+        _flag(err_flag, dev), _raw_stream(dev.index))
+    if st:
+        _check("rlk_token_logprobs", st)
     return r
 
 
 def _gradient(logits, T, V, out, out_dtype):
-    """The dlogits tensor to fill: `out` ([T, at least V], rows contiguous), or a new [T, V] one."""
+    """The dlogits tensor to fill -- `out` ([T, at least V], rows contiguous) or a new [T, V] one --
+    and its C arguments."""
     if out is None:
         dtype = out_dtype or logits.dtype
-        if dtype not in _DTYPES:
+        code = _DTYPES.get(dtype)
+        if code is None:
             raise TypeError(f"out_dtype must be one of {[str(d) for d in _DTYPES]}, got {dtype}")
-        return torch.empty((T, V), dtype=dtype, device=logits.device), V, max(V, 1)
-    oT, oV, old = _rows(out, "out")
+        d = torch.empty((T, V), dtype=dtype, device=logits.device)
+        return d, (d.data_ptr(), code, V, max(V, 1))
+    oT, oV, old, code = _rows(out, "out")
     if oT != T or oV < V:
         raise ValueError(f"out must have {T} rows of at least {V} columns, got {tuple(out.shape)}")
     if out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
     if out.device != logits.device:
         raise ValueError(f"out must be on {logits.device}, got {out.device}")
-    return out, oV, old
+    return out, (out.data_ptr(), code, oV, old)
 
 
 def token_logprobs_bwd(logits: torch.Tensor, y: torch.Tensor, lse: torch.Tensor,
@@ -174,22 +192,25 @@ def token_logprobs_bwd(logits: torch.Tensor, y: torch.Tensor, lse: torch.Tensor,
     """rlk_token_logprobs_bwd -> dlogits of sum_t (g_logp logp + g_entropy entropy), from the
     forward's lse and entropy. The result has the logits' shape and type (or out_dtype: bfloat16
     for float32 logits); `out` supplies it, the logits themselves included."""
-    T, V, ld = _rows(logits, "logits")
+    T, V, ld, code = _rows(logits, "logits")
     dev = logits.device
-    V_true = _true_vocab(V_true, V)
-    p = [_per_row(y, "y", torch.int64, (T,), dev), _per_row(lse, "lse", torch.float32, (T,), dev),
-         None if entropy is None else _per_row(entropy, "entropy", torch.float32, (T,), dev),
-         _per_row(g_logp, "g_logp", torch.float32, (T,), dev),
-         None if g_entropy is None else _per_row(g_entropy, "g_entropy", torch.float32, (T,), dev)]
+    if _away(stream, dev):
+        with _elsewhere(stream, dev, (logits, y, lse, entropy, g_logp, g_entropy, out, err_flag)):
+            return token_logprobs_bwd(logits, y, lse, entropy, g_logp, g_entropy, V_true=V_true,
+                                      temperature=temperature, out=out, out_dtype=out_dtype, err_flag=err_flag)
+    rows, f32 = (T,), torch.float32
     if g_entropy is not None and entropy is None:
         raise ValueError("g_entropy needs the forward's entropy")
-    flag = _flag(err_flag, dev)
-    with _launch_on(stream, dev, (logits, y, lse, entropy, g_logp, g_entropy, out, err_flag)) as handle:
-        dlogits, oV, old = _gradient(logits, T, V, out, out_dtype)
-        st = _load().rlk_token_logprobs_bwd(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
-                                            float(temperature), *p, dlogits.data_ptr(),
-                                            _DTYPES[dlogits.dtype], oV, old, flag, handle)
-    _check("rlk_token_logprobs_bwd", st)
+    p = (_per_row(y, "y", torch.int64, rows, dev), _per_row(lse, "lse", f32, rows, dev),
+         None if entropy is None else _per_row(entropy, "entropy", f32, rows, dev),
+         _per_row(g_logp, "g_logp", f32, rows, dev),
+         None if g_entropy is None else _per_row(g_entropy, "g_entropy", f32, rows, dev))
+    V_true = _true_vocab(V_true, V)
+    dlogits, d = _gradient(logits, T, V, out, out_dtype)
+    st = _load().rlk_token_logprobs_bwd(logits.data_ptr(), code, T, ld, V_true, temperature, *p, *d,
+                                        _flag(err_flag, dev), _raw_stream(dev.index))
+    if st:
+        _check("rlk_token_logprobs_bwd", st)
     return dlogits
 
 
@@ -199,8 +220,7 @@ def _teacher(ids, teacher, T, dev):
     K = ids.shape[1]
     if not 1 <= K <= MAX_TOP_K:
         raise ValueError(f"K must be in 1 .. {MAX_TOP_K}, got {K}")
-    return K, [_per_row(ids, "ids", torch.int64, (T, K), dev),
-               _per_row(teacher, "teacher", torch.float32, (T, K), dev), K]
+    return (_per_row(ids, "ids", torch.int64, (T, K), dev), _per_row(teacher, "teacher", torch.float32, (T, K), dev), K)
 
 
 def distill_topk_fwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *,
@@ -210,18 +230,19 @@ def distill_topk_fwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Ten
     """rlk_distill_topk_fwd -> (loss, lse), fp32 [T] each: the KL divergence from the softmax of
     the teacher's top logits (fp32 [T, K], at columns ids int64 [T, K], -1: none) to
     softmax(logits / temperature), and the student's lse for the backward."""
-    T, V, ld = _rows(logits, "logits")
+    T, V, ld, code = _rows(logits, "logits")
     dev = logits.device
+    if _away(stream, dev):
+        with _elsewhere(stream, dev, (logits, ids, teacher, err_flag)):
+            return distill_topk_fwd(logits, ids, teacher, V_true=V_true, temperature=temperature, err_flag=err_flag)
+    p = _teacher(ids, teacher, T, dev)
     V_true = _true_vocab(V_true, V)
-    _, p = _teacher(ids, teacher, T, dev)
-    flag = _flag(err_flag, dev)
-    with _launch_on(stream, dev, (logits, ids, teacher, err_flag)) as handle:
-        loss = torch.empty(T, dtype=torch.float32, device=dev)
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
-        st = _load().rlk_distill_topk_fwd(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
-                                          float(temperature), *p, loss.data_ptr(), lse.data_ptr(), flag,
-                                          handle)
-    _check("rlk_distill_topk_fwd", st)
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    st = _load().rlk_distill_topk_fwd(logits.data_ptr(), code, T, ld, V_true, temperature, *p, loss.data_ptr(),
+                                      lse.data_ptr(), _flag(err_flag, dev), _raw_stream(dev.index))
+    if st:
+        _check("rlk_distill_topk_fwd", st)
     return loss, lse
 
 
@@ -232,18 +253,21 @@ def distill_topk_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Ten
                      err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rlk_distill_topk_bwd -> dlogits of sum_t g[t] loss[t], from the forward's lse. Shape, type
     and `out` as in :func:`token_logprobs_bwd`."""
-    T, V, ld = _rows(logits, "logits")
+    T, V, ld, code = _rows(logits, "logits")
     dev = logits.device
+    if _away(stream, dev):
+        with _elsewhere(stream, dev, (logits, ids, teacher, lse, g, out, err_flag)):
+            return distill_topk_bwd(logits, ids, teacher, lse, g, V_true=V_true, temperature=temperature, out=out,
+                                    out_dtype=out_dtype, err_flag=err_flag)
+    p = _teacher(ids, teacher, T, dev)
+    lse_p = _per_row(lse, "lse", torch.float32, (T,), dev)
+    g_p = _per_row(g, "g", torch.float32, (T,), dev)
     V_true = _true_vocab(V_true, V)
-    _, p = _teacher(ids, teacher, T, dev)
-    p += [_per_row(lse, "lse", torch.float32, (T,), dev), _per_row(g, "g", torch.float32, (T,), dev)]
-    flag = _flag(err_flag, dev)
-    with _launch_on(stream, dev, (logits, ids, teacher, lse, g, out, err_flag)) as handle:
-        dlogits, oV, old = _gradient(logits, T, V, out, out_dtype)
-        st = _load().rlk_distill_topk_bwd(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
-                                          float(temperature), *p, dlogits.data_ptr(),
-                                          _DTYPES[dlogits.dtype], oV, old, flag, handle)
-    _check("rlk_distill_topk_bwd", st)
+    dlogits, d = _gradient(logits, T, V, out, out_dtype)
+    st = _load().rlk_distill_topk_bwd(logits.data_ptr(), code, T, ld, V_true, temperature, *p, lse_p, g_p, *d,
+                                      _flag(err_flag, dev), _raw_stream(dev.index))
+    if st:
+        _check("rlk_distill_topk_bwd", st)
     return dlogits
 
 
@@ -255,21 +279,23 @@ def distill_topk_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch
     """rlk_distill_topk_fwd_bwd -> (loss, lse, dlogits): :func:`distill_topk_fwd` and
     :func:`distill_topk_bwd` in one call, for weights g known before the loss (a token mask over
     a count). The same bits; the logits are read from memory once."""
-    T, V, ld = _rows(logits, "logits")
+    T, V, ld, code = _rows(logits, "logits")
     dev = logits.device
+    if _away(stream, dev):
+        with _elsewhere(stream, dev, (logits, ids, teacher, g, out, err_flag)):
+            return distill_topk_fwd_bwd(logits, ids, teacher, g, V_true=V_true, temperature=temperature, out=out,
+                                        out_dtype=out_dtype, err_flag=err_flag)
+    p = _teacher(ids, teacher, T, dev)
+    g_p = _per_row(g, "g", torch.float32, (T,), dev)
     V_true = _true_vocab(V_true, V)
-    _, p = _teacher(ids, teacher, T, dev)
-    p.append(_per_row(g, "g", torch.float32, (T,), dev))
-    flag = _flag(err_flag, dev)
-    with _launch_on(stream, dev, (logits, ids, teacher, g, out, err_flag)) as handle:
-        loss = torch.empty(T, dtype=torch.float32, device=dev)
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
-        dlogits, oV, old = _gradient(logits, T, V, out, out_dtype)
-        st = _load().rlk_distill_topk_fwd_bwd(logits.data_ptr(), _DTYPES[logits.dtype], T, ld, V_true,
-                                              float(temperature), *p, loss.data_ptr(), lse.data_ptr(),
-                                              dlogits.data_ptr(), _DTYPES[dlogits.dtype], oV, old, flag,
-                                              handle)
-    _check("rlk_distill_topk_fwd_bwd", st)
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    dlogits, d = _gradient(logits, T, V, out, out_dtype)
+    st = _load().rlk_distill_topk_fwd_bwd(logits.data_ptr(), code, T, ld, V_true, temperature, *p, g_p,
+                                          loss.data_ptr(), lse.data_ptr(), *d, _flag(err_flag, dev),
+                                          _raw_stream(dev.index))
+    if st:
+        _check("rlk_distill_topk_fwd_bwd", st)
     return loss, lse, dlogits
 
 
