@@ -3,6 +3,7 @@
 // (forward, backward, both in one call).
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <utility>
 
 #include "rlk_logits.cuh"
@@ -82,11 +83,12 @@ __device__ __forceinline__ int count_ahead(const Pack<E> (&k)[LEAF_GROUPS], cons
   return n;
 }
 
-// What one leaf leaves behind (see RowSmem); returns how many of the lane's columns stand ahead of
-// the target.
+// What one leaf leaves behind (see RowSmem), at leaf0 / group0 of the cluster's shared memory, from
+// each lane that `puts` (lane 0 alone with ENT: the others lack u). Returns how many of the lane's
+// columns stand ahead of the target.
 template <bool ENT, bool TOP, class E>
 __device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l, float c, const RankOf& rank,
-                                         uint32_t leaf0, uint32_t group0, int lane) {
+                                         uint32_t leaf0, uint32_t group0, bool puts, int lane) {
   float gm[LEAF_GROUPS], m;
 #pragma unroll
   for (int j = 0; j < LEAF_GROUPS; ++j) {
@@ -98,7 +100,7 @@ __device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l,
   float2 x;
   if (m == neg_inf()) x = make_float2(any_nan(k) ? quiet_nan() : 0.f, 0.f);
   else x = leaf_sums<ENT>(k, m, c, lane);
-  if (lane == 0) {
+  if (puts) {
     st_cluster_f32x4(leaf0 + static_cast<uint32_t>(l * 16), m, x.x, x.y, 0.f);
     if (TOP) st_cluster_f32x4(group0 + static_cast<uint32_t>(l * 16), gm[0], gm[1], gm[2], gm[3]);
   }
@@ -106,33 +108,43 @@ __device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l,
   return rank.on && m >= rank.z ? count_ahead(k, rank, l, lane) : 0;
 }
 
-// Leaves that a warp loads at once: 64 bytes a lane and leaf in 16-bit types leave too little in
-// flight (96 -> 83 us at 1820 rows of 151936), 128 in fp32 do.
-template <class E>
-constexpr int kLeavesAtOnce = sizeof(typename E::bits) == 2 ? 1 : 1;
-
 template <bool ENT, bool TOP, class R, class E = typename R::E>
 __device__ __forceinline__ void row_pass(const R& row, float c, const RankOf& rank, const RowSmem& sm, int C, int r) {
-  constexpr int U = kLeavesAtOnce<E>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5, g = r * warps + warp, n_leaves = leaves_of(row.n), step = C * warps;
   if (C > 1) cluster_arrive();  // CTA 0 must have started before anyone writes to it
   bool waited = C == 1;
-  const uint32_t leaf0 = map_to_cta(smem_u32(sm.leaf), 0), group0 = TOP ? map_to_cta(smem_u32(sm.group), 0) : 0;
+  const uint32_t leaf0 = map_to_cta(smem_u32(sm.leaf), 0);
+  const uint32_t group0 = TOP ? map_to_cta(smem_u32(sm.group), 0) : 0;
   int count = 0;
-  for (int l = g; l < n_leaves; l += U * step) {
-    Pack<E> k[U][LEAF_GROUPS];
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u == 0 || l + u * step < n_leaves) load_leaf(row, l + u * step, lane, k[u]);
+  if constexpr (ENT || sizeof(typename E::bits) == 4) {
+    // 64 registers leave no room for a second leaf; the other warps hide the loads
+    for (int l = g; l < n_leaves; l += step) {
+      Pack<E> k[LEAF_GROUPS];
+      load_leaf(row, l, lane, k);
+      if (!waited) {
+        cluster_wait();
+        waited = true;
+      }
+      count += leaf_pass<ENT, TOP>(k, l, c, rank, leaf0, group0, lane == 0, lane);
+    }
+  } else if (g < n_leaves) {
+    // the next leaf is loaded before this one is summed (8192 rows of 151936 in bf16: 378 -> 354 us)
+    Pack<E> k[2][LEAF_GROUPS];
+    load_leaf(row, g, lane, k[0]);
     if (!waited) {
       cluster_wait();
       waited = true;
     }
+    for (int l = g; l < n_leaves; l += 2 * step) {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (u == 0 || l + u * step < n_leaves)
-        count += leaf_pass<ENT, TOP>(k[u], l + u * step, c, rank, leaf0, group0, lane);
+      for (int u = 0; u < 2; ++u) {
+        const int i = l + u * step;
+        if (i >= n_leaves) break;
+        if (i + step < n_leaves) load_leaf(row, i + step, lane, k[u ^ 1]);
+        leaf_pass<ENT, TOP>(k[u], i, c, rank, leaf0, group0, lane == 0, lane);
+      }
+    }
   }
   if (!waited) cluster_wait();
   if (rank.on) {
@@ -589,16 +601,59 @@ struct DistillArgs {
   float* lse;
 };
 
-// Loss of one row by one warp (every lane gets it).
-template <class R>
-__device__ __forceinline__ float row_loss(const TeacherRow& q, const R& row, float lse, float s, int lane) {
+// Loss of one row by one warp (every lane gets it); zk: the student's logits of the entries.
+__device__ __forceinline__ float row_loss(const TeacherRow& q, const float* zk, float lse, float s, int lane) {
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < RLK_MAX_TOP_K / 32; ++i) {
     const int k = lane + 32 * i;
-    if (q.t[k] > 0.f) sum = __fmaf_rn(q.t[k], __fsub_rn(q.logq[k], token_logp(row.at(q.id[k]), s, lse)), sum);
+    if (q.q[k] > 0.f) sum = __fmaf_rn(q.q[k], __fsub_rn(q.logq[k], token_logp(zk[k], s, lse)), sum);
   }
   return warp_sum(sum);
+}
+
+// The student's logits at the entries' columns (0 without an entry), by the warp that made q.
+template <class R>
+__device__ __forceinline__ void gather_logits(const TeacherRow& q, const R& row, float* zk, int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < RLK_MAX_TOP_K / 32; ++i) {
+    const int id = q.id[lane + 32 * i];
+    zk[lane + 32 * i] = id >= 0 ? row.at(id) : 0.f;
+  }
+}
+
+// The loss's outputs of a row, by one warp.
+__device__ __forceinline__ void put_loss(const DistillArgs& a, int64_t t, const TeacherRow& q, const float* zk, float lse,
+                                         int lane) {
+  const float l = row_loss(q, zk, lse, a.in.s, lane);
+  if (lane != 0) return;
+  a.loss[t] = isnan(lse) || q.bad ? quiet_nan() : l;
+  if (a.lse) a.lse[t] = lse;
+  const int flags = q.bad | (isnan(lse) ? RLK_FLAG_NONFINITE : 0);
+  if (flags && a.in.err_flag) atomicOr(a.in.err_flag, flags);
+}
+
+__device__ __forceinline__ bool distill_live(const TeacherRow& q, float lse, float g) {
+  return !isnan(lse) && lse != neg_inf() && q.any && !q.bad && g != 0.f;
+}
+
+// dz of entry k's column, A (p - sum of q over the entries of that column in ascending order), if k
+// is the first of them; false otherwise.
+__device__ __forceinline__ bool entry_dz(const TeacherRow& q, int k, int K, float z, float s, float lse, float A, float* dz) {
+  const int id = q.id[k];
+  float qk = 0.f;
+  for (int j = 0; j < K; j += 4) {  // places past K hold no entry
+    const int4 o = *reinterpret_cast<const int4*>(q.id + j);
+    if (o.x != id && o.y != id && o.z != id && o.w != id) continue;
+    for (int e = 0; e < 4; ++e) {
+      if (q.id[j + e] != id) continue;
+      if (j + e < k) return false;
+      qk = __fadd_rn(qk, q.q[j + e]);
+    }
+  }
+  *dz = __fmul_rn(A, __fsub_rn(prob_of(__fmaf_rn(z, s, -lse)), qk));
+  return true;
 }
 
 // dz = A p, p = e^{s z - lse}.
@@ -619,87 +674,250 @@ struct DistillDz {
   }
 };
 
-// The gradient of one part of a row, by one CTA. q holds the row's teacher distribution.
-template <int U, class G>
-__device__ __forceinline__ void distill_part(const G& part, const typename G::E::bits* z, const TeacherRow& q, float* zs,
-                                             int K, float s, float lse, float g) {
-  const bool live = !isnan(lse) && lse != neg_inf() && q.any && !q.bad && g != 0.f;
-  const float A = __fmul_rn(s, g);
-  // the logits of the teacher's columns, read before anything is written
-  for (int k = threadIdx.x; k < K; k += blockDim.x)
-    zs[k] = live && part.owns(q.id[k]) ? G::E::to_f32(z[q.id[k]]) : 0.f;
-  write_part<U>(part, live, DistillDz{s, lse, A}, [] { __syncthreads(); });
-  __syncthreads();
-  if (!live) return;
-  // the teacher's columns: the first entry of an id writes the sum over its entries
-  for (int k = threadIdx.x; k < K; k += blockDim.x) {
-    const int id = q.id[k];
-    if (id < 0 || !part.owns(id)) continue;
-    bool first = true;
-    float qk = 0.f;
-    for (int j = 0; j < K; ++j) {
-      if (q.id[j] != id) continue;
-      if (j < k) first = false;
-      qk = __fadd_rn(qk, q.t[j]);
-    }
-    if (first) part.put(id, __fmul_rn(A, __fsub_rn(prob_of(__fmaf_rn(zs[k], s, -lse)), qk)));
-  }
-}
-
-// Backward alone: a.parts CTAs of a row, each its own part.
+// Backward alone: a.cluster CTAs of a row, each its own part.
 template <class E, class O, bool AL>
 __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const DistillArgs a) {
   __shared__ TeacherRow q;
-  __shared__ float zs[RLK_MAX_TOP_K];
+  __shared__ float zk[RLK_MAX_TOP_K];
   const LogitRows& in = a.in;
   const int64_t t = blockIdx.x / a.cluster;
   const auto* z = static_cast<const typename E::bits*>(in.base) + t * in.ld;
   const GradPart<E, O, AL> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
-                            static_cast<int>(blockIdx.x % a.cluster), a.cluster, in.err_flag);
+                                static_cast<int>(blockIdx.x % a.cluster), a.cluster, in.err_flag);
   const float lse = a.lse_in[t], g = a.g[t];
-  if (threadIdx.x < 32)
+  if (threadIdx.x < 32) {
     teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, threadIdx.x);
+    __syncwarp();
+    // the logits of the teacher's columns, read before anything is written; other parts may already
+    // have written theirs
+    const bool in_use = g != 0.f;
+#pragma unroll
+    for (int i = 0; i < RLK_MAX_TOP_K / 32; ++i) {
+      const int k = threadIdx.x + 32 * i;
+      zk[k] = in_use && part.owns(q.id[k]) ? E::to_f32(z[q.id[k]]) : 0.f;
+    }
+  }
   __syncthreads();
   if (q.bad && part.lo == 0 && threadIdx.x == 0 && in.err_flag) atomicOr(in.err_flag, q.bad);
-  distill_part<GRAD_PACKS>(part, z, q, zs, a.K, in.s, lse, g);
+  const bool live = distill_live(q, lse, g);
+  const float A = __fmul_rn(in.s, g);
+  write_part<GRAD_PACKS>(part, live, DistillDz{in.s, lse, A}, [] {});
+  __syncthreads();
+  if (!live) return;
+  for (int k = threadIdx.x; k < a.K; k += ROW_THREADS) {
+    float dz;
+    if (q.id[k] >= 0 && part.owns(q.id[k]) && entry_dz(q, k, a.K, zk[k], in.s, lse, A, &dz)) part.put(q.id[k], dz);
+  }
 }
 
-// Forward (a cluster of CTAs a row), and with BWD the gradient in the same launch: every CTA of the
-// row writes its part, whose logits the cluster has just read.
-// AL: the rows are aligned; GAL: the gradient's packs are (always where dlogits are the logits).
-template <class E, class O, bool BWD, bool AL, bool GAL>
+// Forward: a cluster of CTAs a row.
+template <class E, bool AL>
 __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ TeacherRow q;
-  __shared__ float zs[RLK_MAX_TOP_K];
-  __shared__ float lse_s;
+  __shared__ float zk[RLK_MAX_TOP_K];
   const LogitRows& in = a.in;
   const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x / C;
-  const auto* z = static_cast<const typename E::bits*>(in.base) + t * in.ld;
-  const Row<E, AL> row(z, in.n, in.err_flag);
-  if (warp == ROW_THREADS / 32 - 1 && (BWD || r == 0))
+  const Row<E, AL> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
+  if (r == 0 && warp == static_cast<int>(blockDim.x >> 5) - 1) {
     teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, lane);
+    gather_logits(q, row, zk, lane);
+  }
   RowSmem sm{reinterpret_cast<Stats*>(dyn), nullptr, nullptr};
   row_pass<false, false>(row, in.c, RankOf{false, 0, 0.f, 0u, 0u}, sm, C, r);
-  if (r == 0 && warp == 0) {
-    const float lse = row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s);
-    if (BWD && lane < C) st_cluster_u32(map_to_cta(smem_u32(&lse_s), lane), __float_as_uint(lse));
-    const float l = row_loss(q, row, lse, in.s, lane);
-    if (lane == 0) {
-      a.loss[t] = isnan(lse) || q.bad ? quiet_nan() : l;
-      if (a.lse) a.lse[t] = lse;
-      const int flags = q.bad | (isnan(lse) ? RLK_FLAG_NONFINITE : 0);
-      if (flags && in.err_flag) atomicOr(in.err_flag, flags);
+  if (r == 0 && warp == 0) put_loss(a, t, q, zk, row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s), lane);
+}
+
+// ---------------------------------------------------------------------------
+// forward and backward in one launch
+// ---------------------------------------------------------------------------
+// The cluster's CTAs keep the row in their shared memory between the sum and the gradient, so it
+// is read from memory once. CTA r takes leaves r, r + C, ...; its warp w those with local index w,
+// w + W, ..., and copies all of them asynchronously before anything else, one copy group a leaf,
+// so that the whole row is in flight at once and each leaf is summed as it arrives. The warp that
+// summed a leaf writes its gradient: nothing but the leaves' statistics (to every CTA) and the
+// lse crosses warps.
+constexpr int STEP_THREADS = 288;
+constexpr int STEP_CTAS = 4;              // of one SM
+constexpr int STEP_MAX_ROUNDS = 8;        // leaves of one warp
+constexpr int SLOT_SLACK = 32;            // a misaligned pack is cut from up to 32 bytes more
+
+template <class E>
+__host__ __device__ constexpr int slot_bytes() { return ROW_LEAF * static_cast<int>(sizeof(typename E::bits)) + SLOT_SLACK; }
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+
+// Wait until at most n of this thread's copy groups are pending.
+__device__ __forceinline__ void cp_async_wait(int n) {
+  switch (n) {
+    case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+    case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+    case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+    case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+    case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+    case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+    case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+    default: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+  }
+}
+
+// Copies leaf l into a slot, by one warp: vector v holds the 16 bytes of the row that start
+// `shift` bytes before column 8 v (4 v) of the leaf. Vectors that do not lie inside the row are
+// filled element by element, -inf beyond it.
+template <class R, class E = typename R::E>
+__device__ __forceinline__ void copy_leaf(const R& row, int l, unsigned char* slot, int lane) {
+  constexpr int EB = sizeof(typename E::bits), PER = 16 / EB;
+  constexpr int VECS = ROW_LEAF / PER + (R::AL ? 0 : 1);
+  const int c0 = l * ROW_LEAF - static_cast<int>(row.shift) / EB;  // column of the slot's first element
+  const char* src = reinterpret_cast<const char*>(row.p) + static_cast<int64_t>(c0) * EB;
+  const uint32_t dst = smem_u32(slot);
+  if (c0 >= 0 && c0 + VECS * PER <= row.n) {
+#pragma unroll
+    for (int v = lane; v < VECS; v += 32) cp_async16(dst + v * 16, src + v * 16);
+    return;
+  }
+  auto* out = reinterpret_cast<typename E::bits*>(slot);
+  for (int v = lane; v < VECS; v += 32) {
+    const int c = c0 + v * PER;
+    if (c >= 0 && c + PER <= row.n) {
+      cp_async16(dst + v * 16, src + v * 16);
+    } else {
+      for (int i = 0; i < PER; ++i) out[v * PER + i] = c + i >= 0 && c + i < row.n ? row.p[c + i] : E::kNegInf;
     }
   }
-  if constexpr (BWD) {
-    if (C > 1) cluster_sync();  // the loss has read its logits, and every CTA has the lse
-    else __syncthreads();
-    const GradPart<E, O, GAL> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V, r, C,
-                              in.err_flag);
-    distill_part<2>(part, z, q, zs, a.K, in.s, lse_s, a.g[t]);
+}
+
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.relaxed.cluster.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint16_t ld_cluster_u16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.relaxed.cluster.shared::cluster.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Writes the gradient of a leaf (first column c0) from its slot, by one warp; zeros when !live.
+template <class O, class V, class F>
+__device__ __forceinline__ void leaf_grad(const V& view, typename O::bits* out, int c0, int head, int n, int V_, bool live,
+                                          const F& f, int lane) {
+  using E = typename V::E;
+  const int end = min(V_ - c0, ROW_LEAF);        // columns of the leaf to write
+  if (end == ROW_LEAF && head == 0 && c0 + ROW_LEAF <= n && live) {
+#pragma unroll
+    for (int u = 0; u < LEAF_GROUPS; ++u) {
+      const int c = u * LEAF_GROUP + lane * 8;
+      float v[8];
+      f.pack(load_pack(view, c), c0 + c, v);
+      if (dbg_ok(c0 + c + 8 <= V_, view.err)) store_pack<O>(out + c0 + c, v);
+    }
+    return;
   }
+  const int packs = max(0, end - head) / 8;      // 128 of a whole leaf, 127 with a head
+  for (int p = lane; p < packs; p += 32) {
+    const int c = c0 + head + p * 8;
+    float v[8];
+    f.pack(load_pack(view, p * 8), c, v);        // the slot is filled in any case
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (!live || c + e >= n) v[e] = 0.f;
+    if (dbg_ok(c + 8 <= V_, view.err)) store_pack<O>(out + c, v);
+  }
+  if (lane < 16) {  // before the first pack and after the last
+    const int c = lane < 8 ? lane : head + packs * 8 + lane - 8;
+    if (c < end && (lane >= 8 || c < head))
+      out[c0 + c] = O::from_f32(live && c0 + c < n ? f.one(E::to_f32(view.p[c - head]), 0) : 0.f);
+  }
+}
+
+// AL: the rows are aligned; GAL: the gradient's packs are (always where dlogits are the logits).
+template <class E, class O, bool AL, bool GAL>
+__global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(const DistillArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ TeacherRow q;
+  __shared__ float zk[RLK_MAX_TOP_K];
+  __shared__ float lse_s;
+  constexpr int EB = sizeof(typename E::bits), OB = sizeof(typename O::bits), SLOT = slot_bytes<E>();
+  const LogitRows& in = a.in;
+  const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int W = (blockDim.x >> 5) - 1;                       // warps that take leaves; one more for the rest
+  const int64_t t = blockIdx.x / C;
+  const int n_leaves = leaves_of(in.n);
+  const int mine = (n_leaves - r + C - 1) / C;               // this CTA's leaves
+  const int rounds = warp < min(W, mine) ? (mine - warp + W - 1) / W : 0;
+  Stats* leaf = reinterpret_cast<Stats*>(dyn);               // of the whole row
+  unsigned char* slots = dyn + n_leaves * sizeof(Stats);
+  if (C > 1) cluster_arrive();
+  const Row<E, AL> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
+  const float g = a.g[t];
+  for (int j = 0; j < rounds; ++j) {
+    copy_leaf(row, r + (warp + j * W) * C, slots + (warp + j * W) * SLOT, lane);
+    cp_async_commit();
+  }
+  if (warp == W) teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, lane);
+  if (C > 1) cluster_wait();  // every CTA has started: its shared memory may be written
+  const uint32_t to = map_to_cta(smem_u32(leaf), lane < C ? lane : 0);
+  for (int j = 0; j < rounds; ++j) {
+    const int i = warp + j * W;
+    cp_async_wait(rounds - 1 - j);
+    __syncwarp();
+    const Row<E, AL> view(reinterpret_cast<const typename E::bits*>(slots + i * SLOT + row.shift), ROW_LEAF + SLOT_SLACK / EB,
+                          in.err_flag);
+    Pack<E> k[LEAF_GROUPS];
+#pragma unroll
+    for (int u = 0; u < LEAF_GROUPS; ++u) k[u] = load_pack(view, u * LEAF_GROUP + lane * 8);
+    leaf_pass<false, false>(k, r + i * C, in.c, RankOf{false, 0, 0.f, 0u, 0u}, to, 0u, lane < C, lane);
+  }
+  if (C > 1) cluster_sync();
+  else __syncthreads();
+  if (warp == 0) {
+    const float lse = row_lse(fold_leaves(leaf, n_leaves, in.c, lane), in.s);
+    if (lane == 0) lse_s = lse;
+  } else {
+    // the student's logits of the entries: CTA 0 takes all of them from the cluster's slots, for the
+    // loss, the others their own, for the gradient
+    for (int k = threadIdx.x - 32; k < a.K; k += blockDim.x - 32) {
+      const int id = q.id[k], l = id / ROW_LEAF;
+      float z = 0.f;
+      if (id >= 0 && (r == 0 || l % C == r)) {
+        const uint32_t at = map_to_cta(smem_u32(slots + (l / C) * SLOT + row.shift + id % ROW_LEAF * EB), l % C);
+        if constexpr (EB == 4) z = E::to_f32(ld_cluster_u32(at));
+        else z = E::to_f32(ld_cluster_u16(at));
+      }
+      zk[k] = z;
+    }
+  }
+  __syncthreads();
+  if (C > 1) cluster_arrive();  // CTA 0 has read the others' slots
+  const float lse = lse_s;
+  if (r == 0 && warp == 0) put_loss(a, t, q, zk, lse, lane);
+  const bool live = distill_live(q, lse, g);
+  const DistillDz f{in.s, lse, __fmul_rn(in.s, g)};
+  auto* out = static_cast<typename O::bits*>(a.out.base) + t * a.out.ld;
+  const int V = a.out.V;
+  const int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / OB;  // of the row and of every leaf
+  for (int j = 0; j < rounds; ++j) {
+    const int i = warp + j * W;
+    const Row<E, GAL> view(reinterpret_cast<const typename E::bits*>(slots + i * SLOT + row.shift) + head,
+                           ROW_LEAF + SLOT_SLACK / EB, in.err_flag);
+    leaf_grad<O>(view, out, (r + i * C) * ROW_LEAF, head, in.n, V, live, f, lane);
+  }
+  // columns past the last leaf
+  for (int c = n_leaves * ROW_LEAF + r * blockDim.x + threadIdx.x; c < V; c += C * blockDim.x) out[c] = O::from_f32(0.f);
+  __syncthreads();
+  if (live) {  // the teacher's columns
+    for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
+      const int id = q.id[k];
+      float dz;
+      if (id >= 0 && id / ROW_LEAF % C == r && entry_dz(q, k, a.K, zk[k], in.s, lse, f.A, &dz)) out[id] = O::from_f32(dz);
+    }
+  }
+  if (C > 1) cluster_wait();
 }
 
 // CTAs of ROW_THREADS per row: one where the rows fill the GPU, else up to MAX_CLUSTER so that few
@@ -711,16 +929,17 @@ int row_cluster(const LogitRows& in) {
   return c;
 }
 
-// Launches `ctas` CTAs of ROW_THREADS in clusters of `cluster`.
+// Launches `ctas` CTAs in clusters of `cluster`.
 template <class K, class A>
-rlk_status launch_rows(K kernel, const A& args, int64_t ctas, int cluster, size_t smem, void* stream) {
+rlk_status launch_rows(K kernel, const A& args, int64_t ctas, int cluster, size_t smem, void* stream,
+                       int threads = ROW_THREADS) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(ROW_THREADS);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
@@ -730,9 +949,16 @@ rlk_status launch_rows(K kernel, const A& args, int64_t ctas, int cluster, size_
 }
 
 // CTAs of a row in a kernel that writes gradients alone.
-int grad_parts(const GradOut& o) {
+// Parts of up to four rounds of every thread's packs (the work that
+// a CTA does once -- its row's scalars, the teacher's softmax -- is then small: 8192 rows of 151936
+// in bf16 take 715 us with four rounds, 954 with one), as long as that leaves CTAs enough for the GPU.
+int grad_parts(const LogitRows& in, const GradOut& o) {
   constexpr int kCols = 8 * GRAD_PACKS * ROW_THREADS;
-  return (o.V + kCols - 1) / kCols;
+  constexpr int64_t kEnough = 6 * 152;
+  const int64_t rounds = (o.V + kCols - 1) / kCols;
+  int64_t each = in.T * rounds / kEnough;
+  each = each < 1 ? 1 : each > 4 ? 4 : each;
+  return static_cast<int>((rounds + each - 1) / each);
 }
 
 // dlogits: the logits' type, or bf16 for fp32 logits
@@ -840,7 +1066,7 @@ rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t T, 
   a.entropy = entropy;
   a.g_logp = g_logp;
   a.g_entropy = g_entropy;
-  a.parts = grad_parts(a.out);
+  a.parts = grad_parts(a.in, a.out);
   if (T * a.parts > INT32_MAX) return RLK_ERR_UNSUPPORTED;
   return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto al) {
     return launch_rows(token_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, T * a.parts, 1, 0, stream);
@@ -864,9 +1090,64 @@ rlk_status check_distill(const void* logits, int32_t dtype, int64_t T, int64_t l
   return RLK_OK;
 }
 
-template <class K>
-rlk_status launch_distill(K kernel, const DistillArgs& a, void* stream) {
-  return launch_rows(kernel, a, static_cast<int64_t>(a.in.T) * a.cluster, a.cluster, row_smem_bytes(a.in.n, false), stream);
+rlk_status launch_distill_fwd(DistillArgs a, int32_t dtype, void* stream) {
+  a.cluster = row_cluster(a.in);
+  return with_types(dtype, aligned_rows(a.in.base, a.in.ld, dtype_bytes(dtype)), [&](auto e, auto al) {
+    return launch_rows(distill_kernel<decltype(e), decltype(al)::value>, a, static_cast<int64_t>(a.in.T) * a.cluster,
+                       a.cluster, row_smem_bytes(a.in.n, false), stream);
+  });
+}
+
+rlk_status launch_distill_bwd(DistillArgs a, int32_t dtype, int32_t out_dtype, void* stream) {
+  a.cluster = grad_parts(a.in, a.out);
+  const int64_t ctas = static_cast<int64_t>(a.in.T) * a.cluster;
+  if (ctas > INT32_MAX) return RLK_ERR_UNSUPPORTED;
+  return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto al) {
+    return launch_rows(distill_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, ctas, 1, 0, stream);
+  });
+}
+
+// The one-launch step: the smallest cluster whose CTAs hold their share of the row in a quarter of
+// an SM's shared memory, or else in a half or the whole. 0: take two launches -- where the row does
+// not fit, or where a cluster of more than two has more than four waves of rows to work through. A
+// cluster's CTAs wait for one another's sums, and what is resident does not cover that wait: 1024
+// rows of 151936 in bf16 (clusters of 8) take 158 us in one launch and 155 in two, 8192 1205 and
+// 1083, but 256 rows 46 and 57; 2048 rows of 50257 (clusters of 2) 112 and 134.
+constexpr size_t kStepSmem = 220 << 10;
+
+size_t step_smem(int n_leaves, int cluster, int slot) {
+  return n_leaves * sizeof(Stats) + static_cast<size_t>((n_leaves + cluster - 1) / cluster) * slot;
+}
+
+int step_cluster(const LogitRows& in, int slot) {
+  const int L = leaves_of(in.n);
+  for (int ctas = STEP_CTAS; ctas >= 1; ctas /= 2)
+    for (int c = 1; c <= MAX_CLUSTER; c *= 2)
+      if (step_smem(L, c, slot) <= kStepSmem / ctas && (L + c - 1) / c <= STEP_MAX_ROUNDS * (STEP_THREADS / 32 - 1))
+        return c <= 2 || static_cast<int64_t>(in.T) * c <= 4 * 152 * ctas ? c : 0;
+  return 0;
+}
+
+template <class E, class O, bool AL, bool GAL>
+rlk_status launch_step(DistillArgs a, void* stream) {
+  const int L = leaves_of(a.in.n);
+  const size_t smem = step_smem(L, a.cluster, slot_bytes<E>());
+  const auto kernel = distill_step_kernel<E, O, AL, GAL>;
+  if (smem > (40 << 10)) {  // the opt-in for more shared memory, once per device
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return RLK_ERR_CUDA;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (!(done.load(std::memory_order_relaxed) & bit)) {
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kStepSmem)) !=
+          cudaSuccess)
+        return RLK_ERR_CUDA;
+      if (dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  const int share = (L + a.cluster - 1) / a.cluster, most = STEP_THREADS / 32 - 1;
+  const int threads = 32 * ((share < most ? share : most) + 1);
+  return launch_rows(kernel, a, static_cast<int64_t>(a.in.T) * a.cluster, a.cluster, smem, stream, threads);
 }
 
 }  // namespace
@@ -884,11 +1165,7 @@ rlk_status rlk_distill_topk_fwd(const void* logits, int32_t dtype, int64_t T, in
   if (T == 0) return RLK_OK;
   a.loss = loss;
   a.lse = lse;
-  a.cluster = row_cluster(a.in);
-  return with_types(dtype, aligned_rows(logits, ld, dtype_bytes(dtype)), [&](auto e, auto al) {
-    using E = decltype(e);
-    return launch_distill(distill_kernel<E, E, false, decltype(al)::value, false>, a, stream);
-  });
+  return launch_distill_fwd(a, dtype, stream);
 }
 
 rlk_status rlk_distill_topk_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
@@ -903,11 +1180,7 @@ rlk_status rlk_distill_topk_bwd(const void* logits, int32_t dtype, int64_t T, in
   if (T == 0) return RLK_OK;
   a.lse_in = lse;
   a.g = g;
-  a.cluster = grad_parts(a.out);
-  if (T * a.cluster > INT32_MAX) return RLK_ERR_UNSUPPORTED;
-  return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto al) {
-    return launch_rows(distill_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, T * a.cluster, 1, 0, stream);
-  });
+  return launch_distill_bwd(a, dtype, out_dtype, stream);
 }
 
 rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
@@ -918,19 +1191,23 @@ rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, int64_t T
   rlk_status st = check_distill(logits, dtype, T, ld, V_true, temperature, ids, teacher, K, err_flag, &a);
   if (st == RLK_OK) st = check_out(a.in, dtype, dlogits, out_dtype, V, out_ld, &a.out);
   if (st != RLK_OK) return st;
-  if (T > 0 && (!g || !loss)) return RLK_ERR_INVALID_ARG;
+  if (T > 0 && (!g || !loss || !lse)) return RLK_ERR_INVALID_ARG;
   if (T == 0) return RLK_OK;
   a.g = g;
   a.loss = loss;
   a.lse = lse;
-  a.cluster = row_cluster(a.in);
+  a.cluster = step_cluster(a.in, dtype_bytes(dtype) == 4 ? slot_bytes<F32>() : slot_bytes<Bf16>());
+  if (a.cluster == 0) {  // the two calls
+    st = launch_distill_fwd(a, dtype, stream);
+    a.lse_in = lse;
+    return st != RLK_OK ? st : launch_distill_bwd(a, dtype, out_dtype, stream);
+  }
   const bool aligned = aligned_rows(logits, ld, dtype_bytes(dtype));
   return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto gal) {
     using E = decltype(e);
     using O = decltype(o);
     constexpr bool GAL = decltype(gal)::value;
-    return launch_distill(aligned && GAL ? distill_kernel<E, O, true, GAL, GAL> : distill_kernel<E, O, true, false, GAL>,
-                          a, stream);
+    return aligned && GAL ? launch_step<E, O, GAL, GAL>(a, stream) : launch_step<E, O, false, GAL>(a, stream);
   });
 }
 

@@ -402,15 +402,15 @@ __device__ __forceinline__ float prob_of(float d) { return ex2_approx(__fmul_rn(
 // ---------------------------------------------------------------------------
 // the teacher's distribution of one row
 // ---------------------------------------------------------------------------
-struct TeacherRow {                // in shared memory, one entry per k < RLK_MAX_TOP_K
+struct alignas(16) TeacherRow {    // in shared memory, one entry per k < RLK_MAX_TOP_K
   int32_t id[RLK_MAX_TOP_K];       // -1: no entry
-  float t[RLK_MAX_TOP_K];          // teacher value; after teacher_softmax: q (0 without an entry)
+  float q[RLK_MAX_TOP_K];          // 0 without an entry
   float logq[RLK_MAX_TOP_K];       // 0 where q is 0
   int32_t any;                     // some entry has q > 0
   int32_t bad;                     // RLK_FLAG_BAD_TARGET / RLK_FLAG_NONFINITE of the row
 };
 
-// q = softmax(s t_k) over the row's entries, by one warp: lane i takes entries i, i + 32, ...
+// q = softmax(s t_k) over the row's K entries, by one warp: lane i takes entries i, i + 32, ...
 __device__ __forceinline__ void teacher_softmax(TeacherRow& r, const int64_t* ids, const float* t, int K, int n,
                                                 float s, float c, int lane) {
   constexpr int R = RLK_MAX_TOP_K / 32;
@@ -446,7 +446,7 @@ __device__ __forceinline__ void teacher_softmax(TeacherRow& r, const int64_t* id
     const int k = lane + 32 * i;
     const bool some = w[i] > 0.f;
     r.id[k] = id[i];
-    r.t[k] = some ? __fdiv_rn(w[i], sum) : 0.f;
+    r.q[k] = some ? __fdiv_rn(w[i], sum) : 0.f;
     r.logq[k] = some ? __fmaf_rn(v[i], s, -ls) : 0.f;
   }
   if (lane == 0) {

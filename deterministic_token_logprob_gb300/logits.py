@@ -278,7 +278,7 @@ def distill_topk_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch
                          stream=None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """rlk_distill_topk_fwd_bwd -> (loss, lse, dlogits): :func:`distill_topk_fwd` and
     :func:`distill_topk_bwd` in one call, for weights g known before the loss (a token mask over
-    a count). The same bits; the logits are read from memory once."""
+    a count). The same bits; most often the logits are read once."""
     T, V, ld, code = _rows(logits, "logits")
     dev = logits.device
     if _away(stream, dev):

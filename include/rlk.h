@@ -448,7 +448,8 @@ RLK_API rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int
  *            marks missing alternatives); an id may come twice, then both count
  *   teacher  device fp32 [T][K]; -inf: probability 0
  *   g        device fp32 [T]
- *   loss, lse  device fp32 [T]; lse (of the student's logits) feeds the backward, may be NULL
+ *   loss, lse  device fp32 [T]; lse (of the student's logits) feeds the backward; in
+ *            rlk_distill_topk_fwd it may be NULL
  * A row without entries (or with all teacher values -inf) has loss 0 and a zero gradient. A row
  * with an id outside [-1, V_true) (RLK_FLAG_BAD_TARGET) or a teacher value of NaN or +inf
  * (RLK_FLAG_NONFINITE) has loss NaN and a zero gradient. Where the student's logit of an entry
@@ -456,8 +457,8 @@ RLK_API rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int
  * rlk_token_logprobs_bwd, with rows of g = 0 zero.
  *
  * rlk_distill_topk_fwd_bwd gives both at once, for weights g that are known before the loss (a
- * token mask over a count): the same bits as the two calls, and the logits are read from memory
- * once (their second reading is meant to hit in L2).
+ * token mask over a count): the same bits as the two calls, and where a row fits the shared memory
+ * of one or two SMs, or the rows are few, the logits are read once.
  */
 RLK_API rlk_status rlk_distill_topk_fwd(const void* logits, int32_t dtype, int64_t T, int64_t ld,
                                         int64_t V_true, double temperature, const int64_t* ids,
