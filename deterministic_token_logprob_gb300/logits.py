@@ -44,18 +44,27 @@ class TokenLogprobs(NamedTuple):
     top_logp: Optional[torch.Tensor]
 
 
-def _rows(t: torch.Tensor, name: str) -> Tuple[int, int, int, int]:
-    """Checks a [T, V] tensor with contiguous rows; (T, V, row distance, dtype code)."""
+# The current device and stream without building torch objects: a small call (one token, or a small
+# model's step) is bounded by its work on the host.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _rows(t: torch.Tensor, name: str) -> Tuple[int, int, int, int, int]:
+    """Checks a [T, V] CUDA tensor with contiguous rows; (T, V, row distance, dtype code, device index)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError(f"{name} must be a CUDA tensor")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be one of {[str(d) for d in _DTYPES]}, got {t.dtype}")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims, got {tuple(t.shape)}")
-    T, V = t.shape
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name} must have 2 dims, got {tuple(shape)}")
+    T, V = shape
     ld, inner = t.stride()
     if inner != 1 and V > 1:
         raise ValueError(f"{name} must have contiguous rows (stride(1) == 1)")
@@ -63,37 +72,31 @@ def _rows(t: torch.Tensor, name: str) -> Tuple[int, int, int, int]:
         if T > 1:
             raise ValueError(f"{name} must not have overlapping rows")
         ld = V  # the stride of a single row says nothing
-    return T, V, ld, code
+    return T, V, ld, code, dev
 
 
-def _per_row(t, name: str, dtype, shape, device) -> int:
-    """The address of a contiguous tensor of this dtype, shape and device."""
+def _per_row(t, name: str, dtype, shape, dev: int) -> int:
+    """The address of a contiguous tensor of this dtype, shape and device index."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t.data_ptr()
 
 
-def _flag(err_flag, device):
-    return None if err_flag is None else _per_row(err_flag, "err_flag", torch.int32, (1,), device)
+def _flag(err_flag, dev):
+    return None if err_flag is None else _per_row(err_flag, "err_flag", torch.int32, (1,), dev)
 
 
-# The current stream's handle without building a torch.cuda.Stream: a small call (one token, or a
-# small model's step) is bounded by its work on the host.
-_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _away(stream, device) -> bool:
+def _away(stream, dev) -> bool:
     """Whether a call has to change the current stream or device first (see _elsewhere)."""
-    return stream is not None or device.index != torch.cuda.current_device()
+    return stream is not None or dev != _current_device()
 
 
 @contextlib.contextmanager
@@ -127,8 +130,7 @@ def token_logprobs(logits: torch.Tensor, y: Optional[torch.Tensor] = None, *, to
 
     `out` supplies the six output tensors in the order of :class:`TokenLogprobs` (a serving loop
     keeps them between steps); None in a place leaves that output out."""
-    T, V, ld, code = _rows(logits, "logits")
-    dev = logits.device
+    T, V, ld, code, dev = _rows(logits, "logits")
     if _away(stream, dev):
         with _elsewhere(stream, dev, (logits, y, err_flag, *(out or ()))):
             return token_logprobs(logits, y, top_k=top_k, V_true=V_true, temperature=temperature, out=out,
@@ -139,11 +141,12 @@ def token_logprobs(logits: torch.Tensor, y: Optional[torch.Tensor] = None, *, to
     rows, i32, i64, f32 = (T,), torch.int32, torch.int64, torch.float32
     py = None if y is None else _per_row(y, "y", i64, rows, dev)
     if out is None:
-        r = TokenLogprobs(None if y is None else torch.empty(rows, dtype=f32, device=dev),
-                          None if y is None else torch.empty(rows, dtype=i32, device=dev),
-                          torch.empty(rows, dtype=f32, device=dev), torch.empty(rows, dtype=f32, device=dev),
-                          torch.empty((T, top_k), dtype=i64, device=dev) if top_k else None,
-                          torch.empty((T, top_k), dtype=f32, device=dev) if top_k else None)
+        on = logits.device
+        r = TokenLogprobs(None if y is None else torch.empty(T, dtype=f32, device=on),
+                          None if y is None else torch.empty(T, dtype=i32, device=on),
+                          torch.empty(T, dtype=f32, device=on), torch.empty(T, dtype=f32, device=on),
+                          torch.empty((T, top_k), dtype=i64, device=on) if top_k else None,
+                          torch.empty((T, top_k), dtype=f32, device=on) if top_k else None)
     elif len(out) != 6:
         raise ValueError("out must hold six tensors (or None): logp, rank, lse, entropy, top_ids, top_logp")
     else:
@@ -157,7 +160,7 @@ def token_logprobs(logits: torch.Tensor, y: Optional[torch.Tensor] = None, *, to
         None if entropy is None else _per_row(entropy, "entropy", f32, rows, dev),
         None if ids is None else _per_row(ids, "top_ids", i64, (T, top_k), dev),
         None if top is None else _per_row(top, "top_logp", f32, (T, top_k), dev),
-        _flag(err_flag, dev), _raw_stream(dev.index))
+        _flag(err_flag, dev), _raw_stream(dev))
     if st:
         _check("rlk_token_logprobs", st)
     return r
@@ -173,12 +176,12 @@ def _gradient(logits, T, V, out, out_dtype):
             raise TypeError(f"out_dtype must be one of {[str(d) for d in _DTYPES]}, got {dtype}")
         d = torch.empty((T, V), dtype=dtype, device=logits.device)
         return d, (d.data_ptr(), code, V, max(V, 1))
-    oT, oV, old, code = _rows(out, "out")
+    oT, oV, old, code, dev = _rows(out, "out")
     if oT != T or oV < V:
         raise ValueError(f"out must have {T} rows of at least {V} columns, got {tuple(out.shape)}")
     if out_dtype is not None and out.dtype != out_dtype:
         raise TypeError(f"out must be {out_dtype}, got {out.dtype}")
-    if out.device != logits.device:
+    if dev != logits.get_device():
         raise ValueError(f"out must be on {logits.device}, got {out.device}")
     return out, (out.data_ptr(), code, oV, old)
 
@@ -192,8 +195,7 @@ def token_logprobs_bwd(logits: torch.Tensor, y: torch.Tensor, lse: torch.Tensor,
     """rlk_token_logprobs_bwd -> dlogits of sum_t (g_logp logp + g_entropy entropy), from the
     forward's lse and entropy. The result has the logits' shape and type (or out_dtype: bfloat16
     for float32 logits); `out` supplies it, the logits themselves included."""
-    T, V, ld, code = _rows(logits, "logits")
-    dev = logits.device
+    T, V, ld, code, dev = _rows(logits, "logits")
     if _away(stream, dev):
         with _elsewhere(stream, dev, (logits, y, lse, entropy, g_logp, g_entropy, out, err_flag)):
             return token_logprobs_bwd(logits, y, lse, entropy, g_logp, g_entropy, V_true=V_true,
@@ -208,16 +210,17 @@ def token_logprobs_bwd(logits: torch.Tensor, y: torch.Tensor, lse: torch.Tensor,
     V_true = _true_vocab(V_true, V)
     dlogits, d = _gradient(logits, T, V, out, out_dtype)
     st = _load().rlk_token_logprobs_bwd(logits.data_ptr(), code, T, ld, V_true, temperature, *p, *d,
-                                        _flag(err_flag, dev), _raw_stream(dev.index))
+                                        _flag(err_flag, dev), _raw_stream(dev))
     if st:
         _check("rlk_token_logprobs_bwd", st)
     return dlogits
 
 
 def _teacher(ids, teacher, T, dev):
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+    shape = ids.shape if isinstance(ids, torch.Tensor) else ()
+    if len(shape) != 2:
         raise ValueError("ids must be an int64 [T, K] tensor")
-    K = ids.shape[1]
+    K = shape[1]
     if not 1 <= K <= MAX_TOP_K:
         raise ValueError(f"K must be in 1 .. {MAX_TOP_K}, got {K}")
     return (_per_row(ids, "ids", torch.int64, (T, K), dev), _per_row(teacher, "teacher", torch.float32, (T, K), dev), K)
@@ -230,17 +233,16 @@ def distill_topk_fwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Ten
     """rlk_distill_topk_fwd -> (loss, lse), fp32 [T] each: the KL divergence from the softmax of
     the teacher's top logits (fp32 [T, K], at columns ids int64 [T, K], -1: none) to
     softmax(logits / temperature), and the student's lse for the backward."""
-    T, V, ld, code = _rows(logits, "logits")
-    dev = logits.device
+    T, V, ld, code, dev = _rows(logits, "logits")
     if _away(stream, dev):
         with _elsewhere(stream, dev, (logits, ids, teacher, err_flag)):
             return distill_topk_fwd(logits, ids, teacher, V_true=V_true, temperature=temperature, err_flag=err_flag)
     p = _teacher(ids, teacher, T, dev)
     V_true = _true_vocab(V_true, V)
-    loss = torch.empty(T, dtype=torch.float32, device=dev)
-    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    loss = torch.empty(T, dtype=torch.float32, device=logits.device)
+    lse = torch.empty(T, dtype=torch.float32, device=logits.device)
     st = _load().rlk_distill_topk_fwd(logits.data_ptr(), code, T, ld, V_true, temperature, *p, loss.data_ptr(),
-                                      lse.data_ptr(), _flag(err_flag, dev), _raw_stream(dev.index))
+                                      lse.data_ptr(), _flag(err_flag, dev), _raw_stream(dev))
     if st:
         _check("rlk_distill_topk_fwd", st)
     return loss, lse
@@ -253,8 +255,7 @@ def distill_topk_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Ten
                      err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rlk_distill_topk_bwd -> dlogits of sum_t g[t] loss[t], from the forward's lse. Shape, type
     and `out` as in :func:`token_logprobs_bwd`."""
-    T, V, ld, code = _rows(logits, "logits")
-    dev = logits.device
+    T, V, ld, code, dev = _rows(logits, "logits")
     if _away(stream, dev):
         with _elsewhere(stream, dev, (logits, ids, teacher, lse, g, out, err_flag)):
             return distill_topk_bwd(logits, ids, teacher, lse, g, V_true=V_true, temperature=temperature, out=out,
@@ -265,7 +266,7 @@ def distill_topk_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Ten
     V_true = _true_vocab(V_true, V)
     dlogits, d = _gradient(logits, T, V, out, out_dtype)
     st = _load().rlk_distill_topk_bwd(logits.data_ptr(), code, T, ld, V_true, temperature, *p, lse_p, g_p, *d,
-                                      _flag(err_flag, dev), _raw_stream(dev.index))
+                                      _flag(err_flag, dev), _raw_stream(dev))
     if st:
         _check("rlk_distill_topk_bwd", st)
     return dlogits
@@ -279,8 +280,7 @@ def distill_topk_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch
     """rlk_distill_topk_fwd_bwd -> (loss, lse, dlogits): :func:`distill_topk_fwd` and
     :func:`distill_topk_bwd` in one call, for weights g known before the loss (a token mask over
     a count). The same bits; most often the logits are read once."""
-    T, V, ld, code = _rows(logits, "logits")
-    dev = logits.device
+    T, V, ld, code, dev = _rows(logits, "logits")
     if _away(stream, dev):
         with _elsewhere(stream, dev, (logits, ids, teacher, g, out, err_flag)):
             return distill_topk_fwd_bwd(logits, ids, teacher, g, V_true=V_true, temperature=temperature, out=out,
@@ -288,12 +288,12 @@ def distill_topk_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch
     p = _teacher(ids, teacher, T, dev)
     g_p = _per_row(g, "g", torch.float32, (T,), dev)
     V_true = _true_vocab(V_true, V)
-    loss = torch.empty(T, dtype=torch.float32, device=dev)
-    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    loss = torch.empty(T, dtype=torch.float32, device=g.device)
+    lse = torch.empty(T, dtype=torch.float32, device=g.device)
     dlogits, d = _gradient(logits, T, V, out, out_dtype)
     st = _load().rlk_distill_topk_fwd_bwd(logits.data_ptr(), code, T, ld, V_true, temperature, *p, g_p,
                                           loss.data_ptr(), lse.data_ptr(), *d, _flag(err_flag, dev),
-                                          _raw_stream(dev.index))
+                                          _raw_stream(dev))
     if st:
         _check("rlk_distill_topk_fwd_bwd", st)
     return loss, lse, dlogits
