@@ -13,7 +13,8 @@ namespace {
 
 constexpr int ROW_THREADS = 256;
 constexpr int MAX_CLUSTER = 8;                               // CTAs of one row (the portable cluster size)
-constexpr int MAX_ROW_WARPS = MAX_CLUSTER * 32;
+constexpr int MAX_ROW_THREADS = 1024;
+constexpr int MAX_ROW_WARPS = MAX_CLUSTER * MAX_ROW_THREADS / 32;
 constexpr int GROUPS_PER_LEAF = LEAF_GROUPS;                 // 256-column groups, the units of the alternatives' search
 constexpr int GRAD_PACKS = 4;                                // packs a thread has in flight in the gradients
 constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates: 8 columns of each chosen octet
@@ -27,18 +28,34 @@ constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates:
 // the target.
 struct RowSmem {
   Stats* leaf;      // [n_leaves]
-  float* group;     // [round_up(4 n_leaves, 128)]; then their order keys
+  float* group;     // [keys_of(n)]
   int* count;       // [MAX_ROW_WARPS]
 };
 
 __host__ __device__ constexpr int leaves_of(int n) { return (n + ROW_LEAF - 1) / ROW_LEAF; }
 __host__ __device__ constexpr int keys_of(int n) { return (leaves_of(n) * GROUPS_PER_LEAF + 127) / 128 * 128; }
 
-struct RankOf {     // the target of the row, when its rank is wanted
-  bool on;
-  int y;
-  float z;
-  uint32_t ge, gt;  // its logit and the next value above it, in both halves of a word for 16-bit types
+// The target of a row.
+struct RankOf {
+  bool ok = false;       // it is a column
+  bool on = false;       // and its rank is wanted
+  int y = 0;
+  float z = 0.f;
+  uint32_t ge = 0, gt = 0;  // its logit and the next value above it, in both halves of a word for 16-bit types
+  template <class R>
+  __device__ __forceinline__ void load(const R& row, const int64_t* y_ptr, bool wanted) {
+    using E = typename R::E;
+    const int64_t v = y_ptr ? *y_ptr : -1;
+    ok = v >= 0 && v < row.n;
+    on = ok && wanted;
+    if (!ok) return;
+    y = static_cast<int>(v);
+    const typename E::bits b = row.p[v];
+    z = E::to_f32(b);
+    ge = b;
+    gt = next_above<E>(b);
+    if constexpr (sizeof(b) == 2) ge *= 0x10001u, gt *= 0x10001u;
+  }
 };
 
 __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
@@ -108,34 +125,23 @@ __device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l,
   return rank.on && m >= rank.z ? count_ahead(k, rank, l, lane) : 0;
 }
 
-template <bool ENT, bool TOP, class R, class E = typename R::E>
-__device__ __forceinline__ void row_pass(const R& row, float c, const RankOf& rank, const RowSmem& sm, int C, int r) {
+// `begin` runs in every thread after the first loads have been issued: what it loads arrives with them.
+template <bool ENT, bool TOP, class R, class B, class E = typename R::E>
+__device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, const RowSmem& sm, int C, int r, B begin) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5, g = r * warps + warp, n_leaves = leaves_of(row.n), step = C * warps;
   if (C > 1) cluster_arrive();  // CTA 0 must have started before anyone writes to it
-  bool waited = C == 1;
   const uint32_t leaf0 = map_to_cta(smem_u32(sm.leaf), 0);
   const uint32_t group0 = TOP ? map_to_cta(smem_u32(sm.group), 0) : 0;
   int count = 0;
-  if constexpr (ENT || sizeof(typename E::bits) == 4) {
-    // 64 registers leave no room for a second leaf; the other warps hide the loads
-    for (int l = g; l < n_leaves; l += step) {
-      Pack<E> k[LEAF_GROUPS];
-      load_leaf(row, l, lane, k);
-      if (!waited) {
-        cluster_wait();
-        waited = true;
-      }
-      count += leaf_pass<ENT, TOP>(k, l, c, rank, leaf0, group0, lane == 0, lane);
-    }
-  } else if (g < n_leaves) {
-    // the next leaf is loaded before this one is summed (8192 rows of 151936 in bf16: 378 -> 354 us)
-    Pack<E> k[2][LEAF_GROUPS];
-    load_leaf(row, g, lane, k[0]);
-    if (!waited) {
-      cluster_wait();
-      waited = true;
-    }
+  // 64 registers have room for the next leaf's packs in the lean pass over 16-bit types alone (8192
+  // rows of 151936 in bf16: 378 -> 354 us); elsewhere the other warps hide the loads
+  constexpr bool AHEAD = !ENT && sizeof(typename E::bits) == 2;
+  Pack<E> k[AHEAD ? 2 : 1][LEAF_GROUPS];
+  if (g < n_leaves) load_leaf(row, g, lane, k[0]);
+  begin();
+  if (C > 1) cluster_wait();
+  if constexpr (AHEAD) {
     for (int l = g; l < n_leaves; l += 2 * step) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
@@ -145,8 +151,13 @@ __device__ __forceinline__ void row_pass(const R& row, float c, const RankOf& ra
         leaf_pass<ENT, TOP>(k[u], i, c, rank, leaf0, group0, lane == 0, lane);
       }
     }
+  } else {
+    for (int l = g; l < n_leaves;) {
+      count += leaf_pass<ENT, TOP>(k[0], l, c, rank, leaf0, group0, lane == 0, lane);
+      l += step;
+      if (l < n_leaves) load_leaf(row, l, lane, k[0]);
+    }
   }
-  if (!waited) cluster_wait();
   if (rank.on) {
     count = __reduce_add_sync(kFullWarp, count);
     if (lane == 0) st_cluster_u32(map_to_cta(smem_u32(sm.count + g), 0), static_cast<uint32_t>(count));
@@ -156,63 +167,82 @@ __device__ __forceinline__ void row_pass(const R& row, float c, const RankOf& ra
 }
 
 // ---------------------------------------------------------------------------
-// the best of N keys, by one warp
+// the best of N values, by one warp
 // ---------------------------------------------------------------------------
-// Chooses between k and `most` places of key[0 .. N) (all of them when N <= k) that hold its k best --
-// the largest keys, the lower place first among equals -- writes them to `place` in ascending order,
-// and the key >> shift that all of them reach to *bar. N is padded with zero keys to a multiple of
-// 128; the keys hold nothing in their low `shift` bits. A first bar that k places reach is the k-th
-// of the 32 lanes' maxima (k <= 32); where more than `most` reach it, bisection on the key raises
-// it, counting the keys at or above the middle, and ties that no bar can part are cut by place.
-__device__ __forceinline__ int choose_best(const uint32_t* key, int N, int k, int most, int shift, int* place,
-                                           uint32_t* bar, int lane) {
+// The value of the type whose order key >> shift is `bar` (its low bits are 0 in the fp32 image, so
+// 1 in the key of a negative value); the lowest finite value for -inf and below.
+__device__ __forceinline__ float bar_value(uint32_t bar, int shift) {
+  uint32_t key = bar << shift;
+  if (!(key & 0x80000000u)) key |= (1u << shift) - 1u;
+  return key <= order_key(neg_inf()) ? -3.4028235e38f : key_value(key);
+}
+
+// A bar that the k best of v[0 .. N) reach and at most `most` of them, -inf never (all that are not
+// -inf reach the lowest finite value, the bar for N <= k). v is padded with -inf to a multiple of 128.
+// The first try is the k-th of the 32 lanes' maxima (k <= 32); where more than `most` reach it,
+// bisection raises it on the values' order keys, which hold nothing in their low `shift` bits,
+// counting the values at or above the middle. *ties: how many of those equal to the bar are to be
+// taken, lower places first -- all of them, unless ties stand in the way of any such bar.
+__device__ __forceinline__ float choose_bar(const float* v, int N, int k, int most, int shift, int* ties, int lane) {
+  *ties = N;
+  if (N <= k) return -3.4028235e38f;
   const int padded = (N + 127) / 128 * 128;
-  const auto count_from = [&](uint32_t b) {
+  const auto reach = [&](float bar) {
     int n = 0;
     for (int i = lane * 4; i < padded; i += 128) {
-      const uint4 v = *reinterpret_cast<const uint4*>(key + i);
-      n += (v.x >> shift >= b) + (v.y >> shift >= b) + (v.z >> shift >= b) + (v.w >> shift >= b);
+      const float4 x = *reinterpret_cast<const float4*>(v + i);
+      n += (x.x >= bar) + (x.y >= bar) + (x.z >= bar) + (x.w >= bar);
     }
     return __reduce_add_sync(kFullWarp, n);
   };
+  float top = neg_inf();
+  for (int i = lane * 4; i < padded; i += 128) {
+    const float4 x = *reinterpret_cast<const float4*>(v + i);
+    top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+  }
   uint32_t lo = 0;
-  int n = N, ties = N;  // places that reach lo; places at lo that are taken
-  if (N > k) {
-    uint32_t top = 0;
-    for (int i = lane; i < N; i += 32) top = max(top, key[i] >> shift);
-    uint32_t hi = __reduce_max_sync(kFullWarp, top) + 1;  // fewer than k reach it
-    if (k <= 32 && N >= 32) {
-      int before = 0;
+  float bar = -3.4028235e38f;
+  if (k <= 32) {
+    int before = 0;
 #pragma unroll
-      for (int j = 0; j < 32; ++j) {
-        const uint32_t other = __shfl_sync(kFullWarp, top, j);
-        before += other > top || (other == top && j < lane);
-      }
-      lo = __shfl_sync(kFullWarp, top, __ffs(__ballot_sync(kFullWarp, before == k - 1)) - 1);
-      n = count_from(lo);
+    for (int j = 0; j < 32; ++j) {
+      const float other = __shfl_sync(kFullWarp, top, j);
+      before += other > top || (other == top && j < lane);
     }
-    while (n > most && hi - lo > 1) {
+    const uint32_t at = __ballot_sync(kFullWarp, before == k - 1);
+    lo = order_key(__shfl_sync(kFullWarp, top, at ? __ffs(at) - 1 : 0)) >> shift;  // (no such lane: a NaN)
+    bar = bar_value(lo, shift);
+  }
+  int n = reach(bar);
+  if (n > most) {
+    uint32_t hi = (__reduce_max_sync(kFullWarp, order_key(top)) >> shift) + 1;  // fewer than k reach it
+    while (n > most && hi > lo + 1) {
       const uint32_t mid = lo + (hi - lo) / 2;
-      const int m = count_from(mid);
+      const int m = reach(bar_value(mid, shift));
       if (m >= k) lo = mid, n = m;
       else hi = mid;
     }
-    if (n > most) ties = k - count_from(lo + 1);
+    bar = bar_value(lo, shift);
+    if (n > most) *ties = k - reach(bar_value(lo + 1, shift));
   }
+  return bar;
+}
+
+// The places that choose_bar chose, in ascending order; how many there are (at most `most`).
+__device__ __forceinline__ int take_places(const float* v, int N, float bar, int ties, int* place, int most, int lane) {
   int out = 0;
+  const uint32_t below = (1u << lane) - 1u;
   for (int i0 = 0; i0 < N; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t v = i < N ? key[i] >> shift : 0u;
-    const uint32_t below = (1u << lane) - 1u;
-    const uint32_t eq = __ballot_sync(kFullWarp, i < N && v == lo);
-    const bool take = i < N && (v > lo || (v == lo && __popc(eq & below) < ties));
+    const float x = i0 + lane < N ? v[i0 + lane] : neg_inf();
+    const uint32_t eq = __ballot_sync(kFullWarp, x == bar);
+    const bool take = x > bar || (x == bar && __popc(eq & below) < ties);
     const uint32_t taken = __ballot_sync(kFullWarp, take);
-    if (take) place[out + __popc(taken & below)] = i;
+    const int at = out + __popc(taken & below);
+    if (take && at < most) place[at] = i0 + lane;
     out += __popc(taken);
     ties -= min(ties, __popc(eq));
   }
-  *bar = lo;
-  return out;
+  return min(out, most);
 }
 
 struct ScoreArgs {
@@ -234,13 +264,12 @@ struct TopSmem {
   unsigned long long cand[CAND];   // order key in the high word, ~column in the low one
   int place[RLK_MAX_TOP_K];        // chosen groups
   int octet[RLK_MAX_TOP_K];        // chosen octets
-  int n_place, n_octet, n_cand;
-  uint32_t bar;                    // key >> kKeyShift that the chosen reach
-  float lse;
+  int n_place, n_octet, n_cand, ties;
+  float bar, lse;
 };
 
-// Dynamic shared memory of a row: the octets' keys take the place of the leaves' statistics and the
-// groups' keys, which have been used by then.
+// Dynamic shared memory of a row: the octets' maxima take the place of the leaves' statistics and the
+// groups' maxima, which have been used by then.
 __host__ __device__ constexpr size_t row_smem_bytes(int n, bool top) {
   size_t b = leaves_of(n) * sizeof(Stats);
   if (!top) return b;
@@ -251,14 +280,8 @@ __host__ __device__ constexpr size_t row_smem_bytes(int n, bool top) {
 
 __device__ __forceinline__ int chosen_most(int k) { return min(RLK_MAX_TOP_K, 2 * k + 16); }
 
-// The smallest finite value whose order key >> shift reaches `bar`.
-__device__ __forceinline__ float bar_value(uint32_t bar, int shift) {
-  const uint32_t key = bar << shift;
-  return key <= order_key(neg_inf()) ? -3.4028235e38f : key_value(key);
-}
-
-// Adds the columns of a pack (its first column c) that reach the value `bar` to the candidates,
-// `most` of them at the most; n_cand counts them all. Few lanes have any.
+// Adds the columns of a pack (its first column c) that reach `bar` to the candidates, `most` of them
+// at the most; n_cand counts them all. Few lanes have any.
 template <class E>
 __device__ __forceinline__ void offer(const Pack<E>& k, int c, float bar, int most, TopSmem& ts) {
   if (!(pack_max(k) >= bar)) return;
@@ -273,10 +296,11 @@ __device__ __forceinline__ void offer(const Pack<E>& k, int c, float bar, int mo
   }
 }
 
-// The top_k alternatives of a row, by one CTA, from its groups' keys.
+// The top_k alternatives of a row, by one CTA, from its groups' maxima and the bar that choose_bar
+// found for them.
 //  1. The k groups of 256 columns with the largest maxima (lower group first among equals) hold
-//     the k best columns: a column outside them has k group maxima ahead of it. choose_best gives
-//     them and a few more, and a bar that k columns reach.
+//     the k best columns: a column outside them has k group maxima ahead of it. Chosen are they and
+//     a few more that reach the bar, which k columns reach.
 //  2. Their columns that reach the bar are the candidates: little more than k, unless good columns
 //     crowd into few groups or are tied.
 //  3. If they are too many, the same choice among the chosen groups' octets (8 columns) leaves
@@ -286,13 +310,22 @@ template <class R, class E = typename R::E>
 __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowSmem& sm, TopSmem& ts,
                          bool bad, float lse) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int K = a.top_k, chosen = bad ? 0 : ts.n_place;
+  const int K = a.top_k, groups = (row.n + LEAF_GROUP - 1) / LEAF_GROUP, most = chosen_most(K);
+  const float bar = ts.bar;
   const auto pack_of = [&](int c) {
     return packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c);
   };
-  const float bar = bar_value(ts.bar, E::kKeyShift);
-  bool many = !bad && ts.bar == 0 && row.n > FEW;  // every column reaches the bar
-  if (!many) {
+  // the chosen groups: in any order for step 2, in ascending order for step 3
+  const bool tied = ts.ties < groups;
+  bool many = !bad && (tied || (groups <= K && row.n > FEW));
+  if (!many && !bad) {
+    for (int i = threadIdx.x; i < groups; i += blockDim.x)
+      if (sm.group[i] >= bar) {
+        const int at = atomicAdd(&ts.n_place, 1);
+        if (at < most) ts.place[at] = i;
+      }
+    __syncthreads();
+    const int chosen = ts.n_place;
     for (int i0 = warp; i0 < chosen; i0 += 4 * warps) {
       Pack<E> k[4];
       int c[4];
@@ -310,21 +343,27 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowS
     many = ts.n_cand > FEW;
   }
   if (many) {  // the same for the whole CTA
-    uint32_t* okey = reinterpret_cast<uint32_t*>(sm.leaf);
-    const int N = chosen * 32;
+    if (warp == 0) {
+      const int m = take_places(sm.group, groups, bar, ts.ties, ts.place, RLK_MAX_TOP_K, lane);
+      if (lane == 0) ts.n_place = m;
+    }
+    __syncthreads();
+    float* omax = reinterpret_cast<float*>(sm.leaf);
+    const int chosen = ts.n_place, N = chosen * 32;
     for (int i = warp; i < chosen; i += warps)
-      okey[i * 32 + lane] = order_key(pack_max(pack_of(ts.place[i] * LEAF_GROUP + lane * 8)));
-    for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) okey[i] = 0u;
+      omax[i * 32 + lane] = pack_max(pack_of(ts.place[i] * LEAF_GROUP + lane * 8));
+    for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) omax[i] = neg_inf();
     __syncthreads();
     if (warp == 0) {
-      uint32_t b;
-      const int m = choose_best(okey, N, K, chosen_most(K), E::kKeyShift, ts.octet, &b, lane);
+      int ties;
+      const float b = choose_bar(omax, N, K, most, E::kKeyShift, &ties, lane);
+      const int m = take_places(omax, N, b, ties, ts.octet, RLK_MAX_TOP_K, lane);
       if (lane == 0) ts.bar = b, ts.n_octet = m, ts.n_cand = 0;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < ts.n_octet; i += blockDim.x) {
       const int c = ts.place[ts.octet[i] / 32] * LEAF_GROUP + ts.octet[i] % 32 * 8;
-      offer(pack_of(c), c, bar_value(ts.bar, E::kKeyShift), CAND, ts);
+      offer(pack_of(c), c, ts.bar, CAND, ts);
     }
     __syncthreads();
   }
@@ -347,8 +386,9 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowS
   }
 }
 
+// 64 registers a thread, whatever the number of threads: 1024 of them fill an SM.
 template <class E, bool TOP, bool AL>
-__global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const ScoreArgs a) {
+__global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(const ScoreArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ int counts[MAX_ROW_WARPS];
   __shared__ __align__(16) unsigned char top_raw[TOP ? sizeof(TopSmem) : 16];
@@ -357,29 +397,14 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const Sc
   const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x / C;
   const Row<E, AL> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
-  RowSmem sm;
-  sm.leaf = reinterpret_cast<Stats*>(dyn);
-  sm.group = reinterpret_cast<float*>(sm.leaf + leaves_of(in.n));
-  sm.count = counts;
-  const int64_t y = a.y ? a.y[t] : -1;
-  const bool y_ok = y >= 0 && y < in.n;
-  RankOf rank{a.rank != nullptr && y_ok, static_cast<int>(y), 0.f, 0u, 0u};
-  if (y_ok) {
-    const typename E::bits b = row.p[y];
-    rank.z = E::to_f32(b);
-    rank.ge = b;
-    rank.gt = next_above<E>(b);
-    if constexpr (Pack<E>::EB == 2) rank.ge *= 0x10001u, rank.gt *= 0x10001u;
+  const RowSmem sm{reinterpret_cast<Stats*>(dyn), reinterpret_cast<float*>(dyn + leaves_of(in.n) * sizeof(Stats)), counts};
+  if (TOP && r == 0) {
+    if (threadIdx.x == 0) ts.n_cand = ts.n_place = 0;
+    for (int i = leaves_of(in.n) * GROUPS_PER_LEAF + threadIdx.x; i < keys_of(in.n); i += blockDim.x) sm.group[i] = neg_inf();
   }
-  if (TOP && threadIdx.x == 0) ts.n_cand = 0;
-  row_pass<true, TOP>(row, in.c, rank, sm, C, r);
+  RankOf rank;
+  row_pass<true, TOP>(row, in.c, rank, sm, C, r, [&] { rank.load(row, a.y ? a.y + t : nullptr, a.rank != nullptr); });
   if (r != 0) return;
-  const int groups = (in.n + LEAF_GROUP - 1) / LEAF_GROUP;
-  uint32_t* key = reinterpret_cast<uint32_t*>(sm.group);
-  if constexpr (TOP) {  // maxima to keys; places past the last group get key 0: never chosen
-    for (int i = threadIdx.x; i < keys_of(in.n); i += blockDim.x) key[i] = i < groups ? order_key(sm.group[i]) : 0u;
-    __syncthreads();
-  }
   if (warp == (blockDim.x > 32)) {
     const Stats x = fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane);
     const float lse = row_lse(x, in.s);
@@ -392,17 +417,18 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) token_logprobs_kernel(const Sc
       if (TOP) ts.lse = lse;
       if (a.lse) a.lse[t] = lse;
       if (a.entropy) a.entropy[t] = row_entropy(x, in.s);
-      if (a.logp) a.logp[t] = y_ok && !bad ? token_logp(rank.z, in.s, lse) : quiet_nan();
-      if (a.rank) a.rank[t] = y_ok && !bad ? 1 + before : 0;
+      if (a.logp) a.logp[t] = rank.ok && !bad ? token_logp(rank.z, in.s, lse) : quiet_nan();
+      if (a.rank) a.rank[t] = rank.ok && !bad ? 1 + before : 0;
       if (in.err_flag && bad) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
-      if (in.err_flag && a.y && !y_ok) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
+      if (in.err_flag && a.y && !rank.ok) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
     }
   }
   if constexpr (TOP) {
     if (warp == 0) {
-      uint32_t b;
-      const int m = choose_best(key, groups, a.top_k, chosen_most(a.top_k), E::kKeyShift, ts.place, &b, lane);
-      if (lane == 0) ts.bar = b, ts.n_place = m;
+      int ties;
+      const float b = choose_bar(sm.group, (in.n + LEAF_GROUP - 1) / LEAF_GROUP, a.top_k, chosen_most(a.top_k),
+                                 E::kKeyShift, &ties, lane);
+      if (lane == 0) ts.bar = b, ts.ties = ties;
     }
     __syncthreads();
     find_top(row, a, t, sm, ts, isnan(ts.lse), ts.lse);
@@ -712,7 +738,7 @@ __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const Distill
 
 // Forward: a cluster of CTAs a row.
 template <class E, bool AL>
-__global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillArgs a) {
+__global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ TeacherRow q;
   __shared__ float zk[RLK_MAX_TOP_K];
@@ -720,12 +746,14 @@ __global__ void __launch_bounds__(ROW_THREADS, 4) distill_kernel(const DistillAr
   const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t t = blockIdx.x / C;
   const Row<E, AL> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
-  if (r == 0 && warp == static_cast<int>(blockDim.x >> 5) - 1) {
+  const bool reads = r == 0 && warp == static_cast<int>(blockDim.x >> 5) - 1;
+  if (reads) {
     teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, lane);
     gather_logits(q, row, zk, lane);
   }
   RowSmem sm{reinterpret_cast<Stats*>(dyn), nullptr, nullptr};
-  row_pass<false, false>(row, in.c, RankOf{false, 0, 0.f, 0u, 0u}, sm, C, r);
+  RankOf none;
+  row_pass<false, false>(row, in.c, none, sm, C, r, [] {});
   if (r == 0 && warp == 0) put_loss(a, t, q, zk, row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s), lane);
 }
 
@@ -871,7 +899,7 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
     Pack<E> k[LEAF_GROUPS];
 #pragma unroll
     for (int u = 0; u < LEAF_GROUPS; ++u) k[u] = load_pack(view, u * LEAF_GROUP + lane * 8);
-    leaf_pass<false, false>(k, r + i * C, in.c, RankOf{false, 0, 0.f, 0u, 0u}, to, 0u, lane < C, lane);
+    leaf_pass<false, false>(k, r + i * C, in.c, RankOf{}, to, 0u, lane < C, lane);
   }
   if (C > 1) cluster_sync();
   else __syncthreads();
@@ -920,13 +948,26 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
   if (C > 1) cluster_wait();
 }
 
-// CTAs of ROW_THREADS per row: one where the rows fill the GPU, else up to MAX_CLUSTER so that few
-// rows still spread over it; never more than the row has leaves for.
-int row_cluster(const LogitRows& in) {
-  constexpr int64_t kResident = 4 * 152;  // CTAs of ROW_THREADS that run at once
-  int c = 1;
-  while (c < MAX_CLUSTER && 2 * c * in.T <= kResident && 2 * c * (ROW_THREADS / 32) <= 2 * leaves_of(in.n)) c *= 2;
-  return c;
+// CTAs (c, a cluster) and warps (w) of a row in the statistics passes. With 64 registers a thread an
+// SM runs 32 warps, so floor(32 / w) CTAs; a row takes ceil(leaves / (c w)) rounds of leaves, about
+// two more for what surrounds them (the target, the fold, the alternatives) and half a one for each
+// doubling of the cluster. The shape with the least waves x rounds: one CTA of 8 warps where rows
+// fill the GPU, 8 CTAs of 19 for a single row of 149 leaves, CTAs of 2 warps for many short rows.
+struct RowShape {
+  int cluster, threads;
+};
+RowShape row_shape(const LogitRows& in) {
+  const int64_t L = leaves_of(in.n);
+  RowShape best{1, ROW_THREADS};
+  int64_t least = INT64_MAX;
+  for (int c = 1, half = 0; c <= MAX_CLUSTER; c *= 2, ++half)
+    for (int w = 2; w <= 32; ++w) {
+      if (w > 2 && c * (w - 1) >= L) break;  // more warps than leaves
+      const int64_t waves = (in.T * static_cast<int64_t>(c) + 152 * (32 / w) - 1) / (152 * (32 / w));
+      const int64_t cost = waves * (2 * ((L + c * w - 1) / (c * w)) + 4 + half);
+      if (cost < least) least = cost, best = RowShape{c, 32 * w};
+    }
+  return best;
 }
 
 // Launches `ctas` CTAs in clusters of `cluster`.
@@ -1042,12 +1083,13 @@ rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
   a.entropy = entropy;
   a.top_ids = top_ids;
   a.top_logp = top_logp;
-  a.cluster = row_cluster(a.in);
+  const RowShape shape = row_shape(a.in);
+  a.cluster = shape.cluster;
   return with_types(dtype, aligned_rows(logits, ld, dtype_bytes(dtype)), [&](auto e, auto al) {
     using E = decltype(e);
     constexpr bool AL = decltype(al)::value;
     return launch_rows(top_k ? token_logprobs_kernel<E, true, AL> : token_logprobs_kernel<E, false, AL>, a,
-                       T * a.cluster, a.cluster, row_smem_bytes(a.in.n, top_k > 0), stream);
+                       T * a.cluster, a.cluster, row_smem_bytes(a.in.n, top_k > 0), stream, shape.threads);
   });
 }
 
@@ -1091,10 +1133,11 @@ rlk_status check_distill(const void* logits, int32_t dtype, int64_t T, int64_t l
 }
 
 rlk_status launch_distill_fwd(DistillArgs a, int32_t dtype, void* stream) {
-  a.cluster = row_cluster(a.in);
+  const RowShape shape = row_shape(a.in);
+  a.cluster = shape.cluster;
   return with_types(dtype, aligned_rows(a.in.base, a.in.ld, dtype_bytes(dtype)), [&](auto e, auto al) {
     return launch_rows(distill_kernel<decltype(e), decltype(al)::value>, a, static_cast<int64_t>(a.in.T) * a.cluster,
-                       a.cluster, row_smem_bytes(a.in.n, false), stream);
+                       a.cluster, row_smem_bytes(a.in.n, false), stream, shape.threads);
   });
 }
 
