@@ -18,6 +18,8 @@ constexpr int MAX_ROW_WARPS = MAX_CLUSTER * MAX_ROW_THREADS / 32;
 constexpr int GROUPS_PER_LEAF = LEAF_GROUPS;                 // 256-column groups, the units of the alternatives' search
 constexpr int GRAD_PACKS = 4;                                // packs a thread has in flight in the gradients
 constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates: 8 columns of each chosen octet
+constexpr int PLACES = 2 * RLK_MAX_TOP_K;                    // most groups at the first attempt
+constexpr int OCTETS = 4 * RLK_MAX_TOP_K;                    // most octets at the first attempt
 
 // ---------------------------------------------------------------------------
 // one pass over a row by a cluster of CTAs (one CTA when there are rows enough)
@@ -271,11 +273,10 @@ struct ScoreArgs {
 };
 
 // Shared memory of the alternatives' search.
-constexpr int FEW = 256;           // candidates that go straight to the last step
 struct TopSmem {
   unsigned long long cand[CAND];   // order key in the high word, ~column in the low one
-  int place[RLK_MAX_TOP_K];        // chosen groups
-  int octet[RLK_MAX_TOP_K];        // chosen octets
+  int place[PLACES];               // chosen groups
+  int octet[OCTETS];               // first columns of the chosen octets
   int n_place, n_octet, n_cand, ties;
   float bar, lse;
 };
@@ -290,94 +291,86 @@ __host__ __device__ constexpr size_t row_smem_bytes(int n, bool top) {
   return b > octets ? b : octets;
 }
 
-__device__ __forceinline__ int chosen_most(int k) { return min(RLK_MAX_TOP_K, 2 * k + 16); }
-
-// Adds the columns of a pack (its first column c) that reach `bar` to the candidates, `most` of them
-// at the most; n_cand counts them all. Few lanes have any.
-template <class E>
-__device__ __forceinline__ void offer(const Pack<E>& k, int c, float bar, int most, TopSmem& ts) {
-  if (!(pack_max(k) >= bar)) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 z2 = pair(k, i / 2);
-    const float z = i & 1 ? z2.y : z2.x;
-    if (z >= bar) {
-      const int at = atomicAdd(&ts.n_cand, 1);
-      if (at < most) ts.cand[at] = static_cast<unsigned long long>(order_key(z)) << 32 | static_cast<uint32_t>(~(c + i));
-    }
-  }
-}
+// So many may reach a bar: with room above k, a bar is found in fewer steps.
+__device__ __forceinline__ int chosen_most(int k, int room) { return min(room, 2 * k + 16); }
 
 // The top_k alternatives of a row, by one CTA, from its groups' maxima and the bar that choose_bar
 // found for them.
 //  1. The k groups of 256 columns with the largest maxima (lower group first among equals) hold
 //     the k best columns: a column outside them has k group maxima ahead of it. Chosen are they and
 //     a few more that reach the bar, which k columns reach.
-//  2. Their columns that reach the bar are the candidates: little more than k, unless good columns
-//     crowd into few groups or are tied.
-//  3. If they are too many, the same choice among the chosen groups' octets (8 columns) leaves
-//     at most CAND.
+//  2. Their octets (8 columns) that reach the bar.
+//  3. The octets' columns that reach the bar are the candidates: little more than k, unless good
+//     columns crowd into few groups or are tied. If there are more than CAND of them, the same
+//     choice among the octets' maxima leaves 128 octets at most, and so no more than CAND.
 //  4. Each candidate's place is the number of candidates ahead of it.
 template <class R, class E = typename R::E>
 __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowSmem& sm, TopSmem& ts,
                          bool bad, float lse) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int K = a.top_k, groups = (row.n + LEAF_GROUP - 1) / LEAF_GROUP, most = chosen_most(K);
+  const int K = a.top_k, groups = (row.n + LEAF_GROUP - 1) / LEAF_GROUP;
   const float bar = ts.bar;
-  const auto pack_of = [&](int c) {
-    return packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c);
+  const auto octet_max = [&](int c) {
+    return pack_max(packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c));
   };
-  // the chosen groups: in any order for step 2, in ascending order for step 3
-  const bool tied = ts.ties < groups;
-  bool many = !bad && (tied || (groups <= K && row.n > FEW));
+  const auto collect = [&](float reached) {
+    for (int i = threadIdx.x; i < 8 * ts.n_octet; i += blockDim.x) {
+      const int c = ts.octet[i / 8] + i % 8;
+      const float z = c < row.n ? row.at(c) : neg_inf();
+      if (!(z >= reached)) continue;
+      const int at = atomicAdd(&ts.n_cand, 1);
+      if (at < CAND) ts.cand[at] = static_cast<unsigned long long>(order_key(z)) << 32 | static_cast<uint32_t>(~c);
+    }
+    __syncthreads();
+  };
+  const bool tied = ts.ties < groups;  // no bar parts the groups
+  bool many = !bad && (tied || groups <= K);
   if (!many && !bad) {
     for (int i = threadIdx.x; i < groups; i += blockDim.x)
       if (sm.group[i] >= bar) {
         const int at = atomicAdd(&ts.n_place, 1);
-        if (at < most) ts.place[at] = i;
+        if (at < PLACES) ts.place[at] = i;
       }
     __syncthreads();
-    const int chosen = ts.n_place;
-    for (int i0 = warp; i0 < chosen; i0 += 4 * warps) {
-      Pack<E> k[4];
-      int c[4];
-      const int n = min(4, (chosen - i0 + warps - 1) / warps);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        c[u] = u < n ? ts.place[i0 + u * warps] * LEAF_GROUP + lane * 8 : 0;
-        if (u < n) k[u] = pack_of(c[u]);
+    const int chosen = min(ts.n_place, PLACES);
+#pragma unroll 4
+    for (int i = warp; i < chosen; i += warps) {
+      const int c = ts.place[i] * LEAF_GROUP + lane * 8;
+      if (octet_max(c) >= bar) {
+        const int at = atomicAdd(&ts.n_octet, 1);
+        if (at < OCTETS) ts.octet[at] = c;
       }
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (u < n) offer(k[u], c[u], bar, FEW, ts);
     }
     __syncthreads();
-    many = ts.n_cand > FEW;
+    many = ts.n_octet > OCTETS;
+    if (!many) {
+      collect(bar);
+      many = ts.n_cand > CAND;
+    }
   }
   if (many) {  // the same for the whole CTA
     if (warp == 0) {
-      const int m = take_places(sm.group, groups, bar, ts.ties, ts.place, RLK_MAX_TOP_K, lane);
+      int ties;
+      const float b = choose_bar(sm.group, groups, K, RLK_MAX_TOP_K, E::kKeyShift, &ties, lane);
+      const int m = take_places(sm.group, groups, b, ties, ts.place, RLK_MAX_TOP_K, lane);
       if (lane == 0) ts.n_place = m;
     }
     __syncthreads();
     float* omax = reinterpret_cast<float*>(sm.leaf);
     const int chosen = ts.n_place, N = chosen * 32;
-    for (int i = warp; i < chosen; i += warps)
-      omax[i * 32 + lane] = pack_max(pack_of(ts.place[i] * LEAF_GROUP + lane * 8));
+    for (int i = warp; i < chosen; i += warps) omax[i * 32 + lane] = octet_max(ts.place[i] * LEAF_GROUP + lane * 8);
     for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) omax[i] = neg_inf();
     __syncthreads();
     if (warp == 0) {
       int ties;
-      const float b = choose_bar(omax, N, K, most, E::kKeyShift, &ties, lane);
+      const float b = choose_bar(omax, N, K, chosen_most(K, RLK_MAX_TOP_K), E::kKeyShift, &ties, lane);
       const int m = take_places(omax, N, b, ties, ts.octet, RLK_MAX_TOP_K, lane);
+      __syncwarp();
+      for (int i = lane; i < m; i += 32) ts.octet[i] = ts.place[ts.octet[i] / 32] * LEAF_GROUP + ts.octet[i] % 32 * 8;
       if (lane == 0) ts.bar = b, ts.n_octet = m, ts.n_cand = 0;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < ts.n_octet; i += blockDim.x) {
-      const int c = ts.place[ts.octet[i] / 32] * LEAF_GROUP + ts.octet[i] % 32 * 8;
-      offer(pack_of(c), c, ts.bar, CAND, ts);
-    }
-    __syncthreads();
+    collect(ts.bar);
   }
   const int n = ts.n_cand;
   int64_t* ids = a.top_ids + t * K;
@@ -411,7 +404,7 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(cons
   const Row<E, AL> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
   const RowSmem sm{reinterpret_cast<Stats*>(dyn), reinterpret_cast<float*>(dyn + leaves_of(in.n) * sizeof(Stats)), counts};
   if (TOP && r == 0) {
-    if (threadIdx.x == 0) ts.n_cand = ts.n_place = 0;
+    if (threadIdx.x == 0) ts.n_cand = ts.n_place = ts.n_octet = 0;
     for (int i = leaves_of(in.n) * GROUPS_PER_LEAF + threadIdx.x; i < keys_of(in.n); i += blockDim.x) sm.group[i] = neg_inf();
   }
   RankOf rank;
@@ -438,7 +431,7 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(cons
   if constexpr (TOP) {
     if (warp == 0) {
       int ties;
-      const float b = choose_bar(sm.group, (in.n + LEAF_GROUP - 1) / LEAF_GROUP, a.top_k, chosen_most(a.top_k),
+      const float b = choose_bar(sm.group, (in.n + LEAF_GROUP - 1) / LEAF_GROUP, a.top_k, chosen_most(a.top_k, PLACES),
                                  E::kKeyShift, &ties, lane);
       if (lane == 0) ts.bar = b, ts.ties = ties;
     }
