@@ -15,8 +15,11 @@ constexpr int ROW_THREADS = 256;
 constexpr int MAX_CLUSTER = 8;                               // CTAs of one row (the portable cluster size)
 constexpr int MAX_ROW_THREADS = 1024;
 constexpr int MAX_ROW_WARPS = MAX_CLUSTER * MAX_ROW_THREADS / 32;
-constexpr int GROUPS_PER_LEAF = LEAF_GROUPS;                 // 256-column groups, the units of the alternatives' search
+// The units in which the pass keeps maxima for the alternatives' search: groups of 256 columns (four
+// a leaf), or in short rows octets, the packs themselves.
+enum TopCells : int { TOP_NONE = 0, TOP_GROUPS = 1, TOP_OCTETS = 2 };
 constexpr int GRAD_PACKS = 4;                                // packs a thread has in flight in the gradients
+constexpr int SHORT_ROW = 32768;                             // columns up to which the cells are octets
 constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates: 8 columns of each chosen octet
 constexpr int PLACES = 2 * RLK_MAX_TOP_K;                    // most groups at the first attempt
 constexpr int OCTETS = 4 * RLK_MAX_TOP_K;                    // most octets at the first attempt
@@ -26,16 +29,21 @@ constexpr int OCTETS = 4 * RLK_MAX_TOP_K;                    // most octets at t
 // ---------------------------------------------------------------------------
 // Warp g of the row's C x (blockDim / 32) warps takes leaves g, g + (number of warps), ... and
 // leaves what it found in the shared memory of the cluster's CTA 0 (distributed shared memory):
-// (m, s, u) of each leaf, the maxima of its four groups (TOP), and how many columns stand ahead of
-// the target.
+// (m, s, u) of each leaf, the maxima of its cells (TOP), and how many columns stand ahead of the
+// target.
 struct RowSmem {
   Stats* leaf;      // [n_leaves]
-  float* group;     // [keys_of(n)]
+  float* cell;      // [cell_room(n, TOP)]
   int* count;       // [MAX_ROW_WARPS]
 };
 
 __host__ __device__ constexpr int leaves_of(int n) { return (n + ROW_LEAF - 1) / ROW_LEAF; }
-__host__ __device__ constexpr int keys_of(int n) { return (leaves_of(n) * GROUPS_PER_LEAF + 127) / 128 * 128; }
+__host__ __device__ constexpr int cells_of(int n, int top) {
+  return top == TOP_OCTETS ? (n + 7) / 8 : (n + LEAF_GROUP - 1) / LEAF_GROUP;
+}
+__host__ __device__ constexpr int cell_room(int n, int top) {  // whole leaves, a multiple of 128
+  return top == TOP_NONE ? 0 : top == TOP_OCTETS ? leaves_of(n) * 128 : (leaves_of(n) * LEAF_GROUPS + 127) / 128 * 128;
+}
 
 // The target of a row.
 struct RankOf {
@@ -102,26 +110,28 @@ __device__ __forceinline__ int count_ahead(const Pack<E> (&k)[LEAF_GROUPS], cons
   return n;
 }
 
-// What one leaf leaves behind (see RowSmem), at leaf0 / group0 of the cluster's shared memory, from
+// What one leaf leaves behind (see RowSmem), at leaf0 / cell0 of the cluster's shared memory, from
 // each lane that `puts` (lane 0 alone with ENT: the others lack u). Returns how many of the lane's
 // columns stand ahead of the target.
-template <bool ENT, bool TOP, class E>
+template <bool ENT, int TOP, class E>
 __device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l, float c, const RankOf& rank,
-                                         uint32_t leaf0, uint32_t group0, bool puts, int lane) {
+                                         uint32_t leaf0, uint32_t cell0, bool puts, int lane) {
   float gm[LEAF_GROUPS], m;
 #pragma unroll
   for (int j = 0; j < LEAF_GROUPS; ++j) {
     gm[j] = pack_max(k[j]);
-    if constexpr (TOP) gm[j] = warp_max(gm[j]);
+    if constexpr (TOP == TOP_OCTETS)
+      st_cluster_u32(cell0 + static_cast<uint32_t>((l * LEAF_GROUPS + j) * 32 + lane) * 4, __float_as_uint(gm[j]));
+    if constexpr (TOP == TOP_GROUPS) gm[j] = warp_max(gm[j]);
   }
   m = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
-  if constexpr (!TOP) m = warp_max(m);
+  if constexpr (TOP != TOP_GROUPS) m = warp_max(m);
   float2 x;
   if (m == neg_inf()) x = make_float2(any_nan(k) ? quiet_nan() : 0.f, 0.f);
   else x = leaf_sums<ENT>(k, m, c, lane);
   if (puts) {
     st_cluster_f32x4(leaf0 + static_cast<uint32_t>(l * 16), m, x.x, x.y, 0.f);
-    if (TOP) st_cluster_f32x4(group0 + static_cast<uint32_t>(l * 16), gm[0], gm[1], gm[2], gm[3]);
+    if (TOP == TOP_GROUPS) st_cluster_f32x4(cell0 + static_cast<uint32_t>(l * 16), gm[0], gm[1], gm[2], gm[3]);
   }
   // a leaf whose best column is below the target has none ahead of it: for a likely token, most
   return rank.on && m >= rank.z ? count_ahead(k, rank, l, lane) : 0;
@@ -139,13 +149,13 @@ __device__ __forceinline__ void prefetch_leaf(const R& row, int l) {
 }
 
 // `begin` runs in every thread after the first loads have been issued: what it loads arrives with them.
-template <bool ENT, bool TOP, class R, class B, class E = typename R::E>
+template <bool ENT, int TOP, class R, class B, class E = typename R::E>
 __device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, const RowSmem& sm, int C, int r, B begin) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5, g = r * warps + warp, n_leaves = leaves_of(row.n), step = C * warps;
   if (C > 1) cluster_arrive();  // CTA 0 must have started before anyone writes to it
   const uint32_t leaf0 = map_to_cta(smem_u32(sm.leaf), 0);
-  const uint32_t group0 = TOP ? map_to_cta(smem_u32(sm.group), 0) : 0;
+  const uint32_t cell0 = TOP ? map_to_cta(smem_u32(sm.cell), 0) : 0;
   int count = 0;
   // 64 registers have room for the next leaf's packs in the lean pass over 16-bit types alone (8192
   // rows of 151936 in bf16: 378 -> 354 us); elsewhere the other warps hide the loads
@@ -161,13 +171,13 @@ __device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, co
         const int i = l + u * step;
         if (i >= n_leaves) break;
         if (i + step < n_leaves) load_leaf(row, i + step, lane, k[u ^ 1]);
-        leaf_pass<ENT, TOP>(k[u], i, c, rank, leaf0, group0, lane == 0, lane);
+        leaf_pass<ENT, TOP>(k[u], i, c, rank, leaf0, cell0, lane == 0, lane);
       }
     }
   } else {
     for (int l = g; l < n_leaves;) {
       if (lane == 0) prefetch_leaf(row, l + step);
-      count += leaf_pass<ENT, TOP>(k[0], l, c, rank, leaf0, group0, lane == 0, lane);
+      count += leaf_pass<ENT, TOP>(k[0], l, c, rank, leaf0, cell0, lane == 0, lane);
       l += step;
       if (l < n_leaves) load_leaf(row, l, lane, k[0]);
     }
@@ -193,16 +203,19 @@ __device__ __forceinline__ float bar_value(uint32_t bar, int shift) {
 
 // A bar that the k best of v[0 .. N) reach and at most `most` of them, -inf never (all that are not
 // -inf reach the lowest finite value, the bar for N <= k). v is padded with -inf to a multiple of 128.
-// The first try is the k-th of the 32 lanes' maxima (k <= 32); where more than `most` reach it,
-// bisection raises it on the values' order keys, which hold nothing in their low `shift` bits,
-// counting the values at or above the middle. *ties: how many of those equal to the bar are to be
-// taken, lower places first -- all of them, unless ties stand in the way of any such bar.
+// The first try is the k-th of the 32 lanes' maxima, or for k > 32 steps down from the least of them,
+// doubled until k values reach it; where more than `most` do, bisection raises it on the values' order
+// keys, which hold nothing in their low `shift` bits, counting the values at or above the middle.
+// *ties: how many of those equal to the bar are to be taken, lower places first -- all of them, unless
+// ties stand in the way of any such bar.
 __device__ __forceinline__ float choose_bar(const float* v, int N, int k, int most, int shift, int* ties, int lane) {
+  constexpr float kLowest = -3.4028235e38f;
   *ties = N;
-  if (N <= k) return -3.4028235e38f;
+  if (N <= k) return kLowest;
   const int padded = (N + 127) / 128 * 128;
   const auto reach = [&](float bar) {
     int n = 0;
+#pragma unroll 4
     for (int i = lane * 4; i < padded; i += 128) {
       const float4 x = *reinterpret_cast<const float4*>(v + i);
       n += (x.x >= bar) + (x.y >= bar) + (x.z >= bar) + (x.w >= bar);
@@ -210,26 +223,35 @@ __device__ __forceinline__ float choose_bar(const float* v, int N, int k, int mo
     return __reduce_add_sync(kFullWarp, n);
   };
   float top = neg_inf();
+#pragma unroll 4
   for (int i = lane * 4; i < padded; i += 128) {
     const float4 x = *reinterpret_cast<const float4*>(v + i);
     top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
   }
-  uint32_t lo = 0;
-  float bar = -3.4028235e38f;
-  if (k <= 32) {
-    int before = 0;
+  int before = 0;  // lanes whose maximum stands ahead of this one's
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const float other = __shfl_sync(kFullWarp, top, j);
-      before += other > top || (other == top && j < lane);
-    }
-    const uint32_t at = __ballot_sync(kFullWarp, before == k - 1);
-    lo = order_key(__shfl_sync(kFullWarp, top, at ? __ffs(at) - 1 : 0)) >> shift;  // (no such lane: a NaN)
-    bar = bar_value(lo, shift);
+  for (int j = 0; j < 32; ++j) {
+    const float other = __shfl_sync(kFullWarp, top, j);
+    before += other > top || (other == top && j < lane);
   }
+  const auto ranked = [&](int r) {  // the r-th largest of them (r from 0; -inf where a NaN is among them)
+    const uint32_t at = __ballot_sync(kFullWarp, before == r);
+    const float x = __shfl_sync(kFullWarp, top, at ? __ffs(at) - 1 : 0);
+    return at ? x : neg_inf();
+  };
+  const float best = ranked(0);
+  uint32_t hi = (order_key(best) >> shift) + 1;  // fewer than k reach it
+  uint32_t lo = order_key(ranked(min(k, 32) - 1)) >> shift;
+  float bar = bar_value(lo, shift);
   int n = reach(bar);
+  for (float d = __fsub_rn(best, bar); n < k && bar > kLowest; d = __fadd_rn(d, d)) {
+    hi = lo;
+    const float next = __fsub_rn(bar, d);
+    lo = next < bar ? order_key(next) >> shift : 0u;  // (no step: d is 0 or lost against the bar)
+    bar = bar_value(lo, shift);
+    n = reach(bar);
+  }
   if (n > most) {
-    uint32_t hi = (__reduce_max_sync(kFullWarp, order_key(top)) >> shift) + 1;  // fewer than k reach it
     while (n > most && hi > lo + 1) {
       const uint32_t mid = lo + (hi - lo) / 2;
       const int m = reach(bar_value(mid, shift));
@@ -281,34 +303,31 @@ struct TopSmem {
   float bar, lse;
 };
 
-// Dynamic shared memory of a row: the octets' maxima take the place of the leaves' statistics and the
-// groups' maxima, which have been used by then.
-__host__ __device__ constexpr size_t row_smem_bytes(int n, bool top) {
-  size_t b = leaves_of(n) * sizeof(Stats);
-  if (!top) return b;
-  b += static_cast<size_t>(keys_of(n)) * 4;
+// Dynamic shared memory of a row. Where the cells are groups, the maxima of the chosen groups' octets
+// may take the place of the leaves' statistics and the cells, which have been used by then.
+__host__ __device__ constexpr size_t row_smem_bytes(int n, int top) {
+  const size_t b = leaves_of(n) * sizeof(Stats) + static_cast<size_t>(cell_room(n, top)) * 4;
   const size_t octets = RLK_MAX_TOP_K * 32 * 4;
-  return b > octets ? b : octets;
+  return top == TOP_GROUPS && b < octets ? octets : b;
 }
 
 // So many may reach a bar: with room above k, a bar is found in fewer steps.
 __device__ __forceinline__ int chosen_most(int k, int room) { return min(room, 2 * k + 16); }
 
-// The top_k alternatives of a row, by one CTA, from its groups' maxima and the bar that choose_bar
-// found for them.
-//  1. The k groups of 256 columns with the largest maxima (lower group first among equals) hold
-//     the k best columns: a column outside them has k group maxima ahead of it. Chosen are they and
-//     a few more that reach the bar, which k columns reach.
-//  2. Their octets (8 columns) that reach the bar.
-//  3. The octets' columns that reach the bar are the candidates: little more than k, unless good
+// The top_k alternatives of a row, by one CTA, from its cells' maxima and the bar that choose_bar found
+// for them.
+//  1. The k cells with the largest maxima (lower cell first among equals) hold the k best columns: a
+//     column outside them has k cells' maxima ahead of it. Chosen are they and some more that reach
+//     the bar, which k columns reach; of groups, the octets (8 columns) that reach it.
+//  2. The octets' columns that reach the bar are the candidates: little more than k, unless good
 //     columns crowd into few groups or are tied. If there are more than CAND of them, the same
 //     choice among the octets' maxima leaves 128 octets at most, and so no more than CAND.
-//  4. Each candidate's place is the number of candidates ahead of it.
-template <class R, class E = typename R::E>
+//  3. Each candidate's place is the number of candidates ahead of it (many are sorted instead).
+template <int TOP, class R, class E = typename R::E>
 __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowSmem& sm, TopSmem& ts,
                          bool bad, float lse) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int K = a.top_k, groups = (row.n + LEAF_GROUP - 1) / LEAF_GROUP;
+  const int K = a.top_k, cells = cells_of(row.n, TOP);
   const float bar = ts.bar;
   const auto octet_max = [&](int c) {
     return pack_max(packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c));
@@ -323,25 +342,29 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowS
     }
     __syncthreads();
   };
-  const bool tied = ts.ties < groups;  // no bar parts the groups
-  bool many = !bad && (tied || groups <= K);
+  // without ties at the bar, and with cells to choose among
+  bool many = !bad && (ts.ties < cells || (TOP == TOP_GROUPS && cells <= K));
   if (!many && !bad) {
-    for (int i = threadIdx.x; i < groups; i += blockDim.x)
-      if (sm.group[i] >= bar) {
-        const int at = atomicAdd(&ts.n_place, 1);
-        if (at < PLACES) ts.place[at] = i;
+    int* list = TOP == TOP_GROUPS ? ts.place : ts.octet;
+    int* count = TOP == TOP_GROUPS ? &ts.n_place : &ts.n_octet;
+    for (int i = threadIdx.x; i < cells; i += blockDim.x)
+      if (sm.cell[i] >= bar) {
+        const int at = atomicAdd(count, 1);
+        if (at < (TOP == TOP_GROUPS ? PLACES : OCTETS)) list[at] = TOP == TOP_GROUPS ? i : i * 8;
       }
     __syncthreads();
-    const int chosen = min(ts.n_place, PLACES);
+    if constexpr (TOP == TOP_GROUPS) {
+      const int chosen = min(ts.n_place, PLACES);
 #pragma unroll 4
-    for (int i = warp; i < chosen; i += warps) {
-      const int c = ts.place[i] * LEAF_GROUP + lane * 8;
-      if (octet_max(c) >= bar) {
-        const int at = atomicAdd(&ts.n_octet, 1);
-        if (at < OCTETS) ts.octet[at] = c;
+      for (int i = warp; i < chosen; i += warps) {
+        const int c = ts.place[i] * LEAF_GROUP + lane * 8;
+        if (octet_max(c) >= bar) {
+          const int at = atomicAdd(&ts.n_octet, 1);
+          if (at < OCTETS) ts.octet[at] = c;
+        }
       }
+      __syncthreads();
     }
-    __syncthreads();
     many = ts.n_octet > OCTETS;
     if (!many) {
       collect(bar);
@@ -349,24 +372,33 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowS
     }
   }
   if (many) {  // the same for the whole CTA
-    if (warp == 0) {
-      int ties;
-      const float b = choose_bar(sm.group, groups, K, RLK_MAX_TOP_K, E::kKeyShift, &ties, lane);
-      const int m = take_places(sm.group, groups, b, ties, ts.place, RLK_MAX_TOP_K, lane);
-      if (lane == 0) ts.n_place = m;
+    const float* omax = sm.cell;
+    int N = cells;
+    if constexpr (TOP == TOP_GROUPS) {
+      if (warp == 0) {
+        int ties;
+        const float b = choose_bar(sm.cell, cells, K, RLK_MAX_TOP_K, E::kKeyShift, &ties, lane);
+        const int m = take_places(sm.cell, cells, b, ties, ts.place, RLK_MAX_TOP_K, lane);
+        if (lane == 0) ts.n_place = m;
+      }
+      __syncthreads();
+      float* o = reinterpret_cast<float*>(sm.leaf);
+      const int chosen = ts.n_place;
+      omax = o;
+      N = chosen * 32;
+      for (int i = warp; i < chosen; i += warps) o[i * 32 + lane] = octet_max(ts.place[i] * LEAF_GROUP + lane * 8);
+      for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) o[i] = neg_inf();
+      __syncthreads();
     }
-    __syncthreads();
-    float* omax = reinterpret_cast<float*>(sm.leaf);
-    const int chosen = ts.n_place, N = chosen * 32;
-    for (int i = warp; i < chosen; i += warps) omax[i * 32 + lane] = octet_max(ts.place[i] * LEAF_GROUP + lane * 8);
-    for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) omax[i] = neg_inf();
-    __syncthreads();
     if (warp == 0) {
       int ties;
-      const float b = choose_bar(omax, N, K, chosen_most(K, RLK_MAX_TOP_K), E::kKeyShift, &ties, lane);
+      const float b = choose_bar(omax, N, K, RLK_MAX_TOP_K, E::kKeyShift, &ties, lane);
       const int m = take_places(omax, N, b, ties, ts.octet, RLK_MAX_TOP_K, lane);
       __syncwarp();
-      for (int i = lane; i < m; i += 32) ts.octet[i] = ts.place[ts.octet[i] / 32] * LEAF_GROUP + ts.octet[i] % 32 * 8;
+      for (int i = lane; i < m; i += 32) {
+        const int o = ts.octet[i];
+        ts.octet[i] = TOP == TOP_GROUPS ? ts.place[o / 32] * LEAF_GROUP + o % 32 * 8 : o * 8;
+      }
       if (lane == 0) ts.bar = b, ts.n_octet = m, ts.n_cand = 0;
     }
     __syncthreads();
@@ -375,15 +407,34 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowS
   const int n = ts.n_cand;
   int64_t* ids = a.top_ids + t * K;
   float* lps = a.top_logp + t * K;
-  for (int i = threadIdx.x; i < n; i += blockDim.x) {
-    const unsigned long long me = ts.cand[i];
-    int place = 0;
+  const auto put = [&](int place, unsigned long long c) {
+    ids[place] = static_cast<int64_t>(~static_cast<uint32_t>(c));
+    lps[place] = token_logp(key_value(static_cast<uint32_t>(c >> 32)), a.in.s, lse);
+  };
+  if ((n + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x) * n <= 1024) {  // a pass over the others for each
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const unsigned long long me = ts.cand[i];
+      int place = 0;
 #pragma unroll 8
-    for (int j = 0; j < n; ++j) place += ts.cand[j] > me;
-    if (place < K) {
-      ids[place] = static_cast<int64_t>(~static_cast<uint32_t>(me));
-      lps[place] = token_logp(key_value(static_cast<uint32_t>(me >> 32)), a.in.s, lse);
+      for (int j = 0; j < n; ++j) place += ts.cand[j] > me;
+      if (place < K) put(place, me);
     }
+  } else {  // for a small CTA, or many of them, a bitonic network over the next power of two is less (64 rows of
+            // 1000 with k = 100: 115 -> 31 us)
+    const int size = n <= 256 ? 256 : n <= 512 ? 512 : 1024;
+    static_assert(CAND == 1024, "the network's largest size");
+    for (int i = n + threadIdx.x; i < size; i += blockDim.x) ts.cand[i] = 0;
+    for (int run = 2; run <= size; run *= 2)
+      for (int d = run / 2; d >= 1; d /= 2) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < size / 2; i += blockDim.x) {
+          const int x = 2 * i - (i & (d - 1)), y = x + d;  // i-th pair at distance d
+          const unsigned long long p = ts.cand[x], q = ts.cand[y];
+          if ((p < q) == ((x & run) == 0)) ts.cand[x] = q, ts.cand[y] = p;
+        }
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < min(n, K); i += blockDim.x) put(i, ts.cand[i]);
   }
   for (int i = n + threadIdx.x; i < K; i += blockDim.x) {
     ids[i] = -1;
@@ -392,7 +443,7 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowS
 }
 
 // 64 registers a thread, whatever the number of threads: 1024 of them fill an SM.
-template <class E, bool TOP, bool AL>
+template <class E, int TOP, bool AL>
 __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(const ScoreArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ int counts[MAX_ROW_WARPS];
@@ -405,7 +456,8 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(cons
   const RowSmem sm{reinterpret_cast<Stats*>(dyn), reinterpret_cast<float*>(dyn + leaves_of(in.n) * sizeof(Stats)), counts};
   if (TOP && r == 0) {
     if (threadIdx.x == 0) ts.n_cand = ts.n_place = ts.n_octet = 0;
-    for (int i = leaves_of(in.n) * GROUPS_PER_LEAF + threadIdx.x; i < keys_of(in.n); i += blockDim.x) sm.group[i] = neg_inf();
+    if (TOP == TOP_GROUPS)
+      for (int i = leaves_of(in.n) * LEAF_GROUPS + threadIdx.x; i < cell_room(in.n, TOP); i += blockDim.x) sm.cell[i] = neg_inf();
   }
   RankOf rank;
   row_pass<true, TOP>(row, in.c, rank, sm, C, r, [&] { rank.load(row, a.y ? a.y + t : nullptr, a.rank != nullptr); });
@@ -431,12 +483,12 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(cons
   if constexpr (TOP) {
     if (warp == 0) {
       int ties;
-      const float b = choose_bar(sm.group, (in.n + LEAF_GROUP - 1) / LEAF_GROUP, a.top_k, chosen_most(a.top_k, PLACES),
+      const float b = choose_bar(sm.cell, cells_of(in.n, TOP), a.top_k, chosen_most(a.top_k, TOP == TOP_GROUPS ? PLACES : OCTETS),
                                  E::kKeyShift, &ties, lane);
       if (lane == 0) ts.bar = b, ts.ties = ties;
     }
     __syncthreads();
-    find_top(row, a, t, sm, ts, isnan(ts.lse), ts.lse);
+    find_top<TOP>(row, a, t, sm, ts, isnan(ts.lse), ts.lse);
   }
 }
 
@@ -758,7 +810,7 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const Disti
   }
   RowSmem sm{reinterpret_cast<Stats*>(dyn), nullptr, nullptr};
   RankOf none;
-  row_pass<false, false>(row, in.c, none, sm, C, r, [] {});
+  row_pass<false, TOP_NONE>(row, in.c, none, sm, C, r, [] {});
   if (r == 0 && warp == 0) put_loss(a, t, q, zk, row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s), lane);
 }
 
@@ -904,7 +956,7 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
     Pack<E> k[LEAF_GROUPS];
 #pragma unroll
     for (int u = 0; u < LEAF_GROUPS; ++u) k[u] = load_pack(view, u * LEAF_GROUP + lane * 8);
-    leaf_pass<false, false>(k, r + i * C, in.c, RankOf{}, to, 0u, lane < C, lane);
+    leaf_pass<false, TOP_NONE>(k, r + i * C, in.c, RankOf{}, to, 0u, lane < C, lane);
   }
   if (C > 1) cluster_sync();
   else __syncthreads();
@@ -958,16 +1010,20 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
 // two more for what surrounds them (the target, the fold, the alternatives) and half a one for each
 // doubling of the cluster. The shape with the least waves x rounds: one CTA of 8 warps where rows
 // fill the GPU (4 take 579 us where 8 take 509 and 16 564: 8192 rows of 151936 in bf16 with 20
-// alternatives), 8 CTAs of 19 for a single row of 149 leaves; a warp a leaf for short rows.
+// alternatives), 8 CTAs of 19 for a single row of 149 leaves. Short rows take a warp a leaf; a few of
+// them at least 4 or 8, to find the alternatives (64 rows of 1000 with k = 100: 31 -> 15 us; 4096
+// rows with k = 50 take 46 us with 2 warps, 55 with 8).
 struct RowShape {
   int cluster, threads;
 };
-RowShape row_shape(const LogitRows& in) {
+RowShape row_shape(const LogitRows& in, int top_k) {
   const int64_t L = leaves_of(in.n);
   RowShape best{1, ROW_THREADS};
   int64_t least = INT64_MAX;
+  const bool few_rows = in.T <= 4 * 152;
+  const int fewest = L >= 8 || (few_rows && top_k > 32) ? 8 : few_rows && top_k > 0 && L < 4 ? 4 : L < 2 ? 2 : static_cast<int>(L);
   for (int c = 1, half = 0; c <= MAX_CLUSTER; c *= 2, ++half)
-    for (int w = L < 2 ? 2 : L < 8 ? static_cast<int>(L) : 8; w <= 32; ++w) {
+    for (int w = fewest; w <= 32; ++w) {
       if (w > 8 && c * (w - 1) >= L) break;  // more warps than leaves
       const int64_t waves = (in.T * static_cast<int64_t>(c) + 152 * (32 / w) - 1) / (152 * (32 / w));
       const int64_t cost = waves * (2 * ((L + c * w - 1) / (c * w)) + 4 + half);
@@ -1089,13 +1145,16 @@ rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
   a.entropy = entropy;
   a.top_ids = top_ids;
   a.top_logp = top_logp;
-  const RowShape shape = row_shape(a.in);
+  const RowShape shape = row_shape(a.in, top_k);
   a.cluster = shape.cluster;
   return with_types(dtype, aligned_rows(logits, ld, dtype_bytes(dtype)), [&](auto e, auto al) {
     using E = decltype(e);
     constexpr bool AL = decltype(al)::value;
-    return launch_rows(top_k ? token_logprobs_kernel<E, true, AL> : token_logprobs_kernel<E, false, AL>, a,
-                       T * a.cluster, a.cluster, row_smem_bytes(a.in.n, top_k > 0), stream, shape.threads);
+    const int top = top_k == 0 ? TOP_NONE : V_true <= SHORT_ROW ? TOP_OCTETS : TOP_GROUPS;
+    const auto kernel = top == TOP_NONE     ? token_logprobs_kernel<E, TOP_NONE, AL>
+                        : top == TOP_OCTETS ? token_logprobs_kernel<E, TOP_OCTETS, AL>
+                                            : token_logprobs_kernel<E, TOP_GROUPS, AL>;
+    return launch_rows(kernel, a, T * a.cluster, a.cluster, row_smem_bytes(a.in.n, top), stream, shape.threads);
   });
 }
 
@@ -1139,11 +1198,11 @@ rlk_status check_distill(const void* logits, int32_t dtype, int64_t T, int64_t l
 }
 
 rlk_status launch_distill_fwd(DistillArgs a, int32_t dtype, void* stream) {
-  const RowShape shape = row_shape(a.in);
+  const RowShape shape = row_shape(a.in, 0);
   a.cluster = shape.cluster;
   return with_types(dtype, aligned_rows(a.in.base, a.in.ld, dtype_bytes(dtype)), [&](auto e, auto al) {
     return launch_rows(distill_kernel<decltype(e), decltype(al)::value>, a, static_cast<int64_t>(a.in.T) * a.cluster,
-                       a.cluster, row_smem_bytes(a.in.n, false), stream, shape.threads);
+                       a.cluster, row_smem_bytes(a.in.n, TOP_NONE), stream, shape.threads);
   });
 }
 
