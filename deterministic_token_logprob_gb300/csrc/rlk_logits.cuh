@@ -167,8 +167,10 @@ struct Row {
   int32_t n;
   uint32_t shift;  // bytes that p lies past a 16-byte boundary; the same for every thread
   int32_t* err;    // for the index checks of debug-checks builds
-  __device__ __forceinline__ Row(const typename E::bits* p_, int n_, int32_t* err_)
-      : p(p_), n(n_), shift(AL ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p_) & 15u)), err(err_) {}
+  int32_t room;    // likewise: bytes before p that may be read (a copy of a part of a row has some)
+  __device__ __forceinline__ Row(const typename E::bits* p_, int n_, int32_t* err_, int room_ = 0)
+      : p(p_), n(n_), shift(AL ? 0u : static_cast<uint32_t>(reinterpret_cast<uintptr_t>(p_) & 15u)), err(err_),
+        room(room_) {}
   __device__ __forceinline__ float at(int64_t c) const { return dbg_ok(c >= 0 && c < n, err) ? E::to_f32(p[c]) : 0.f; }
 };
 
@@ -190,7 +192,7 @@ __device__ __forceinline__ Pack<E> load_pack(const R& r, int c0) {
   constexpr int W = Pack<E>::WORDS, EB = Pack<E>::EB;
   Pack<E> k{};
   // the first byte of the first vector and the last of the last one lie in the row
-  if (!dbg_ok(c0 >= 0 && static_cast<int64_t>(c0) * EB >= r.shift &&
+  if (!dbg_ok(c0 >= 0 && static_cast<int64_t>(c0) * EB + r.room >= r.shift &&
                   static_cast<int64_t>(c0 + 8) * EB + (R::AL ? 0 : 16 - static_cast<int>(r.shift)) <=
                       static_cast<int64_t>(r.n) * EB,
               r.err))
@@ -398,62 +400,6 @@ __device__ __forceinline__ float token_logp(float z, float s, float lse) {
 // e^{s (z - b)} as the gradient forms it: d = s z - lse (one rounding, small where p counts),
 // p = ex2(d log2 e).
 __device__ __forceinline__ float prob_of(float d) { return ex2_approx(__fmul_rn(d, kLog2e)); }
-
-// ---------------------------------------------------------------------------
-// the teacher's distribution of one row
-// ---------------------------------------------------------------------------
-struct alignas(16) TeacherRow {    // in shared memory, one entry per k < RLK_MAX_TOP_K
-  int32_t id[RLK_MAX_TOP_K];       // -1: no entry
-  float q[RLK_MAX_TOP_K];          // 0 without an entry
-  float logq[RLK_MAX_TOP_K];       // 0 where q is 0
-  int32_t any;                     // some entry has q > 0
-  int32_t bad;                     // RLK_FLAG_BAD_TARGET / RLK_FLAG_NONFINITE of the row
-};
-
-// q = softmax(s t_k) over the row's K entries, by one warp: lane i takes entries i, i + 32, ...
-__device__ __forceinline__ void teacher_softmax(TeacherRow& r, const int64_t* ids, const float* t, int K, int n,
-                                                float s, float c, int lane) {
-  constexpr int R = RLK_MAX_TOP_K / 32;
-  int32_t id[R];
-  float v[R];
-  float m = neg_inf();
-  bool bad = false, inf = false;
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int k = lane + 32 * i;
-    const int64_t x = k < K ? ids[k] : -1;
-    v[i] = k < K ? t[k] : neg_inf();
-    bad |= x < -1 || x >= n;
-    id[i] = x < 0 || x >= n ? -1 : static_cast<int32_t>(x);
-    if (id[i] < 0) v[i] = neg_inf();
-    inf |= !(v[i] < __int_as_float(0x7f800000));  // NaN or +inf
-    m = fmaxf(m, v[i]);
-  }
-  bad = __any_sync(kFullWarp, bad);
-  inf = __any_sync(kFullWarp, inf);
-  m = warp_max(m);
-  float w[R], sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    v[i] = v[i] > neg_inf() ? __fsub_rn(v[i], m) : neg_inf();
-    w[i] = ex2_approx(__fmul_rn(v[i], c));
-    sum = __fadd_rn(sum, w[i]);
-  }
-  sum = warp_sum(sum);
-  const float ls = logf(sum);
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int k = lane + 32 * i;
-    const bool some = w[i] > 0.f;
-    r.id[k] = id[i];
-    r.q[k] = some ? __fdiv_rn(w[i], sum) : 0.f;
-    r.logq[k] = some ? __fmaf_rn(v[i], s, -ls) : 0.f;
-  }
-  if (lane == 0) {
-    r.any = m > neg_inf();
-    r.bad = (bad ? RLK_FLAG_BAD_TARGET : 0) | (inf ? RLK_FLAG_NONFINITE : 0);
-  }
-}
 
 // ---------------------------------------------------------------------------
 // host-side checks shared by the entry points

@@ -1,0 +1,176 @@
+// rlk_logits_grad.cuh -- writing the gradient with respect to a row of logits: which CTA writes which
+// columns, in packs that are aligned in the output whatever their alignment in the logits.
+#pragma once
+
+#include <utility>
+
+#include "rlk_logits_row.cuh"
+
+namespace rlk {
+namespace {
+
+constexpr int GRAD_PACKS = 4;                                // packs a thread has in flight in the gradients
+
+struct GradOut {
+  void* base;
+  int64_t ld;
+  int32_t V;
+};
+
+// The columns of one row of dlogits that one CTA writes, in packs of 8 that are 16-byte aligned in
+// the output: `head` columns lie before the first of them, fewer than 8 after the last. The row is
+// divided into `parts` runs of packs; the first part takes the head, the last the tail. The input
+// packs of the same columns may lie at any alignment (Row); where dlogits are the logits
+// themselves they are aligned as well, so no thread reads a column that another one writes.
+template <class E_, class O_, bool AL>
+struct GradPart {
+  using E = E_;
+  using O = O_;
+  Row<E, AL> in;              // from column `head` on
+  typename O::bits* out;      // the row's first column
+  int n, V, head, packs, q0, q1, lo, hi;
+  __device__ __forceinline__ GradPart(const typename E::bits* z, int n_, typename O::bits* o, int V_, int part, int parts,
+                                      int32_t* err)
+      : in(z, n_, err), out(o), n(n_), V(V_) {
+    constexpr int OB = sizeof(typename O::bits);
+    head = min(V, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(o) & 15u)) & 15u) / OB);
+    packs = (V - head) / 8;
+    const int per = (packs + parts - 1) / parts;
+    q0 = min(packs, part * per);
+    q1 = min(packs, q0 + per);
+    lo = part == 0 ? 0 : head + 8 * q0;
+    hi = part == parts - 1 ? V : head + 8 * q1;
+    in = Row<E, AL>(z + head, max(0, n - head), err);
+  }
+  __device__ __forceinline__ bool owns(int64_t c) const { return c >= lo && c < hi; }
+  __device__ __forceinline__ void put(int c, float v) const {
+    if (dbg_ok(c >= 0 && c < V, in.err)) out[c] = O::from_f32(v);
+  }
+};
+
+template <class O>
+__device__ __forceinline__ void store_pack(typename O::bits* p, const float (&v)[8]) {
+  uint4* q = reinterpret_cast<uint4*>(p);
+  if constexpr (sizeof(typename O::bits) == 4) {
+    q[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    q[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+  } else {
+    q[0] = make_uint4(O::pack2(v[0], v[1]), O::pack2(v[2], v[3]), O::pack2(v[4], v[5]), O::pack2(v[6], v[7]));
+  }
+}
+
+// Writes f(z, column) for the part's columns (0 past the row's n columns, and everywhere when !live,
+// without reading). Each thread has U packs in flight; `first` runs in every thread between the
+// first loads and the first store.
+template <int U, class G, class F, class B>
+__device__ __forceinline__ void write_part(const G& g, bool live, F f, B first) {
+  using E = typename G::E;
+  using O = typename G::O;
+  const int tid = threadIdx.x, threads = blockDim.x;
+  bool begun = false;
+  const auto put_pack = [&](const Pack<E>& k, int c) {
+    float v[8];
+    f.pack(k, g.head + c, v);
+    if (c + 8 > g.in.n) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c + i >= g.in.n) v[i] = 0.f;
+    }
+    if (dbg_ok(g.head + c + 8 <= g.V, g.in.err)) store_pack<O>(g.out + g.head + c, v);
+  };
+  for (int q = g.q0; !begun || q < g.q1; q += U * threads) {
+    Pack<E> k[U];
+    const bool full = live && q + U * threads <= g.q1 && packs_inside(g.in, q * 8, (q + U * threads) * 8);
+    if (full) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) k[u] = load_pack(g.in, (q + tid + u * threads) * 8);
+    } else if (live) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int p = q + tid + u * threads;
+        if (p < g.q1) k[u] = packs_inside(g.in, p * 8, p * 8 + 8) ? load_pack(g.in, p * 8) : load_pack_edge(g.in, p * 8);
+      }
+    }
+    if (!begun) {
+      begun = true;
+      first();
+      // the columns outside the packs: before the head and after the last pack
+      const int tail0 = g.head + 8 * g.packs;
+      if (tid < 16) {
+        const int c = tid < 8 ? tid : tail0 + tid - 8;
+        if (g.owns(c) && (tid >= 8 || c < g.head))
+          g.put(c, live && c < g.n ? f.one(E::to_f32(g.in.p[c - g.head]), c) : 0.f);
+      }
+    }
+    if (full) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) put_pack(k[u], (q + tid + u * threads) * 8);
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int p = q + tid + u * threads;
+        if (p >= g.q1) break;
+        if (live) {
+          put_pack(k[u], p * 8);
+        } else {
+          const float v[8] = {};
+          store_pack<O>(g.out + g.head + p * 8, v);
+        }
+      }
+    }
+  }
+}
+
+// CTAs of a row in a kernel that writes gradients alone.
+// Parts of up to four rounds of every thread's packs (the work that
+// a CTA does once -- its row's scalars, the teacher's softmax -- is then small: 8192 rows of 151936
+// in bf16 take 715 us with four rounds, 954 with one), as long as that leaves CTAs enough for the GPU.
+inline int grad_parts(const LogitRows& in, const GradOut& o) {
+  constexpr int kCols = 8 * GRAD_PACKS * ROW_THREADS;
+  constexpr int64_t kEnough = 6 * 152;
+  const int64_t rounds = (o.V + kCols - 1) / kCols;
+  int64_t each = in.T * rounds / kEnough;
+  each = each < 1 ? 1 : each > 4 ? 4 : each;
+  return static_cast<int>((rounds + each - 1) / each);
+}
+
+// dlogits: the logits' type, or bf16 for fp32 logits
+inline rlk_status check_out(const LogitRows& in, int32_t dtype, void* dlogits, int32_t out_dtype, int64_t V, int64_t out_ld,
+                     GradOut* o) {
+  const int eb = dtype_bytes(out_dtype);
+  if (eb == 0 || V < in.n || out_ld < V) return RLK_ERR_INVALID_ARG;
+  if (out_dtype != dtype && !(dtype == RLK_DTYPE_F32 && out_dtype == RLK_DTYPE_BF16)) return RLK_ERR_UNSUPPORTED;
+  if (V > RLK_MAX_LOGITS_VOCAB) return RLK_ERR_UNSUPPORTED;
+  if (in.T > 0 && (!dlogits || reinterpret_cast<uintptr_t>(dlogits) % eb != 0)) return RLK_ERR_INVALID_ARG;
+  // in place: the very same array; otherwise the two address ranges are apart
+  if (in.T > 0 && !(dlogits == in.base && out_dtype == dtype && (out_ld == in.ld || in.T == 1))) {
+    const auto span = [&](const void* p, int64_t ld, int64_t n, int bytes) {
+      const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+      return std::pair<uintptr_t, uintptr_t>(a, a + static_cast<uintptr_t>(((in.T - 1) * ld + n) * bytes));
+    };
+    const auto z = span(in.base, in.ld, in.n, dtype_bytes(dtype)), d = span(dlogits, out_ld, V, eb);
+    if (z.first < d.second && d.first < z.second) return RLK_ERR_INVALID_ARG;
+  }
+  *o = GradOut{dlogits, out_ld, static_cast<int32_t>(V)};
+  return RLK_OK;
+}
+
+// Whether the packs of every row's gradient are aligned in the logits as well: both sets of rows
+// are, or they lie alike (the same type, and the same distance from a boundary in every row).
+inline bool aligned_pair(const LogitRows& in, int32_t dtype, const GradOut& o, int32_t out_dtype) {
+  const int eb = dtype_bytes(dtype), ob = dtype_bytes(out_dtype);
+  if (aligned_rows(in.base, in.ld, eb) && aligned_rows(o.base, o.ld, ob)) return true;
+  return eb == ob && (reinterpret_cast<uintptr_t>(in.base) - reinterpret_cast<uintptr_t>(o.base)) % 16 == 0 &&
+         (in.ld - o.ld) * eb % 16 == 0;
+}
+
+template <class F>
+inline rlk_status with_types(int32_t dtype, int32_t out_dtype, bool aligned, F f) {
+  const auto al = [&](auto e, auto o) { return aligned ? f(e, o, Flag<true>{}) : f(e, o, Flag<false>{}); };
+  if (dtype == RLK_DTYPE_BF16) return al(Bf16{}, Bf16{});
+  if (dtype == RLK_DTYPE_F16) return al(F16{}, F16{});
+  return out_dtype == RLK_DTYPE_BF16 ? al(F32{}, Bf16{}) : al(F32{}, F32{});
+}
+
+}  // namespace
+}  // namespace rlk

@@ -1,0 +1,447 @@
+// rlk_token_logprobs.cu -- rlk_token_logprobs and rlk_token_logprobs_bwd: log probabilities of given
+// tokens from logits, with rank, entropy and top alternatives, and the gradient of logp and entropy.
+#include <cuda_runtime.h>
+
+#include "rlk_logits_grad.cuh"
+
+namespace rlk {
+namespace {
+
+constexpr int SHORT_ROW = 32768;                             // columns up to which the cells are octets
+constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates: 8 columns of each chosen octet
+constexpr int PLACES = 2 * RLK_MAX_TOP_K;                    // most groups at the first attempt
+constexpr int OCTETS = 4 * RLK_MAX_TOP_K;                    // most octets at the first attempt
+
+// ---------------------------------------------------------------------------
+// the best of N values, by one warp
+// ---------------------------------------------------------------------------
+// The value of the type whose order key >> shift is `bar` (its low bits are 0 in the fp32 image, so
+// 1 in the key of a negative value); the lowest finite value for -inf and below.
+__device__ __forceinline__ float bar_value(uint32_t bar, int shift) {
+  uint32_t key = bar << shift;
+  if (!(key & 0x80000000u)) key |= (1u << shift) - 1u;
+  return key <= order_key(neg_inf()) ? -3.4028235e38f : key_value(key);
+}
+
+// A bar that the k best of v[0 .. N) reach and at most `most` of them, -inf never (all that are not
+// -inf reach the lowest finite value, the bar for N <= k). v is padded with -inf to a multiple of 128.
+// The first try is the k-th of the 32 lanes' maxima, or for k > 32 steps down from the least of them,
+// doubled until k values reach it; where more than `most` do, bisection raises it on the values' order
+// keys, which hold nothing in their low `shift` bits, counting the values at or above the middle.
+// *ties: how many of those equal to the bar are to be taken, lower places first -- all of them, unless
+// ties stand in the way of any such bar.
+__device__ __forceinline__ float choose_bar(const float* v, int N, int k, int most, int shift, int* ties, int lane) {
+  constexpr float kLowest = -3.4028235e38f;
+  *ties = N;
+  if (N <= k) return kLowest;
+  const int padded = (N + 127) / 128 * 128;
+  const auto reach = [&](float bar) {
+    int n = 0;
+#pragma unroll 4
+    for (int i = lane * 4; i < padded; i += 128) {
+      const float4 x = *reinterpret_cast<const float4*>(v + i);
+      n += (x.x >= bar) + (x.y >= bar) + (x.z >= bar) + (x.w >= bar);
+    }
+    return __reduce_add_sync(kFullWarp, n);
+  };
+  float top = neg_inf();
+#pragma unroll 4
+  for (int i = lane * 4; i < padded; i += 128) {
+    const float4 x = *reinterpret_cast<const float4*>(v + i);
+    top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+  }
+  int before = 0;  // lanes whose maximum stands ahead of this one's
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    const float other = __shfl_sync(kFullWarp, top, j);
+    before += other > top || (other == top && j < lane);
+  }
+  const auto ranked = [&](int r) {  // the r-th largest of them (r from 0; -inf where a NaN is among them)
+    const uint32_t at = __ballot_sync(kFullWarp, before == r);
+    const float x = __shfl_sync(kFullWarp, top, at ? __ffs(at) - 1 : 0);
+    return at ? x : neg_inf();
+  };
+  const float best = ranked(0);
+  uint32_t hi = (order_key(best) >> shift) + 1;  // fewer than k reach it
+  uint32_t lo = order_key(ranked(min(k, 32) - 1)) >> shift;
+  float bar = bar_value(lo, shift);
+  int n = reach(bar);
+  for (float d = __fsub_rn(best, bar); n < k && bar > kLowest; d = __fadd_rn(d, d)) {
+    hi = lo;
+    const float next = __fsub_rn(bar, d);
+    lo = next < bar ? order_key(next) >> shift : 0u;  // (no step: d is 0 or lost against the bar)
+    bar = bar_value(lo, shift);
+    n = reach(bar);
+  }
+  if (n > most) {
+    while (n > most && hi > lo + 1) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      const int m = reach(bar_value(mid, shift));
+      if (m >= k) lo = mid, n = m;
+      else hi = mid;
+    }
+    bar = bar_value(lo, shift);
+    if (n > most) *ties = k - reach(bar_value(lo + 1, shift));
+  }
+  return bar;
+}
+
+// The places that choose_bar chose, in ascending order; how many there are (at most `most`).
+__device__ __forceinline__ int take_places(const float* v, int N, float bar, int ties, int* place, int most, int lane) {
+  int out = 0;
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i0 = 0; i0 < N; i0 += 32) {
+    const float x = i0 + lane < N ? v[i0 + lane] : neg_inf();
+    const uint32_t eq = __ballot_sync(kFullWarp, x == bar);
+    const bool take = x > bar || (x == bar && __popc(eq & below) < ties);
+    const uint32_t taken = __ballot_sync(kFullWarp, take);
+    const int at = out + __popc(taken & below);
+    if (take && at < most) place[at] = i0 + lane;
+    out += __popc(taken);
+    ties -= min(ties, __popc(eq));
+  }
+  return min(out, most);
+}
+
+struct ScoreArgs {
+  LogitRows in;
+  int32_t cluster;
+  const int64_t* y;
+  int32_t top_k;
+  float* logp;
+  int32_t* rank;
+  float* lse;
+  float* entropy;
+  int64_t* top_ids;
+  float* top_logp;
+};
+
+// Shared memory of the alternatives' search.
+struct TopSmem {
+  unsigned long long cand[CAND];   // order key in the high word, ~column in the low one
+  int place[PLACES];               // chosen groups
+  int octet[OCTETS];               // first columns of the chosen octets
+  int n_place, n_octet, n_cand, ties;
+  float bar, lse;
+};
+
+// Dynamic shared memory of a row. Where the cells are groups, the maxima of the chosen groups' octets
+// may take the place of the leaves' statistics and the cells, which have been used by then.
+__host__ __device__ constexpr size_t row_smem_bytes(int n, int top) {
+  const size_t b = leaves_of(n) * sizeof(Stats) + static_cast<size_t>(cell_room(n, top)) * 4;
+  const size_t octets = RLK_MAX_TOP_K * 32 * 4;
+  return top == TOP_GROUPS && b < octets ? octets : b;
+}
+
+// So many may reach a bar: with room above k, a bar is found in fewer steps.
+__device__ __forceinline__ int chosen_most(int k, int room) { return min(room, 2 * k + 16); }
+
+// The top_k alternatives of a row, by one CTA, from its cells' maxima and the bar that choose_bar found
+// for them.
+//  1. The k cells with the largest maxima (lower cell first among equals) hold the k best columns: a
+//     column outside them has k cells' maxima ahead of it. Chosen are they and some more that reach
+//     the bar, which k columns reach; of groups, the octets (8 columns) that reach it.
+//  2. The octets' columns that reach the bar are the candidates: little more than k, unless good
+//     columns crowd into few groups or are tied. If there are more than CAND of them, the same
+//     choice among the octets' maxima leaves 128 octets at most, and so no more than CAND.
+//  3. Each candidate's place is the number of candidates ahead of it (many are sorted instead).
+template <int TOP, class R, class E = typename R::E>
+__device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowSmem& sm, TopSmem& ts,
+                         bool bad, float lse) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int K = a.top_k, cells = cells_of(row.n, TOP);
+  const float bar = ts.bar;
+  const auto octet_max = [&](int c) {
+    return pack_max(packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c));
+  };
+  const auto collect = [&](float reached) {
+    for (int i = threadIdx.x; i < 8 * ts.n_octet; i += blockDim.x) {
+      const int c = ts.octet[i / 8] + i % 8;
+      const float z = c < row.n ? row.at(c) : neg_inf();
+      if (!(z >= reached)) continue;
+      const int at = atomicAdd(&ts.n_cand, 1);
+      if (at < CAND) ts.cand[at] = static_cast<unsigned long long>(order_key(z)) << 32 | static_cast<uint32_t>(~c);
+    }
+    __syncthreads();
+  };
+  // without ties at the bar, and with cells to choose among
+  bool many = !bad && (ts.ties < cells || (TOP == TOP_GROUPS && cells <= K));
+  if (!many && !bad) {
+    int* list = TOP == TOP_GROUPS ? ts.place : ts.octet;
+    int* count = TOP == TOP_GROUPS ? &ts.n_place : &ts.n_octet;
+    for (int i = threadIdx.x; i < cells; i += blockDim.x)
+      if (sm.cell[i] >= bar) {
+        const int at = atomicAdd(count, 1);
+        if (at < (TOP == TOP_GROUPS ? PLACES : OCTETS)) list[at] = TOP == TOP_GROUPS ? i : i * 8;
+      }
+    __syncthreads();
+    if constexpr (TOP == TOP_GROUPS) {
+      const int chosen = min(ts.n_place, PLACES);
+#pragma unroll 4
+      for (int i = warp; i < chosen; i += warps) {
+        const int c = ts.place[i] * LEAF_GROUP + lane * 8;
+        if (octet_max(c) >= bar) {
+          const int at = atomicAdd(&ts.n_octet, 1);
+          if (at < OCTETS) ts.octet[at] = c;
+        }
+      }
+      __syncthreads();
+    }
+    many = ts.n_octet > OCTETS;
+    if (!many) {
+      collect(bar);
+      many = ts.n_cand > CAND;
+    }
+  }
+  if (many) {  // the same for the whole CTA
+    const float* omax = sm.cell;
+    int N = cells;
+    if constexpr (TOP == TOP_GROUPS) {
+      if (warp == 0) {
+        int ties;
+        const float b = choose_bar(sm.cell, cells, K, RLK_MAX_TOP_K, E::kKeyShift, &ties, lane);
+        const int m = take_places(sm.cell, cells, b, ties, ts.place, RLK_MAX_TOP_K, lane);
+        if (lane == 0) ts.n_place = m;
+      }
+      __syncthreads();
+      float* o = reinterpret_cast<float*>(sm.leaf);
+      const int chosen = ts.n_place;
+      omax = o;
+      N = chosen * 32;
+      for (int i = warp; i < chosen; i += warps) o[i * 32 + lane] = octet_max(ts.place[i] * LEAF_GROUP + lane * 8);
+      for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) o[i] = neg_inf();
+      __syncthreads();
+    }
+    if (warp == 0) {
+      int ties;
+      const float b = choose_bar(omax, N, K, RLK_MAX_TOP_K, E::kKeyShift, &ties, lane);
+      const int m = take_places(omax, N, b, ties, ts.octet, RLK_MAX_TOP_K, lane);
+      __syncwarp();
+      for (int i = lane; i < m; i += 32) {
+        const int o = ts.octet[i];
+        ts.octet[i] = TOP == TOP_GROUPS ? ts.place[o / 32] * LEAF_GROUP + o % 32 * 8 : o * 8;
+      }
+      if (lane == 0) ts.bar = b, ts.n_octet = m, ts.n_cand = 0;
+    }
+    __syncthreads();
+    collect(ts.bar);
+  }
+  const int n = ts.n_cand;
+  int64_t* ids = a.top_ids + t * K;
+  float* lps = a.top_logp + t * K;
+  const auto put = [&](int place, unsigned long long c) {
+    ids[place] = static_cast<int64_t>(~static_cast<uint32_t>(c));
+    lps[place] = token_logp(key_value(static_cast<uint32_t>(c >> 32)), a.in.s, lse);
+  };
+  if ((n + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x) * n <= 1024) {  // a pass over the others for each
+    for (int i = threadIdx.x; i < n; i += blockDim.x) {
+      const unsigned long long me = ts.cand[i];
+      int place = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) place += ts.cand[j] > me;
+      if (place < K) put(place, me);
+    }
+  } else {  // for a small CTA, or many of them, a bitonic network over the next power of two is less (64 rows of
+            // 1000 with k = 100: 115 -> 31 us)
+    const int size = n <= 256 ? 256 : n <= 512 ? 512 : 1024;
+    static_assert(CAND == 1024, "the network's largest size");
+    for (int i = n + threadIdx.x; i < size; i += blockDim.x) ts.cand[i] = 0;
+    for (int run = 2; run <= size; run *= 2)
+      for (int d = run / 2; d >= 1; d /= 2) {
+        __syncthreads();
+        for (int i = threadIdx.x; i < size / 2; i += blockDim.x) {
+          const int x = 2 * i - (i & (d - 1)), y = x + d;  // i-th pair at distance d
+          const unsigned long long p = ts.cand[x], q = ts.cand[y];
+          if ((p < q) == ((x & run) == 0)) ts.cand[x] = q, ts.cand[y] = p;
+        }
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < min(n, K); i += blockDim.x) put(i, ts.cand[i]);
+  }
+  for (int i = n + threadIdx.x; i < K; i += blockDim.x) {
+    ids[i] = -1;
+    lps[i] = bad ? quiet_nan() : neg_inf();
+  }
+}
+
+// 64 registers a thread, whatever the number of threads: 1024 of them fill an SM.
+template <class E, int TOP, bool AL>
+__global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(const ScoreArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ int counts[MAX_ROW_WARPS];
+  __shared__ __align__(16) unsigned char top_raw[TOP ? sizeof(TopSmem) : 16];
+  TopSmem& ts = *reinterpret_cast<TopSmem*>(top_raw);
+  const LogitRows& in = a.in;
+  const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x / C;
+  const Row<E, AL> row(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n, in.err_flag);
+  const RowSmem sm{reinterpret_cast<Stats*>(dyn), reinterpret_cast<float*>(dyn + leaves_of(in.n) * sizeof(Stats)), counts};
+  if (TOP && r == 0) {
+    if (threadIdx.x == 0) ts.n_cand = ts.n_place = ts.n_octet = 0;
+    if (TOP == TOP_GROUPS)
+      for (int i = leaves_of(in.n) * LEAF_GROUPS + threadIdx.x; i < cell_room(in.n, TOP); i += blockDim.x) sm.cell[i] = neg_inf();
+  }
+  RankOf rank;
+  row_pass<true, TOP>(row, in.c, rank, sm, C, r, [&] { rank.load(row, a.y ? a.y + t : nullptr, a.rank != nullptr); });
+  if (r != 0) return;
+  if (warp == (blockDim.x > 32)) {
+    const Stats x = fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane);
+    const float lse = row_lse(x, in.s);
+    const bool bad = isnan(lse);
+    int before = 0;
+    if (rank.on)
+      for (int i = lane; i < C * static_cast<int>(blockDim.x >> 5); i += 32) before += counts[i];
+    before = __reduce_add_sync(kFullWarp, before);
+    if (lane == 0) {
+      if (TOP) ts.lse = lse;
+      if (a.lse) a.lse[t] = lse;
+      if (a.entropy) a.entropy[t] = row_entropy(x, in.s);
+      if (a.logp) a.logp[t] = rank.ok && !bad ? token_logp(rank.z, in.s, lse) : quiet_nan();
+      if (a.rank) a.rank[t] = rank.ok && !bad ? 1 + before : 0;
+      if (in.err_flag && bad) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
+      if (in.err_flag && a.y && !rank.ok) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
+    }
+  }
+  if constexpr (TOP) {
+    if (warp == 0) {
+      int ties;
+      const float b = choose_bar(sm.cell, cells_of(in.n, TOP), a.top_k, chosen_most(a.top_k, TOP == TOP_GROUPS ? PLACES : OCTETS),
+                                 E::kKeyShift, &ties, lane);
+      if (lane == 0) ts.bar = b, ts.ties = ties;
+    }
+    __syncthreads();
+    find_top<TOP>(row, a, t, sm, ts, isnan(ts.lse), ts.lse);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the gradient
+// ---------------------------------------------------------------------------
+struct TokenGradArgs {
+  LogitRows in;
+  GradOut out;
+  int32_t parts;     // CTAs of a row
+  const int64_t* y;
+  const float* lse;
+  const float* entropy;
+  const float* g_logp;
+  const float* g_entropy;
+};
+
+constexpr float kLowestLogp = -1e4f;  // p = 0 far above it, and B d stays a number
+
+// dz = p (A + B d), and p (A + B d) + C at the target, with d = s z - lse = log p. A masked column
+// (d = -inf) has p = 0 and a finite d.
+struct TokenDz {
+  float s, lse, A, B, C;
+  int y;
+  __device__ __forceinline__ float one(float z, int c) const {
+    const float d = fmaxf(__fmaf_rn(z, s, -lse), kLowestLogp);
+    const float p = prob_of(d), t = __fmaf_rn(B, d, A);
+    return c == y ? __fmaf_rn(p, t, C) : __fmul_rn(p, t);
+  }
+  template <class E>
+  __device__ __forceinline__ void pack(const Pack<E>& k, int c, float (&v)[8]) const {
+    const F32x2 ss = pack_f32x2(s, s), nl = pack_f32x2(-lse, -lse), le = pack_f32x2(kLog2e, kLog2e);
+    const F32x2 AA = pack_f32x2(A, A), BB = pack_f32x2(B, B);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 z = pair(k, i);
+      const float2 d = unpack_f32x2(fma2(pack_f32x2(z.x, z.y), ss, nl));
+      const F32x2 dd = pack_f32x2(fmaxf(d.x, kLowestLogp), fmaxf(d.y, kLowestLogp));
+      const float2 x = unpack_f32x2(mul2(dd, le));
+      const float2 r = unpack_f32x2(mul2(pack_f32x2(ex2_approx(x.x), ex2_approx(x.y)), fma2(BB, dd, AA)));
+      v[2 * i] = r.x;
+      v[2 * i + 1] = r.y;
+    }
+    if (static_cast<unsigned>(y - c) < 8u) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 z = pair(k, i);
+        if (y == c + 2 * i) v[2 * i] = one(z.x, y);
+        if (y == c + 2 * i + 1) v[2 * i + 1] = one(z.y, y);
+      }
+    }
+  }
+};
+
+template <class E, class O, bool AL>
+__global__ void __launch_bounds__(ROW_THREADS) token_grad_kernel(const TokenGradArgs a) {
+  const LogitRows& in = a.in;
+  const int64_t t = blockIdx.x / a.parts;
+  const GradPart<E, O, AL> part(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n,
+                                static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
+                                static_cast<int>(blockIdx.x % a.parts), a.parts, in.err_flag);
+  const float lse = a.lse[t], g = a.g_logp[t], ge = a.g_entropy ? a.g_entropy[t] : 0.f;
+  const float ent = a.g_entropy ? a.entropy[t] : 0.f;
+  const int64_t y = a.y[t];
+  const bool y_ok = y >= 0 && y < in.n;
+  if (!y_ok && threadIdx.x == 0 && part.lo == 0 && in.err_flag) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
+  const bool live = y_ok && !isnan(lse) && lse != neg_inf() && !(g == 0.f && ge == 0.f);
+  const TokenDz dz{in.s, lse, __fmul_rn(-in.s, __fmaf_rn(ge, ent, g)), __fmul_rn(-in.s, ge), __fmul_rn(in.s, g),
+                   static_cast<int>(y)};
+  write_part<GRAD_PACKS>(part, live, dz, [] {});  // every thread reads and writes columns of its own
+}
+
+}  // namespace
+}  // namespace rlk
+
+using namespace rlk;
+
+extern "C" {
+
+rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
+                              double temperature, const int64_t* y, int32_t top_k, float* logp, int32_t* rank,
+                              float* lse, float* entropy, int64_t* top_ids, float* top_logp, int32_t* err_flag,
+                              void* stream) {
+  ScoreArgs a{};
+  const rlk_status st = check_logits(logits, dtype, T, ld, V_true, temperature, err_flag, &a.in);
+  if (st != RLK_OK) return st;
+  if (top_k < 0 || (T > 0 && !y && (logp || rank))) return RLK_ERR_INVALID_ARG;
+  if (top_k > RLK_MAX_TOP_K) return RLK_ERR_UNSUPPORTED;
+  if (T > 0 && top_k > 0 && (!top_ids || !top_logp)) return RLK_ERR_INVALID_ARG;
+  if (T == 0) return RLK_OK;
+  a.y = y;
+  a.top_k = top_k;
+  a.logp = logp;
+  a.rank = rank;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logp = top_logp;
+  const RowShape shape = row_shape(a.in, top_k);
+  a.cluster = shape.cluster;
+  return with_types(dtype, aligned_rows(logits, ld, dtype_bytes(dtype)), [&](auto e, auto al) {
+    using E = decltype(e);
+    constexpr bool AL = decltype(al)::value;
+    const int top = top_k == 0 ? TOP_NONE : V_true <= SHORT_ROW ? TOP_OCTETS : TOP_GROUPS;
+    const auto kernel = top == TOP_NONE     ? token_logprobs_kernel<E, TOP_NONE, AL>
+                        : top == TOP_OCTETS ? token_logprobs_kernel<E, TOP_OCTETS, AL>
+                                            : token_logprobs_kernel<E, TOP_GROUPS, AL>;
+    return launch_rows(kernel, a, T * a.cluster, a.cluster, row_smem_bytes(a.in.n, top), stream, shape.threads);
+  });
+}
+
+rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld, int64_t V_true,
+                                  double temperature, const int64_t* y, const float* lse, const float* entropy,
+                                  const float* g_logp, const float* g_entropy, void* dlogits, int32_t out_dtype,
+                                  int64_t V, int64_t out_ld, int32_t* err_flag, void* stream) {
+  TokenGradArgs a{};
+  rlk_status st = check_logits(logits, dtype, T, ld, V_true, temperature, err_flag, &a.in);
+  if (st == RLK_OK) st = check_out(a.in, dtype, dlogits, out_dtype, V, out_ld, &a.out);
+  if (st != RLK_OK) return st;
+  if (T > 0 && (!y || !lse || !g_logp || (g_entropy && !entropy))) return RLK_ERR_INVALID_ARG;
+  if (T == 0) return RLK_OK;
+  a.y = y;
+  a.lse = lse;
+  a.entropy = entropy;
+  a.g_logp = g_logp;
+  a.g_entropy = g_entropy;
+  a.parts = grad_parts(a.in, a.out);
+  if (T * a.parts > INT32_MAX) return RLK_ERR_UNSUPPORTED;
+  return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto al) {
+    return launch_rows(token_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, T * a.parts, 1, 0, stream);
+  });
+}
+
+}  // extern "C"
