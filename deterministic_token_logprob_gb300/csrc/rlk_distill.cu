@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const Distill
   if (q.bad && part.lo == 0 && threadIdx.x == 0 && in.err_flag) atomicOr(in.err_flag, q.bad);
   const bool live = distill_live(q, lse, g);
   const float A = __fmul_rn(in.s, g);
-  write_part<GRAD_PACKS>(part, live, DistillDz{in.s, lse, A}, [] {});
+  write_part<GRAD_PACKS>(part, live, DistillDz{in.s, lse, A});
   __syncthreads();
   if (!live) return;
   for (int k = threadIdx.x; k < a.K; k += ROW_THREADS) {

@@ -60,14 +60,12 @@ __device__ __forceinline__ void store_pack(typename O::bits* p, const float (&v)
 }
 
 // Writes f(z, column) for the part's columns (0 past the row's n columns, and everywhere when !live,
-// without reading). Each thread has U packs in flight; `first` runs in every thread between the
-// first loads and the first store.
-template <int U, class G, class F, class B>
-__device__ __forceinline__ void write_part(const G& g, bool live, F f, B first) {
+// without reading). Each thread has U packs in flight.
+template <int U, class G, class F>
+__device__ __forceinline__ void write_part(const G& g, bool live, const F& f) {
   using E = typename G::E;
   using O = typename G::O;
   const int tid = threadIdx.x, threads = blockDim.x;
-  bool begun = false;
   const auto put_pack = [&](const Pack<E>& k, int c) {
     float v[8];
     f.pack(k, g.head + c, v);
@@ -78,7 +76,13 @@ __device__ __forceinline__ void write_part(const G& g, bool live, F f, B first) 
     }
     if (dbg_ok(g.head + c + 8 <= g.V, g.in.err)) store_pack<O>(g.out + g.head + c, v);
   };
-  for (int q = g.q0; !begun || q < g.q1; q += U * threads) {
+  // the columns outside the packs: before the head and after the last pack
+  if (tid < 16) {
+    const int c = tid < 8 ? tid : g.head + 8 * g.packs + tid - 8;
+    if (g.owns(c) && (tid >= 8 || c < g.head))
+      g.put(c, live && c < g.n ? f.one(E::to_f32(g.in.p[c - g.head]), c) : 0.f);
+  }
+  for (int q = g.q0; q < g.q1; q += U * threads) {
     Pack<E> k[U];
     const bool full = live && q + U * threads <= g.q1 && packs_inside(g.in, q * 8, (q + U * threads) * 8);
     if (full) {
@@ -89,17 +93,6 @@ __device__ __forceinline__ void write_part(const G& g, bool live, F f, B first) 
       for (int u = 0; u < U; ++u) {
         const int p = q + tid + u * threads;
         if (p < g.q1) k[u] = packs_inside(g.in, p * 8, p * 8 + 8) ? load_pack(g.in, p * 8) : load_pack_edge(g.in, p * 8);
-      }
-    }
-    if (!begun) {
-      begun = true;
-      first();
-      // the columns outside the packs: before the head and after the last pack
-      const int tail0 = g.head + 8 * g.packs;
-      if (tid < 16) {
-        const int c = tid < 8 ? tid : tail0 + tid - 8;
-        if (g.owns(c) && (tid >= 8 || c < g.head))
-          g.put(c, live && c < g.n ? f.one(E::to_f32(g.in.p[c - g.head]), c) : 0.f);
       }
     }
     if (full) {

@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(ROW_THREADS) token_grad_kernel(const TokenGrad
   const bool live = y_ok && !isnan(lse) && lse != neg_inf() && !(g == 0.f && ge == 0.f);
   const TokenDz dz{in.s, lse, __fmul_rn(-in.s, __fmaf_rn(ge, ent, g)), __fmul_rn(-in.s, ge), __fmul_rn(in.s, g),
                    static_cast<int>(y)};
-  write_part<GRAD_PACKS>(part, live, dz, [] {});  // every thread reads and writes columns of its own
+  write_part<GRAD_PACKS>(part, live, dz);  // every thread reads and writes columns of its own
 }
 
 }  // namespace
