@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const Disti
   }
   RowSmem sm{reinterpret_cast<Stats*>(dyn), nullptr, nullptr};
   RankOf none;
-  row_pass<false, TOP_NONE>(row, in.c, none, sm, C, r, [] {});
+  row_pass<false, false>(row, in.c, none, sm, C, r, [] {});
   if (r == 0 && warp == 0) put_loss(a, t, q, zk, row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s), lane);
 }
 
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
     Pack<E> k[LEAF_GROUPS];
 #pragma unroll
     for (int u = 0; u < LEAF_GROUPS; ++u) k[u] = load_pack(view, u * LEAF_GROUP + lane * 8);
-    leaf_pass<false, TOP_NONE>(k, r + i * C, in.c, RankOf{}, to, 0u, lane < C, lane);
+    leaf_pass<false, false>(k, r + i * C, in.c, RankOf{}, to, 0u, lane < C, lane);
   }
   if (C > 1) cluster_sync();
   else __syncthreads();
@@ -468,7 +468,7 @@ rlk_status launch_step(DistillArgs a, void* stream) {
   }
   const int share = (L + a.cluster - 1) / a.cluster, most = STEP_THREADS / 32 - 1;
   const int threads = 32 * ((share < most ? share : most) + 1);
-  return launch_rows(kernel, a, static_cast<int64_t>(a.in.T) * a.cluster, a.cluster, smem, stream, threads);
+  return launch_rows(kernel, a, static_cast<int64_t>(a.in.T) * a.cluster, a.cluster, smem, stream, threads, false);
 }
 
 }  // namespace

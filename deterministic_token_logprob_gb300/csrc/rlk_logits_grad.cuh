@@ -114,10 +114,9 @@ __device__ __forceinline__ void write_part(const G& g, bool live, const F& f) {
   }
 }
 
-// CTAs of a row in a kernel that writes gradients alone.
-// Parts of up to four rounds of every thread's packs (the work that
-// a CTA does once -- its row's scalars, the teacher's softmax -- is then small: 8192 rows of 151936
-// in bf16 take 715 us with four rounds, 954 with one), as long as that leaves CTAs enough for the GPU.
+// CTAs of a row in a kernel that writes gradients alone: parts of up to four rounds of every thread's
+// packs (what a CTA does once -- its row's scalars, the teacher's softmax -- is then small: 8192 rows of
+// 151936 in bf16 take 715 us with four rounds, 954 with one), as long as that leaves the GPU full.
 inline int grad_parts(const LogitRows& in, const GradOut& o) {
   constexpr int kCols = 8 * GRAD_PACKS * ROW_THREADS;
   constexpr int64_t kEnough = 6 * 152;
@@ -128,8 +127,8 @@ inline int grad_parts(const LogitRows& in, const GradOut& o) {
 }
 
 // dlogits: the logits' type, or bf16 for fp32 logits
-inline rlk_status check_out(const LogitRows& in, int32_t dtype, void* dlogits, int32_t out_dtype, int64_t V, int64_t out_ld,
-                     GradOut* o) {
+inline rlk_status check_out(const LogitRows& in, int32_t dtype, void* dlogits, int32_t out_dtype, int64_t V,
+                            int64_t out_ld, GradOut* o) {
   const int eb = dtype_bytes(out_dtype);
   if (eb == 0 || V < in.n || out_ld < V) return RLK_ERR_INVALID_ARG;
   if (out_dtype != dtype && !(dtype == RLK_DTYPE_F32 && out_dtype == RLK_DTYPE_BF16)) return RLK_ERR_UNSUPPORTED;

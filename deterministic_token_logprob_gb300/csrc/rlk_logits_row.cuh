@@ -13,30 +13,22 @@ constexpr int MAX_CLUSTER = 8;                               // CTAs of one row 
 constexpr int MAX_ROW_THREADS = 1024;
 constexpr int MAX_ROW_WARPS = MAX_CLUSTER * MAX_ROW_THREADS / 32;
 
-// The units in which the pass keeps maxima for the alternatives' search: groups of 256 columns (four
-// a leaf), or in short rows octets, the packs themselves.
-enum TopCells : int { TOP_NONE = 0, TOP_GROUPS = 1, TOP_OCTETS = 2 };
-
 // ---------------------------------------------------------------------------
 // one pass over a row by a cluster of CTAs (one CTA when there are rows enough)
 // ---------------------------------------------------------------------------
 // Warp g of the row's C x (blockDim / 32) warps takes leaves g, g + (number of warps), ... and
 // leaves what it found in the shared memory of the cluster's CTA 0 (distributed shared memory):
-// (m, s, u) of each leaf, the maxima of its cells (TOP), and how many columns stand ahead of the
-// target.
+// (m, s, u) of each leaf, the maxima of its 32 cells (TOP: a cell is the 32 columns that a lane
+// holds, so its maximum costs nothing), and how many columns stand ahead of the target.
 struct RowSmem {
   Stats* leaf;      // [n_leaves]
-  float* cell;      // [cell_room(n, TOP)]
+  float* cell;      // [cell_room(n)]
   int* count;       // [MAX_ROW_WARPS]
 };
 
 __host__ __device__ constexpr int leaves_of(int n) { return (n + ROW_LEAF - 1) / ROW_LEAF; }
-__host__ __device__ constexpr int cells_of(int n, int top) {
-  return top == TOP_OCTETS ? (n + 7) / 8 : (n + LEAF_GROUP - 1) / LEAF_GROUP;
-}
-__host__ __device__ constexpr int cell_room(int n, int top) {  // whole leaves, a multiple of 128
-  return top == TOP_NONE ? 0 : top == TOP_OCTETS ? leaves_of(n) * 128 : (leaves_of(n) * LEAF_GROUPS + 127) / 128 * 128;
-}
+__host__ __device__ constexpr int cells_of(int n) { return leaves_of(n) * 32; }
+__host__ __device__ constexpr int cell_room(int n) { return (cells_of(n) + 127) / 128 * 128; }
 
 // The target of a row.
 struct RankOf {
@@ -106,25 +98,17 @@ __device__ __forceinline__ int count_ahead(const Pack<E> (&k)[LEAF_GROUPS], cons
 // What one leaf leaves behind (see RowSmem), at leaf0 / cell0 of the cluster's shared memory, from
 // each lane that `puts` (lane 0 alone with ENT: the others lack u). Returns how many of the lane's
 // columns stand ahead of the target.
-template <bool ENT, int TOP, class E>
+template <bool ENT, bool TOP, class E>
 __device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l, float c, const RankOf& rank,
                                          uint32_t leaf0, uint32_t cell0, bool puts, int lane) {
-  float gm[LEAF_GROUPS], m;
-#pragma unroll
-  for (int j = 0; j < LEAF_GROUPS; ++j) {
-    gm[j] = pack_max(k[j]);
-    if constexpr (TOP == TOP_OCTETS)
-      st_cluster_u32(cell0 + static_cast<uint32_t>((l * LEAF_GROUPS + j) * 32 + lane) * 4, __float_as_uint(gm[j]));
-    if constexpr (TOP == TOP_GROUPS) gm[j] = warp_max(gm[j]);
-  }
-  m = fmaxf(fmaxf(gm[0], gm[1]), fmaxf(gm[2], gm[3]));
-  if constexpr (TOP != TOP_GROUPS) m = warp_max(m);
+  float m = fmaxf(fmaxf(pack_max(k[0]), pack_max(k[1])), fmaxf(pack_max(k[2]), pack_max(k[3])));
+  if constexpr (TOP) st_cluster_u32(cell0 + static_cast<uint32_t>(l * 32 + lane) * 4, __float_as_uint(m));
+  m = warp_max(m);
   float2 x;
   if (m == neg_inf()) x = make_float2(any_nan(k) ? quiet_nan() : 0.f, 0.f);
   else x = leaf_sums<ENT>(k, m, c, lane);
   if (puts) {
     st_cluster_f32x4(leaf0 + static_cast<uint32_t>(l * 16), m, x.x, x.y, 0.f);
-    if (TOP == TOP_GROUPS) st_cluster_f32x4(cell0 + static_cast<uint32_t>(l * 16), gm[0], gm[1], gm[2], gm[3]);
   }
   // a leaf whose best column is below the target has none ahead of it: for a likely token, most
   return rank.on && m >= rank.z ? count_ahead(k, rank, l, lane) : 0;
@@ -142,7 +126,7 @@ __device__ __forceinline__ void prefetch_leaf(const R& row, int l) {
 }
 
 // `begin` runs in every thread after the first loads have been issued: what it loads arrives with them.
-template <bool ENT, int TOP, class R, class B, class E = typename R::E>
+template <bool ENT, bool TOP, class R, class B, class E = typename R::E>
 __device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, const RowSmem& sm, int C, int r, B begin) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5, g = r * warps + warp, n_leaves = leaves_of(row.n), step = C * warps;
@@ -216,7 +200,7 @@ inline RowShape row_shape(const LogitRows& in, int top_k) {
 // Launches `ctas` CTAs in clusters of `cluster`.
 template <class K, class A>
 inline rlk_status launch_rows(K kernel, const A& args, int64_t ctas, int cluster, size_t smem, void* stream,
-                       int threads = ROW_THREADS) {
+                              int threads = ROW_THREADS, bool opt_in = true) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
@@ -228,6 +212,11 @@ inline rlk_status launch_rows(K kernel, const A& args, int64_t ctas, int cluster
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 1 ? 1 : 0;
+  // beyond what any kernel may have without asking (its static part takes up to 14 KB of 48): rows of
+  // more than about 230,000 columns, with alternatives
+  if (smem > (32 << 10) && opt_in &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return RLK_ERR_CUDA;
   if (cudaLaunchKernelEx(&cfg, kernel, args) != cudaSuccess) return RLK_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
 }

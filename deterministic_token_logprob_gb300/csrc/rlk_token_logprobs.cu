@@ -7,10 +7,9 @@
 namespace rlk {
 namespace {
 
-constexpr int SHORT_ROW = 32768;                             // columns up to which the cells are octets
-constexpr int CAND = 8 * RLK_MAX_TOP_K;                      // most candidates: 8 columns of each chosen octet
-constexpr int PLACES = 2 * RLK_MAX_TOP_K;                    // most groups at the first attempt
-constexpr int OCTETS = 4 * RLK_MAX_TOP_K;                    // most octets at the first attempt
+constexpr int CAND = 8 * RLK_MAX_TOP_K;     // most candidates: 8 columns of each of 128 octets
+constexpr int PLACES = 2 * RLK_MAX_TOP_K;   // most cells at the first attempt
+constexpr int OCTETS = 4 * RLK_MAX_TOP_K;   // most octets at the first attempt
 
 // ---------------------------------------------------------------------------
 // the best of N values, by one warp
@@ -23,14 +22,16 @@ __device__ __forceinline__ float bar_value(uint32_t bar, int shift) {
   return key <= order_key(neg_inf()) ? -3.4028235e38f : key_value(key);
 }
 
-// A bar that the k best of v[0 .. N) reach and at most `most` of them, -inf never (all that are not
-// -inf reach the lowest finite value, the bar for N <= k). v is padded with -inf to a multiple of 128.
+// A bar that the k best of N values reach and at most `most` of them, -inf never (all that are not
+// -inf reach the lowest finite value, the bar for N <= k). get(i) gives values i .. i + 3 (i a multiple
+// of 4), -inf from N up to the next multiple of 128.
 // The first try is the k-th of the 32 lanes' maxima, or for k > 32 steps down from the least of them,
 // doubled until k values reach it; where more than `most` do, bisection raises it on the values' order
 // keys, which hold nothing in their low `shift` bits, counting the values at or above the middle.
 // *ties: how many of those equal to the bar are to be taken, lower places first -- all of them, unless
 // ties stand in the way of any such bar.
-__device__ __forceinline__ float choose_bar(const float* v, int N, int k, int most, int shift, int* ties, int lane) {
+template <class G>
+__device__ __forceinline__ float choose_bar(const G& get, int N, int k, int most, int shift, int* ties, int lane) {
   constexpr float kLowest = -3.4028235e38f;
   *ties = N;
   if (N <= k) return kLowest;
@@ -39,16 +40,23 @@ __device__ __forceinline__ float choose_bar(const float* v, int N, int k, int mo
     int n = 0;
 #pragma unroll 4
     for (int i = lane * 4; i < padded; i += 128) {
-      const float4 x = *reinterpret_cast<const float4*>(v + i);
+      const float4 x = get(i);
       n += (x.x >= bar) + (x.y >= bar) + (x.z >= bar) + (x.w >= bar);
     }
     return __reduce_add_sync(kFullWarp, n);
   };
   float top = neg_inf();
+  if (N <= 256) {  // few values: every lane its share of them
+    for (int i = lane; i < N; i += 32) {
+      const float4 x = get(i & ~3);
+      top = fmaxf(top, i & 2 ? (i & 1 ? x.w : x.z) : (i & 1 ? x.y : x.x));
+    }
+  } else {
 #pragma unroll 4
-  for (int i = lane * 4; i < padded; i += 128) {
-    const float4 x = *reinterpret_cast<const float4*>(v + i);
-    top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+    for (int i = lane * 4; i < padded; i += 128) {
+      const float4 x = get(i);
+      top = fmaxf(fmaxf(top, fmaxf(x.x, x.y)), fmaxf(x.z, x.w));
+    }
   }
   int before = 0;  // lanes whose maximum stands ahead of this one's
 #pragma unroll
@@ -119,37 +127,38 @@ struct ScoreArgs {
 // Shared memory of the alternatives' search.
 struct TopSmem {
   unsigned long long cand[CAND];   // order key in the high word, ~column in the low one
-  int place[PLACES];               // chosen groups
+  int place[PLACES];               // chosen cells (groups at the second attempt)
   int octet[OCTETS];               // first columns of the chosen octets
-  int n_place, n_octet, n_cand, ties;
+  int n_place, n_octet, n_cand;
   float bar, lse;
 };
 
-// Dynamic shared memory of a row. Where the cells are groups, the maxima of the chosen groups' octets
-// may take the place of the leaves' statistics and the cells, which have been used by then.
-__host__ __device__ constexpr size_t row_smem_bytes(int n, int top) {
-  const size_t b = leaves_of(n) * sizeof(Stats) + static_cast<size_t>(cell_room(n, top)) * 4;
-  const size_t octets = RLK_MAX_TOP_K * 32 * 4;
-  return top == TOP_GROUPS && b < octets ? octets : b;
+// Dynamic shared memory of a row: leaves and cells, or in their place, once they have been used, the
+// maxima of the groups (256 columns) and of the octets of 128 groups.
+__host__ __device__ constexpr int groups_of(int n) { return (n + LEAF_GROUP - 1) / LEAF_GROUP; }
+__host__ __device__ constexpr int group_room(int n) { return (groups_of(n) + 127) / 128 * 128; }
+__host__ __device__ constexpr size_t row_smem_bytes(int n, bool top) {
+  const size_t b = leaves_of(n) * sizeof(Stats);
+  if (!top) return b;
+  const size_t first = b + cell_room(n) * 4;
+  const size_t exact = group_room(n) * 4 + (groups_of(n) < RLK_MAX_TOP_K ? (groups_of(n) + 3) / 4 * 4 : RLK_MAX_TOP_K) * 32 * 4;
+  return first > exact ? first : exact;
 }
 
-// So many may reach a bar: with room above k, a bar is found in fewer steps.
-__device__ __forceinline__ int chosen_most(int k, int room) { return min(room, 2 * k + 16); }
-
-// The top_k alternatives of a row, by one CTA, from its cells' maxima and the bar that choose_bar found
-// for them.
-//  1. The k cells with the largest maxima (lower cell first among equals) hold the k best columns: a
-//     column outside them has k cells' maxima ahead of it. Chosen are they and some more that reach
-//     the bar, which k columns reach; of groups, the octets (8 columns) that reach it.
-//  2. The octets' columns that reach the bar are the candidates: little more than k, unless good
-//     columns crowd into few groups or are tied. If there are more than CAND of them, the same
-//     choice among the octets' maxima leaves 128 octets at most, and so no more than CAND.
-//  3. Each candidate's place is the number of candidates ahead of it (many are sorted instead).
-template <int TOP, class R, class E = typename R::E>
-__device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowSmem& sm, TopSmem& ts,
+// The top_k alternatives of a row, by one CTA, from its cells' maxima and a bar that k of them reach.
+//  1. The k best columns reach the bar, so they stand in cells that reach it, and there in octets (8
+//     consecutive columns) that do. In a short row the octets' own maxima give a higher bar.
+//  2. The octets' columns that reach the bar are the candidates: little more than k.
+//  3. If there are too many on the way (good columns crowd into few cells, or ties stand at the bar), the
+//     row is gone through once more for its groups of 256 columns: the k groups with the largest maxima
+//     (lower group first among equals) hold the k best columns, for a column outside them has k
+//     groups' maxima ahead of it; and so do the k best of those groups' octets.
+//  4. Each candidate's place is the number of candidates ahead of it (many are sorted instead).
+template <class R, class E = typename R::E>
+__device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, unsigned char* dyn, const float* cell, TopSmem& ts,
                          bool bad, float lse) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  const int K = a.top_k, cells = cells_of(row.n, TOP);
+  const int K = a.top_k, cells = cells_of(row.n);
   const float bar = ts.bar;
   const auto octet_max = [&](int c) {
     return pack_max(packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c));
@@ -164,64 +173,85 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowS
     }
     __syncthreads();
   };
-  // without ties at the bar, and with cells to choose among
-  bool many = !bad && (ts.ties < cells || (TOP == TOP_GROUPS && cells <= K));
-  if (!many && !bad) {
-    int* list = TOP == TOP_GROUPS ? ts.place : ts.octet;
-    int* count = TOP == TOP_GROUPS ? &ts.n_place : &ts.n_octet;
+  bool many = false;
+  if (!bad) {
     for (int i = threadIdx.x; i < cells; i += blockDim.x)
-      if (sm.cell[i] >= bar) {
-        const int at = atomicAdd(count, 1);
-        if (at < (TOP == TOP_GROUPS ? PLACES : OCTETS)) list[at] = TOP == TOP_GROUPS ? i : i * 8;
+      if (cell[i] >= bar) {
+        const int at = atomicAdd(&ts.n_place, 1);
+        if (at < PLACES) ts.place[at] = i;
       }
     __syncthreads();
-    if constexpr (TOP == TOP_GROUPS) {
-      const int chosen = min(ts.n_place, PLACES);
-#pragma unroll 4
-      for (int i = warp; i < chosen; i += warps) {
-        const int c = ts.place[i] * LEAF_GROUP + lane * 8;
-        if (octet_max(c) >= bar) {
-          const int at = atomicAdd(&ts.n_octet, 1);
-          if (at < OCTETS) ts.octet[at] = c;
-        }
+    many = ts.n_place > PLACES;
+  }
+  if (!many && !bad) {
+    const int octets = LEAF_GROUPS * ts.n_place;
+    const auto column_of = [&](int i) {
+      const int x = ts.place[i / LEAF_GROUPS];
+      return x / 32 * ROW_LEAF + i % LEAF_GROUPS * LEAF_GROUP + x % 32 * 8;
+    };
+    const auto list = [&](int c) {
+      const int at = atomicAdd(&ts.n_octet, 1);
+      if (at < OCTETS) ts.octet[at] = c;
+    };
+    if (cells >= 3 * K) {
+      for (int i = threadIdx.x; i < octets; i += blockDim.x) {
+        const int c = column_of(i);
+        if (octet_max(c) >= bar) list(c);
+      }
+    } else {  // few cells against k: the bar is low, and the octets raise it
+      float* omax = reinterpret_cast<float*>(ts.cand);  // not yet in use
+      static_assert(LEAF_GROUPS * PLACES * sizeof(float) <= sizeof(ts.cand), "room for the octets' maxima");
+      for (int i = threadIdx.x; i < (octets + 127) / 128 * 128; i += blockDim.x)
+        omax[i] = i < octets ? octet_max(column_of(i)) : neg_inf();
+      __syncthreads();
+      if (warp == 0) {
+        int ties;
+        const auto get = [&](int i) { return *reinterpret_cast<const float4*>(omax + i); };
+        const float b = choose_bar(get, octets, K, min(OCTETS, K + K / 2 + 16), E::kKeyShift, &ties, lane);
+        if (lane == 0) ts.bar = b;
       }
       __syncthreads();
+      for (int i = threadIdx.x; i < octets; i += blockDim.x)
+        if (omax[i] >= ts.bar) list(column_of(i));
     }
+    __syncthreads();
     many = ts.n_octet > OCTETS;
     if (!many) {
-      collect(bar);
+      collect(ts.bar);
       many = ts.n_cand > CAND;
     }
   }
   if (many) {  // the same for the whole CTA
-    const float* omax = sm.cell;
-    int N = cells;
-    if constexpr (TOP == TOP_GROUPS) {
-      if (warp == 0) {
-        int ties;
-        const float b = choose_bar(sm.cell, cells, K, RLK_MAX_TOP_K, E::kKeyShift, &ties, lane);
-        const int m = take_places(sm.cell, cells, b, ties, ts.place, RLK_MAX_TOP_K, lane);
-        if (lane == 0) ts.n_place = m;
-      }
-      __syncthreads();
-      float* o = reinterpret_cast<float*>(sm.leaf);
-      const int chosen = ts.n_place;
-      omax = o;
-      N = chosen * 32;
-      for (int i = warp; i < chosen; i += warps) o[i * 32 + lane] = octet_max(ts.place[i] * LEAF_GROUP + lane * 8);
-      for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) o[i] = neg_inf();
-      __syncthreads();
-    }
-    if (warp == 0) {
+    __syncthreads();  // cells and leaves have been read, the counts too
+    const int groups = groups_of(row.n);
+    float* gmax = reinterpret_cast<float*>(dyn);
+    float* omax = gmax + group_room(row.n);
+    const auto best_of = [&](const float* v, int N, int* place) {
       int ties;
-      const float b = choose_bar(omax, N, K, RLK_MAX_TOP_K, E::kKeyShift, &ties, lane);
-      const int m = take_places(omax, N, b, ties, ts.octet, RLK_MAX_TOP_K, lane);
+      const auto get = [&](int i) { return *reinterpret_cast<const float4*>(v + i); };
+      const float b = choose_bar(get, N, K, RLK_MAX_TOP_K, E::kKeyShift, &ties, lane);
+      if (lane == 0) ts.bar = b;
+      return take_places(v, N, b, ties, place, RLK_MAX_TOP_K, lane);
+    };
+    for (int g = warp; g < group_room(row.n); g += warps) {
+      const float m = g < groups ? warp_max(octet_max(g * LEAF_GROUP + lane * 8)) : neg_inf();
+      if (lane == 0) gmax[g] = m;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const int m = best_of(gmax, groups, ts.place);
+      if (lane == 0) ts.n_place = m;
+    }
+    __syncthreads();
+    const int chosen = ts.n_place, N = chosen * 32;
+    for (int i = warp; i < chosen; i += warps) omax[i * 32 + lane] = octet_max(ts.place[i] * LEAF_GROUP + lane * 8);
+    for (int i = N + threadIdx.x; i < (N + 127) / 128 * 128; i += blockDim.x) omax[i] = neg_inf();
+    __syncthreads();
+    if (warp == 0) {
+      const int m = best_of(omax, N, ts.octet);
       __syncwarp();
-      for (int i = lane; i < m; i += 32) {
-        const int o = ts.octet[i];
-        ts.octet[i] = TOP == TOP_GROUPS ? ts.place[o / 32] * LEAF_GROUP + o % 32 * 8 : o * 8;
-      }
-      if (lane == 0) ts.bar = b, ts.n_octet = m, ts.n_cand = 0;
+      for (int i = lane; i < m; i += 32) ts.octet[i] = ts.place[ts.octet[i] / 32] * LEAF_GROUP + ts.octet[i] % 32 * 8;
+      if (lane == 0) ts.n_octet = m, ts.n_cand = 0;
     }
     __syncthreads();
     collect(ts.bar);
@@ -265,7 +295,7 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, const RowS
 }
 
 // 64 registers a thread, whatever the number of threads: 1024 of them fill an SM.
-template <class E, int TOP, bool AL>
+template <class E, bool TOP, bool AL>
 __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(const ScoreArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ int counts[MAX_ROW_WARPS];
@@ -278,8 +308,7 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(cons
   const RowSmem sm{reinterpret_cast<Stats*>(dyn), reinterpret_cast<float*>(dyn + leaves_of(in.n) * sizeof(Stats)), counts};
   if (TOP && r == 0) {
     if (threadIdx.x == 0) ts.n_cand = ts.n_place = ts.n_octet = 0;
-    if (TOP == TOP_GROUPS)
-      for (int i = leaves_of(in.n) * LEAF_GROUPS + threadIdx.x; i < cell_room(in.n, TOP); i += blockDim.x) sm.cell[i] = neg_inf();
+    for (int i = cells_of(in.n) + threadIdx.x; i < cell_room(in.n); i += blockDim.x) sm.cell[i] = neg_inf();
   }
   RankOf rank;
   row_pass<true, TOP>(row, in.c, rank, sm, C, r, [&] { rank.load(row, a.y ? a.y + t : nullptr, a.rank != nullptr); });
@@ -304,13 +333,24 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(cons
   }
   if constexpr (TOP) {
     if (warp == 0) {
+      // from the leaves' maxima where they are many against k, else from the cells'
+      const int L = leaves_of(in.n), K = a.top_k;
       int ties;
-      const float b = choose_bar(sm.cell, cells_of(in.n, TOP), a.top_k, chosen_most(a.top_k, TOP == TOP_GROUPS ? PLACES : OCTETS),
-                                 E::kKeyShift, &ties, lane);
-      if (lane == 0) ts.bar = b, ts.ties = ties;
+      float b;
+      if (L >= 2 * K && L >= 32) {
+        const auto get = [&](int i) {
+          const auto at = [&](int j) { return j < L ? sm.leaf[j].m : neg_inf(); };
+          return make_float4(at(i), at(i + 1), at(i + 2), at(i + 3));
+        };
+        b = choose_bar(get, L, K, K + 16, E::kKeyShift, &ties, lane);
+      } else {
+        const auto get = [&](int i) { return *reinterpret_cast<const float4*>(sm.cell + i); };
+        b = choose_bar(get, cells_of(in.n), K, min(PLACES, 2 * K + 16), E::kKeyShift, &ties, lane);
+      }
+      if (lane == 0) ts.bar = b;
     }
     __syncthreads();
-    find_top<TOP>(row, a, t, sm, ts, isnan(ts.lse), ts.lse);
+    find_top(row, a, t, dyn, sm.cell, ts, isnan(ts.lse), ts.lse);
   }
 }
 
@@ -414,11 +454,9 @@ rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
   return with_types(dtype, aligned_rows(logits, ld, dtype_bytes(dtype)), [&](auto e, auto al) {
     using E = decltype(e);
     constexpr bool AL = decltype(al)::value;
-    const int top = top_k == 0 ? TOP_NONE : V_true <= SHORT_ROW ? TOP_OCTETS : TOP_GROUPS;
-    const auto kernel = top == TOP_NONE     ? token_logprobs_kernel<E, TOP_NONE, AL>
-                        : top == TOP_OCTETS ? token_logprobs_kernel<E, TOP_OCTETS, AL>
-                                            : token_logprobs_kernel<E, TOP_GROUPS, AL>;
-    return launch_rows(kernel, a, T * a.cluster, a.cluster, row_smem_bytes(a.in.n, top), stream, shape.threads);
+    const size_t smem = row_smem_bytes(a.in.n, top_k > 0);
+    return top_k ? launch_rows(token_logprobs_kernel<E, true, AL>, a, T * a.cluster, a.cluster, smem, stream, shape.threads)
+                 : launch_rows(token_logprobs_kernel<E, false, AL>, a, T * a.cluster, a.cluster, smem, stream, shape.threads);
   });
 }
 

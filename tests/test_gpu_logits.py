@@ -83,6 +83,49 @@ def test_largest_vocabulary(rlk):
     ref.assert_scores(r, ref.scores(z, V - 3, 1.0, y, 128), z, V - 3, 1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_long_rows(rlk, dtype):
+    """Rows beyond the shared memory that a step in one launch has, and beyond what a search for
+    alternatives gets without asking."""
+    V, n, K = 900000, 899999, 40
+    z, gen = make(3, V, n, dtype, seed=30)
+    y = torch.randint(0, n, (3,), generator=gen, device="cuda")
+    r = rlk.token_logprobs(z, y, top_k=K, V_true=n)
+    ref.assert_scores(r, ref.scores(z, n, 1.0, y, K), z, n, 1.0)
+    ids, t = distill_inputs(3, n, K, gen)
+    g = torch.rand(3, generator=gen, device="cuda")
+    loss, lse, d = rlk.distill_topk_fwd_bwd(z, ids, t, g, V_true=n)
+    want = ref.distill(z, n, V, 1.0, ids, t, g, lse)
+    ref.assert_within(loss, want["loss"], ref.EPS_SUM + 64 * ref.EPS * want["loss_scale"], "loss")
+    ref.assert_grad(d, want["dlogits"], want["bound"])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_alternatives_that_crowd_or_tie(rlk, dtype):
+    """The best columns side by side, in one lane's columns, or tied beyond what a bar can part: the
+    second attempts of the search; and denormals, which order like other values."""
+    n = 40000
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    z = torch.randn((8, n), generator=gen, device="cuda").to(dtype)
+    col = torch.arange(n, device="cuda")
+    z[0, 20000:20300] = (20 + torch.arange(300, device="cuda") * 0.125).to(dtype)      # side by side
+    z[1, (col % 256 < 8)] += 30                                                       # lane 0 of every leaf
+    z[2] = (col % 3).to(dtype)                                                        # 13333 ties for the best
+    z[3] = (-(col % 7).float()).to(dtype)                                             # ties of zero, then -1, ...
+    z[4] = -4.0; z[4, 777] = -1.0; z[4, 30000:30050] = -2.0                           # ties below the best
+    z[5] = torch.finfo(dtype).tiny * (torch.rand(n, generator=gen, device="cuda") - 0.5)
+    z[6] = -float("inf"); z[6, ::1000] = 1.0                                          # 40 equal, nothing else
+    z[7] = z[7].abs().neg()
+    y = torch.randint(0, n, (8,), generator=gen, device="cuda")
+    for k in (1, 20, 64, 128):
+        r = rlk.token_logprobs(z, y, top_k=k)
+        ref.assert_scores(r, ref.scores(z, n, 1.0, y, k), z, n, 1.0)
+        for cut in (900, 5000):
+            r = rlk.token_logprobs(z[:, 20000:20000 + cut], torch.zeros_like(y), top_k=k)
+            part = z[:, 20000:20000 + cut]
+            ref.assert_scores(r, ref.scores(part, cut, 1.0, torch.zeros_like(y), k), part, cut, 1.0)
+
+
 def special_rows(dtype, n, gen):
     """Rows where masks, ties and special values go wrong, and a target for each."""
     big = torch.finfo(dtype).max
