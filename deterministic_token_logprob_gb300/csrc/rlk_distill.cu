@@ -150,7 +150,10 @@ struct DistillDz {
   }
 };
 
-// Backward alone: a.cluster CTAs of a row, each its own part.
+// Backward alone: a.cluster CTAs of a row, each its own part. Columns outside the teacher's entries have
+// dz = A p; the entries, few, are written over it, so the stream over the row does not look for them.
+// Bound by memory: 1000 rows of 32003, fp32 to bf16, take 37 us (5.2 TB/s: one and a half waves of
+// CTAs), 8192 rows of 151936 in bf16 715 us (7.0 TB/s).
 template <class E, class O, bool AL>
 __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const DistillArgs a) {
   __shared__ TeacherRow q;
@@ -186,7 +189,9 @@ __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const Distill
   }
 }
 
-// Forward: a cluster of CTAs a row.
+// Forward: a cluster of CTAs a row. The last warp of CTA 0 gathers the student's logits at the teacher's
+// columns while the others go over the row. Bound by memory with many rows: 8192 rows of 151936 in bf16
+// take 353 us (7.0 TB/s), 512 29 us (5.4 TB/s: one wave, whose start and end count).
 template <class E, bool AL>
 __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
@@ -215,7 +220,8 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const Disti
 // w + W, ..., and copies all of them asynchronously before anything else, one copy group a leaf,
 // so that the whole row is in flight at once and each leaf is summed as it arrives. The warp that
 // summed a leaf writes its gradient: nothing but the leaves' statistics (to every CTA) and the
-// lse crosses warps.
+// lse crosses warps. 2048 rows of 50257 in bf16 take 112 us, two launches 134; 16 rows of 4096 4.2 us
+// on the GPU.
 constexpr int STEP_THREADS = 288;
 constexpr int STEP_CTAS = 4;              // of one SM
 constexpr int STEP_MAX_ROUNDS = 8;        // leaves of one warp
@@ -433,7 +439,7 @@ rlk_status launch_distill_bwd(DistillArgs a, int32_t dtype, int32_t out_dtype, v
 // not fit, or where a cluster of more than two has more than four waves of rows to work through. A
 // cluster's CTAs wait for one another's sums, and what is resident does not cover that wait: 1024
 // rows of 151936 in bf16 (clusters of 8) take 158 us in one launch and 155 in two, 8192 1205 and
-// 1083, but 256 rows 46 and 57; 2048 rows of 50257 (clusters of 2) 112 and 134.
+// 1083, but 256 rows 46 and 57.
 constexpr size_t kStepSmem = 220 << 10;
 
 size_t step_smem(int n_leaves, int cluster, int slot) {

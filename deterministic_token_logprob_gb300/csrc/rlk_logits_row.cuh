@@ -116,7 +116,7 @@ __device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l,
 
 // Starts the copy of a leaf into L2, where the whole leaf lies inside the row: the passes that have no
 // registers for a second leaf have the next one on its way all the same (8192 rows of 151936 in bf16
-// with 20 alternatives: 509 -> 485 us; two leaves ahead 488, four 497).
+// with 20 alternatives: 474 -> 444 us; two leaves ahead 448).
 template <class R>
 __device__ __forceinline__ void prefetch_leaf(const R& row, int l) {
   constexpr int EB = sizeof(*row.p);
@@ -135,7 +135,7 @@ __device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, co
   const uint32_t cell0 = TOP ? map_to_cta(smem_u32(sm.cell), 0) : 0;
   int count = 0;
   // 64 registers have room for the next leaf's packs in the lean pass over 16-bit types alone (8192
-  // rows of 151936 in bf16: 378 -> 354 us); elsewhere the other warps hide the loads
+  // rows of 151936 in bf16: 362 -> 353 us); elsewhere the other warps hide the loads
   constexpr bool AHEAD = !ENT && sizeof(typename E::bits) == 2;
   Pack<E> k[AHEAD ? 2 : 1][LEAF_GROUPS];
   if (g < n_leaves) load_leaf(row, g, lane, k[0]);
@@ -174,26 +174,31 @@ __device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, co
 // SM runs 32 warps, so floor(32 / w) CTAs; a row takes ceil(leaves / (c w)) rounds of leaves, about
 // two more for what surrounds them (the target, the fold, the alternatives) and half a one for each
 // doubling of the cluster. The shape with the least waves x rounds: one CTA of 8 warps where rows
-// fill the GPU (4 take 579 us where 8 take 509 and 16 564: 8192 rows of 151936 in bf16 with 20
+// fill the GPU (4 take 540 us where 8 take 444 and 16 509: 8192 rows of 151936 in bf16 with 20
 // alternatives), 8 CTAs of 19 for a single row of 149 leaves. Short rows take a warp a leaf; a few of
-// them at least 4 or 8, to find the alternatives (64 rows of 1000 with k = 100: 31 -> 15 us; 4096
-// rows with k = 50 take 46 us with 2 warps, 55 with 8).
+// them at least 4 or 8, to find the alternatives (64 rows of 1000 with k = 100: 33 -> 17 us; 4096
+// rows with k = 50 take 37 us with 2 warps, 56 with 8). Of the widths in between, those that use the
+// 32 warps well are tried; with 16 waves of rows and more the answer is known.
 struct RowShape {
   int cluster, threads;
 };
 inline RowShape row_shape(const LogitRows& in, int top_k) {
-  const int64_t L = leaves_of(in.n);
-  RowShape best{1, ROW_THREADS};
-  int64_t least = INT64_MAX;
-  const bool few_rows = in.T <= 4 * 152;
-  const int fewest = L >= 8 || (few_rows && top_k > 32) ? 8 : few_rows && top_k > 0 && L < 4 ? 4 : L < 2 ? 2 : static_cast<int>(L);
-  for (int c = 1, half = 0; c <= MAX_CLUSTER; c *= 2, ++half)
-    for (int w = fewest; w <= 32; ++w) {
-      if (w > 8 && c * (w - 1) >= L) break;  // more warps than leaves
-      const int64_t waves = (in.T * static_cast<int64_t>(c) + 152 * (32 / w) - 1) / (152 * (32 / w));
-      const int64_t cost = waves * (2 * ((L + c * w - 1) / (c * w)) + 4 + half);
+  const int L = leaves_of(in.n);
+  const uint32_t T = static_cast<uint32_t>(in.T);
+  const bool few_rows = T <= 4 * 152;
+  const int fewest = L >= 8 || (few_rows && top_k > 32) ? 8 : few_rows && top_k > 0 && L < 4 ? 4 : L < 2 ? 2 : L;
+  RowShape best{1, 32 * fewest};
+  if (T >= 16 * 152) return best;
+  uint32_t least = UINT32_MAX;
+  for (int c = 1, half = 0; c <= MAX_CLUSTER; c *= 2, ++half) {
+    const int each = (L + c - 1) / c;  // leaves of a CTA: more warps would idle
+    for (int w : {fewest, 10, 12, 14, 16, 20, 25, 32, each}) {
+      if (w < fewest || w > 32 || (w > fewest && w > each)) continue;
+      const uint32_t room = 152u * (32 / w), waves = (T * c + room - 1) / room;
+      const uint32_t cost = waves * (2 * ((L + c * w - 1) / (c * w)) + 4 + half);
       if (cost < least) least = cost, best = RowShape{c, 32 * w};
     }
+  }
   return best;
 }
 

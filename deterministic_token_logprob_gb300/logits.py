@@ -288,8 +288,7 @@ def distill_topk_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch
     p = _teacher(ids, teacher, T, dev)
     g_p = _per_row(g, "g", torch.float32, (T,), dev)
     V_true = _true_vocab(V_true, V)
-    loss = torch.empty(T, dtype=torch.float32, device=g.device)
-    lse = torch.empty(T, dtype=torch.float32, device=g.device)
+    loss, lse = torch.empty_like(g), torch.empty_like(g)
     dlogits, d = _gradient(logits, T, V, out, out_dtype)
     st = _load().rlk_distill_topk_fwd_bwd(logits.data_ptr(), code, T, ld, V_true, temperature, *p, g_p,
                                           loss.data_ptr(), lse.data_ptr(), *d, _flag(err_flag, dev),
