@@ -2,11 +2,12 @@
 // from a teacher's top logits) share: element types, the row statistics and their fixed
 // order, the gradient's arithmetic and the host-side argument checks.
 //
-// Row statistics of the scaled logits x = s z (s = 1 / temperature) over v < V_true:
-//   M = max z,  S = sum e^{s (z - M)},  U = sum e^{s (z - M)} (z - M)
-//   lse = s M + log S,   entropy = -sum p log p = log S - s U / S    (both terms >= 0)
+// Row statistics of the scaled logits s z (s = 1 / temperature) over v < V_true, with
+// x = c (z - M), c = s log2 e, so that 2^x = e^{s (z - M)}:
+//   M = max z,  S = sum 2^x,  U = sum 2^x x
+//   lse = s M + log S,   entropy = -sum p log p = log S - log 2 U / S    (both terms >= 0)
 // The row is cut into leaves of 1024 columns. A warp takes a leaf: lane i holds the columns
-// 256 j + 8 i .. + 7 (j = 0..3), subtracts the leaf's own maximum (exact, order-free), and
+// 256 j + 8 i .. + 7 (j = 0..3), takes x about the leaf's own maximum (exact, order-free), and
 // sums even and odd columns separately in ascending order; the lanes combine by an
 // xor-butterfly. Leaves are combined by one warp: lane i folds leaves i, i + 32, ... in
 // ascending order, then the same butterfly. The order depends on column indices alone, so
@@ -250,16 +251,25 @@ __device__ __forceinline__ float2 pair(const Pack<E>& k, int i) {
   else return E::to_f32x2(k.w[i]);
 }
 
-// Largest element of a pack (NaN is passed over).
-template <class E>
-__device__ __forceinline__ float pack_max(const Pack<E>& k) {
+// Largest element of a lane's packs (NaN is passed over).
+template <class E, int N>
+__device__ __forceinline__ float pack_max(const Pack<E> (&k)[N]) {
   if constexpr (Pack<E>::EB == 4) {
-    float m = __uint_as_float(k.w[0]);
+    float m = __uint_as_float(k[0].w[0]);
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = fmaxf(m, __uint_as_float(k.w[i]));
+    for (int j = 0; j < N; ++j)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = fmaxf(m, __uint_as_float(k[j].w[i]));
     return m;
   } else {
-    const float2 m = E::to_f32x2(E::max2(E::max2(k.w[0], k.w[1]), E::max2(k.w[2], k.w[3])));
+    uint32_t x[Pack<E>::WORDS];
+#pragma unroll
+    for (int i = 0; i < Pack<E>::WORDS; ++i) {
+      x[i] = k[0].w[i];
+#pragma unroll
+      for (int j = 1; j < N; ++j) x[i] = E::max2(x[i], k[j].w[i]);
+    }
+    const float2 m = E::to_f32x2(E::max2(E::max2(x[0], x[1]), E::max2(x[2], x[3])));
     return fmaxf(m.x, m.y);
   }
 }
@@ -268,7 +278,7 @@ __device__ __forceinline__ float pack_max(const Pack<E>& k) {
 // row statistics
 // ---------------------------------------------------------------------------
 struct alignas(16) Stats {
-  float m, s, u, pad;
+  float m, s, u, r;
 };
 
 __device__ __forceinline__ float warp_max(float v) {
@@ -309,40 +319,61 @@ __device__ __forceinline__ float2 warp_sum_pair(float a, float b, int lane) {
   return make_float2(v, __shfl_down_sync(kFullWarp, v, 16));
 }
 
-// s and, with ENT, u of a leaf about its maximum m (not -inf). NaN or +inf among the columns makes s NaN.
+// s and, with ENT, u of a leaf about its maximum m (not -inf), in powers of two: x = c z - b with
+// b = rn(c m), so that an element takes one product-and-sum, and *r = b - c m, which fold_leaves takes
+// out again. NaN or +inf among the columns makes s NaN.
 template <bool ENT, class E>
-__device__ __forceinline__ float2 leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], float m, float c, int lane) {
-  const F32x2 nm = pack_f32x2(-m, -m), cc = pack_f32x2(c, c);
-  F32x2 s2 = 0, u2 = 0;  // even and odd columns
+__device__ __forceinline__ float2 leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], float m, float c, float* r, int lane) {
+  constexpr float kHuge = 3.4028235e38f;
+  const float b = __fmul_rn(m, c);
+  *r = -__fmaf_rn(m, c, -b);
+  const bool over = !(fabsf(b) <= kHuge);
+  float sl = 0.f, ul = 0.f;
+  const auto sums = [&] {
+    const F32x2 nb = pack_f32x2(-b, -b), cc = pack_f32x2(c, c);
+    F32x2 s2 = 0, u2 = 0;  // even and odd columns
 #pragma unroll
-  for (int j = 0; j < LEAF_GROUPS; ++j)
+    for (int j = 0; j < LEAF_GROUPS; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 z = pair(k[j], i);
-      const F32x2 d = add2(pack_f32x2(z.x, z.y), nm);
-      const float2 x = unpack_f32x2(mul2(d, cc));
-      const F32x2 w = pack_f32x2(ex2_approx(x.x), ex2_approx(x.y));
-      s2 = add2(s2, w);
-      if constexpr (ENT) u2 = fma2(w, d, u2);
-    }
-  const float2 s = unpack_f32x2(s2), u = unpack_f32x2(u2);
-  const float sl = __fadd_rn(s.x, s.y);
-  if constexpr (!ENT) return make_float2(warp_sum(sl), 0.f);
-  float ul = __fadd_rn(u.x, u.y);
-  if (__any_sync(kFullWarp, isnan(ul))) {
-    // masked columns: weight 0 times d = -inf. Once more with d kept finite (a NaN logit reaches
-    // s through its weight); every other term is what it was.
-    float v[2] = {0.f, 0.f};
+      for (int i = 0; i < 4; ++i) {
+        const float2 z = pair(k[j], i);
+        const F32x2 xx = fma2(pack_f32x2(z.x, z.y), cc, nb);
+        const float2 x = unpack_f32x2(xx);
+        const F32x2 w = pack_f32x2(ex2_approx(x.x), ex2_approx(x.y));
+        s2 = add2(s2, w);
+        if constexpr (ENT) u2 = fma2(w, xx, u2);
+      }
+    const float2 s = unpack_f32x2(s2), u = unpack_f32x2(u2);
+    sl = __fadd_rn(s.x, s.y);
+    if constexpr (ENT) ul = __fadd_rn(u.x, u.y);
+  };
+  // x kept finite where a masked column (weight 0) would have -inf (a NaN logit reaches s through its
+  // weight); every other term is what it was. Or, where c m is beyond fp32, x from z - m.
+  const auto careful_sums = [&] {
+    float v[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < LEAF_GROUPS; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 z = pair(k[j], i / 2);
-        const float d = __fsub_rn(i & 1 ? z.y : z.x, m);
-        v[i & 1] = __fmaf_rn(ex2_approx(__fmul_rn(d, c)), fmaxf(d, -3.4028235e38f), v[i & 1]);
+        const float2 p = pair(k[j], i / 2);
+        const float z = i & 1 ? p.y : p.x;
+        const float x = over ? __fmul_rn(__fsub_rn(z, m), c) : __fmaf_rn(z, c, -b);
+        const float e = ex2_approx(x);
+        w[i & 1] = __fadd_rn(w[i & 1], e);
+        if constexpr (ENT) v[i & 1] = __fmaf_rn(e, fmaxf(x, -kHuge), v[i & 1]);
       }
+    sl = __fadd_rn(w[0], w[1]);
     ul = __fadd_rn(v[0], v[1]);
+  };
+  if (over) *r = 0.f;
+  if constexpr (!ENT) {
+    if (over) careful_sums();
+    else sums();
+  } else {
+    sums();
+    if (over || __any_sync(kFullWarp, isnan(ul))) careful_sums();
   }
+  if constexpr (!ENT) return make_float2(warp_sum(sl), 0.f);
   return warp_sum_pair(sl, ul, lane);
 }
 
@@ -368,11 +399,11 @@ __device__ __forceinline__ Stats fold_leaves(const Stats* leaf, int n_leaves, fl
   for (int l = lane; l < n_leaves; l += 32) {
     const Stats x = leaf[l];
     if (x.s == 0.f) continue;  // nothing but -inf
-    const float d = __fsub_rn(x.m, M);
-    const float f = ex2_approx(__fmul_rn(d, c));
+    const float e = __fmaf_rn(__fsub_rn(x.m, M), c, x.r);  // the leaf's base against the row's
+    const float f = ex2_approx(e);
     S = __fmaf_rn(x.s, f, S);
-    // u relative to M: sum w (z - M) = u + s (m - M); a leaf too far down to count adds nothing
-    if (f != 0.f) U = __fmaf_rn(f, __fmaf_rn(x.s, d, x.u), U);
+    // u relative to M: sum w (x + e); a leaf too far down to count adds nothing
+    if (f != 0.f) U = __fmaf_rn(f, __fmaf_rn(x.s, e, x.u), U);
   }
   return Stats{M, warp_sum(S), warp_sum(U), 0.f};
 }
@@ -386,10 +417,11 @@ __device__ __forceinline__ float row_lse(const Stats& r, float s) {
   return __fmaf_rn(r.m, s, logf(r.s));
 }
 
-__device__ __forceinline__ float row_entropy(const Stats& r, float s) {
+__device__ __forceinline__ float row_entropy(const Stats& r) {
   if (isnan(r.s)) return quiet_nan();
   if (r.s == 0.f) return 0.f;
-  return __fsub_rn(logf(r.s), __fmul_rn(s, __fdiv_rn(r.u, r.s)));
+  constexpr float kLn2 = 0.69314718f;
+  return __fsub_rn(logf(r.s), __fmul_rn(kLn2, __fdiv_rn(r.u, r.s)));
 }
 
 // s z - lse with one rounding: log p of the token. -inf where the row is empty.

@@ -18,7 +18,7 @@ constexpr int MAX_ROW_WARPS = MAX_CLUSTER * MAX_ROW_THREADS / 32;
 // ---------------------------------------------------------------------------
 // Warp g of the row's C x (blockDim / 32) warps takes leaves g, g + (number of warps), ... and
 // leaves what it found in the shared memory of the cluster's CTA 0 (distributed shared memory):
-// (m, s, u) of each leaf, the maxima of its 32 cells (TOP: a cell is the 32 columns that a lane
+// (m, s, u, r) of each leaf, the maxima of its 32 cells (TOP: a cell is the 32 columns that a lane
 // holds, so its maximum costs nothing), and how many columns stand ahead of the target.
 struct RowSmem {
   Stats* leaf;      // [n_leaves]
@@ -101,14 +101,14 @@ __device__ __forceinline__ int count_ahead(const Pack<E> (&k)[LEAF_GROUPS], cons
 template <bool ENT, bool TOP, class E>
 __device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l, float c, const RankOf& rank,
                                          uint32_t leaf0, uint32_t cell0, bool puts, int lane) {
-  float m = fmaxf(fmaxf(pack_max(k[0]), pack_max(k[1])), fmaxf(pack_max(k[2]), pack_max(k[3])));
+  float m = pack_max(k), r = 0.f;
   if constexpr (TOP) st_cluster_u32(cell0 + static_cast<uint32_t>(l * 32 + lane) * 4, __float_as_uint(m));
   m = warp_max(m);
   float2 x;
   if (m == neg_inf()) x = make_float2(any_nan(k) ? quiet_nan() : 0.f, 0.f);
-  else x = leaf_sums<ENT>(k, m, c, lane);
+  else x = leaf_sums<ENT>(k, m, c, &r, lane);
   if (puts) {
-    st_cluster_f32x4(leaf0 + static_cast<uint32_t>(l * 16), m, x.x, x.y, 0.f);
+    st_cluster_f32x4(leaf0 + static_cast<uint32_t>(l * 16), m, x.x, x.y, r);
   }
   // a leaf whose best column is below the target has none ahead of it: for a likely token, most
   return rank.on && m >= rank.z ? count_ahead(k, rank, l, lane) : 0;

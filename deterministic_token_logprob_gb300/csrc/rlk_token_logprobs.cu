@@ -161,7 +161,8 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, unsigned c
   const int K = a.top_k, cells = cells_of(row.n);
   const float bar = ts.bar;
   const auto octet_max = [&](int c) {
-    return pack_max(packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c));
+    const Pack<E> k[1] = {packs_inside(row, c, c + 8) ? load_pack(row, c) : load_pack_edge(row, c)};
+    return pack_max(k);
   };
   const auto collect = [&](float reached) {
     for (int i = threadIdx.x; i < 8 * ts.n_octet; i += blockDim.x) {
@@ -332,7 +333,7 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(cons
     if (lane == 0) {
       if (TOP) ts.lse = lse;
       if (a.lse) a.lse[t] = lse;
-      if (a.entropy) a.entropy[t] = row_entropy(x, in.s);
+      if (a.entropy) a.entropy[t] = row_entropy(x);
       if (a.logp) a.logp[t] = rank.ok && !bad ? token_logp(rank.z, in.s, lse) : quiet_nan();
       if (a.rank) a.rank[t] = rank.ok && !bad ? 1 + before : 0;
       if (in.err_flag && bad) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
