@@ -321,13 +321,14 @@ __device__ __forceinline__ float2 warp_sum_pair(float a, float b, int lane) {
 
 // s and, with ENT, u of a leaf about its maximum m (not -inf), in powers of two: x = c z - b with
 // b = rn(c m), so that an element takes one product-and-sum, and *r = b - c m, which fold_leaves takes
-// out again. NaN or +inf among the columns makes s NaN.
+// out again. Where |b| is so large that its rounding counts in the exponent, x comes from z - m (r = 0).
+// NaN or +inf among the columns makes s NaN.
 template <bool ENT, class E>
 __device__ __forceinline__ float2 leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], float m, float c, float* r, int lane) {
   constexpr float kHuge = 3.4028235e38f;
   const float b = __fmul_rn(m, c);
   *r = -__fmaf_rn(m, c, -b);
-  const bool over = !(fabsf(b) <= kHuge);
+  const bool over = !(fabsf(b) <= 268435456.f);  // 2^28: up to there |r| <= 16, far inside the range of 2^r
   float sl = 0.f, ul = 0.f;
   const auto sums = [&] {
     const F32x2 nb = pack_f32x2(-b, -b), cc = pack_f32x2(c, c);
@@ -348,7 +349,7 @@ __device__ __forceinline__ float2 leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], flo
     if constexpr (ENT) ul = __fadd_rn(u.x, u.y);
   };
   // x kept finite where a masked column (weight 0) would have -inf (a NaN logit reaches s through its
-  // weight); every other term is what it was. Or, where c m is beyond fp32, x from z - m.
+  // weight); every other term is what it was. Or, with `over`, x from z - m.
   const auto careful_sums = [&] {
     float v[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll

@@ -173,6 +173,30 @@ def test_masks_ties_and_special_values(rlk, dtype, n):
         assert int(err) == rlk.RLK_FLAG_BAD_TARGET | rlk.RLK_FLAG_NONFINITE
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("temperature", [1e-6, 1.0])
+def test_scaled_logits_at_the_edge_of_fp32(rlk, dtype, temperature):
+    """s z is finite while s z log2(e) is not, in some leaves or in all of them."""
+    n, edge = 5003, 3.0e38 * temperature
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    z = torch.randn((10, n), generator=gen, device="cuda")
+    y = torch.randint(0, n, (10,), generator=gen, device="cuda")
+    z[0] = edge                                   # uniform at the edge
+    z[1] = -edge
+    z[2] = -edge; z[2, 7] = edge                  # one column takes all
+    z[3] = -edge; z[3, ::100] = edge              # 51 columns share it
+    z[4, :1024] = -edge                           # a leaf far down, the others ordinary
+    z[5, 1024:2048] = -edge
+    z[6, 4096:] = edge                            # the last leaf takes all
+    z[7, 2000] = edge / 2                         # a maximum below the edge, its leaf's sums in range
+    z[8] = edge / 2; z[8, 3000:] = edge
+    z[9] = -INF; z[9, 50:60] = -edge              # masked besides
+    z = z.to(dtype)
+    for k in (0, 20):
+        r = rlk.token_logprobs(z, y, top_k=k, temperature=temperature)
+        ref.assert_scores(r, ref.scores(z, n, 1 / temperature, y, k), z, n, 1 / temperature)
+
+
 def test_flags_name_their_cause(rlk):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     z = torch.zeros((2, 64), device="cuda")
