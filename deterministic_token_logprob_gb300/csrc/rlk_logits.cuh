@@ -348,18 +348,17 @@ __device__ __forceinline__ float2 leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], flo
     sl = __fadd_rn(s.x, s.y);
     if constexpr (ENT) ul = __fadd_rn(u.x, u.y);
   };
-  // x kept finite where a masked column (weight 0) would have -inf (a NaN logit reaches s through its
-  // weight); every other term is what it was. Or, with `over`, x from z - m.
+  // x = c (z - 0) - b, the same bits, kept finite where a masked column (weight 0) has -inf (a NaN logit
+  // reaches s through its weight); or x = c (z - m) - 0 with `over`. In single values: pairs spill.
   const auto careful_sums = [&] {
+    const float nm = over ? -m : 0.f, nb = over ? 0.f : -b;
     float v[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < LEAF_GROUPS; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float2 p = pair(k[j], i / 2);
-        const float z = i & 1 ? p.y : p.x;
-        const float x = over ? __fmul_rn(__fsub_rn(z, m), c) : __fmaf_rn(z, c, -b);
-        const float e = ex2_approx(x);
+        const float2 z = pair(k[j], i / 2);
+        const float x = __fmaf_rn(__fadd_rn(i & 1 ? z.y : z.x, nm), c, nb), e = ex2_approx(x);
         w[i & 1] = __fadd_rn(w[i & 1], e);
         if constexpr (ENT) v[i & 1] = __fmaf_rn(e, fmaxf(x, -kHuge), v[i & 1]);
       }
