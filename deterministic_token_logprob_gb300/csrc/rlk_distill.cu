@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const Distill
 
 // Forward: a cluster of CTAs a row. The last warp of CTA 0 gathers the student's logits at the teacher's
 // columns while the others go over the row. Bound by memory with many rows: 8192 rows of 151936 in bf16
-// take 353 us (7.0 TB/s), 512 29 us (5.4 TB/s: one wave, whose start and end count).
+// take 351 us (7.1 TB/s), 512 29 us (5.4 TB/s: one wave, whose start and end count).
 template <class E, bool AL>
 __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const DistillArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];

@@ -349,7 +349,8 @@ __device__ __forceinline__ float2 leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], flo
     if constexpr (ENT) ul = __fadd_rn(u.x, u.y);
   };
   // x = c (z - 0) - b, the same bits, kept finite where a masked column (weight 0) has -inf (a NaN logit
-  // reaches s through its weight); or x = c (z - m) - 0 with `over`. In single values: pairs spill.
+  // reaches s through its weight); or x = c (z - m) - 0 with `over`. In single values: paired
+  // ones spill (4096 rows of 151936 in fp32 with 64 alternatives: 386 -> 418 us).
   const auto careful_sums = [&] {
     const float nm = over ? -m : 0.f, nb = over ? 0.f : -b;
     float v[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};

@@ -116,7 +116,7 @@ __device__ __forceinline__ int leaf_pass(const Pack<E> (&k)[LEAF_GROUPS], int l,
 
 // Starts the copy of a leaf into L2, where the whole leaf lies inside the row: the passes that have no
 // registers for a second leaf have the next one on its way all the same (8192 rows of 151936 in bf16
-// with 20 alternatives: 474 -> 444 us; two leaves ahead 448).
+// with 20 alternatives: 464 -> 433 us; two leaves ahead 436).
 template <class R>
 __device__ __forceinline__ void prefetch_leaf(const R& row, int l) {
   constexpr int EB = sizeof(*row.p);
@@ -135,7 +135,7 @@ __device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, co
   const uint32_t cell0 = TOP ? map_to_cta(smem_u32(sm.cell), 0) : 0;
   int count = 0;
   // 64 registers have room for the next leaf's packs in the lean pass over 16-bit types alone (8192
-  // rows of 151936 in bf16: 362 -> 353 us); elsewhere the other warps hide the loads
+  // rows of 151936 in bf16: 357 -> 351 us); elsewhere the other warps hide the loads
   constexpr bool AHEAD = !ENT && sizeof(typename E::bits) == 2;
   Pack<E> k[AHEAD ? 2 : 1][LEAF_GROUPS];
   if (g < n_leaves) load_leaf(row, g, lane, k[0]);
@@ -174,7 +174,7 @@ __device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, co
 // SM runs 32 warps, so floor(32 / w) CTAs; a row takes ceil(leaves / (c w)) rounds of leaves, about
 // two more for what surrounds them (the target, the fold, the alternatives) and half a one for each
 // doubling of the cluster. The shape with the least waves x rounds: one CTA of 8 warps where rows
-// fill the GPU (4 take 540 us where 8 take 444 and 16 509: 8192 rows of 151936 in bf16 with 20
+// fill the GPU (4 take 528 us where 8 take 433 and 16 501: 8192 rows of 151936 in bf16 with 20
 // alternatives), 8 CTAs of 19 for a single row of 149 leaves. Short rows take a warp a leaf; a few of
 // them at least 4 or 8, to find the alternatives (64 rows of 1000 with k = 100: 33 -> 17 us; 4096
 // rows with k = 50 take 37 us with 2 warps, 56 with 8). Of the widths in between, those that use the

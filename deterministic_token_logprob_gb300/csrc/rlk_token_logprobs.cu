@@ -296,13 +296,14 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, unsigned c
 }
 
 // logp, rank, lse and entropy in one pass over the row, the alternatives from what the pass left in
-// shared memory and a few hundred columns read again (from L2). The pass reads each logit once and
-// takes 6 instructions (without the entropy) to 8 a 16-bit element, 10.8 with 20 alternatives and all
-// that surrounds the pass: with 16-bit types the instructions bind, not the memory (8192 rows of 151936
-// in bf16: 394 us for 2.49 GB, 6.3 TB/s, without alternatives, 444 us with 20; 4096 in fp32 with 64:
-// 381 us, 6.5 TB/s). Few rows are bound by latency: a single one takes 7 us on the GPU, on 8 SMs.
-// Persistent CTAs, whose finishing warp overlaps the next row's pass, are slower (749 us against 485
-// at that step): finishing a row takes one warp 30 us.
+// shared memory and a few hundred columns read again (from L2). The pass reads each logit once. With
+// 16-bit types and alternatives the instructions bind, not the memory: about 10 an element, of which a
+// third is what each lane does once for the 32 elements that it has of a leaf (8192 rows of 151936 in
+// bf16 with 20 alternatives: 434 us for 2.49 GB, 5.7 TB/s; without any 385 us, 6.5 TB/s; 4096 in fp32 with
+// 64: 386 us, 6.4 TB/s, with none 338 us, 7.3 TB/s). Few rows are bound by latency: a single one takes
+// 8 us on the GPU, on 8 SMs.
+// Persistent CTAs, whose finishing warp overlaps the next row's pass, are slower (749 us against 485 at
+// that step): finishing a row takes one warp 30 us.
 // 64 registers a thread, whatever the number of threads: 1024 of them fill an SM.
 template <class E, bool TOP, bool AL>
 __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(const ScoreArgs a) {
