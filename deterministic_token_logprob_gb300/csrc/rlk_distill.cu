@@ -164,29 +164,28 @@ __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const Distill
   const GradPart<E, O, AL> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
                                 static_cast<int>(blockIdx.x % a.cluster), a.cluster, in.err_flag);
   const float lse = a.lse_in[t], g = a.g[t];
+  const bool in_place = in.base == a.out.base;
   if (threadIdx.x < 32) {
     teacher_softmax(q, a.ids + t * a.K, a.teacher + t * a.K, a.K, in.n, in.s, in.c, threadIdx.x);
     __syncwarp();
-    // the logits of the teacher's columns, read before anything is written; other parts may already
-    // have written theirs
-    const bool in_use = g != 0.f;
-#pragma unroll
-    for (int i = 0; i < RLK_MAX_TOP_K / 32; ++i) {
-      const int k = threadIdx.x + 32 * i;
-      zk[k] = in_use && part.owns(q.id[k]) ? E::to_f32(z[q.id[k]]) : 0.f;
-    }
+    // in place: the logits of the teacher's columns, read before anything is written; other parts may
+    // already have written theirs
+    if (in_place && g != 0.f)
+      for (int k = threadIdx.x; k < a.K; k += 32)
+        if (part.owns(q.id[k])) zk[k] = E::to_f32(z[q.id[k]]);
   }
   __syncthreads();
   if (q.bad && part.lo == 0 && threadIdx.x == 0 && in.err_flag) atomicOr(in.err_flag, q.bad);
   const bool live = distill_live(q, lse, g);
   const float A = __fmul_rn(in.s, g);
   write_part<GRAD_PACKS>(part, live, DistillDz{in.s, lse, A});
+  const int k = threadIdx.x;
+  static_assert(RLK_MAX_TOP_K <= ROW_THREADS, "a thread an entry");
+  const bool patches = live && k < a.K && part.owns(q.id[k]);
+  const float zy = !patches ? 0.f : in_place ? zk[k] : E::to_f32(z[q.id[k]]);  // from L2 now
   __syncthreads();
-  if (!live) return;
-  for (int k = threadIdx.x; k < a.K; k += ROW_THREADS) {
-    float dz;
-    if (q.id[k] >= 0 && part.owns(q.id[k]) && entry_dz(q, k, a.K, zk[k], in.s, lse, A, &dz)) part.put(q.id[k], dz);
-  }
+  float dz;
+  if (patches && entry_dz(q, k, a.K, zy, in.s, lse, A, &dz)) part.put(q.id[k], dz);
 }
 
 // Forward: a cluster of CTAs a row. The last warp of CTA 0 gathers the student's logits at the teacher's
