@@ -152,8 +152,9 @@ struct DistillDz {
 
 // Backward alone: a.cluster CTAs of a row, each its own part. Columns outside the teacher's entries have
 // dz = A p; the entries, few, are written over it, so the stream over the row does not look for them.
-// Bound by memory: 1000 rows of 32003, fp32 to bf16, take 37 us (5.2 TB/s: one and a half waves of
-// CTAs), 8192 rows of 151936 in bf16 715 us (7.0 TB/s).
+// Bound by memory: 1000 rows of 32003, fp32 to bf16, take 39 us (4.9 TB/s: one and a half waves of
+// CTAs), 8192 rows of 151936 in bf16 716 us (6.9 TB/s). The teacher's columns are read again at the end,
+// from L2 (728 us where the CTA waited for them at the start).
 template <class E, class O, bool AL>
 __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const DistillArgs a) {
   __shared__ TeacherRow q;
@@ -438,7 +439,7 @@ rlk_status launch_distill_bwd(DistillArgs a, int32_t dtype, int32_t out_dtype, v
 // not fit, or where a cluster of more than two has more than four waves of rows to work through. A
 // cluster's CTAs wait for one another's sums, and what is resident does not cover that wait: 1024
 // rows of 151936 in bf16 (clusters of 8) take 158 us in one launch and 155 in two, 8192 1205 and
-// 1083, but 256 rows 46 and 57.
+// 1069, but 256 rows 46 and 57.
 constexpr size_t kStepSmem = 220 << 10;
 
 size_t step_smem(int n_leaves, int cluster, int slot) {

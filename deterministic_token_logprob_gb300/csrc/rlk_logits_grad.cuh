@@ -116,7 +116,7 @@ __device__ __forceinline__ void write_part(const G& g, bool live, const F& f) {
 
 // CTAs of a row in a kernel that writes gradients alone: parts of up to four rounds of every thread's
 // packs (what a CTA does once -- its row's scalars, the teacher's softmax -- is then small: 8192 rows of
-// 151936 in bf16 take 715 us with four rounds, 954 with one), as long as that leaves the GPU full.
+// 151936 in bf16 take 711 us with four rounds, 954 with one), as long as that leaves the GPU full.
 inline int grad_parts(const LogitRows& in, const GradOut& o) {
   constexpr int kCols = 8 * GRAD_PACKS * ROW_THREADS;
   constexpr int64_t kEnough = 6 * 152;
