@@ -152,9 +152,9 @@ struct DistillDz {
 
 // Backward alone: a.cluster CTAs of a row, each its own part. Columns outside the teacher's entries have
 // dz = A p; the entries, few, are written over it, so the stream over the row does not look for them.
-// Bound by memory: 1000 rows of 32003, fp32 to bf16, take 39 us (4.9 TB/s: one and a half waves of
-// CTAs), 8192 rows of 151936 in bf16 716 us (6.9 TB/s). The teacher's columns are read again at the end,
-// from L2 (728 us where the CTA waited for them at the start).
+// Bound by memory: 1000 rows of 32003, fp32 to bf16, take 38 us (5.0 TB/s: one and a half waves of
+// CTAs), 8192 rows of 151936 in bf16 713 us (7.0 TB/s). The teacher's columns are read again at the end,
+// from L2 (728 us against 716 where the CTA waited for them at the start).
 template <class E, class O, bool AL>
 __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const DistillArgs a) {
   __shared__ TeacherRow q;
@@ -164,6 +164,10 @@ __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const Distill
   const auto* z = static_cast<const typename E::bits*>(in.base) + t * in.ld;
   const GradPart<E, O, AL> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
                                 static_cast<int>(blockIdx.x % a.cluster), a.cluster, in.err_flag);
+  // The first CTAs, two of an SM, wait for their teachers all at once while the memory has nothing to do
+  // (200 rows of 151936 in bf16: 24.1 -> 21.7 us); later ones wait while others work, and prefetching for
+  // them only crowds the writes (all CTAs: 8192 rows 716 -> 781 us).
+  if (blockIdx.x < 2 * 152 && threadIdx.x == 32) part.prefetch();
   const float lse = a.lse_in[t], g = a.g[t];
   const bool in_place = in.base == a.out.base;
   if (threadIdx.x < 32) {

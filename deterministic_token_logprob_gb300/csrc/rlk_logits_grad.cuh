@@ -42,6 +42,13 @@ struct GradPart {
     hi = part == parts - 1 ? V : head + 8 * q1;
     in = Row<E, AL>(z + head, max(0, n - head), err);
   }
+  // Starts the copy of the part's logits into L2 (the whole vectors among them), by one thread.
+  __device__ __forceinline__ void prefetch() const {
+    const uintptr_t a = (reinterpret_cast<uintptr_t>(in.p + 8 * q0) + 15) & ~uintptr_t{15};
+    const uintptr_t b = reinterpret_cast<uintptr_t>(in.p + min(in.n, 8 * q1)) & ~uintptr_t{15};
+    if (a < b)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(a), "r"(static_cast<uint32_t>(b - a)) : "memory");
+  }
   __device__ __forceinline__ bool owns(int64_t c) const { return c >= lo && c < hi; }
   __device__ __forceinline__ void put(int c, float v) const {
     if (dbg_ok(c >= 0 && c < V, in.err)) out[c] = O::from_f32(v);
