@@ -428,11 +428,12 @@ rlk_status check_distill(const void* logits, int32_t dtype, int64_t T, int64_t l
 }
 
 rlk_status launch_distill_fwd(DistillArgs a, int32_t dtype, void* stream) {
-  const RowShape shape = row_shape(a.in, 0);
+  const size_t smem = leaves_of(a.in.n) * sizeof(Stats);
+  const RowShape shape = row_shape(a.in, 0, smem + ROW_SMEM_FIXED);
   a.cluster = shape.cluster;
   return with_types(dtype, aligned_rows(a.in.base, a.in.ld, dtype_bytes(dtype)), [&](auto e, auto al) {
     return launch_rows(distill_kernel<decltype(e), decltype(al)::value>, a, static_cast<int64_t>(a.in.T) * a.cluster,
-                       a.cluster, leaves_of(a.in.n) * sizeof(Stats), stream, shape.threads);
+                       a.cluster, smem, stream, shape.threads);
   });
 }
 

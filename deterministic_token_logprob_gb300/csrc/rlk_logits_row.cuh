@@ -171,30 +171,39 @@ __device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, co
 // launch shapes and types (host)
 // ---------------------------------------------------------------------------
 // CTAs (c, a cluster) and warps (w) of a row in the statistics passes. With 64 registers a thread an
-// SM runs 32 warps, so floor(32 / w) CTAs; a row takes ceil(leaves / (c w)) rounds of leaves, about
-// two more for what surrounds them (the target, the fold, the alternatives) and half a one for each
-// doubling of the cluster. The shape with the least waves x rounds: one CTA of 8 warps where rows
-// fill the GPU (4 take 528 us where 8 take 433 and 16 501: 8192 rows of 151936 in bf16 with 20
-// alternatives), 8 CTAs of 19 for a single row of 149 leaves. Short rows take a warp a leaf; a few of
-// them at least 4 or 8, to find the alternatives (64 rows of 1000 with k = 100: 33 -> 17 us; 4096
-// rows with k = 50 take 37 us with 2 warps, 56 with 8). Of the widths in between, those that use the
-// 32 warps well are tried; with 16 waves of rows and more the answer is known.
+// SM runs 32 warps, so floor(32 / w) CTAs, if their shared memory (smem bytes each) fits; a row takes
+// ceil(leaves / (c w)) rounds of leaves, about two more for what surrounds them (the target, the fold,
+// the alternatives) and half a one for each doubling of the cluster. The shape with the least waves x
+// rounds is taken, among widths that use the 32 warps well: 8 CTAs of 19 for a single row of 149 leaves.
+// Where rows fill the GPU many times over the answer is known. Without alternatives it is one CTA of 4
+// warps (4096 rows of 32000 in bf16, distillation's forward: 51 us, with 8 warps 61), with them one of 8,
+// for they need shared memory and every warp (8192 rows of 151936 in bf16 with 20: 4 warps take 528 us, 8
+// 433, 16 501). In between, narrow CTAs save a wave (796 rows of 50257 in f16 with 20: 35 -> 32.5 us).
+// Rows of more than 100 leaves have rounds enough and take 8 warps in any case (4096 rows of 151936 in
+// fp32: 338 us with 8, 350 with 4; 800 in bf16 with 20 alternatives 59.6 with 10, 62.7 with 5, where rows
+// of 100000 take 43.7 and 42.6). Short rows take a warp a leaf; a few of them at least 4 or 8, to find
+// the alternatives (64 rows of 1000 with k = 100: 33 -> 17 us; 4096 rows with k = 50 take 37 us with 2
+// warps, 56 with 8).
 struct RowShape {
   int cluster, threads;
 };
-inline RowShape row_shape(const LogitRows& in, int top_k) {
+constexpr size_t SM_SMEM = 228 << 10;     // shared memory of an SM
+constexpr size_t ROW_SMEM_FIXED = 4 << 10;  // what a row kernel takes besides its dynamic part (and 1 KB of the system's)
+inline RowShape row_shape(const LogitRows& in, int top_k, size_t smem) {
   const int L = leaves_of(in.n);
   const uint32_t T = static_cast<uint32_t>(in.T);
-  const bool few_rows = T <= 4 * 152;
-  const int fewest = L >= 8 || (few_rows && top_k > 32) ? 8 : few_rows && top_k > 0 && L < 4 ? 4 : L < 2 ? 2 : L;
-  RowShape best{1, 32 * fewest};
+  const bool few_rows = T <= 4 * 152, top = top_k > 0;
+  const int usual = L >= 8 || (few_rows && top_k > 32) ? 8 : few_rows && top && L < 4 ? 4 : L < 2 ? 2 : L;
+  const int least_warps = L >= 8 && L <= 100 ? 4 : usual;  // of a CTA that has a row to itself
+  RowShape best{1, 32 * (top ? usual : least_warps)};
   if (T >= 16 * 152) return best;
+  const uint32_t fit = static_cast<uint32_t>(SM_SMEM / smem);
   uint32_t least = UINT32_MAX;
   for (int c = 1, half = 0; c <= MAX_CLUSTER; c *= 2, ++half) {
     const int each = (L + c - 1) / c;  // leaves of a CTA: more warps would idle
-    for (int w : {fewest, 10, 12, 14, 16, 20, 25, 32, each}) {
-      if (w < fewest || w > 32 || (w > fewest && w > each)) continue;
-      const uint32_t room = 152u * (32 / w), waves = (T * c + room - 1) / room;
+    for (int w : {4, 5, 6, 7, usual, 10, 12, 14, 16, 20, 25, 32, each}) {
+      if (w > 32 || w < (c == 1 ? least_warps : usual) || (w > usual && w > each)) continue;
+      const uint32_t ctas = 32u / w < fit ? 32u / w : fit, room = 152u * (ctas ? ctas : 1), waves = (T * c + room - 1) / room;
       const uint32_t cost = waves * (2 * ((L + c * w - 1) / (c * w)) + 4 + half);
       if (cost < least) least = cost, best = RowShape{c, 32 * w};
     }

@@ -462,12 +462,12 @@ rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t T, int6
   a.entropy = entropy;
   a.top_ids = top_ids;
   a.top_logp = top_logp;
-  const RowShape shape = row_shape(a.in, top_k);
+  const size_t smem = row_smem_bytes(a.in.n, top_k > 0);
+  const RowShape shape = row_shape(a.in, top_k, smem + (top_k ? sizeof(TopSmem) : 0) + ROW_SMEM_FIXED);
   a.cluster = shape.cluster;
   return with_types(dtype, aligned_rows(logits, ld, dtype_bytes(dtype)), [&](auto e, auto al) {
     using E = decltype(e);
     constexpr bool AL = decltype(al)::value;
-    const size_t smem = row_smem_bytes(a.in.n, top_k > 0);
     return top_k ? launch_rows(token_logprobs_kernel<E, true, AL>, a, T * a.cluster, a.cluster, smem, stream, shape.threads)
                  : launch_rows(token_logprobs_kernel<E, false, AL>, a, T * a.cluster, a.cluster, smem, stream, shape.threads);
   });
