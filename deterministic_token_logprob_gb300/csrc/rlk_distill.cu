@@ -448,10 +448,12 @@ rlk_status launch_distill_bwd(DistillArgs a, int32_t dtype, int32_t out_dtype, v
 
 // The one-launch step: the smallest cluster whose CTAs hold their share of the row in a quarter of
 // an SM's shared memory, or else in a half or the whole. 0: take two launches -- where the row does
-// not fit, or where a cluster of more than two has more than four waves of rows to work through. A
-// cluster's CTAs wait for one another's sums, and what is resident does not cover that wait: 1024
-// rows of 151936 in bf16 (clusters of 8) take 158 us in one launch and 155 in two, 8192 1205 and
-// 1069, but 256 rows 46 and 57.
+// not fit, or where a cluster of more than two (in fp32, with half as many leaves in the same memory, of
+// two) has more than four waves of rows to work through. A cluster's CTAs wait for one another's sums,
+// and what is resident does not cover that wait: 8192 rows of 151936 in bf16 (clusters of 8) take 1205
+// us in one launch and 1069 in two, 4096 of 16000 in fp32 (of 2) 156 and 137, but 600 of them 25 and
+// 30, 500 of 100000 in bf16 (of 4) 50 and 59, 4096 of 50176 (of 2) 184 and 201, 8192 of 16000 (one CTA)
+// 119 and 153.
 constexpr size_t kStepSmem = 220 << 10;
 
 size_t step_smem(int n_leaves, int cluster, int slot) {
@@ -463,7 +465,7 @@ int step_cluster(const LogitRows& in, int slot) {
   for (int ctas = STEP_CTAS; ctas >= 1; ctas /= 2)
     for (int c = 1; c <= MAX_CLUSTER; c *= 2)
       if (step_smem(L, c, slot) <= kStepSmem / ctas && (L + c - 1) / c <= STEP_MAX_ROUNDS * (STEP_THREADS / 32 - 1))
-        return c <= 2 || static_cast<int64_t>(in.T) * c <= 4 * 152 * ctas ? c : 0;
+        return c <= (slot == slot_bytes<F32>() ? 1 : 2) || static_cast<int64_t>(in.T) * c <= 4 * 152 * ctas ? c : 0;
   return 0;
 }
 
