@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const Disti
 // w + W, ..., and copies all of them asynchronously before anything else, one copy group a leaf,
 // so that the whole row is in flight at once and each leaf is summed as it arrives. The warp that
 // summed a leaf writes its gradient: nothing but the leaves' statistics (to every CTA) and the
-// lse crosses warps. 2048 rows of 50257 in bf16 take 112 us, two launches 134; 16 rows of 4096 4.2 us
-// on the GPU.
+// lse crosses warps. 2048 rows of 50257 in bf16 take 112 us, two launches 123; 16 rows of 4096 in
+// fp32 6.4 us with 64 entries, 4.4 with 8, two launches 8.5.
 constexpr int STEP_THREADS = 288;
 constexpr int STEP_CTAS = 4;              // of one SM
 constexpr int STEP_MAX_ROUNDS = 8;        // leaves of one warp
