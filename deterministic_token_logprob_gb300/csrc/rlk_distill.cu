@@ -78,12 +78,12 @@ struct DistillArgs {
 };
 
 // Loss of one row by one warp (every lane gets it); zk: the student's logits of the entries.
-__device__ __forceinline__ float row_loss(const TeacherRow& q, const float* zk, float lse, float s, int lane) {
+__device__ __forceinline__ float row_loss(const TeacherRow& q, const float* zk, const RowLog& p, float s, int lane) {
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < RLK_MAX_TOP_K / 32; ++i) {
     const int k = lane + 32 * i;
-    if (q.q[k] > 0.f) sum = __fmaf_rn(q.q[k], __fsub_rn(q.logq[k], token_logp(zk[k], s, lse)), sum);
+    if (q.q[k] > 0.f) sum = __fmaf_rn(q.q[k], __fsub_rn(q.logq[k], token_logp(zk[k], s, p)), sum);
   }
   return warp_sum(sum);
 }
@@ -100,13 +100,13 @@ __device__ __forceinline__ void gather_logits(const TeacherRow& q, const R& row,
 }
 
 // The loss's outputs of a row, by one warp.
-__device__ __forceinline__ void put_loss(const DistillArgs& a, int64_t t, const TeacherRow& q, const float* zk, float lse,
-                                         int lane) {
-  const float l = row_loss(q, zk, lse, a.in.s, lane);
+__device__ __forceinline__ void put_loss(const DistillArgs& a, int64_t t, const TeacherRow& q, const float* zk,
+                                         const RowLog& p, int lane) {
+  const float l = row_loss(q, zk, p, a.in.s, lane);
   if (lane != 0) return;
-  a.loss[t] = isnan(lse) || q.bad ? quiet_nan() : l;
-  if (a.lse) a.lse[t] = lse;
-  const int flags = q.bad | (isnan(lse) ? RLK_FLAG_NONFINITE : 0);
+  a.loss[t] = isnan(p.l) || q.bad ? quiet_nan() : l;
+  if (a.lse) a.lse[t] = row_lse(p, a.in.s);
+  const int flags = q.bad | (isnan(p.l) ? RLK_FLAG_NONFINITE : 0);
   if (flags && a.in.err_flag) atomicOr(a.in.err_flag, flags);
 }
 
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const Disti
   row_pass<false, false>(row, in.c, none, sm, C, r, [&] {
     if constexpr (BEHIND) read_teacher();
   });
-  if (r == 0 && warp == 0) put_loss(a, t, q, zk, row_lse(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane), in.s), lane);
+  if (r == 0 && warp == 0) put_loss(a, t, q, zk, row_log(fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane)), lane);
 }
 
 // ---------------------------------------------------------------------------
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ TeacherRow q;
   __shared__ float zk[RLK_MAX_TOP_K];
-  __shared__ float lse_s;
+  __shared__ RowLog p_s;
   constexpr int EB = sizeof(typename E::bits), OB = sizeof(typename O::bits), SLOT = slot_bytes<E>();
   const LogitRows& in = a.in;
   const int C = a.cluster, r = blockIdx.x % C, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -371,8 +371,8 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
   if (C > 1) cluster_sync();
   else __syncthreads();
   if (warp == 0) {
-    const float lse = row_lse(fold_leaves(leaf, n_leaves, in.c, lane), in.s);
-    if (lane == 0) lse_s = lse;
+    const RowLog p = row_log(fold_leaves(leaf, n_leaves, in.c, lane));
+    if (lane == 0) p_s = p;
   } else {
     // the student's logits of the entries: CTA 0 takes all of them from the cluster's slots, for the
     // loss, the others their own, for the gradient
@@ -389,8 +389,9 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
   }
   __syncthreads();
   if (C > 1) cluster_arrive();  // CTA 0 has read the others' slots
-  const float lse = lse_s;
-  if (r == 0 && warp == 0) put_loss(a, t, q, zk, lse, lane);
+  const RowLog p = p_s;
+  const float lse = row_lse(p, in.s);
+  if (r == 0 && warp == 0) put_loss(a, t, q, zk, p, lane);
   const bool live = distill_live(q, lse, g);
   const DistillDz f{in.s, lse, __fmul_rn(in.s, g)};
   auto* out = static_cast<typename O::bits*>(a.out.base) + t * a.out.ld;

@@ -6,6 +6,7 @@
 // x = c (z - M), c = s log2 e, so that 2^x = e^{s (z - M)}:
 //   M = max z,  S = sum 2^x,  U = sum 2^x x
 //   lse = s M + log S,   entropy = -sum p log p = log S - log 2 U / S    (both terms >= 0)
+//   log p = s (z - M) - log S: not s z - lse, whose fp32 lse has lost log S where |s M| is large
 // The row is cut into leaves of 1024 columns. A warp takes a leaf: lane i holds the columns
 // 256 j + 8 i .. + 7 (j = 0..3), takes x about the leaf's own maximum (exact, order-free), and
 // sums even and odd columns separately in ascending order; the lanes combine by an
@@ -411,11 +412,22 @@ __device__ __forceinline__ Stats fold_leaves(const Stats* leaf, int n_leaves, fl
 
 __device__ __forceinline__ float quiet_nan() { return __int_as_float(0x7fc00000); }
 
-// lse = s M + log S; -inf for an empty row, NaN for one that holds NaN or +inf.
-__device__ __forceinline__ float row_lse(const Stats& r, float s) {
-  if (isnan(r.s)) return quiet_nan();
-  if (r.s == 0.f) return neg_inf();
-  return __fmaf_rn(r.m, s, logf(r.s));
+// What a row's log probabilities are formed from: log p = s (z - m) - l, with m = M and l = log S. An
+// empty row has m = -inf (and l = 0), a row that holds NaN or +inf l = NaN.
+struct RowLog {
+  float m, l;
+};
+
+__device__ __forceinline__ RowLog row_log(const Stats& r) {
+  if (isnan(r.s)) return RowLog{quiet_nan(), quiet_nan()};
+  if (r.s == 0.f) return RowLog{neg_inf(), 0.f};
+  return RowLog{r.m, fmaxf(logf(r.s), 0.f)};  // S >= 1, the maximum's own term, but for its rounding
+}
+
+// lse = s M + log S; -inf for an empty row, NaN for one that holds NaN or +inf; infinite where s M is
+// beyond fp32.
+__device__ __forceinline__ float row_lse(const RowLog& q, float s) {
+  return q.m == neg_inf() ? neg_inf() : __fmaf_rn(q.m, s, q.l);
 }
 
 __device__ __forceinline__ float row_entropy(const Stats& r) {
@@ -425,9 +437,12 @@ __device__ __forceinline__ float row_entropy(const Stats& r) {
   return __fsub_rn(logf(r.s), __fmul_rn(kLn2, __fdiv_rn(r.u, r.s)));
 }
 
-// s z - lse with one rounding: log p of the token. -inf where the row is empty.
-__device__ __forceinline__ float token_logp(float z, float s, float lse) {
-  return lse == neg_inf() ? neg_inf() : __fmaf_rn(z, s, -lse);
+// log p = s (z - m) - l of a column. -inf where the row is empty. With s < 1, s z - s m may be within fp32
+// where z - m is not.
+__device__ __forceinline__ float token_logp(float z, float s, const RowLog& q) {
+  if (q.m == neg_inf()) return neg_inf();
+  const float d = __fsub_rn(z, q.m);
+  return d == neg_inf() && s < 1.f ? __fsub_rn(__fmaf_rn(z, s, -__fmul_rn(q.m, s)), q.l) : __fmaf_rn(d, s, -q.l);
 }
 
 // e^{s (z - b)} as the gradient forms it: d = s z - lse (one rounding, small where p counts),

@@ -130,7 +130,8 @@ struct TopSmem {
   int place[PLACES];               // chosen cells (groups at the second attempt)
   int octet[OCTETS];               // first columns of the chosen octets
   int n_place, n_octet, n_cand;
-  float bar, lse;
+  float bar;
+  RowLog q;
 };
 
 // Dynamic shared memory of a row: leaves and cells, or in their place, once they have been used, the
@@ -155,8 +156,9 @@ __host__ __device__ constexpr size_t row_smem_bytes(int n, bool top) {
 //     groups' maxima ahead of it; and so do the k best of those groups' octets.
 //  4. Each candidate's place is the number of candidates ahead of it (many are sorted instead).
 template <class R, class E = typename R::E>
-__device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, unsigned char* dyn, const float* cell, TopSmem& ts,
-                         bool bad, float lse) {
+__device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, unsigned char* dyn, const float* cell, TopSmem& ts) {
+  const RowLog q = ts.q;
+  const bool bad = isnan(q.l);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int K = a.top_k, cells = cells_of(row.n);
   const float bar = ts.bar;
@@ -262,7 +264,7 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, unsigned c
   float* lps = a.top_logp + t * K;
   const auto put = [&](int place, unsigned long long c) {
     ids[place] = static_cast<int64_t>(~static_cast<uint32_t>(c));
-    lps[place] = token_logp(key_value(static_cast<uint32_t>(c >> 32)), a.in.s, lse);
+    lps[place] = token_logp(key_value(static_cast<uint32_t>(c >> 32)), a.in.s, q);
   };
   if ((n + static_cast<int>(blockDim.x) - 1) / static_cast<int>(blockDim.x) * n <= 1024) {  // a pass over the others for each
     for (int i = threadIdx.x; i < n; i += blockDim.x) {
@@ -325,17 +327,17 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(cons
   if (r != 0) return;
   if (warp == (blockDim.x > 32)) {
     const Stats x = fold_leaves(sm.leaf, leaves_of(in.n), in.c, lane);
-    const float lse = row_lse(x, in.s);
-    const bool bad = isnan(lse);
+    const RowLog q = row_log(x);
+    const bool bad = isnan(q.l);
     int before = 0;
     if (rank.on)
       for (int i = lane; i < C * static_cast<int>(blockDim.x >> 5); i += 32) before += counts[i];
     before = __reduce_add_sync(kFullWarp, before);
     if (lane == 0) {
-      if (TOP) ts.lse = lse;
-      if (a.lse) a.lse[t] = lse;
+      if (TOP) ts.q = q;
+      if (a.lse) a.lse[t] = row_lse(q, in.s);
       if (a.entropy) a.entropy[t] = row_entropy(x);
-      if (a.logp) a.logp[t] = rank.ok && !bad ? token_logp(rank.z, in.s, lse) : quiet_nan();
+      if (a.logp) a.logp[t] = rank.ok && !bad ? token_logp(rank.z, in.s, q) : quiet_nan();
       if (a.rank) a.rank[t] = rank.ok && !bad ? 1 + before : 0;
       if (in.err_flag && bad) atomicOr(in.err_flag, RLK_FLAG_NONFINITE);
       if (in.err_flag && a.y && !rank.ok) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
@@ -360,7 +362,7 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(cons
       if (lane == 0) ts.bar = b;
     }
     __syncthreads();
-    find_top(row, a, t, dyn, sm.cell, ts, isnan(ts.lse), ts.lse);
+    find_top(row, a, t, dyn, sm.cell, ts);
   }
 }
 

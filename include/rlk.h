@@ -381,6 +381,12 @@ RLK_API rlk_status rlk_linear_logp_bwd_fp8(const void* h, const void* W, const v
  * columns about their own maximum, then all leaves about the row's), so every output of a row
  * depends on that row's inputs alone: not on T, on the other rows, on alignment or strides, on
  * the launch shape or on the GPU's SM count. e^x = ex2.approx.ftz(x log2 e), log is logf.
+ * Log probabilities (logp, top_logp and those in the distillation loss) are formed as
+ * s (z - M) - log S about the row's maximum M, S = sum e^{s (z - M)}, and are as good for logits far
+ * from zero -- an offset, a low temperature, a row masked wholly by a finite value -- as for others; they
+ * are never above 0. lse = s M + log S is one fp32: it loses 2^-24 |lse|, and is infinite where s M is
+ * beyond fp32's range (bf16 or fp32 logits of the type's lowest value at a temperature below 1), while
+ * the row's other outputs are not.
  * Nothing needs a workspace. T == 0 returns RLK_OK and launches nothing.
  *
  * Special rows. -inf logits are masked columns: probability 0. A row of nothing but -inf has

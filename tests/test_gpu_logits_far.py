@@ -1,0 +1,159 @@
+"""Rows whose logits lie far from zero -- offsets, low temperatures, masks by a finite value, s z
+beyond the range of fp32 -- against plain 64-bit forms about the row's maximum M:
+
+  d = s (z - M),  L = log sum e^d,  log p = d - L
+
+Error of a log probability: L is off by the row sum's relative error EPS_SUM (logits_ref) and its own
+rounding, d by the roundings of s, of z - M and of the product, each 2^-24 |d|; none grows with |s M|.
+Where M and z are far apart, z - M or log p may leave fp32's range: then both are -inf."""
+import math
+
+import pytest
+import torch
+
+import logits_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.bfloat16, torch.float16, torch.float32]
+INF = math.inf
+TEMPERATURES = [1.0, 0.7, 0.01, 1e-3, 1e-6, 3.0]
+
+
+@pytest.fixture(scope="module")
+def rlk():
+    from deterministic_token_logprob_gb300 import build
+    build.build()
+    import deterministic_token_logprob_gb300 as m
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return m
+
+
+def far_rows(dtype, n, seed):
+    """Rows far from zero; row 12 is ordinary, row 13 empty."""
+    lowest = torch.finfo(dtype).min
+    mask = -6e4 if dtype == torch.float16 else -1e9
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def randn():
+        return torch.randn(n, generator=gen, device="cuda")
+
+    hide = torch.rand((3, n), generator=gen, device="cuda") < 0.95
+    col = torch.arange(n, device="cuda")
+    rows = [
+        torch.full((n,), lowest, device="cuda"),                     # masked wholly, by the type's lowest value
+        torch.full((n,), mask, device="cuda"),                       # and by a usual one
+        torch.full((n,), -3000.0, device="cuda"),
+        torch.where(hide[0], lowest, randn() * 3),                   # masked partly
+        torch.where(hide[1], mask, randn() * 3),
+        randn() + 1000,                                              # an offset
+        randn() * 2 + 30,                                            # usual logits (far at a low temperature)
+        randn() * 500 - 20000,
+        torch.where(col % 2 == 0, -INF, lowest),                     # masked both ways
+        torch.where(col == n // 2, lowest, -INF),                    # one finite column, the lowest
+        torch.full((n,), -lowest, device="cuda"),                    # the largest value everywhere
+        torch.where(col % 3 == 0, 512.0, 511.0),
+        randn() * 3,
+        torch.full((n,), -INF, device="cuda"),
+    ]
+    return torch.stack(rows).to(dtype), gen
+
+
+def exact(z, s):
+    """(d, L, log p) in 64 bits; an empty row has log p -inf and L 0."""
+    z = z.double()
+    M = z.max(1, keepdim=True).values
+    d = torch.where(z == -INF, z, s * (z - torch.where(M == -INF, torch.zeros_like(M), M)))
+    L = torch.where(M == -INF, torch.zeros_like(M), d.exp().sum(1, keepdim=True).log())
+    return d, L, d - L
+
+
+def logp_tolerance(d, L):
+    """Of log probabilities with this distance d from the row's maximum."""
+    d = torch.where(d.isfinite(), d.abs(), torch.zeros_like(d))
+    return ref.EPS_SUM + ref.EPS * (2 * d + 2 * L.abs() + 1)
+
+
+@pytest.mark.parametrize("temperature", TEMPERATURES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,copies", [(1, 1), (40, 1), (5003, 1), (5003, 100), (40000, 1), (40000, 30)])
+def test_scores_far_from_zero(rlk, dtype, temperature, n, copies):
+    z, gen = far_rows(dtype, n, seed=n)
+    z = z.repeat(copies, 1)                        # other launch shapes
+    T, s = z.shape[0], 1.0 / temperature
+    y = torch.randint(0, n, (T,), generator=gen, device="cuda")
+    d, L, lp = exact(z, s)
+    for k in (0, 20):
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        r = rlk.token_logprobs(z, y, top_k=k, temperature=temperature, err_flag=err)
+        at = y[:, None]
+        ref.assert_within(r.logp, lp.gather(1, at)[:, 0], logp_tolerance(d.gather(1, at), L)[:, 0], "logp")
+        assert not (r.logp > 0).any()
+        want = ref.scores(z, n, s, y, k)           # its lse, entropy and whole numbers are safe
+        lse0 = torch.where(want["lse"].isfinite(), want["lse"].abs(), torch.zeros_like(want["lse"]))
+        ref.assert_within(r.lse, want["lse"], ref.EPS_SUM + 2 * ref.EPS * lse0, "lse")
+        ref.assert_within(r.entropy, want["entropy"], ref.EPS_SUM * (2 + 2 * want["entropy"]), "entropy")
+        assert torch.equal(r.rank, want["rank"])
+        if k:
+            assert torch.equal(r.top_ids, want["top_ids"])
+            none = r.top_ids < 0
+            at = r.top_ids.clamp(min=0)
+            ref.assert_within(r.top_logp, lp.gather(1, at).masked_fill(none, -INF),
+                              logp_tolerance(d.gather(1, at), L), "top_logp")
+            assert not (r.top_logp > 0).any()
+        assert int(err) == 0
+
+
+def near_teacher(z, K, gen):
+    """Entries among the row's best columns (a mask's log probability may leave fp32's range), some
+    absent; for z of one column or more."""
+    T, n = z.shape
+    best = z.float().topk(min(n, 2 * K), 1).indices
+    ids = best.gather(1, torch.randint(0, best.shape[1], (T, K), generator=gen, device="cuda"))
+    ids = torch.where(z.gather(1, ids) < z.float().max(1, keepdim=True).values - 1e4, torch.full_like(ids, -1), ids)
+    ids[::3, -1] = -1
+    return ids, torch.randn((T, K), generator=gen, device="cuda") * 4 - 2000
+
+
+def loss_and_tolerance(z, s, ids, t):
+    d, L, lp = exact(z, s)
+    q, logq, _ = ref.teacher(ids, t, z.shape[1], s)
+    at = ids.clamp(min=0)
+    term = logq - lp.gather(1, at)
+    loss = torch.where(q > 0, q * term, torch.zeros_like(q)).sum(1)
+    # q and log q: ex2, the sum over K and its logarithm (16 eps), |log q| in the exponent; then the sums
+    tol = q * (logp_tolerance(d.gather(1, at), L) + ref.EPS * (16 + 4 * logq.abs()) * (1 + term.abs()))
+    return loss, torch.where(q > 0, tol, torch.zeros_like(q)).sum(1) + ref.EPS
+
+
+@pytest.mark.parametrize("temperature", TEMPERATURES)
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,copies", [(1, 1), (40, 1), (5003, 1), (5003, 100), (40000, 1), (40000, 60)])
+def test_distillation_loss_far_from_zero(rlk, dtype, temperature, n, copies):
+    z, gen = far_rows(dtype, n, seed=n + 1)
+    z = z.repeat(copies, 1)
+    ids, t = near_teacher(z, 12, gen)
+    s = 1.0 / temperature
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss, lse = rlk.distill_topk_fwd(z, ids, t, temperature=temperature, err_flag=err)
+    want, tol = loss_and_tolerance(z, s, ids, t)
+    ref.assert_within(loss, want, tol, "loss")
+    g = torch.zeros(z.shape[0], device="cuda")
+    loss2, lse2, _ = rlk.distill_topk_fwd_bwd(z, ids, t, g, temperature=temperature, err_flag=err)
+    assert torch.equal(loss2, loss) and torch.equal(lse2, lse)
+    assert int(err) == 0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_a_mask_that_leaves_nothing_gives_a_uniform_row(rlk, dtype):
+    """The divergence from one teacher token to n equal ones is log n, and no log probability is above 0."""
+    n = 50257
+    for value in (torch.finfo(dtype).min, -6e4, -1e4):
+        z = torch.full((2, n), value, dtype=dtype, device="cuda")
+        y = torch.tensor([0, n - 1], device="cuda")
+        for tau in (1.0, 0.5):
+            r = rlk.token_logprobs(z, y, top_k=3, temperature=tau)
+            loss, _ = rlk.distill_topk_fwd(z, y[:, None], torch.zeros((2, 1), device="cuda"), temperature=tau)
+            tol = ref.EPS_SUM + 2 * ref.EPS * math.log(n)
+            for got, sign in ((r.logp, -1), (r.top_logp, -1), (r.entropy, 1), (loss, 1)):
+                assert float((got - sign * math.log(n)).abs().max()) <= tol, (value, tau)
