@@ -111,12 +111,13 @@ __device__ __forceinline__ void put_loss(const DistillArgs& a, int64_t t, const 
 }
 
 __device__ __forceinline__ bool distill_live(const TeacherRow& q, float lse, float g) {
-  return !isnan(lse) && lse != neg_inf() && q.any && !q.bad && g != 0.f;
+  return !isnan(lse) && q.any && !q.bad && g != 0.f;
 }
 
 // dz of entry k's column, A (p - sum of q over the entries of that column in ascending order), if k
 // is the first of them; false otherwise.
-__device__ __forceinline__ bool entry_dz(const TeacherRow& q, int k, int K, float z, float s, float lse, float A, float* dz) {
+__device__ __forceinline__ bool entry_dz(const TeacherRow& q, int k, int K, float z, float s, const RowLog& p, float A,
+                                         float* dz) {
   const int id = q.id[k];
   float qk = 0.f;
   for (int j = 0; j < K; j += 4) {  // places past K hold no entry
@@ -128,27 +129,40 @@ __device__ __forceinline__ bool entry_dz(const TeacherRow& q, int k, int K, floa
       qk = __fadd_rn(qk, q.q[j + e]);
     }
   }
-  *dz = __fmul_rn(A, __fsub_rn(prob_of(__fmaf_rn(z, s, -lse)), qk));
+  *dz = __fmul_rn(A, __fsub_rn(prob_of(log_p<true>(z, s, p)), qk));
   return true;
 }
 
-// dz = A p, p = e^{s z - lse}.
+// dz = A p, log p = s (z - m) - l.
+template <bool AWAY>
 struct DistillDz {
-  float s, lse, A;
-  __device__ __forceinline__ float one(float z, int) const { return __fmul_rn(A, prob_of(__fmaf_rn(z, s, -lse))); }
+  float s;
+  RowLog p;
+  float A;
+  __device__ __forceinline__ float one(float z, int) const {
+    return __fmul_rn(A, prob_of(log_p<AWAY>(z, s, p)));
+  }
   template <class E>
   __device__ __forceinline__ void pack(const Pack<E>& k, int, float (&v)[8]) const {
-    const F32x2 ss = pack_f32x2(s, s), nl = pack_f32x2(-lse, -lse), le = pack_f32x2(kLog2e, kLog2e), AA = pack_f32x2(A, A);
+    const F32x2 le = pack_f32x2(kLog2e, kLog2e), AA = pack_f32x2(A, A);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 z = pair(k, i);
-      const float2 x = unpack_f32x2(mul2(fma2(pack_f32x2(z.x, z.y), ss, nl), le));
+      const float2 x = unpack_f32x2(mul2(log_p<AWAY>(pair(k, i), s, p), le));
       const float2 r = unpack_f32x2(mul2(AA, pack_f32x2(ex2_approx(x.x), ex2_approx(x.y))));
       v[2 * i] = r.x;
       v[2 * i + 1] = r.y;
     }
   }
 };
+
+// The teacher's columns, written over the stream's; k: this thread's entry if it is one to write, else -1.
+template <class G>
+__device__ __forceinline__ void patch_entry(const TeacherRow& q, int k, int K, float z, float s, const RowLog& p, float A,
+                                            const G& out) {
+  __syncthreads();
+  float dz;
+  if (k >= 0 && entry_dz(q, k, K, z, s, p, A, &dz)) out.put(q.id[k], dz);
+}
 
 // Backward alone: a.cluster CTAs of a row, each its own part. Columns outside the teacher's entries have
 // dz = A p; the entries, few, are written over it, so the stream over the row does not look for them.
@@ -159,6 +173,7 @@ template <class E, class O, bool AL>
 __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const DistillArgs a) {
   __shared__ TeacherRow q;
   __shared__ float zk[RLK_MAX_TOP_K];
+  extern __shared__ __align__(16) unsigned char dyn[];
   const LogitRows& in = a.in;
   const int64_t t = blockIdx.x / a.cluster;
   const auto* z = static_cast<const typename E::bits*>(in.base) + t * in.ld;
@@ -183,14 +198,22 @@ __global__ void __launch_bounds__(ROW_THREADS) distill_grad_kernel(const Distill
   if (q.bad && part.lo == 0 && threadIdx.x == 0 && in.err_flag) atomicOr(in.err_flag, q.bad);
   const bool live = distill_live(q, lse, g);
   const float A = __fmul_rn(in.s, g);
-  write_part<GRAD_PACKS>(part, live, DistillDz{in.s, lse, A});
   const int k = threadIdx.x;
   static_assert(RLK_MAX_TOP_K <= ROW_THREADS, "a thread an entry");
-  const bool patches = live && k < a.K && part.owns(q.id[k]);
+  if (live && lse_is_coarse<O>(lse)) {  // the first of the row's CTAs reads and writes all of it
+    if (part.lo != 0) return;
+    const bool entry = k < a.K && q.id[k] >= 0;
+    const float zy = entry ? E::to_f32(z[q.id[k]]) : 0.f;
+    const RowLog p = read_row_log<E>(z, in.n, in.c, reinterpret_cast<Stats*>(dyn), in.err_flag);
+    write_row<E, O>(z, in.n, part.out, a.out.V, p.m != neg_inf(), DistillDz<true>{in.s, p, A});
+    patch_entry(q, entry && p.m != neg_inf() ? k : -1, a.K, zy, in.s, p, A, part);
+    return;
+  }
+  const RowLog p{0.f, lse};
+  write_part<GRAD_PACKS>(part, live && lse != neg_inf(), DistillDz<false>{in.s, p, A});
+  const bool patches = live && lse != neg_inf() && k < a.K && part.owns(q.id[k]);
   const float zy = !patches ? 0.f : in_place ? zk[k] : E::to_f32(z[q.id[k]]);  // from L2 now
-  __syncthreads();
-  float dz;
-  if (patches && entry_dz(q, k, a.K, zy, in.s, lse, A, &dz)) part.put(q.id[k], dz);
+  patch_entry(q, patches ? k : -1, a.K, zy, in.s, p, A, part);
 }
 
 // Forward: a cluster of CTAs a row. The last warp of CTA 0 gathers the student's logits at the teacher's
@@ -389,19 +412,27 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
   }
   __syncthreads();
   if (C > 1) cluster_arrive();  // CTA 0 has read the others' slots
-  const RowLog p = p_s;
-  const float lse = row_lse(p, in.s);
+  RowLog p = p_s;
   if (r == 0 && warp == 0) put_loss(a, t, q, zk, p, lane);
-  const bool live = distill_live(q, lse, g);
-  const DistillDz f{in.s, lse, __fmul_rn(in.s, g)};
+  const float lse = row_lse(p, in.s);
+  const bool live = p.m != neg_inf() && distill_live(q, lse, g);
+  const bool coarse = lse_is_coarse<O>(lse);
+  if (!coarse) p = RowLog{0.f, lse};  // as the backward alone
+  const float A = __fmul_rn(in.s, g);
   auto* out = static_cast<typename O::bits*>(a.out.base) + t * a.out.ld;
   const int V = a.out.V;
   const int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / OB;  // of the row and of every leaf
   for (int j = 0; j < rounds; ++j) {
-    const int i = warp + j * W;
-    const Row<E, GAL> view(reinterpret_cast<const typename E::bits*>(slots + i * SLOT + row.shift) + head,
-                           ROW_LEAF + SLOT_SLACK / EB, in.err_flag, row.shift + head * EB);
-    leaf_grad<O>(view, out, (r + i * C) * ROW_LEAF, head, in.n, V, live, f, lane);
+    const int i = warp + j * W, c0 = (r + i * C) * ROW_LEAF;
+    const auto* first = reinterpret_cast<const typename E::bits*>(slots + i * SLOT + row.shift);
+    if (coarse) {  // rare; the difference z - m in the stream over all rows takes 2 % (2048 of 50257 in bf16: 112 -> 114 us)
+      const DistillDz<true> f{in.s, p, A};
+      for (int c = lane; c < min(V - c0, ROW_LEAF); c += 32)
+        out[c0 + c] = O::from_f32(live && c0 + c < in.n ? f.one(E::to_f32(first[c]), c0 + c) : 0.f);
+    } else {
+      const Row<E, GAL> view(first + head, ROW_LEAF + SLOT_SLACK / EB, in.err_flag, row.shift + head * EB);
+      leaf_grad<O>(view, out, c0, head, in.n, V, live, DistillDz<false>{in.s, p, A}, lane);
+    }
   }
   // columns past the last leaf
   for (int c = n_leaves * ROW_LEAF + r * blockDim.x + threadIdx.x; c < V; c += C * blockDim.x) out[c] = O::from_f32(0.f);
@@ -410,7 +441,7 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
     for (int k = threadIdx.x; k < a.K; k += blockDim.x) {
       const int id = q.id[k];
       float dz;
-      if (id >= 0 && id / ROW_LEAF % C == r && entry_dz(q, k, a.K, zk[k], in.s, lse, f.A, &dz)) out[id] = O::from_f32(dz);
+      if (id >= 0 && id / ROW_LEAF % C == r && entry_dz(q, k, a.K, zk[k], in.s, p, A, &dz)) out[id] = O::from_f32(dz);
     }
   }
   if (C > 1) cluster_wait();
@@ -443,7 +474,8 @@ rlk_status launch_distill_bwd(DistillArgs a, int32_t dtype, int32_t out_dtype, v
   const int64_t ctas = static_cast<int64_t>(a.in.T) * a.cluster;
   if (ctas > INT32_MAX) return RLK_ERR_UNSUPPORTED;
   return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto al) {
-    return launch_rows(distill_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, ctas, 1, 0, stream);
+    return launch_rows(distill_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, ctas, 1,
+                       leaves_of(a.in.n) * sizeof(Stats), stream);
   });
 }
 

@@ -36,6 +36,7 @@ constexpr uint32_t kFullWarp = 0xffffffffu;
 struct Bf16 {
   using bits = uint16_t;
   static constexpr bits kNegInf = 0xFF80u;
+  static constexpr float kLseRange = 4096.f;  // see lse_is_coarse
   static constexpr int kKeyShift = 16;  // low bits of the fp32 image that carry nothing
   static __device__ __forceinline__ float to_f32(bits b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
   static __device__ __forceinline__ bits from_f32(float v) { return static_cast<bits>(pack_bf16x2(v, 0.f) & 0xFFFFu); }
@@ -57,6 +58,7 @@ struct Bf16 {
 struct F16 {
   using bits = uint16_t;
   static constexpr bits kNegInf = 0xFC00u;
+  static constexpr float kLseRange = 512.f;  // see lse_is_coarse
   static constexpr int kKeyShift = 13;
   static __device__ __forceinline__ float to_f32(bits b) { return __half2float(__ushort_as_half(b)); }
   static __device__ __forceinline__ bits from_f32(float v) { return __half_as_ushort(__float2half_rn(v)); }
@@ -80,6 +82,7 @@ struct F16 {
 struct F32 {
   using bits = uint32_t;
   static constexpr bits kNegInf = 0xFF800000u;
+  static constexpr float kLseRange = 256.f;  // see lse_is_coarse
   static constexpr int kKeyShift = 0;
   static __device__ __forceinline__ float to_f32(bits b) { return __uint_as_float(b); }
   static __device__ __forceinline__ bits from_f32(float v) { return __float_as_uint(v); }
@@ -320,19 +323,31 @@ __device__ __forceinline__ float2 warp_sum_pair(float a, float b, int lane) {
   return make_float2(v, __shfl_down_sync(kFullWarp, v, 16));
 }
 
-// s and, with ENT, u of a leaf about its maximum m (not -inf), in powers of two: x = c z - b with
-// b = rn(c m), so that an element takes one product-and-sum, and *r = b - c m, which fold_leaves takes
-// out again. Where |b| is so large that its rounding counts in the exponent, x comes from z - m (r = 0).
-// NaN or +inf among the columns makes s NaN.
+// The exponents of a leaf about its maximum m (not -inf), in powers of two: x = c z - b with b = rn(c m),
+// so that an element takes one product-and-sum, and r = b - c m, which fold_leaves takes out again. Where |b| is
+// so large that its rounding counts in the exponent (`over`), x comes from z - m (r = 0). of() gives
+// either in one form, c (z - 0) - b with the same bits or c (z - m) - 0.
+struct LeafBase {
+  float b, r, nm, nb;
+  bool over;
+  __device__ __forceinline__ float of(float z, float c) const { return __fmaf_rn(__fadd_rn(z, nm), c, nb); }
+};
+__device__ __forceinline__ LeafBase leaf_base(float m, float c) {
+  const float b = __fmul_rn(m, c);
+  const bool over = !(fabsf(b) <= 268435456.f);  // 2^28: up to there |r| <= 16, far inside the range of 2^r
+  return LeafBase{b, over ? 0.f : -__fmaf_rn(m, c, -b), over ? -m : 0.f, over ? 0.f : -b, over};
+}
+
+// s and, with ENT, u of a leaf about its maximum m (not -inf), and *r. NaN or +inf among the columns makes
+// s NaN.
 template <bool ENT, class E>
 __device__ __forceinline__ float2 leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], float m, float c, float* r, int lane) {
   constexpr float kHuge = 3.4028235e38f;
-  const float b = __fmul_rn(m, c);
-  *r = -__fmaf_rn(m, c, -b);
-  const bool over = !(fabsf(b) <= 268435456.f);  // 2^28: up to there |r| <= 16, far inside the range of 2^r
+  const LeafBase at = leaf_base(m, c);
+  *r = at.r;
   float sl = 0.f, ul = 0.f;
   const auto sums = [&] {
-    const F32x2 nb = pack_f32x2(-b, -b), cc = pack_f32x2(c, c);
+    const F32x2 nb = pack_f32x2(-at.b, -at.b), cc = pack_f32x2(c, c);
     F32x2 s2 = 0, u2 = 0;  // even and odd columns
 #pragma unroll
     for (int j = 0; j < LEAF_GROUPS; ++j)
@@ -349,31 +364,28 @@ __device__ __forceinline__ float2 leaf_sums(const Pack<E> (&k)[LEAF_GROUPS], flo
     sl = __fadd_rn(s.x, s.y);
     if constexpr (ENT) ul = __fadd_rn(u.x, u.y);
   };
-  // x = c (z - 0) - b, the same bits, kept finite where a masked column (weight 0) has -inf (a NaN logit
-  // reaches s through its weight); or x = c (z - m) - 0 with `over`. In single values: paired
-  // ones spill (4096 rows of 151936 in fp32 with 64 alternatives: 386 -> 418 us).
+  // x kept finite where a masked column (weight 0) has -inf (a NaN logit reaches s through its weight), or
+  // with `over`. In single values: paired ones spill (4096 rows of 151936 in fp32 with 64 alternatives: 386 -> 418 us).
   const auto careful_sums = [&] {
-    const float nm = over ? -m : 0.f, nb = over ? 0.f : -b;
     float v[2] = {0.f, 0.f}, w[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < LEAF_GROUPS; ++j)
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float2 z = pair(k[j], i / 2);
-        const float x = __fmaf_rn(__fadd_rn(i & 1 ? z.y : z.x, nm), c, nb), e = ex2_approx(x);
+        const float x = at.of(i & 1 ? z.y : z.x, c), e = ex2_approx(x);
         w[i & 1] = __fadd_rn(w[i & 1], e);
         if constexpr (ENT) v[i & 1] = __fmaf_rn(e, fmaxf(x, -kHuge), v[i & 1]);
       }
     sl = __fadd_rn(w[0], w[1]);
     ul = __fadd_rn(v[0], v[1]);
   };
-  if (over) *r = 0.f;
   if constexpr (!ENT) {
-    if (over) careful_sums();
+    if (at.over) careful_sums();
     else sums();
   } else {
     sums();
-    if (over || __any_sync(kFullWarp, isnan(ul))) careful_sums();
+    if (at.over || __any_sync(kFullWarp, isnan(ul))) careful_sums();
   }
   if constexpr (!ENT) return make_float2(warp_sum(sl), 0.f);
   return warp_sum_pair(sl, ul, lane);
@@ -424,10 +436,12 @@ __device__ __forceinline__ RowLog row_log(const Stats& r) {
   return RowLog{r.m, fmaxf(logf(r.s), 0.f)};  // S >= 1, the maximum's own term, but for its rounding
 }
 
-// lse = s M + log S; -inf for an empty row, NaN for one that holds NaN or +inf; infinite where s M is
-// beyond fp32.
+// lse = s M + log S; -inf for an empty row alone, NaN for one that holds NaN or +inf. Where s M is beyond
+// fp32 it is +inf or, below, the lowest finite value.
 __device__ __forceinline__ float row_lse(const RowLog& q, float s) {
-  return q.m == neg_inf() ? neg_inf() : __fmaf_rn(q.m, s, q.l);
+  if (q.m == neg_inf()) return neg_inf();
+  const float lse = __fmaf_rn(q.m, s, q.l);
+  return lse == neg_inf() ? -3.4028235e38f : lse;
 }
 
 __device__ __forceinline__ float row_entropy(const Stats& r) {
@@ -445,8 +459,20 @@ __device__ __forceinline__ float token_logp(float z, float s, const RowLog& q) {
   return d == neg_inf() && s < 1.f ? __fsub_rn(__fmaf_rn(z, s, -__fmul_rn(q.m, s)), q.l) : __fmaf_rn(d, s, -q.l);
 }
 
-// e^{s (z - b)} as the gradient forms it: d = s z - lse (one rounding, small where p counts),
-// p = ex2(d log2 e).
+// log p of a column and of a pair, d = s (z - m) - l, as the gradients form it. AWAY: m may be other than 0
+// (z - 0 is z: the bits are the same).
+template <bool AWAY>
+__device__ __forceinline__ float log_p(float z, float s, const RowLog& q) {
+  return __fmaf_rn(AWAY ? __fsub_rn(z, q.m) : z, s, -q.l);
+}
+template <bool AWAY>
+__device__ __forceinline__ F32x2 log_p(float2 z, float s, const RowLog& q) {
+  F32x2 x = pack_f32x2(z.x, z.y);
+  if constexpr (AWAY) x = add2(x, pack_f32x2(-q.m, -q.m));
+  return fma2(x, pack_f32x2(s, s), pack_f32x2(-q.l, -q.l));
+}
+
+// e^d as the gradients form it, d = log p.
 __device__ __forceinline__ float prob_of(float d) { return ex2_approx(__fmul_rn(d, kLog2e)); }
 
 // ---------------------------------------------------------------------------

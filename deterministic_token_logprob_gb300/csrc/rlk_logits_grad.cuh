@@ -121,6 +121,77 @@ __device__ __forceinline__ void write_part(const G& g, bool live, const F& f) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// log p from the caller's lse, or from the row again
+// ---------------------------------------------------------------------------
+// The gradient needs log p = s (z - m) - l of every column. The forward's lse serves as l, with m = 0,
+// while its rounding, 2^-24 |lse|, which is a relative error of every p, stays small against what p has
+// anyway: against the sum's error (2^-17) for a gradient in fp32, up to |lse| = 256; against an eighth of
+// the gradient's own rounding in f16 (2^-12, up to 512) and in bf16 (2^-9, up to 4096). Beyond that --
+// a large offset, a low temperature, a row masked wholly by a finite value -- one fp32 does not hold
+// log S well enough (at 10^9 not at all), and M and log S come from the row once more.
+
+// Whether the row of this lse (not NaN) is to be read again, for a gradient of type O.
+template <class O>
+__device__ __forceinline__ bool lse_is_coarse(float lse) {
+  return fabsf(lse) > O::kLseRange && lse != neg_inf();
+}
+
+// M and log S of a row, by one CTA, with the forward's bits: every leaf as in leaf_pass, its statistics
+// (leaf: shared memory for the row's leaves) folded by fold_leaves. Every thread has read the row when it
+// returns. A leaf is read twice, pack by pack, and write_row goes element by element: such rows are rare,
+// and this small they leave the stream over the others its registers (whole leaves in registers, or packs in
+// write_row, cost the gradients of other rows 2 to 13 %). 8192 rows of 151936 in bf16 take 4.0 ms where all
+// of them come here (711 us where none does), 2000 of 50264 in fp32 531 us (122).
+template <class E>
+__device__ __noinline__ RowLog read_row_log(const typename E::bits* z, int n, float c, Stats* leaf, int32_t* err) {
+  __shared__ RowLog found;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5, L = leaves_of(n);
+  const Row<E, false> row(z, n, err);
+  for (int l = warp; l < L; l += warps) {
+    const int c0 = l * ROW_LEAF + lane * 8;
+    const auto octet = [&](int j) {  // this lane's j-th pack
+      const int x = c0 + j * LEAF_GROUP;
+      return packs_inside(row, x, x + 8) ? load_pack(row, x) : load_pack_edge(row, x);
+    };
+    float m = neg_inf();
+#pragma unroll 1
+    for (int j = 0; j < LEAF_GROUPS; ++j) {
+      const Pack<E> k[1] = {octet(j)};
+      m = fmaxf(m, pack_max(k));
+    }
+    m = warp_max(m);
+    const LeafBase at = leaf_base(m, c);
+    float even = 0.f, odd = 0.f;
+#pragma unroll 1
+    for (int j = 0; j < LEAF_GROUPS; ++j) {
+      const Pack<E> k = octet(j);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = pair(k, i);
+        even = __fadd_rn(even, ex2_approx(at.of(x.x, c)));
+        odd = __fadd_rn(odd, ex2_approx(at.of(x.y, c)));
+      }
+    }
+    const float s = m == neg_inf() ? 0.f : warp_sum(__fadd_rn(even, odd));
+    if (lane == 0) leaf[l] = Stats{m, s, 0.f, at.r};
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const RowLog p = row_log(fold_leaves(leaf, L, c, lane));
+    if (lane == 0) found = p;
+  }
+  __syncthreads();
+  return found;
+}
+
+// Writes f of a whole row, by one CTA (zeros when !live); a thread reads the columns that it writes.
+template <class E, class O, class F>
+__device__ __forceinline__ void write_row(const typename E::bits* z, int n, typename O::bits* out, int V, bool live, const F& f) {
+#pragma unroll 4
+  for (int i = threadIdx.x; i < V; i += ROW_THREADS) out[i] = O::from_f32(live && i < n ? f.one(E::to_f32(z[i]), i) : 0.f);
+}
+
 // CTAs of a row in a kernel that writes gradients alone: parts of up to four rounds of every thread's
 // packs (what a CTA does once -- its row's scalars, the teacher's softmax -- is then small: 8192 rows of
 // 151936 in bf16 take 711 us with four rounds, 954 with one), as long as that leaves the GPU full.

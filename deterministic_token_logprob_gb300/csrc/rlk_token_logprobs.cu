@@ -382,29 +382,30 @@ struct TokenGradArgs {
 
 constexpr float kLowestLogp = -1e4f;  // p = 0 far above it, and B d stays a number
 
-// dz = p (A + B d), and p (A + B d) + C at the target, with d = s z - lse = log p. A masked column
+// dz = p (A + B d), and p (A + B d) + C at the target, with d = s (z - m) - l = log p. A masked column
 // (d = -inf) has p = 0 and a finite d.
+template <bool AWAY>
 struct TokenDz {
-  float s, lse, A, B, C;
+  float s;
+  RowLog r;
+  float A, B, C;
   int y;
   __device__ __forceinline__ float one(float z, int c) const {
-    const float d = fmaxf(__fmaf_rn(z, s, -lse), kLowestLogp);
+    const float d = fmaxf(log_p<AWAY>(z, s, r), kLowestLogp);
     const float p = prob_of(d), t = __fmaf_rn(B, d, A);
     return c == y ? __fmaf_rn(p, t, C) : __fmul_rn(p, t);
   }
   template <class E>
   __device__ __forceinline__ void pack(const Pack<E>& k, int c, float (&v)[8]) const {
-    const F32x2 ss = pack_f32x2(s, s), nl = pack_f32x2(-lse, -lse), le = pack_f32x2(kLog2e, kLog2e);
-    const F32x2 AA = pack_f32x2(A, A), BB = pack_f32x2(B, B);
+    const F32x2 le = pack_f32x2(kLog2e, kLog2e), AA = pack_f32x2(A, A), BB = pack_f32x2(B, B);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 z = pair(k, i);
-      const float2 d = unpack_f32x2(fma2(pack_f32x2(z.x, z.y), ss, nl));
+      const float2 d = unpack_f32x2(log_p<AWAY>(pair(k, i), s, r));
       const F32x2 dd = pack_f32x2(fmaxf(d.x, kLowestLogp), fmaxf(d.y, kLowestLogp));
       const float2 x = unpack_f32x2(mul2(dd, le));
-      const float2 r = unpack_f32x2(mul2(pack_f32x2(ex2_approx(x.x), ex2_approx(x.y)), fma2(BB, dd, AA)));
-      v[2 * i] = r.x;
-      v[2 * i + 1] = r.y;
+      const float2 dz = unpack_f32x2(mul2(pack_f32x2(ex2_approx(x.x), ex2_approx(x.y)), fma2(BB, dd, AA)));
+      v[2 * i] = dz.x;
+      v[2 * i + 1] = dz.y;
     }
     if (static_cast<unsigned>(y - c) < 8u) {
 #pragma unroll
@@ -417,25 +418,45 @@ struct TokenDz {
   }
 };
 
+struct TokenRow {  // what a row of the gradient has of its own
+  float g, ge, ent;
+  int64_t y;
+};
+
+template <bool AWAY>
+__device__ __forceinline__ TokenDz<AWAY> token_dz(const TokenGradArgs& a, const RowLog& r, const TokenRow& x) {
+  const float s = a.in.s;
+  return TokenDz<AWAY>{s, r, __fmul_rn(-s, __fmaf_rn(x.ge, x.ent, x.g)), __fmul_rn(-s, x.ge), __fmul_rn(s, x.g),
+                       static_cast<int>(x.y)};
+}
+
 // Nothing but the row's lse, entropy and two weights crosses columns, so a row is cut at will: parts of
 // 8192 to 32768 columns a CTA (grad_parts), in packs whose stores are whole aligned vectors. Bound by
 // memory: 8192 rows of 151936 in bf16 take 711 us for 4.97 GB, 7.0 TB/s.
+// In fp32 to bf16 four CTAs an SM (64 registers) are best: 2000 rows of 50264 take 88.2 us, with the 76 registers
+// that the compiler takes by itself 89.4; in fp32 throughout 129.9 and 120.9.
 template <class E, class O, bool AL>
-__global__ void __launch_bounds__(ROW_THREADS) token_grad_kernel(const TokenGradArgs a) {
+__global__ void __launch_bounds__(ROW_THREADS, AL && sizeof(typename E::bits) > sizeof(typename O::bits) ? 4 : 0)
+token_grad_kernel(const TokenGradArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
   const LogitRows& in = a.in;
   const int64_t t = blockIdx.x / a.parts;
-  const GradPart<E, O, AL> part(static_cast<const typename E::bits*>(in.base) + t * in.ld, in.n,
-                                static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
+  const auto* z = static_cast<const typename E::bits*>(in.base) + t * in.ld;
+  const GradPart<E, O, AL> part(z, in.n, static_cast<typename O::bits*>(a.out.base) + t * a.out.ld, a.out.V,
                                 static_cast<int>(blockIdx.x % a.parts), a.parts, in.err_flag);
-  const float lse = a.lse[t], g = a.g_logp[t], ge = a.g_entropy ? a.g_entropy[t] : 0.f;
-  const float ent = a.g_entropy ? a.entropy[t] : 0.f;
-  const int64_t y = a.y[t];
-  const bool y_ok = y >= 0 && y < in.n;
+  const float lse = a.lse[t];
+  const TokenRow x{a.g_logp[t], a.g_entropy ? a.g_entropy[t] : 0.f, a.g_entropy ? a.entropy[t] : 0.f, a.y[t]};
+  const bool y_ok = x.y >= 0 && x.y < in.n;
   if (!y_ok && threadIdx.x == 0 && part.lo == 0 && in.err_flag) atomicOr(in.err_flag, RLK_FLAG_BAD_TARGET);
-  const bool live = y_ok && !isnan(lse) && lse != neg_inf() && !(g == 0.f && ge == 0.f);
-  const TokenDz dz{in.s, lse, __fmul_rn(-in.s, __fmaf_rn(ge, ent, g)), __fmul_rn(-in.s, ge), __fmul_rn(in.s, g),
-                   static_cast<int>(y)};
-  write_part<GRAD_PACKS>(part, live, dz);  // every thread reads and writes columns of its own
+  const bool live = y_ok && !isnan(lse) && !(x.g == 0.f && x.ge == 0.f);
+  if (live && lse_is_coarse<O>(lse)) {  // the first of the row's CTAs reads and writes all of it
+    if (part.lo != 0) return;
+    const RowLog r = read_row_log<E>(z, in.n, in.c, reinterpret_cast<Stats*>(dyn), in.err_flag);
+    write_row<E, O>(z, in.n, part.out, a.out.V, r.m != neg_inf(), token_dz<true>(a, r, x));
+    return;
+  }
+  // every thread reads and writes columns of its own
+  write_part<GRAD_PACKS>(part, live && lse != neg_inf(), token_dz<false>(a, RowLog{0.f, lse}, x));
 }
 
 }  // namespace
@@ -493,7 +514,8 @@ rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t T, 
   a.parts = grad_parts(a.in, a.out);
   if (T * a.parts > INT32_MAX) return RLK_ERR_UNSUPPORTED;
   return with_types(dtype, out_dtype, aligned_pair(a.in, dtype, a.out, out_dtype), [&](auto e, auto o, auto al) {
-    return launch_rows(token_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, T * a.parts, 1, 0, stream);
+    return launch_rows(token_grad_kernel<decltype(e), decltype(o), decltype(al)::value>, a, T * a.parts, 1,
+                       leaves_of(a.in.n) * sizeof(Stats), stream);
   });
 }
 

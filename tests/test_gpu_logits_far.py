@@ -91,7 +91,8 @@ def test_scores_far_from_zero(rlk, dtype, temperature, n, copies):
         assert not (r.logp > 0).any()
         want = ref.scores(z, n, s, y, k)           # its lse, entropy and whole numbers are safe
         lse0 = torch.where(want["lse"].isfinite(), want["lse"].abs(), torch.zeros_like(want["lse"]))
-        ref.assert_within(r.lse, want["lse"], ref.EPS_SUM + 2 * ref.EPS * lse0, "lse")
+        lse = torch.where((z == -INF).all(1), want["lse"], want["lse"].clamp(min=torch.finfo(torch.float32).min))
+        ref.assert_within(r.lse, lse, ref.EPS_SUM + 2 * ref.EPS * lse0, "lse")   # -inf: an empty row alone
         ref.assert_within(r.entropy, want["entropy"], ref.EPS_SUM * (2 + 2 * want["entropy"]), "entropy")
         assert torch.equal(r.rank, want["rank"])
         if k:
@@ -157,3 +158,135 @@ def test_a_mask_that_leaves_nothing_gives_a_uniform_row(rlk, dtype):
             tol = ref.EPS_SUM + 2 * ref.EPS * math.log(n)
             for got, sign in ((r.logp, -1), (r.top_logp, -1), (r.entropy, 1), (loss, 1)):
                 assert float((got - sign * math.log(n)).abs().max()) <= tol, (value, tau)
+
+
+OUTS = [(torch.bfloat16, None), (torch.float16, None), (torch.float32, None), (torch.float32, torch.bfloat16)]
+
+
+NEAR = {torch.float32: 256, torch.float16: 512, torch.bfloat16: 4096}
+
+
+def p_error(d, L, lp, z, s, out):
+    """(p, relative error of the kernels' p): as of a log probability, then its product with log2 e and
+    ex2. Rows whose |lse| is at most NEAR may take p from the fp32 lse, which is off by 2^-24 |lse|, with
+    s z rounded like it: half of that limit's 2^-23, an eighth of what the output's rounding adds in f16 and
+    bf16."""
+    M = z.double().max(1, keepdim=True).values.nan_to_num(neginf=0.0)
+    near = NEAR[out] * ((s * M + L).abs() <= NEAR[out] + 1).double()
+    a, b = (torch.where(v.isfinite(), v.abs(), torch.zeros_like(v)) for v in (d, lp))
+    return lp.exp(), ref.EPS_SUM + ref.EPS * (2 * a + L.abs() + 2 * b + 8 + near)
+
+
+def token_grad(z, s, y, g, ge, out):
+    """(dlogits, bound of the kernel's error before its output rounding) in 64 bits."""
+    d, L, lp = exact(z, s)
+    p, rel = p_error(d, L, lp, z, s, out)
+    lp = torch.where(p > 0, lp, torch.zeros_like(lp))
+    H = -(p * lp).sum(1, keepdim=True)
+    g, ge = g.double()[:, None], ge.double()[:, None]
+    dz = -s * p * (g + ge * (lp + H))
+    dz.scatter_add_(1, y[:, None], s * g.expand_as(L))
+    size = g.abs() + ge.abs() * (lp.abs() + H)
+    bound = s * p * (rel * size + ge.abs() * (rel + ref.EPS_SUM * (2 + 2 * H)) + 4 * ref.EPS * size)
+    bound = bound + s * 2e-38 * (1 + g.abs() + 200 * ge.abs())     # p flushed to zero
+    bound.scatter_add_(1, y[:, None], s * g.abs().expand_as(L) * 2 * ref.EPS)
+    empty = (z == -INF).all(1, keepdim=True)
+    return dz.masked_fill(empty, 0.0), bound.masked_fill(empty, 0.0)
+
+
+def distill_grad(z, s, ids, t, g, out):
+    d, L, lp = exact(z, s)
+    p, rel = p_error(d, L, lp, z, s, out)
+    q, logq, _ = ref.teacher(ids, t, z.shape[1], s)
+    g = g.double()[:, None]
+    dz, bound = s * g * p, s * g.abs() * (p * (rel + 4 * ref.EPS) + 2e-38)
+    at = ids.clamp(min=0)
+    dz.scatter_add_(1, at, -s * g * q)
+    bound.scatter_add_(1, at, s * g.abs() * q * ref.EPS * (16 + 4 * logq.abs()))
+    none = (z == -INF).all(1, keepdim=True) | ~(q > 0).any(1, keepdim=True)
+    return dz.masked_fill(none, 0.0), bound.masked_fill(none, 0.0)
+
+
+def assert_grad_sums_to_zero(got, want, bound):
+    ref.assert_grad(got, want, bound)
+    dt = got.dtype
+    room = (bound * (1 + ref.OUT_EPS[dt]) + want.abs() * ref.OUT_EPS[dt] + ref.OUT_TINY[dt]).sum(1)
+    total = got.double().sum(1)
+    assert bool((total.abs() <= room + 1e-12).all()), (total, room)
+
+
+@pytest.mark.parametrize("temperature", TEMPERATURES)
+@pytest.mark.parametrize("dtype,out_dtype", OUTS)
+@pytest.mark.parametrize("n,copies", [(1, 1), (40, 1), (5003, 1), (5003, 50), (40000, 1)])
+def test_token_gradient_far_from_zero(rlk, dtype, out_dtype, temperature, n, copies):
+    z, gen = far_rows(dtype, n, seed=n + 2)
+    z = z.repeat(copies, 1)
+    T, s = z.shape[0], 1.0 / temperature
+    y = torch.randint(0, n, (T,), generator=gen, device="cuda")
+    g = torch.randn(T, generator=gen, device="cuda") * min(1.0, temperature)   # s g in the range of f16
+    ge = torch.randn(T, generator=gen, device="cuda") * 0.1 * min(1.0, temperature)
+    r = rlk.token_logprobs(z, y, temperature=temperature)
+    d = rlk.token_logprobs_bwd(z, y, r.lse, r.entropy, g, ge, temperature=temperature, out_dtype=out_dtype)
+    assert_grad_sums_to_zero(d, *token_grad(z, s, y, g, ge, d.dtype))
+    if out_dtype is None:                          # in place: the same bits
+        z2 = z.clone()
+        assert torch.equal(rlk.token_logprobs_bwd(z2, y, r.lse, r.entropy, g, ge, temperature=temperature, out=z2), d)
+    d = rlk.token_logprobs_bwd(z, y, r.lse, None, g, temperature=temperature, out_dtype=out_dtype)
+    assert_grad_sums_to_zero(d, *token_grad(z, s, y, g, torch.zeros_like(g), d.dtype))
+    zero = torch.zeros_like(g)
+    assert torch.count_nonzero(rlk.token_logprobs_bwd(z, y, r.lse, r.entropy, zero, zero, temperature=temperature)) == 0
+
+
+@pytest.mark.parametrize("temperature", TEMPERATURES)
+@pytest.mark.parametrize("dtype,out_dtype", OUTS)
+@pytest.mark.parametrize("n,copies", [(1, 1), (40, 1), (5003, 1), (5003, 50), (40000, 1)])
+def test_distillation_gradient_far_from_zero(rlk, dtype, out_dtype, temperature, n, copies):
+    z, gen = far_rows(dtype, n, seed=n + 3)
+    z = z.repeat(copies, 1)
+    ids, t = near_teacher(z, 12, gen)
+    g = torch.randn(z.shape[0], generator=gen, device="cuda") * min(1.0, temperature)
+    kw = dict(temperature=temperature)
+    _, lse = rlk.distill_topk_fwd(z, ids, t, **kw)
+    d = rlk.distill_topk_bwd(z, ids, t, lse, g, out_dtype=out_dtype, **kw)
+    assert_grad_sums_to_zero(d, *distill_grad(z, 1.0 / temperature, ids, t, g, d.dtype))
+    assert torch.equal(rlk.distill_topk_fwd_bwd(z, ids, t, g, out_dtype=out_dtype, **kw)[2], d)
+    if out_dtype is None:
+        z2, z3 = z.clone(), z.clone()
+        assert torch.equal(rlk.distill_topk_bwd(z2, ids, t, lse, g, out=z2, **kw), d)
+        assert torch.equal(rlk.distill_topk_fwd_bwd(z3, ids, t, g, out=z3, **kw)[2], d)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("T,n", [(3, 300001), (60, 151669), (700, 33001)])
+def test_gradients_of_far_rows_among_others(rlk, dtype, T, n):
+    """Long rows (two launches in the one-call step, many parts a row), misaligned, with columns beyond
+    V_true, every third row far from zero."""
+    V = n + 6
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    buf = torch.full((T * (V + 1) + 3,), math.nan, dtype=dtype, device="cuda")
+    z = buf[3:].view(T, V + 1)[:, :V]
+    x = torch.randn((T, n), generator=gen, device="cuda") * 3
+    x[::3] -= 5000.0
+    x[::6] = torch.finfo(dtype).min
+    z[:, :n] = x.to(dtype)
+    del x
+    y = torch.randint(0, n, (T,), generator=gen, device="cuda")
+    ids, t = near_teacher(z[:, :n], 9, gen)
+    g = torch.rand(T, generator=gen, device="cuda") + 0.5
+    r = rlk.token_logprobs(z, y, V_true=n)
+    d = rlk.token_logprobs_bwd(z, y, r.lse, r.entropy, g, g, V_true=n)
+    _, lse, step = rlk.distill_topk_fwd_bwd(z, ids, t, g, V_true=n)
+    dd = rlk.distill_topk_bwd(z, ids, t, lse, g, V_true=n)
+    assert torch.equal(step, dd)
+    assert torch.count_nonzero(d[:, n:]) == 0 and torch.count_nonzero(dd[:, n:]) == 0
+    for a in range(0, T, 100):
+        b = slice(a, min(T, a + 100))
+        zb = z[b, :n]
+        assert_grad_sums_to_zero(d[b, :n], *token_grad(zb, 1.0, y[b], g[b], g[b], dtype))
+        assert_grad_sums_to_zero(dd[b, :n], *distill_grad(zb, 1.0, ids[b], t[b], g[b], dtype))
+    out = z.clone()                                # rows V apart
+    assert torch.equal(rlk.token_logprobs_bwd(out, y, r.lse, r.entropy, g, g, V_true=n, out=out), d)
+    out = z.clone()
+    assert torch.equal(rlk.distill_topk_bwd(out, ids, t, lse, g, V_true=n, out=out), dd)
+    rlk.distill_topk_fwd_bwd(z, ids, t, g, V_true=n, out=z)
+    assert torch.equal(z, dd)
