@@ -309,6 +309,24 @@ def bwd_dz_view(workspace: torch.Tensor, T: int, V_local: int) -> torch.Tensor:
     return workspace[:n].view(torch.bfloat16).view(T, Vd)
 
 
+class _OnceFn(torch.autograd.Function):
+    """A gradient with a history that refuses: it depends on the logits and on the incoming gradients,
+    and what has to differentiate it again must not take it for a constant. (once_differentiable
+    looks at the incoming gradients alone, which are constants where the loss is linear in the output.)"""
+
+    @staticmethod
+    def forward(ctx, gradient, *inputs):
+        return gradient.view_as(gradient)
+
+    @staticmethod
+    def backward(ctx, g):
+        raise RuntimeError("the operators over logits are differentiable once: their gradients have no derivative")
+
+
+def _once(gradient, *inputs):
+    return _OnceFn.apply(gradient, *inputs) if torch.is_grad_enabled() else gradient   # enabled by create_graph alone
+
+
 class _TokenLogprobsFn(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, y, V_true, temperature):
@@ -321,12 +339,13 @@ class _TokenLogprobsFn(torch.autograd.Function):
     def backward(ctx, g_logp, g_entropy):
         logits, y, lse, entropy = ctx.saved_tensors
         d = token_logprobs_bwd(logits, y, lse, entropy, g_logp.contiguous(), g_entropy.contiguous(), **ctx.args)
-        return d, None, None, None
+        return _once(d, logits, g_logp, g_entropy), None, None, None
 
 
 def token_logprobs_autograd(logits: torch.Tensor, y: torch.Tensor, *, V_true: Optional[int] = None,
                             temperature: float = 1.0) -> Tuple[torch.Tensor, torch.Tensor]:
-    """(logp, entropy) of each row, fp32 [T], differentiable in the logits (both gradients)."""
+    """(logp, entropy) of each row, fp32 [T], differentiable in the logits (both gradients), once: a
+    second derivative raises RuntimeError."""
     return _TokenLogprobsFn.apply(logits, y, V_true, temperature)
 
 
@@ -341,11 +360,12 @@ class _DistillTopkFn(torch.autograd.Function):
     @staticmethod
     def backward(ctx, g):
         logits, ids, teacher, lse = ctx.saved_tensors
-        return distill_topk_bwd(logits, ids, teacher, lse, g.contiguous(), **ctx.args), None, None, None, None
+        d = distill_topk_bwd(logits, ids, teacher, lse, g.contiguous(), **ctx.args)
+        return _once(d, logits, g), None, None, None, None
 
 
 def distill_topk(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Tensor, *,
                  V_true: Optional[int] = None, temperature: float = 1.0) -> torch.Tensor:
     """The distillation loss of each row, fp32 [T], differentiable in the logits (the teacher is
-    a constant)."""
+    a constant), once: a second derivative raises RuntimeError."""
     return _DistillTopkFn.apply(logits, ids, teacher, V_true, temperature)
