@@ -49,6 +49,8 @@ class TokenLogprobs(NamedTuple):
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda index: torch.cuda.current_stream(index).cuda_stream)
+# Tells autograd that tensors have been written to (a kernel's writes are not its to see).
+_written = getattr(torch._C, "_increment_version", torch.autograd.graph.increment_version)
 
 
 def _rows(t: torch.Tensor, name: str) -> Tuple[int, int, int, int, int]:
@@ -163,6 +165,9 @@ def token_logprobs(logits: torch.Tensor, y: Optional[torch.Tensor] = None, *, to
         _flag(err_flag, dev), _raw_stream(dev))
     if st:
         _check("rlk_token_logprobs", st)
+    if out is not None:
+        some = logp is None or rank is None or lse is None or entropy is None or ids is None or top is None
+        _written([x for x in r if x is not None] if some else r)
     return r
 
 
@@ -194,7 +199,8 @@ def token_logprobs_bwd(logits: torch.Tensor, y: torch.Tensor, lse: torch.Tensor,
                        err_flag: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rlk_token_logprobs_bwd -> dlogits of sum_t (g_logp logp + g_entropy entropy), from the
     forward's lse and entropy. The result has the logits' shape and type (or out_dtype: bfloat16
-    for float32 logits); `out` supplies it, the logits themselves included."""
+    for float32 logits); `out` supplies it, the logits themselves included (autograd takes it for
+    modified in place)."""
     T, V, ld, code, dev = _rows(logits, "logits")
     if _away(stream, dev):
         with _elsewhere(stream, dev, (logits, y, lse, entropy, g_logp, g_entropy, out, err_flag)):
@@ -213,6 +219,8 @@ def token_logprobs_bwd(logits: torch.Tensor, y: torch.Tensor, lse: torch.Tensor,
                                         _flag(err_flag, dev), _raw_stream(dev))
     if st:
         _check("rlk_token_logprobs_bwd", st)
+    if out is not None:
+        _written((out,))
     return dlogits
 
 
@@ -269,6 +277,8 @@ def distill_topk_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch.Ten
                                       _flag(err_flag, dev), _raw_stream(dev))
     if st:
         _check("rlk_distill_topk_bwd", st)
+    if out is not None:
+        _written((out,))
     return dlogits
 
 
@@ -295,6 +305,8 @@ def distill_topk_fwd_bwd(logits: torch.Tensor, ids: torch.Tensor, teacher: torch
                                           _raw_stream(dev))
     if st:
         _check("rlk_distill_topk_fwd_bwd", st)
+    if out is not None:
+        _written((out,))
     return loss, lse, dlogits
 
 

@@ -33,3 +33,46 @@ def test_second_derivatives_are_refused(rlk):
         assert torch.equal(d.detach(), first)                    # the first derivative is as ever
         with pytest.raises(RuntimeError, match="differentiable once"):
             (x.sum() + (d * d).sum()).backward()
+
+
+def test_what_a_call_overwrites_cannot_be_taken_for_what_was_saved(rlk):
+    """A gradient written over logits that an earlier forward saved, and scores written over buffers
+    that something saved, make that backward fail instead of giving other numbers."""
+    z, y, ids, t = inputs()
+    T = z.shape[0]
+    g = torch.ones(T, device="cuda")
+    r = rlk.token_logprobs(z, y)
+    writes = [lambda x: rlk.token_logprobs_bwd(x, y, r.lse, r.entropy, g, g, out=x),
+              lambda x: rlk.distill_topk_bwd(x, ids, t, r.lse, g, out=x),
+              lambda x: rlk.distill_topk_fwd_bwd(x, ids, t, g, out=x),
+              lambda x: rlk.distill_topk_fwd_bwd(x, ids, t, g, out=x, stream=torch.cuda.current_stream())]
+    for write in writes:
+        x = z.clone().requires_grad_()
+        loss = rlk.distill_topk(x, ids, t).sum() + rlk.token_logprobs_autograd(x, y)[0].sum()
+        write(x.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+    for k, names in ((0, ("logp", "lse", "entropy")), (3, ("logp", "lse", "entropy", "top_logp"))):
+        out = rlk.token_logprobs(z, y, top_k=k)
+        for name in names:
+            w = torch.ones_like(getattr(out, name), requires_grad=True)
+            loss = (w * getattr(out, name)).sum()
+            rlk.token_logprobs(z + 1, y, top_k=k, out=out)
+            with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+                loss.backward()
+
+
+def test_tensors_of_inference_mode_serve_as_outputs(rlk):
+    z, y, ids, t = inputs()
+    want = rlk.token_logprobs(z, y, top_k=3)
+    g = torch.ones(z.shape[0], device="cuda")
+    grad = rlk.token_logprobs_bwd(z, y, want.lse, None, g)
+    with torch.inference_mode():
+        buffers = [torch.empty_like(x) for x in want]
+        d = torch.empty_like(z)
+        rlk.token_logprobs(z, y, top_k=3, out=buffers)
+    for x in buffers:
+        x.detach()
+    rlk.token_logprobs(z, y, top_k=3, out=buffers)
+    assert all(torch.equal(a, b) for a, b in zip(buffers, want))
+    assert torch.equal(rlk.token_logprobs_bwd(z, y, want.lse, None, g, out=d), grad)
