@@ -22,7 +22,7 @@ Qwen3-30B step, one rank's calls of that split, and the CPU oracle baseline.
 step a bounded sample of the same workload, extrapolated per token).
 --case times one stage alone (per-kernel timings, small ncu captures).
 --record-traffic writes the per-launch DRAM bytes of an ncu capture of the
-step to profiles/traffic_qwen3_8b.json together with the library sources' hash.
+step to profiles/traffic_qwen3_8b.json together with the tile kernels' sources' hash.
 """
 from __future__ import annotations
 
@@ -49,7 +49,7 @@ L2_BYTES = 129 * 1024 * 1024
 
 
 # DRAM traffic per launch of each tile kernel, from one ncu capture of the full-size step
-# (`--record-traffic` writes it; bench reads it back only while the library's sources
+# (`--record-traffic` writes it; bench reads it back only while the tile kernels' sources
 # still hash to the value recorded with it).
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "traffic_qwen3_8b.json")
 STAGE_OF_MODE = {0: "fwd", 1: "dz", 2: "dH", 3: "dW"}
@@ -84,7 +84,7 @@ def record_traffic(csv_path: str, command: str, out_path: str = TRAFFIC_FILE):
                           "traffic_bytes_per_launch": (e["read"] + e["write"]) / n}
     rec = {"workload": "qwen3_8b fwd+bwd T=8192 H=4096 V=151936 V_true=151669",
            "metrics": "dram__bytes_read.sum + dram__bytes_write.sum (ncu, 1 pass per launch)",
-           "command": command, "library_sources_sha256": libbuild.sources_sha256(),
+           "command": command, "library_sources_sha256": libbuild.tile_kernel_sources_sha256(),
            "kernels": kernels}
     with open(out_path, "w") as f:
         json.dump(rec, f, indent=1)
@@ -100,8 +100,8 @@ def traffic_per_launch(stage: str):
         return None, "no traffic record"
     with open(TRAFFIC_FILE) as f:
         rec = json.load(f)
-    if rec.get("library_sources_sha256") != libbuild.sources_sha256():
-        return None, "traffic record predates the current library sources"
+    if rec.get("library_sources_sha256") != libbuild.tile_kernel_sources_sha256():
+        return None, "traffic record predates the current tile kernels' sources"
     k = rec.get("kernels", {}).get(stage)
     if not k:
         return None, f"no {stage} launch in the traffic record"

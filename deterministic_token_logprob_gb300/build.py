@@ -56,6 +56,22 @@ def sources_sha256() -> str:
     return h.hexdigest()
 
 
+# What the bf16 tile kernels of a forward + backward and their launches are made of: the four kernels, the host
+# code that sizes their launches, and the headers that they include (of rlk.h only flags, status codes and limits).
+TILE_KERNEL_SOURCES = ["rlk_api.cu", "rlk_gemm_fwd.cu", "rlk_gemm_dz.cu", "rlk_gemm_dh.cu", "rlk_gemm_dw.cu",
+                       "rlk_ptx.cuh", "rlk_gemm.cuh", "rlk_internal.h"]
+
+
+def tile_kernel_sources_sha256() -> str:
+    """SHA-256 over the tile kernels' sources: two trees with the same value move the same DRAM bytes in
+    a step, whatever other operators the library holds."""
+    h = hashlib.sha256()
+    for s in TILE_KERNEL_SOURCES:
+        with open(os.path.join(CSRC, s), "rb") as f:
+            h.update(f.read())
+    return h.hexdigest()
+
+
 def _stamp(extra) -> str:
     h = hashlib.sha256(sources_sha256().encode())
     h.update(" ".join(ARCH + FLAGS + list(extra)).encode())
