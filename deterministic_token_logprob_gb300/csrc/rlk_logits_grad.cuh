@@ -2,8 +2,6 @@
 // columns, in packs that are aligned in the output whatever their alignment in the logits.
 #pragma once
 
-#include <utility>
-
 #include "rlk_logits_row.cuh"
 
 namespace rlk {
@@ -212,14 +210,17 @@ inline rlk_status check_out(const LogitRows& in, int32_t dtype, void* dlogits, i
   if (out_dtype != dtype && !(dtype == RLK_DTYPE_F32 && out_dtype == RLK_DTYPE_BF16)) return RLK_ERR_UNSUPPORTED;
   if (V > RLK_MAX_LOGITS_VOCAB) return RLK_ERR_UNSUPPORTED;
   if (in.T > 0 && (!dlogits || reinterpret_cast<uintptr_t>(dlogits) % eb != 0)) return RLK_ERR_INVALID_ARG;
-  // in place: the very same array; otherwise the two address ranges are apart
-  if (in.T > 0 && !(dlogits == in.base && out_dtype == dtype && (out_ld == in.ld || in.T == 1))) {
-    const auto span = [&](const void* p, int64_t ld, int64_t n, int bytes) {
-      const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-      return std::pair<uintptr_t, uintptr_t>(a, a + static_cast<uintptr_t>(((in.T - 1) * ld + n) * bytes));
-    };
-    const auto z = span(in.base, in.ld, in.n, dtype_bytes(dtype)), d = span(dlogits, out_ld, V, eb);
-    if (z.first < d.second && d.first < z.second) return RLK_ERR_INVALID_ARG;
+  // in place: the very same array; otherwise no row of one meets a row of the other
+  const int64_t zd = in.ld * dtype_bytes(dtype), dd = out_ld * eb;  // bytes from row to row
+  if (in.T > 0 && !(dlogits == in.base && out_dtype == dtype && (zd == dd || in.T == 1))) {
+    const uintptr_t z = reinterpret_cast<uintptr_t>(in.base), d = reinterpret_cast<uintptr_t>(dlogits);
+    const uintptr_t zn = static_cast<uintptr_t>(in.n) * dtype_bytes(dtype), dn = static_cast<uintptr_t>(V) * eb;
+    if (z < d + (in.T - 1) * dd + dn && d < z + (in.T - 1) * zd + zn) {
+      // the arrays as a whole meet: rows the same distance apart may lie side by side all the same
+      if (in.T == 1 || zd != dd) return RLK_ERR_INVALID_ARG;
+      const uintptr_t at = ((d % zd) + zd - z % zd) % zd;  // where the gradient's rows start, from the logits' on
+      if (at < zn || at + dn > static_cast<uintptr_t>(zd)) return RLK_ERR_INVALID_ARG;
+    }
   }
   *o = GradOut{dlogits, out_ld, static_cast<int32_t>(V)};
   return RLK_OK;

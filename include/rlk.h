@@ -440,7 +440,9 @@ RLK_API rlk_status rlk_token_logprobs(const void* logits, int32_t dtype, int64_t
  *            rlk_linear_logp_bwd's workspace are such an array (bf16, V = out_ld =
  *            round_up(V_local, 256)): with dlogits there, RLK_BWD_DH and RLK_BWD_DW of
  *            rlk_linear_logp_bwd_stages give this loss's dH and dW. dlogits may be the logits
- *            themselves (same type, base and row distance); else the two must not overlap.
+ *            themselves (same type, base and row distance). Else no row of one may meet a
+ *            row of the other: the arrays' address ranges are apart, or the rows are the same
+ *            number of bytes apart and lie side by side (column slices of one wider buffer).
  */
 RLK_API rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int64_t T, int64_t ld,
                                           int64_t V_true, double temperature, const int64_t* y,
