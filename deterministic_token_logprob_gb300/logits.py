@@ -105,6 +105,8 @@ def _away(stream, dev) -> bool:
 def _elsewhere(stream, device, tensors):
     """Makes `device` and `stream` current, so that outputs belong to that stream, and records
     `tensors` as used there."""
+    if stream is not None and stream.device_index != device:
+        raise ValueError(f"stream must be one of cuda:{device}, got one of {stream.device}")
     with torch.cuda.device(device):
         if stream is None:
             yield
