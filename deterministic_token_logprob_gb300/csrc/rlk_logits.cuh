@@ -448,7 +448,8 @@ __device__ __forceinline__ float row_entropy(const Stats& r) {
   if (isnan(r.s)) return quiet_nan();
   if (r.s == 0.f) return 0.f;
   constexpr float kLn2 = 0.69314718f;
-  return __fsub_rn(logf(r.s), __fmul_rn(kLn2, __fdiv_rn(r.u, r.s)));
+  // neither term is below 0 but for the rounding of S and of the leaf's base
+  return fmaxf(__fsub_rn(logf(r.s), __fmul_rn(kLn2, __fdiv_rn(r.u, r.s))), 0.f);
 }
 
 // log p = s (z - m) - l of a column. -inf where the row is empty. With s < 1, s z - s m may be within fp32

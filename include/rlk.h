@@ -384,7 +384,7 @@ RLK_API rlk_status rlk_linear_logp_bwd_fp8(const void* h, const void* W, const v
  * Log probabilities (logp, top_logp and those in the distillation loss) are formed as
  * s (z - M) - log S about the row's maximum M, S = sum e^{s (z - M)}, and are as good for logits far
  * from zero -- an offset, a low temperature, a row masked wholly by a finite value -- as for others; they
- * are never above 0. lse = s M + log S is one fp32: it loses 2^-24 |lse|, and where s M is beyond
+ * are never above 0; entropy is never below 0. lse = s M + log S is one fp32: it loses 2^-24 |lse|, and where s M is beyond
  * fp32's range (bf16 or fp32 logits of the type's lowest value at a temperature below 1, say) it is
  * +inf or, below, fp32's lowest value: -inf marks an empty row alone.
  * The gradients take log p = s z - lse from the caller's lse while what it has lost is small against

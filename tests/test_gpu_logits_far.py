@@ -290,3 +290,15 @@ def test_gradients_of_far_rows_among_others(rlk, dtype, T, n):
     assert torch.equal(rlk.distill_topk_bwd(out, ids, t, lse, g, V_true=n, out=out), dd)
     rlk.distill_topk_fwd_bwd(z, ids, t, g, V_true=n, out=z)
     assert torch.equal(z, dd)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_entropy_is_never_below_zero(rlk, dtype):
+    """Not even by a rounding, in rows where one token takes all (its square root or logarithm may follow)."""
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for n in (1, 7, 5000):
+        z = (torch.randn((600, n), generator=gen, device="cuda") * 5 +
+             torch.randn((600, 1), generator=gen, device="cuda") * 50).to(dtype)
+        for tau in (1.0, 0.7, 0.01, 1e-6, 3.0):
+            assert float(rlk.token_logprobs(z, temperature=tau, top_k=1).entropy.min()) >= 0.0
+            assert float(rlk.token_logprobs(z, temperature=tau).entropy.min()) >= 0.0
