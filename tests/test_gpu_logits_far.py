@@ -302,3 +302,36 @@ def test_entropy_is_never_below_zero(rlk, dtype):
         for tau in (1.0, 0.7, 0.01, 1e-6, 3.0):
             assert float(rlk.token_logprobs(z, temperature=tau, top_k=1).entropy.min()) >= 0.0
             assert float(rlk.token_logprobs(z, temperature=tau).entropy.min()) >= 0.0
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_checked_build_raises_no_flag_on_far_rows(rlk, dtype):
+    """The reads of a row taken again stay inside it, misaligned, with columns beyond V_true, in place too."""
+    from deterministic_token_logprob_gb300 import build
+    build.build(debug_checks=True)
+    n, V = 20003, 20010
+
+    def run():
+        rows, gen = far_rows(dtype, n, seed=5)
+        T = rows.shape[0]
+        z = torch.full((T, V + 1), math.nan, dtype=dtype, device="cuda")[:, 1:]
+        z[:, :n] = rows
+        y = torch.randint(0, n, (T,), generator=gen, device="cuda")
+        ids, t = near_teacher(rows, 12, gen)
+        g = torch.rand(T, generator=gen, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        kw = dict(V_true=n, err_flag=err)
+        r = rlk.token_logprobs(z, y, top_k=7, **kw)
+        out = [*r, rlk.token_logprobs_bwd(z, y, r.lse, r.entropy, g, g, **kw), *rlk.distill_topk_fwd(z, ids, t, **kw),
+               rlk.distill_topk_bwd(z, ids, t, r.lse, g, **kw), *rlk.distill_topk_fwd_bwd(z, ids, t, g, **kw)]
+        out.append(rlk.distill_topk_bwd(z, ids, t, r.lse, g, out=z, **kw))
+        torch.cuda.synchronize()
+        return out, int(err)
+
+    with rlk.library(build.DEBUG_LIB):
+        assert rlk.debug_checks()
+        checked, flag = run()
+    plain, plain_flag = run()
+    assert flag == 0 and plain_flag == 0
+    for a, b in zip(checked, plain):
+        assert torch.equal(a, b)
