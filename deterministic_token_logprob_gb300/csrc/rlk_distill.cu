@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const Disti
     gather_logits(q, row, zk, lane);
   };
   // behind the first leaf's loads (4096 rows of 8000 in bf16: 33.1 -> 28.5 us), but for misaligned rows of
-  // 16-bit types, where both together spill (796 rows of 50257: 25.4 -> 27.3)
+  // 16-bit types, where both together spill (796 rows of 50257: 25.4 -> 27.3; as it is, 16 bytes stored and 56
+  // loaded)
   constexpr bool BEHIND = AL || sizeof(typename E::bits) == 4;
   if constexpr (!BEHIND) read_teacher();
   row_pass<false, false>(row, in.c, none, sm, C, r, [&] {
@@ -254,8 +255,9 @@ __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) distill_kernel(const Disti
 // w + W, ..., and copies all of them asynchronously before anything else, one copy group a leaf,
 // so that the whole row is in flight at once and each leaf is summed as it arrives. The warp that
 // summed a leaf writes its gradient: nothing but the leaves' statistics (to every CTA) and the
-// lse crosses warps. 2048 rows of 50257 in bf16 take 112 us, two launches 123; 16 rows of 4096 in
-// fp32 6.4 us with 64 entries, 4.4 with 8, two launches 8.5.
+// lse crosses warps. 2048 rows of 50257 in bf16 take 113 us, two launches 123; 16 rows of 4096 in
+// fp32 6.5 us with 64 entries, 4.2 with 8, two launches 8.5. 56 registers a thread: the forms for misaligned
+// fp32 rows spill (8 to 12 bytes stored, 8 to 36 loaded).
 constexpr int STEP_THREADS = 288;
 constexpr int STEP_CTAS = 4;              // of one SM
 constexpr int STEP_MAX_ROUNDS = 8;        // leaves of one warp
@@ -422,16 +424,21 @@ __global__ void __launch_bounds__(STEP_THREADS, STEP_CTAS) distill_step_kernel(c
   auto* out = static_cast<typename O::bits*>(a.out.base) + t * a.out.ld;
   const int V = a.out.V;
   const int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(out) & 15u)) & 15u) / OB;  // of the row and of every leaf
+  // Coarse rows are rare, and z - m in the stream over all rows takes 2 % with 16-bit types (2048 of 50257 in bf16:
+  // 112 -> 114 us): they get a plain loop. In fp32 the loop costs more, by spills (4096 misaligned rows of 12001: 100 ->
+  // 110), and the difference nothing.
+  constexpr bool ONE = EB == 4;
   for (int j = 0; j < rounds; ++j) {
     const int i = warp + j * W, c0 = (r + i * C) * ROW_LEAF;
     const auto* first = reinterpret_cast<const typename E::bits*>(slots + i * SLOT + row.shift);
-    if (coarse) {  // rare; the difference z - m in the stream over all rows takes 2 % (2048 of 50257 in bf16: 112 -> 114 us)
+    if (!ONE && coarse) {
       const DistillDz<true> f{in.s, p, A};
+#pragma unroll 1
       for (int c = lane; c < min(V - c0, ROW_LEAF); c += 32)
         out[c0 + c] = O::from_f32(live && c0 + c < in.n ? f.one(E::to_f32(first[c]), c0 + c) : 0.f);
     } else {
       const Row<E, GAL> view(first + head, ROW_LEAF + SLOT_SLACK / EB, in.err_flag, row.shift + head * EB);
-      leaf_grad<O>(view, out, c0, head, in.n, V, live, DistillDz<false>{in.s, p, A}, lane);
+      leaf_grad<O>(view, out, c0, head, in.n, V, live, DistillDz<ONE>{in.s, p, A}, lane);
     }
   }
   // columns past the last leaf
