@@ -170,6 +170,8 @@ __device__ __forceinline__ void row_pass(const R& row, float c, RankOf& rank, co
 // ---------------------------------------------------------------------------
 // launch shapes and types (host)
 // ---------------------------------------------------------------------------
+// The numbers below are of the whole GPU: 152 SMs of 228 KB. On fewer SMs the shapes are other than the best, and
+// the results the same.
 // CTAs (c, a cluster) and warps (w) of a row in the statistics passes. With 64 registers a thread an
 // SM runs 32 warps, so floor(32 / w) CTAs, if their shared memory (smem bytes each) fits; a row takes
 // ceil(leaves / (c w)) rounds of leaves, about two more for what surrounds them (the target, the fold,

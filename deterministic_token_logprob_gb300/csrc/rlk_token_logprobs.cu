@@ -301,12 +301,14 @@ __device__ void find_top(const R& row, const ScoreArgs& a, int64_t t, unsigned c
 // shared memory and a few hundred columns read again (from L2). The pass reads each logit once. With
 // 16-bit types and alternatives the instructions bind, not the memory: about 10 an element, of which a
 // third is what each lane does once for the 32 elements that it has of a leaf (8192 rows of 151936 in
-// bf16 with 20 alternatives: 434 us for 2.49 GB, 5.7 TB/s; without any 385 us, 6.5 TB/s; 4096 in fp32 with
+// bf16 with 20 alternatives: 429 us for 2.49 GB, 5.8 TB/s; without any 382 us, 6.5 TB/s; 4096 in fp32 with
 // 64: 386 us, 6.4 TB/s, with none 338 us, 7.3 TB/s). Few rows are bound by latency: a single one takes
 // 8 us on the GPU, on 8 SMs.
 // Persistent CTAs, whose finishing warp overlaps the next row's pass, are slower (749 us against 485 at
 // that step): finishing a row takes one warp 30 us.
-// 64 registers a thread, whatever the number of threads: 1024 of them fill an SM.
+// 64 registers a thread, whatever the number of threads: 1024 of them fill an SM. In 16-bit types that
+// spills three to eight of them (20 bytes stored and 12 loaded in the aligned bf16 form with alternatives,
+// 32 and 28 in the misaligned one), in fp32 none but one in the misaligned form with alternatives.
 template <class E, bool TOP, bool AL>
 __global__ void __launch_bounds__(MAX_ROW_THREADS, 1) token_logprobs_kernel(const ScoreArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];

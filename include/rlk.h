@@ -455,6 +455,7 @@ RLK_API rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int
  * Distillation from a teacher's top logits. q = softmax(s t_k) over the row's entries, and
  *   loss[t] = sum_k q_k (log q_k - (x_{id_k} - lse))       (the KL divergence from q to p)
  *   dlogits[t][v] = s g[t] (p_v - sum_{k : id_k = v} q_k)  of sum_t g[t] loss[t]
+ * (no factor temperature^2: a caller who wants gradients of one size at every temperature has it in g).
  * (teacher log probabilities serve as well as logits: q does not change under a shift).
  *   ids      device int64 [T][K], K in 1 .. RLK_MAX_TOP_K; id -1: no entry (as rlk_token_logprobs
  *            marks missing alternatives); an id may come twice, then both count
@@ -469,8 +470,9 @@ RLK_API rlk_status rlk_token_logprobs_bwd(const void* logits, int32_t dtype, int
  * rlk_token_logprobs_bwd, with rows of g = 0 zero.
  *
  * rlk_distill_topk_fwd_bwd gives both at once, for weights g that are known before the loss (a
- * token mask over a count): the same bits as the two calls, and where a row fits the shared memory
- * of one or two SMs, or the rows are few, the logits are read once.
+ * token mask over a count): the same bits as the two calls. The logits are read once for rows of up to
+ * 53248 columns in 16-bit types and 13312 in fp32, and for longer ones where they are few: up to
+ * 608 rows of 106496 (53248 in fp32), 304 of 212992 (106496). Else they are read twice, which is faster there.
  */
 RLK_API rlk_status rlk_distill_topk_fwd(const void* logits, int32_t dtype, int64_t T, int64_t ld,
                                         int64_t V_true, double temperature, const int64_t* ids,
