@@ -7,7 +7,8 @@ sum_t g_t logp_t. It is a C ABI shared library (include/rlk.h, built into
 (tcgen05 / TMEM / TMA); this package is its thin ctypes binding. Next to it stand the
 operators over logits that already exist (module ``logits``): token log probabilities with
 rank, entropy and top alternatives, and distillation from a teacher's top logits, each with
-its gradient.
+its gradient; and the operators around the head in a training step (module ``training``): embedding
+lookup and layer norm with their gradients, and the norm over all gradients with clipping.
 """
 from ._binding import (  # noqa: F401
     LEAF_WIDTH, MAX_SHARDS, RLK_BWD_DH, RLK_BWD_DW, RLK_BWD_DZ, RLK_ERR_CUDA, RLK_ERR_INVALID_ARG,
@@ -23,3 +24,6 @@ from .logits import (  # noqa: F401
     MAX_LOGITS_VOCAB, MAX_TOP_K, RLK_DTYPE_BF16, RLK_DTYPE_F16, RLK_DTYPE_F32, TokenLogprobs,
     bwd_dz_view, distill_topk, distill_topk_bwd, distill_topk_fwd, distill_topk_fwd_bwd,
     token_logprobs, token_logprobs_autograd, token_logprobs_bwd)
+from .training import (  # noqa: F401
+    MAX_TENSORS, clip_grad_norm, embedding, embedding_bwd, embedding_bwd_workspace_bytes, embedding_fwd, grad_norm,
+    layer_norm, layer_norm_bwd, layer_norm_bwd_workspace_bytes, layer_norm_fwd)

@@ -124,6 +124,24 @@ def _declare(lib):
     lib.rlk_distill_topk_bwd.restype = ctypes.c_int
     lib.rlk_distill_topk_fwd_bwd.argtypes = rows + [P, P, I32, P, P, P] + grad + [P, P]
     lib.rlk_distill_topk_fwd_bwd.restype = ctypes.c_int
+    lib.rlk_embedding_fwd.argtypes = [P, I32, I64, I64, I64, I64, I64, P, I64, F64, P, I32, I64, P, P]
+    lib.rlk_embedding_fwd.restype = ctypes.c_int
+    lib.rlk_embedding_bwd_workspace.argtypes = [I64, I64]
+    lib.rlk_embedding_bwd_workspace.restype = SZ
+    lib.rlk_embedding_bwd.argtypes = [P, I32, I64, I64, I64, P, I64, I64, I64, F64, P, I32, P, P, SZ, P]
+    lib.rlk_embedding_bwd.restype = ctypes.c_int
+    lib.rlk_layer_norm_fwd.argtypes = [P, I32, I64, I64, I64, P, P, I32, I32, F64, P, I32, I64, P, P, P, P]
+    lib.rlk_layer_norm_fwd.restype = ctypes.c_int
+    lib.rlk_layer_norm_bwd_workspace.argtypes = [I64, I64]
+    lib.rlk_layer_norm_bwd_workspace.restype = SZ
+    lib.rlk_layer_norm_bwd.argtypes = [P, I32, I64, P, I32, I64, I64, I64, P, I32, P, P, P, I64, P, P, P, P, SZ, P]
+    lib.rlk_layer_norm_bwd.restype = ctypes.c_int
+    lib.rlk_grad_norm_workspace.argtypes = [I32]
+    lib.rlk_grad_norm_workspace.restype = SZ
+    lib.rlk_grad_norm.argtypes = [P, P, P, I32, P, P, P, SZ, P]
+    lib.rlk_grad_norm.restype = ctypes.c_int
+    lib.rlk_clip_grad_norm.argtypes = [P, P, P, I32, F64, P, P, P, P, P, SZ, P]
+    lib.rlk_clip_grad_norm.restype = ctypes.c_int
     lib.rlk_status_string.argtypes = [ctypes.c_int]
     lib.rlk_status_string.restype = ctypes.c_char_p
     lib.rlk_version.argtypes = []

@@ -30,10 +30,11 @@ OUT_DEBUG = os.path.join(PKG, "_build_debug")
 DEBUG_LIB = os.path.join(OUT_DEBUG, "librlk.so")
 
 SOURCES = ["rlk_api.cu", "rlk_gemm_fwd.cu", "rlk_gemm_dz.cu", "rlk_gemm_dh.cu", "rlk_gemm_dw.cu", "rlk_gemm_fp8.cu",
-           "rlk_quant.cu", "rlk_noalloc.cu", "rlk_token_logprobs.cu", "rlk_distill.cu"]
+           "rlk_quant.cu", "rlk_noalloc.cu", "rlk_token_logprobs.cu", "rlk_distill.cu", "rlk_embedding.cu", "rlk_layer_norm.cu",
+           "rlk_clip.cu"]
 HEADERS = [os.path.join(CSRC, f) for f in (
     "rlk_ptx.cuh", "rlk_gemm.cuh", "rlk_internal.h", "rlk_logits.cuh", "rlk_logits_row.cuh",
-    "rlk_logits_grad.cuh")] + [os.path.join(INCLUDE, "rlk.h")]
+    "rlk_logits_grad.cuh", "rlk_rows.cuh")] + [os.path.join(INCLUDE, "rlk.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--fmad=false", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC]

@@ -336,7 +336,7 @@ class _OnceFn(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g):
-        raise RuntimeError("the operators over logits are differentiable once: their gradients have no derivative")
+        raise RuntimeError("this operator is differentiable once: its gradient has no derivative")
 
 
 def _once(gradient, *inputs):

@@ -493,6 +493,124 @@ RLK_API rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, i
                                             int32_t* err_flag, void* stream);
 
 /*
+ * Operators around the head in a training step: what turns tokens into the first hidden values and the
+ * last ones into h, each with its gradient, and the norm of all gradients. The table of an embedding is a
+ * [V][H] array like W; a tied model has one for both, and its dW is the head's with the embedding's added.
+ * Common arguments:
+ *   dtype    RLK_DTYPE_* of the rows; results have the same type, or RLK_DTYPE_BF16 for fp32 rows
+ *   H        1 .. RLK_MAX_HIDDEN; rows `ld` elements apart (at least H), aligned to their element size only.
+ *            Rows that all start on 16-byte boundaries, with H % 8 == 0, are the fast case
+ *   T        0 .. RLK_MAX_TOKENS
+ *   err_flag device int32 or NULL, as everywhere
+ *   workspace, workspace_bytes: device scratch of the size that the query returns, 256-byte aligned; what it
+ *            holds before a call does not matter
+ * A result may not meet an input, but for the cases that an entry point names: the arrays are apart, or
+ * their rows are the same number of bytes apart and lie side by side (column slices of one wider buffer).
+ * Numerical contract: fp32 sums in fixed orders that follow from columns, and for sums over tokens from the
+ * order of the tokens, so that a result never depends on alignment, strides, the launch shape or the GPU's SM count;
+ * a row of a lookup, of a norm or of dx depends on that row's inputs alone, and a row of an embedding's dW on that
+ * token's rows alone.
+ */
+#define RLK_MAX_TOKENS (1 << 24)
+
+/*
+ * out[t] = scale * table[ids[t] - vocab_start], rounded once to out_dtype: the rows of a table, or of a shard of one that
+ * holds the tokens [vocab_start, vocab_start + V_local).
+ *   table    device [V_local][ld];  ids: device int64 [T];  out: device [T][out_ld]
+ *   V_true   tokens are 0 .. V_true - 1
+ * The row of a token that is not in the shard is zero, and so is that of id -1 (padding); any other id outside
+ * [0, V_true) gets a row of NaN, and RLK_FLAG_BAD_TARGET is ORed into *err_flag.
+ */
+RLK_API rlk_status rlk_embedding_fwd(const void* table, int32_t dtype, int64_t V_local, int64_t H, int64_t ld,
+                                     int64_t vocab_start, int64_t V_true, const int64_t* ids, int64_t T, double scale,
+                                     void* out, int32_t out_dtype, int64_t out_ld, int32_t* err_flag, void* stream);
+
+/* Bytes of device workspace rlk_embedding_bwd needs: the sorted tokens (16 T bytes) and the sums of tokens that
+ * come more than 32 times (up to T H / 4 bytes). */
+RLK_API size_t rlk_embedding_bwd_workspace(int64_t T, int64_t H);
+
+/*
+ * The table's gradient: dW[v - vocab_start] = scale * sum of dout[t] over the t with ids[t] = v.
+ *   dout     device [T][ld] of type dtype;  ids: device int64 [T]
+ *   dW       device fp32 [V_local][H], as rlk_linear_logp_bwd writes it (any 4-byte alignment)
+ *   accumulate  0: dW is written, with zeros in the rows of tokens that do not come; 1: the gradient is added to what dW
+ *            holds (a tied model's head has been there), one rounding an element, and other rows are not touched
+ * Ids of -1 and of other shards add nothing; any other id outside [0, V_true) adds nothing and ORs RLK_FLAG_BAD_TARGET
+ * in. A token's rows are added in the order of t, in runs of 32 whose sums are added in turn: the order
+ * does not depend on the other tokens or on the shard. T == 0 with accumulate == 0 writes zeros.
+ */
+RLK_API rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t H, int64_t ld,
+                                     const int64_t* ids, int64_t V_local, int64_t vocab_start, int64_t V_true,
+                                     double scale, float* dW, int32_t accumulate, int32_t* err_flag, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
+ * Layer norm of each row:
+ *   y_c = (x_c - mean) rstd weight_c + bias_c,   rstd = (mean_c (x_c - mean)^2 + eps)^(-1/2)
+ * or, with centered == 0, the same with mean = 0 (the root-mean-square norm).
+ *   x        device [T][ld] of type dtype;  y: device [T][out_ld] of type out_dtype, which may be x itself
+ *   weight, bias  device [H] of type weight_dtype (the rows' type or RLK_DTYPE_F32), either may be NULL
+ *   eps      RLK_MIN_NORM_EPS .. 1
+ *   mean, rstd  device fp32 [T], for the backward; either may be NULL
+ * The variance is summed about the mean, which is corrected by what its own rounding lost; rows whose sums are beyond
+ * fp32 are summed once more at a smaller scale. A row that holds a NaN or an infinity is NaN throughout, and
+ * RLK_FLAG_NONFINITE is ORed into *err_flag.
+ */
+#define RLK_MIN_NORM_EPS 1e-18
+
+RLK_API rlk_status rlk_layer_norm_fwd(const void* x, int32_t dtype, int64_t T, int64_t H, int64_t ld,
+                                      const void* weight, const void* bias, int32_t weight_dtype, int32_t centered,
+                                      double eps, void* y, int32_t out_dtype, int64_t out_ld, float* mean, float* rstd,
+                                      int32_t* err_flag, void* stream);
+
+/* Bytes of device workspace rlk_layer_norm_bwd needs: 8 T bytes, and the parts of dw and db of 152 strips of rows. */
+RLK_API size_t rlk_layer_norm_bwd_workspace(int64_t T, int64_t H);
+
+/*
+ * Gradients of the layer norm, with h = (x - mean) rstd and g = dy weight:
+ *   dx_c = rstd (g_c - mean_c g - h_c mean_c(g h)),   dw_c = sum_t dy h,   db_c = sum_t dy
+ * (without the term mean_c g when the norm is not centered).
+ *   dy       device [T][dy_ld] of type dy_dtype (the forward's out_dtype)
+ *   x, dtype, ld, T, H, weight, weight_dtype: as in the forward
+ *   mean, rstd  device fp32 [T] from the forward; mean NULL: not centered
+ *   dx       device [T][dx_ld] of type dtype, or NULL; it may be dy or x itself (same type and row distance)
+ *   dw, db   device fp32 [H], each may be NULL; at least one of dx, dw and db is wanted. T == 0 writes zeros to them
+ * Rows are dealt to 152 strips, row t to strip t mod 152; a strip adds its rows in ascending order, and the
+ * strips' sums are added in ascending order.
+ */
+RLK_API rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t dy_ld, const void* x, int32_t dtype,
+                                      int64_t ld, int64_t T, int64_t H, const void* weight, int32_t weight_dtype,
+                                      const float* mean, const float* rstd, void* dx, int64_t dx_ld, float* dw,
+                                      float* db, int32_t* err_flag, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * The 2-norm over all elements of n tensors, and gradients scaled so that it is at most max_norm:
+ *   norm = sqrt(sum g^2),   out = g if norm <= max_norm, else g (max_norm / norm)
+ *   grads, sizes, dtypes  host arrays of n: device pointers (aligned to their element size only), element counts
+ *            (0 .. RLK_MAX_TENSOR_ELEMENTS), RLK_DTYPE_*; read before the call returns
+ *   n        0 .. RLK_MAX_TENSORS
+ *   outs, out_dtypes  host arrays of n: where the results go (same count; same type, or RLK_DTYPE_BF16 for fp32), a
+ *            gradient itself among them. Results meet neither one another nor any other gradient
+ *   max_norm above 0 (infinity: never scaled)
+ *   norm     device fp32 [1]: the norm before scaling
+ * Squares that would overflow or vanish in fp32 are summed at another scale. A norm that is not finite (a NaN or an
+ * infinity among the gradients, or a norm beyond fp32) leaves the gradients unscaled, and RLK_FLAG_NONFINITE is ORed
+ * into *err_flag: a trainer skips that step. Sums are taken in an order that follows from sizes and types.
+ */
+#define RLK_MAX_TENSORS (1 << 14)
+#define RLK_MAX_TENSOR_ELEMENTS ((int64_t)1 << 40)
+
+RLK_API size_t rlk_grad_norm_workspace(int32_t n);
+
+RLK_API rlk_status rlk_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int32_t n,
+                                 float* norm, int32_t* err_flag, void* workspace, size_t workspace_bytes, void* stream);
+
+RLK_API rlk_status rlk_clip_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int32_t n,
+                                      double max_norm, void* const* outs, const int32_t* out_dtypes, float* norm,
+                                      int32_t* err_flag, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Forward without a workspace argument, for callers that cannot allocate device
  * memory: runtimes whose device memory is fully reserved up front by another
  * allocator (a serving engine that pre-plans every buffer), or latency-critical
