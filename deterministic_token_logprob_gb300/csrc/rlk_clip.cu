@@ -47,14 +47,11 @@ constexpr float kHuge = 1.2089258196146292e24f;  // 2^80
 
 template <class E>
 __device__ __forceinline__ float squares(const Pack<E>& k, float f) {
-  float v[8];
+  F32x2 v[4];
   unpack(k, v);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = __fmul_rn(v[i], f);
-    v[i] = __fmul_rn(v[i], v[i]);
-  }
-  return tree8(v);
+  for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(f));  // a power of two
+  return low_plus_high(dot4(v, v, 0));
 }
 
 template <class E>
@@ -156,10 +153,10 @@ __device__ __forceinline__ void scale_chunk(const Piece& p, uint32_t chunk, floa
   for (int j = 0; j < CE / (8 * CLIP_THREADS); ++j) {
     const int c = 8 * (j * CLIP_THREADS + static_cast<int>(threadIdx.x));
     if (c >= n) break;
-    float v[8];
+    F32x2 v[4];
     unpack(load_columns<E, false>(row, c, n, err), v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = f == 1.f ? v[i] : __fmul_rn(v[i], f);  // a NaN's bits survive a copy
+    for (int i = 0; i < 4; ++i) v[i] = f == 1.f ? v[i] : mul2(v[i], both(f));  // a NaN's bits survive a copy
     if (al && c + 8 <= n) store_columns<O, true>(out, c, n, v, err);
     else store_columns<O, false>(out, c, n, v, err);
   }

@@ -45,14 +45,14 @@ __global__ void __launch_bounds__(256) lookup_kernel(const LookupArgs a) {
   const auto* row = static_cast<const typename E::bits*>(a.table) + static_cast<int64_t>(r < 0 ? 0 : r) * a.ld;
   auto* out = static_cast<typename O::bits*>(a.out) + t * a.out_ld;
   for (int c = 8 * threadIdx.x; c < a.H; c += 8 * 256) {
-    float v[8];
+    F32x2 v[4];
     if (r >= 0) {
       unpack(load_columns<E, AL>(row, c, a.H, a.shard.err), v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], a.scale);
+      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(a.scale));
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = r == -2 ? quiet_nan() : 0.f;
+      for (int i = 0; i < 4; ++i) v[i] = both(r == -2 ? quiet_nan() : 0.f);
     }
     store_columns<O, AL>(out, c, a.H, v, a.shard.err);
   }
@@ -274,14 +274,14 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
   const int width = (a.H + 7) / 8 * 8;
   const int c = 8 * static_cast<int>(blockIdx.y * blockDim.x + threadIdx.x);
   const bool on = c < a.H;
-  float s[8] = {};
+  F32x2 s[4] = {};
   for (int i = 0; i < n; ++i) {
     const uint32_t t = __shfl_sync(kFullWarp, mine, i);
     if (!on) continue;
-    float v[8];
+    F32x2 v[4];
     unpack(load_columns<E, AL>(static_cast<const typename E::bits*>(a.dout) + static_cast<int64_t>(t) * a.ld, c, a.H, a.err), v);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = __fadd_rn(s[j], v[j]);
+    for (int j = 0; j < 4; ++j) s[j] = add2(s[j], v[j]);
   }
   if (!alone) {
     // leave the run's sum; the CTA that is through last adds them up
@@ -289,9 +289,7 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
     const int32_t slot = n == RUN ? (p + RUN - 1) / RUN : a.slots + seg;
     const bool ok = dbg_ok(slot < 2 * a.slots && seg < a.slots, a.err);
     if (on && ok) {
-      float* at = a.part + static_cast<int64_t>(slot) * width + c;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) at[j] = s[j];
+      store_columns<F32, true>(reinterpret_cast<uint32_t*>(a.part) + static_cast<int64_t>(slot) * width, c, width, s, a.err);
     }
     const int32_t end = more >> 31 && n == RUN ? first_not_below(a, row + 1, p + RUN, a.T, lane) : p + n;
     const int32_t runs = (end - start + RUN - 1) / RUN;
@@ -303,23 +301,23 @@ __global__ void __launch_bounds__(256) gather_kernel(const GatherArgs a) {
     __threadfence();
     if (!on) return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = 0.f;
+    for (int j = 0; j < 4; ++j) s[j] = 0;
     for (int i = 0; i < runs; ++i) {
       const int32_t q = start + i * RUN;
       const int32_t from = q + RUN <= end ? (q + RUN - 1) / RUN : a.slots + seg;
       const float4* at = reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(from) * width + c);
       const float4 x = __ldcg(at), y = __ldcg(at + 1);
-      const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+      const F32x2 v[4] = {pack_f32x2(x.x, x.y), pack_f32x2(x.z, x.w), pack_f32x2(y.x, y.y), pack_f32x2(y.z, y.w)};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[j] = __fadd_rn(s[j], v[j]);
+      for (int j = 0; j < 4; ++j) s[j] = add2(s[j], v[j]);
     }
   }
   if (!on) return;
   auto* out = reinterpret_cast<uint32_t*>(a.dW) + static_cast<int64_t>(row) * a.H;
-  float old[8] = {};
+  F32x2 old[4] = {};
   if (a.add) unpack(load_columns<F32, AL>(out, c, a.H, a.err), old);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) s[j] = a.add ? __fmaf_rn(s[j], a.scale, old[j]) : __fmul_rn(s[j], a.scale);
+  for (int j = 0; j < 4; ++j) s[j] = a.add ? fma2(s[j], both(a.scale), old[j]) : mul2(s[j], both(a.scale));
   store_columns<F32, AL>(out, c, a.H, s, a.err);
 }
 

@@ -4,15 +4,23 @@
 //   h_c = (x_c - m) r,  y_c = h_c w_c + b_c
 // and, with g_c = dy_c w_c,
 //   dx_c = r (g_c - [centered] mean g - h_c mean(g h)),   dw_c = sum_t dy_tc h_tc,   db_c = sum_t dy_tc
+//
+// Both directions are bound by memory: the forward reads x and writes y, the backward reads x and dy
+// and writes dx, once each.
 #include "rlk_rows.cuh"
 
 namespace rlk {
 namespace {
 
 constexpr int NORM_THREADS = SLOTS;
-// Strips of rows whose parts of dw and db are summed apart: row t belongs to strip t mod 152, so that
-// the order of the sum over rows depends on T alone.
-constexpr int NORM_STRIPS = 152;
+
+// Rows are dealt to strips, whose parts of dw and db are summed apart: row t belongs to strip t mod S. S follows
+// from T and the width alone, and so does the order of the sum over rows: two CTAs on each of 152 SMs,
+// each of as many teams as the width leaves room for.
+constexpr int NORM_CTAS = 304;
+__host__ __device__ constexpr int strips_of(int64_t T, int n) {
+  return static_cast<int>(T < NORM_CTAS * (8 / team_warps(n)) ? T : NORM_CTAS * (8 / team_warps(n)));
+}
 
 // A row that overflows fp32 in its sums is taken once more as x 2^-80.
 constexpr float kShrink = 8.271806125530277e-25f;  // 2^-80
@@ -20,77 +28,72 @@ constexpr float kGrow = 1.2089258196146292e24f;    // 2^80
 
 struct Vector {  // weight or bias: fp32 or the rows' type, or absent
   const void* p;
-  int32_t dtype;
+  bool f32;
 };
 
-__device__ __forceinline__ float element(const Vector& w, int c) {
-  if (w.dtype == RLK_DTYPE_F32) return static_cast<const float*>(w.p)[c];
-  const uint16_t b = static_cast<const uint16_t*>(w.p)[c];
-  return w.dtype == RLK_DTYPE_BF16 ? Bf16::to_f32(b) : F16::to_f32(b);
-}
-
-__device__ __forceinline__ void vector8(const Vector& w, int c0, int n, float absent, float (&v)[8]) {
+// 8 columns of a vector; AL: it starts on a 16-byte boundary and n is a multiple of 8.
+template <class E, bool AL>
+__device__ __forceinline__ void vector8(const Vector& w, int c0, int n, float absent, F32x2 (&v)[4], int32_t* err) {
+  if (!w.p) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = w.p && c0 + i < n ? element(w, c0 + i) : absent;
+    for (int i = 0; i < 4; ++i) v[i] = both(absent);
+  } else if (sizeof(typename E::bits) == 4 || w.f32) {
+    unpack(load_columns<F32, AL>(static_cast<const uint32_t*>(w.p), c0, n, err), v);
+  } else {
+    unpack(load_columns<E, AL>(static_cast<const typename E::bits*>(w.p), c0, n, err), v);
+  }
 }
 
-// Sums of two values over the 256 slots, in the fixed order; every thread gets both. `room`: 16 floats of
-// shared memory that no other call is using.
-__device__ __forceinline__ float2 slots_sum(float a, float b, float* room) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const float2 s = warp_sum_pair(a, b, lane);
-  __syncthreads();
-  if (lane == 0) room[warp] = s.x, room[8 + warp] = s.y;
-  __syncthreads();
-  float x[8], y[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = room[i], y[i] = room[8 + i];
-  return make_float2(tree8(x), tree8(y));
-}
-
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
 struct RowStats {
   float k;     // what x is multiplied by (1, or 2^-80 for a row whose sums are beyond fp32)
   float m, c;  // mean of k x: m + c (m rounded, c what that lost)
   float r;     // 1 / sqrt(mean (k x - mean)^2 + k^2 eps)
 };
 
-// The statistics of a row; f(j, v) gives the j-th of this thread's packs as 8 values (0 beyond the row),
-// n is the row's length.
-template <class F>
-__device__ __forceinline__ RowStats row_stats(int n, bool centered, float eps, float* room, const F& f) {
-  const int packs = (n + 7) / 8;
+__device__ __forceinline__ void shrink(F32x2 (&v)[4], float k) {
+  if (k == 1.f) return;  // the same for the whole team
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(k));
+}
+
+// The statistics of a row of n columns. each(f) calls f(c0, v) with the columns of every pack of this thread; FULL: no pack
+// reaches beyond the row. room: 4 W floats.
+template <int W, bool FULL, class Each>
+__device__ __forceinline__ RowStats row_stats(int n, bool centered, float eps, float* room, const Each& each) {
   const float len = static_cast<float>(n);
   RowStats s{1.f, 0.f, 0.f, 0.f};
   float q;
   for (;;) {
     if (centered) {
-      float a = 0.f;
-      for (int p = threadIdx.x; p < packs; p += SLOTS) {
-        float v[8];
-        f(p, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __fmul_rn(v[i], s.k);
-        a = __fadd_rn(a, tree8(v));
-      }
-      s.m = __fdiv_rn(slots_sum(a, 0.f, room).x, len);
+      F32x2 a = 0;
+      each([&](int, F32x2 (&v)[4]) {
+        shrink(v, s.k);
+        a = add2(a, tree4(v));
+      });
+      s.m = __fdiv_rn(team_sum<W>(low_plus_high(a), 0.f, room).x, len);
     }
-    float a = 0.f, b = 0.f;
-    for (int p = threadIdx.x; p < packs; p += SLOTS) {
-      float v[8], d[8];
-      f(p, v);
+    F32x2 a = 0, b = 0;
+    each([&](int c0, F32x2 (&v)[4]) {
+      shrink(v, s.k);
+      F32x2 d[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        d[i] = 8 * p + i < n ? __fsub_rn(__fmul_rn(v[i], s.k), s.m) : 0.f;
-        v[i] = __fmul_rn(d[i], d[i]);
-      }
-      a = __fadd_rn(a, tree8(v));
-      b = __fadd_rn(b, tree8(d));
-    }
-    const float2 t = slots_sum(a, b, room);
+      for (int i = 0; i < 4; ++i) d[i] = add2(v[i], both(-s.m));
+      if constexpr (!FULL) clear_beyond(d, c0, n);
+      b = add2(b, tree4(d));
+      a = dot4(d, d, a);
+    });
+    const float2 t = team_sum<W>(low_plus_high(a), low_plus_high(b), room + 2 * W);
     q = __fdiv_rn(t.x, len);
     s.c = centered ? __fdiv_rn(t.y, len) : 0.f;
     if (isfinite(q) || s.k != 1.f) break;
     s.k = kShrink;
+    // the sums to come use the room again
+    if constexpr (W == 8) __syncthreads();
+    else if constexpr (W > 1)
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x / (32 * W))), "n"(32 * W) : "memory");
   }
   const float var = fmaxf(__fmaf_rn(-s.c, s.c, q), 0.f);
   if (!isfinite(q)) s.r = quiet_nan();  // a NaN or an infinity in the row
@@ -119,29 +122,79 @@ __device__ __forceinline__ void put_stats(const NormArgs& a, int64_t t, const Ro
   if (isnan(s.r) && a.err) atomicOr(a.err, RLK_FLAG_NONFINITE);
 }
 
-template <class E, class O, bool AL>
-__global__ void __launch_bounds__(NORM_THREADS) norm_fwd_any_kernel(const NormArgs a) {
-  __shared__ float room[16];
-  const int64_t t = blockIdx.x;
-  const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
-  auto* y = static_cast<typename O::bits*>(a.y) + t * a.out_ld;
-  const auto get = [&](int p, float (&v)[8]) { unpack(load_columns<E, AL>(x, 8 * p, a.H, a.err), v); };
-  const RowStats s = row_stats(a.H, a.centered, a.eps, room, get);
-  if (threadIdx.x == 0) put_stats(a, t, s);
-  for (int p = threadIdx.x; p < (a.H + 7) / 8; p += SLOTS) {
-    float v[8], w[8], b[8];
-    get(p, v);
-    vector8(a.w, 8 * p, a.H, 1.f, w);
-    vector8(a.b, 8 * p, a.H, 0.f, b);
+// y of a pack, v its k x
+__device__ __forceinline__ void norm_pack(F32x2 (&v)[4], const RowStats& s, const F32x2 (&w)[4], const F32x2 (&b)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float d = __fsub_rn(__fsub_rn(__fmul_rn(v[i], s.k), s.m), s.c);
-      v[i] = __fmaf_rn(__fmul_rn(d, s.r), w[i], b[i]);
-    }
-    store_columns<O, AL>(y, 8 * p, a.H, v, a.err);
+  for (int i = 0; i < 4; ++i) {
+    const F32x2 d = add2(add2(v[i], both(-s.m)), both(-s.c));
+    v[i] = fma2(mul2(d, both(s.r)), w[i], b[i]);
   }
 }
 
+// Rows of whole packs on 16-byte boundaries, K packs a thread, which stay in registers between the two sums and the
+// result. W warps a row: 8 / W rows a CTA.
+template <class E, class O, int W, int K>
+__global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormArgs a) {
+  __shared__ float rooms[32];
+  const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W), packs = a.H / 8;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
+  if (t >= a.T) return;  // the whole team
+  const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
+  Pack<E> k[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j)
+    if (tid + j * SLOTS < packs) k[j] = load_columns<E, true>(x, 8 * (tid + j * SLOTS), a.H, a.err);
+  const auto each = [&](auto f) {
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (tid + j * SLOTS < packs) {
+        F32x2 v[4];
+        unpack(k[j], v);
+        f(8 * (tid + j * SLOTS), v);
+      }
+  };
+  const RowStats s = row_stats<W, true>(a.H, a.centered, a.eps, rooms + team * 4 * W, each);
+  if (tid == 0) put_stats(a, t, s);
+  auto* y = static_cast<typename O::bits*>(a.y) + t * a.out_ld;
+  each([&](int c0, F32x2 (&v)[4]) {
+    F32x2 w[4], b[4];
+    vector8<E, true>(a.w, c0, a.H, 1.f, w, a.err);
+    vector8<E, true>(a.b, c0, a.H, 0.f, b, a.err);
+    shrink(v, s.k);
+    norm_pack(v, s, w, b);
+    store_columns<O, true>(y, c0, a.H, v, a.err);
+  });
+}
+
+// Any row, one CTA each: it is read three times (from L1 or L2 after the first).
+template <class E, class O>
+__global__ void __launch_bounds__(NORM_THREADS) norm_fwd_any_kernel(const NormArgs a) {
+  __shared__ float room[32];
+  const int64_t t = blockIdx.x;
+  const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
+  auto* y = static_cast<typename O::bits*>(a.y) + t * a.out_ld;
+  const auto each = [&](auto f) {
+    for (int c = 8 * threadIdx.x; c < a.H; c += 8 * SLOTS) {
+      F32x2 v[4];
+      unpack(load_columns<E, false>(x, c, a.H, a.err), v);
+      f(c, v);
+    }
+  };
+  const RowStats s = row_stats<8, false>(a.H, a.centered, a.eps, room, each);
+  if (threadIdx.x == 0) put_stats(a, t, s);
+  each([&](int c0, F32x2 (&v)[4]) {
+    F32x2 w[4], b[4];
+    vector8<E, false>(a.w, c0, a.H, 1.f, w, a.err);
+    vector8<E, false>(a.b, c0, a.H, 0.f, b, a.err);
+    shrink(v, s.k);
+    norm_pack(v, s, w, b);
+    store_columns<O, false>(y, c0, a.H, v, a.err);
+  });
+}
+
+// ---------------------------------------------------------------------------
+// backward
+// ---------------------------------------------------------------------------
 struct NormGradArgs {
   const void *dy, *x;
   void* dx;
@@ -149,43 +202,173 @@ struct NormGradArgs {
   int32_t H;
   Vector w;
   const float *mean, *rstd;
-  float* row;         // [T][2]: mean g, mean(g h)
+  float* row;              // [T][2]: mean g, mean(g h)
   float *part_w, *part_b;  // [strips][H]
   float *dw, *db;
-  int32_t strips;
+  int32_t strips, stages;
   int32_t* err;
 };
 
-// h and g of 8 columns
-__device__ __forceinline__ void norm_terms(const float (&x)[8], const float (&dy)[8], const float (&w)[8], float m, float r,
-                                           float (&h)[8], float (&g)[8]) {
+// h of a pack, into x
+__device__ __forceinline__ void norm_h(F32x2 (&x)[4], float m, float r) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    h[i] = __fmul_rn(__fsub_rn(x[i], m), r);
-    g[i] = __fmul_rn(dy[i], w[i]);
+  for (int i = 0; i < 4; ++i) x[i] = mul2(add2(x[i], both(-m)), both(r));
+}
+
+// the pack's part of sum g and sum g h
+__device__ __forceinline__ void norm_sums(const F32x2 (&h)[4], const F32x2 (&dy)[4], const F32x2 (&w)[4], F32x2& s1, F32x2& s2) {
+  F32x2 g[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = mul2(dy[i], w[i]);
+  s1 = dot4(dy, w, s1);
+  s2 = dot4(g, h, s2);
+}
+
+// dx of a pack
+__device__ __forceinline__ void norm_dx(const F32x2 (&h)[4], const F32x2 (&dy)[4], const F32x2 (&w)[4], float c1, float c2,
+                                        float r, F32x2 (&dx)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) dx[i] = mul2(fma2(h[i], both(-c2), fma2(dy[i], w[i], both(-c1))), both(r));
+}
+
+// the pack's part of dw and db
+__device__ __forceinline__ void norm_vectors(const F32x2 (&h)[4], const F32x2 (&dy)[4], F32x2 (&sw)[4], F32x2 (&sb)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sw[i] = fma2(dy[i], h[i], sw[i]);
+    sb[i] = add2(sb[i], dy[i]);
   }
 }
 
-template <class E, class O, bool AL>
+__device__ __forceinline__ void copy_async_16(void* shared, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(shared)), "l"(global) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The packs of one row that a warp's threads own (8 W apart for the j-th of each), copied into shared memory and read from it
+// by the same warp. Copies go by 16-byte vectors in the order of addresses; `room` holds the first halves of all packs,
+// then (fp32) the second ones, so that neither meets a bank twice.
+template <class E, int K>
+struct RowRing {
+  static constexpr int HALVES = sizeof(typename E::bits) * 8 / 16;
+  static __device__ __forceinline__ void fetch(uint4* room, const void* row, int warp, int lane, int packs, bool ok) {
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+#pragma unroll
+      for (int i = 0; i < HALVES; ++i) {
+        const int u = i * 32 + lane, p = warp * 32 + j * SLOTS + u / HALVES;  // vector u of the warp's 32 HALVES
+        if (p < packs && ok) copy_async_16(room + (u % HALVES) * packs + p, static_cast<const uint4*>(row) + p * HALVES + u % HALVES);
+      }
+  }
+  static __device__ __forceinline__ void read(const uint4* room, int p, int packs, F32x2 (&v)[4]) {
+    Pack<E> k;
+#pragma unroll
+    for (int i = 0; i < HALVES; ++i) ld_vec(k.w + 4 * i, room + i * packs + p);
+    unpack(k, v);
+  }
+};
+
+// Rows of whole packs on 16-byte boundaries, up to 8192 columns. A team of W warps takes a strip's rows in turn; the next
+// stages - 1 rows are on their way into shared memory meanwhile. Each thread keeps the sums of dw and db of its columns.
+template <class E, class O, int W, int K>
+__global__ void __launch_bounds__(NORM_THREADS, K <= 2 ? 2 : 1) norm_bwd_kernel(const NormGradArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];
+  __shared__ float rooms[32];
+  constexpr int XH = RowRing<E, K>::HALVES, DH = RowRing<O, K>::HALVES;
+  const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W), warp = tid >> 5, lane = tid & 31, packs = a.H / 8;
+  const int64_t strip = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
+  if (strip >= a.strips) return;  // the whole team
+  const int stage_vecs = packs * (XH + DH);
+  uint4* ring = reinterpret_cast<uint4*>(dyn) + static_cast<int64_t>(team) * a.stages * stage_vecs;
+  float* room = rooms + team * 4 * W;
+  const auto fetch = [&](int64_t t, int stage) {
+    const bool ok = t < a.T;
+    uint4* to = ring + stage * stage_vecs;
+    RowRing<E, K>::fetch(to, static_cast<const typename E::bits*>(a.x) + t * a.ld, warp, lane, packs, ok);
+    RowRing<O, K>::fetch(to + packs * XH, static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld, warp, lane, packs, ok);
+    copies_commit();
+  };
+  for (int i = 0; i < a.stages - 1; ++i) fetch(strip + static_cast<int64_t>(i) * a.strips, i);
+  F32x2 w[K][4], sw[K][4], sb[K][4];
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const int c0 = 8 * (tid + j * SLOTS);
+    if (c0 < a.H) vector8<E, true>(a.w, c0, a.H, 1.f, w[j], a.err);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sw[j][i] = sb[j][i] = 0;
+  }
+  const float len = static_cast<float>(a.H);
+  float m = a.mean ? a.mean[strip] : 0.f, r = a.rstd[strip];
+  int stage = 0, odd = 0;
+  for (int64_t t = strip; t < a.T; t += a.strips) {
+    __syncwarp();  // the stage that is filled next has been read by the whole warp
+    fetch(t + static_cast<int64_t>(a.stages - 1) * a.strips, stage == 0 ? a.stages - 1 : stage - 1);
+    const int64_t next = t + a.strips < a.T ? t + a.strips : t;
+    const float m1 = a.mean ? a.mean[next] : 0.f, r1 = a.rstd[next];
+    if (a.stages == 3) copies_wait<2>();
+    else copies_wait<3>();
+    __syncwarp();
+    const uint4* xs = ring + stage * stage_vecs;
+    F32x2 h[K][4], dy[K][4], s1 = 0, s2 = 0;
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (tid + j * SLOTS < packs) {
+        RowRing<E, K>::read(xs, tid + j * SLOTS, packs, h[j]);
+        RowRing<O, K>::read(xs + packs * XH, tid + j * SLOTS, packs, dy[j]);
+        norm_h(h[j], m, r);
+        norm_vectors(h[j], dy[j], sw[j], sb[j]);
+        norm_sums(h[j], dy[j], w[j], s1, s2);
+      }
+    if (a.dx) {
+      const float2 s = team_sum<W>(low_plus_high(s1), low_plus_high(s2), room + odd * 2 * W);
+      const float c1 = a.mean ? __fdiv_rn(s.x, len) : 0.f, c2 = __fdiv_rn(s.y, len);
+      auto* dx = static_cast<typename E::bits*>(a.dx) + t * a.dx_ld;
+#pragma unroll
+      for (int j = 0; j < K; ++j)
+        if (tid + j * SLOTS < packs) {
+          F32x2 v[4];
+          norm_dx(h[j], dy[j], w[j], c1, c2, r, v);
+          store_columns<E, true>(dx, 8 * (tid + j * SLOTS), a.H, v, a.err);
+        }
+    }
+    m = m1;
+    r = r1;
+    odd ^= 1;
+    stage = stage + 1 == a.stages ? 0 : stage + 1;
+  }
+  copies_wait<0>();
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const int c0 = 8 * (tid + j * SLOTS);
+    if (c0 >= a.H) continue;
+    if (a.part_w) store_columns<F32, true>(reinterpret_cast<uint32_t*>(a.part_w) + strip * a.H, c0, a.H, sw[j], a.err);
+    if (a.part_b) store_columns<F32, true>(reinterpret_cast<uint32_t*>(a.part_b) + strip * a.H, c0, a.H, sb[j], a.err);
+  }
+}
+
+// Any rows: first what the whole row gives, then the columns.
+template <class E, class O>
 __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_rows_kernel(const NormGradArgs a) {
   __shared__ float room[16];
   const int64_t t = blockIdx.x;
   const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
   const auto* dy = static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld;
   const float m = a.mean ? a.mean[t] : 0.f, r = a.rstd[t];
-  float s1 = 0.f, s2 = 0.f;
-  for (int p = threadIdx.x; p < (a.H + 7) / 8; p += SLOTS) {
-    float xv[8], dv[8], w[8], h[8], g[8];
-    unpack(load_columns<E, AL>(x, 8 * p, a.H, a.err), xv);
-    unpack(load_columns<O, AL>(dy, 8 * p, a.H, a.err), dv);
-    vector8(a.w, 8 * p, a.H, 1.f, w);
-    norm_terms(xv, dv, w, m, r, h, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = 8 * p + i < a.H ? __fmul_rn(g[i], h[i]) : 0.f;
-    s1 = __fadd_rn(s1, tree8(g));
-    s2 = __fadd_rn(s2, tree8(h));
+  F32x2 s1 = 0, s2 = 0;
+  for (int c = 8 * threadIdx.x; c < a.H; c += 8 * SLOTS) {
+    F32x2 h[4], dv[4], w[4];
+    unpack(load_columns<E, false>(x, c, a.H, a.err), h);
+    unpack(load_columns<O, false>(dy, c, a.H, a.err), dv);
+    vector8<E, false>(a.w, c, a.H, 1.f, w, a.err);
+    norm_h(h, m, r);
+    clear_beyond(h, c, a.H);
+    norm_sums(h, dv, w, s1, s2);
   }
-  const float2 s = slots_sum(s1, s2, room);
+  const float2 s = team_sum<8>(low_plus_high(s1), low_plus_high(s2), room);
   if (threadIdx.x == 0) {
     const float len = static_cast<float>(a.H);
     a.row[2 * t] = a.mean ? __fdiv_rn(s.x, len) : 0.f;
@@ -193,52 +376,87 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_rows_kernel(const NormG
   }
 }
 
-// dx, and the strip's part of dw and db, of 8 columns a thread.
-template <class E, class O, bool AL>
+template <class E, class O>
 __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_columns_kernel(const NormGradArgs a) {
   const int c0 = 8 * static_cast<int>(blockIdx.x * NORM_THREADS + threadIdx.x);
   if (c0 >= a.H) return;
-  float w[8], sw[8] = {}, sb[8] = {};
-  vector8(a.w, c0, a.H, 1.f, w);
+  F32x2 w[4], sw[4] = {}, sb[4] = {};
+  vector8<E, false>(a.w, c0, a.H, 1.f, w, a.err);
   for (int64_t t = blockIdx.y; t < a.T; t += a.strips) {
-    float xv[8], dv[8], h[8], g[8];
-    unpack(load_columns<E, AL>(static_cast<const typename E::bits*>(a.x) + t * a.ld, c0, a.H, a.err), xv);
-    unpack(load_columns<O, AL>(static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld, c0, a.H, a.err), dv);
+    F32x2 h[4], dv[4], v[4];
+    unpack(load_columns<E, false>(static_cast<const typename E::bits*>(a.x) + t * a.ld, c0, a.H, a.err), h);
+    unpack(load_columns<O, false>(static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld, c0, a.H, a.err), dv);
     const float m = a.mean ? a.mean[t] : 0.f, r = a.rstd[t];
-    norm_terms(xv, dv, w, m, r, h, g);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      sw[i] = __fmaf_rn(dv[i], h[i], sw[i]);
-      sb[i] = __fadd_rn(sb[i], dv[i]);
-    }
+    norm_h(h, m, r);
+    norm_vectors(h, dv, sw, sb);
     if (!a.dx) continue;
-    const float c1 = a.row[2 * t], c2 = a.row[2 * t + 1];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) g[i] = __fmul_rn(__fmaf_rn(-h[i], c2, __fsub_rn(g[i], c1)), r);
-    store_columns<E, AL>(static_cast<typename E::bits*>(a.dx) + t * a.dx_ld, c0, a.H, g, a.err);
+    norm_dx(h, dv, w, a.row[2 * t], a.row[2 * t + 1], r, v);
+    store_columns<E, false>(static_cast<typename E::bits*>(a.dx) + t * a.dx_ld, c0, a.H, v, a.err);
   }
   const int64_t at = static_cast<int64_t>(blockIdx.y) * a.H;
   if (a.part_w) store_columns<F32, false>(reinterpret_cast<uint32_t*>(a.part_w) + at, c0, a.H, sw, a.err);
   if (a.part_b) store_columns<F32, false>(reinterpret_cast<uint32_t*>(a.part_b) + at, c0, a.H, sb, a.err);
 }
 
-// dw and db from the strips' parts, added in ascending order.
-__global__ void __launch_bounds__(NORM_THREADS) norm_fold_kernel(const NormGradArgs a) {
-  const int c = blockIdx.x * NORM_THREADS + threadIdx.x;
-  if (c >= a.H) return;
+// dw and db from the strips' parts: warp i adds strips i, i + 32, ... in ascending order, then the 32 sums are added as a
+// balanced tree.
+__global__ void __launch_bounds__(1024) norm_fold_kernel(const NormGradArgs a) {
+  __shared__ float sums[32][33];
   const float* part = blockIdx.y ? a.part_b : a.part_w;
   float* out = blockIdx.y ? a.db : a.dw;
   if (!part) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   float s = 0.f;
+  if (c < a.H) {
 #pragma unroll 8
-  for (int i = 0; i < a.strips; ++i) s = __fadd_rn(s, part[static_cast<int64_t>(i) * a.H + c]);
-  out[c] = s;
+    for (int i = warp; i < a.strips; i += 32) s = __fadd_rn(s, part[static_cast<int64_t>(i) * a.H + c]);
+  }
+  sums[lane][warp] = s;
+  __syncthreads();
+  const float v = warp_sum(sums[warp][lane]);  // a column a warp
+  if (lane == 0 && blockIdx.x * 32 + warp < a.H) out[blockIdx.x * 32 + warp] = v;
 }
 
-inline int32_t strips_of(int64_t T) { return static_cast<int32_t>(T < NORM_STRIPS ? T : NORM_STRIPS); }
-
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
 inline bool vector_ok(const void* p, int32_t dtype, int32_t rows_dtype) {
   return !p || ((dtype == rows_dtype || dtype == RLK_DTYPE_F32) && on_boundary(p, dtype_bytes(dtype)));
+}
+
+// Calls f with the team's width and the packs a thread for rows of H columns, 8 per thread and pack.
+template <class F>
+inline rlk_status with_team(int64_t H, F f) {
+  const auto w = [&](auto warps, auto k) { return f(warps, k); };
+  using std::integral_constant;
+  switch (team_warps(static_cast<int>(H))) {
+    case 1: return w(integral_constant<int, 1>{}, integral_constant<int, 1>{});
+    case 2: return w(integral_constant<int, 2>{}, integral_constant<int, 1>{});
+    case 4: return w(integral_constant<int, 4>{}, integral_constant<int, 1>{});
+    default: break;
+  }
+  if (H <= 2048) return w(integral_constant<int, 8>{}, integral_constant<int, 1>{});
+  if (H <= 4096) return w(integral_constant<int, 8>{}, integral_constant<int, 2>{});
+  if (H <= 8192) return w(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+  return w(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+}
+
+constexpr int64_t FWD_KEPT = 16384;  // columns of a row that stays in registers (8 packs a thread)
+constexpr int64_t BWD_KEPT = 8192;   // and of one whose sums of dw and db do (4 packs)
+constexpr int BWD_SMEM = 110 * 1024;      // of each of the two CTAs of an SM
+constexpr int BWD_SMEM_ONE = 220 * 1024;  // of its only one
+
+template <class E, class O, int W, int K>
+inline rlk_status launch_norm_bwd(NormGradArgs a, int64_t stage_bytes, cudaStream_t s) {
+  // 4 stages, or as many as the CTAs of an SM (two of up to 2 packs a thread, by registers) have room for
+  const int64_t cta = stage_bytes * (8 / W), n = (K <= 2 ? BWD_SMEM : BWD_SMEM_ONE) / cta;
+  a.stages = static_cast<int32_t>(n > 4 ? 4 : n);  // 3 at least
+  const size_t smem = static_cast<size_t>(cta * a.stages);
+  const auto kernel = norm_bwd_kernel<E, O, W, K>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+    return RLK_ERR_CUDA;
+  kernel<<<static_cast<unsigned>((a.strips + 8 / W - 1) / (8 / W)), NORM_THREADS, smem, s>>>(a);
+  return launched();
 }
 
 }  // namespace
@@ -261,22 +479,30 @@ rlk_status rlk_layer_norm_fwd(const void* x, int32_t dtype, int64_t T, int64_t H
   const RowSpan in{x, T, H, ld, dtype_bytes(dtype)}, out{y, T, H, out_ld, dtype_bytes(out_dtype)};
   if (!same_rows(in, out) && !rows_apart(in, out)) return RLK_ERR_INVALID_ARG;
   if (T == 0) return RLK_OK;
+  const bool f32 = weight_dtype == RLK_DTYPE_F32;
   const NormArgs a{x, y, T, ld, out_ld, static_cast<int32_t>(H), centered != 0, static_cast<float>(eps),
-                   Vector{weight, weight_dtype}, Vector{bias, weight_dtype}, mean, rstd, err_flag};
-  const bool al = whole_packs(x, T, H, ld, in.eb) && whole_packs(y, T, H, out_ld, out.eb);
+                   Vector{weight, f32}, Vector{bias, f32}, mean, rstd, err_flag};
+  const bool kept = H <= FWD_KEPT && whole_packs(x, T, H, ld, in.eb) && whole_packs(y, T, H, out_ld, out.eb) &&
+                    on_boundary(weight, 16) && on_boundary(bias, 16);
+  const auto s = static_cast<cudaStream_t>(stream);
   return with_pair(dtype, out_dtype, [&](auto e, auto o) {
     using E = decltype(e);
     using O = decltype(o);
-    const auto s = static_cast<cudaStream_t>(stream);
-    if (al) norm_fwd_any_kernel<E, O, true><<<static_cast<unsigned>(T), NORM_THREADS, 0, s>>>(a);
-    else norm_fwd_any_kernel<E, O, false><<<static_cast<unsigned>(T), NORM_THREADS, 0, s>>>(a);
-    return launched();
+    if (!kept) {
+      norm_fwd_any_kernel<E, O><<<static_cast<unsigned>(T), NORM_THREADS, 0, s>>>(a);
+      return launched();
+    }
+    return with_team(H, [&](auto w, auto k) {
+      constexpr int W = decltype(w)::value, K = decltype(k)::value;
+      norm_fwd_kernel<E, O, W, K><<<static_cast<unsigned>((T + 8 / W - 1) / (8 / W)), NORM_THREADS, 0, s>>>(a);
+      return launched();
+    });
   });
 }
 
 size_t rlk_layer_norm_bwd_workspace(int64_t T, int64_t H) {
-  if (T <= 0 || H <= 0) return 0;
-  return carved(T * 2 * sizeof(float)) + 2 * carved(strips_of(T) * H * sizeof(float));
+  if (T <= 0 || H <= 0 || H > RLK_MAX_HIDDEN) return 0;
+  return carved(T * 2 * sizeof(float)) + 2 * carved(strips_of(T, static_cast<int>(H)) * H * sizeof(float));
 }
 
 rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t dy_ld, const void* x, int32_t dtype, int64_t ld,
@@ -303,29 +529,32 @@ rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t dy_ld, c
   }
   if (!workspace || !on_boundary(workspace, 256) || workspace_bytes < rlk_layer_norm_bwd_workspace(T, H))
     return RLK_ERR_WORKSPACE;
-  NormGradArgs a{dy, x, dx, T, dy_ld, ld, dx_ld, static_cast<int32_t>(H), Vector{weight, weight_dtype}, mean, rstd,
-                 static_cast<float*>(workspace), nullptr, nullptr, dw, db, strips_of(T), err_flag};
+  NormGradArgs a{dy, x, dx, T, dy_ld, ld, dx_ld, static_cast<int32_t>(H), Vector{weight, weight_dtype == RLK_DTYPE_F32},
+                 mean, rstd, static_cast<float*>(workspace), nullptr, nullptr, dw, db,
+                 strips_of(T, static_cast<int>(H)), 0, err_flag};
   const size_t part = carved(a.strips * H * sizeof(float));
   char* after = static_cast<char*>(workspace) + carved(T * 2 * sizeof(float));
   if (dw) a.part_w = reinterpret_cast<float*>(after);
   if (db) a.part_b = reinterpret_cast<float*>(after + part);
-  const bool al = whole_packs(x, T, H, ld, xs.eb) && whole_packs(dy, T, H, dy_ld, ds.eb) &&
-                  (!dx || whole_packs(dx, T, H, dx_ld, os.eb));
-  const unsigned blocks = static_cast<unsigned>((H + 8 * NORM_THREADS - 1) / (8 * NORM_THREADS));
-  return with_pair(dtype, dy_dtype, [&](auto e, auto o) {
+  const bool kept = H <= BWD_KEPT && whole_packs(x, T, H, ld, xs.eb) && whole_packs(dy, T, H, dy_ld, ds.eb) &&
+                    (!dx || whole_packs(dx, T, H, dx_ld, os.eb)) && on_boundary(weight, 16);
+  st = with_pair(dtype, dy_dtype, [&](auto e, auto o) {
     using E = decltype(e);
     using O = decltype(o);
-    const auto go = [&](auto aligned) {
-      constexpr bool AL = decltype(aligned)::value;
-      if (dx) norm_bwd_rows_kernel<E, O, AL><<<static_cast<unsigned>(T), NORM_THREADS, 0, s>>>(a);
-      norm_bwd_columns_kernel<E, O, AL><<<dim3(blocks, a.strips), NORM_THREADS, 0, s>>>(a);
-    };
-    if (al) go(Is<true>{});
-    else go(Is<false>{});
-    if (dw || db)
-      norm_fold_kernel<<<dim3(static_cast<unsigned>((H + NORM_THREADS - 1) / NORM_THREADS), 2), NORM_THREADS, 0, s>>>(a);
+    if (kept)
+      return with_team(H, [&](auto w, auto k) {
+        constexpr int W = decltype(w)::value, K = decltype(k)::value;
+        if constexpr (K <= 4) return launch_norm_bwd<E, O, W, K>(a, H * (xs.eb + ds.eb), s);
+        else return RLK_ERR_UNSUPPORTED;  // rows of BWD_KEPT columns have 4 packs a thread at most
+      });
+    if (dx) norm_bwd_rows_kernel<E, O><<<static_cast<unsigned>(T), NORM_THREADS, 0, s>>>(a);
+    const unsigned blocks = static_cast<unsigned>((H + 8 * NORM_THREADS - 1) / (8 * NORM_THREADS));
+    norm_bwd_columns_kernel<E, O><<<dim3(blocks, a.strips), NORM_THREADS, 0, s>>>(a);
     return launched();
   });
+  if (st != RLK_OK || !(dw || db)) return st;
+  norm_fold_kernel<<<dim3(static_cast<unsigned>((H + 31) / 32), 2), 1024, 0, s>>>(a);
+  return launched();
 }
 
 }  // extern "C"

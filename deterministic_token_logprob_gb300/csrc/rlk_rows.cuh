@@ -2,11 +2,13 @@
 // values cut into packs of 8 columns, their loads and stores at any alignment, sums over a row in one
 // fixed order, and the host-side argument checks.
 //
-// Order of a row's sums: pack p (columns 8 p .. 8 p + 7) belongs to slot p mod 256; a slot adds its
-// packs in ascending order, each pack's 8 values as a balanced tree; 32 slots combine by an
-// xor-butterfly, the eight groups of 32 by a balanced tree. Slots without packs hold 0, so that a row
-// of few packs can be taken by fewer warps with the same bits. The order depends on column indices
-// alone: not on the row's address, on alignment or on how many rows a CTA takes.
+// Order of a row's sums: pack p (columns 8 p .. 8 p + 7) belongs to slot p mod 256; a slot adds the even
+// and the odd columns of its packs apart, in ascending order of packs (a pack's four pairs as a balanced
+// tree; sums of products one by one, each product unrounded), and then the two; 32 slots combine by an
+// xor-butterfly, the eight groups of 32 by a balanced tree. Slots without packs hold 0, so that a row of few
+// packs is taken by fewer warps with the same bits.
+// The order depends on column indices alone: not on the row's address, on alignment or on how many
+// rows a CTA takes.
 #pragma once
 
 #include "rlk_logits.cuh"
@@ -37,38 +39,89 @@ __device__ __forceinline__ Pack<E> load_columns(const typename E::bits* row, int
   return k;
 }
 
+// The four pairs of a pack in fp32.
 template <class E>
-__device__ __forceinline__ void unpack(const Pack<E>& k, float (&v)[8]) {
+__device__ __forceinline__ void unpack(const Pack<E>& k, F32x2 (&v)[4]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 x = pair(k, i);
-    v[2 * i] = x.x;
-    v[2 * i + 1] = x.y;
+    v[i] = pack_f32x2(x.x, x.y);
+  }
+}
+
+// The assembler turns a packed product whose one use is a packed sum into a fused operation, whatever their rounding
+// modifiers say (seen on inputs that tell the two apart), and so differently from kernel to kernel. Products that
+// are added are therefore written as fused operations throughout; mul2 serves where no add2 follows, or where the product is exact.
+__device__ __forceinline__ F32x2 both(float v) { return pack_f32x2(v, v); }
+
+// 0 in the columns at and beyond n of a pack that starts at c0.
+__device__ __forceinline__ void clear_beyond(F32x2 (&v)[4], int c0, int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = unpack_f32x2(v[i]);
+    v[i] = pack_f32x2(c0 + 2 * i < n ? x.x : 0.f, c0 + 2 * i + 1 < n ? x.y : 0.f);
   }
 }
 
 template <class O, bool AL>
-__device__ __forceinline__ void store_columns(typename O::bits* row, int c0, int n, const float (&v)[8], int32_t* err) {
+__device__ __forceinline__ void store_columns(typename O::bits* row, int c0, int n, const F32x2 (&x)[4], int32_t* err) {
   if (!dbg_ok(c0 >= 0 && c0 < n && (!AL || c0 + 8 <= n), err)) return;
+  float2 v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = unpack_f32x2(x[i]);
   if constexpr (AL) {
     uint4* q = reinterpret_cast<uint4*>(row + c0);
     if constexpr (sizeof(typename O::bits) == 4) {
-      q[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
-      q[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+      q[0] = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+      q[1] = make_uint4(__float_as_uint(v[2].x), __float_as_uint(v[2].y), __float_as_uint(v[3].x), __float_as_uint(v[3].y));
     } else {
-      q[0] = make_uint4(O::pack2(v[0], v[1]), O::pack2(v[2], v[3]), O::pack2(v[4], v[5]), O::pack2(v[6], v[7]));
+      q[0] = make_uint4(O::pack2(v[0].x, v[0].y), O::pack2(v[1].x, v[1].y), O::pack2(v[2].x, v[2].y), O::pack2(v[3].x, v[3].y));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (c0 + i < n) row[c0 + i] = O::from_f32(v[i]);
+      if (c0 + i < n) row[c0 + i] = O::from_f32(i & 1 ? v[i / 2].y : v[i / 2].x);
   }
 }
 
-__device__ __forceinline__ float tree8(const float (&v)[8]) {
-  return __fadd_rn(__fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3])),
-                   __fadd_rn(__fadd_rn(v[4], v[5]), __fadd_rn(v[6], v[7])));
+__device__ __forceinline__ F32x2 tree4(const F32x2 (&v)[4]) { return add2(add2(v[0], v[1]), add2(v[2], v[3])); }
+// a + sum of x y over a pack's pairs, in ascending order
+__device__ __forceinline__ F32x2 dot4(const F32x2 (&x)[4], const F32x2 (&y)[4], F32x2 a) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a = fma2(x[i], y[i], a);
+  return a;
 }
+__device__ __forceinline__ float low_plus_high(F32x2 v) {
+  const float2 x = unpack_f32x2(v);
+  return __fadd_rn(x.x, x.y);
+}
+
+// Sums of two values over the slots of a row that W warps (a team, one of 8 / W of a CTA of 256) hold, in the fixed
+// order; every thread of the team gets both. `room`: 2 W floats of shared memory of the team's own, which the call
+// after this one does not use (one barrier a call then does).
+template <int W>
+__device__ __forceinline__ float2 team_sum(float a, float b, float* room) {
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W;
+  const bool low = lane < 16;
+  float v = __fadd_rn(low ? a : b, __shfl_xor_sync(kFullWarp, low ? b : a, 16));
+#pragma unroll
+  for (int d = 8; d >= 1; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFullWarp, v, d));
+  if constexpr (W == 1) return make_float2(__shfl_sync(kFullWarp, v, 0), __shfl_sync(kFullWarp, v, 16));
+  if ((lane & 15) == 0) room[(low ? 0 : W) + warp] = v;
+  if constexpr (W == 8) __syncthreads();
+  else asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x / (32 * W))), "n"(32 * W) : "memory");
+  float x[2 * W];
+#pragma unroll
+  for (int i = 0; i < 2 * W; ++i) x[i] = room[i];
+#pragma unroll
+  for (int d = 1; d < W; d *= 2)
+#pragma unroll
+    for (int i = 0; i < 2 * W; i += 2 * d) x[i] = __fadd_rn(x[i], x[i + d]);
+  return make_float2(x[0], x[W]);
+}
+
+// Warps that take a row of n columns: 1, 2, 4 or 8.
+__host__ __device__ constexpr int team_warps(int n) { return n <= 256 ? 1 : n <= 512 ? 2 : n <= 1024 ? 4 : 8; }
 
 // ---------------------------------------------------------------------------
 // host side

@@ -334,6 +334,12 @@ def test_norm_layouts(rlk, H):
             assert all(torch.equal(a, g) for a, g in zip(got, grads))
             to.fill_(9.0)
             assert bool((buf == 9.0).all())
+        odd = torch.empty(T * H + 1, dtype=dtype, device="cuda")[1:].view(T, H).copy_(x)
+        for centered in (True, False):                       # without weights
+            bare = [rlk.layer_norm_fwd(v, centered=centered, out_dtype=out) for v in (x, odd)]
+            assert torch.equal(bare[0][0], bare[1][0]) and torch.equal(bare[0][2], bare[1][2])
+            bare = [rlk.layer_norm_bwd(dy, v, None, bare[0][1], bare[0][2]) for v in (x, odd)]
+            assert all(torch.equal(p, q) for p, q in zip(*bare))
         some = rlk.layer_norm_fwd(x[5:9], w, b, out_dtype=out)
         assert torch.equal(some[0], y[5:9]) and torch.equal(some[1], mean[5:9])
         assert torch.equal(rlk.layer_norm_bwd(dy[5:9], x[5:9], w, mean[5:9], rstd[5:9])[0], grads[0][5:9])

@@ -1,8 +1,8 @@
 """Plain 64-bit forms of the operators around the head, and how far fp32 sums in a tree may be from them.
 
 U is half a step of fp32 (2^-24), the most that one operation is off, relative to its result. A row's
-sum goes through DEPTH(H) additions at most: ceil(ceil(H / 8) / 256) of a slot's packs, 3 within a
-pack, 5 in a warp, 3 over the warps. Every bound below counts roundings, times U, times the magnitudes that
+sum goes through depth(H) additions at most: 4 for each of a slot's ceil(ceil(H / 8) / 256) packs, 1 of even
+and odd columns, 5 in a warp, 3 over the warps. Every bound below counts roundings, times U, times the magnitudes that
 they round; second orders are inside the few roundings that each count is rounded up by.
 """
 import math
@@ -15,7 +15,7 @@ TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2
 
 
 def depth(H):
-    return -(-(-(-H // 8)) // 256) + 11
+    return 4 * -(-(-(-H // 8)) // 256) + 9
 
 
 def close(got, want, tol, name=""):
@@ -115,7 +115,8 @@ def norm_grad(dy, x, w, mean, rstd):
         t1 = torch.zeros_like(t1)
     dx = r * (g - c1 - h * c2)
     tx = r * (t1 + h.abs() * t2 + U * (4 * g.abs() + 3 * c1.abs() + 6 * (h * c2).abs()))
-    n = -(-T // 152) + min(T, 152) + 4              # additions in a strip, and over strips
+    S = min(T, 304 * (8 if H <= 256 else 4 if H <= 512 else 2 if H <= 1024 else 1))
+    n = -(-T // S) + -(-S // 32) + 5 + 3            # additions in a strip, over strips of a group, over groups; a term's own
     dw, db = (dy * h).sum(0), dy.sum(0)
     return (dx, dw, db), (tx, n * U * (dy * h).abs().sum(0), n * U * dy.abs().sum(0))
 
@@ -124,8 +125,8 @@ def norm_grad(dy, x, w, mean, rstd):
 
 
 def total_norm(grads):
-    """(norm, relative tolerance): per square one rounding, 3 in a pack, one for each pack of a thread's share (4
-    a chunk at most); half of all that through the root, and one to fp32."""
+    """(norm, relative tolerance): 5 roundings in a pack, one for each pack of a thread's share (4 a chunk at most);
+    half of all that through the root, and one to fp32."""
     chunks = sum(-(-g.numel() * g.element_size() // 16384) for g in grads)
     n = math.sqrt(math.fsum(float(g.double().square().sum()) for g in grads))
     return n, (0.5 * (4 * -(-chunks // 608) + 6) + 1) * U
