@@ -26,4 +26,4 @@ from .logits import (  # noqa: F401
     token_logprobs, token_logprobs_autograd, token_logprobs_bwd)
 from .training import (  # noqa: F401
     MAX_TENSORS, clip_grad_norm, embedding, embedding_bwd, embedding_bwd_workspace_bytes, embedding_fwd, grad_norm,
-    layer_norm, layer_norm_bwd, layer_norm_bwd_workspace_bytes, layer_norm_fwd)
+    grad_norm_workspace_bytes, layer_norm, layer_norm_bwd, layer_norm_bwd_workspace_bytes, layer_norm_fwd)

@@ -3,9 +3,9 @@
 //   out[t] = s E[id_t],   dE[v] (+)= s sum_{t : id_t = v} dout[t]
 //
 // The gradient sorts (token, position) stably, so that a token's positions stand side by side in
-// ascending order, and adds their rows in runs of 32 positions of that token: a run in ascending order,
-// then the runs in ascending order. What a row of dE holds depends on that token's rows alone, not on
-// which other tokens the batch or the shard has.
+// ascending order, and adds their rows in a fixed order: runs of 16 positions of that token, groups of 16
+// runs, all groups, each in ascending order. What a row of dE holds depends on that token's rows alone,
+// not on which other tokens the batch or the shard has.
 #include <algorithm>
 
 #include "rlk_rows.cuh"
@@ -71,7 +71,8 @@ constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
 constexpr int SORT_BINS = 512;  // 9 bits at most at a time: two passes for up to 2^18 rows
 constexpr int SORT_CTAS = 16;
-constexpr int RUN = 32;         // positions of one token that are added in one go
+constexpr int RUN = 16;         // positions of one token that are added in one go
+constexpr int GROUP = 16;       // runs
 
 struct Entry {
   uint32_t row;  // of the table; `rows`: none
@@ -85,16 +86,24 @@ struct SortArgs {
   Shard shard;
   int32_t* done;       // counters of the runs, to be zeroed
   int32_t n_done;
+  uint4* runs;         // [T]: those of tokens of several runs from the front, the others from the back
+  int32_t* n_runs;     // how many of each
   float* dW;           // to be zeroed by the other clusters, where n_zero > 0
   int64_t n_zero;
 };
 
-struct SortSmem {
+struct alignas(16) SortSmem {
   uint32_t count[SORT_WARPS][SORT_BINS];  // digits of each warp; then how many stand before the warp in this CTA
+  uint32_t lanes[SORT_WARPS][SORT_BINS];  // of a group's digits
   uint32_t total[SORT_CTAS][SORT_BINS];   // of each CTA of the cluster, which puts its own into all of them
   uint32_t base[SORT_BINS];               // where this CTA's entries of a digit start
   uint32_t warp_sum[SORT_WARPS];
 };
+
+__device__ __forceinline__ void st_cluster_u32x4(uint32_t addr, uint4 v) {
+  asm volatile("st.relaxed.cluster.shared::cluster.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
 
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
@@ -102,18 +111,31 @@ __device__ __forceinline__ uint32_t cluster_size() {
   return r;
 }
 
-__device__ __forceinline__ Entry sort_entry(const SortArgs& a, const Entry* src, int32_t t) {
+// Entries t, t + 32, ... below last, all of them on their way at once.
+template <int N>
+__device__ __forceinline__ void read_entries(const SortArgs& a, const Entry* src, int32_t t, int32_t last, Entry (&e)[N]) {
   if (src) {
-    const uint2 v = __ldcg(reinterpret_cast<const uint2*>(src + t));
-    return Entry{v.x, v.y};
+#pragma unroll
+    for (int g = 0; g < N; ++g)
+      if (t + 32 * g < last) {
+        const uint2 v = __ldcg(reinterpret_cast<const uint2*>(src + t + 32 * g));
+        e[g] = Entry{v.x, v.y};
+      }
+    return;
   }
-  const int32_t r = a.shard.row_of(a.ids[t]);
-  return Entry{r < 0 ? static_cast<uint32_t>(a.shard.rows) : static_cast<uint32_t>(r), static_cast<uint32_t>(t)};
+  int64_t id[N];
+#pragma unroll
+  for (int g = 0; g < N; ++g) id[g] = t + 32 * g < last ? a.ids[t + 32 * g] : -1;
+#pragma unroll
+  for (int g = 0; g < N; ++g) {
+    const int32_t r = a.shard.row_of(id[g]);
+    e[g] = Entry{r < 0 ? static_cast<uint32_t>(a.shard.rows) : static_cast<uint32_t>(r), static_cast<uint32_t>(t + 32 * g)};
+  }
 }
 
-// KEPT: every warp has up to KEPT groups of 32 positions, which stay in registers between the two ways through them;
-// 0: any number, read again.
-template <int KEPT>
+// A warp's positions go by in groups of 32, KEPT of them read at a time. ALL: those are all that a warp has, and they stay in
+// registers between the two ways through them.
+template <int KEPT, bool ALL>
 __device__ __forceinline__ void sort_tokens(const SortArgs& a, SortSmem& m) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank(), ctas = cluster_size();
@@ -124,42 +146,31 @@ __device__ __forceinline__ void sort_tokens(const SortArgs& a, SortSmem& m) {
   const int32_t last = static_cast<int32_t>(min(static_cast<int64_t>(a.T), lo + per));
   const int each = (a.bits + a.passes - 1) / a.passes;
   const int bins = 1 << each;
-  uint32_t* mine = m.count[warp];
+  uint32_t *mine = m.count[warp], *same = m.lanes[warp];
 
   for (int i = rank * SORT_THREADS + threadIdx.x; i < a.n_done; i += ctas * SORT_THREADS) a.done[i] = 0;
   for (int pass = 0; pass < a.passes; ++pass) {
     const Entry* src = pass == 0 ? nullptr : pass & 1 ? a.a : a.b;
     Entry* dst = pass & 1 ? a.b : a.a;
     const int shift = pass * each;
-    Entry kept[KEPT ? KEPT : 1];
-    if constexpr (KEPT > 0) {
+    Entry kept[KEPT];
+    // f(entry, digit, whether there is an entry) of each group
+    const auto groups = [&](bool again, auto f) {
+      for (int32_t t0 = first; t0 < last; t0 += 32 * KEPT) {
+        if (!ALL || !again) read_entries<KEPT>(a, src, t0 + lane, last, kept);
 #pragma unroll
-      for (int g = 0; g < KEPT; ++g)
-        if (first + 32 * g + lane < last) kept[g] = sort_entry(a, src, first + 32 * g + lane);
-    }
-    // f(digit, entry, lanes of the same digit) of each group; a digit beyond the bins: no entry
-    const auto groups = [&](auto f) {
-      const auto group = [&](const Entry& e, bool on) {
-        const uint32_t d = on ? (e.row >> shift) & static_cast<uint32_t>(bins - 1) : 0xFFFFFFFFu;
-        f(d, e, __match_any_sync(kFullWarp, d), on);
-      };
-      if constexpr (KEPT > 0) {
-#pragma unroll
-        for (int g = 0; g < KEPT; ++g)
-          if (first + 32 * g < last) group(kept[g], first + 32 * g + lane < last);
-      } else {
-        for (int32_t t = first; t < last; t += 32) {
-          Entry e{0, 0};
-          if (t + lane < last) e = sort_entry(a, src, t + lane);
-          group(e, t + lane < last);
+        for (int g = 0; g < KEPT; ++g) {
+          if (t0 + 32 * g >= last) break;
+          const bool on = t0 + 32 * g + lane < last;
+          f(kept[g], on ? (kept[g].row >> shift) & static_cast<uint32_t>(bins - 1) : 0, on);
         }
+        if (ALL) break;
       }
     };
-    for (int b = lane; b < bins; b += 32) mine[b] = 0;
+    for (int b = lane; b < bins; b += 32) mine[b] = same[b] = 0;
     __syncwarp();
-    groups([&](uint32_t d, const Entry&, uint32_t like, bool on) {
-      if (on && lane == __ffs(like) - 1) mine[d] += __popc(like);
-      __syncwarp();
+    groups(false, [&](const Entry&, uint32_t d, bool on) {
+      if (on) atomicAdd(&mine[d], 1u);
     });
     __syncthreads();
     const int b = threadIdx.x;
@@ -172,8 +183,12 @@ __device__ __forceinline__ void sort_tokens(const SortArgs& a, SortSmem& m) {
         m.count[w][b] = run;
         run += c[w];
       }
-      const uint32_t to = smem_u32(&m.total[rank][b]);
-      for (uint32_t c = 0; c < ctas; ++c) st_cluster_u32(map_to_cta(to, c), run);
+      m.total[rank][b] = run;
+    }
+    __syncthreads();
+    if (warp < static_cast<int>(ctas) && warp != static_cast<int>(rank)) {  // a warp for each other CTA
+      const uint32_t to = map_to_cta(smem_u32(m.total[rank]), warp);
+      for (int i = 4 * lane; i < bins; i += 128) st_cluster_u32x4(to + 4 * i, *reinterpret_cast<const uint4*>(&m.total[rank][i]));
     }
     cluster_sync();
     // all entries of lower digits, and those of this digit in CTAs before this one
@@ -199,10 +214,16 @@ __device__ __forceinline__ void sort_tokens(const SortArgs& a, SortSmem& m) {
       m.base[b] = lower + sum - all + before;
     }
     __syncthreads();
-    groups([&](uint32_t d, const Entry& e, uint32_t like, bool on) {
-      const uint32_t at = on ? m.base[d] + mine[d] + __popc(like & ((1u << lane) - 1)) : 0;
+    groups(true, [&](const Entry& e, uint32_t d, bool on) {
+      if (on) atomicOr(&same[d], 1u << lane);  // the lanes of each digit
       __syncwarp();
-      if (on && lane == __ffs(like) - 1) mine[d] += __popc(like);
+      const uint32_t like = on ? same[d] : 0, before = like & ((1u << lane) - 1);
+      const uint32_t at = on ? m.base[d] + mine[d] + __popc(before) : 0;
+      __syncwarp();
+      if (on && before == 0) {
+        mine[d] += __popc(like);
+        same[d] = 0;
+      }
       __syncwarp();
       if (on && dbg_ok(at < static_cast<uint32_t>(a.T), a.shard.err)) dst[at] = e;
     });
@@ -210,12 +231,95 @@ __device__ __forceinline__ void sort_tokens(const SortArgs& a, SortSmem& m) {
   }
 }
 
-template <int KEPT>
+// The first position in [lo, hi] from which on all rows are >= row (hi is such a one), by a whole warp.
+template <class At>
+__device__ __forceinline__ int32_t first_not_below(uint32_t row, int32_t lo, int32_t hi, int lane, const At& row_at) {
+  while (lo < hi) {
+    const int32_t step = (hi - lo + 31) / 32, base = lo;
+    const int64_t q = static_cast<int64_t>(lo) + static_cast<int64_t>(lane) * step;
+    const bool yes = q >= hi || row_at(static_cast<int32_t>(q)) >= row;
+    const uint32_t m = __ballot_sync(kFullWarp, yes);
+    const int f = m ? __ffs(m) - 1 : 32;
+    if (f < 32) hi = static_cast<int32_t>(min(static_cast<int64_t>(hi), static_cast<int64_t>(base) + static_cast<int64_t>(f) * step));
+    if (f > 0) lo = static_cast<int32_t>(min(static_cast<int64_t>(hi), static_cast<int64_t>(base) + static_cast<int64_t>(f - 1) * step + 1));
+  }
+  return hi;
+}
+
+// A run: its first position and whether it is the token's only one, the token's first position, row, and the run's first t.
+__device__ __forceinline__ uint4 pack_run(int32_t p, int32_t start, bool alone, uint32_t row, uint32_t t) {
+  return make_uint4(static_cast<uint32_t>(p) | (alone ? 0x80000000u : 0u), static_cast<uint32_t>(start), row, t);
+}
+
+// Lists the runs of the sorted positions: a warp goes through as many as it sorted, 4 groups of 32 at a time. The list's order
+// is whatever the counters give: which warp adds up which run changes nothing. Tokens of several runs come first, so that the
+// chain of sums that they end in does not come last.
+__device__ __forceinline__ void list_runs(const SortArgs& a, const Entry* sorted) {
+  constexpr int G = 4;
+  constexpr uint32_t kNone = 0xFFFFFFFFu;
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(cluster_size()) * SORT_WARPS;
+  const int32_t per = static_cast<int32_t>((a.T + 32 * warps - 1) / (32 * warps)) * 32;
+  const int64_t lo = (static_cast<int64_t>(cluster_ctarank()) * SORT_WARPS + (threadIdx.x >> 5)) * per;
+  const int32_t first = static_cast<int32_t>(min(static_cast<int64_t>(a.T), lo));
+  const int32_t last = static_cast<int32_t>(min(static_cast<int64_t>(a.T), lo + per));
+  const auto row_at = [&](int32_t p) { return __ldcg(&sorted[p].row); };
+  int32_t start0 = -1;           // where the token of the position before the group starts; -1: not known
+  uint32_t row0 = kNone;         // its row
+  if (first < last && first > 0) row0 = row_at(first - 1);
+  for (int32_t p0 = first; p0 < last; p0 += 32 * G) {
+    Entry e[G];
+    uint32_t far[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int32_t p = p0 + 32 * g + lane;
+      const uint2 v = p < last ? __ldcg(reinterpret_cast<const uint2*>(sorted + p)) : make_uint2(kNone, 0);
+      e[g] = Entry{v.x, v.y};
+      far[g] = p < last && p + RUN < a.T ? row_at(p + RUN) : kNone;
+    }
+    int32_t start[G];
+    uint32_t here[G], alone[G];
+    int several = 0, single = 0;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int32_t q0 = p0 + 32 * g;
+      uint32_t before = __shfl_up_sync(kFullWarp, e[g].row, 1);
+      if (lane == 0) before = row0;
+      const uint32_t heads = __ballot_sync(kFullWarp, e[g].row != before);
+      const uint32_t mine = heads & (0xFFFFFFFFu >> (31 - lane));  // heads at or before this lane
+      if (!(heads & 1u) && start0 < 0) start0 = first_not_below(row0, 0, q0 - 1, lane, row_at);
+      start[g] = mine ? q0 + 31 - __clz(mine) : start0;
+      here[g] = __ballot_sync(kFullWarp, e[g].row < static_cast<uint32_t>(a.shard.rows) && (q0 + lane - start[g]) % RUN == 0);
+      alone[g] = here[g] & __ballot_sync(kFullWarp, start[g] == q0 + lane && far[g] != e[g].row);
+      several += __popc(here[g] & ~alone[g]);
+      single += __popc(alone[g]);
+      row0 = __shfl_sync(kFullWarp, e[g].row, 31);
+      start0 = __shfl_sync(kFullWarp, start[g], 31);
+    }
+    int32_t at = 0;
+    if (lane < 2 && (lane ? single : several)) at = atomicAdd(&a.n_runs[lane], lane ? single : several);
+    int32_t front = __shfl_sync(kFullWarp, at, 0), back = a.T - 1 - __shfl_sync(kFullWarp, at, 1);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const int32_t p = p0 + 32 * g + lane;
+      const uint32_t below = (1u << lane) - 1;
+      const bool one = alone[g] >> lane & 1u;
+      const int32_t to = one ? back - __popc(alone[g] & below) : front + __popc(here[g] & ~alone[g] & below);
+      if ((here[g] >> lane & 1u) && dbg_ok(to >= 0 && to < a.T, a.shard.err)) a.runs[to] = pack_run(p, start[g], one, e[g].row, e[g].t);
+      front += __popc(here[g] & ~alone[g]);
+      back -= __popc(alone[g]);
+    }
+  }
+}
+
+template <int KEPT, bool ALL>
 __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   const uint32_t ctas = cluster_size();
   if (blockIdx.x < ctas) {
-    sort_tokens<KEPT>(a, *reinterpret_cast<SortSmem*>(dyn));
+    if (blockIdx.x == 0 && threadIdx.x < 2) a.n_runs[threadIdx.x] = 0;  // the cluster's barriers stand before its first use
+    sort_tokens<KEPT, ALL>(a, *reinterpret_cast<SortSmem*>(dyn));
+    list_runs(a, a.passes & 1 ? a.a : a.b);
     griddep_launch_dependents();
     return;
   }
@@ -237,6 +341,10 @@ __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortArg
 // ---------------------------------------------------------------------------
 struct GatherArgs {
   const Entry* sorted;  // [T]
+  const uint4* runs;
+  const int32_t* n_runs;
+  const int64_t* ids;   // of few tokens, which are not sorted
+  Shard shard;
   const void* dout;
   float* dW;
   int64_t ld;
@@ -244,92 +352,31 @@ struct GatherArgs {
   float scale;
   bool add;
   float* part;          // [2 slots][H rounded up to 8]: sums of the runs of tokens of more than one run
-  int32_t* done;        // [slots][slices]: runs of such a token that are through
-  int32_t slots;
+  int32_t* done;        // [3 slots][slices]: runs of such a group, and groups of such a token, that are through
+  int32_t slots, slices;
   int32_t* err;
 };
 
-__device__ __forceinline__ Entry entry_at(const GatherArgs& a, int32_t p) {
-  return dbg_ok(p >= 0 && p < a.T, a.err) ? a.sorted[p] : Entry{0xFFFFFFFFu, 0};
-}
-__device__ __forceinline__ uint32_t row_at(const GatherArgs& a, int32_t p) { return entry_at(a, p).row; }
+constexpr int GATHER_THREADS = 256;
 
-// The first position in [lo, hi] from which on all rows are >= row (hi is such a one), by a whole warp.
-__device__ __forceinline__ int32_t first_not_below(const GatherArgs& a, uint32_t row, int32_t lo, int32_t hi, int lane) {
-  while (lo < hi) {
-    const int32_t step = (hi - lo + 31) / 32;
-    const int64_t q = static_cast<int64_t>(lo) + static_cast<int64_t>(lane) * step;
-    const bool yes = q >= hi || row_at(a, static_cast<int32_t>(q)) >= row;
-    const uint32_t m = __ballot_sync(kFullWarp, yes);
-    const int f = m ? __ffs(m) - 1 : 32;
-    const int32_t base = lo;
-    if (f < 32) hi = static_cast<int32_t>(min(static_cast<int64_t>(hi), static_cast<int64_t>(base) + static_cast<int64_t>(f) * step));
-    if (f > 0) lo = static_cast<int32_t>(min(static_cast<int64_t>(hi), static_cast<int64_t>(base) + static_cast<int64_t>(f - 1) * step + 1));
-  }
-  return hi;
-}
-
-constexpr int GATHER_WARPS = 8;
-
-// A CTA takes a position, each of its warps a slice of 256 C columns; it has work where a run starts there. Bound by memory where
-// the tokens are many; what it takes is a chain of two loads (entries, then rows) and many warps to hide it, so everything
-// that the entries around the position tell is read at once, and the row of dW with the rows that are added to it.
-template <class E, bool AL, int C>
-__global__ void __launch_bounds__(32 * GATHER_WARPS) gather_kernel(const GatherArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int slice = static_cast<int>(blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5));
-  const int slices = static_cast<int>(gridDim.y * (blockDim.x >> 5));
-  const int32_t p = static_cast<int32_t>(blockIdx.x);
-  griddep_wait();
-  // this position and those after it, and the 32 before it
-  const int32_t back = p - 1 - lane, at = p + lane, beyond = p + RUN;
-  const Entry e = at < a.T ? entry_at(a, at) : Entry{0xFFFFFFFFu, 0};
-  const uint32_t row_back = back >= 0 ? row_at(a, back) : 0xFFFFFFFFu;
-  const uint32_t row_beyond = beyond < a.T ? row_at(a, beyond) : 0xFFFFFFFFu;
-  const uint32_t row = __shfl_sync(kFullWarp, e.row, 0);
-  if (row >= static_cast<uint32_t>(a.rows)) return;
-  // does a run start here?
-  const uint32_t same = __ballot_sync(kFullWarp, row_back == row);
-  int32_t start = p;
-  if (same & 1u) {
-    if (same != kFullWarp) return;
-    start = first_not_below(a, row, 0, p - RUN, lane);
-    if ((p - start) % RUN != 0) return;
-  }
-  const int n = __popc(__ballot_sync(kFullWarp, e.row == row));  // its length
-  const bool more = row_beyond == row, alone = start == p && !more;
-
-  const int c0 = 256 * C * slice + 8 * lane;
-  const auto on = [&](int j) { return c0 + 256 * j < a.H; };
-  auto* out = reinterpret_cast<uint32_t*>(a.dW) + static_cast<int64_t>(row) * a.H;
-  Pack<F32> old[C];
-  if (a.add && alone) {
-#pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (on(j)) old[j] = load_columns<F32, AL>(out, c0 + 256 * j, a.H, a.err);
-  }
-  F32x2 s[C][4];
-#pragma unroll
-  for (int j = 0; j < C; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s[j][i] = 0;
-  constexpr int U = 8 / C > 4 ? 4 : 8 / C;  // rows in flight
+// s += n rows of dout, row at(i) as the i-th, in C packs of a thread 256 columns apart from column c0 on.
+template <class E, bool AL, int C, class At>
+__device__ __forceinline__ void add_rows(const GatherArgs& a, int n, int c0, F32x2 (&s)[C][4], const At& at) {
+  constexpr int U = (sizeof(typename E::bits) == 4 ? 4 : 8) / C;  // rows in flight
   for (int i = 0; i < n; i += U) {
     Pack<E> k[U][C];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const uint32_t t = __shfl_sync(kFullWarp, e.t, (i + u) & 31);
-      const auto* r = static_cast<const typename E::bits*>(a.dout) + static_cast<int64_t>(t) * a.ld;
+      const auto* row = static_cast<const typename E::bits*>(a.dout) + static_cast<int64_t>(at(min(i + u, n - 1))) * a.ld;
 #pragma unroll
       for (int j = 0; j < C; ++j)
-        if (i + u < n && on(j)) k[u][j] = load_columns<E, AL>(r, c0 + 256 * j, a.H, a.err);
+        if (i + u < n && c0 + 256 * j < a.H) k[u][j] = load_columns<E, AL>(row, c0 + 256 * j, a.H, a.err);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (i + u >= n) break;
 #pragma unroll
       for (int j = 0; j < C; ++j) {
-        if (!on(j)) continue;
         F32x2 v[4];
         unpack(k[u][j], v);
 #pragma unroll
@@ -337,98 +384,255 @@ __global__ void __launch_bounds__(32 * GATHER_WARPS) gather_kernel(const GatherA
       }
     }
   }
-  if (!alone) {
-    // leave the run's sum; the warp that is through last adds them up
-    const int width = (a.H + 7) / 8 * 8;
-    const int32_t seg = (start + RUN - 1) / RUN;  // a token of several runs starts with a whole one
-    const int32_t slot = n == RUN ? (p + RUN - 1) / RUN : a.slots + seg;
-    const bool ok = dbg_ok(slot < 2 * a.slots && seg < a.slots, a.err);
+}
+
+// Writes a pack of a row of dW; old: what it held, where the gradient is added.
+template <bool AL>
+__device__ __forceinline__ void put_row(const GatherArgs& a, uint32_t* out, int c0, F32x2 (&s)[4], const Pack<F32>& old) {
+  F32x2 v[4];
+  unpack(old, v);
 #pragma unroll
-    for (int j = 0; j < C; ++j)
-      if (on(j) && ok)
-        store_columns<F32, true>(reinterpret_cast<uint32_t*>(a.part) + static_cast<int64_t>(slot) * width, c0 + 256 * j, width,
-                                 s[j], a.err);
-    const int32_t end = more ? first_not_below(a, row + 1, p + RUN, a.T, lane) : p + n;
-    const int32_t runs = (end - start + RUN - 1) / RUN;
-    __threadfence();
-    __syncwarp();
-    int32_t before = 0;
-    if (lane == 0 && ok) before = atomicAdd(&a.done[static_cast<int64_t>(seg) * slices + slice], 1);
-    if (__shfl_sync(kFullWarp, before, 0) != runs - 1) return;
-    __threadfence();
-    if (a.add) {
+  for (int i = 0; i < 4; ++i) s[i] = a.add ? fma2(s[i], both(a.scale), v[i]) : mul2(s[i], both(a.scale));
+  store_columns<F32, AL>(out, c0, a.H, s, a.err);
+}
+
+// Leaves a warp's part of a sum in its slot and counts it; whether it was the last of `parts`.
+template <int C>
+__device__ __forceinline__ bool leave_part(const GatherArgs& a, int32_t slot, int32_t counter, int32_t parts, int slice, int c0,
+                                           const F32x2 (&s)[C][4]) {
+  const int width = (a.H + 7) / 8 * 8;
+  const bool ok = dbg_ok(slot >= 0 && slot < 2 * a.slots && counter >= 0 && counter < 3 * a.slots, a.err);
 #pragma unroll
-      for (int j = 0; j < C; ++j)
-        if (on(j)) old[j] = load_columns<F32, AL>(out, c0 + 256 * j, a.H, a.err);
-    }
+  for (int j = 0; j < C; ++j)
+    if (ok && c0 + 256 * j < a.H)
+      store_columns<F32, true>(reinterpret_cast<uint32_t*>(a.part) + static_cast<int64_t>(slot) * width, c0 + 256 * j, width, s[j], a.err);
+  __threadfence();
+  __syncwarp();
+  int32_t before = -1;
+  if ((threadIdx.x & 31) == 0 && ok) before = atomicAdd(&a.done[static_cast<int64_t>(counter) * a.slices + slice], 1);
+  const bool last = __shfl_sync(kFullWarp, before, 0) == parts - 1;
+  if (last) __threadfence();
+  return last;
+}
+
+// The runs of a token of several: a whole run's slot is the multiple of RUN that it holds (over RUN), the last and shorter
+// one's follows from the token's first position (such a token starts with a whole run).
+struct Token {
+  int32_t start, end;
+  __device__ __forceinline__ int32_t first() const { return (start + RUN - 1) / RUN; }
+  __device__ __forceinline__ int32_t slot(const GatherArgs& a, int32_t run) const {
+    const int32_t q = start + run * RUN;
+    return q + RUN <= end ? (q + RUN - 1) / RUN : a.slots + first();
+  }
+};
+
+// s = the sum of runs lo, lo + each, ... of a token below hi, in that order
+template <int C>
+__device__ __forceinline__ void add_parts(const GatherArgs& a, const Token& k, int32_t lo, int32_t hi, int32_t each, int c0,
+                                          F32x2 (&s)[C][4]) {
+  constexpr int U = 4;  // of a pack in flight
+  const int width = (a.H + 7) / 8 * 8;
 #pragma unroll
-    for (int j = 0; j < C; ++j)
+  for (int j = 0; j < C; ++j) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s[j][i] = 0;
-#pragma unroll(4 / C)
-    for (int32_t i = 0; i < runs; ++i) {
-      const int32_t q = start + i * RUN;
-      const int32_t from = q + RUN <= end ? (q + RUN - 1) / RUN : a.slots + seg;
+    for (int i = 0; i < 4; ++i) s[j][i] = 0;
+    if (c0 + 256 * j >= a.H) continue;
+#pragma unroll 1
+    for (int32_t r = lo; r < hi; r += U * each) {
+      float4 x[U], y[U];
 #pragma unroll
-      for (int j = 0; j < C; ++j) {
-        if (!on(j)) continue;
-        const float4* r = reinterpret_cast<const float4*>(a.part + static_cast<int64_t>(from) * width + c0 + 256 * j);
-        const float4 x = __ldcg(r), y = __ldcg(r + 1);
-        s[j][0] = add2(s[j][0], pack_f32x2(x.x, x.y));
-        s[j][1] = add2(s[j][1], pack_f32x2(x.z, x.w));
-        s[j][2] = add2(s[j][2], pack_f32x2(y.x, y.y));
-        s[j][3] = add2(s[j][3], pack_f32x2(y.z, y.w));
+      for (int u = 0; u < U; ++u) {
+        const float* at = a.part + static_cast<int64_t>(k.slot(a, min(r + u * each, hi - 1))) * width + c0 + 256 * j;
+        x[u] = __ldcg(reinterpret_cast<const float4*>(at));
+        y[u] = __ldcg(reinterpret_cast<const float4*>(at) + 1);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (r + u * each >= hi) break;
+        s[j][0] = add2(s[j][0], pack_f32x2(x[u].x, x[u].y));
+        s[j][1] = add2(s[j][1], pack_f32x2(x[u].z, x[u].w));
+        s[j][2] = add2(s[j][2], pack_f32x2(y[u].x, y[u].y));
+        s[j][3] = add2(s[j][3], pack_f32x2(y[u].z, y[u].w));
       }
     }
   }
-#pragma unroll
-  for (int j = 0; j < C; ++j) {
-    if (!on(j)) continue;
-    if (a.add) {
-      F32x2 v[4];
-      unpack(old[j], v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[j][i] = fma2(s[j][i], both(a.scale), v[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s[j][i] = mul2(s[j][i], both(a.scale));
-    }
-    store_columns<F32, AL>(out, c0 + 256 * j, a.H, s[j], a.err);
-  }
 }
 
-// Packs of a slice's columns a lane: with 4, up to 1024 columns a warp.
-inline int slice_packs(int64_t H, bool aligned) { return !aligned || H <= 1024 ? 1 : 2; }
+// A CTA takes a run, each of its warps a slice of 256 C columns. A run is a chain of loads -- where it starts, its entries, its
+// rows and the row of dW -- which many small CTAs hide. Runs are short so that a token that comes often is spread over CTAs; the
+// warp that is through last in a group of runs adds up the group, and the last of the groups the token (a group's sum takes the
+// place of its first run's).
+template <class E, bool AL, int C>
+__global__ void __launch_bounds__(GATHER_THREADS, 3) gather_kernel(const GatherArgs a) {
+  const int lane = threadIdx.x & 31;
+  const int slice = static_cast<int>(blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)), c0 = 256 * C * slice + 8 * lane;
+  griddep_wait();
+  const int several = a.n_runs[0], runs_in_all = several + a.n_runs[1], i = static_cast<int>(blockIdx.x);
+  if (i >= runs_in_all) return;
+  const uint4 run = a.runs[i < several ? i : a.T - 1 - (i - several)];
+  const int32_t p = static_cast<int32_t>(run.x & 0x7FFFFFFFu);
+  const bool alone = run.x >> 31;
+  const uint32_t row = run.z;
+  if (!dbg_ok(p < a.T && row < static_cast<uint32_t>(a.rows) && run.w < static_cast<uint32_t>(a.T), a.err)) return;
+  const auto in = [&](uint32_t t) { return static_cast<const typename E::bits*>(a.dout) + static_cast<int64_t>(t) * a.ld; };
+  auto* out = reinterpret_cast<uint32_t*>(a.dW) + static_cast<int64_t>(row) * a.H;
+  // the run's other entries, its first row and the row of dW, all at once
+  const Entry e = lane < RUN && p + lane < a.T ? a.sorted[p + lane] : Entry{0xFFFFFFFFu, 0};
+  Pack<E> k0[C];
+  Pack<F32> old[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+    if (c0 + 256 * j < a.H) k0[j] = load_columns<E, AL>(in(run.w), c0 + 256 * j, a.H, a.err);
+  const auto read_old = [&] {
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+      if (a.add && c0 + 256 * j < a.H) old[j] = load_columns<F32, AL>(out, c0 + 256 * j, a.H, a.err);
+  };
+  if (alone) read_old();
+  const int n = __popc(__ballot_sync(kFullWarp, e.row == row) & 0xFFFFu);
+  F32x2 s[C][4];
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    unpack(k0[j], s[j]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[j][i] = add2(s[j][i], 0);  // -0 becomes 0, as in a sum of several
+  }
+  add_rows<E, AL, C>(a, n - 1, c0, s, [&](int r) { return __shfl_sync(kFullWarp, e.t, r + 1); });
+  if (!alone) {
+    Token k{static_cast<int32_t>(run.y), p + n};
+    if (n == RUN && p + RUN < a.T)
+      k.end = first_not_below(row + 1, p + RUN, a.T, lane, [&](int32_t q) { return a.sorted[q].row; });
+    const int32_t runs = (k.end - k.start + RUN - 1) / RUN, mine = (p - k.start) / RUN, lo = mine / GROUP * GROUP, hi = min(runs, lo + GROUP);
+    if (!leave_part<C>(a, k.slot(a, mine), k.slot(a, lo), hi - lo, slice, c0, s)) return;
+    add_parts<C>(a, k, lo, hi, 1, c0, s);
+    if (runs > GROUP) {
+      if (!leave_part<C>(a, k.slot(a, lo), 2 * a.slots + k.first(), (runs + GROUP - 1) / GROUP, slice, c0, s)) return;
+      add_parts<C>(a, k, 0, runs, GROUP, c0, s);
+    }
+    read_old();
+  }
+#pragma unroll
+  for (int j = 0; j < C; ++j)
+    if (c0 + 256 * j < a.H) put_row<AL>(a, out, c0 + 256 * j, s[j], old[j]);
+}
+
+// ---------------------------------------------------------------------------
+// few tokens
+// ---------------------------------------------------------------------------
+// Up to FEW_TOKENS tokens need no sorting: every CTA reads all ids, and the one of a token's first position has its others
+// from that. The CTAs behind those write zeros into the rows that no token points at (where dW is new). One launch: 64
+// rows of 256 into 4096 take 3 us on the GPU, with the sort 7.5. Sums in the same order as above, the same bits.
+constexpr int FEW_TOKENS = 256;
+constexpr int ZERO_ROWS = 2048;  // rows that a CTA zeroes, at most
+
+template <class E, bool AL>
+__global__ void __launch_bounds__(GATHER_THREADS) gather_few_kernel(const GatherArgs a, int32_t blocks, int32_t per) {
+  __shared__ int32_t row_at_t[FEW_TOKENS];
+  __shared__ uint32_t list[FEW_TOKENS];
+  __shared__ int32_t found;  // positions of the token, 0: this is not its first
+  __shared__ uint8_t met[ZERO_ROWS];
+  const int tid = threadIdx.x, threads = blockDim.x;
+  for (int t = tid; t < a.T; t += threads) row_at_t[t] = a.shard.row_of(a.ids[t]);
+  const int32_t z = static_cast<int32_t>(blockIdx.x) - a.T * blocks;
+  if (z >= 0) {
+    const int32_t r0 = z * per, n = min(per, a.rows - r0);
+    for (int i = tid; i < n; i += threads) met[i] = 0;
+    __syncthreads();
+    for (int t = tid; t < a.T; t += threads) {
+      const int32_t i = row_at_t[t] - r0;
+      if (row_at_t[t] >= 0 && i >= 0 && i < n) met[i] = 1;
+    }
+    __syncthreads();
+    // tx threads a row
+    int tx = 1;
+    while (tx < threads && tx * 4 < a.H) tx *= 2;
+    const int x = tid % tx, ty = threads / tx;
+    for (int i = tid / tx; i < n; i += ty) {
+      if (met[i]) continue;
+      float* row = a.dW + static_cast<int64_t>(r0 + i) * a.H;
+      if constexpr (AL) {
+        for (int c = 4 * x; c < a.H; c += 4 * tx) *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      } else {
+        for (int c = x; c < a.H; c += tx) row[c] = 0.f;
+      }
+    }
+    return;
+  }
+  __syncthreads();
+  const int p = static_cast<int>(blockIdx.x) / blocks, block = static_cast<int>(blockIdx.x) % blocks;
+  const int32_t row = row_at_t[p];
+  if (row < 0) return;
+  if (tid < 32) {
+    int n = 0;
+    bool first = true;
+    for (int t = 0; t < a.T; t += 32) {
+      const bool like = t + tid < a.T && row_at_t[t + tid] == row;
+      const uint32_t m = __ballot_sync(kFullWarp, like);
+      if (like) list[n + __popc(m & ((1u << tid) - 1))] = t + tid;
+      if (n == 0 && m != 0) first = t + __ffs(m) - 1 == p;
+      n += __popc(m);
+    }
+    if (tid == 0) found = first ? n : 0;
+  }
+  __syncthreads();
+  const int n = found, c0 = 8 * (block * threads + tid);
+  if (n == 0 || c0 >= a.H) return;
+  auto* out = reinterpret_cast<uint32_t*>(a.dW) + static_cast<int64_t>(row) * a.H;
+  Pack<F32> old{};
+  if (a.add) old = load_columns<F32, AL>(out, c0, a.H, a.err);
+  F32x2 s[1][4] = {};
+  if (n <= RUN) {
+    add_rows<E, AL, 1>(a, n, c0, s, [&](int i) { return list[i]; });
+  } else {
+    static_assert(FEW_TOKENS <= RUN * GROUP, "one group");
+    for (int i = 0; i < n; i += RUN) {
+      F32x2 v[1][4] = {};
+      add_rows<E, AL, 1>(a, min(RUN, n - i), c0, v, [&](int q) { return list[i + q]; });
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[0][j] = add2(s[0][j], v[0][j]);
+    }
+  }
+  put_row<AL>(a, out, c0, s[0], old);
+}
 
 struct Room {  // the workspace of a gradient
-  size_t a, b, done, part, all;
+  size_t a, b, runs, done, part, all;
   int32_t slots;
 };
 
 inline Room room_of(int64_t T, int64_t H) {
   Room r{};
+  if (T <= FEW_TOKENS) return r;
   r.slots = static_cast<int32_t>(T / RUN + 1);
-  r.a = 0;
   r.b = carved(T * sizeof(Entry));
-  r.done = 2 * r.b;
-  r.part = r.done + carved(static_cast<size_t>(r.slots) * ((H + 255) / 256 + GATHER_WARPS) * sizeof(int32_t));
+  r.runs = 2 * r.b;
+  r.done = r.runs + carved((T + 1) * sizeof(uint4));  // the list, and how many it has
+  r.part = r.done + carved(3 * static_cast<size_t>(r.slots) * ((H + 255) / 256 + 8) * sizeof(int32_t));
   r.all = r.part + carved(2 * static_cast<size_t>(r.slots) * ((H + 7) / 8 * 8) * sizeof(float));
   return r;
 }
 
-// A kernel that may start while the one before it on the stream ends (it waits for it by itself).
-template <class A>
-inline rlk_status launch_after(void (*kernel)(A), const A& a, dim3 grid, int threads, cudaStream_t s) {
+template <int KEPT, bool ALL>
+inline rlk_status launch_sort(const SortArgs& q, int ctas, int64_t zero, cudaStream_t s) {
+  static OncePerDevice allowed;
+  const auto kernel = sort_tokens_kernel<KEPT, ALL>;
+  if (!allowed([&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)) == cudaSuccess &&
+               cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+      }))
+    return RLK_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas + zero));
+  cfg.blockDim = dim3(SORT_THREADS);
+  cfg.dynamicSmemBytes = sizeof(SortSmem);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = ctas;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kernel, q) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
 }
 
 inline rlk_status check_shard(int64_t rows, int64_t start, int64_t V_true) {
@@ -490,50 +694,53 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
     return RLK_OK;
   }
   const Room r = room_of(T, H);
-  if (!workspace || !on_boundary(workspace, 256) || workspace_bytes < r.all) return RLK_ERR_WORKSPACE;
+  if (r.all > 0 && (!workspace || !on_boundary(workspace, 256) || workspace_bytes < r.all)) return RLK_ERR_WORKSPACE;
   const bool al = whole_packs(dout, T, H, ld, in.eb) && on_boundary(dW, 16);
-  const int packs = slice_packs(H, al);
-  const int warps = static_cast<int>(std::min<int64_t>(GATHER_WARPS, (H + 256 * packs - 1) / (256 * packs)));
-  const int blocks = static_cast<int>((H + 256 * packs * warps - 1) / (256 * packs * warps)), slices = blocks * warps;
+  const Shard shard{vocab_start, V_local, V_true, err_flag};
+  GatherArgs g{nullptr, nullptr, nullptr, ids, shard, dout, dW, ld, static_cast<int32_t>(T), static_cast<int32_t>(H),
+               static_cast<int32_t>(V_local), static_cast<float>(scale), accumulate != 0, nullptr, nullptr, r.slots, 0, err_flag};
+  if (T <= FEW_TOKENS) {
+    const int threads = static_cast<int>(H >= 8 * GATHER_THREADS ? GATHER_THREADS : (H + 255) / 256 * 32);
+    const int32_t blocks = static_cast<int32_t>((H + 8 * threads - 1) / (8 * threads));
+    // the CTAs that write zeros: eight an SM, or as many as their share of the rows asks for
+    const int32_t per = static_cast<int32_t>(std::min<int64_t>(ZERO_ROWS, (V_local + 1215) / 1216));
+    const int64_t ctas = T * blocks + (accumulate ? 0 : (V_local + per - 1) / per);
+    return with_type(dtype, [&](auto e) {
+      const auto kernel = al ? gather_few_kernel<decltype(e), true> : gather_few_kernel<decltype(e), false>;
+      kernel<<<static_cast<unsigned>(ctas), threads, 0, s>>>(g, blocks, per);
+      return launched();
+    });
+  }
+  const int packs = H > 256 ? 2 : 1;  // a lane's in a slice
+  const int warps = static_cast<int>(std::min<int64_t>(GATHER_THREADS / 32, (H + 256 * packs - 1) / (256 * packs)));
+  const int blocks = static_cast<int>((H + 256 * packs * warps - 1) / (256 * packs * warps));
+  g.slices = blocks * warps;
   char* ws = static_cast<char*>(workspace);
-  SortArgs q{ids, reinterpret_cast<Entry*>(ws + r.a), reinterpret_cast<Entry*>(ws + r.b), static_cast<int32_t>(T), 0, 0,
-             Shard{vocab_start, V_local, V_true, err_flag}, reinterpret_cast<int32_t*>(ws + r.done), r.slots * slices,
-             dW, accumulate ? 0 : V_local * H};
+  auto* runs = reinterpret_cast<uint4*>(ws + r.runs);
+  auto* n_runs = reinterpret_cast<int32_t*>(runs + T);
+  SortArgs q{ids, reinterpret_cast<Entry*>(ws + r.a), reinterpret_cast<Entry*>(ws + r.b), static_cast<int32_t>(T), 0, 0, shard,
+             reinterpret_cast<int32_t*>(ws + r.done), 3 * r.slots * g.slices, runs, n_runs, dW, accumulate ? 0 : V_local * H};
   while (V_local >> q.bits) ++q.bits;  // rows and the mark behind them: 0 .. V_local
   q.passes = (q.bits + 8) / 9;
-
-  // one cluster sorts, the others (if any) zero dW
+  // one cluster sorts, two positions a thread while it can; the others (if any) zero dW: 304 CTAs, two an SM
   int ctas = 1;
   while (ctas < SORT_CTAS && T > 2 * SORT_THREADS * ctas) ctas *= 2;
-  int64_t zero = accumulate ? 0 : (V_local * H + 16 * 4 * SORT_THREADS - 1) / (16 * 4 * SORT_THREADS);
-  if (zero > 456) zero = 456;
+  int64_t zero = accumulate ? 0 : std::min<int64_t>(304, (V_local * H + 64 * SORT_THREADS - 1) / (64 * SORT_THREADS));
   zero = (zero + ctas - 1) / ctas * ctas;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas + zero));
-  cfg.blockDim = dim3(SORT_THREADS);
-  cfg.dynamicSmemBytes = sizeof(SortSmem);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  const int64_t groups = (T + 32 * SORT_WARPS * ctas - 1) / (32 * SORT_WARPS * ctas);
-  const auto sort = groups <= 1 ? sort_tokens_kernel<1> : groups <= 4 ? sort_tokens_kernel<4> : sort_tokens_kernel<0>;
-  if (cudaFuncSetAttribute(sort, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)) != cudaSuccess ||
-      cudaFuncSetAttribute(sort, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return RLK_ERR_CUDA;
-  if (cudaLaunchKernelEx(&cfg, sort, q) != cudaSuccess) return RLK_ERR_CUDA;
-
-  const GatherArgs g{q.passes & 1 ? q.a : q.b, dout, dW, ld, q.T, static_cast<int32_t>(H), static_cast<int32_t>(V_local),
-                     static_cast<float>(scale), accumulate != 0, reinterpret_cast<float*>(ws + r.part), q.done, r.slots,
-                     err_flag};
+  const int64_t groups = (T + SORT_THREADS * ctas - 1) / (SORT_THREADS * ctas);
+  st = groups <= 2 ? launch_sort<2, true>(q, ctas, zero, s)
+                   : groups <= 8 ? launch_sort<8, true>(q, ctas, zero, s) : launch_sort<8, false>(q, ctas, zero, s);
+  if (st != RLK_OK) return st;
+  g.sorted = q.passes & 1 ? q.a : q.b;
+  g.runs = runs;
+  g.n_runs = n_runs;
+  g.part = reinterpret_cast<float*>(ws + r.part);
+  g.done = q.done;
   return with_type(dtype, [&](auto e) {
     using E = decltype(e);
-    const auto kernel = !al ? gather_kernel<E, false, 1>
-                        : packs == 1 ? gather_kernel<E, true, 1> : gather_kernel<E, true, 2>;
-    return launch_after(kernel, g, dim3(static_cast<unsigned>(T), blocks), 32 * warps, s);
+    const auto kernel = packs == 1 ? (al ? gather_kernel<E, true, 1> : gather_kernel<E, false, 1>)
+                                   : (al ? gather_kernel<E, true, 2> : gather_kernel<E, false, 2>);
+    return launch_after(kernel, dim3(static_cast<unsigned>(T), blocks), 32 * warps, s, g);
   });
 }
 

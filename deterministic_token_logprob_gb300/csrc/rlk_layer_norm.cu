@@ -340,6 +340,7 @@ __global__ void __launch_bounds__(NORM_THREADS, K <= 2 ? 2 : 1) norm_bwd_kernel(
     odd ^= 1;
     stage = stage + 1 == a.stages ? 0 : stage + 1;
   }
+  griddep_launch_dependents();
   copies_wait<0>();
 #pragma unroll
   for (int j = 0; j < K; ++j) {
@@ -405,6 +406,7 @@ __global__ void __launch_bounds__(1024) norm_fold_kernel(const NormGradArgs a) {
   const float* part = blockIdx.y ? a.part_b : a.part_w;
   float* out = blockIdx.y ? a.db : a.dw;
   if (!part) return;
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (c < a.H) {
@@ -453,7 +455,10 @@ inline rlk_status launch_norm_bwd(NormGradArgs a, int64_t stage_bytes, cudaStrea
   a.stages = static_cast<int32_t>(n > 4 ? 4 : n);  // 3 at least
   const size_t smem = static_cast<size_t>(cta * a.stages);
   const auto kernel = norm_bwd_kernel<E, O, W, K>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+  static OncePerDevice allowed;
+  if (!allowed([&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K <= 2 ? BWD_SMEM : BWD_SMEM_ONE) == cudaSuccess;
+      }))
     return RLK_ERR_CUDA;
   kernel<<<static_cast<unsigned>((a.strips + 8 / W - 1) / (8 / W)), NORM_THREADS, smem, s>>>(a);
   return launched();
@@ -553,8 +558,7 @@ rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t dy_ld, c
     return launched();
   });
   if (st != RLK_OK || !(dw || db)) return st;
-  norm_fold_kernel<<<dim3(static_cast<unsigned>((H + 31) / 32), 2), 1024, 0, s>>>(a);
-  return launched();
+  return launch_after(norm_fold_kernel, dim3(static_cast<unsigned>((H + 31) / 32), 2), 1024, s, a);
 }
 
 }  // extern "C"

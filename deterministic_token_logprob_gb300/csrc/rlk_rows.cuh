@@ -11,6 +11,8 @@
 // rows a CTA takes.
 #pragma once
 
+#include <atomic>
+
 #include "rlk_logits.cuh"
 
 namespace rlk {
@@ -184,6 +186,36 @@ inline rlk_status with_pair(int32_t dtype, int32_t out_dtype, F f) {
   if (dtype == RLK_DTYPE_BF16) return f(Bf16{}, Bf16{});
   if (dtype == RLK_DTYPE_F16) return f(F16{}, F16{});
   return out_dtype == RLK_DTYPE_BF16 ? f(F32{}, Bf16{}) : f(F32{}, F32{});
+}
+
+// What a kernel has to be allowed, asked for once per device (racing first calls ask for the same).
+struct OncePerDevice {
+  std::atomic<uint64_t> done{0};
+  template <class F>
+  bool operator()(F ask) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev >= 0 && dev < 64 ? uint64_t{1} << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return true;
+    if (!ask()) return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
+  }
+};
+
+// A kernel that may start while the one before it on the stream ends (it waits for it by itself).
+template <class... A>
+inline rlk_status launch_after(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t s, const A&... a) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a...) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
 }
 
 inline rlk_status launched() { return cudaGetLastError() == cudaSuccess ? RLK_OK : RLK_ERR_CUDA; }

@@ -525,8 +525,8 @@ RLK_API rlk_status rlk_embedding_fwd(const void* table, int32_t dtype, int64_t V
                                      int64_t vocab_start, int64_t V_true, const int64_t* ids, int64_t T, double scale,
                                      void* out, int32_t out_dtype, int64_t out_ld, int32_t* err_flag, void* stream);
 
-/* Bytes of device workspace rlk_embedding_bwd needs: the sorted tokens (16 T bytes) and the sums of tokens that
- * come more than 32 times (up to T H / 4 bytes). */
+/* Bytes of device workspace rlk_embedding_bwd needs: the sorted tokens (32 T bytes) and the sums of tokens that
+ * come more than 16 times (up to T H / 2 bytes); 0 (and workspace may be NULL) for up to 256 tokens. */
 RLK_API size_t rlk_embedding_bwd_workspace(int64_t T, int64_t H);
 
 /*
@@ -536,8 +536,8 @@ RLK_API size_t rlk_embedding_bwd_workspace(int64_t T, int64_t H);
  *   accumulate  0: dW is written, with zeros in the rows of tokens that do not come; 1: the gradient is added to what dW
  *            holds (a tied model's head has been there), one rounding an element, and other rows are not touched
  * Ids of -1 and of other shards add nothing; any other id outside [0, V_true) adds nothing and ORs RLK_FLAG_BAD_TARGET
- * in. A token's rows are added in the order of t, in runs of 32 whose sums are added in turn: the order
- * does not depend on the other tokens or on the shard. T == 0 with accumulate == 0 writes zeros.
+ * in. A token's rows are added in the order of t, in runs of 16, the runs' sums in groups of 16, and the groups' sums:
+ * the order does not depend on the other tokens or on the shard. T == 0 with accumulate == 0 writes zeros.
  */
 RLK_API rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t H, int64_t ld,
                                      const int64_t* ids, int64_t V_local, int64_t vocab_start, int64_t V_true,

@@ -128,8 +128,8 @@ def many_tokens(gen, T, V, kind):
         return torch.randint(0, V, (T,), generator=gen, device="cuda")
     if kind == "one":
         return torch.full((T,), V - 1, device="cuda")
-    if kind == "runs":  # tokens that come 1, 31, 32, 33, 63, 64, 65, ... times
-        n = torch.tensor([1, 31, 32, 33, 63, 64, 65, 1, 96, 97, 2, 129], device="cuda")
+    if kind == "runs":  # tokens that come 1, 15, 16, 17, 31, 32, 33, ... times, and the last one as often as there is room
+        n = torch.tensor([1, 15, 31, 16, 32, 33, 17, 63, 64, 65, 1, 96, 97, 2, 129, 255, 256, 257, 513], device="cuda")
         n = torch.repeat_interleave(torch.arange(len(n), device="cuda"), n)
         x = torch.full((T,), V - 1, device="cuda")
         x[:min(T, len(n))] = n[:T] % V
@@ -141,7 +141,8 @@ def many_tokens(gen, T, V, kind):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("T,H,V,kind", [
     (1, 8, 1, "one"), (1, 1, 1, "one"), (2, 64, 5, "even"), (31, 7, 3, "even"), (33, 256, 1, "one"), (64, 256, 4096, "zipf"),
-    (700, 40, 20, "runs"), (700, 2056, 20, "runs"), (1000, 257, 300, "even"), (1024, 64, 1 << 18, "zipf"),
+    (700, 40, 20, "runs"), (700, 2056, 20, "runs"), (2500, 264, 30, "runs"), (255, 72, 9, "runs"), (256, 4096, 50, "zipf"),
+    (256, 30, 3000, "one"), (257, 72, 5000, "even"), (10, 16, 3000000, "even"), (1000, 257, 300, "even"), (1024, 64, 1 << 18, "zipf"),
     (1025, 64, (1 << 18) - 1, "zipf"), (3000, 4096, 151936, "zipf"), (5000, 4104, 4000, "even"), (4097, 1001, 511, "zipf"),
     (8192, 520, 512, "zipf"), (9000, 264, 50257, "one"), (20000, 16, 1000, "runs"), (16385, 24, 1 << 20, "even"),
     (300, 8200, 100, "zipf"), (300, 65536, 7, "runs"), (200000, 8, 151936, "zipf"), (100, 2, 1 << 24, "even")])
@@ -547,7 +548,7 @@ def test_refusals(rlk):
             (ValueError, lambda: rlk.embedding_bwd(x, ids[:3], 4)), (ValueError, lambda: rlk.embedding_bwd(x, ids, 4, accumulate=True)),
             (ValueError, lambda: rlk.embedding_bwd(x, ids, 4, out=torch.ones((5, 16), device="cuda"))),
             (TypeError, lambda: rlk.embedding_bwd(x, ids, 4, out=x.half())), (rlk.RlkError, lambda: rlk.embedding_bwd(x, ids, 4, out=x)),
-            (ValueError, lambda: rlk.embedding_bwd(x, ids, 4, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))),
+            (ValueError, lambda: rlk.embedding_bwd(x.repeat(100, 1), ids.repeat(100), 4, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))),
             (rlk.RlkError, lambda: rlk.embedding_bwd(x, ids, 0)),
             (TypeError, lambda: rlk.layer_norm_fwd(x, w.half())), (TypeError, lambda: rlk.layer_norm_fwd(x.half(), w, w.half())),
             (ValueError, lambda: rlk.layer_norm_fwd(x, w[:8])), (rlk.RlkError, lambda: rlk.layer_norm_fwd(x, w, eps=0.0)),

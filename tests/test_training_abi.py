@@ -31,7 +31,7 @@ def call(fn, defaults, **k):
 
 LOOKUP = dict(table=FAKE, dtype=BF16, V=4096, H=64, ld=64, start=0, V_true=4096, ids=FAKE, T=0, scale=1.0, out=FAR,
               out_dtype=BF16, out_ld=64, err=None, stream=None)
-TABLE = dict(dout=FAKE, dtype=BF16, T=4, H=64, ld=64, ids=FAKE, V=4096, start=0, V_true=4096, scale=1.0, dW=FAR, add=1,
+TABLE = dict(dout=FAKE, dtype=BF16, T=300, H=64, ld=64, ids=FAKE, V=4096, start=0, V_true=4096, scale=1.0, dW=FAR, add=1,
              err=None, ws=None, ws_bytes=0, stream=None)
 NORM = dict(x=FAKE, dtype=BF16, T=0, H=64, ld=64, w=FAKE, b=FAKE, wdtype=F32, centered=1, eps=1e-5, y=FAR, out_dtype=BF16,
             out_ld=64, mean=FAKE, rstd=FAKE, err=None, stream=None)
@@ -71,7 +71,7 @@ def test_lookup_arguments(lib):
 def test_table_gradient_arguments(lib):
     f = lib.rlk_embedding_bwd
     assert call(f, TABLE) == WORKSPACE
-    need = lib.rlk_embedding_bwd_workspace(4, 64)
+    need = lib.rlk_embedding_bwd_workspace(300, 64)
     assert call(f, TABLE, ws=FAKE, ws_bytes=need - 1) == WORKSPACE
     assert call(f, TABLE, ws=HALF, ws_bytes=need) == WORKSPACE
     assert call(f, TABLE, T=0) == OK                                # nothing to add
@@ -92,7 +92,7 @@ def test_table_gradient_arguments(lib):
     assert call(f, TABLE, T=(1 << 24) + 1, **more) == UNSUPPORTED
     assert call(f, TABLE, V=(1 << 24) + 1, **more) == UNSUPPORTED
     assert call(f, TABLE, H=(1 << 16) + 1, ld=1 << 17, **more) == UNSUPPORTED
-    assert lib.rlk_embedding_bwd_workspace(0, 64) == 0
+    assert lib.rlk_embedding_bwd_workspace(0, 64) == lib.rlk_embedding_bwd_workspace(256, 64) == 0
     assert lib.rlk_embedding_bwd_workspace(-1, 64) == 0
 
 
