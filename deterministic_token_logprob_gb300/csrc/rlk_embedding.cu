@@ -543,11 +543,11 @@ __global__ void __launch_bounds__(GATHER_THREADS) gather_few_kernel(const Gather
       if (row_at_t[t] >= 0 && i >= 0 && i < n) met[i] = 1;
     }
     __syncthreads();
-    // tx threads a row
+    // tx threads a row, of threads / tx (1 at least) rows at a time; threads beyond them have none
     int tx = 1;
-    while (tx < threads && tx * 4 < a.H) tx *= 2;
+    while (2 * tx <= threads && tx * 4 < a.H) tx *= 2;
     const int x = tid % tx, ty = threads / tx;
-    for (int i = tid / tx; i < n; i += ty) {
+    for (int i = tid / tx; i < n && tid < tx * ty; i += ty) {
       if (met[i]) continue;
       float* row = a.dW + static_cast<int64_t>(r0 + i) * a.H;
       if constexpr (AL) {

@@ -166,6 +166,18 @@ def test_table_gradient(rlk, dtype, T, H, V, kind):
     assert torch.equal(got, rlk.embedding_bwd(dout, ids, V, scale=0.7))          # the same bits again
 
 
+@pytest.mark.parametrize("H", [1, 3, 5, 127, 129, 255, 260, 513, 520, 640, 768, 776, 1030, 1288, 1544, 1800, 2040, 2047, 2056, 2600, 4097])
+def test_table_gradient_zero_rows(rlk, H):
+    """Rows without a token, at widths that leave a CTA's threads unevenly divided over them."""
+    for T, V in ((3, 50), (3, 3000), (300, 70), (300, 3000)):
+        ids = torch.arange(T, device="cuda") * 2 % V
+        dout = torch.ones((T, H), dtype=torch.bfloat16, device="cuda")
+        buf = torch.full((V * H + 16,), 7.0, device="cuda")
+        got = rlk.embedding_bwd(dout, ids, V, out=buf[8:8 + V * H].view(V, H))
+        assert torch.equal(got, torch.bincount(ids, minlength=V).float()[:, None].expand(V, H))
+        assert bool((buf[:8] == 7.0).all()) and bool((buf[8 + V * H:] == 7.0).all())
+
+
 def test_table_gradient_ids(rlk):
     """Padding and other shards add nothing, what is no token neither (flagged); shards give the rows of the whole."""
     gen = rng(4)
