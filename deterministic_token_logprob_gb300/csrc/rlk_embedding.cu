@@ -88,8 +88,6 @@ struct SortArgs {
   int32_t n_done;
   uint4* runs;         // [T]: those of tokens of several runs from the front, the others from the back
   int32_t* n_runs;     // how many of each
-  float* dW;           // to be zeroed by the other clusters, where n_zero > 0
-  int64_t n_zero;
 };
 
 struct alignas(16) SortSmem {
@@ -315,24 +313,9 @@ __device__ __forceinline__ void list_runs(const SortArgs& a, const Entry* sorted
 template <int KEPT, bool ALL>
 __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
-  const uint32_t ctas = cluster_size();
-  if (blockIdx.x < ctas) {
-    if (blockIdx.x == 0 && threadIdx.x < 2) a.n_runs[threadIdx.x] = 0;  // the cluster's barriers stand before its first use
-    sort_tokens<KEPT, ALL>(a, *reinterpret_cast<SortSmem*>(dyn));
-    list_runs(a, a.passes & 1 ? a.a : a.b);
-    griddep_launch_dependents();
-    return;
-  }
-  // every other cluster: zeros into dW, whole vectors between its first and last boundary
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x - ctas) * SORT_THREADS + threadIdx.x;
-  const int64_t n = static_cast<int64_t>(gridDim.x - ctas) * SORT_THREADS;
-  const int64_t head = min(a.n_zero, static_cast<int64_t>((16 - (reinterpret_cast<uintptr_t>(a.dW) & 15)) & 15) / 4);
-  const int64_t vecs = (a.n_zero - head) / 4;
-  uint4* v = reinterpret_cast<uint4*>(a.dW + head);
-#pragma unroll 4
-  for (int64_t i = i0; i < vecs; i += n) v[i] = make_uint4(0, 0, 0, 0);
-  if (i0 < head) a.dW[i0] = 0.f;
-  if (i0 < a.n_zero - head - 4 * vecs) a.dW[head + 4 * vecs + i0] = 0.f;
+  if (blockIdx.x == 0 && threadIdx.x < 2) a.n_runs[threadIdx.x] = 0;  // the cluster's barriers stand before its first use
+  sort_tokens<KEPT, ALL>(a, *reinterpret_cast<SortSmem*>(dyn));
+  list_runs(a, a.passes & 1 ? a.a : a.b);
   griddep_launch_dependents();
 }
 
@@ -354,10 +337,53 @@ struct GatherArgs {
   float* part;          // [2 slots][H rounded up to 8]: sums of the runs of tokens of more than one run
   int32_t* done;        // [3 slots][slices]: runs of such a group, and groups of such a token, that are through
   int32_t slots, slices;
+  int32_t zero_per;     // rows that a CTA behind those of the runs zeroes, where dW is new (0: it is not)
   int32_t* err;
 };
 
 constexpr int GATHER_THREADS = 256;
+constexpr int ZERO_ROWS = 2048;  // zero_per at most
+
+// Zeros into the rows r0 .. r0 + n of dW that are not met, by a CTA.
+template <bool AL>
+__device__ __forceinline__ void zero_rows(const GatherArgs& a, int32_t r0, int32_t n, const uint8_t* met) {
+  const int threads = blockDim.x;
+  // tx threads a row, of threads / tx (1 at least) rows at a time; threads beyond them have none
+  int tx = 1;
+  while (2 * tx <= threads && tx * 4 < a.H) tx *= 2;
+  const int x = threadIdx.x % tx, ty = threads / tx;
+  for (int i = threadIdx.x / tx; i < n && static_cast<int>(threadIdx.x) < tx * ty; i += ty) {
+    if (met[i]) continue;
+    float* row = a.dW + static_cast<int64_t>(r0 + i) * a.H;
+    if constexpr (AL) {
+#pragma unroll 4
+      for (int c = 4 * x; c < a.H; c += 4 * tx) *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+    } else {
+#pragma unroll 4
+      for (int c = x; c < a.H; c += tx) row[c] = 0.f;
+    }
+  }
+}
+
+// The same by the sorted tokens.
+template <bool AL>
+__device__ __forceinline__ void zero_absent_rows(const GatherArgs& a, int32_t z, uint8_t* met) {
+  const int32_t r0 = z * a.zero_per, n = min(a.zero_per, a.rows - r0), lane = threadIdx.x & 31;
+  const auto row_at = [&](int32_t q) { return a.sorted[q].row; };
+  const int32_t lo = first_not_below(static_cast<uint32_t>(r0), 0, a.T, lane, row_at);
+  const int32_t hi = first_not_below(static_cast<uint32_t>(r0 + n), lo, a.T, lane, row_at);
+  for (int i = threadIdx.x; i < n; i += blockDim.x) {
+    int32_t from = lo, to = hi;  // the row's first entry is in [from, to]
+    while (from < to) {
+      const int32_t mid = (from + to) / 2;
+      if (row_at(mid) < static_cast<uint32_t>(r0 + i)) from = mid + 1;
+      else to = mid;
+    }
+    met[i] = from < hi && row_at(from) == static_cast<uint32_t>(r0 + i);
+  }
+  __syncthreads();
+  zero_rows<AL>(a, r0, n, met);
+}
 
 // s += n rows of dout, row at(i) as the i-th, in C packs of a thread 256 columns apart from column c0 on.
 template <class E, bool AL, int C, class At>
@@ -466,7 +492,12 @@ template <class E, bool AL, int C>
 __global__ void __launch_bounds__(GATHER_THREADS, 3) gather_kernel(const GatherArgs a) {
   const int lane = threadIdx.x & 31;
   const int slice = static_cast<int>(blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)), c0 = 256 * C * slice + 8 * lane;
+  __shared__ uint8_t met[ZERO_ROWS];
   griddep_wait();
+  if (static_cast<int>(blockIdx.x) >= a.T) {
+    if (blockIdx.y == 0) zero_absent_rows<AL>(a, static_cast<int32_t>(blockIdx.x) - a.T, met);
+    return;
+  }
   const int several = a.n_runs[0], runs_in_all = several + a.n_runs[1], i = static_cast<int>(blockIdx.x);
   if (i >= runs_in_all) return;
   const uint4 run = a.runs[i < several ? i : a.T - 1 - (i - several)];
@@ -523,10 +554,9 @@ __global__ void __launch_bounds__(GATHER_THREADS, 3) gather_kernel(const GatherA
 // from that. The CTAs behind those write zeros into the rows that no token points at (where dW is new). One launch: 64
 // rows of 256 into 4096 take 3 us on the GPU, with the sort 7.5. Sums in the same order as above, the same bits.
 constexpr int FEW_TOKENS = 256;
-constexpr int ZERO_ROWS = 2048;  // rows that a CTA zeroes, at most
 
 template <class E, bool AL>
-__global__ void __launch_bounds__(GATHER_THREADS) gather_few_kernel(const GatherArgs a, int32_t blocks, int32_t per) {
+__global__ void __launch_bounds__(GATHER_THREADS) gather_few_kernel(const GatherArgs a, int32_t blocks) {
   __shared__ int32_t row_at_t[FEW_TOKENS];
   __shared__ uint32_t list[FEW_TOKENS];
   __shared__ int32_t found;  // positions of the token, 0: this is not its first
@@ -535,7 +565,7 @@ __global__ void __launch_bounds__(GATHER_THREADS) gather_few_kernel(const Gather
   for (int t = tid; t < a.T; t += threads) row_at_t[t] = a.shard.row_of(a.ids[t]);
   const int32_t z = static_cast<int32_t>(blockIdx.x) - a.T * blocks;
   if (z >= 0) {
-    const int32_t r0 = z * per, n = min(per, a.rows - r0);
+    const int32_t r0 = z * a.zero_per, n = min(a.zero_per, a.rows - r0);
     for (int i = tid; i < n; i += threads) met[i] = 0;
     __syncthreads();
     for (int t = tid; t < a.T; t += threads) {
@@ -543,19 +573,7 @@ __global__ void __launch_bounds__(GATHER_THREADS) gather_few_kernel(const Gather
       if (row_at_t[t] >= 0 && i >= 0 && i < n) met[i] = 1;
     }
     __syncthreads();
-    // tx threads a row, of threads / tx (1 at least) rows at a time; threads beyond them have none
-    int tx = 1;
-    while (2 * tx <= threads && tx * 4 < a.H) tx *= 2;
-    const int x = tid % tx, ty = threads / tx;
-    for (int i = tid / tx; i < n && tid < tx * ty; i += ty) {
-      if (met[i]) continue;
-      float* row = a.dW + static_cast<int64_t>(r0 + i) * a.H;
-      if constexpr (AL) {
-        for (int c = 4 * x; c < a.H; c += 4 * tx) *reinterpret_cast<float4*>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-      } else {
-        for (int c = x; c < a.H; c += tx) row[c] = 0.f;
-      }
-    }
+    zero_rows<AL>(a, r0, n, met);
     return;
   }
   __syncthreads();
@@ -613,7 +631,7 @@ inline Room room_of(int64_t T, int64_t H) {
 }
 
 template <int KEPT, bool ALL>
-inline rlk_status launch_sort(const SortArgs& q, int ctas, int64_t zero, cudaStream_t s) {
+inline rlk_status launch_sort(const SortArgs& q, int ctas, cudaStream_t s) {
   static OncePerDevice allowed;
   const auto kernel = sort_tokens_kernel<KEPT, ALL>;
   if (!allowed([&] {
@@ -622,7 +640,7 @@ inline rlk_status launch_sort(const SortArgs& q, int ctas, int64_t zero, cudaStr
       }))
     return RLK_ERR_CUDA;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas + zero));
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(SORT_THREADS);
   cfg.dynamicSmemBytes = sizeof(SortSmem);
   cfg.stream = s;
@@ -698,16 +716,19 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
   const bool al = whole_packs(dout, T, H, ld, in.eb) && on_boundary(dW, 16);
   const Shard shard{vocab_start, V_local, V_true, err_flag};
   GatherArgs g{nullptr, nullptr, nullptr, ids, shard, dout, dW, ld, static_cast<int32_t>(T), static_cast<int32_t>(H),
-               static_cast<int32_t>(V_local), static_cast<float>(scale), accumulate != 0, nullptr, nullptr, r.slots, 0, err_flag};
+               static_cast<int32_t>(V_local), static_cast<float>(scale), accumulate != 0, nullptr, nullptr, r.slots, 0, 0, err_flag};
+  // the CTAs that write zeros: eight an SM at least, of half a megabyte at most (151936 rows of 4096, 8192 tokens: 366 us;
+  // eight an SM of 2 MB each 378, four of 4 MB 434; 4096 rows of 256, 64 tokens: 3.3 us, with four times the CTAs 4.6)
+  const int64_t share = std::min<int64_t>((V_local + 1215) / 1216, std::max<int64_t>(1, 131072 / H));
+  g.zero_per = accumulate ? 0 : static_cast<int32_t>(std::min<int64_t>(ZERO_ROWS, share));
+  const int64_t zero = accumulate ? 0 : (V_local + g.zero_per - 1) / g.zero_per;
   if (T <= FEW_TOKENS) {
     const int threads = static_cast<int>(H >= 8 * GATHER_THREADS ? GATHER_THREADS : (H + 255) / 256 * 32);
     const int32_t blocks = static_cast<int32_t>((H + 8 * threads - 1) / (8 * threads));
-    // the CTAs that write zeros: eight an SM, or as many as their share of the rows asks for
-    const int32_t per = static_cast<int32_t>(std::min<int64_t>(ZERO_ROWS, (V_local + 1215) / 1216));
-    const int64_t ctas = T * blocks + (accumulate ? 0 : (V_local + per - 1) / per);
+    const int64_t ctas = T * blocks + zero;
     return with_type(dtype, [&](auto e) {
       const auto kernel = al ? gather_few_kernel<decltype(e), true> : gather_few_kernel<decltype(e), false>;
-      kernel<<<static_cast<unsigned>(ctas), threads, 0, s>>>(g, blocks, per);
+      kernel<<<static_cast<unsigned>(ctas), threads, 0, s>>>(g, blocks);
       return launched();
     });
   }
@@ -719,17 +740,14 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
   auto* runs = reinterpret_cast<uint4*>(ws + r.runs);
   auto* n_runs = reinterpret_cast<int32_t*>(runs + T);
   SortArgs q{ids, reinterpret_cast<Entry*>(ws + r.a), reinterpret_cast<Entry*>(ws + r.b), static_cast<int32_t>(T), 0, 0, shard,
-             reinterpret_cast<int32_t*>(ws + r.done), 3 * r.slots * g.slices, runs, n_runs, dW, accumulate ? 0 : V_local * H};
+             reinterpret_cast<int32_t*>(ws + r.done), 3 * r.slots * g.slices, runs, n_runs};
   while (V_local >> q.bits) ++q.bits;  // rows and the mark behind them: 0 .. V_local
   q.passes = (q.bits + 8) / 9;
-  // one cluster sorts, two positions a thread while it can; the others (if any) zero dW: 304 CTAs, two an SM
-  int ctas = 1;
+  int ctas = 1;  // two positions a thread while there are CTAs
   while (ctas < SORT_CTAS && T > 2 * SORT_THREADS * ctas) ctas *= 2;
-  int64_t zero = accumulate ? 0 : std::min<int64_t>(304, (V_local * H + 64 * SORT_THREADS - 1) / (64 * SORT_THREADS));
-  zero = (zero + ctas - 1) / ctas * ctas;
   const int64_t groups = (T + SORT_THREADS * ctas - 1) / (SORT_THREADS * ctas);
-  st = groups <= 2 ? launch_sort<2, true>(q, ctas, zero, s)
-                   : groups <= 8 ? launch_sort<8, true>(q, ctas, zero, s) : launch_sort<8, false>(q, ctas, zero, s);
+  st = groups <= 2 ? launch_sort<2, true>(q, ctas, s)
+                   : groups <= 8 ? launch_sort<8, true>(q, ctas, s) : launch_sort<8, false>(q, ctas, s);
   if (st != RLK_OK) return st;
   g.sorted = q.passes & 1 ? q.a : q.b;
   g.runs = runs;
@@ -740,7 +758,7 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
     using E = decltype(e);
     const auto kernel = packs == 1 ? (al ? gather_kernel<E, true, 1> : gather_kernel<E, false, 1>)
                                    : (al ? gather_kernel<E, true, 2> : gather_kernel<E, false, 2>);
-    return launch_after(kernel, dim3(static_cast<unsigned>(T), blocks), 32 * warps, s, g);
+    return launch_after(kernel, dim3(static_cast<unsigned>(T + zero), blocks), 32 * warps, s, g);
   });
 }
 
