@@ -2,9 +2,11 @@
 //
 //   norm = sqrt(sum over tensors and elements of g^2),   out = g min(1, max_norm / norm)
 //
-// The tensors are cut into chunks of 16 KB; the chunks, in order, are dealt to 608 shares of equal
-// length, and a CTA takes a share. What a share adds up, and in what order, follows from the tensors' sizes
-// and types alone, and so does the order of the 608 sums: the norm has the same bits wherever the tensors lie.
+// The tensors are cut into chunks of 16 KB, which are dealt in turn to 608 shares, a CTA each. What a share adds up, and in
+// what order, follows from the tensors' sizes and types alone, and so does the order of the 608 sums: the norm has the same
+// bits wherever the tensors lie. The sum reads 2.5 GB of fp32 in 335 us (7.4 TB/s). Scaling reads and writes: there CTAs that
+// stay and take chunk after chunk are slower (920 us) than a CTA a chunk (683 us, 7.3 TB/s), which then needs the factor ready; for few
+// chunks, where the launch between would cost more, every CTA folds the shares itself.
 #include <algorithm>
 #include <new>
 
@@ -14,8 +16,10 @@ namespace rlk {
 namespace {
 
 constexpr int CLIP_THREADS = 256;
-constexpr int SHARES = 608;          // four CTAs on each of 152 SMs
+constexpr int CTAS = 4;              // on each SM
+constexpr int SHARES = 152 * CTAS;
 constexpr int CHUNK_BYTES = 16384;   // 64 bytes a thread: two packs of fp32, four of 16-bit types
+constexpr int MANY_CHUNKS = 8 * SHARES;  // beyond, a CTA scales one chunk (80 MB; the launch between costs 2 us)
 constexpr int BATCH = 512;           // tensors of one launch: their table is a kernel parameter (16 KB)
 constexpr int FEW = 32;              // a smaller table, for the calls that are bound by the host
 
@@ -27,51 +31,74 @@ struct Piece {
   int16_t dtype, out_dtype;
 };
 
+// Sums of squares at three scales (Blue's sums): what would overflow or vanish in fp32 is squared as x 2^-80 or x 2^80. All in
+// fp32: this GPU adds two doubles an SM and cycle, and a fold of the shares in doubles by every CTA took 7 us.
+struct alignas(16) Squares {
+  float mid = 0.f, big = 0.f, small = 0.f, none = 0.f;
+};
 template <int N>
 struct ClipArgs {
   Piece piece[N];
   int32_t n;
   uint32_t chunks;
-  double* sums;         // [launches][SHARES], this launch's first
+  Squares* sums;        // [launches][SHARES], this launch's first
   int32_t* err;
 };
 
-__host__ __device__ constexpr int chunk_elements(int eb) { return CHUNK_BYTES / eb; }
+constexpr float kShrunk = 8.271806125530277e-25f;  // 2^-80
+constexpr float kGrown = 1.2089258196146292e24f;   // 2^80
 
-// Sums of squares at three scales (Blue's sums): what would overflow or vanish in fp32 is squared as x 2^-80 or x 2^80.
-struct Squares {
-  float mid = 0.f, big = 0.f, small = 0.f;
+template <class E>
+constexpr int CHUNK = CHUNK_BYTES / static_cast<int>(sizeof(typename E::bits));  // elements
+template <class E>
+constexpr int PACKS = CHUNK<E> / (8 * CLIP_THREADS);                             // of a thread
+
+// The sum of squares of a thread's packs of a chunk, get(j) the j-th of them, at the scale that holds it.
+template <class E, int UNROLL, class Get>
+__device__ __forceinline__ void add_squares(Squares& s, const Get& get) {
+  const auto at = [&](float f) {
+    F32x2 a = 0;
+#pragma unroll(UNROLL)
+    for (int j = 0; j < PACKS<E>; ++j) {
+      F32x2 v[4];
+      unpack(get(j), v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(f));  // a power of two
+      a = dot4(v, v, a);
+    }
+    return low_plus_high(a);
+  };
+  const float q = at(1.f);
+  if (q >= 8.077935669463161e-28f && q <= 1.2089258196146292e24f) {  // 2^-90 .. 2^80: 2^39 of them stay in fp32
+    s.mid = __fadd_rn(s.mid, q);
+    return;
+  }
+  const bool tiny = q < 1.f;  // else too large, NaN or infinite
+  const float r = at(tiny ? kGrown : kShrunk);
+  if (tiny) s.small = __fadd_rn(s.small, r);
+  else s.big = __fadd_rn(s.big, r);
+}
+
+// The sum of a value and what its rounding has lost (two-sum), and of two such.
+struct Exact {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float v) {
+    const float t = __fadd_rn(hi, v), b = __fsub_rn(t, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(v, b)));
+    hi = t;
+  }
 };
-constexpr float kTiny = 8.271806125530277e-25f;  // 2^-80
-constexpr float kHuge = 1.2089258196146292e24f;  // 2^80
 
-template <class E>
-__device__ __forceinline__ float squares(const Pack<E>& k, float f) {
-  F32x2 v[4];
-  unpack(k, v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(f));  // a power of two
-  return low_plus_high(dot4(v, v, 0));
-}
-
-template <class E>
-__device__ __forceinline__ void add_squares(const Pack<E>& k, Squares& s) {
-  const float q = squares(k, 1.f);
-  if (q >= 8.077935669463161e-28f && q <= 1.2676506002282294e30f) s.mid = __fadd_rn(s.mid, q);  // 2^-90 .. 2^100
-  else if (q < 1.f) s.small = __fadd_rn(s.small, squares(k, kHuge));
-  else s.big = __fadd_rn(s.big, squares(k, kTiny));  // NaN and infinities too
-}
-
-// The sum over the CTA's threads, in one order; valid in every thread.
-__device__ __forceinline__ double block_sum(double v, double* room) {
-#pragma unroll
-  for (int d = 16; d >= 1; d >>= 1) v = __dadd_rn(v, __shfl_xor_sync(kFullWarp, v, d));
+// The sum over the CTA's threads, in one order; every thread gets it. room: 8 floats each.
+__device__ __forceinline__ float block_sum(float v, float* room) {
+  v = warp_sum(v);
+  __syncthreads();
   if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = room[0];
+  float x[8];
 #pragma unroll
-  for (int w = 1; w < CLIP_THREADS / 32; ++w) v = __dadd_rn(v, room[w]);
-  return v;
+  for (int i = 0; i < 8; ++i) x[i] = room[i];
+  return __fadd_rn(__fadd_rn(__fadd_rn(x[0], x[1]), __fadd_rn(x[2], x[3])), __fadd_rn(__fadd_rn(x[4], x[5]), __fadd_rn(x[6], x[7])));
 }
 
 template <int N>
@@ -85,117 +112,175 @@ __device__ __forceinline__ int piece_of(const ClipArgs<N>& a, uint32_t chunk) {
   return lo;
 }
 
-__device__ __forceinline__ uint32_t share_start(uint32_t chunks, int share) {
-  return static_cast<uint32_t>(static_cast<uint64_t>(chunks) * share / SHARES);
-}
-
+// Chunks lo, lo + SHARES, ... below hi of a tensor. A misaligned one's packs are cut from their neighbours' vectors, so that every thread owns the
+// elements that it owns of an aligned one.
 template <class E>
-__device__ __forceinline__ void add_chunk(const Piece& p, uint32_t chunk, Squares& s, int32_t* err) {
-  constexpr int CE = chunk_elements(sizeof(typename E::bits));
-  const int64_t at = static_cast<int64_t>(chunk) * CE;
-  const int n = static_cast<int>(min(static_cast<int64_t>(CE), p.n - at));
-  const auto* row = static_cast<const typename E::bits*>(p.in) + at;
+__device__ __noinline__ Squares sum_chunks(const Piece p, uint32_t lo, uint32_t hi, Squares s, int32_t* err) {
+  const int tid = static_cast<int>(threadIdx.x);
+  const auto* in = static_cast<const typename E::bits*>(p.in) + static_cast<int64_t>(lo) * CHUNK<E>;
+  int64_t left = p.n - static_cast<int64_t>(lo) * CHUNK<E>;
+  const bool aligned = (reinterpret_cast<uintptr_t>(p.in) & 15) == 0;
+#pragma unroll 1
+  for (uint32_t c = lo; c < hi; c += SHARES) {
+    if (aligned && left >= CHUNK<E>) {
+      Pack<E> k[PACKS<E>];
 #pragma unroll
-  for (int j = 0; j < CE / (8 * CLIP_THREADS); ++j) {
-    const int c = 8 * (j * CLIP_THREADS + static_cast<int>(threadIdx.x));
-    if (c < n) add_squares<E>(load_columns<E, false>(row, c, n, err), s);
+      for (int j = 0; j < PACKS<E>; ++j) k[j] = load_columns<E, true>(in + 8 * tid, 8 * j * CLIP_THREADS, CHUNK<E> - 8 * tid, err);
+      add_squares<E, PACKS<E>>(s, [&](int j) { return k[j]; });
+    } else {
+      const int n = static_cast<int>(min(static_cast<int64_t>(CHUNK<E>), left));
+      add_squares<E, 1>(s, [&](int j) {
+        const int at = 8 * (j * CLIP_THREADS + tid);
+        return at < n ? load_columns<E, false>(in, at, n, err) : Pack<E>{};
+      });
+    }
+    in += static_cast<int64_t>(SHARES) * CHUNK<E>;
+    left -= static_cast<int64_t>(SHARES) * CHUNK<E>;
   }
+  return s;
 }
 
 template <int N>
-__global__ void __launch_bounds__(CLIP_THREADS) sum_squares_kernel(const __grid_constant__ ClipArgs<N> a) {
-  __shared__ double room[CLIP_THREADS / 32];
-  uint32_t c = share_start(a.chunks, blockIdx.x);
-  const uint32_t end = share_start(a.chunks, blockIdx.x + 1);
+__global__ void __launch_bounds__(CLIP_THREADS, CTAS) sum_squares_kernel(const __grid_constant__ ClipArgs<N> a) {
+  __shared__ float room[CLIP_THREADS / 32];
   Squares s;
-  if (c < end) {
-    for (int i = piece_of(a, c); c < end; ++i) {
-      const Piece& p = a.piece[i];
-      const uint32_t stop = i + 1 < a.n ? min(end, a.piece[i + 1].chunk0) : end;
-      for (; c < stop; ++c) {
-        if (p.dtype == RLK_DTYPE_F32) add_chunk<F32>(p, c - p.chunk0, s, a.err);
-        else if (p.dtype == RLK_DTYPE_BF16) add_chunk<Bf16>(p, c - p.chunk0, s, a.err);
-        else add_chunk<F16>(p, c - p.chunk0, s, a.err);
-      }
-    }
+  for (uint32_t c = blockIdx.x; c < a.chunks;) {
+    const int i = piece_of(a, c);
+    const Piece& p = a.piece[i];
+    const uint32_t end = i + 1 < a.n ? a.piece[i + 1].chunk0 : a.chunks, lo = c - p.chunk0, hi = end - p.chunk0;
+    if (p.dtype == RLK_DTYPE_F32) s = sum_chunks<F32>(p, lo, hi, s, a.err);
+    else if (p.dtype == RLK_DTYPE_BF16) s = sum_chunks<Bf16>(p, lo, hi, s, a.err);
+    else s = sum_chunks<F16>(p, lo, hi, s, a.err);
+    c += (end - c + SHARES - 1) / SHARES * SHARES;
   }
-  // 2^160 and 2^-160 undo the scales
-  double d = __dadd_rn(static_cast<double>(s.mid), __dmul_rn(static_cast<double>(s.small), 6.842277657836021e-49));
-  d = __dadd_rn(d, __dmul_rn(static_cast<double>(s.big), 1.461501637330903e48));
-  d = block_sum(d, room);
-  if (threadIdx.x == 0) a.sums[blockIdx.x] = d;
-}
-
-// The norm from the shares' sums, by one CTA; the same bits in each.
-__device__ __forceinline__ double norm_of(const double* sums, int n, double* room) {
-  double d = 0.;
-  for (int i = threadIdx.x; i < n; i += CLIP_THREADS) d = __dadd_rn(d, sums[i]);
-  return __dsqrt_rn(block_sum(d, room));
-}
-
-__global__ void __launch_bounds__(CLIP_THREADS) norm_kernel(const double* sums, int n, float* norm, int32_t* err) {
-  __shared__ double room[CLIP_THREADS / 32];
-  const float v = static_cast<float>(norm_of(sums, n, room));
-  if (threadIdx.x != 0) return;
-  *norm = v;
-  if (!isfinite(v) && err) atomicOr(err, RLK_FLAG_NONFINITE);
-}
-
-template <class E, class O>
-__device__ __forceinline__ void scale_chunk(const Piece& p, uint32_t chunk, float f, int32_t* err) {
-  constexpr int CE = chunk_elements(sizeof(typename E::bits));
-  const int64_t at = static_cast<int64_t>(chunk) * CE;
-  const int n = static_cast<int>(min(static_cast<int64_t>(CE), p.n - at));
-  const auto* row = static_cast<const typename E::bits*>(p.in) + at;
-  auto* out = static_cast<typename O::bits*>(p.out) + at;
-  const bool al = (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-#pragma unroll
-  for (int j = 0; j < CE / (8 * CLIP_THREADS); ++j) {
-    const int c = 8 * (j * CLIP_THREADS + static_cast<int>(threadIdx.x));
-    if (c >= n) break;
-    F32x2 v[4];
-    unpack(load_columns<E, false>(row, c, n, err), v);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = f == 1.f ? v[i] : mul2(v[i], both(f));  // a NaN's bits survive a copy
-    if (al && c + 8 <= n) store_columns<O, true>(out, c, n, v, err);
-    else store_columns<O, false>(out, c, n, v, err);
+  griddep_launch_dependents();
+  Squares all;
+  const bool odd = __syncthreads_or(s.big != 0.f || s.small != 0.f);  // NaN counts
+  all.mid = block_sum(s.mid, room);
+  if (odd) {
+    all.big = block_sum(s.big, room);
+    all.small = block_sum(s.small, room);
   }
+  if (threadIdx.x == 0) a.sums[blockIdx.x] = all;
+}
+
+// The norm from the shares' sums, by one CTA; the same bits in each, and in every thread.
+__device__ __forceinline__ float norm_of(const Squares* sums, int n, float* room) {
+  Exact mid, big, small;
+  for (int i = threadIdx.x; i < n; i += CLIP_THREADS) {
+    const float4 v = __ldcg(reinterpret_cast<const float4*>(sums + i));
+    mid.add(v.x);
+    if (v.y != 0.f) big.add(v.y);
+    if (v.z != 0.f) small.add(v.z);
+  }
+  const bool odd = __syncthreads_or(big.hi != 0.f || small.hi != 0.f);
+  float m = block_sum(__fadd_rn(mid.hi, mid.lo), room), b = 0.f, s = 0.f;
+  if (odd) {
+    b = block_sum(__fadd_rn(big.hi, big.lo), room);
+    s = block_sum(__fadd_rn(small.hi, small.lo), room);
+  }
+  // each scale against the next larger one in which there is something
+  const auto down = [](float v) { return __fmul_rn(__fmul_rn(v, kShrunk), kShrunk); };
+  if (b != 0.f) return __fmul_rn(__fsqrt_rn(__fadd_rn(b, down(m))), kGrown);
+  if (m != 0.f) return __fsqrt_rn(__fadd_rn(m, down(s)));
+  return __fmul_rn(__fsqrt_rn(s), kShrunk);
 }
 
 struct ClipNorm {
-  const double* sums;
+  const Squares* sums;
   int32_t n;
-  double max_norm;
+  float max_norm;
   float* norm;
+  float* factor;        // null: not wanted, or (in scaling) not known yet
+  int32_t* err;
 };
 
-// A norm beyond fp32, or none, leaves the gradients as they are.
-template <int N>
-__global__ void __launch_bounds__(CLIP_THREADS) scale_kernel(const __grid_constant__ ClipArgs<N> a, const ClipNorm q) {
-  __shared__ double room[CLIP_THREADS / 32];
-  const double norm = norm_of(q.sums, q.n, room);
-  const float v = static_cast<float>(norm);
-  if (blockIdx.x == 0 && threadIdx.x == 0 && q.norm) {
+// The norm and the factor, by a CTA that writes them or by one that wants the factor alone. A norm beyond fp32, or none, leaves
+// the gradients as they are.
+__device__ __forceinline__ float find_norm(const ClipNorm& q, bool write, float* room) {
+  const float v = norm_of(q.sums, q.n, room);
+  if (write && threadIdx.x == 0) {
     *q.norm = v;
-    if (!isfinite(v) && a.err) atomicOr(a.err, RLK_FLAG_NONFINITE);
+    if (!isfinite(v) && q.err) atomicOr(q.err, RLK_FLAG_NONFINITE);
   }
-  const float f = isfinite(v) && norm > q.max_norm ? static_cast<float>(__ddiv_rn(q.max_norm, norm)) : 1.f;
-  uint32_t c = share_start(a.chunks, blockIdx.x);
-  const uint32_t end = share_start(a.chunks, blockIdx.x + 1);
-  if (c >= end) return;
-  for (int i = piece_of(a, c); c < end; ++i) {
-    const Piece& p = a.piece[i];
-    const uint32_t stop = i + 1 < a.n ? min(end, a.piece[i + 1].chunk0) : end;
-    if (f == 1.f && p.in == p.out && p.dtype == p.out_dtype) {
-      c = max(c, stop);
-      continue;
+  return isfinite(v) && v > q.max_norm ? __fdiv_rn(q.max_norm, v) : 1.f;
+}
+
+__global__ void __launch_bounds__(CLIP_THREADS) norm_kernel(const ClipNorm q) {
+  __shared__ float room[CLIP_THREADS / 32];
+  griddep_wait();
+  const float f = find_norm(q, true, room);
+  griddep_launch_dependents();
+  if (q.factor && threadIdx.x == 0) *q.factor = f;
+}
+
+// Chunks c, c - step, ... down to 0 of a tensor, times f; the last ones first, since L2 holds them from the sum. A thread owns packs that
+// are aligned in the output; where the gradient lies alike (in place above all) it reads what it writes and no more.
+template <class E, class O>
+__device__ __noinline__ void scale_chunks(const Piece p, uint32_t c, uint32_t step, float f, int32_t* err) {
+  const int tid = static_cast<int>(threadIdx.x);
+  const auto* in0 = static_cast<const typename E::bits*>(p.in);
+  auto* out0 = static_cast<typename O::bits*>(p.out);
+  const int head0 = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(out0) & 15)) & 15) / static_cast<int>(sizeof(*out0));
+  const bool plain = f == 1.f;  // a NaN's bits survive a copy
+  const auto put = [&](const Pack<E>& k, typename O::bits* out, int c, int n) {
+    F32x2 v[4];
+    unpack(k, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = plain ? v[i] : mul2(v[i], both(f));
+    store_columns<O, true>(out, c, n, v, err);
+  };
+  const bool alike = ((reinterpret_cast<uintptr_t>(in0) + head0 * sizeof(*in0)) & 15) == 0;
+#pragma unroll 1
+  for (;; c -= step) {
+    const int64_t at = static_cast<int64_t>(c) * CHUNK<E>;
+    const int n = static_cast<int>(min(static_cast<int64_t>(CHUNK<E>), p.n - at)), head = min(head0, n), packs = (n - head) / 8;
+    const auto* in = in0 + at + head;
+    auto* out = out0 + at + head;
+    if (tid < 16) {  // the elements outside the packs
+      const int i = tid < 8 ? tid - head : 8 * packs + tid - 8;
+      if ((tid < 8 ? i < 0 : i < n - head) && dbg_ok(i >= -head && i < n - head, err)) {
+        const float v = E::to_f32(in[i]);
+        out[i] = O::from_f32(plain ? v : __fmul_rn(v, f));
+      }
     }
-    for (; c < stop; ++c) {
-      if (p.dtype == RLK_DTYPE_BF16) scale_chunk<Bf16, Bf16>(p, c - p.chunk0, f, a.err);
-      else if (p.dtype == RLK_DTYPE_F16) scale_chunk<F16, F16>(p, c - p.chunk0, f, a.err);
-      else if (p.out_dtype == RLK_DTYPE_F32) scale_chunk<F32, F32>(p, c - p.chunk0, f, a.err);
-      else scale_chunk<F32, Bf16>(p, c - p.chunk0, f, a.err);
+    if (alike && packs >= PACKS<E> * CLIP_THREADS - 1) {  // a whole chunk: all packs, or all but one where there is a head
+      const bool last = (PACKS<E> - 1) * CLIP_THREADS + tid < packs;
+      Pack<E> k[PACKS<E>];
+#pragma unroll
+      for (int j = 0; j < PACKS<E>; ++j)
+        if (j < PACKS<E> - 1 || last) k[j] = load_columns<E, true>(in + 8 * tid, 8 * j * CLIP_THREADS, n - head - 8 * tid, err);
+#pragma unroll
+      for (int j = 0; j < PACKS<E>; ++j)
+        if (j < PACKS<E> - 1 || last) put(k[j], out + 8 * tid, 8 * j * CLIP_THREADS, n - head - 8 * tid);
+    } else {
+#pragma unroll 1
+      for (int q = tid; q < packs; q += CLIP_THREADS)
+        put(alike ? load_columns<E, true>(in, 8 * q, n - head, err) : load_columns<E, false>(in, 8 * q, n - head, err), out, 8 * q,
+            n - head);
     }
+    if (c < step) return;
+  }
+}
+
+template <int N>
+__global__ void __launch_bounds__(CLIP_THREADS, CTAS) scale_kernel(const __grid_constant__ ClipArgs<N> a, const ClipNorm q) {
+  __shared__ float room[CLIP_THREADS / 32];
+  griddep_wait();
+  const float f = q.factor ? *q.factor : find_norm(q, blockIdx.x == 0 && q.norm, room);
+  if (blockIdx.x >= a.chunks) return;
+  for (uint32_t c = a.chunks - 1 - blockIdx.x;;) {  // the last ones first
+    const Piece& p = a.piece[piece_of(a, c)];
+    const uint32_t at = c - p.chunk0;
+    if (!(f == 1.f && p.in == p.out && p.dtype == p.out_dtype)) {
+      if (p.dtype == RLK_DTYPE_BF16) scale_chunks<Bf16, Bf16>(p, at, gridDim.x, f, a.err);
+      else if (p.dtype == RLK_DTYPE_F16) scale_chunks<F16, F16>(p, at, gridDim.x, f, a.err);
+      else if (p.out_dtype == RLK_DTYPE_F32) scale_chunks<F32, F32>(p, at, gridDim.x, f, a.err);
+      else scale_chunks<F32, Bf16>(p, at, gridDim.x, f, a.err);
+    }
+    const uint32_t back = at / gridDim.x * gridDim.x + gridDim.x;  // past the tensor's first chunk of this CTA
+    if (c < back) return;
+    c -= back;
   }
 }
 
@@ -209,7 +294,7 @@ struct Tensors {
 };
 
 inline int64_t chunks_of(int64_t n, int32_t dtype) {
-  const int64_t each = chunk_elements(dtype_bytes(dtype));
+  const int64_t each = CHUNK_BYTES / dtype_bytes(dtype);
   return (n + each - 1) / each;
 }
 
@@ -259,7 +344,7 @@ inline int32_t launches_of(int32_t n) { return n <= FEW ? 1 : (n + BATCH - 1) / 
 
 // Calls f with the table of each launch.
 template <int N, class F>
-inline rlk_status each_batch(const Tensors& t, double* sums, int32_t* err, F f) {
+inline rlk_status each_batch(const Tensors& t, Squares* sums, int32_t* err, F f) {
   for (int32_t first = 0, k = 0; first == 0 || first < t.n; first += N, ++k) {
     ClipArgs<N> a;
     a.n = std::min(N, t.n - first);
@@ -279,19 +364,27 @@ inline rlk_status each_batch(const Tensors& t, double* sums, int32_t* err, F f) 
 }
 
 template <int N>
-inline rlk_status run_clip(const Tensors& t, double max_norm, float* norm, int32_t* err, double* sums, cudaStream_t s) {
+inline rlk_status run_clip(const Tensors& t, double max_norm, float* norm, int32_t* err, Squares* sums, cudaStream_t s) {
   rlk_status st = each_batch<N>(t, sums, err, [&](const ClipArgs<N>& a, int32_t) {
     sum_squares_kernel<N><<<SHARES, CLIP_THREADS, 0, s>>>(a);
     return launched();
   });
   if (st != RLK_OK) return st;
   const int32_t n = launches_of(t.n) * SHARES;
-  if (!t.out) {
-    norm_kernel<<<1, CLIP_THREADS, 0, s>>>(sums, n, norm, err);
-    return launched();
+  ClipNorm q{sums, n, static_cast<float>(max_norm), norm, nullptr, err};
+  if (!t.out) return launch_after(norm_kernel, dim3(1), CLIP_THREADS, s, q);
+  int64_t chunks = 0;
+  for (int32_t i = 0; i < t.n; ++i) chunks += chunks_of(t.sizes[i], t.dtypes[i]);
+  const bool many = chunks > MANY_CHUNKS || launches_of(t.n) > 1;
+  if (many) {
+    q.factor = reinterpret_cast<float*>(sums + n);
+    st = launch_after(norm_kernel, dim3(1), CLIP_THREADS, s, q);
+    if (st != RLK_OK) return st;
   }
   return each_batch<N>(t, sums, err, [&](const ClipArgs<N>& a, int32_t k) {
-    scale_kernel<N><<<SHARES, CLIP_THREADS, 0, s>>>(a, ClipNorm{sums, n, max_norm, k == 0 ? norm : nullptr});
+    const dim3 grid(many ? std::max(a.chunks, 1u) : static_cast<unsigned>(SHARES));
+    if (k == 0) return launch_after(scale_kernel<N>, grid, CLIP_THREADS, s, a, q);
+    scale_kernel<N><<<grid, CLIP_THREADS, 0, s>>>(a, q);
     return launched();
   });
 }
@@ -302,7 +395,7 @@ inline rlk_status clip(const Tensors& t, double max_norm, float* norm, int32_t* 
   if (st != RLK_OK) return st;
   if (!norm || !on_boundary(norm, 4)) return RLK_ERR_INVALID_ARG;
   if (!workspace || !on_boundary(workspace, 256) || bytes < rlk_grad_norm_workspace(t.n)) return RLK_ERR_WORKSPACE;
-  double* sums = static_cast<double*>(workspace);
+  auto* sums = static_cast<Squares*>(workspace);
   const auto s = static_cast<cudaStream_t>(stream);
   return t.n <= FEW ? run_clip<FEW>(t, max_norm, norm, err, sums, s) : run_clip<BATCH>(t, max_norm, norm, err, sums, s);
 }
@@ -314,7 +407,7 @@ using namespace rlk;
 
 extern "C" {
 
-size_t rlk_grad_norm_workspace(int32_t n) { return n < 0 ? 0 : static_cast<size_t>(launches_of(n)) * SHARES * sizeof(double); }
+size_t rlk_grad_norm_workspace(int32_t n) { return n < 0 ? 0 : (static_cast<size_t>(launches_of(n)) * SHARES + 1) * sizeof(Squares); }
 
 rlk_status rlk_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int32_t n, float* norm,
                          int32_t* err_flag, void* workspace, size_t workspace_bytes, void* stream) {

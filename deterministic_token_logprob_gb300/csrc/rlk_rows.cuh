@@ -25,12 +25,9 @@ struct Is {
   static constexpr bool value = V;
 };
 
-// 8 columns of a row of n, from column c0 (a multiple of 8) on; 0 beyond the row. AL: the row starts on
-// a 16-byte boundary and n is a multiple of 8.
-template <class E, bool AL>
-__device__ __forceinline__ Pack<E> load_columns(const typename E::bits* row, int c0, int n, int32_t* err) {
-  const Row<E, AL> r(row, n, err);
-  if (AL || packs_inside(r, c0, c0 + 8)) return load_pack(r, c0);
+// A pack at a row's end or before its first boundary, element by element; 0 beyond the row.
+template <class E>
+__device__ __noinline__ Pack<E> load_edge(const typename E::bits* row, int c0, int n) {
   Pack<E> k{};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -39,6 +36,15 @@ __device__ __forceinline__ Pack<E> load_columns(const typename E::bits* row, int
     else k.w[i / 2] |= b << (i & 1 ? 16 : 0);
   }
   return k;
+}
+
+// 8 columns of a row of n, from column c0 (a multiple of 8) on; 0 beyond the row. AL: the row starts on
+// a 16-byte boundary and n is a multiple of 8.
+template <class E, bool AL>
+__device__ __forceinline__ Pack<E> load_columns(const typename E::bits* row, int c0, int n, int32_t* err) {
+  const Row<E, AL> r(row, n, err);
+  if (AL || packs_inside(r, c0, c0 + 8)) return load_pack(r, c0);
+  return load_edge<E>(row, c0, n);
 }
 
 // The four pairs of a pack in fp32.

@@ -241,15 +241,18 @@ _contiguous, _dtype_of = torch.Tensor.is_contiguous, attrgetter("dtype")
 
 def _listed(tensors, name: str, dev: int):
     """Addresses and dtype codes of dense CUDA tensors of one device, as arrays."""
-    if set(map(_device_of, tensors)) != {dev}:
+    if not tensors or set(map(_device_of, tensors)) != {dev}:
         raise ValueError(f"{name} must all be CUDA tensors of one device")
     if not all(map(_contiguous, tensors)):
         raise ValueError(f"{name} must be contiguous")
     dtypes = list(map(_dtype_of, tensors))
-    try:
+    for d in set(dtypes):
+        if d not in _DTYPES:
+            raise TypeError(f"{name} must be of {[str(d) for d in _DTYPES]}, got {d}")
+    if dtypes.count(dtypes[0]) == len(dtypes):
+        codes = array.array("i", [_DTYPES[dtypes[0]]]) * len(dtypes)
+    else:
         codes = array.array("i", map(_DTYPES.__getitem__, dtypes))
-    except KeyError as e:
-        raise TypeError(f"{name} must be of {[str(d) for d in _DTYPES]}, got {e.args[0]}") from None
     return array.array("Q", map(_data_ptr, tensors)), codes
 
 
@@ -312,7 +315,7 @@ def clip_grad_norm(grads: Union[torch.Tensor, Sequence[torch.Tensor]], max_norm:
                    norm: Optional[torch.Tensor] = None, err_flag: Optional[torch.Tensor] = None,
                    workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """rlk_clip_grad_norm -> the norm over all gradients, as :func:`grad_norm`, and the gradients times max_norm / norm
-    where that is below 1: in place, or into `out`, tensors of the same shapes (and types, or bfloat16 for
+    where that is below 1: in place, or into `out`, tensors of the same element counts (and types, or bfloat16 for
     float32). A norm that is not finite leaves them unscaled and raises RLK_FLAG_NONFINITE in err_flag."""
     grads, dev = _gradients(grads)
     outs = grads if out is None else ((out,) if isinstance(out, torch.Tensor) else tuple(out))
@@ -324,10 +327,10 @@ def clip_grad_norm(grads: Union[torch.Tensor, Sequence[torch.Tensor]], max_norm:
     at, codes = _listed(grads, "gradients", dev)
     to, ocodes = at, codes
     if out is not None:
-        if len(outs) != len(grads) or any(not isinstance(o, torch.Tensor) or o.shape != g.shape for o, g in zip(outs, grads)):
-            raise ValueError("out must hold a tensor of each gradient's shape")
         to, ocodes = _listed(outs, "out", dev)
     sizes = array.array("q", map(_numel, grads))
+    if out is not None and array.array("q", map(_numel, outs)) != sizes:
+        raise ValueError("out must hold a tensor of each gradient's element count")
     n = len(grads)
     r = _norm_result(norm, grads[0], dev)
     ws, wp, nbytes = _scratch(grad_norm_workspace_bytes(n), grads[0], workspace)

@@ -648,7 +648,7 @@ def test_dirty_workspaces(rlk):
     for fill in (0, 255, 127):
         for f in (lambda **k: rlk.embedding_bwd(d["dy"], ids, 90, **k), lambda **k: rlk.grad_norm([d["x"]], **k),
                   lambda **k: rlk.layer_norm_bwd(d["dy"], d["x"], d["w"], mean, rstd, **k)):
-            n = max(rlk.embedding_bwd_workspace_bytes(T, H), rlk.layer_norm_bwd_workspace_bytes(T, H), 608 * 8) + 77
+            n = max(rlk.embedding_bwd_workspace_bytes(T, H), rlk.layer_norm_bwd_workspace_bytes(T, H), rlk.grad_norm_workspace_bytes(1)) + 77
             ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
             got, want = f(workspace=ws), f()
             for a, b in zip(got if isinstance(got, tuple) else (got,), want if isinstance(want, tuple) else (want,)):

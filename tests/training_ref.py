@@ -126,8 +126,9 @@ def norm_grad(dy, x, w, mean, rstd):
 
 
 def total_norm(grads):
-    """(norm, relative tolerance): 5 roundings in a pack, one for each pack of a thread's share (4 a chunk at most);
-    half of all that through the root, and one to fp32."""
+    """(norm, relative tolerance): 16 products a thread and chunk added up one by one, even and odd apart, 17 roundings;
+    one for each chunk of a share, 8 over a CTA's threads, 2 of the shares of a thread (which keep what they lose), 8 over threads
+    again; half of all that through the root, and its own. A scale beside the norm's adds one more."""
     chunks = sum(-(-g.numel() * g.element_size() // 16384) for g in grads)
     n = math.sqrt(math.fsum(float(g.double().square().sum()) for g in grads))
-    return n, (0.5 * (4 * -(-chunks // 608) + 6) + 1) * U
+    return n, (0.5 * (-(-chunks // 608) + 36) + 1) * U
