@@ -112,6 +112,8 @@ __device__ __forceinline__ int piece_of(const ClipArgs<N>& a, uint32_t chunk) {
   return lo;
 }
 
+__device__ __forceinline__ bool on_vector_boundary(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
 // Chunks lo, lo + SHARES, ... below hi of a tensor. A misaligned one's packs are cut from their neighbours' vectors, so that every thread owns the
 // elements that it owns of an aligned one.
 template <class E>
@@ -119,13 +121,13 @@ __device__ __noinline__ Squares sum_chunks(const Piece p, uint32_t lo, uint32_t 
   const int tid = static_cast<int>(threadIdx.x);
   const auto* in = static_cast<const typename E::bits*>(p.in) + static_cast<int64_t>(lo) * CHUNK<E>;
   int64_t left = p.n - static_cast<int64_t>(lo) * CHUNK<E>;
-  const bool aligned = (reinterpret_cast<uintptr_t>(p.in) & 15) == 0;
+  const bool aligned = on_vector_boundary(p.in);
 #pragma unroll 1
   for (uint32_t c = lo; c < hi; c += SHARES) {
     if (aligned && left >= CHUNK<E>) {
       Pack<E> k[PACKS<E>];
 #pragma unroll
-      for (int j = 0; j < PACKS<E>; ++j) k[j] = load_columns<E, true>(in + 8 * tid, 8 * j * CLIP_THREADS, CHUNK<E> - 8 * tid, err);
+      for (int j = 0; j < PACKS<E>; ++j) k[j] = load_columns<E, true, false>(in + 8 * tid, 8 * j * CLIP_THREADS, CHUNK<E> - 8 * tid, err);
       add_squares<E, PACKS<E>>(s, [&](int j) { return k[j]; });
     } else {
       const int n = static_cast<int>(min(static_cast<int64_t>(CHUNK<E>), left));
@@ -228,9 +230,9 @@ __device__ __noinline__ void scale_chunks(const Piece p, uint32_t c, uint32_t st
     unpack(k, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = plain ? v[i] : mul2(v[i], both(f));
-    store_columns<O, true>(out, c, n, v, err);
+    store_columns<O, true, false>(out, c, n, v, err);
   };
-  const bool alike = ((reinterpret_cast<uintptr_t>(in0) + head0 * sizeof(*in0)) & 15) == 0;
+  const bool alike = on_vector_boundary(in0 + head0);
 #pragma unroll 1
   for (;; c -= step) {
     const int64_t at = static_cast<int64_t>(c) * CHUNK<E>;
@@ -249,14 +251,14 @@ __device__ __noinline__ void scale_chunks(const Piece p, uint32_t c, uint32_t st
       Pack<E> k[PACKS<E>];
 #pragma unroll
       for (int j = 0; j < PACKS<E>; ++j)
-        if (j < PACKS<E> - 1 || last) k[j] = load_columns<E, true>(in + 8 * tid, 8 * j * CLIP_THREADS, n - head - 8 * tid, err);
+        if (j < PACKS<E> - 1 || last) k[j] = load_columns<E, true, false>(in + 8 * tid, 8 * j * CLIP_THREADS, n - head - 8 * tid, err);
 #pragma unroll
       for (int j = 0; j < PACKS<E>; ++j)
         if (j < PACKS<E> - 1 || last) put(k[j], out + 8 * tid, 8 * j * CLIP_THREADS, n - head - 8 * tid);
     } else {
 #pragma unroll 1
       for (int q = tid; q < packs; q += CLIP_THREADS)
-        put(alike ? load_columns<E, true>(in, 8 * q, n - head, err) : load_columns<E, false>(in, 8 * q, n - head, err), out, 8 * q,
+        put(alike ? load_columns<E, true, false>(in, 8 * q, n - head, err) : load_columns<E, false>(in, 8 * q, n - head, err), out, 8 * q,
             n - head);
     }
     if (c < step) return;

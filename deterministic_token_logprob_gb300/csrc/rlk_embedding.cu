@@ -713,7 +713,7 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
   }
   const Room r = room_of(T, H);
   if (r.all > 0 && (!workspace || !on_boundary(workspace, 256) || workspace_bytes < r.all)) return RLK_ERR_WORKSPACE;
-  const bool al = whole_packs(dout, T, H, ld, in.eb) && on_boundary(dW, 16);
+  const bool al = whole_packs(dout, T, H, ld, in.eb) && on_boundary(dW, 32);
   const Shard shard{vocab_start, V_local, V_true, err_flag};
   GatherArgs g{nullptr, nullptr, nullptr, ids, shard, dout, dW, ld, static_cast<int32_t>(T), static_cast<int32_t>(H),
                static_cast<int32_t>(V_local), static_cast<float>(scale), accumulate != 0, nullptr, nullptr, r.slots, 0, 0, err_flag};

@@ -7,19 +7,25 @@
 //
 // Both directions are bound by memory: the forward reads x and writes y, the backward reads x and dy
 // and writes dx, once each.
+#include <type_traits>
+
 #include "rlk_rows.cuh"
 
 namespace rlk {
 namespace {
 
-constexpr int NORM_THREADS = SLOTS;
+
+// Warps that take a row. Forward: up to 4 packs a thread before another warp, since a row's two sums and its few scalars cost
+// every warp the same (4096 columns: 4 warps); backward: few packs a thread, whose sums of dw and db it keeps (8 warps).
+__host__ __device__ constexpr int fwd_warps(int n) { return n <= 512 ? 1 : n <= 1024 ? 2 : n <= 4096 ? 4 : 8; }
+__host__ __device__ constexpr int bwd_warps(int n) { return n <= 256 ? 1 : n <= 512 ? 2 : n <= 1024 ? 4 : 8; }
 
 // Rows are dealt to strips, whose parts of dw and db are summed apart: row t belongs to strip t mod S. S follows
 // from T and the width alone, and so does the order of the sum over rows: two CTAs on each of 152 SMs,
 // each of as many teams as the width leaves room for.
 constexpr int NORM_CTAS = 304;
 __host__ __device__ constexpr int strips_of(int64_t T, int n) {
-  return static_cast<int>(T < NORM_CTAS * (8 / team_warps(n)) ? T : NORM_CTAS * (8 / team_warps(n)));
+  return static_cast<int>(T < NORM_CTAS * (8 / bwd_warps(n)) ? T : NORM_CTAS * (8 / bwd_warps(n)));
 }
 
 // A row that overflows fp32 in its sums is taken once more as x 2^-80.
@@ -31,7 +37,7 @@ struct Vector {  // weight or bias: fp32 or the rows' type, or absent
   bool f32;
 };
 
-// 8 columns of a vector; AL: it starts on a 16-byte boundary and n is a multiple of 8.
+// 8 columns of a vector; AL: it starts on a 32-byte boundary and n is a multiple of 8.
 template <class E, bool AL>
 __device__ __forceinline__ void vector8(const Vector& w, int c0, int n, float absent, F32x2 (&v)[4], int32_t* err) {
   if (!w.p) {
@@ -91,9 +97,7 @@ __device__ __forceinline__ RowStats row_stats(int n, bool centered, float eps, f
     if (isfinite(q) || s.k != 1.f) break;
     s.k = kShrink;
     // the sums to come use the room again
-    if constexpr (W == 8) __syncthreads();
-    else if constexpr (W > 1)
-      asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x / (32 * W))), "n"(32 * W) : "memory");
+    team_barrier<W>();
   }
   const float var = fmaxf(__fmaf_rn(-s.c, s.c, q), 0.f);
   if (!isfinite(q)) s.r = quiet_nan();  // a NaN or an infinity in the row
@@ -131,10 +135,10 @@ __device__ __forceinline__ void norm_pack(F32x2 (&v)[4], const RowStats& s, cons
   }
 }
 
-// Rows of whole packs on 16-byte boundaries, K packs a thread, which stay in registers between the two sums and the
+// Rows of whole packs, K packs a thread, which stay in registers between the two sums and the
 // result. W warps a row: 8 / W rows a CTA.
 template <class E, class O, int W, int K>
-__global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(ROW_CTA) norm_fwd_kernel(const NormArgs a) {
   __shared__ float rooms[32];
   const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W), packs = a.H / 8;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
@@ -143,14 +147,14 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormArgs a
   Pack<E> k[K];
 #pragma unroll
   for (int j = 0; j < K; ++j)
-    if (tid + j * SLOTS < packs) k[j] = load_columns<E, true>(x, 8 * (tid + j * SLOTS), a.H, a.err);
+    if (tid + j * 32 * W < packs) k[j] = load_columns<E, true>(x, 8 * (tid + j * 32 * W), a.H, a.err);
   const auto each = [&](auto f) {
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (tid + j * SLOTS < packs) {
+      if (tid + j * 32 * W < packs) {
         F32x2 v[4];
         unpack(k[j], v);
-        f(8 * (tid + j * SLOTS), v);
+        f(8 * (tid + j * 32 * W), v);
       }
   };
   const RowStats s = row_stats<W, true>(a.H, a.centered, a.eps, rooms + team * 4 * W, each);
@@ -166,22 +170,24 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_fwd_kernel(const NormArgs a
   });
 }
 
-// Any row, one CTA each: it is read three times (from L1 or L2 after the first).
-template <class E, class O>
-__global__ void __launch_bounds__(NORM_THREADS) norm_fwd_any_kernel(const NormArgs a) {
-  __shared__ float room[32];
-  const int64_t t = blockIdx.x;
+// Any row: it is read three times (from L1 or L2 after the first).
+template <class E, class O, int W>
+__global__ void __launch_bounds__(ROW_CTA) norm_fwd_any_kernel(const NormArgs a) {
+  __shared__ float rooms[32];
+  const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W);
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
+  if (t >= a.T) return;  // the whole team
   const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
   auto* y = static_cast<typename O::bits*>(a.y) + t * a.out_ld;
   const auto each = [&](auto f) {
-    for (int c = 8 * threadIdx.x; c < a.H; c += 8 * SLOTS) {
+    for (int c = 8 * tid; c < a.H; c += 8 * 32 * W) {
       F32x2 v[4];
       unpack(load_columns<E, false>(x, c, a.H, a.err), v);
       f(c, v);
     }
   };
-  const RowStats s = row_stats<8, false>(a.H, a.centered, a.eps, room, each);
-  if (threadIdx.x == 0) put_stats(a, t, s);
+  const RowStats s = row_stats<W, false>(a.H, a.centered, a.eps, rooms + team * 4 * W, each);
+  if (tid == 0) put_stats(a, t, s);
   each([&](int c0, F32x2 (&v)[4]) {
     F32x2 w[4], b[4];
     vector8<E, false>(a.w, c0, a.H, 1.f, w, a.err);
@@ -249,7 +255,7 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The packs of one row that a warp's threads own (8 W apart for the j-th of each), copied into shared memory and read from it
+// The packs of one row that a warp's threads own (256 packs apart for the j-th of each), copied into shared memory and read from it
 // by the same warp. Copies go by 16-byte vectors in the order of addresses; `room` holds the first halves of all packs,
 // then (fp32) the second ones, so that neither meets a bank twice.
 template <class E, int K>
@@ -260,7 +266,7 @@ struct RowRing {
     for (int j = 0; j < K; ++j)
 #pragma unroll
       for (int i = 0; i < HALVES; ++i) {
-        const int u = i * 32 + lane, p = warp * 32 + j * SLOTS + u / HALVES;  // vector u of the warp's 32 HALVES
+        const int u = i * 32 + lane, p = warp * 32 + j * 256 + u / HALVES;  // vector u of the warp's 32 HALVES
         if (p < packs && ok) copy_async_16(room + (u % HALVES) * packs + p, static_cast<const uint4*>(row) + p * HALVES + u % HALVES);
       }
   }
@@ -272,10 +278,10 @@ struct RowRing {
   }
 };
 
-// Rows of whole packs on 16-byte boundaries, up to 8192 columns. A team of W warps takes a strip's rows in turn; the next
+// Rows of whole packs, up to 8192 columns. A team of W warps takes a strip's rows in turn; the next
 // stages - 1 rows are on their way into shared memory meanwhile. Each thread keeps the sums of dw and db of its columns.
 template <class E, class O, int W, int K>
-__global__ void __launch_bounds__(NORM_THREADS, K <= 2 ? 2 : 1) norm_bwd_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const NormGradArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ float rooms[32];
   constexpr int XH = RowRing<E, K>::HALVES, DH = RowRing<O, K>::HALVES;
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(NORM_THREADS, K <= 2 ? 2 : 1) norm_bwd_kernel(
   F32x2 w[K][4], sw[K][4], sb[K][4];
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    const int c0 = 8 * (tid + j * SLOTS);
+    const int c0 = 8 * (tid + j * 256);
     if (c0 < a.H) vector8<E, true>(a.w, c0, a.H, 1.f, w[j], a.err);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sw[j][i] = sb[j][i] = 0;
@@ -316,9 +322,9 @@ __global__ void __launch_bounds__(NORM_THREADS, K <= 2 ? 2 : 1) norm_bwd_kernel(
     F32x2 h[K][4], dy[K][4], s1 = 0, s2 = 0;
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (tid + j * SLOTS < packs) {
-        RowRing<E, K>::read(xs, tid + j * SLOTS, packs, h[j]);
-        RowRing<O, K>::read(xs + packs * XH, tid + j * SLOTS, packs, dy[j]);
+      if (tid + j * 256 < packs) {
+        RowRing<E, K>::read(xs, tid + j * 256, packs, h[j]);
+        RowRing<O, K>::read(xs + packs * XH, tid + j * 256, packs, dy[j]);
         norm_h(h[j], m, r);
         norm_vectors(h[j], dy[j], sw[j], sb[j]);
         norm_sums(h[j], dy[j], w[j], s1, s2);
@@ -329,10 +335,10 @@ __global__ void __launch_bounds__(NORM_THREADS, K <= 2 ? 2 : 1) norm_bwd_kernel(
       auto* dx = static_cast<typename E::bits*>(a.dx) + t * a.dx_ld;
 #pragma unroll
       for (int j = 0; j < K; ++j)
-        if (tid + j * SLOTS < packs) {
+        if (tid + j * 256 < packs) {
           F32x2 v[4];
           norm_dx(h[j], dy[j], w[j], c1, c2, r, v);
-          store_columns<E, true>(dx, 8 * (tid + j * SLOTS), a.H, v, a.err);
+          store_columns<E, true>(dx, 8 * (tid + j * 256), a.H, v, a.err);
         }
     }
     m = m1;
@@ -344,7 +350,7 @@ __global__ void __launch_bounds__(NORM_THREADS, K <= 2 ? 2 : 1) norm_bwd_kernel(
   copies_wait<0>();
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    const int c0 = 8 * (tid + j * SLOTS);
+    const int c0 = 8 * (tid + j * 256);
     if (c0 >= a.H) continue;
     if (a.part_w) store_columns<F32, true>(reinterpret_cast<uint32_t*>(a.part_w) + strip * a.H, c0, a.H, sw[j], a.err);
     if (a.part_b) store_columns<F32, true>(reinterpret_cast<uint32_t*>(a.part_b) + strip * a.H, c0, a.H, sb[j], a.err);
@@ -353,14 +359,14 @@ __global__ void __launch_bounds__(NORM_THREADS, K <= 2 ? 2 : 1) norm_bwd_kernel(
 
 // Any rows: first what the whole row gives, then the columns.
 template <class E, class O>
-__global__ void __launch_bounds__(NORM_THREADS) norm_bwd_rows_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(ROW_CTA) norm_bwd_rows_kernel(const NormGradArgs a) {
   __shared__ float room[16];
   const int64_t t = blockIdx.x;
   const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
   const auto* dy = static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld;
   const float m = a.mean ? a.mean[t] : 0.f, r = a.rstd[t];
   F32x2 s1 = 0, s2 = 0;
-  for (int c = 8 * threadIdx.x; c < a.H; c += 8 * SLOTS) {
+  for (int c = 8 * threadIdx.x; c < a.H; c += 8 * 256) {
     F32x2 h[4], dv[4], w[4];
     unpack(load_columns<E, false>(x, c, a.H, a.err), h);
     unpack(load_columns<O, false>(dy, c, a.H, a.err), dv);
@@ -378,8 +384,8 @@ __global__ void __launch_bounds__(NORM_THREADS) norm_bwd_rows_kernel(const NormG
 }
 
 template <class E, class O>
-__global__ void __launch_bounds__(NORM_THREADS) norm_bwd_columns_kernel(const NormGradArgs a) {
-  const int c0 = 8 * static_cast<int>(blockIdx.x * NORM_THREADS + threadIdx.x);
+__global__ void __launch_bounds__(ROW_CTA) norm_bwd_columns_kernel(const NormGradArgs a) {
+  const int c0 = 8 * static_cast<int>(blockIdx.x * ROW_CTA + threadIdx.x);
   if (c0 >= a.H) return;
   F32x2 w[4], sw[4] = {}, sb[4] = {};
   vector8<E, false>(a.w, c0, a.H, 1.f, w, a.err);
@@ -426,21 +432,28 @@ inline bool vector_ok(const void* p, int32_t dtype, int32_t rows_dtype) {
   return !p || ((dtype == rows_dtype || dtype == RLK_DTYPE_F32) && on_boundary(p, dtype_bytes(dtype)));
 }
 
-// Calls f with the team's width and the packs a thread for rows of H columns, 8 per thread and pack.
+template <int V>
+using Int = std::integral_constant<int, V>;
+
+// Calls f with the warps a row and the packs a thread, for rows of H columns.
 template <class F>
-inline rlk_status with_team(int64_t H, F f) {
-  const auto w = [&](auto warps, auto k) { return f(warps, k); };
-  using std::integral_constant;
-  switch (team_warps(static_cast<int>(H))) {
-    case 1: return w(integral_constant<int, 1>{}, integral_constant<int, 1>{});
-    case 2: return w(integral_constant<int, 2>{}, integral_constant<int, 1>{});
-    case 4: return w(integral_constant<int, 4>{}, integral_constant<int, 1>{});
-    default: break;
-  }
-  if (H <= 2048) return w(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-  if (H <= 4096) return w(integral_constant<int, 8>{}, integral_constant<int, 2>{});
-  if (H <= 8192) return w(integral_constant<int, 8>{}, integral_constant<int, 4>{});
-  return w(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+inline rlk_status with_fwd_team(int64_t H, F f) {
+  if (H <= 256) return f(Int<1>{}, Int<1>{});
+  if (H <= 512) return f(Int<1>{}, Int<2>{});
+  if (H <= 1024) return f(Int<2>{}, Int<2>{});
+  if (H <= 2048) return f(Int<4>{}, Int<2>{});
+  if (H <= 4096) return f(Int<4>{}, Int<4>{});
+  if (H <= 8192) return f(Int<8>{}, Int<4>{});
+  return f(Int<8>{}, Int<8>{});
+}
+template <class F>
+inline rlk_status with_bwd_team(int64_t H, F f) {
+  if (H <= 256) return f(Int<1>{}, Int<1>{});
+  if (H <= 512) return f(Int<2>{}, Int<1>{});
+  if (H <= 1024) return f(Int<4>{}, Int<1>{});
+  if (H <= 2048) return f(Int<8>{}, Int<1>{});
+  if (H <= 4096) return f(Int<8>{}, Int<2>{});
+  return f(Int<8>{}, Int<4>{});
 }
 
 constexpr int64_t FWD_KEPT = 16384;  // columns of a row that stays in registers (8 packs a thread)
@@ -460,7 +473,7 @@ inline rlk_status launch_norm_bwd(NormGradArgs a, int64_t stage_bytes, cudaStrea
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K <= 2 ? BWD_SMEM : BWD_SMEM_ONE) == cudaSuccess;
       }))
     return RLK_ERR_CUDA;
-  kernel<<<static_cast<unsigned>((a.strips + 8 / W - 1) / (8 / W)), NORM_THREADS, smem, s>>>(a);
+  kernel<<<static_cast<unsigned>((a.strips + 8 / W - 1) / (8 / W)), ROW_CTA, smem, s>>>(a);
   return launched();
 }
 
@@ -488,18 +501,15 @@ rlk_status rlk_layer_norm_fwd(const void* x, int32_t dtype, int64_t T, int64_t H
   const NormArgs a{x, y, T, ld, out_ld, static_cast<int32_t>(H), centered != 0, static_cast<float>(eps),
                    Vector{weight, f32}, Vector{bias, f32}, mean, rstd, err_flag};
   const bool kept = H <= FWD_KEPT && whole_packs(x, T, H, ld, in.eb) && whole_packs(y, T, H, out_ld, out.eb) &&
-                    on_boundary(weight, 16) && on_boundary(bias, 16);
+                    on_boundary(weight, 32) && on_boundary(bias, 32);
   const auto s = static_cast<cudaStream_t>(stream);
   return with_pair(dtype, out_dtype, [&](auto e, auto o) {
     using E = decltype(e);
     using O = decltype(o);
-    if (!kept) {
-      norm_fwd_any_kernel<E, O><<<static_cast<unsigned>(T), NORM_THREADS, 0, s>>>(a);
-      return launched();
-    }
-    return with_team(H, [&](auto w, auto k) {
+    return with_fwd_team(H, [&](auto w, auto k) {
       constexpr int W = decltype(w)::value, K = decltype(k)::value;
-      norm_fwd_kernel<E, O, W, K><<<static_cast<unsigned>((T + 8 / W - 1) / (8 / W)), NORM_THREADS, 0, s>>>(a);
+      const auto kernel = kept ? norm_fwd_kernel<E, O, W, K> : norm_fwd_any_kernel<E, O, W>;
+      kernel<<<static_cast<unsigned>((T + 8 / W - 1) / (8 / W)), ROW_CTA, 0, s>>>(a);
       return launched();
     });
   });
@@ -542,19 +552,17 @@ rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t dy_ld, c
   if (dw) a.part_w = reinterpret_cast<float*>(after);
   if (db) a.part_b = reinterpret_cast<float*>(after + part);
   const bool kept = H <= BWD_KEPT && whole_packs(x, T, H, ld, xs.eb) && whole_packs(dy, T, H, dy_ld, ds.eb) &&
-                    (!dx || whole_packs(dx, T, H, dx_ld, os.eb)) && on_boundary(weight, 16);
+                    (!dx || whole_packs(dx, T, H, dx_ld, os.eb)) && on_boundary(weight, 32);
   st = with_pair(dtype, dy_dtype, [&](auto e, auto o) {
     using E = decltype(e);
     using O = decltype(o);
     if (kept)
-      return with_team(H, [&](auto w, auto k) {
-        constexpr int W = decltype(w)::value, K = decltype(k)::value;
-        if constexpr (K <= 4) return launch_norm_bwd<E, O, W, K>(a, H * (xs.eb + ds.eb), s);
-        else return RLK_ERR_UNSUPPORTED;  // rows of BWD_KEPT columns have 4 packs a thread at most
+      return with_bwd_team(H, [&](auto w, auto k) {
+        return launch_norm_bwd<E, O, decltype(w)::value, decltype(k)::value>(a, H * (xs.eb + ds.eb), s);
       });
-    if (dx) norm_bwd_rows_kernel<E, O><<<static_cast<unsigned>(T), NORM_THREADS, 0, s>>>(a);
-    const unsigned blocks = static_cast<unsigned>((H + 8 * NORM_THREADS - 1) / (8 * NORM_THREADS));
-    norm_bwd_columns_kernel<E, O><<<dim3(blocks, a.strips), NORM_THREADS, 0, s>>>(a);
+    if (dx) norm_bwd_rows_kernel<E, O><<<static_cast<unsigned>(T), ROW_CTA, 0, s>>>(a);
+    const unsigned blocks = static_cast<unsigned>((H + 8 * ROW_CTA - 1) / (8 * ROW_CTA));
+    norm_bwd_columns_kernel<E, O><<<dim3(blocks, a.strips), ROW_CTA, 0, s>>>(a);
     return launched();
   });
   if (st != RLK_OK || !(dw || db)) return st;

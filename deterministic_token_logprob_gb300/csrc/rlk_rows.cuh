@@ -2,13 +2,11 @@
 // values cut into packs of 8 columns, their loads and stores at any alignment, sums over a row in one
 // fixed order, and the host-side argument checks.
 //
-// Order of a row's sums: pack p (columns 8 p .. 8 p + 7) belongs to slot p mod 256; a slot adds the even
-// and the odd columns of its packs apart, in ascending order of packs (a pack's four pairs as a balanced
-// tree; sums of products one by one, each product unrounded), and then the two; 32 slots combine by an
-// xor-butterfly, the eight groups of 32 by a balanced tree. Slots without packs hold 0, so that a row of few
-// packs is taken by fewer warps with the same bits.
-// The order depends on column indices alone: not on the row's address, on alignment or on how many
-// rows a CTA takes.
+// Order of a row's sums over n columns: pack p (columns 8 p .. 8 p + 7) belongs to slot p mod S, S = 32 W with W warps a row
+// (a power of two that follows from n and the kind of sum); a slot adds the even and the odd columns of its packs apart, in
+// ascending order of packs (a pack's four pairs as a balanced tree; sums of products one by one, each product
+// unrounded), and then the two; 32 slots combine by an xor-butterfly, the groups of 32 by a balanced tree. The
+// order depends on column indices alone: not on the row's address, on alignment or on how many rows a CTA takes.
 #pragma once
 
 #include <atomic>
@@ -18,7 +16,7 @@
 namespace rlk {
 namespace {
 
-constexpr int SLOTS = 256;  // of a row's sums; the threads of the widest team that takes one row
+constexpr int ROW_CTA = 256;  // threads of a CTA: 8 / W teams, a row each
 
 template <bool V>
 struct Is {
@@ -38,10 +36,20 @@ __device__ __noinline__ Pack<E> load_edge(const typename E::bits* row, int c0, i
   return k;
 }
 
-// 8 columns of a row of n, from column c0 (a multiple of 8) on; 0 beyond the row. AL: the row starts on
-// a 16-byte boundary and n is a multiple of 8.
-template <class E, bool AL>
+// 8 columns of a row of n, from column c0 (a multiple of 8) on; 0 beyond the row. AL: every pack lies on a boundary of its
+// own size (whole_packs). An fp32 pack is then one 32-byte load: two of 16 bytes each, 32 apart from lane to lane, take L1
+// twice as long (8192 rows of 4096, fp32 to bf16 forward: L1 73 % busy). Without WIDE 16-byte boundaries do, and loads.
+template <class E, bool AL, bool WIDE = true>
 __device__ __forceinline__ Pack<E> load_columns(const typename E::bits* row, int c0, int n, int32_t* err) {
+  if constexpr (AL && WIDE && sizeof(typename E::bits) == 4) {
+    Pack<E> k{};
+    if (dbg_ok(c0 >= 0 && c0 + 8 <= n && (reinterpret_cast<uintptr_t>(row + c0) & 31) == 0, err))
+      asm("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+          : "=r"(k.w[0]), "=r"(k.w[1]), "=r"(k.w[2]), "=r"(k.w[3]), "=r"(k.w[4]), "=r"(k.w[5]), "=r"(k.w[6]), "=r"(k.w[7])
+          : "l"(row + c0)
+          : "memory");
+    return k;
+  }
   const Row<E, AL> r(row, n, err);
   if (AL || packs_inside(r, c0, c0 + 8)) return load_pack(r, c0);
   return load_edge<E>(row, c0, n);
@@ -71,19 +79,24 @@ __device__ __forceinline__ void clear_beyond(F32x2 (&v)[4], int c0, int n) {
   }
 }
 
-template <class O, bool AL>
+template <class O, bool AL, bool WIDE = true>
 __device__ __forceinline__ void store_columns(typename O::bits* row, int c0, int n, const F32x2 (&x)[4], int32_t* err) {
   if (!dbg_ok(c0 >= 0 && c0 < n && (!AL || c0 + 8 <= n), err)) return;
   float2 v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) v[i] = unpack_f32x2(x[i]);
   if constexpr (AL) {
-    uint4* q = reinterpret_cast<uint4*>(row + c0);
-    if constexpr (sizeof(typename O::bits) == 4) {
-      q[0] = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
-      q[1] = make_uint4(__float_as_uint(v[2].x), __float_as_uint(v[2].y), __float_as_uint(v[3].x), __float_as_uint(v[3].y));
+    if constexpr (sizeof(typename O::bits) == 4 && !WIDE) {
+      float4* q = reinterpret_cast<float4*>(row + c0);
+      q[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+      q[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+    } else if constexpr (sizeof(typename O::bits) == 4) {
+      if (!dbg_ok((reinterpret_cast<uintptr_t>(row + c0) & 31) == 0, err)) return;
+      asm volatile("st.global.v8.f32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y),
+                   "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y), "l"(row + c0)
+                   : "memory");
     } else {
-      q[0] = make_uint4(O::pack2(v[0].x, v[0].y), O::pack2(v[1].x, v[1].y), O::pack2(v[2].x, v[2].y), O::pack2(v[3].x, v[3].y));
+      *reinterpret_cast<uint4*>(row + c0) = make_uint4(O::pack2(v[0].x, v[0].y), O::pack2(v[1].x, v[1].y), O::pack2(v[2].x, v[2].y), O::pack2(v[3].x, v[3].y));
     }
   } else {
 #pragma unroll
@@ -108,6 +121,8 @@ __device__ __forceinline__ float low_plus_high(F32x2 v) {
 // order; every thread of the team gets both. `room`: 2 W floats of shared memory of the team's own, which the call
 // after this one does not use (one barrier a call then does).
 template <int W>
+__device__ __forceinline__ void team_barrier();
+template <int W>
 __device__ __forceinline__ float2 team_sum(float a, float b, float* room) {
   const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W;
   const bool low = lane < 16;
@@ -116,8 +131,7 @@ __device__ __forceinline__ float2 team_sum(float a, float b, float* room) {
   for (int d = 8; d >= 1; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFullWarp, v, d));
   if constexpr (W == 1) return make_float2(__shfl_sync(kFullWarp, v, 0), __shfl_sync(kFullWarp, v, 16));
   if ((lane & 15) == 0) room[(low ? 0 : W) + warp] = v;
-  if constexpr (W == 8) __syncthreads();
-  else asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x / (32 * W))), "n"(32 * W) : "memory");
+  team_barrier<W>();
   float x[2 * W];
 #pragma unroll
   for (int i = 0; i < 2 * W; ++i) x[i] = room[i];
@@ -128,18 +142,22 @@ __device__ __forceinline__ float2 team_sum(float a, float b, float* room) {
   return make_float2(x[0], x[W]);
 }
 
-// Warps that take a row of n columns: 1, 2, 4 or 8.
-__host__ __device__ constexpr int team_warps(int n) { return n <= 256 ? 1 : n <= 512 ? 2 : n <= 1024 ? 4 : 8; }
+// Another barrier of a team of W warps.
+template <int W>
+__device__ __forceinline__ void team_barrier() {
+  if constexpr (W == 8) __syncthreads();
+  else if constexpr (W > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + static_cast<int>(threadIdx.x / (32 * W))), "n"(32 * W) : "memory");
+}
 
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 inline bool on_boundary(const void* p, int64_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
 
-// T rows of n elements, `ld` elements apart: whether every row starts on a 16-byte boundary and is a
-// whole number of packs.
+// T rows of n elements of eb bytes, `ld` elements apart: whether every row is a whole number of packs of 8, each on a boundary
+// of its own size (16 bytes, 32 for fp32).
 inline bool whole_packs(const void* p, int64_t T, int64_t n, int64_t ld, int eb) {
-  return on_boundary(p, 16) && n % 8 == 0 && (T <= 1 || ld * eb % 16 == 0);
+  return on_boundary(p, 8 * eb) && n % 8 == 0 && (T <= 1 || ld % 8 == 0);
 }
 
 struct RowSpan {  // T rows of n elements of eb bytes, ld elements apart

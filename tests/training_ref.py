@@ -1,8 +1,9 @@
 """Plain 64-bit forms of the operators around the head, and how far fp32 sums in a tree may be from them.
 
 U is half a step of fp32 (2^-24), the most that one operation is off, relative to its result. A row's
-sum goes through depth(H) additions at most: 4 for each of a slot's ceil(ceil(H / 8) / 256) packs, 1 of even
-and odd columns, 5 in a warp, 3 over the warps. Every bound below counts roundings, times U, times the magnitudes that
+sum goes through depth(H, S) additions at most: 4 for each of a slot's ceil(ceil(H / 8) / S) packs, 1 of even
+and odd columns, 5 in a warp, 3 over the warps; S slots, in the forward 32 up to 512 columns, 64 up to 1024, 128 up to
+4096 and 256 beyond, in the backward 32 up to 256, 64 up to 512, 128 up to 1024. Every bound below counts roundings, times U, times the magnitudes that
 they round; second orders are inside the few roundings that each count is rounded up by.
 """
 import math
@@ -14,8 +15,9 @@ STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0
 TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -150}  # half of the smallest value
 
 
-def depth(H):
-    return 4 * -(-(-(-H // 8)) // 256) + 9
+def depth(H, forward):
+    S = 32 * ((1 if H <= 512 else 2 if H <= 1024 else 4 if H <= 4096 else 8) if forward else (1 if H <= 256 else 2 if H <= 512 else 4 if H <= 1024 else 8))
+    return 4 * -(-(-(-H // 8)) // S) + 9
 
 
 def close(got, want, tol, name=""):
@@ -83,11 +85,11 @@ def norm(x, w, b, eps, centered):
     w = torch.ones(H, dtype=torch.float64, device=x.device) if w is None else w.double()
     b = torch.zeros(H, dtype=torch.float64, device=x.device) if b is None else b.double()
     y = d * r * w + b
-    D, size = depth(H) + 4, d.abs().mean(1, keepdim=True)
+    D, size = depth(H, True) + 4, d.abs().mean(1, keepdim=True)
     # x - m and the correction c: three roundings; c itself is a sum of differences over H. Before the correction the
     # mean is off by depth roundings of mean |x|, which the sum of differences sees in full and the square of which leaves
     # the variance to second order
-    off = depth(H) * U * x.abs().mean(1, keepdim=True)
+    off = depth(H, True) * U * x.abs().mean(1, keepdim=True)
     td = 3 * U * (d.abs() + off) + D * U * (size + off)
     tvar = (D * U * (var + off * off) + 2 * size * D * U * (size + off)) * 2
     tr = r * (0.5 * tvar / (var + eps) + 4 * U)
@@ -109,7 +111,7 @@ def norm_grad(dy, x, w, mean, rstd):
     g = dy * w                                      # one
     c1 = g.mean(1, keepdim=True) if mean is not None else torch.zeros_like(r)
     c2 = (g * h).mean(1, keepdim=True)
-    D = depth(H)
+    D = depth(H, False)
     t1 = (D + 3) * U * g.abs().mean(1, keepdim=True)
     t2 = (D + 6) * U * (g * h).abs().mean(1, keepdim=True)
     if mean is None:
