@@ -15,9 +15,8 @@ namespace rlk {
 namespace {
 
 
-// Warps that take a row. Forward: up to 4 packs a thread before another warp, since a row's two sums and its few scalars cost
-// every warp the same (4096 columns: 4 warps); backward: few packs a thread, whose sums of dw and db it keeps (8 warps).
-__host__ __device__ constexpr int fwd_warps(int n) { return n <= 512 ? 1 : n <= 1024 ? 2 : n <= 4096 ? 4 : 8; }
+// Warps that take a row, in the backward: few packs a thread, whose sums of dw and db it keeps. (The forward has up to 4 packs a
+// thread before another warp, since a row's two sums and its few scalars cost every warp the same: with_fwd_team.)
 __host__ __device__ constexpr int bwd_warps(int n) { return n <= 256 ? 1 : n <= 512 ? 2 : n <= 1024 ? 4 : 8; }
 
 // Rows are dealt to strips, whose parts of dw and db are summed apart: row t belongs to strip t mod S. S follows
@@ -65,46 +64,19 @@ __device__ __forceinline__ void shrink(F32x2 (&v)[4], float k) {
   for (int i = 0; i < 4; ++i) v[i] = mul2(v[i], both(k));
 }
 
-// The statistics of a row of n columns. each(f) calls f(c0, v) with the columns of every pack of this thread; FULL: no pack
-// reaches beyond the row. room: 4 W floats.
-template <int W, bool FULL, class Each>
-__device__ __forceinline__ RowStats row_stats(int n, bool centered, float eps, float* room, const Each& each) {
-  const float len = static_cast<float>(n);
-  RowStats s{1.f, 0.f, 0.f, 0.f};
-  float q;
-  for (;;) {
-    if (centered) {
-      F32x2 a = 0;
-      each([&](int, F32x2 (&v)[4]) {
-        shrink(v, s.k);
-        a = add2(a, tree4(v));
-      });
-      s.m = __fdiv_rn(team_sum<W>(low_plus_high(a), 0.f, room).x, len);
-    }
-    F32x2 a = 0, b = 0;
-    each([&](int c0, F32x2 (&v)[4]) {
-      shrink(v, s.k);
-      F32x2 d[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) d[i] = add2(v[i], both(-s.m));
-      if constexpr (!FULL) clear_beyond(d, c0, n);
-      b = add2(b, tree4(d));
-      a = dot4(d, d, a);
-    });
-    const float2 t = team_sum<W>(low_plus_high(a), low_plus_high(b), room + 2 * W);
-    q = __fdiv_rn(t.x, len);
-    s.c = centered ? __fdiv_rn(t.y, len) : 0.f;
-    if (isfinite(q) || s.k != 1.f) break;
-    s.k = kShrink;
-    // the sums to come use the room again
-    team_barrier<W>();
-  }
+// 1 / sqrt(v) of a normal v: the approximation and one Newton step
+__device__ __forceinline__ float inverse_root(float v) {
+  const float y = rsqrtf(v);
+  return __fmaf_rn(__fmul_rn(0.5f, y), __fmaf_rn(-__fmul_rn(v, y), y, 1.f), y);
+}
+
+// r from the mean square q of k x - m
+__device__ __forceinline__ float row_scale(const RowStats& s, float q, float eps) {
   const float var = fmaxf(__fmaf_rn(-s.c, s.c, q), 0.f);
-  if (!isfinite(q)) s.r = quiet_nan();  // a NaN or an infinity in the row
-  else if (s.k == 1.f) s.r = __frcp_rn(__fsqrt_rn(__fadd_rn(var, eps)));
-  else if (var > 1.17549435e-38f) s.r = __frcp_rn(__fsqrt_rn(var));  // eps is 2^-34 of it at most
-  else s.r = __fmul_rn(__frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(__fmul_rn(var, kGrow), kGrow), eps))), kGrow);
-  return s;
+  if (!isfinite(q)) return quiet_nan();  // a NaN or an infinity in the row
+  if (s.k == 1.f) return inverse_root(__fadd_rn(var, eps));
+  if (var > 1.17549435e-38f) return inverse_root(var);  // eps is 2^-34 of it at most
+  return __fmul_rn(inverse_root(__fadd_rn(__fmul_rn(__fmul_rn(var, kGrow), kGrow), eps)), kGrow);
 }
 
 struct NormArgs {
@@ -112,6 +84,7 @@ struct NormArgs {
   void* y;
   int64_t T, ld, out_ld;
   int32_t H;
+  float inv;     // 1 / H
   bool centered;
   float eps;
   Vector w, b;
@@ -126,76 +99,113 @@ __device__ __forceinline__ void put_stats(const NormArgs& a, int64_t t, const Ro
   if (isnan(s.r) && a.err) atomicOr(a.err, RLK_FLAG_NONFINITE);
 }
 
-// y of a pack, v its k x
-__device__ __forceinline__ void norm_pack(F32x2 (&v)[4], const RowStats& s, const F32x2 (&w)[4], const F32x2 (&b)[4]) {
+// y of a pack, v its k x - m
+template <class E, class O, bool AL>
+__device__ __forceinline__ void put_pack(const NormArgs& a, typename O::bits* y, int c0, F32x2 (&v)[4], const RowStats& s) {
+  F32x2 w[4], b[4];
+  vector8<E, AL>(a.w, c0, a.H, 1.f, w, a.err);
+  vector8<E, AL>(a.b, c0, a.H, 0.f, b, a.err);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const F32x2 d = add2(add2(v[i], both(-s.m)), both(-s.c));
-    v[i] = fma2(mul2(d, both(s.r)), w[i], b[i]);
+    if (a.centered) v[i] = add2(v[i], both(-s.c));
+    v[i] = fma2(mul2(v[i], both(s.r)), w[i], b[i]);
   }
+  store_columns<O, AL>(y, c0, a.H, v, a.err);
 }
 
-// Rows of whole packs, K packs a thread, which stay in registers between the two sums and the
-// result. W warps a row: 8 / W rows a CTA.
+// Rows of whole packs, K packs a thread, which stay in registers (as k x, then k x - m) between the two sums and the result. W
+// warps a row: 8 / W rows a CTA. Bound by the instructions in 16-bit types (about 11 an element), by memory in fp32.
 template <class E, class O, int W, int K>
 __global__ void __launch_bounds__(ROW_CTA) norm_fwd_kernel(const NormArgs a) {
-  __shared__ float rooms[32];
+  __shared__ __align__(16) float rooms[32];
   const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W), packs = a.H / 8;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
   if (t >= a.T) return;  // the whole team
   const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
-  Pack<E> k[K];
-#pragma unroll
-  for (int j = 0; j < K; ++j)
-    if (tid + j * 32 * W < packs) k[j] = load_columns<E, true>(x, 8 * (tid + j * 32 * W), a.H, a.err);
+  float* room = rooms + team * 4 * W;
+  F32x2 v[K][4];
   const auto each = [&](auto f) {
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (tid + j * 32 * W < packs) {
-        F32x2 v[4];
-        unpack(k[j], v);
-        f(8 * (tid + j * 32 * W), v);
-      }
+      if (tid + j * 32 * W < packs) f(v[j], 8 * (tid + j * 32 * W));
   };
-  const RowStats s = row_stats<W, true>(a.H, a.centered, a.eps, rooms + team * 4 * W, each);
+  RowStats s{1.f, 0.f, 0.f, 0.f};
+  float q;
+  for (;;) {
+    each([&](F32x2 (&d)[4], int c0) { unpack(load_columns<E, true>(x, c0, a.H, a.err), d); });
+    if (s.k != 1.f) each([&](F32x2 (&d)[4], int) { shrink(d, s.k); });
+    F32x2 p = 0, b = 0;
+    if (a.centered) {
+      each([&](F32x2 (&d)[4], int) { p = add2(p, tree4(d)); });
+      s.m = __fmul_rn(team_sum<W>(low_plus_high(p), 0.f, room).x, a.inv);
+      p = 0;
+      each([&](F32x2 (&d)[4], int) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = add2(d[i], both(-s.m));
+        b = add2(b, tree4(d));
+      });
+    }
+    each([&](F32x2 (&d)[4], int) { p = dot4(d, d, p); });
+    const float2 sums = team_sum<W>(low_plus_high(p), low_plus_high(b), room + 2 * W);
+    q = __fmul_rn(sums.x, a.inv);
+    s.c = __fmul_rn(sums.y, a.inv);
+    if (isfinite(q) || s.k != 1.f) break;
+    s.k = kShrink;
+    team_barrier<W>();  // the sums to come use the room again
+  }
+  s.r = row_scale(s, q, a.eps);
   if (tid == 0) put_stats(a, t, s);
   auto* y = static_cast<typename O::bits*>(a.y) + t * a.out_ld;
-  each([&](int c0, F32x2 (&v)[4]) {
-    F32x2 w[4], b[4];
-    vector8<E, true>(a.w, c0, a.H, 1.f, w, a.err);
-    vector8<E, true>(a.b, c0, a.H, 0.f, b, a.err);
-    shrink(v, s.k);
-    norm_pack(v, s, w, b);
-    store_columns<O, true>(y, c0, a.H, v, a.err);
-  });
+  each([&](F32x2 (&d)[4], int c0) { put_pack<E, O, true>(a, y, c0, d, s); });
 }
 
-// Any row: it is read three times (from L1 or L2 after the first).
+// Any row, the same sums: it is read three times (from L1 or L2 after the first).
 template <class E, class O, int W>
 __global__ void __launch_bounds__(ROW_CTA) norm_fwd_any_kernel(const NormArgs a) {
-  __shared__ float rooms[32];
+  __shared__ __align__(16) float rooms[32];
   const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W);
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
   if (t >= a.T) return;  // the whole team
   const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
-  auto* y = static_cast<typename O::bits*>(a.y) + t * a.out_ld;
-  const auto each = [&](auto f) {
+  float* room = rooms + team * 4 * W;
+  RowStats s{1.f, 0.f, 0.f, 0.f};
+  const auto each = [&](auto f) {  // k x - m of every pack
     for (int c = 8 * tid; c < a.H; c += 8 * 32 * W) {
       F32x2 v[4];
       unpack(load_columns<E, false>(x, c, a.H, a.err), v);
+      shrink(v, s.k);
+      if (a.centered) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = add2(v[i], both(-s.m));
+      }
       f(c, v);
     }
   };
-  const RowStats s = row_stats<W, false>(a.H, a.centered, a.eps, rooms + team * 4 * W, each);
+  float q;
+  for (;;) {
+    s.m = 0.f;
+    F32x2 p = 0, b = 0;
+    if (a.centered) {
+      each([&](int, F32x2 (&d)[4]) { p = add2(p, tree4(d)); });
+      s.m = __fmul_rn(team_sum<W>(low_plus_high(p), 0.f, room).x, a.inv);
+      p = 0;
+    }
+    each([&](int c0, F32x2 (&d)[4]) {
+      if (c0 + 8 > a.H) clear_beyond(d, c0, a.H);
+      if (a.centered) b = add2(b, tree4(d));
+      p = dot4(d, d, p);
+    });
+    const float2 sums = team_sum<W>(low_plus_high(p), low_plus_high(b), room + 2 * W);
+    q = __fmul_rn(sums.x, a.inv);
+    s.c = __fmul_rn(sums.y, a.inv);
+    if (isfinite(q) || s.k != 1.f) break;
+    s.k = kShrink;
+    team_barrier<W>();
+  }
+  s.r = row_scale(s, q, a.eps);
   if (tid == 0) put_stats(a, t, s);
-  each([&](int c0, F32x2 (&v)[4]) {
-    F32x2 w[4], b[4];
-    vector8<E, false>(a.w, c0, a.H, 1.f, w, a.err);
-    vector8<E, false>(a.b, c0, a.H, 0.f, b, a.err);
-    shrink(v, s.k);
-    norm_pack(v, s, w, b);
-    store_columns<O, false>(y, c0, a.H, v, a.err);
-  });
+  auto* y = static_cast<typename O::bits*>(a.y) + t * a.out_ld;
+  each([&](int c0, F32x2 (&d)[4]) { put_pack<E, O, false>(a, y, c0, d, s); });
 }
 
 // ---------------------------------------------------------------------------
@@ -256,24 +266,27 @@ __device__ __forceinline__ void copies_wait() {
 }
 
 // The packs of one row that a warp's threads own (256 packs apart for the j-th of each), copied into shared memory and read from it
-// by the same warp. Copies go by 16-byte vectors in the order of addresses; `room` holds the first halves of all packs,
-// then (fp32) the second ones, so that neither meets a bank twice.
+// by the same warp. Copies go by 16-byte vectors in the order of addresses, into the same order, but that the two halves of
+// an fp32 pack change places in every other four packs: its reads, 32 bytes apart, then meet no bank twice. (Halves kept apart in
+// two arrays cost the copies: 8192 rows of 4096 in fp32 105 us.)
 template <class E, int K>
 struct RowRing {
   static constexpr int HALVES = sizeof(typename E::bits) * 8 / 16;
+  static __device__ __forceinline__ int place(int vec) { return HALVES == 2 ? vec ^ (vec >> 3 & 1) : vec; }
   static __device__ __forceinline__ void fetch(uint4* room, const void* row, int warp, int lane, int packs, bool ok) {
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
       for (int i = 0; i < HALVES; ++i) {
         const int u = i * 32 + lane, p = warp * 32 + j * 256 + u / HALVES;  // vector u of the warp's 32 HALVES
-        if (p < packs && ok) copy_async_16(room + (u % HALVES) * packs + p, static_cast<const uint4*>(row) + p * HALVES + u % HALVES);
+        const int at = p * HALVES + u % HALVES;
+        if (p < packs && ok) copy_async_16(room + place(at), static_cast<const uint4*>(row) + at);
       }
   }
-  static __device__ __forceinline__ void read(const uint4* room, int p, int packs, F32x2 (&v)[4]) {
+  static __device__ __forceinline__ void read(const uint4* room, int p, F32x2 (&v)[4]) {
     Pack<E> k;
 #pragma unroll
-    for (int i = 0; i < HALVES; ++i) ld_vec(k.w + 4 * i, room + i * packs + p);
+    for (int i = 0; i < HALVES; ++i) ld_vec(k.w + 4 * i, room + place(p * HALVES + i));
     unpack(k, v);
   }
 };
@@ -283,7 +296,7 @@ struct RowRing {
 template <class E, class O, int W, int K>
 __global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const NormGradArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
-  __shared__ float rooms[32];
+  __shared__ __align__(16) float rooms[32];
   constexpr int XH = RowRing<E, K>::HALVES, DH = RowRing<O, K>::HALVES;
   const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W), warp = tid >> 5, lane = tid & 31, packs = a.H / 8;
   const int64_t strip = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
@@ -315,7 +328,8 @@ __global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const
     fetch(t + static_cast<int64_t>(a.stages - 1) * a.strips, stage == 0 ? a.stages - 1 : stage - 1);
     const int64_t next = t + a.strips < a.T ? t + a.strips : t;
     const float m1 = a.mean ? a.mean[next] : 0.f, r1 = a.rstd[next];
-    if (a.stages == 3) copies_wait<2>();
+    if (a.stages == 2) copies_wait<1>();
+    else if (a.stages == 3) copies_wait<2>();
     else copies_wait<3>();
     __syncwarp();
     const uint4* xs = ring + stage * stage_vecs;
@@ -323,8 +337,8 @@ __global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const
 #pragma unroll
     for (int j = 0; j < K; ++j)
       if (tid + j * 256 < packs) {
-        RowRing<E, K>::read(xs, tid + j * 256, packs, h[j]);
-        RowRing<O, K>::read(xs + packs * XH, tid + j * 256, packs, dy[j]);
+        RowRing<E, K>::read(xs, tid + j * 256, h[j]);
+        RowRing<O, K>::read(xs + packs * XH, tid + j * 256, dy[j]);
         norm_h(h[j], m, r);
         norm_vectors(h[j], dy[j], sw[j], sb[j]);
         norm_sums(h[j], dy[j], w[j], s1, s2);
@@ -360,7 +374,7 @@ __global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const
 // Any rows: first what the whole row gives, then the columns.
 template <class E, class O>
 __global__ void __launch_bounds__(ROW_CTA) norm_bwd_rows_kernel(const NormGradArgs a) {
-  __shared__ float room[16];
+  __shared__ __align__(16) float room[16];
   const int64_t t = blockIdx.x;
   const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
   const auto* dy = static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld;
@@ -498,7 +512,7 @@ rlk_status rlk_layer_norm_fwd(const void* x, int32_t dtype, int64_t T, int64_t H
   if (!same_rows(in, out) && !rows_apart(in, out)) return RLK_ERR_INVALID_ARG;
   if (T == 0) return RLK_OK;
   const bool f32 = weight_dtype == RLK_DTYPE_F32;
-  const NormArgs a{x, y, T, ld, out_ld, static_cast<int32_t>(H), centered != 0, static_cast<float>(eps),
+  const NormArgs a{x, y, T, ld, out_ld, static_cast<int32_t>(H), 1.f / static_cast<float>(H), centered != 0, static_cast<float>(eps),
                    Vector{weight, f32}, Vector{bias, f32}, mean, rstd, err_flag};
   const bool kept = H <= FWD_KEPT && whole_packs(x, T, H, ld, in.eb) && whole_packs(y, T, H, out_ld, out.eb) &&
                     on_boundary(weight, 32) && on_boundary(bias, 32);

@@ -118,7 +118,7 @@ __device__ __forceinline__ float low_plus_high(F32x2 v) {
 }
 
 // Sums of two values over the slots of a row that W warps (a team, one of 8 / W of a CTA of 256) hold, in the fixed
-// order; every thread of the team gets both. `room`: 2 W floats of shared memory of the team's own, which the call
+// order; every thread of the team gets both. `room`: 2 W floats of shared memory of the team's own (16-byte aligned), which the call
 // after this one does not use (one barrier a call then does).
 template <int W>
 __device__ __forceinline__ void team_barrier();
@@ -133,8 +133,16 @@ __device__ __forceinline__ float2 team_sum(float a, float b, float* room) {
   if ((lane & 15) == 0) room[(low ? 0 : W) + warp] = v;
   team_barrier<W>();
   float x[2 * W];
+  if constexpr (W >= 4) {
 #pragma unroll
-  for (int i = 0; i < 2 * W; ++i) x[i] = room[i];
+    for (int i = 0; i < 2 * W; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(room + i);
+      x[i] = q.x, x[i + 1] = q.y, x[i + 2] = q.z, x[i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i) x[i] = room[i];
+  }
 #pragma unroll
   for (int d = 1; d < W; d *= 2)
 #pragma unroll

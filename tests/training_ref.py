@@ -85,7 +85,7 @@ def norm(x, w, b, eps, centered):
     w = torch.ones(H, dtype=torch.float64, device=x.device) if w is None else w.double()
     b = torch.zeros(H, dtype=torch.float64, device=x.device) if b is None else b.double()
     y = d * r * w + b
-    D, size = depth(H, True) + 4, d.abs().mean(1, keepdim=True)
+    D, size = depth(H, True) + 5, d.abs().mean(1, keepdim=True)
     # x - m and the correction c: three roundings; c itself is a sum of differences over H. Before the correction the
     # mean is off by depth roundings of mean |x|, which the sum of differences sees in full and the square of which leaves
     # the variance to second order
