@@ -15,9 +15,9 @@ namespace rlk {
 namespace {
 
 
-// Warps that take a row, in the backward: few packs a thread, whose sums of dw and db it keeps. (The forward has up to 4 packs a
-// thread before another warp, since a row's two sums and its few scalars cost every warp the same: with_fwd_team.)
-__host__ __device__ constexpr int bwd_warps(int n) { return n <= 256 ? 1 : n <= 512 ? 2 : n <= 1024 ? 4 : 8; }
+// Warps that take a row in the backward. A row's two sums and its few scalars cost every warp the same, so a thread has 2 packs,
+// whose sums of dw and db it keeps, before another warp has any (in the forward 4: with_fwd_team).
+__host__ __device__ constexpr int bwd_warps(int n) { return n <= 512 ? 1 : n <= 1024 ? 2 : n <= 2048 ? 4 : 8; }
 
 // Rows are dealt to strips, whose parts of dw and db are summed apart: row t belongs to strip t mod S. S follows
 // from T and the width alone, and so does the order of the sum over rows: two CTAs on each of 152 SMs,
@@ -99,9 +99,21 @@ __device__ __forceinline__ void put_stats(const NormArgs& a, int64_t t, const Ro
   if (isnan(s.r) && a.err) atomicOr(a.err, RLK_FLAG_NONFINITE);
 }
 
+// A row of n results by way of shared memory, for rows of any alignment: packs are put there as they come, then the team's W
+// warps write them out in the order of addresses. (Element by element from the packs, every store touches as many sectors as
+// the pack's eight together.) `stage`: n elements rounded up to a pack; a team barrier stands before its next use.
+template <class O, int W>
+__device__ __forceinline__ void write_out(typename O::bits* out, const typename O::bits* stage, int n, int tid, int32_t* err) {
+  team_barrier<W>();
+  if constexpr (W == 1) __syncwarp();
+#pragma unroll 8
+  for (int c = tid; c < n; c += 32 * W)
+    if (dbg_ok(c >= 0 && c < n, err)) out[c] = stage[c];
+}
+
 // y of a pack, v its k x - m
-template <class E, class O, bool AL>
-__device__ __forceinline__ void put_pack(const NormArgs& a, typename O::bits* y, int c0, F32x2 (&v)[4], const RowStats& s) {
+template <class E, bool AL>
+__device__ __forceinline__ void norm_pack(const NormArgs& a, int c0, F32x2 (&v)[4], const RowStats& s) {
   F32x2 w[4], b[4];
   vector8<E, AL>(a.w, c0, a.H, 1.f, w, a.err);
   vector8<E, AL>(a.b, c0, a.H, 0.f, b, a.err);
@@ -110,15 +122,15 @@ __device__ __forceinline__ void put_pack(const NormArgs& a, typename O::bits* y,
     if (a.centered) v[i] = add2(v[i], both(-s.c));
     v[i] = fma2(mul2(v[i], both(s.r)), w[i], b[i]);
   }
-  store_columns<O, AL>(y, c0, a.H, v, a.err);
 }
 
-// Rows of whole packs, K packs a thread, which stay in registers (as k x, then k x - m) between the two sums and the result. W
-// warps a row: 8 / W rows a CTA. Bound by the instructions in 16-bit types (about 11 an element), by memory in fp32.
-template <class E, class O, int W, int K>
+// Rows of up to 16384 columns, K packs a thread, which stay in registers (as k x, then k x - m) between the two sums and the
+// result. W warps a row: 8 / W rows a CTA. Bound by the instructions in 16-bit types, by memory in fp32.
+template <class E, class O, int W, int K, bool AL>
 __global__ void __launch_bounds__(ROW_CTA) norm_fwd_kernel(const NormArgs a) {
+  extern __shared__ __align__(16) unsigned char dyn[];  // stages (write_out), unless AL
   __shared__ __align__(16) float rooms[32];
-  const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W), packs = a.H / 8;
+  const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W), packs = (a.H + 7) / 8;
   const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
   if (t >= a.T) return;  // the whole team
   const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
@@ -132,16 +144,17 @@ __global__ void __launch_bounds__(ROW_CTA) norm_fwd_kernel(const NormArgs a) {
   RowStats s{1.f, 0.f, 0.f, 0.f};
   float q;
   for (;;) {
-    each([&](F32x2 (&d)[4], int c0) { unpack(load_columns<E, true>(x, c0, a.H, a.err), d); });
+    each([&](F32x2 (&d)[4], int c0) { unpack(load_columns<E, AL>(x, c0, a.H, a.err), d); });
     if (s.k != 1.f) each([&](F32x2 (&d)[4], int) { shrink(d, s.k); });
     F32x2 p = 0, b = 0;
     if (a.centered) {
       each([&](F32x2 (&d)[4], int) { p = add2(p, tree4(d)); });
       s.m = __fmul_rn(team_sum<W>(low_plus_high(p), 0.f, room).x, a.inv);
       p = 0;
-      each([&](F32x2 (&d)[4], int) {
+      each([&](F32x2 (&d)[4], int c0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[i] = add2(d[i], both(-s.m));
+        if (!AL && c0 + 8 > a.H) clear_beyond(d, c0, a.H);
         b = add2(b, tree4(d));
       });
     }
@@ -156,18 +169,24 @@ __global__ void __launch_bounds__(ROW_CTA) norm_fwd_kernel(const NormArgs a) {
   s.r = row_scale(s, q, a.eps);
   if (tid == 0) put_stats(a, t, s);
   auto* y = static_cast<typename O::bits*>(a.y) + t * a.out_ld;
-  each([&](F32x2 (&d)[4], int c0) { put_pack<E, O, true>(a, y, c0, d, s); });
+  auto* stage = reinterpret_cast<typename O::bits*>(dyn) + team * 8 * packs;
+  each([&](F32x2 (&d)[4], int c0) {
+    norm_pack<E, AL>(a, c0, d, s);
+    if constexpr (AL) store_columns<O, true>(y, c0, a.H, d, a.err);
+    else store_columns<O, true, false>(stage, c0, 8 * packs, d, a.err);
+  });
+  if constexpr (!AL) write_out<O, W>(y, stage, a.H, tid, a.err);
 }
 
-// Any row, the same sums: it is read three times (from L1 or L2 after the first).
-template <class E, class O, int W>
-__global__ void __launch_bounds__(ROW_CTA) norm_fwd_any_kernel(const NormArgs a) {
+// Longer rows, by 8 warps: they are read three times (from L1 or L2 after the first).
+template <class E, class O>
+__global__ void __launch_bounds__(ROW_CTA) norm_fwd_long_kernel(const NormArgs a) {
   __shared__ __align__(16) float rooms[32];
-  const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W);
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
-  if (t >= a.T) return;  // the whole team
+  constexpr int W = 8;
+  const int tid = threadIdx.x;
+  const int64_t t = blockIdx.x;
   const auto* x = static_cast<const typename E::bits*>(a.x) + t * a.ld;
-  float* room = rooms + team * 4 * W;
+  float* room = rooms;
   RowStats s{1.f, 0.f, 0.f, 0.f};
   const auto each = [&](auto f) {  // k x - m of every pack
     for (int c = 8 * tid; c < a.H; c += 8 * 32 * W) {
@@ -205,7 +224,10 @@ __global__ void __launch_bounds__(ROW_CTA) norm_fwd_any_kernel(const NormArgs a)
   s.r = row_scale(s, q, a.eps);
   if (tid == 0) put_stats(a, t, s);
   auto* y = static_cast<typename O::bits*>(a.y) + t * a.out_ld;
-  each([&](int c0, F32x2 (&d)[4]) { put_pack<E, O, false>(a, y, c0, d, s); });
+  each([&](int c0, F32x2 (&d)[4]) {
+    norm_pack<E, false>(a, c0, d, s);
+    store_columns<O, false>(y, c0, a.H, d, a.err);
+  });
 }
 
 // ---------------------------------------------------------------------------
@@ -216,6 +238,7 @@ struct NormGradArgs {
   void* dx;
   int64_t T, dy_ld, ld, dx_ld;
   int32_t H;
+  float inv;               // 1 / H
   Vector w;
   const float *mean, *rstd;
   float* row;              // [T][2]: mean g, mean(g h)
@@ -231,12 +254,13 @@ __device__ __forceinline__ void norm_h(F32x2 (&x)[4], float m, float r) {
   for (int i = 0; i < 4; ++i) x[i] = mul2(add2(x[i], both(-m)), both(r));
 }
 
-// the pack's part of sum g and sum g h
-__device__ __forceinline__ void norm_sums(const F32x2 (&h)[4], const F32x2 (&dy)[4], const F32x2 (&w)[4], F32x2& s1, F32x2& s2) {
+// the pack's part of sum g (where the mean counts) and sum g h
+__device__ __forceinline__ void norm_sums(const F32x2 (&h)[4], const F32x2 (&dy)[4], const F32x2 (&w)[4], bool centered, F32x2& s1,
+                                          F32x2& s2) {
   F32x2 g[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) g[i] = mul2(dy[i], w[i]);
-  s1 = dot4(dy, w, s1);
+  if (centered) s1 = dot4(dy, w, s1);
   s2 = dot4(g, h, s2);
 }
 
@@ -247,13 +271,13 @@ __device__ __forceinline__ void norm_dx(const F32x2 (&h)[4], const F32x2 (&dy)[4
   for (int i = 0; i < 4; ++i) dx[i] = mul2(fma2(h[i], both(-c2), fma2(dy[i], w[i], both(-c1))), both(r));
 }
 
-// the pack's part of dw and db
-__device__ __forceinline__ void norm_vectors(const F32x2 (&h)[4], const F32x2 (&dy)[4], F32x2 (&sw)[4], F32x2 (&sb)[4]) {
+// the pack's part of dw and, where it is wanted, db
+__device__ __forceinline__ void norm_vectors(const F32x2 (&h)[4], const F32x2 (&dy)[4], bool bias, F32x2 (&sw)[4], F32x2 (&sb)[4]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    sw[i] = fma2(dy[i], h[i], sw[i]);
-    sb[i] = add2(sb[i], dy[i]);
-  }
+  for (int i = 0; i < 4; ++i) sw[i] = fma2(dy[i], h[i], sw[i]);
+  if (!bias) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sb[i] = add2(sb[i], dy[i]);
 }
 
 __device__ __forceinline__ void copy_async_16(void* shared, const void* global) {
@@ -265,11 +289,11 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// The packs of one row that a warp's threads own (256 packs apart for the j-th of each), copied into shared memory and read from it
+// The packs of one row that a warp's threads own (32 W packs apart for the j-th of each), copied into shared memory and read from it
 // by the same warp. Copies go by 16-byte vectors in the order of addresses, into the same order, but that the two halves of
 // an fp32 pack change places in every other four packs: its reads, 32 bytes apart, then meet no bank twice. (Halves kept apart in
 // two arrays cost the copies: 8192 rows of 4096 in fp32 105 us.)
-template <class E, int K>
+template <class E, int W, int K>
 struct RowRing {
   static constexpr int HALVES = sizeof(typename E::bits) * 8 / 16;
   static __device__ __forceinline__ int place(int vec) { return HALVES == 2 ? vec ^ (vec >> 3 & 1) : vec; }
@@ -278,7 +302,7 @@ struct RowRing {
     for (int j = 0; j < K; ++j)
 #pragma unroll
       for (int i = 0; i < HALVES; ++i) {
-        const int u = i * 32 + lane, p = warp * 32 + j * 256 + u / HALVES;  // vector u of the warp's 32 HALVES
+        const int u = i * 32 + lane, p = warp * 32 + j * 32 * W + u / HALVES;  // vector u of the warp's 32 HALVES
         const int at = p * HALVES + u % HALVES;
         if (p < packs && ok) copy_async_16(room + place(at), static_cast<const uint4*>(row) + at);
       }
@@ -291,69 +315,89 @@ struct RowRing {
   }
 };
 
-// Rows of whole packs, up to 8192 columns. A team of W warps takes a strip's rows in turn; the next
-// stages - 1 rows are on their way into shared memory meanwhile. Each thread keeps the sums of dw and db of its columns.
-template <class E, class O, int W, int K>
+// Rows of up to 8192 columns. A team of W warps takes a strip's rows in turn; the next stages - 1 rows are on their way into
+// shared memory meanwhile (unless they are misaligned). Each thread keeps the sums of dw and db of its columns.
+template <class E, class O, int W, int K, bool AL>
 __global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const NormGradArgs a) {
-  extern __shared__ __align__(16) unsigned char dyn[];
+  extern __shared__ __align__(16) unsigned char dyn[];  // AL: the rows to come; else stages (write_out)
   __shared__ __align__(16) float rooms[32];
-  constexpr int XH = RowRing<E, K>::HALVES, DH = RowRing<O, K>::HALVES;
-  const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W), warp = tid >> 5, lane = tid & 31, packs = a.H / 8;
+  using XRing = RowRing<E, W, K>;
+  using DRing = RowRing<O, W, K>;
+  constexpr int XH = XRing::HALVES, DH = DRing::HALVES;
+  const int team = threadIdx.x / (32 * W), tid = threadIdx.x % (32 * W), warp = tid >> 5, lane = tid & 31, packs = (a.H + 7) / 8;
   const int64_t strip = static_cast<int64_t>(blockIdx.x) * (8 / W) + team;
   if (strip >= a.strips) return;  // the whole team
   const int stage_vecs = packs * (XH + DH);
   uint4* ring = reinterpret_cast<uint4*>(dyn) + static_cast<int64_t>(team) * a.stages * stage_vecs;
+  auto* staged = reinterpret_cast<typename E::bits*>(dyn) + team * 8 * packs;
   float* room = rooms + team * 4 * W;
+  const auto x_row = [&](int64_t t) { return static_cast<const typename E::bits*>(a.x) + t * a.ld; };
+  const auto dy_row = [&](int64_t t) { return static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld; };
   const auto fetch = [&](int64_t t, int stage) {
-    const bool ok = t < a.T;
-    uint4* to = ring + stage * stage_vecs;
-    RowRing<E, K>::fetch(to, static_cast<const typename E::bits*>(a.x) + t * a.ld, warp, lane, packs, ok);
-    RowRing<O, K>::fetch(to + packs * XH, static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld, warp, lane, packs, ok);
-    copies_commit();
+    if constexpr (AL) {
+      uint4* to = ring + stage * stage_vecs;
+      XRing::fetch(to, x_row(t), warp, lane, packs, t < a.T);
+      DRing::fetch(to + packs * XH, dy_row(t), warp, lane, packs, t < a.T);
+      copies_commit();
+    }
   };
   for (int i = 0; i < a.stages - 1; ++i) fetch(strip + static_cast<int64_t>(i) * a.strips, i);
   F32x2 w[K][4], sw[K][4], sb[K][4];
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    const int c0 = 8 * (tid + j * 256);
-    if (c0 < a.H) vector8<E, true>(a.w, c0, a.H, 1.f, w[j], a.err);
+    const int c0 = 8 * (tid + j * 32 * W);
+    if (c0 < a.H) vector8<E, AL>(a.w, c0, a.H, 1.f, w[j], a.err);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sw[j][i] = sb[j][i] = 0;
   }
-  const float len = static_cast<float>(a.H);
-  float m = a.mean ? a.mean[strip] : 0.f, r = a.rstd[strip];
+  const bool centered = a.mean, bias = a.part_b;
+  float m = centered ? a.mean[strip] : 0.f, r = a.rstd[strip];
   int stage = 0, odd = 0;
   for (int64_t t = strip; t < a.T; t += a.strips) {
-    __syncwarp();  // the stage that is filled next has been read by the whole warp
+    if constexpr (AL) __syncwarp();  // the stage that is filled next has been read by the whole warp
     fetch(t + static_cast<int64_t>(a.stages - 1) * a.strips, stage == 0 ? a.stages - 1 : stage - 1);
     const int64_t next = t + a.strips < a.T ? t + a.strips : t;
-    const float m1 = a.mean ? a.mean[next] : 0.f, r1 = a.rstd[next];
-    if (a.stages == 2) copies_wait<1>();
-    else if (a.stages == 3) copies_wait<2>();
-    else copies_wait<3>();
-    __syncwarp();
-    const uint4* xs = ring + stage * stage_vecs;
+    const float m1 = centered ? a.mean[next] : 0.f, r1 = a.rstd[next];
     F32x2 h[K][4], dy[K][4], s1 = 0, s2 = 0;
+    if constexpr (AL) {
+      if (a.stages == 3) copies_wait<2>();
+      else copies_wait<3>();
+      __syncwarp();
+    }
+    const uint4* xs = ring + stage * stage_vecs;
 #pragma unroll
     for (int j = 0; j < K; ++j)
-      if (tid + j * 256 < packs) {
-        RowRing<E, K>::read(xs, tid + j * 256, h[j]);
-        RowRing<O, K>::read(xs + packs * XH, tid + j * 256, dy[j]);
+      if (const int p = tid + j * 32 * W; p < packs) {
+        if constexpr (AL) {
+          XRing::read(xs, p, h[j]);
+          DRing::read(xs + packs * XH, p, dy[j]);
+        } else {
+          unpack(load_columns<E, false>(x_row(t), 8 * p, a.H, a.err), h[j]);
+          unpack(load_columns<O, false>(dy_row(t), 8 * p, a.H, a.err), dy[j]);
+        }
+      }
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (const int p = tid + j * 32 * W; p < packs) {
         norm_h(h[j], m, r);
-        norm_vectors(h[j], dy[j], sw[j], sb[j]);
-        norm_sums(h[j], dy[j], w[j], s1, s2);
+        if (!AL && 8 * p + 8 > a.H) clear_beyond(h[j], 8 * p, a.H);
+        norm_vectors(h[j], dy[j], bias, sw[j], sb[j]);
+        norm_sums(h[j], dy[j], w[j], centered, s1, s2);
       }
     if (a.dx) {
       const float2 s = team_sum<W>(low_plus_high(s1), low_plus_high(s2), room + odd * 2 * W);
-      const float c1 = a.mean ? __fdiv_rn(s.x, len) : 0.f, c2 = __fdiv_rn(s.y, len);
+      const float c1 = __fmul_rn(s.x, a.inv), c2 = __fmul_rn(s.y, a.inv);
       auto* dx = static_cast<typename E::bits*>(a.dx) + t * a.dx_ld;
 #pragma unroll
       for (int j = 0; j < K; ++j)
-        if (tid + j * 256 < packs) {
+        if (const int p = tid + j * 32 * W; p < packs) {
           F32x2 v[4];
           norm_dx(h[j], dy[j], w[j], c1, c2, r, v);
-          store_columns<E, true>(dx, 8 * (tid + j * 256), a.H, v, a.err);
+          if constexpr (AL) store_columns<E, true>(dx, 8 * p, a.H, v, a.err);
+          else store_columns<E, true, false>(staged, 8 * p, 8 * packs, v, a.err);
         }
+      if constexpr (!AL) write_out<E, W>(dx, staged, a.H, tid, a.err);  // the next row's sum stands before the next stage's packs
+      if constexpr (!AL && W == 1) __syncwarp();
     }
     m = m1;
     r = r1;
@@ -361,18 +405,18 @@ __global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const
     stage = stage + 1 == a.stages ? 0 : stage + 1;
   }
   griddep_launch_dependents();
-  copies_wait<0>();
+  if constexpr (AL) copies_wait<0>();
 #pragma unroll
   for (int j = 0; j < K; ++j) {
-    const int c0 = 8 * (tid + j * 256);
+    const int c0 = 8 * (tid + j * 32 * W);
     if (c0 >= a.H) continue;
-    if (a.part_w) store_columns<F32, true>(reinterpret_cast<uint32_t*>(a.part_w) + strip * a.H, c0, a.H, sw[j], a.err);
-    if (a.part_b) store_columns<F32, true>(reinterpret_cast<uint32_t*>(a.part_b) + strip * a.H, c0, a.H, sb[j], a.err);
+    if (a.part_w) store_columns<F32, AL>(reinterpret_cast<uint32_t*>(a.part_w) + strip * a.H, c0, a.H, sw[j], a.err);
+    if (a.part_b) store_columns<F32, AL>(reinterpret_cast<uint32_t*>(a.part_b) + strip * a.H, c0, a.H, sb[j], a.err);
   }
 }
 
-// Any rows: first what the whole row gives, then the columns.
-template <class E, class O>
+// Longer rows: first what the whole row gives (8 warps), then the columns.
+template <class E, class O, bool AL>
 __global__ void __launch_bounds__(ROW_CTA) norm_bwd_rows_kernel(const NormGradArgs a) {
   __shared__ __align__(16) float room[16];
   const int64_t t = blockIdx.x;
@@ -380,43 +424,44 @@ __global__ void __launch_bounds__(ROW_CTA) norm_bwd_rows_kernel(const NormGradAr
   const auto* dy = static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld;
   const float m = a.mean ? a.mean[t] : 0.f, r = a.rstd[t];
   F32x2 s1 = 0, s2 = 0;
-  for (int c = 8 * threadIdx.x; c < a.H; c += 8 * 256) {
+#pragma unroll 2
+  for (int c = 8 * threadIdx.x; c < a.H; c += 8 * ROW_CTA) {
     F32x2 h[4], dv[4], w[4];
-    unpack(load_columns<E, false>(x, c, a.H, a.err), h);
-    unpack(load_columns<O, false>(dy, c, a.H, a.err), dv);
-    vector8<E, false>(a.w, c, a.H, 1.f, w, a.err);
+    unpack(load_columns<E, AL>(x, c, a.H, a.err), h);
+    unpack(load_columns<O, AL>(dy, c, a.H, a.err), dv);
+    vector8<E, AL>(a.w, c, a.H, 1.f, w, a.err);
     norm_h(h, m, r);
-    clear_beyond(h, c, a.H);
-    norm_sums(h, dv, w, s1, s2);
+    if (!AL && c + 8 > a.H) clear_beyond(h, c, a.H);
+    norm_sums(h, dv, w, a.mean, s1, s2);
   }
   const float2 s = team_sum<8>(low_plus_high(s1), low_plus_high(s2), room);
   if (threadIdx.x == 0) {
-    const float len = static_cast<float>(a.H);
-    a.row[2 * t] = a.mean ? __fdiv_rn(s.x, len) : 0.f;
-    a.row[2 * t + 1] = __fdiv_rn(s.y, len);
+    a.row[2 * t] = __fmul_rn(s.x, a.inv);
+    a.row[2 * t + 1] = __fmul_rn(s.y, a.inv);
   }
 }
 
-template <class E, class O>
+template <class E, class O, bool AL>
 __global__ void __launch_bounds__(ROW_CTA) norm_bwd_columns_kernel(const NormGradArgs a) {
   const int c0 = 8 * static_cast<int>(blockIdx.x * ROW_CTA + threadIdx.x);
   if (c0 >= a.H) return;
   F32x2 w[4], sw[4] = {}, sb[4] = {};
-  vector8<E, false>(a.w, c0, a.H, 1.f, w, a.err);
+  vector8<E, AL>(a.w, c0, a.H, 1.f, w, a.err);
+#pragma unroll 2
   for (int64_t t = blockIdx.y; t < a.T; t += a.strips) {
     F32x2 h[4], dv[4], v[4];
-    unpack(load_columns<E, false>(static_cast<const typename E::bits*>(a.x) + t * a.ld, c0, a.H, a.err), h);
-    unpack(load_columns<O, false>(static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld, c0, a.H, a.err), dv);
+    unpack(load_columns<E, AL>(static_cast<const typename E::bits*>(a.x) + t * a.ld, c0, a.H, a.err), h);
+    unpack(load_columns<O, AL>(static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld, c0, a.H, a.err), dv);
     const float m = a.mean ? a.mean[t] : 0.f, r = a.rstd[t];
     norm_h(h, m, r);
-    norm_vectors(h, dv, sw, sb);
+    norm_vectors(h, dv, a.part_b, sw, sb);
     if (!a.dx) continue;
     norm_dx(h, dv, w, a.row[2 * t], a.row[2 * t + 1], r, v);
-    store_columns<E, false>(static_cast<typename E::bits*>(a.dx) + t * a.dx_ld, c0, a.H, v, a.err);
+    store_columns<E, AL>(static_cast<typename E::bits*>(a.dx) + t * a.dx_ld, c0, a.H, v, a.err);
   }
   const int64_t at = static_cast<int64_t>(blockIdx.y) * a.H;
-  if (a.part_w) store_columns<F32, false>(reinterpret_cast<uint32_t*>(a.part_w) + at, c0, a.H, sw, a.err);
-  if (a.part_b) store_columns<F32, false>(reinterpret_cast<uint32_t*>(a.part_b) + at, c0, a.H, sb, a.err);
+  if (a.part_w) store_columns<F32, AL>(reinterpret_cast<uint32_t*>(a.part_w) + at, c0, a.H, sw, a.err);
+  if (a.part_b) store_columns<F32, AL>(reinterpret_cast<uint32_t*>(a.part_b) + at, c0, a.H, sb, a.err);
 }
 
 // dw and db from the strips' parts: warp i adds strips i, i + 32, ... in ascending order, then the 32 sums are added as a
@@ -454,8 +499,8 @@ template <class F>
 inline rlk_status with_fwd_team(int64_t H, F f) {
   if (H <= 256) return f(Int<1>{}, Int<1>{});
   if (H <= 512) return f(Int<1>{}, Int<2>{});
-  if (H <= 1024) return f(Int<2>{}, Int<2>{});
-  if (H <= 2048) return f(Int<4>{}, Int<2>{});
+  if (H <= 1024) return f(Int<1>{}, Int<4>{});
+  if (H <= 2048) return f(Int<2>{}, Int<4>{});
   if (H <= 4096) return f(Int<4>{}, Int<4>{});
   if (H <= 8192) return f(Int<8>{}, Int<4>{});
   return f(Int<8>{}, Int<8>{});
@@ -463,9 +508,9 @@ inline rlk_status with_fwd_team(int64_t H, F f) {
 template <class F>
 inline rlk_status with_bwd_team(int64_t H, F f) {
   if (H <= 256) return f(Int<1>{}, Int<1>{});
-  if (H <= 512) return f(Int<2>{}, Int<1>{});
-  if (H <= 1024) return f(Int<4>{}, Int<1>{});
-  if (H <= 2048) return f(Int<8>{}, Int<1>{});
+  if (H <= 512) return f(Int<1>{}, Int<2>{});
+  if (H <= 1024) return f(Int<2>{}, Int<2>{});
+  if (H <= 2048) return f(Int<4>{}, Int<2>{});
   if (H <= 4096) return f(Int<8>{}, Int<2>{});
   return f(Int<8>{}, Int<4>{});
 }
@@ -474,21 +519,36 @@ constexpr int64_t FWD_KEPT = 16384;  // columns of a row that stays in registers
 constexpr int64_t BWD_KEPT = 8192;   // and of one whose sums of dw and db do (4 packs)
 constexpr int BWD_SMEM = 110 * 1024;      // of each of the two CTAs of an SM
 constexpr int BWD_SMEM_ONE = 220 * 1024;  // of its only one
+constexpr int FWD_SMEM = static_cast<int>(FWD_KEPT * sizeof(float));
+
+// Launches a kernel whose dynamic shared memory may be up to `most` bytes.
+template <auto Kernel, class A>
+inline rlk_status launch_rows_of(const A& a, int64_t ctas, int64_t smem, int most, cudaStream_t s) {
+  static OncePerDevice allowed;
+  if (!allowed([&] { return cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) == cudaSuccess; }))
+    return RLK_ERR_CUDA;
+  Kernel<<<static_cast<unsigned>(ctas), ROW_CTA, static_cast<size_t>(smem), s>>>(a);
+  return launched();
+}
 
 template <class E, class O, int W, int K>
-inline rlk_status launch_norm_bwd(NormGradArgs a, int64_t stage_bytes, cudaStream_t s) {
-  // 4 stages, or as many as the CTAs of an SM (two of up to 2 packs a thread, by registers) have room for
-  const int64_t cta = stage_bytes * (8 / W), n = (K <= 2 ? BWD_SMEM : BWD_SMEM_ONE) / cta;
-  a.stages = static_cast<int32_t>(n > 4 ? 4 : n);  // 3 at least
-  const size_t smem = static_cast<size_t>(cta * a.stages);
-  const auto kernel = norm_bwd_kernel<E, O, W, K>;
-  static OncePerDevice allowed;
-  if (!allowed([&] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, K <= 2 ? BWD_SMEM : BWD_SMEM_ONE) == cudaSuccess;
-      }))
-    return RLK_ERR_CUDA;
-  kernel<<<static_cast<unsigned>((a.strips + 8 / W - 1) / (8 / W)), ROW_CTA, smem, s>>>(a);
-  return launched();
+inline rlk_status launch_norm_fwd(const NormArgs& a, bool aligned, cudaStream_t s) {
+  const int64_t ctas = (a.T + 8 / W - 1) / (8 / W);
+  if (aligned) return launch_rows_of<norm_fwd_kernel<E, O, W, K, true>>(a, ctas, 0, FWD_SMEM, s);
+  const int64_t stages = static_cast<int64_t>(8 / W) * ((a.H + 7) / 8 * 8) * sizeof(typename O::bits);
+  return launch_rows_of<norm_fwd_kernel<E, O, W, K, false>>(a, ctas, stages, FWD_SMEM, s);
+}
+
+template <class E, class O, int W, int K>
+inline rlk_status launch_norm_bwd(NormGradArgs a, bool aligned, cudaStream_t s) {
+  constexpr int most = K <= 2 ? BWD_SMEM : BWD_SMEM_ONE;
+  const int64_t ctas = (a.strips + 8 / W - 1) / (8 / W), columns = static_cast<int64_t>(8 / W) * ((a.H + 7) / 8 * 8);
+  a.stages = 1;
+  if (!aligned) return launch_rows_of<norm_bwd_kernel<E, O, W, K, false>>(a, ctas, columns * sizeof(typename E::bits), most, s);
+  // 4 stages, or as many as the CTAs of an SM (two of up to 2 packs a thread, by registers) have room for: 3 at least
+  const int64_t stage = columns * (sizeof(typename E::bits) + sizeof(typename O::bits));
+  a.stages = static_cast<int32_t>(most / stage > 4 ? 4 : most / stage);
+  return launch_rows_of<norm_bwd_kernel<E, O, W, K, true>>(a, ctas, a.stages * stage, most, s);
 }
 
 }  // namespace
@@ -514,18 +574,17 @@ rlk_status rlk_layer_norm_fwd(const void* x, int32_t dtype, int64_t T, int64_t H
   const bool f32 = weight_dtype == RLK_DTYPE_F32;
   const NormArgs a{x, y, T, ld, out_ld, static_cast<int32_t>(H), 1.f / static_cast<float>(H), centered != 0, static_cast<float>(eps),
                    Vector{weight, f32}, Vector{bias, f32}, mean, rstd, err_flag};
-  const bool kept = H <= FWD_KEPT && whole_packs(x, T, H, ld, in.eb) && whole_packs(y, T, H, out_ld, out.eb) &&
-                    on_boundary(weight, 32) && on_boundary(bias, 32);
+  const bool al = whole_packs(x, T, H, ld, in.eb) && whole_packs(y, T, H, out_ld, out.eb) && on_boundary(weight, 32) &&
+                  on_boundary(bias, 32);
   const auto s = static_cast<cudaStream_t>(stream);
   return with_pair(dtype, out_dtype, [&](auto e, auto o) {
     using E = decltype(e);
     using O = decltype(o);
-    return with_fwd_team(H, [&](auto w, auto k) {
-      constexpr int W = decltype(w)::value, K = decltype(k)::value;
-      const auto kernel = kept ? norm_fwd_kernel<E, O, W, K> : norm_fwd_any_kernel<E, O, W>;
-      kernel<<<static_cast<unsigned>((T + 8 / W - 1) / (8 / W)), ROW_CTA, 0, s>>>(a);
+    if (H > FWD_KEPT) {
+      norm_fwd_long_kernel<E, O><<<static_cast<unsigned>(T), ROW_CTA, 0, s>>>(a);
       return launched();
-    });
+    }
+    return with_fwd_team(H, [&](auto w, auto k) { return launch_norm_fwd<E, O, decltype(w)::value, decltype(k)::value>(a, al, s); });
   });
 }
 
@@ -558,26 +617,28 @@ rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t dy_ld, c
   }
   if (!workspace || !on_boundary(workspace, 256) || workspace_bytes < rlk_layer_norm_bwd_workspace(T, H))
     return RLK_ERR_WORKSPACE;
-  NormGradArgs a{dy, x, dx, T, dy_ld, ld, dx_ld, static_cast<int32_t>(H), Vector{weight, weight_dtype == RLK_DTYPE_F32},
+  NormGradArgs a{dy, x, dx, T, dy_ld, ld, dx_ld, static_cast<int32_t>(H), 1.f / static_cast<float>(H), Vector{weight, weight_dtype == RLK_DTYPE_F32},
                  mean, rstd, static_cast<float*>(workspace), nullptr, nullptr, dw, db,
                  strips_of(T, static_cast<int>(H)), 0, err_flag};
   const size_t part = carved(a.strips * H * sizeof(float));
   char* after = static_cast<char*>(workspace) + carved(T * 2 * sizeof(float));
   if (dw) a.part_w = reinterpret_cast<float*>(after);
   if (db) a.part_b = reinterpret_cast<float*>(after + part);
-  const bool kept = H <= BWD_KEPT && whole_packs(x, T, H, ld, xs.eb) && whole_packs(dy, T, H, dy_ld, ds.eb) &&
-                    (!dx || whole_packs(dx, T, H, dx_ld, os.eb)) && on_boundary(weight, 32);
+  const bool al = whole_packs(x, T, H, ld, xs.eb) && whole_packs(dy, T, H, dy_ld, ds.eb) &&
+                  (!dx || whole_packs(dx, T, H, dx_ld, os.eb)) && on_boundary(weight, 32);
   st = with_pair(dtype, dy_dtype, [&](auto e, auto o) {
     using E = decltype(e);
     using O = decltype(o);
-    if (kept)
-      return with_bwd_team(H, [&](auto w, auto k) {
-        return launch_norm_bwd<E, O, decltype(w)::value, decltype(k)::value>(a, H * (xs.eb + ds.eb), s);
-      });
-    if (dx) norm_bwd_rows_kernel<E, O><<<static_cast<unsigned>(T), ROW_CTA, 0, s>>>(a);
-    const unsigned blocks = static_cast<unsigned>((H + 8 * ROW_CTA - 1) / (8 * ROW_CTA));
-    norm_bwd_columns_kernel<E, O><<<dim3(blocks, a.strips), ROW_CTA, 0, s>>>(a);
-    return launched();
+    if (H <= BWD_KEPT)
+      return with_bwd_team(H, [&](auto w, auto k) { return launch_norm_bwd<E, O, decltype(w)::value, decltype(k)::value>(a, al, s); });
+    const auto go = [&](auto aligned) {
+      constexpr bool AL = decltype(aligned)::value;
+      if (dx) norm_bwd_rows_kernel<E, O, AL><<<static_cast<unsigned>(T), ROW_CTA, 0, s>>>(a);
+      const unsigned blocks = static_cast<unsigned>((H + 8 * ROW_CTA - 1) / (8 * ROW_CTA));
+      norm_bwd_columns_kernel<E, O, AL><<<dim3(blocks, a.strips), ROW_CTA, 0, s>>>(a);
+      return launched();
+    };
+    return al ? go(Is<true>{}) : go(Is<false>{});
   });
   if (st != RLK_OK || !(dw || db)) return st;
   return launch_after(norm_fold_kernel, dim3(static_cast<unsigned>((H + 31) / 32), 2), 1024, s, a);

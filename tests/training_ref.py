@@ -2,8 +2,8 @@
 
 U is half a step of fp32 (2^-24), the most that one operation is off, relative to its result. A row's
 sum goes through depth(H, S) additions at most: 4 for each of a slot's ceil(ceil(H / 8) / S) packs, 1 of even
-and odd columns, 5 in a warp, 3 over the warps; S slots, in the forward 32 up to 512 columns, 64 up to 1024, 128 up to
-4096 and 256 beyond, in the backward 32 up to 256, 64 up to 512, 128 up to 1024. Every bound below counts roundings, times U, times the magnitudes that
+and odd columns, 5 in a warp, 3 over the warps; S slots, in the forward 32 up to 1024 columns, 64 up to 2048, 128 up to
+4096 and 256 beyond, in the backward 32 up to 512, 64 up to 1024, 128 up to 2048. Every bound below counts roundings, times U, times the magnitudes that
 they round; second orders are inside the few roundings that each count is rounded up by.
 """
 import math
@@ -16,7 +16,8 @@ TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2
 
 
 def depth(H, forward):
-    S = 32 * ((1 if H <= 512 else 2 if H <= 1024 else 4 if H <= 4096 else 8) if forward else (1 if H <= 256 else 2 if H <= 512 else 4 if H <= 1024 else 8))
+    S = 32 * ((1 if H <= 1024 else 2 if H <= 2048 else 4 if H <= 4096 else 8) if forward else
+              (1 if H <= 512 else 2 if H <= 1024 else 4 if H <= 2048 else 8))
     return 4 * -(-(-(-H // 8)) // S) + 9
 
 
@@ -118,7 +119,7 @@ def norm_grad(dy, x, w, mean, rstd):
         t1 = torch.zeros_like(t1)
     dx = r * (g - c1 - h * c2)
     tx = r * (t1 + h.abs() * t2 + U * (4 * g.abs() + 3 * c1.abs() + 6 * (h * c2).abs()))
-    S = min(T, 304 * (8 if H <= 256 else 4 if H <= 512 else 2 if H <= 1024 else 1))
+    S = min(T, 304 * (8 if H <= 512 else 4 if H <= 1024 else 2 if H <= 2048 else 1))
     n = -(-T // S) + -(-S // 32) + 5 + 3            # additions in a strip, over strips of a group, over groups; a term's own
     dw, db = (dy * h).sum(0), dy.sum(0)
     return (dx, dw, db), (tx, n * U * (dy * h).abs().sum(0), n * U * dy.abs().sum(0))
