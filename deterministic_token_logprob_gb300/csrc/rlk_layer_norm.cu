@@ -84,6 +84,7 @@ struct NormArgs {
   void* y;
   int64_t T, ld, out_ld;
   int32_t H;
+  int32_t ahead; // rows from one to the one that is asked for with it
   float inv;     // 1 / H
   bool centered;
   float eps;
@@ -143,6 +144,8 @@ __global__ void __launch_bounds__(ROW_CTA) norm_fwd_kernel(const NormArgs a) {
   };
   RowStats s{1.f, 0.f, 0.f, 0.f};
   float q;
+  if (AL && tid == 0 && t + a.ahead < a.T)  // the row of a CTA to come, into L2: more on its way than registers hold
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x + a.ahead * a.ld), "r"(a.H * static_cast<int>(sizeof(*x))) : "memory");
   for (;;) {
     each([&](F32x2 (&d)[4], int c0) { unpack(load_columns<E, AL>(x, c0, a.H, a.err), d); });
     if (s.k != 1.f) each([&](F32x2 (&d)[4], int) { shrink(d, s.k); });
@@ -296,16 +299,16 @@ __device__ __forceinline__ void copies_wait() {
 template <class E, int W, int K>
 struct RowRing {
   static constexpr int HALVES = sizeof(typename E::bits) * 8 / 16;
+  static constexpr int STEP = 32 * W * HALVES;  // vectors from a thread's pack to its next
   static __device__ __forceinline__ int place(int vec) { return HALVES == 2 ? vec ^ (vec >> 3 & 1) : vec; }
-  static __device__ __forceinline__ void fetch(uint4* room, const void* row, int warp, int lane, int packs, bool ok) {
+  // row: of the matrix, from the warp's vector `lane` on; room: of the ring, from the place of that vector on; left: vectors from
+  // that one to the row's end. (Places differ as vectors do over multiples of 16.)
+  static __device__ __forceinline__ void fetch(uint4* room, const uint4* row, int left) {
 #pragma unroll
     for (int j = 0; j < K; ++j)
 #pragma unroll
-      for (int i = 0; i < HALVES; ++i) {
-        const int u = i * 32 + lane, p = warp * 32 + j * 32 * W + u / HALVES;  // vector u of the warp's 32 HALVES
-        const int at = p * HALVES + u % HALVES;
-        if (p < packs && ok) copy_async_16(room + place(at), static_cast<const uint4*>(row) + at);
-      }
+      for (int i = 0; i < HALVES; ++i)
+        if (const int u = j * STEP + i * 32; u < left) copy_async_16(room + u, row + u);
   }
   static __device__ __forceinline__ void read(const uint4* room, int p, F32x2 (&v)[4]) {
     Pack<E> k;
@@ -333,15 +336,26 @@ __global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const
   float* room = rooms + team * 4 * W;
   const auto x_row = [&](int64_t t) { return static_cast<const typename E::bits*>(a.x) + t * a.ld; };
   const auto dy_row = [&](int64_t t) { return static_cast<const typename O::bits*>(a.dy) + t * a.dy_ld; };
-  const auto fetch = [&](int64_t t, int stage) {
+  // the copies: of row t_in, this thread's first vector of it, and where that goes in stage 0
+  const int xv = warp * 32 * XH + lane, dv = warp * 32 * DH + lane;
+  const uint4 *x_in = reinterpret_cast<const uint4*>(x_row(strip)) + xv, *dy_in = reinterpret_cast<const uint4*>(dy_row(strip)) + dv;
+  const int64_t x_step = a.strips * a.ld * static_cast<int64_t>(sizeof(typename E::bits)) / 16;
+  const int64_t dy_step = a.strips * a.dy_ld * static_cast<int64_t>(sizeof(typename O::bits)) / 16;
+  uint4 *x_to = ring + XRing::place(xv), *dy_to = ring + packs * XH + DRing::place(dv);
+  int64_t t_in = strip;
+  const auto fetch = [&](int stage) {
     if constexpr (AL) {
-      uint4* to = ring + stage * stage_vecs;
-      XRing::fetch(to, x_row(t), warp, lane, packs, t < a.T);
-      DRing::fetch(to + packs * XH, dy_row(t), warp, lane, packs, t < a.T);
+      if (t_in < a.T) {
+        XRing::fetch(x_to + stage * stage_vecs, x_in, packs * XH - xv);
+        DRing::fetch(dy_to + stage * stage_vecs, dy_in, packs * DH - dv);
+      }
       copies_commit();
+      x_in += x_step;
+      dy_in += dy_step;
+      t_in += a.strips;
     }
   };
-  for (int i = 0; i < a.stages - 1; ++i) fetch(strip + static_cast<int64_t>(i) * a.strips, i);
+  for (int i = 0; i < a.stages - 1; ++i) fetch(i);
   F32x2 w[K][4], sw[K][4], sb[K][4];
 #pragma unroll
   for (int j = 0; j < K; ++j) {
@@ -355,7 +369,7 @@ __global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const
   int stage = 0, odd = 0;
   for (int64_t t = strip; t < a.T; t += a.strips) {
     if constexpr (AL) __syncwarp();  // the stage that is filled next has been read by the whole warp
-    fetch(t + static_cast<int64_t>(a.stages - 1) * a.strips, stage == 0 ? a.stages - 1 : stage - 1);
+    fetch(stage == 0 ? a.stages - 1 : stage - 1);
     const int64_t next = t + a.strips < a.T ? t + a.strips : t;
     const float m1 = centered ? a.mean[next] : 0.f, r1 = a.rstd[next];
     F32x2 h[K][4], dy[K][4], s1 = 0, s2 = 0;
@@ -519,6 +533,7 @@ constexpr int64_t FWD_KEPT = 16384;  // columns of a row that stays in registers
 constexpr int64_t BWD_KEPT = 8192;   // and of one whose sums of dw and db do (4 packs)
 constexpr int BWD_SMEM = 110 * 1024;      // of each of the two CTAs of an SM
 constexpr int BWD_SMEM_ONE = 220 * 1024;  // of its only one
+constexpr int64_t FWD_AHEAD = 16 << 20;   // bytes
 constexpr int FWD_SMEM = static_cast<int>(FWD_KEPT * sizeof(float));
 
 // Launches a kernel whose dynamic shared memory may be up to `most` bytes.
@@ -572,7 +587,7 @@ rlk_status rlk_layer_norm_fwd(const void* x, int32_t dtype, int64_t T, int64_t H
   if (!same_rows(in, out) && !rows_apart(in, out)) return RLK_ERR_INVALID_ARG;
   if (T == 0) return RLK_OK;
   const bool f32 = weight_dtype == RLK_DTYPE_F32;
-  const NormArgs a{x, y, T, ld, out_ld, static_cast<int32_t>(H), 1.f / static_cast<float>(H), centered != 0, static_cast<float>(eps),
+  const NormArgs a{x, y, T, ld, out_ld, static_cast<int32_t>(H), static_cast<int32_t>(FWD_AHEAD / (H * in.eb)), 1.f / static_cast<float>(H), centered != 0, static_cast<float>(eps),
                    Vector{weight, f32}, Vector{bias, f32}, mean, rstd, err_flag};
   const bool al = whole_packs(x, T, H, ld, in.eb) && whole_packs(y, T, H, out_ld, out.eb) && on_boundary(weight, 32) &&
                   on_boundary(bias, 32);
