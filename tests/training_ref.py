@@ -2,7 +2,7 @@
 
 U is half a step of fp32 (2^-24), the most that one operation is off, relative to its result. A row's
 sum goes through depth(H, S) additions at most: 4 for each of a slot's ceil(ceil(H / 8) / S) packs, 1 of even
-and odd columns, 5 in a warp, 3 over the warps; S slots, in the forward 32 up to 1024 columns, 64 up to 2048, 128 up to
+and odd columns, 5 in a warp, 3 over the warps; S slots (at least), in the forward 32 up to 1024 columns, 64 up to 2048, 128 up to
 4096 and 256 beyond, in the backward 32 up to 512, 64 up to 1024, 128 up to 2048. Every bound below counts roundings, times U, times the magnitudes that
 they round; second orders are inside the few roundings that each count is rounded up by.
 """
