@@ -536,7 +536,7 @@ RLK_API size_t rlk_embedding_bwd_workspace(int64_t T, int64_t H);
  *   accumulate  0: dW is written, with zeros in the rows of tokens that do not come; 1: the gradient is added to what dW
  *            holds (a tied model's head has been there), one rounding an element, and other rows are not touched
  * Ids of -1 and of other shards add nothing; any other id outside [0, V_true) adds nothing and ORs RLK_FLAG_BAD_TARGET
- * in. A token's rows are added in the order of t, in runs of 16, the runs' sums in groups of 16, and the groups' sums:
+ * in. A token's rows are added in the order of t, in runs of 16, the runs' sums in groups of 8, and the groups' sums:
  * the order does not depend on the other tokens or on the shard. T == 0 with accumulate == 0 writes zeros.
  */
 RLK_API rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t H, int64_t ld,

@@ -129,7 +129,7 @@ def many_tokens(gen, T, V, kind):
     if kind == "one":
         return torch.full((T,), V - 1, device="cuda")
     if kind == "runs":  # tokens that come 1, 15, 16, 17, 31, 32, 33, ... times, and the last one as often as there is room
-        n = torch.tensor([1, 15, 31, 16, 32, 33, 17, 63, 64, 65, 1, 96, 97, 2, 129, 255, 256, 257, 513], device="cuda")
+        n = torch.tensor([1, 15, 31, 16, 32, 33, 17, 63, 64, 65, 1, 96, 97, 2, 127, 128, 129, 255, 256, 257], device="cuda")
         n = torch.repeat_interleave(torch.arange(len(n), device="cuda"), n)
         x = torch.full((T,), V - 1, device="cuda")
         x[:min(T, len(n))] = n[:T] % V

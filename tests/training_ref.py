@@ -54,8 +54,8 @@ def lookup(table, ids, scale, start, V_true):
 
 
 def table_grad(dout, ids, V, scale, start, V_true, before):
-    """(dW, tolerance): a term of n rows of one token goes through 16 additions in its run, 16 of its group's runs,
-    one for each group of 256, and a product."""
+    """(dW, tolerance): a term of n rows of one token goes through 16 additions in its run, 8 of its group's runs,
+    one for each group of 128, and a product."""
     s = float(torch.tensor(scale, dtype=torch.float32))
     r = ids - start
     here = (ids >= 0) & (ids < V_true) & (r >= 0) & (r < V)
@@ -65,7 +65,7 @@ def table_grad(dout, ids, V, scale, start, V_true, before):
     dW.index_add_(0, r[here], d)
     size.index_add_(0, r[here], d.abs())
     n = torch.bincount(r[here], minlength=V).double()[:, None]
-    tol = (n.clamp(max=16) + (n / 16).ceil().clamp(max=16) + (n / 256).ceil() + 2) * U * size * abs(s)
+    tol = (n.clamp(max=16) + (n / 16).ceil().clamp(max=8) + (n / 128).ceil() + 2) * U * size * abs(s)
     dW *= s
     if before is not None:
         dW = dW + before.double()
