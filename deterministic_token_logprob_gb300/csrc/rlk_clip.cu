@@ -2,8 +2,8 @@
 //
 //   norm = sqrt(sum over tensors and elements of g^2),   out = g min(1, max_norm / norm)
 //
-// The tensors are cut into chunks of 16 KB, which are dealt in turn to 608 shares, a CTA each. What a share adds up, and in
-// what order, follows from the tensors' sizes and types alone, and so does the order of the 608 sums: the norm has the same
+// The tensors are cut into chunks of 16 KB, which are dealt in turn to 912 shares, a CTA each. What a share adds up, and in
+// what order, follows from the tensors' sizes and types alone, and so does the order of the 912 sums: the norm has the same
 // bits wherever the tensors lie. The sum reads 2.5 GB of fp32 in 335 us (7.4 TB/s). Scaling reads and writes: there CTAs that
 // stay and take chunk after chunk are slower (920 us) than a CTA a chunk (683 us, 7.3 TB/s), which then needs the factor ready; for few
 // chunks, where the launch between would cost more, every CTA folds the shares itself.
@@ -16,10 +16,10 @@ namespace rlk {
 namespace {
 
 constexpr int CLIP_THREADS = 256;
-constexpr int CTAS = 4;              // on each SM
-constexpr int SHARES = 152 * CTAS;
+constexpr int SHARES = 912;          // six CTAs on each of 152 SMs
+constexpr int SCALERS = 608;         // CTAs that scale few chunks
 constexpr int CHUNK_BYTES = 16384;   // 64 bytes a thread: two packs of fp32, four of 16-bit types
-constexpr int MANY_CHUNKS = 8 * SHARES;  // beyond, a CTA scales one chunk (80 MB; the launch between costs 2 us)
+constexpr int MANY_CHUNKS = 8 * SCALERS;  // beyond, a CTA scales one chunk (80 MB; the launch between costs 2 us)
 constexpr int BATCH = 512;           // tensors of one launch: their table is a kernel parameter (16 KB)
 constexpr int FEW = 32;              // a smaller table, for the calls that are bound by the host
 
@@ -143,7 +143,7 @@ __device__ __noinline__ Squares sum_chunks(const Piece p, uint32_t lo, uint32_t 
 }
 
 template <int N>
-__global__ void __launch_bounds__(CLIP_THREADS, CTAS) sum_squares_kernel(const __grid_constant__ ClipArgs<N> a) {
+__global__ void __launch_bounds__(CLIP_THREADS, 6) sum_squares_kernel(const __grid_constant__ ClipArgs<N> a) {
   __shared__ float room[CLIP_THREADS / 32];
   Squares s;
   for (uint32_t c = blockIdx.x; c < a.chunks;) {
@@ -266,7 +266,7 @@ __device__ __noinline__ void scale_chunks(const Piece p, uint32_t c, uint32_t st
 }
 
 template <int N>
-__global__ void __launch_bounds__(CLIP_THREADS, CTAS) scale_kernel(const __grid_constant__ ClipArgs<N> a, const ClipNorm q) {
+__global__ void __launch_bounds__(CLIP_THREADS, 4) scale_kernel(const __grid_constant__ ClipArgs<N> a, const ClipNorm q) {
   __shared__ float room[CLIP_THREADS / 32];
   griddep_wait();
   const float f = q.factor ? *q.factor : find_norm(q, blockIdx.x == 0 && q.norm, room);
@@ -384,7 +384,7 @@ inline rlk_status run_clip(const Tensors& t, double max_norm, float* norm, int32
     if (st != RLK_OK) return st;
   }
   return each_batch<N>(t, sums, err, [&](const ClipArgs<N>& a, int32_t k) {
-    const dim3 grid(many ? std::max(a.chunks, 1u) : static_cast<unsigned>(SHARES));
+    const dim3 grid(std::max(many ? a.chunks : std::min<uint32_t>(a.chunks, SCALERS), 1u));
     if (k == 0) return launch_after(scale_kernel<N>, grid, CLIP_THREADS, s, a, q);
     scale_kernel<N><<<grid, CLIP_THREADS, 0, s>>>(a, q);
     return launched();

@@ -134,4 +134,4 @@ def total_norm(grads):
     again; half of all that through the root, and its own. A scale beside the norm's adds one more."""
     chunks = sum(-(-g.numel() * g.element_size() // 16384) for g in grads)
     n = math.sqrt(math.fsum(float(g.double().square().sum()) for g in grads))
-    return n, (0.5 * (-(-chunks // 608) + 36) + 1) * U
+    return n, (0.5 * (-(-chunks // 912) + 36) + 1) * U
