@@ -4,7 +4,7 @@
 //
 // The tensors are cut into chunks of 16 KB, which are dealt in turn to 912 shares, a CTA each. What a share adds up, and in
 // what order, follows from the tensors' sizes and types alone, and so does the order of the 912 sums: the norm has the same
-// bits wherever the tensors lie. The sum reads 2.5 GB of fp32 in 335 us (7.4 TB/s). Scaling reads and writes: there CTAs that
+// bits wherever the tensors lie. The sum reads 2.5 GB of fp32 in 338 us (7.4 TB/s). Scaling reads and writes: there CTAs that
 // stay and take chunk after chunk are slower (920 us) than a CTA a chunk (683 us, 7.3 TB/s), which then needs the factor ready; for few
 // chunks, where the launch between would cost more, every CTA folds the shares itself.
 #include <algorithm>
@@ -34,7 +34,8 @@ struct Piece {
 // Sums of squares at three scales (Blue's sums): what would overflow or vanish in fp32 is squared as x 2^-80 or x 2^80. All in
 // fp32: this GPU adds two doubles an SM and cycle, and a fold of the shares in doubles by every CTA took 7 us.
 struct alignas(16) Squares {
-  float mid = 0.f, big = 0.f, small = 0.f, none = 0.f;
+  float mid = 0.f, big = 0.f, small = 0.f;
+  float lost = 0.f;  // what the roundings of mid's sum have lost: a thread may add many chunks (18000 of 280 GB)
 };
 template <int N>
 struct ClipArgs {
@@ -53,6 +54,17 @@ constexpr int CHUNK = CHUNK_BYTES / static_cast<int>(sizeof(typename E::bits)); 
 template <class E>
 constexpr int PACKS = CHUNK<E> / (8 * CLIP_THREADS);                             // of a thread
 
+// hi + lo += v: the sum and what its rounding loses (two-sum)
+__device__ __forceinline__ void add_exactly(float& hi, float& lo, float v) {
+  const float t = __fadd_rn(hi, v), b = __fsub_rn(t, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(v, b)));
+  hi = t;
+}
+struct Exact {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float v) { add_exactly(hi, lo, v); }
+};
+
 // The sum of squares of a thread's packs of a chunk, get(j) the j-th of them, at the scale that holds it.
 template <class E, int UNROLL, class Get>
 __device__ __forceinline__ void add_squares(Squares& s, const Get& get) {
@@ -70,7 +82,7 @@ __device__ __forceinline__ void add_squares(Squares& s, const Get& get) {
   };
   const float q = at(1.f);
   if (q >= 8.077935669463161e-28f && q <= 1.2089258196146292e24f) {  // 2^-90 .. 2^80: 2^39 of them stay in fp32
-    s.mid = __fadd_rn(s.mid, q);
+    add_exactly(s.mid, s.lost, q);
     return;
   }
   const bool tiny = q < 1.f;  // else too large, NaN or infinite
@@ -78,16 +90,6 @@ __device__ __forceinline__ void add_squares(Squares& s, const Get& get) {
   if (tiny) s.small = __fadd_rn(s.small, r);
   else s.big = __fadd_rn(s.big, r);
 }
-
-// The sum of a value and what its rounding has lost (two-sum), and of two such.
-struct Exact {
-  float hi = 0.f, lo = 0.f;
-  __device__ __forceinline__ void add(float v) {
-    const float t = __fadd_rn(hi, v), b = __fsub_rn(t, hi);
-    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(v, b)));
-    hi = t;
-  }
-};
 
 // The sum over the CTA's threads, in one order; every thread gets it. room: 8 floats each.
 __device__ __forceinline__ float block_sum(float v, float* room) {
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(CLIP_THREADS, 6) sum_squares_kernel(const __gr
   griddep_launch_dependents();
   Squares all;
   const bool odd = __syncthreads_or(s.big != 0.f || s.small != 0.f);  // NaN counts
-  all.mid = block_sum(s.mid, room);
+  all.mid = block_sum(__fadd_rn(s.mid, s.lost), room);
   if (odd) {
     all.big = block_sum(s.big, room);
     all.small = block_sum(s.small, room);
@@ -304,11 +306,12 @@ struct Extent {
   uintptr_t from, to;
 };
 
-// Every written tensor is its own gradient, or meets no gradient and no other written one.
-inline rlk_status check_written(const Tensors& t) {
-  Extent* e = new (std::nothrow) Extent[2 * static_cast<size_t>(t.n)];
+// Every written tensor is its own gradient, or meets no gradient and no other written one; the norm meets none of them.
+inline rlk_status check_written(const Tensors& t, const float* norm) {
+  Extent* e = new (std::nothrow) Extent[2 * static_cast<size_t>(t.n) + 1];
   if (!e) return RLK_ERR_CUDA;
   int32_t k = 0;
+  e[k++] = Extent{reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + sizeof(float)};
   for (int32_t i = 0; i < t.n; ++i) {
     if (t.sizes[i] == 0) continue;
     const uintptr_t in = reinterpret_cast<uintptr_t>(t.in[i]), out = reinterpret_cast<uintptr_t>(t.out[i]);
@@ -323,7 +326,7 @@ inline rlk_status check_written(const Tensors& t) {
   return apart ? RLK_OK : RLK_ERR_INVALID_ARG;
 }
 
-inline rlk_status check_tensors(const Tensors& t) {
+inline rlk_status check_tensors(const Tensors& t, const float* norm) {
   if (t.n < 0 || (t.n > 0 && (!t.in || !t.sizes || !t.dtypes))) return RLK_ERR_INVALID_ARG;
   if (t.n > RLK_MAX_TENSORS) return RLK_ERR_UNSUPPORTED;
   int64_t chunks = 0;
@@ -339,7 +342,8 @@ inline rlk_status check_tensors(const Tensors& t) {
     if (t.sizes[i] > 0 && (!t.out[i] || !on_boundary(t.out[i], dtype_bytes(t.out_dtypes[i])))) return RLK_ERR_INVALID_ARG;
   }
   if (chunks > INT32_MAX) return RLK_ERR_UNSUPPORTED;
-  return t.out ? check_written(t) : RLK_OK;
+  if (!norm || !on_boundary(norm, 4)) return RLK_ERR_INVALID_ARG;
+  return t.out ? check_written(t, norm) : RLK_OK;
 }
 
 inline int32_t launches_of(int32_t n) { return n <= FEW ? 1 : (n + BATCH - 1) / BATCH; }
@@ -393,9 +397,8 @@ inline rlk_status run_clip(const Tensors& t, double max_norm, float* norm, int32
 
 inline rlk_status clip(const Tensors& t, double max_norm, float* norm, int32_t* err, void* workspace, size_t bytes,
                        void* stream) {
-  const rlk_status st = check_tensors(t);
+  const rlk_status st = check_tensors(t, norm);
   if (st != RLK_OK) return st;
-  if (!norm || !on_boundary(norm, 4)) return RLK_ERR_INVALID_ARG;
   if (!workspace || !on_boundary(workspace, 256) || bytes < rlk_grad_norm_workspace(t.n)) return RLK_ERR_WORKSPACE;
   auto* sums = static_cast<Squares*>(workspace);
   const auto s = static_cast<cudaStream_t>(stream);

@@ -499,7 +499,8 @@ RLK_API rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, i
  * Common arguments:
  *   dtype    RLK_DTYPE_* of the rows; results have the same type, or RLK_DTYPE_BF16 for fp32 rows
  *   H        1 .. RLK_MAX_HIDDEN; rows `ld` elements apart (at least H), aligned to their element size only.
- *            Rows that all start on 16-byte boundaries, with H % 8 == 0, are the fast case
+ *            Rows that all start on 16-byte boundaries (fp32 ones, weight, bias and dW on 32-byte ones), with
+ *            H % 8 == 0, are the fast case
  *   T        0 .. RLK_MAX_TOKENS
  *   err_flag device int32 or NULL, as everywhere
  *   workspace, workspace_bytes: device scratch of the size that the query returns, 256-byte aligned; what it
@@ -514,8 +515,8 @@ RLK_API rlk_status rlk_distill_topk_fwd_bwd(const void* logits, int32_t dtype, i
 #define RLK_MAX_TOKENS (1 << 24)
 
 /*
- * out[t] = scale * table[ids[t] - vocab_start], rounded once to out_dtype: the rows of a table, or of a shard of one that
- * holds the tokens [vocab_start, vocab_start + V_local).
+ * out[t] = scale * table[ids[t] - vocab_start], the product in fp32 (scale as well), then rounded to out_dtype: the rows of a
+ * table, or of a shard of one that holds the tokens [vocab_start, vocab_start + V_local).
  *   table    device [V_local][ld];  ids: device int64 [T];  out: device [T][out_ld]
  *   V_true   tokens are 0 .. V_true - 1
  * The row of a token that is not in the shard is zero, and so is that of id -1 (padding); any other id outside
@@ -563,7 +564,7 @@ RLK_API rlk_status rlk_layer_norm_fwd(const void* x, int32_t dtype, int64_t T, i
                                       double eps, void* y, int32_t out_dtype, int64_t out_ld, float* mean, float* rstd,
                                       int32_t* err_flag, void* stream);
 
-/* Bytes of device workspace rlk_layer_norm_bwd needs: 8 T bytes, and the parts of dw and db of 152 strips of rows. */
+/* Bytes of device workspace rlk_layer_norm_bwd needs: 8 T bytes, and the parts of dw and db of every strip of rows (below). */
 RLK_API size_t rlk_layer_norm_bwd_workspace(int64_t T, int64_t H);
 
 /*
@@ -575,8 +576,10 @@ RLK_API size_t rlk_layer_norm_bwd_workspace(int64_t T, int64_t H);
  *   mean, rstd  device fp32 [T] from the forward; mean NULL: not centered
  *   dx       device [T][dx_ld] of type dtype, or NULL; it may be dy or x itself (same type and row distance)
  *   dw, db   device fp32 [H], each may be NULL; at least one of dx, dw and db is wanted. T == 0 writes zeros to them
- * Rows are dealt to 152 strips, row t to strip t mod 152; a strip adds its rows in ascending order, and the
- * strips' sums are added in ascending order.
+ * Rows are dealt to S strips, row t to strip t mod S, with S = T, or 304, 608, 1216 and 2432 for H above 2048, 1024, 512 and
+ * otherwise where T is larger; a strip adds its rows in ascending order. Of the strips' sums, those of strips i, i + 32, ... are
+ * added in ascending order, and the 32 results as a balanced tree. A row whose x, dy or statistics hold a NaN makes that row of dx and
+ * all or those columns of dw and db NaN, whatever its dy: rows of padding are to hold finite values in both.
  */
 RLK_API rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t dy_ld, const void* x, int32_t dtype,
                                       int64_t ld, int64_t T, int64_t H, const void* weight, int32_t weight_dtype,
@@ -593,7 +596,7 @@ RLK_API rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t 
  *   outs, out_dtypes  host arrays of n: where the results go (same count; same type, or RLK_DTYPE_BF16 for fp32), a
  *            gradient itself among them. Results meet neither one another nor any other gradient
  *   max_norm above 0 (infinity: never scaled)
- *   norm     device fp32 [1]: the norm before scaling
+ *   norm     device fp32 [1]: the norm before scaling; with outs, it meets no gradient and no result
  * Squares that would overflow or vanish in fp32 are summed at another scale. A norm that is not finite (a NaN or an
  * infinity among the gradients, or a norm beyond fp32) leaves the gradients unscaled, and RLK_FLAG_NONFINITE is ORed
  * into *err_flag: a trainer skips that step. Sums are taken in an order that follows from sizes and types.

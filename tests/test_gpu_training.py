@@ -531,6 +531,15 @@ def test_clip_values(rlk):
     assert float(rlk.clip_grad_norm(zero, 1.0)) == 0.0 and not zero.any()
 
 
+def test_norm_of_many_elements(rlk):
+    """2^32 equal elements, 535 chunks a thread. Relative to the sum of squares: 17 roundings of a chunk's, 2 of the sum of chunks,
+    whose losses are kept, 8 in a warp and between warps, as many where the shares are joined (3 sums with their losses, 8)
+    and the root's: 38 half steps at most, of which the root leaves 19."""
+    g = torch.full((1 << 32,), 0.0123, dtype=torch.bfloat16, device="cuda")
+    want = 65536 * float(g[0])
+    assert abs(float(rlk.grad_norm([g])) / want - 1) <= 20 * ref.U
+
+
 def test_clip_far_elements(rlk):
     """A tensor of more than 2^31 elements."""
     n = (1 << 31) + 12345
@@ -738,3 +747,66 @@ def test_step_of_a_tied_model(rlk):
     assert abs(float(norm) / total - 1) < 1e-2 and total > 0.01
     for got, was in zip((dW, dw), before):
         assert float((got.double() - was.double() * (0.01 / float(norm))).abs().max()) <= 3 * ref.U * float(was.abs().max())
+
+
+def test_norm_beside_the_gradients(rlk):
+    """A norm in the gradients' own buffer: refused where clipping would write it under a reader."""
+    g = torch.ones(101, device="cuda")
+    with pytest.raises(rlk.RlkError):
+        rlk.clip_grad_norm([g], 1.0, norm=g[40])
+    with pytest.raises(rlk.RlkError):
+        rlk.clip_grad_norm([g[:100]], 1.0, out=[g[1:]], norm=torch.empty((), device="cuda"))
+    assert g.tolist() == [1.0] * 101
+    rlk.clip_grad_norm([g[:100]], 5.0, norm=g[100])
+    assert g.tolist() == [0.5] * 100 + [10.0]
+
+
+def test_two_threads(rlk):
+    """Calls from two host threads at once, on streams of their own."""
+    import threading
+    d = [call_inputs(seed=i) for i in range(2)]
+    want = [all_calls(rlk, x) for x in d]
+    torch.cuda.synchronize()
+    same = [0, 0]
+
+    def work(i):
+        s = torch.cuda.Stream()
+        for _ in range(20):
+            got = all_calls(rlk, d[i], s)
+            s.synchronize()
+            same[i] += all(torch.equal(a, b) for a, b in zip(got, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert same == [20, 20]
+
+
+def test_captured_autograd_step(rlk):
+    """Forward and backward of the differentiable forms in a graph, replayed on new tokens. No eager graph of the same
+    leaves is alive when the capture starts."""
+    gen = rng(12)
+    T, H, V = 300, 64, 50
+    table = torch.randn((V, H), generator=gen, device="cuda").requires_grad_()
+    w = torch.randn(H, generator=gen, device="cuda").requires_grad_()
+    ids, other = many_tokens(gen, T, V, "zipf"), many_tokens(gen, T, V, "even")
+
+    def step():
+        y = rlk.layer_norm(rlk.embedding(table, ids, scale=2.0), w, centered=False)
+        return torch.autograd.grad(y.square().sum(), (table, w))
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for new in (ids.clone(), other):
+        ids.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, step()))

@@ -161,7 +161,7 @@ class Tensors:
         a = [None if k in null else self.address(i) for i, k in enumerate(("grads", "sizes", "dtypes"))]
         return self.lib.rlk_grad_norm(*a, self.k if n is None else n, norm, None, ws, ws_bytes, None)
 
-    def clip(self, max_norm=1.0, norm=FAKE, ws=None, ws_bytes=0, **null):
+    def clip(self, max_norm=1.0, norm=FAR, ws=None, ws_bytes=0, **null):
         a = [None if k in null else self.address(i) for i, k in enumerate(("grads", "sizes", "dtypes", "outs", "odtypes"))]
         return self.lib.rlk_clip_grad_norm(*a[:3], self.k, max_norm, *a[3:], norm, None, ws, ws_bytes, None)
 
@@ -210,3 +210,9 @@ def test_clip_arguments(lib):
     # side by side
     assert Tensors(lib, at=(0x100000, 0x100000 + 400), n=(100, 50), dtypes=(F32, F32)).clip() == WORKSPACE
     assert Tensors(lib, at=(0x100000, 0x100000 + 396), n=(100, 50), dtypes=(F32, F32)).clip() == INVALID
+    # the norm over a gradient or a result
+    for norm in (0x100000, 0x100004, 0x200000):
+        assert Tensors(lib).clip(norm=norm) == INVALID
+        assert Tensors(lib).norm(norm=norm) == WORKSPACE
+    assert Tensors(lib, to=(0x300000, 0x400000), odtypes=(BF16, BF16)).clip(norm=0x400000) == INVALID
+    assert Tensors(lib, to=(0x300000, 0x400000), odtypes=(BF16, BF16)).clip(norm=0x500000) == WORKSPACE
