@@ -330,10 +330,10 @@ __device__ __forceinline__ void list_runs(const SortArgs& a, const Entry* sorted
 template <int KEPT, bool ALL>
 __global__ void __launch_bounds__(SORT_THREADS) sort_tokens_kernel(const SortArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];
+  griddep_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x < 2) a.n_runs[threadIdx.x] = 0;  // the cluster's barriers stand before its first use
   sort_tokens<KEPT, ALL>(a, *reinterpret_cast<SortSmem*>(dyn));
   list_runs(a, a.passes & 1 ? a.a : a.b);
-  griddep_launch_dependents();
 }
 
 // ---------------------------------------------------------------------------
@@ -354,12 +354,21 @@ struct GatherArgs {
   float* part;          // [2 slots][H rounded up to 8]: sums of the runs of tokens of more than one run
   int32_t* done;        // [3 slots][slices]: runs of such a group, and groups of such a token, that are through
   int32_t slots, slices;
+  int32_t ahead;        // rows of dout that a CTA asks for while the tokens are sorted
   int32_t zero_per;     // rows that a CTA behind those of the runs zeroes, where dW is new (0: it is not)
   int32_t* err;
 };
 
 constexpr int GATHER_THREADS = 256;
 constexpr int ZERO_ROWS = 2048;  // zero_per at most
+// 16-bit rows: up to so many warps of a pack a lane, each has 8 rows in flight, else two packs and 2 rows. Few warps wait for the longest chain
+// of rows (2048 rows of 2048 added to dW, tokens as in text: 19.0 us for 22.7; spread evenly 16.9 for 16.2), many for the memory (16384
+// rows: 44.6 us for 51.7, evenly 65.4 for 74.5). fp32 rows have a pack a lane and 4 rows (8192 rows of 2048: 31.5 us, two and 2 37.5).
+constexpr int64_t FEW_WARPS = 16384;
+// While one cluster sorts, the first CTAs of the next kernel ask for dout, if L2 holds that much besides the rows of dW (16384 rows of
+// 2048 in bf16, 67 MB: 44.6 us for 46.9; of 512 CTAs instead of 128 8192 rows of 4096 take 48.3 us for 46.1).
+constexpr int AHEAD_CTAS = 128;
+constexpr int64_t AHEAD_BYTES = 80 << 20;
 
 // Zeros into the rows r0 .. r0 + n of dW that are not met, by a CTA.
 template <bool AL>
@@ -403,9 +412,8 @@ __device__ __forceinline__ void zero_absent_rows(const GatherArgs& a, int32_t z,
 }
 
 // s += n rows of dout, row at(i) as the i-th, in C packs of a thread 256 columns apart from column c0 on.
-template <class E, bool AL, int C, class At>
+template <class E, bool AL, int C, int U, class At>  // U rows in flight
 __device__ __forceinline__ void add_rows(const GatherArgs& a, int n, int c0, F32x2 (&s)[C][4], const At& at) {
-  constexpr int U = 4 / C;  // rows in flight
   for (int i = 0; i < n; i += U) {
     Pack<E> k[U][C];
 #pragma unroll
@@ -501,16 +509,22 @@ __device__ __forceinline__ void add_parts(const GatherArgs& a, const Token& k, i
   }
 }
 
-// A CTA takes a run, each of its warps a slice of 256 C columns. A run is a chain of loads -- where it starts, its rows and the row
-// of dW -- which many small CTAs hide: 16384 rows of 2048 in bf16 added to dW, tokens spread evenly, move 321 MB in 51 us (6.3
-// TB/s; 24 warps an SM and 8 rows in flight in each 59 us, warps that stay and take run after run 94). Runs and groups are short
+// A CTA takes a run, each of its warps a slice of 256 C columns, U rows in flight. A run is a chain of loads -- where it starts, its rows
+// and the row of dW -- which many small CTAs hide: 16384 rows of 2048 in bf16 added to dW, tokens spread evenly, move 321 MB in 65 us with the
+// sort (at 24 warps an SM 8 us more, with warps that stay and take run after run 43). Runs and groups are short
 // so that a token that comes often is spread over CTAs and its chain of sums is short; the warp that is through last in a
 // group of runs adds up the group, and the last of the groups the token (a group's sum takes the place of its first run's).
-template <class E, bool AL, int C>
-__global__ void __launch_bounds__(GATHER_THREADS, 4) gather_kernel(const GatherArgs a) {
+template <class E, bool AL, int C, int U>
+__global__ void __launch_bounds__(GATHER_THREADS, U == 8 ? 3 : 4) gather_kernel(const GatherArgs a) {
   const int lane = threadIdx.x & 31;
   const int slice = static_cast<int>(blockIdx.y * (blockDim.x >> 5) + (threadIdx.x >> 5)), c0 = 256 * C * slice + 8 * lane;
   __shared__ uint8_t met[ZERO_ROWS];
+  if (AL && blockIdx.y == 0) {  // dout into L2
+    for (int i = threadIdx.x; i < a.ahead; i += blockDim.x)
+      if (const int64_t t = static_cast<int64_t>(blockIdx.x) * a.ahead + i; t < a.T)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const typename E::bits*>(a.dout) + t * a.ld),
+                     "r"(a.H * static_cast<int>(sizeof(typename E::bits))) : "memory");
+  }
   griddep_wait();
   if (static_cast<int>(blockIdx.x) >= a.T) {
     if (blockIdx.y == 0) zero_absent_rows<AL>(a, static_cast<int32_t>(blockIdx.x) - a.T, met);
@@ -546,7 +560,7 @@ __global__ void __launch_bounds__(GATHER_THREADS, 4) gather_kernel(const GatherA
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[j][i] = add2(s[j][i], 0);  // -0 becomes 0, as in a sum of several
   }
-  add_rows<E, AL, C>(a, n - 1, c0, s, [&](int r) { return __shfl_sync(kFullWarp, e.t, r + 1); });
+  add_rows<E, AL, C, U>(a, n - 1, c0, s, [&](int r) { return __shfl_sync(kFullWarp, e.t, r + 1); });
   if (!alone) {
     Token k{static_cast<int32_t>(run.y), p + n};
     if (n == RUN && p + RUN < a.T)
@@ -622,14 +636,14 @@ __global__ void __launch_bounds__(GATHER_THREADS) gather_few_kernel(const Gather
     for (int j = 0; j < 4; ++j) to[0][j] = add2(to[0][j], v[0][j]);
   };
   if (n <= RUN) {
-    add_rows<E, AL, 1>(a, n, c0, s, [&](int i) { return list[i]; });
+    add_rows<E, AL, 1, 4>(a, n, c0, s, [&](int i) { return list[i]; });
   } else {
     for (int g = 0; g < n; g += RUN * GROUP) {
       const int stop = min(n, g + RUN * GROUP);
       F32x2 sum[1][4] = {};
       for (int i = g; i < stop; i += RUN) {
         F32x2 v[1][4] = {};
-        add_rows<E, AL, 1>(a, min(RUN, stop - i), c0, v, [&](int q) { return list[i + q]; });
+        add_rows<E, AL, 1, 4>(a, min(RUN, stop - i), c0, v, [&](int q) { return list[i + q]; });
         add(sum, v);
       }
       add(s, sum);
@@ -747,7 +761,7 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
   const bool al = whole_packs(dout, T, H, ld, in.eb) && on_boundary(dW, 32);
   const Shard shard{vocab_start, V_local, V_true, err_flag};
   GatherArgs g{nullptr, nullptr, nullptr, ids, shard, dout, dW, ld, static_cast<int32_t>(T), static_cast<int32_t>(H),
-               static_cast<int32_t>(V_local), static_cast<float>(scale), accumulate != 0, nullptr, nullptr, r.slots, 0, 0, err_flag};
+               static_cast<int32_t>(V_local), static_cast<float>(scale), accumulate != 0, nullptr, nullptr, r.slots, 0, 0, 0, err_flag};
   // the CTAs that write zeros: eight an SM at least, of half a megabyte at most (151936 rows of 4096, 8192 tokens: 366 us;
   // eight an SM of 2 MB each 378, four of 4 MB 434; 4096 rows of 256, 64 tokens: 3.3 us, with four times the CTAs 4.6)
   const int64_t share = std::min<int64_t>((V_local + 1215) / 1216, std::max<int64_t>(1, 131072 / H));
@@ -763,7 +777,7 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
       return launched();
     });
   }
-  const int packs = H > 256 ? 2 : 1;  // a lane's in a slice
+  const int packs = in.eb == 4 || H <= 256 || T * ((H + 255) / 256) <= FEW_WARPS ? 1 : 2;  // a lane's in a slice
   const int warps = static_cast<int>(std::min<int64_t>(GATHER_THREADS / 32, (H + 256 * packs - 1) / (256 * packs)));
   const int blocks = static_cast<int>((H + 256 * packs * warps - 1) / (256 * packs * warps));
   g.slices = blocks * warps;
@@ -785,11 +799,13 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
   g.n_runs = n_runs;
   g.part = reinterpret_cast<float*>(ws + r.part);
   g.done = q.done;
+  if (al && T * H * in.eb <= AHEAD_BYTES) g.ahead = static_cast<int32_t>((T + AHEAD_CTAS - 1) / AHEAD_CTAS);
+  const auto go = [&](auto kernel) { return launch_after(kernel, dim3(static_cast<unsigned>(T + zero), blocks), 32 * warps, s, g); };
   return with_type(dtype, [&](auto e) {
     using E = decltype(e);
-    const auto kernel = packs == 1 ? (al ? gather_kernel<E, true, 1> : gather_kernel<E, false, 1>)
-                                   : (al ? gather_kernel<E, true, 2> : gather_kernel<E, false, 2>);
-    return launch_after(kernel, dim3(static_cast<unsigned>(T + zero), blocks), 32 * warps, s, g);
+    if constexpr (sizeof(typename E::bits) == 4) return go(al ? gather_kernel<E, true, 1, 4> : gather_kernel<E, false, 1, 4>);
+    else if (packs == 2) return go(al ? gather_kernel<E, true, 2, 2> : gather_kernel<E, false, 2, 2>);
+    else return go(al ? gather_kernel<E, true, 1, 8> : gather_kernel<E, false, 1, 8>);
   });
 }
 
