@@ -182,7 +182,9 @@ __global__ void __launch_bounds__(ROW_CTA, K <= 4 ? 4 : 2) norm_fwd_kernel(const
   if constexpr (!AL) write_out<O, W>(y, stage, a.H, tid, a.err);
 }
 
-// Longer rows, by 8 warps: they are read three times (from L1 or L2 after the first).
+// Longer rows, and many misaligned ones of more than 8192 columns, by 8 warps: they are read three times (from L1 or L2 after the
+// first). Misaligned rows keep registers from more than two CTAs an SM otherwise (4096 of 12001 in bf16: 110 us for 141, in fp32 171 for
+// 179), which few rows do not need (400 of 16383 in fp32: 29.4 us for 25.6).
 template <class E, class O>
 __global__ void __launch_bounds__(ROW_CTA) norm_fwd_long_kernel(const NormArgs a) {
   __shared__ __align__(16) float rooms[32];
@@ -532,6 +534,8 @@ inline rlk_status with_bwd_team(int64_t H, F f) {
 }
 
 constexpr int64_t FWD_KEPT = 16384;  // columns of a row that stays in registers (8 packs a thread)
+constexpr int64_t FWD_KEPT_ODD = 8192; // of many misaligned rows
+constexpr int64_t FWD_MANY = 1024;     // rows
 constexpr int64_t BWD_KEPT = 8192;   // and of one whose sums of dw and db do (4 packs)
 constexpr int BWD_SMEM = 110 * 1024;      // of each of the two CTAs of an SM
 constexpr int BWD_SMEM_ONE = 220 * 1024;  // of its only one
@@ -597,7 +601,7 @@ rlk_status rlk_layer_norm_fwd(const void* x, int32_t dtype, int64_t T, int64_t H
   return with_pair(dtype, out_dtype, [&](auto e, auto o) {
     using E = decltype(e);
     using O = decltype(o);
-    if (H > FWD_KEPT) {
+    if (H > (!al && T > FWD_MANY ? FWD_KEPT_ODD : FWD_KEPT)) {
       norm_fwd_long_kernel<E, O><<<static_cast<unsigned>(T), ROW_CTA, 0, s>>>(a);
       return launched();
     }

@@ -810,3 +810,23 @@ def test_captured_autograd_step(rlk):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, step()))
+
+
+@pytest.mark.parametrize("dtype,out", PAIRS)
+@pytest.mark.parametrize("T", [1024, 1025])
+def test_norm_many_wide_misaligned_rows(rlk, dtype, out, T):
+    """The bits of aligned rows, and those of few rows, whichever kernel takes them."""
+    H = 9000
+    gen = rng(13)
+    x = randn(gen, T, H, dtype=dtype)
+    w, b = (torch.randn(H, generator=gen, device="cuda") for _ in range(2))
+    x[7] = 3e38 if dtype is not torch.float16 else 60000.0   # the sums are taken once more, at a smaller scale
+    x[7, ::2] *= -1
+    away = torch.empty(T * H + 1, dtype=dtype, device="cuda")[1:].view(T, H)
+    away.copy_(x)
+    for centered in (True, False):
+        want = rlk.layer_norm_fwd(x, w, b, centered=centered, out_dtype=out)
+        got = rlk.layer_norm_fwd(away, w, b, centered=centered, out_dtype=out)
+        few = rlk.layer_norm_fwd(away[:9], w, b, centered=centered, out_dtype=out)
+        for a, c, d in zip(want, got, few):
+            assert a is None or (torch.equal(a, c) and torch.equal(a[:9], d))
