@@ -30,6 +30,11 @@ constexpr int LEAF_GROUP = 256;      // columns a warp covers with 8 per lane
 constexpr int LEAF_GROUPS = ROW_LEAF / LEAF_GROUP;
 constexpr uint32_t kFullWarp = 0xffffffffu;
 
+// The two halves of a cluster's barrier. A CTA's shared memory may be touched by the others once it has started: what writes
+// there arrives at its beginning and waits before the first such write.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // element types
 // ---------------------------------------------------------------------------
