@@ -163,7 +163,7 @@ __device__ __forceinline__ void sort_tokens(const SortArgs& a, SortSmem& m) {
   const int bins = 1 << each;
   uint32_t *mine = m.count[warp], *same = m.lanes[warp];
 
-  cluster_arrive();
+  if (ctas > 1) cluster_arrive();
   for (int i = rank * SORT_THREADS + threadIdx.x; i < a.n_done; i += ctas * SORT_THREADS) a.done[i] = 0;
   for (int pass = 0; pass < a.passes; ++pass) {
     const Entry* src = pass == 0 ? nullptr : pass & 1 ? a.a : a.b;
@@ -202,7 +202,7 @@ __device__ __forceinline__ void sort_tokens(const SortArgs& a, SortSmem& m) {
       m.total[rank][b] = run;
     }
     __syncthreads();
-    if (pass == 0) cluster_wait();  // every CTA has started: its shared memory may be written
+    if (pass == 0 && ctas > 1) cluster_wait();  // every CTA has started: its shared memory may be written
     if (warp < static_cast<int>(ctas) && warp != static_cast<int>(rank)) {  // a warp for each other CTA
       const uint32_t to = map_to_cta(smem_u32(m.total[rank]), warp);
       for (int i = 4 * lane; i < bins; i += 128) st_cluster_u32x4(to + 4 * i, *reinterpret_cast<const uint4*>(&m.total[rank][i]));

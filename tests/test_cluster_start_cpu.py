@@ -41,12 +41,13 @@ def test_every_cta_has_started(file, head, write):
 
 
 def test_halves_of_the_sorts_barrier_pair_up():
-    """Each thread arrives once, before the passes, and waits once, in the first: neither under a condition that
-    threads of a CTA see differently."""
+    """Each thread arrives once, before the passes, and waits once, in the first: both where there are other CTAs, which
+    all threads see alike."""
     s = body("rlk_embedding.cu", "void sort_tokens(")
     assert s.count("cluster_arrive()") == s.count("cluster_wait()") == 1
     assert s.index("cluster_arrive()") < s.index("for (int pass = 0;")
-    assert re.search(r"\n    if \(pass == 0\) cluster_wait\(\);", s)
+    assert re.search(r"\n  if \(ctas > 1\) cluster_arrive\(\);", s)
+    assert re.search(r"\n    if \(pass == 0 && ctas > 1\) cluster_wait\(\);", s)
 
 
 def test_no_other_source_writes_across_ctas():
