@@ -671,27 +671,47 @@ inline Room room_of(int64_t T, int64_t H) {
   return r;
 }
 
-template <int KEPT, bool ALL>
-inline rlk_status launch_sort(const SortArgs& q, int ctas, cudaStream_t s) {
-  static OncePerDevice allowed;
-  const auto kernel = sort_tokens_kernel<KEPT, ALL>;
-  if (!allowed([&] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)) == cudaSuccess &&
-               cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-      }))
-    return RLK_ERR_CUDA;
+// A launch of the sort as a cluster of `ctas`.
+struct SortLaunch {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
-  cfg.blockDim = dim3(SORT_THREADS);
-  cfg.dynamicSmemBytes = sizeof(SortSmem);
-  cfg.stream = s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ctas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, q) == cudaSuccess ? RLK_OK : RLK_ERR_CUDA;
+  SortLaunch(int ctas, cudaStream_t s) {
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(SORT_THREADS);
+    cfg.dynamicSmemBytes = sizeof(SortSmem);
+    cfg.stream = s;
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = ctas;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+  SortLaunch(const SortLaunch&) = delete;  // cfg points into it
+};
+
+using SortKernel = void (*)(SortArgs);
+constexpr SortKernel kSorts[] = {sort_tokens_kernel<2, true>, sort_tokens_kernel<8, true>, sort_tokens_kernel<8, false>};
+
+// The largest cluster of the sort, 0 for an error: SORT_CTAS where the device can place one.
+inline int sort_ctas_at_most() {
+  static KnownPerDevice known;
+  return known([] {
+    for (SortKernel k : kSorts)
+      if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(SortSmem)) != cudaSuccess ||
+          cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return 0;
+    return cluster_that_fits(SORT_CTAS, [](int ctas) {
+      const SortLaunch l(ctas, nullptr);
+      for (SortKernel k : kSorts) {
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, k, &l.cfg) != cudaSuccess || n < 1) {
+          cudaGetLastError();
+          return false;
+        }
+      }
+      return true;
+    });
+  });
 }
 
 inline rlk_status check_shard(int64_t rows, int64_t start, int64_t V_true) {
@@ -790,12 +810,13 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
              reinterpret_cast<int32_t*>(ws + r.done), 3 * r.slots * g.slices, runs, n_runs};
   while (V_local >> q.bits) ++q.bits;  // rows and the mark behind them: 0 .. V_local
   q.passes = (q.bits + 8) / 9;
+  const int most = sort_ctas_at_most();
+  if (most == 0) return RLK_ERR_CUDA;
   int ctas = 1;  // two positions a thread while there are CTAs
-  while (ctas < SORT_CTAS && T > 2 * SORT_THREADS * ctas) ctas *= 2;
+  while (ctas < most && T > 2 * SORT_THREADS * ctas) ctas *= 2;
   const int64_t groups = (T + SORT_THREADS * ctas - 1) / (SORT_THREADS * ctas);
-  st = groups <= 2 ? launch_sort<2, true>(q, ctas, s)
-                   : groups <= 8 ? launch_sort<8, true>(q, ctas, s) : launch_sort<8, false>(q, ctas, s);
-  if (st != RLK_OK) return st;
+  const SortLaunch sort(ctas, s);
+  if (cudaLaunchKernelEx(&sort.cfg, kSorts[groups <= 2 ? 0 : groups <= 8 ? 1 : 2], q) != cudaSuccess) return RLK_ERR_CUDA;
   g.sorted = q.passes & 1 ? q.a : q.b;
   g.runs = runs;
   g.n_runs = n_runs;

@@ -235,6 +235,28 @@ struct OncePerDevice {
   }
 };
 
+// The same for a whole number above 0 (0: it could not be found out, and is asked for again).
+struct KnownPerDevice {
+  std::atomic<int> of[64] = {};
+  template <class F>
+  int operator()(F ask) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (dev < 0 || dev >= 64) return ask();
+    int v = of[dev].load(std::memory_order_acquire);
+    if (v == 0) of[dev].store(v = ask(), std::memory_order_release);
+    return v;
+  }
+};
+
+// CTAs of a cluster: `want`, or half of it and so on while fits(ctas) says that the device has no place for it (a part of a
+// GPU may have none for more than the 8 that every device takes).
+template <class Fits>
+inline int cluster_that_fits(int want, Fits fits) {
+  while (want > 8 && !fits(want)) want /= 2;
+  return want;
+}
+
 // A kernel that may start while the one before it on the stream ends (it waits for it by itself).
 template <class... A>
 inline rlk_status launch_after(void (*kernel)(A...), dim3 grid, int threads, cudaStream_t s, const A&... a) {

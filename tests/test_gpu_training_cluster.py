@@ -38,3 +38,26 @@ def test_sort_beside_other_work(rlk, T, V):
         got.append(rlk.embedding_bwd(dout, ids, V))
     torch.cuda.synchronize()
     assert all(torch.equal(g, alone) for g in got)
+
+
+FIRST = """
+import torch
+import deterministic_token_logprob_gb300 as rlk
+ids = torch.arange(5000, device="cuda") % 77
+dout = torch.ones((5000, 16), device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    dW = rlk.embedding_bwd(dout, ids, 100)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(dW, torch.bincount(ids, minlength=100).float()[:, None].expand(100, 16))
+"""
+
+
+def test_first_call_is_captured(rlk):
+    """What the sort asks the device before its first launch may be asked while a graph is captured."""
+    import subprocess
+    import sys
+    r = subprocess.run([sys.executable, "-c", FIRST], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stderr
