@@ -254,10 +254,13 @@ struct NormGradArgs {
   int32_t* err;
 };
 
-// h of a pack, into x
+// h of a pack, into x. A finite row may differ from its mean by more than fp32 holds (its r is 2^-120 at most, H being 2^16): it is halved
+// first, which loses nothing there, and r doubled.
 __device__ __forceinline__ void norm_h(F32x2 (&x)[4], float m, float r) {
+  const bool wide = r < 7.888609052210118e-31f;  // 2^-100
+  const float k = wide ? 0.5f : 1.f, km = __fmul_rn(-k, m), rk = wide ? __fadd_rn(r, r) : r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = mul2(add2(x[i], both(-m)), both(r));
+  for (int i = 0; i < 4; ++i) x[i] = mul2(fma2(x[i], both(k), both(km)), both(rk));
 }
 
 // the pack's part of sum g (where the mean counts) and sum g h

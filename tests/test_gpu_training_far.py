@@ -1,0 +1,54 @@
+"""The norm's gradient and the gradient norm at the ends of fp32, against 64-bit forms with the bounds of training_ref."""
+import math
+
+import pytest
+import torch
+
+import training_ref as ref
+from test_gpu_training import norm_inputs, randn, rng
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def rlk():
+    from deterministic_token_logprob_gb300 import build
+    build.build()
+    import deterministic_token_logprob_gb300 as m
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    return m
+
+
+def far_rows(gen, H, dtype):
+    """Offsets much larger than what varies, rows near both ends of fp32, and rows that differ from their mean by more than
+    fp32 holds (H of one column has none)."""
+    z = torch.randn((6, H), generator=gen, device="cuda")
+    two = torch.full_like(z[0], 2e38)
+    two[::max(8, H // 2)] = -3e38                             # x - m below -2^128
+    sides = torch.where(torch.arange(H, device="cuda") % 2 == 0, 3.3e38, -3.3e38)
+    sides[H // 2] = -3.3e38
+    rows = [z[0] + 1000.0, z[1] * 1e30, z[2].clamp(-3, 3) * 1e38, z[3] * 1e-30, torch.full_like(z[4], 3e38), z[5] * 1e-3 - 64.0,
+            two, sides, z[0] * 1e-39, z[1]]
+    return torch.stack(rows).to(dtype)
+
+
+@pytest.mark.parametrize("dtype,out", [(torch.float32, torch.float32), (torch.float32, torch.bfloat16), (torch.bfloat16, torch.bfloat16)])
+@pytest.mark.parametrize("H", [8, 100, 4096, 8193, 16384, 20000])
+def test_norm_gradient_far_values(rlk, dtype, out, H):
+    """Rows that the forward takes have a gradient that is finite and within the bounds, from the forward's statistics."""
+    gen = rng(H)
+    x = far_rows(gen, H, dtype)
+    assert bool(x.isfinite().all())
+    w = torch.randn(H, generator=gen, device="cuda")
+    dy = randn(gen, len(x), H, dtype=out)
+    odd = torch.empty(x.numel() + 1, dtype=dtype, device="cuda")[1:].view(x.shape).copy_(x)
+    for centered in (True, False):
+        y, mean, rstd = rlk.layer_norm_fwd(x, w, centered=centered, out_dtype=out)
+        assert bool(y.isfinite().all()) and bool(rstd.isfinite().all())
+        got = rlk.layer_norm_bwd(dy, x, w, mean, rstd)
+        want, tol = ref.norm_grad(dy, x, w, mean, rstd)
+        for g, a, t, name in zip(got, want, tol, ("dx", "dw", "db")):
+            # a term below fp32's normal values is off by half of the smallest one, the sum by that for each row
+            ref.close(g, a, ref.rounded(a, g.dtype, t) + len(x) * ref.TINY[torch.float32], name)
+        again = rlk.layer_norm_bwd(dy, odd, w, mean, rstd)
+        assert all(torch.equal(a, b) for a, b in zip(got, again))
