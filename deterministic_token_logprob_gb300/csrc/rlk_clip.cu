@@ -63,6 +63,8 @@ __device__ __forceinline__ void add_exactly(float& hi, float& lo, float v) {
 struct Exact {
   float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(float v) { add_exactly(hi, lo, v); }
+  // An infinity has lost nothing (what add_exactly takes for its loss is NaN)
+  __device__ __forceinline__ float sum() const { return isfinite(hi) ? __fadd_rn(hi, lo) : hi; }
 };
 
 // The sum of squares of a thread's packs of a chunk, get(j) the j-th of them, at the scale that holds it.
@@ -178,10 +180,10 @@ __device__ __forceinline__ float norm_of(const Squares* sums, int n, float* room
     if (v.z != 0.f) small.add(v.z);
   }
   const bool odd = __syncthreads_or(big.hi != 0.f || small.hi != 0.f);
-  float m = block_sum(__fadd_rn(mid.hi, mid.lo), room), b = 0.f, s = 0.f;
+  float m = block_sum(mid.sum(), room), b = 0.f, s = 0.f;
   if (odd) {
-    b = block_sum(__fadd_rn(big.hi, big.lo), room);
-    s = block_sum(__fadd_rn(small.hi, small.lo), room);
+    b = block_sum(big.sum(), room);
+    s = block_sum(small.sum(), room);
   }
   // each scale against the next larger one in which there is something
   const auto down = [](float v) { return __fmul_rn(__fmul_rn(v, kShrunk), kShrunk); };

@@ -601,7 +601,8 @@ RLK_API rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t 
  *   norm     device fp32 [1]: the norm before scaling; with outs, it meets no gradient and no result
  * Squares that would overflow or vanish in fp32 are summed at another scale. A norm that is not finite (a NaN or an
  * infinity among the gradients, or a norm beyond fp32) leaves the gradients unscaled, and RLK_FLAG_NONFINITE is ORed
- * into *err_flag: a trainer skips that step. Sums are taken in an order that follows from sizes and types.
+ * into *err_flag: a trainer skips that step. It is NaN where there is a NaN, and infinite otherwise. Sums are taken in an order that
+ * follows from sizes and types.
  */
 #define RLK_MAX_TENSORS (1 << 14)
 #define RLK_MAX_TENSOR_ELEMENTS ((int64_t)1 << 40)

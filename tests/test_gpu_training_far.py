@@ -52,3 +52,24 @@ def test_norm_gradient_far_values(rlk, dtype, out, H):
             ref.close(g, a, ref.rounded(a, g.dtype, t) + len(x) * ref.TINY[torch.float32], name)
         again = rlk.layer_norm_bwd(dy, odd, w, mean, rstd)
         assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_norm_of_infinities(rlk):
+    """The root of a sum with an infinity in it is infinite, and NaN where there is a NaN; a norm beyond fp32 is infinite too."""
+    big = torch.finfo(torch.float32).max
+    for dtype in (torch.float32, torch.bfloat16, torch.float16):
+        z = torch.randn(20000, generator=rng(1), device="cuda").to(dtype)
+        for at in ([0], [19999], [5, 17000], list(range(0, 20000, 7))):
+            for sign in (1, -1):
+                g = z.clone()
+                g[at] = sign * math.inf
+                err = torch.zeros(1, dtype=torch.int32, device="cuda")
+                assert float(rlk.grad_norm([z, g], err_flag=err)) == math.inf and int(err) == rlk.RLK_FLAG_NONFINITE
+                mine = [z.clone(), g.clone()]
+                assert float(rlk.clip_grad_norm(mine, 1.0, err_flag=err)) == math.inf
+                assert torch.equal(mine[0], z) and torch.equal(mine[1], g)
+                g[1234] = math.nan
+                assert math.isnan(float(rlk.grad_norm([g, z])))
+    for n in (2, 5000, 3_000_000):
+        assert float(rlk.grad_norm(torch.full((n,), big, device="cuda"))) == math.inf
+    assert float(rlk.grad_norm(torch.full((1,), big, device="cuda"))) == big
