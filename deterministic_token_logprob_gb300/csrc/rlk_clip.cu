@@ -32,17 +32,17 @@ struct Piece {
 };
 
 // Sums of squares at three scales (Blue's sums): what would overflow or vanish in fp32 is squared as x 2^-80 or x 2^80. All in
-// fp32: this GPU adds two doubles an SM and cycle, and a fold of the shares in doubles by every CTA took 7 us.
-struct alignas(16) Squares {
+// fp32, with what the sums' roundings lose (a thread may add many chunks, 18000 of 280 GB): this GPU adds two doubles an SM and cycle,
+// and a fold of the shares in doubles by every CTA took 7 us.
+struct alignas(16) Share {
   float mid = 0.f, big = 0.f, small = 0.f;
-  float lost = 0.f;  // what the roundings of mid's sum have lost: a thread may add many chunks (18000 of 280 GB)
 };
 template <int N>
 struct ClipArgs {
   Piece piece[N];
   int32_t n;
   uint32_t chunks;
-  Squares* sums;        // [launches][SHARES], this launch's first
+  Share* sums;        // [launches][SHARES], this launch's first
   int32_t* err;
 };
 
@@ -54,22 +54,35 @@ constexpr int CHUNK = CHUNK_BYTES / static_cast<int>(sizeof(typename E::bits)); 
 template <class E>
 constexpr int PACKS = CHUNK<E> / (8 * CLIP_THREADS);                             // of a thread
 
-// hi + lo += v: the sum and what its rounding loses (two-sum)
-__device__ __forceinline__ void add_exactly(float& hi, float& lo, float v) {
-  const float t = __fadd_rn(hi, v), b = __fsub_rn(t, hi);
-  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(v, b)));
-  hi = t;
-}
+// hi + lo: a sum and what its roundings have lost (two-sum)
 struct Exact {
   float hi = 0.f, lo = 0.f;
-  __device__ __forceinline__ void add(float v) { add_exactly(hi, lo, v); }
-  // An infinity has lost nothing (what add_exactly takes for its loss is NaN)
+  __device__ __forceinline__ void add(float v) {
+    const float t = __fadd_rn(hi, v), b = __fsub_rn(t, hi);
+    lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, b)), __fsub_rn(v, b)));
+    hi = t;
+  }
+  // An infinity has lost nothing (what add takes for its loss is NaN)
   __device__ __forceinline__ float sum() const { return isfinite(hi) ? __fadd_rn(hi, lo) : hi; }
 };
 
+// A thread's sums at the outer scales are seldom touched, and stay out of the way of the others: in shared memory, behind a call
+// (216 tensors of 302 MB in bf16 take 49.6 us; written out in line 50.5, in registers, of which 16-bit types spill, 51.8; without
+// what the outer scales lose 49.2).
+struct Rare {
+  Exact big, small;
+};
+__device__ __forceinline__ Rare& rare_sums() {
+  __shared__ __align__(16) float room[CLIP_THREADS][4];
+  uint32_t tid;  // read again by each use: kept from the first to the last it takes a register from the loop between
+  asm volatile("mov.u32 %0, %%tid.x;" : "=r"(tid));
+  return reinterpret_cast<Rare&>(room[tid]);
+}
+__device__ __noinline__ void add_rare(bool tiny, float r) { (tiny ? rare_sums().small : rare_sums().big).add(r); }
+
 // The sum of squares of a thread's packs of a chunk, get(j) the j-th of them, at the scale that holds it.
 template <class E, int UNROLL, class Get>
-__device__ __forceinline__ void add_squares(Squares& s, const Get& get) {
+__device__ __forceinline__ void add_squares(Exact& mid, const Get& get) {
   const auto at = [&](float f) {
     F32x2 a = 0;
 #pragma unroll(UNROLL)
@@ -84,13 +97,12 @@ __device__ __forceinline__ void add_squares(Squares& s, const Get& get) {
   };
   const float q = at(1.f);
   if (q >= 8.077935669463161e-28f && q <= 1.2089258196146292e24f) {  // 2^-90 .. 2^80: 2^39 of them stay in fp32
-    add_exactly(s.mid, s.lost, q);
+    mid.add(q);
     return;
   }
   const bool tiny = q < 1.f;  // else too large, NaN or infinite
   const float r = at(tiny ? kGrown : kShrunk);
-  if (tiny) s.small = __fadd_rn(s.small, r);
-  else s.big = __fadd_rn(s.big, r);
+  if (r != 0.f) add_rare(tiny, r);
 }
 
 // The sum over the CTA's threads, in one order; every thread gets it. room: 8 floats each.
@@ -121,7 +133,7 @@ __device__ __forceinline__ bool on_vector_boundary(const void* p) { return (rein
 // Chunks lo, lo + SHARES, ... below hi of a tensor. A misaligned one's packs are cut from their neighbours' vectors, so that every thread owns the
 // elements that it owns of an aligned one.
 template <class E>
-__device__ __noinline__ Squares sum_chunks(const Piece p, uint32_t lo, uint32_t hi, Squares s, int32_t* err) {
+__device__ __noinline__ Exact sum_chunks(const Piece p, uint32_t lo, uint32_t hi, Exact s, int32_t* err) {
   const int tid = static_cast<int>(threadIdx.x);
   const auto* in = static_cast<const typename E::bits*>(p.in) + static_cast<int64_t>(lo) * CHUNK<E>;
   int64_t left = p.n - static_cast<int64_t>(lo) * CHUNK<E>;
@@ -149,7 +161,8 @@ __device__ __noinline__ Squares sum_chunks(const Piece p, uint32_t lo, uint32_t 
 template <int N>
 __global__ void __launch_bounds__(CLIP_THREADS, 6) sum_squares_kernel(const __grid_constant__ ClipArgs<N> a) {
   __shared__ float room[CLIP_THREADS / 32];
-  Squares s;
+  Exact s;
+  rare_sums() = Rare{};
   for (uint32_t c = blockIdx.x; c < a.chunks;) {
     const int i = piece_of(a, c);
     const Piece& p = a.piece[i];
@@ -160,18 +173,19 @@ __global__ void __launch_bounds__(CLIP_THREADS, 6) sum_squares_kernel(const __gr
     c += (end - c + SHARES - 1) / SHARES * SHARES;
   }
   griddep_launch_dependents();
-  Squares all;
-  const bool odd = __syncthreads_or(s.big != 0.f || s.small != 0.f);  // NaN counts
-  all.mid = block_sum(__fadd_rn(s.mid, s.lost), room);
+  Share all;
+  const Rare rare = rare_sums();
+  const bool odd = __syncthreads_or(rare.big.hi != 0.f || rare.small.hi != 0.f);  // NaN counts
+  all.mid = block_sum(s.sum(), room);
   if (odd) {
-    all.big = block_sum(s.big, room);
-    all.small = block_sum(s.small, room);
+    all.big = block_sum(rare.big.sum(), room);
+    all.small = block_sum(rare.small.sum(), room);
   }
   if (threadIdx.x == 0) a.sums[blockIdx.x] = all;
 }
 
 // The norm from the shares' sums, by one CTA; the same bits in each, and in every thread.
-__device__ __forceinline__ float norm_of(const Squares* sums, int n, float* room) {
+__device__ __forceinline__ float norm_of(const Share* sums, int n, float* room) {
   Exact mid, big, small;
   for (int i = threadIdx.x; i < n; i += CLIP_THREADS) {
     const float4 v = __ldcg(reinterpret_cast<const float4*>(sums + i));
@@ -193,7 +207,7 @@ __device__ __forceinline__ float norm_of(const Squares* sums, int n, float* room
 }
 
 struct ClipNorm {
-  const Squares* sums;
+  const Share* sums;
   int32_t n;
   float max_norm;
   float* norm;
@@ -352,7 +366,7 @@ inline int32_t launches_of(int32_t n) { return n <= FEW ? 1 : (n + BATCH - 1) / 
 
 // Calls f with the table of each launch.
 template <int N, class F>
-inline rlk_status each_batch(const Tensors& t, Squares* sums, int32_t* err, F f) {
+inline rlk_status each_batch(const Tensors& t, Share* sums, int32_t* err, F f) {
   for (int32_t first = 0, k = 0; first == 0 || first < t.n; first += N, ++k) {
     ClipArgs<N> a;
     a.n = std::min(N, t.n - first);
@@ -372,7 +386,7 @@ inline rlk_status each_batch(const Tensors& t, Squares* sums, int32_t* err, F f)
 }
 
 template <int N>
-inline rlk_status run_clip(const Tensors& t, double max_norm, float* norm, int32_t* err, Squares* sums, cudaStream_t s) {
+inline rlk_status run_clip(const Tensors& t, double max_norm, float* norm, int32_t* err, Share* sums, cudaStream_t s) {
   rlk_status st = each_batch<N>(t, sums, err, [&](const ClipArgs<N>& a, int32_t) {
     sum_squares_kernel<N><<<SHARES, CLIP_THREADS, 0, s>>>(a);
     return launched();
@@ -402,7 +416,7 @@ inline rlk_status clip(const Tensors& t, double max_norm, float* norm, int32_t* 
   const rlk_status st = check_tensors(t, norm);
   if (st != RLK_OK) return st;
   if (!workspace || !on_boundary(workspace, 256) || bytes < rlk_grad_norm_workspace(t.n)) return RLK_ERR_WORKSPACE;
-  auto* sums = static_cast<Squares*>(workspace);
+  auto* sums = static_cast<Share*>(workspace);
   const auto s = static_cast<cudaStream_t>(stream);
   return t.n <= FEW ? run_clip<FEW>(t, max_norm, norm, err, sums, s) : run_clip<BATCH>(t, max_norm, norm, err, sums, s);
 }
@@ -414,7 +428,7 @@ using namespace rlk;
 
 extern "C" {
 
-size_t rlk_grad_norm_workspace(int32_t n) { return n < 0 ? 0 : (static_cast<size_t>(launches_of(n)) * SHARES + 1) * sizeof(Squares); }
+size_t rlk_grad_norm_workspace(int32_t n) { return n < 0 ? 0 : (static_cast<size_t>(launches_of(n)) * SHARES + 1) * sizeof(Share); }
 
 rlk_status rlk_grad_norm(const void* const* grads, const int64_t* sizes, const int32_t* dtypes, int32_t n, float* norm,
                          int32_t* err_flag, void* workspace, size_t workspace_bytes, void* stream) {

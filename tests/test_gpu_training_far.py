@@ -73,3 +73,14 @@ def test_norm_of_infinities(rlk):
     for n in (2, 5000, 3_000_000):
         assert float(rlk.grad_norm(torch.full((n,), big, device="cuda"))) == math.inf
     assert float(rlk.grad_norm(torch.full((1,), big, device="cuda"))) == big
+
+
+@pytest.mark.parametrize("v", [1e-15, 1.7e-15, 3.3e-16, 1e25, 1.3e25, 1e30])
+def test_norm_of_many_elements_far_from_one(rlk, v):
+    """2^31 equal elements whose squares are summed at another scale (a power of two, which rounds nothing), 575 chunks a thread. Relative
+    to the sum of squares: 9 roundings of a chunk's 16 values, 2 of the sum of chunks, whose losses are kept, 8 in a warp and
+    between warps, as many where the shares are joined (3 sums with their losses, 8), and one beside the other scales: 31 half steps
+    at most, of which the root leaves 15.5, its own rounding and that of the result's scale apart."""
+    g = torch.full((1 << 31,), v, device="cuda")
+    want = math.sqrt(2.0 ** 31) * float(g[0])
+    assert abs(float(rlk.grad_norm([g])) / want - 1) <= 18 * ref.U
