@@ -216,14 +216,18 @@ struct ClipNorm {
 };
 
 // The norm and the factor, by a CTA that writes them or by one that wants the factor alone. A norm beyond fp32, or none, leaves
-// the gradients as they are.
+// the gradients as they are. A factor below fp32's normal values would have lost digits (1e-41 has 13): then it is taken for the gradients
+// times 2^-126, and less than 0 to say so.
+constexpr float kLeast = 1.1754943508222875e-38f;  // 2^-126
 __device__ __forceinline__ float find_norm(const ClipNorm& q, bool write, float* room) {
   const float v = norm_of(q.sums, q.n, room);
   if (write && threadIdx.x == 0) {
     *q.norm = v;
     if (!isfinite(v) && q.err) atomicOr(q.err, RLK_FLAG_NONFINITE);
   }
-  return isfinite(v) && v > q.max_norm ? __fdiv_rn(q.max_norm, v) : 1.f;
+  if (!(isfinite(v) && v > q.max_norm)) return 1.f;
+  const float f = __fdiv_rn(q.max_norm, v);
+  return f >= kLeast || q.max_norm == 0.f ? f : -__fdiv_rn(q.max_norm, __fmul_rn(v, kLeast));
 }
 
 __global__ void __launch_bounds__(CLIP_THREADS) norm_kernel(const ClipNorm q) {
@@ -242,7 +246,7 @@ __device__ __noinline__ void scale_chunks(const Piece p, uint32_t c, uint32_t st
   const auto* in0 = static_cast<const typename E::bits*>(p.in);
   auto* out0 = static_cast<typename O::bits*>(p.out);
   const int head0 = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(out0) & 15)) & 15) / static_cast<int>(sizeof(*out0));
-  const bool plain = f == 1.f;  // a NaN's bits survive a copy
+  const bool plain = f == 1.f;  // fp32 keeps a NaN's bits
   const auto put = [&](const Pack<E>& k, typename O::bits* out, int c, int n) {
     F32x2 v[4];
     unpack(k, v);
@@ -283,6 +287,25 @@ __device__ __noinline__ void scale_chunks(const Piece p, uint32_t c, uint32_t st
   }
 }
 
+// The same chunks times 2^-126 and then f, element by element: a norm of more than 2^126 times max_norm is no step's to be fast.
+template <class E, class O>
+__device__ __noinline__ void scale_chunks_twice(const Piece p, uint32_t c, uint32_t step, float f, int32_t* err) {
+  const auto* in = static_cast<const typename E::bits*>(p.in);
+  auto* out = static_cast<typename O::bits*>(p.out);
+  for (;; c -= step) {
+    const int64_t at = static_cast<int64_t>(c) * CHUNK<E>, end = min(p.n, at + CHUNK<E>);
+    for (int64_t i = at + threadIdx.x; i < end; i += CLIP_THREADS)
+      if (dbg_ok(i >= 0 && i < p.n, err)) out[i] = O::from_f32(__fmul_rn(__fmul_rn(E::to_f32(in[i]), kLeast), f));
+    if (c < step) return;
+  }
+}
+
+template <class E, class O>
+__device__ __forceinline__ void scale_piece(const Piece& p, uint32_t c, uint32_t step, float f, int32_t* err) {
+  if (f < 0.f) scale_chunks_twice<E, O>(p, c, step, -f, err);
+  else scale_chunks<E, O>(p, c, step, f, err);
+}
+
 template <int N>
 __global__ void __launch_bounds__(CLIP_THREADS, 4) scale_kernel(const __grid_constant__ ClipArgs<N> a, const ClipNorm q) {
   __shared__ float room[CLIP_THREADS / 32];
@@ -293,10 +316,10 @@ __global__ void __launch_bounds__(CLIP_THREADS, 4) scale_kernel(const __grid_con
     const Piece& p = a.piece[piece_of(a, c)];
     const uint32_t at = c - p.chunk0;
     if (!(f == 1.f && p.in == p.out && p.dtype == p.out_dtype)) {
-      if (p.dtype == RLK_DTYPE_BF16) scale_chunks<Bf16, Bf16>(p, at, gridDim.x, f, a.err);
-      else if (p.dtype == RLK_DTYPE_F16) scale_chunks<F16, F16>(p, at, gridDim.x, f, a.err);
-      else if (p.out_dtype == RLK_DTYPE_F32) scale_chunks<F32, F32>(p, at, gridDim.x, f, a.err);
-      else scale_chunks<F32, Bf16>(p, at, gridDim.x, f, a.err);
+      if (p.dtype == RLK_DTYPE_BF16) scale_piece<Bf16, Bf16>(p, at, gridDim.x, f, a.err);
+      else if (p.dtype == RLK_DTYPE_F16) scale_piece<F16, F16>(p, at, gridDim.x, f, a.err);
+      else if (p.out_dtype == RLK_DTYPE_F32) scale_piece<F32, F32>(p, at, gridDim.x, f, a.err);
+      else scale_piece<F32, Bf16>(p, at, gridDim.x, f, a.err);
     }
     const uint32_t back = at / gridDim.x * gridDim.x + gridDim.x;  // past the tensor's first chunk of this CTA
     if (c < back) return;

@@ -84,3 +84,39 @@ def test_norm_of_many_elements_far_from_one(rlk, v):
     g = torch.full((1 << 31,), v, device="cuda")
     want = math.sqrt(2.0 ** 31) * float(g[0])
     assert abs(float(rlk.grad_norm([g])) / want - 1) <= 18 * ref.U
+
+
+@pytest.mark.parametrize("dtype,out", [(torch.float32, torch.float32), (torch.float32, torch.bfloat16), (torch.bfloat16, torch.bfloat16)])
+@pytest.mark.parametrize("size,max_norm", [(1e36, 1.0), (1e36, 1e-3), (1e35, 1e-9), (1e36, 1e-30), (1e30, 1e-12), (1e36, 2.0 ** -126),
+                                           (1e34, 1e-42), (1e5, 1e-40), (1.0, 1e-50), (1e36, 1e30)])
+def test_clip_by_factors_below_normal_values(rlk, dtype, out, size, max_norm):
+    """max_norm / norm may lie below fp32's normal values where results do not. The factor costs the norm's bound and three half steps
+    (the norm's own, max_norm's and the division's), the product two; below the normal values, where the gradient times 2^-126, the norm times
+    2^-126 and the factor may lie, half of the smallest value each, times 4 (what a gradient times 2^-126 is at most)."""
+    z = torch.randn(30011, generator=rng(4), device="cuda")
+    z[::5] *= 1e-6
+    flat = (z * size).to(dtype)
+    grads = list(flat.split([7, 20000, 10004]))
+    want, rel = ref.total_norm(grads)
+    f = max_norm / want
+    to = torch.full((30011 + 3,), 7.0, dtype=out, device="cuda")
+    norm = rlk.clip_grad_norm(grads, max_norm, out=list(to[1:-2].split([7, 20000, 10004])))
+    assert abs(float(norm) / want - 1) <= rel
+    exact = flat.double() * f
+    tol = exact.abs() * (rel + 5 * ref.U) + 8 * ref.TINY[torch.float32]
+    ref.close(to[1:-2], exact, ref.rounded(exact, out, tol))
+    assert to[0] == 7.0 and to[-2:].tolist() == [7.0, 7.0]
+    if dtype is out:
+        mine = flat.clone()
+        assert torch.equal(rlk.clip_grad_norm(list(mine.split([7, 20000, 10004])), max_norm), norm) and torch.equal(mine, to[1:-2])
+
+
+def test_clip_many_chunks_by_a_factor_below_normal_values(rlk):
+    """The same where a CTA scales one chunk: 2^25 elements of two values, in place."""
+    g = torch.full((1 << 25,), 1e34, device="cuda")
+    g[::3] = -3e30
+    want, _ = ref.total_norm([g])
+    exact = g.double() * (1e-5 / want)
+    rlk.clip_grad_norm([g], 1e-5)
+    # sums of equal squares, 2^25 of them: 40 half steps at most (test_norm_of_many_elements)
+    ref.close(g, exact, ref.rounded(exact, torch.float32, exact.abs() * 45 * ref.U))
