@@ -321,7 +321,8 @@ def clip_grad_norm(grads: Union[torch.Tensor, Sequence[torch.Tensor]], max_norm:
     outs = grads if out is None else ((out,) if isinstance(out, torch.Tensor) else tuple(out))
     if _away(stream, dev):
         with _elsewhere(stream, dev, (*grads, *(() if out is None else outs), norm, err_flag, workspace)):
-            return clip_grad_norm(grads, max_norm, out=out, norm=norm, err_flag=err_flag, workspace=workspace)
+            return clip_grad_norm(grads, max_norm, out=None if out is None else outs, norm=norm, err_flag=err_flag,
+                                  workspace=workspace)
     if not max_norm > 0 or math.isnan(max_norm):
         raise ValueError(f"max_norm must be above 0, got {max_norm}")
     at, codes = _listed(grads, "gradients", dev)
