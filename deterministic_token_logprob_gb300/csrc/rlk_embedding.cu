@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(THREADS) lookup_kernel(const LookupArgs a) {
 // stable and its result unique. A token without a row here sorts behind the last row.
 constexpr int SORT_THREADS = 512;
 constexpr int SORT_WARPS = SORT_THREADS / 32;
-constexpr int SORT_BINS = 512;  // 9 bits at most at a time: two passes for up to 2^18 rows
+constexpr int SORT_BINS = 512;  // 9 bits at most at a time: two passes for up to 2^18 - 1 rows (and the mark behind them)
 constexpr int SORT_CTAS = 16;
 constexpr int RUN = 16;         // positions of one token that are added in one go
 constexpr int GROUP = 8;        // runs
@@ -659,6 +659,15 @@ struct Room {  // the workspace of a gradient
   int32_t slots;
 };
 
+// CTAs of a run, and the warps of each: a slice of 256 `packs` columns a warp.
+struct Slices {
+  int warps, blocks;
+  Slices(int64_t H, int packs)
+      : warps(static_cast<int>(std::min<int64_t>(GATHER_THREADS / 32, (H + 256 * packs - 1) / (256 * packs)))),
+        blocks(static_cast<int>((H + 256 * packs * warps - 1) / (256 * packs * warps))) {}
+  int all() const { return blocks * warps; }
+};
+
 inline Room room_of(int64_t T, int64_t H) {
   Room r{};
   if (T <= FEW_TOKENS) return r;
@@ -666,7 +675,8 @@ inline Room room_of(int64_t T, int64_t H) {
   r.b = carved(T * sizeof(Entry));
   r.runs = 2 * r.b;
   r.done = r.runs + carved((T + 1) * sizeof(uint4));  // the list, and how many it has
-  r.part = r.done + carved(3 * static_cast<size_t>(r.slots) * ((H + 255) / 256 + 8) * sizeof(int32_t));
+  const int slices = std::max(Slices(H, 1).all(), Slices(H, 2).all());
+  r.part = r.done + carved(3 * static_cast<size_t>(r.slots) * slices * sizeof(int32_t));
   r.all = r.part + carved(2 * static_cast<size_t>(r.slots) * ((H + 7) / 8 * 8) * sizeof(float));
   return r;
 }
@@ -800,9 +810,8 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
     });
   }
   const int packs = in.eb == 4 || H <= 256 || T * ((H + 255) / 256) <= FEW_WARPS ? 1 : 2;  // a lane's in a slice
-  const int warps = static_cast<int>(std::min<int64_t>(GATHER_THREADS / 32, (H + 256 * packs - 1) / (256 * packs)));
-  const int blocks = static_cast<int>((H + 256 * packs * warps - 1) / (256 * packs * warps));
-  g.slices = blocks * warps;
+  const Slices cut(H, packs);
+  g.slices = cut.all();
   char* ws = static_cast<char*>(workspace);
   auto* runs = reinterpret_cast<uint4*>(ws + r.runs);
   auto* n_runs = reinterpret_cast<int32_t*>(runs + T);
@@ -823,7 +832,7 @@ rlk_status rlk_embedding_bwd(const void* dout, int32_t dtype, int64_t T, int64_t
   g.part = reinterpret_cast<float*>(ws + r.part);
   g.done = q.done;
   if (al && T * H * in.eb <= AHEAD_BYTES) g.ahead = static_cast<int32_t>((T + AHEAD_CTAS - 1) / AHEAD_CTAS);
-  const auto go = [&](auto kernel) { return launch_after(kernel, dim3(static_cast<unsigned>(T + zero), blocks), 32 * warps, s, g); };
+  const auto go = [&](auto kernel) { return launch_after(kernel, dim3(static_cast<unsigned>(T + zero), cut.blocks), 32 * cut.warps, s, g); };
   return with_type(dtype, [&](auto e) {
     using E = decltype(e);
     if constexpr (sizeof(typename E::bits) == 4) return go(al ? gather_kernel<E, true, 1, 4> : gather_kernel<E, false, 1, 4>);

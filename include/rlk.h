@@ -526,8 +526,10 @@ RLK_API rlk_status rlk_embedding_fwd(const void* table, int32_t dtype, int64_t V
                                      int64_t vocab_start, int64_t V_true, const int64_t* ids, int64_t T, double scale,
                                      void* out, int32_t out_dtype, int64_t out_ld, int32_t* err_flag, void* stream);
 
-/* Bytes of device workspace rlk_embedding_bwd needs: the sorted tokens (32 T bytes) and the sums of tokens that
- * come more than 16 times (up to T H / 2 bytes); 0 (and workspace may be NULL) for up to 256 tokens. */
+/* Bytes of device workspace rlk_embedding_bwd needs; 0 (and workspace may be NULL) for up to 256 tokens. Beyond, with n = T / 16 + 1 and
+ * H rounded up to 8: the sorted tokens and their runs (32 T + 16 bytes), the sums of tokens that come more than 16 times (8 n H) and
+ * counters of those sums (12 n for every 256 columns begun, beyond 2048 columns for every 2048 begun 8 times that), each of the five arrays
+ * rounded up to 256 bytes. */
 RLK_API size_t rlk_embedding_bwd_workspace(int64_t T, int64_t H);
 
 /*
