@@ -246,7 +246,7 @@ __device__ __noinline__ void scale_chunks(const Piece p, uint32_t c, uint32_t st
   const auto* in0 = static_cast<const typename E::bits*>(p.in);
   auto* out0 = static_cast<typename O::bits*>(p.out);
   const int head0 = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(out0) & 15)) & 15) / static_cast<int>(sizeof(*out0));
-  const bool plain = f == 1.f;  // fp32 keeps a NaN's bits
+  const bool plain = f == 1.f;  // not even a NaN's bits change in fp32 (16-bit types have one NaN on the way back)
   const auto put = [&](const Pack<E>& k, typename O::bits* out, int c, int n) {
     F32x2 v[4];
     unpack(k, v);

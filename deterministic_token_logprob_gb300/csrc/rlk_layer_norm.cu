@@ -326,7 +326,7 @@ struct RowRing {
 
 // Rows of up to 8192 columns. A team of W warps takes a strip's rows in turn; the next stages - 1 rows are on their way into
 // shared memory meanwhile (unless they are misaligned). Each thread keeps the sums of dw and db of its columns. 8192 rows of 4096 in
-// bf16 take 37.4 us with the fold (0.79 of the copy rate: 16 warps an SM issue in 46 % of the cycles), in fp32 64 (0.93).
+// bf16 take 37.8 us with the fold (0.78 of the copy rate: 16 warps an SM issue in 47 % of the cycles), in fp32 64 (0.93).
 template <class E, class O, int W, int K, bool AL>
 __global__ void __launch_bounds__(ROW_CTA, K <= 2 ? 2 : 1) norm_bwd_kernel(const NormGradArgs a) {
   extern __shared__ __align__(16) unsigned char dyn[];  // AL: the rows to come; else stages (write_out)

@@ -1,7 +1,8 @@
 """Operators around the head in a training step: embedding lookup (:func:`embedding_fwd`) and the
 table's gradient (:func:`embedding_bwd`, new or added to the head's dW of a tied model), layer norm
 and its gradient (:func:`layer_norm_fwd`, :func:`layer_norm_bwd`), and the norm over all gradients
-(:func:`grad_norm`) with clipping (:func:`clip_grad_norm`).
+(:func:`grad_norm`) with clipping (:func:`clip_grad_norm`). Where gradients are shards, that norm is the
+shards' own.
 
 Argument marshalling around the C entry points of the same names (include/rlk.h states their
 mathematics, special rows and errors); all arithmetic runs in the library's CUDA kernels. Rows are
@@ -15,7 +16,6 @@ from __future__ import annotations
 
 import array
 import functools
-import math
 from operator import attrgetter
 from typing import Optional, Sequence, Tuple, Union
 
@@ -323,7 +323,7 @@ def clip_grad_norm(grads: Union[torch.Tensor, Sequence[torch.Tensor]], max_norm:
         with _elsewhere(stream, dev, (*grads, *(() if out is None else outs), norm, err_flag, workspace)):
             return clip_grad_norm(grads, max_norm, out=None if out is None else outs, norm=norm, err_flag=err_flag,
                                   workspace=workspace)
-    if not max_norm > 0 or math.isnan(max_norm):
+    if not max_norm > 0:   # NaN neither
         raise ValueError(f"max_norm must be above 0, got {max_norm}")
     at, codes = _listed(grads, "gradients", dev)
     to, ocodes = at, codes

@@ -582,8 +582,8 @@ RLK_API size_t rlk_layer_norm_bwd_workspace(int64_t T, int64_t H);
  * otherwise where T is larger; a strip adds its rows in ascending order. Of the strips' sums, those of strips i, i + 32, ... are
  * added in ascending order, and the 32 results as a balanced tree. Finite rows of any size have the h of their statistics: a row that
  * differs from its mean by more than fp32 holds is halved first. The mean is the forward's, rounded to fp32: h carries half a step of
- * mean rstd. Sums of dy weight, and of their products with h, are to stay inside fp32. A row whose x, dy or statistics hold a NaN makes that row of dx and
- * all or those columns of dw and db NaN, whatever its dy: rows of padding are to hold finite values in both.
+ * mean rstd. Sums of dy weight, and of their products with h, are to stay inside fp32. A row whose x, dy or statistics hold a NaN
+ * makes that row of dx and all or those columns of dw and db NaN, whatever its dy: rows of padding are to hold finite values in both.
  */
 RLK_API rlk_status rlk_layer_norm_bwd(const void* dy, int32_t dy_dtype, int64_t dy_ld, const void* x, int32_t dtype,
                                       int64_t ld, int64_t T, int64_t H, const void* weight, int32_t weight_dtype,
