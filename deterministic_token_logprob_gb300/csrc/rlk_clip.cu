@@ -42,7 +42,7 @@ struct ClipArgs {
   Piece piece[N];
   int32_t n;
   uint32_t chunks;
-  Share* sums;        // [launches][SHARES], this launch's first
+  Share* sums;          // [launches][SHARES], this launch's first
   int32_t* err;
 };
 
@@ -302,7 +302,7 @@ __device__ __noinline__ void scale_chunks_twice(const Piece p, uint32_t c, uint3
 
 template <class E, class O>
 __device__ __forceinline__ void scale_piece(const Piece& p, uint32_t c, uint32_t step, float f, int32_t* err) {
-  if (f < 0.f) scale_chunks_twice<E, O>(p, c, step, -f, err);
+  if (!(f > 0.f)) scale_chunks_twice<E, O>(p, c, step, fabsf(f), err);  // -0 is one of those factors, too
   else scale_chunks<E, O>(p, c, step, f, err);
 }
 

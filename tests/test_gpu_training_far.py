@@ -120,3 +120,13 @@ def test_clip_many_chunks_by_a_factor_below_normal_values(rlk):
     rlk.clip_grad_norm([g], 1e-5)
     # sums of equal squares, 2^25 of them: 40 half steps at most (test_norm_of_many_elements)
     ref.close(g, exact, ref.rounded(exact, torch.float32, exact.abs() * 45 * ref.U))
+
+
+def test_clip_to_almost_nothing(rlk):
+    """A factor that rounds to nothing leaves zeros with the gradients' signs."""
+    for max_norm in (1e-45, 1e-50, 1e-300):
+        for size in (1e36, 1e5, 1e-3):
+            g = (torch.randn(5003, generator=rng(3), device="cuda")[1:] * size)
+            sign = g.signbit()
+            rlk.clip_grad_norm(g, max_norm)
+            assert torch.equal(g.signbit(), sign) and float(g.abs().max()) <= 2.0 ** -149
